@@ -1,0 +1,747 @@
+// Grouped-query decode attention over a paged KV cache, with an optional
+// sliding window and a few first tokens that stay visible (sinks).
+//
+// One query token per sequence b attends to the positions
+//     K(b) = { j < len_b : j >= len_b - window  or  j < sinks }
+// (window <= 0: every j < len_b); position j lives in row j % S of page
+// page_table[b][j / S].  Per head, o = sum_j p_j v_j / sum_j p_j with
+// p_j = 2^(x_j - max x), x_j = q . k_j * scale * log2(e).
+//
+// 4 FLOP per cache byte and query head: the work is bound by HBM, so the
+// design streams every visible page once and keeps the SMs evenly loaded:
+//
+//  * Flat work list.  A sequence is cut into chunks of 32 positions (only those
+//    that hold a visible one) and all chunks of all (sequence, KV head) units
+//    are numbered consecutively; each of 2 CTAs per SM takes one equal
+//    contiguous range.  Lengths are read on the device, so ragged batches and
+//    a captured graph whose sequences grow stay balanced, and the page table
+//    may be far wider than the sequences are long.
+//  * A CTA whose range cuts a unit writes a partial (max, sum, O) per head to
+//    the workspace; the last CTA of the unit to arrive (ticket) joins the
+//    partials in CTA order, so the result does not depend on who is last.
+//  * Two producer warps (K, V) stream chunks with TMA into a shared-memory
+//    ring: a box of up to 32 rows x D channels per copy, the page and
+//    the KV head being coordinates of one 5D tensor map, so either memory
+//    order of a page costs nothing and addresses are 64-bit.  The 32 lanes
+//    look up 32 boxes' pages at once.
+//  * Four consumer warps, one chunk each: S^T = K q^T (rows x heads) and
+//    O^T += V^T P^T with mma.sync m16n8k16.  With at most 16 query heads per
+//    KV head the product is 8 or 16 columns wide; the warp-level instruction
+//    takes the heads as its n = 8 columns, leaves the softmax statistics in
+//    registers and P^T one 8 x 8 transpose away from the next operand, where a
+//    tcgen05 tile would need 128 rows, a round trip through tensor memory and
+//    P staged in shared memory, for a tensor pipe that is mostly idle either
+//    way.
+//  * P is split into two 16-bit terms (P = hi + lo), so the P V product keeps
+//    ~16 bits of P instead of 8 (bf16): a second MMA on operands that are in
+//    registers already.  Sums and statistics are fp32; the output is rounded
+//    once.
+#include <cuda.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kChunk = 32;        // positions per chunk
+constexpr int kCW = 4;            // consumer warps
+constexpr int kNT = (kCW + 2) * 32;
+constexpr int kCtasPerSm = 2;
+constexpr int kMaxCtas = 2 * 192; // workspace slots (2 CTAs on up to 192 SMs)
+constexpr int kMinChunks = kCW;   // a CTA's range is at least one chunk per consumer warp
+
+template <int D, int NT>
+struct PgCfg {
+    static constexpr int HP = NT * 8;                       // padded heads per KV head
+    static constexpr int PANELS = D / 64;
+    static constexpr int TILE = kChunk * D * 2;             // K (or V) bytes of a chunk
+    static constexpr int LDM = D + 4;                       // floats per merge row (bank spread)
+    static constexpr int MERGE = kCW * HP * LDM * 4;
+    static constexpr int ML = kCW * HP * 2 * 4;
+    static constexpr int MISC = 1024;                       // barriers, flags
+    static constexpr int BUDGET = 113 * 1024 - 1024;        // two CTAs per SM, alignment slack
+    static constexpr int FIT = (BUDGET - MERGE - ML - MISC) / (2 * TILE);
+    static constexpr int SLOTS = FIT > 8 ? 8 : FIT;
+    static constexpr int OFF_K = 0;
+    static constexpr int OFF_V = SLOTS * TILE;
+    static constexpr int OFF_M = 2 * SLOTS * TILE;
+    static constexpr int OFF_ML = OFF_M + MERGE;
+    static constexpr int OFF_MISC = OFF_ML + ML;
+    static constexpr int SMEM = OFF_MISC + MISC + 1024;
+    static_assert(SLOTS >= 4, "at least one slot per consumer warp");
+};
+
+struct PgParams {
+    const void *q;
+    void *o;
+    long long q_sb, q_sh, o_sb, o_sh;      // element strides (batch, head)
+    const int32_t *table;
+    long long table_stride;
+    const int32_t *seq_len;
+    int B, Hkv, G;
+    int S, BR;                             // page size, rows per TMA box
+    int max_pages, num_pages;
+    int window, sinks;
+    float c_log2;
+    float *part_o;                         // [2 CTAs][HP][D]
+    float *part_ml;                        // [2 CTAs][HP][2]
+    unsigned *tickets;                     // [B * Hkv]
+    unsigned *err;
+};
+
+struct Misc {
+    uint64_t full_k[8], full_v[8], empty_k[8], empty_v[8];
+    long long warp_sum[kNT / 32];
+    long long start_off;
+    int start_b;
+    int abort;
+    unsigned last;
+    int bad[8];                            // per slot: a page id of the chunk is out of range
+    int warp_bad[kCW];
+};
+static_assert(sizeof(Misc) <= 1024, "barrier block must fit its reserved bytes");
+
+// The chunks of one sequence that hold a visible position: chunks [0, n1) for
+// the sinks and [c2, ...) for the window (one run from 0 where they touch).
+struct Plan {
+    int len, lo, s_end, n1, c2, n;
+};
+
+__device__ __forceinline__ Plan make_plan(const PgParams &p, int len) {
+    Plan r;
+    r.len = len;
+    r.lo = r.s_end = r.n1 = r.c2 = r.n = 0;
+    if (len < 1 || (long long)len > (long long)p.max_pages * p.S) return r;
+    if (p.window > 0 && len > p.window) r.lo = len - p.window;
+    r.s_end = imin(p.sinks, r.lo);
+    const int end = (len - 1) / kChunk + 1;
+    r.n1 = r.s_end > 0 ? (r.s_end - 1) / kChunk + 1 : 0;
+    r.c2 = r.lo / kChunk;
+    if (r.n1 >= r.c2) r.n1 = r.c2 = 0;
+    r.n = r.n1 + end - r.c2;
+    return r;
+}
+
+__device__ __forceinline__ int chunk_of(const Plan &r, int v) {
+    return v < r.n1 ? v : v - r.n1 + r.c2;
+}
+
+// One CTA's range of the flat chunk list, a segment (part of one unit) at a time.
+struct Walk {
+    const PgParams &p;
+    Plan plan;
+    int b, kvh, v0, cnt;
+    long long left;                        // chunks of the range from this segment on
+    long long flat;                        // flat index of the segment's first chunk
+
+    __device__ Walk(const PgParams &pp, int b0, long long off, long long f0, long long count)
+        : p(pp), b(b0), left(count), flat(f0) {
+        plan = make_plan(p, p.seq_len[b]);
+        kvh = int(off / plan.n);
+        v0 = int(off % plan.n);
+        cnt = int(left < plan.n - v0 ? left : plan.n - v0);
+    }
+    __device__ bool next() {
+        left -= cnt;
+        flat += cnt;
+        if (left <= 0) return false;
+        v0 = 0;
+        if (++kvh == p.Hkv) {
+            kvh = 0;
+            do {                            // the range ends inside the list: b stays below B
+                plan = make_plan(p, p.seq_len[++b]);
+            } while (plan.n == 0);
+        }
+        cnt = int(left < plan.n ? left : plan.n);
+        return true;
+    }
+};
+
+// ------------------------------------------------------- warp-level MMA
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+    if constexpr (F16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+                     "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+                     "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D, int NT, bool F16>
+__global__ void __launch_bounds__(kNT, kCtasPerSm)
+decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                    const PgParams p) {
+    using C = PgCfg<D, NT>;
+    using H = H16<F16>;
+    using T = typename H::T;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024 - (ptx::smem_addr(smem_raw) & 1023)) & 1023);
+    Misc *ms = reinterpret_cast<Misc *>(smem + C::OFF_MISC);
+    volatile int *abort = &ms->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cta = blockIdx.x, ctas = gridDim.x;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::SLOTS; ++s) {
+            ptx::mbar_init(&ms->full_k[s], 1);
+            ptx::mbar_init(&ms->full_v[s], 1);
+            ptx::mbar_init(&ms->empty_k[s], 1);
+            ptx::mbar_init(&ms->empty_v[s], 1);
+        }
+        ptx::fence_barrier_init();
+        ms->abort = 0;
+    }
+    // programmatic dependent launch: nothing global is read or written before
+    // the previous kernel (an append, say) has completed
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+
+    // ---- the flat list's length, this CTA's range and where it starts.
+    //      Sequences with nothing to attend to are dealt out over the CTAs:
+    //      length 0 writes zeros, a length outside the table is reported and
+    //      its output left as it was.
+    long long total = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kNT) {
+        const int b = b0 + threadIdx.x;
+        if (b < p.B) {
+            const int len = p.seq_len[b];
+            const Plan r = make_plan(p, len);
+            total += r.n;
+            if (r.n == 0 && b % ctas == cta) {
+                if (len != 0) {
+                    raise_device_error(p.err, kDevCheck);
+                } else {
+                    for (int h = 0; h < p.Hkv * p.G; ++h) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + b * p.o_sb +
+                                                               h * p.o_sh);
+                        for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+    if (lane == 0) ms->warp_sum[warp] = total;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < kNT / 32; ++w) total += ms->warp_sum[w];
+    __syncthreads();
+    total *= p.Hkv;
+    long long per = (total + ctas - 1) / ctas;
+    if (per < kMinChunks) per = kMinChunks;
+    const long long f0 = per * cta;
+    if (f0 >= total) return;
+    const long long f1 = f0 + per < total ? f0 + per : total;
+    long long carry = 0;                               // chunks of the sequences before this tile
+    for (int b0 = 0; b0 < p.B; b0 += kNT) {
+        const int b = b0 + threadIdx.x;
+        const long long n = b < p.B ? make_plan(p, p.seq_len[b]).n : 0;
+        long long inc = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += up;
+        }
+        if (lane == 31) ms->warp_sum[warp] = inc;
+        __syncthreads();
+        long long before = carry, tile = 0;
+        for (int w = 0; w < kNT / 32; ++w) {
+            if (w < warp) before += ms->warp_sum[w];
+            tile += ms->warp_sum[w];
+        }
+        before += inc - n;
+        if (n > 0 && f0 >= before * p.Hkv && f0 < (before + n) * p.Hkv) {
+            ms->start_b = b;
+            ms->start_off = f0 - before * p.Hkv;
+        }
+        carry += tile;
+        __syncthreads();
+        if (carry * p.Hkv > f0) break;
+    }
+
+    Walk w(p, ms->start_b, ms->start_off, f0, f1 - f0);
+    int f = 0;                                         // chunk number within the CTA's range
+
+    if (warp >= kCW) {
+        // ------------------------------------------------ producer warps
+        const bool is_k = warp == kCW;
+        const CUtensorMap *tm = is_k ? &tk : &tv;
+        uint64_t *full = is_k ? ms->full_k : ms->full_v;
+        uint64_t *empty = is_k ? ms->empty_k : ms->empty_v;
+        uint8_t *ring = smem + (is_k ? C::OFF_K : C::OFF_V);
+        if (lane == 0) ptx::prefetch_tmap(tm);
+        const uint64_t pol = ptx::l2_policy_evict_first();
+        const int nb = kChunk / p.BR;                  // boxes per chunk: 1, 2 or 4
+        const unsigned bits = (1u << nb) - 1u;
+        const int box_bytes = p.BR * D * 2;
+        const int group = 32 / nb;                     // chunks whose boxes the lanes look up at once
+        bool ok = true;
+        do {
+            const int32_t *row = p.table + (long long)w.b * p.table_stride;
+            for (int g0 = 0; ok && g0 < w.cnt; g0 += group) {
+                const int gi = g0 + lane / nb;
+                int page = 0, prow = 0;
+                bool need = false;
+                if (gi < w.cnt) {
+                    const int pos = chunk_of(w.plan, w.v0 + gi) * kChunk + (lane % nb) * p.BR;
+                    // a box without a visible position is not read: its page
+                    // may not exist (past the end) or may be free again
+                    need = pos < w.plan.len && (pos + p.BR > w.plan.lo || pos < w.plan.s_end);
+                    if (need) {
+                        page = row[pos / p.S];
+                        prow = pos % p.S;
+                    }
+                }
+                const bool bad = need && (page < 0 || page >= p.num_pages);
+                if (bad) {
+                    raise_device_error(p.err, kDevCheck);
+                    page = p.num_pages;                // outside the map: the copy fills zeros
+                }
+                const unsigned needs = __ballot_sync(0xffffffffu, need);
+                const unsigned bads = __ballot_sync(0xffffffffu, bad);
+                const int in_group = imin(group, w.cnt - g0);
+                for (int i = 0; i < in_group; ++i, ++f) {
+                    const int s = f % C::SLOTS;
+                    if (f >= C::SLOTS &&
+                        !__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(
+                                                     &empty[s], ((f / C::SLOTS) - 1) & 1, p.err, abort))) {
+                        ok = false;
+                        break;
+                    }
+                    const unsigned mine = (needs >> (i * nb)) & bits;
+                    if (lane == 0) {
+                        if (is_k) ms->bad[s] = ((bads >> (i * nb)) & bits) != 0;
+                        ptx::mbar_arrive_expect_tx(&full[s], __popc(mine) * box_bytes);
+                    }
+                    __syncwarp();
+                    const int pg = __shfl_sync(0xffffffffu, page, i * nb + lane % nb);
+                    const int pr = __shfl_sync(0xffffffffu, prow, i * nb + lane % nb);
+                    if (lane < nb && ((mine >> lane) & 1u))
+                        ptx::tma_load_5d(ring + s * C::TILE + lane * box_bytes, tm, 0, pr, 0, w.kvh, pg,
+                                         &full[s], pol);
+                }
+            }
+        } while (ok && w.next());
+        // after a timeout: let the copies already issued land (bounded) before
+        // the CTA's shared memory is released
+        if (!ok && lane == 0)
+            for (int i = imax(0, f - C::SLOTS); i < f; ++i)
+                ptx::mbar_wait(&full[i % C::SLOTS], (i / C::SLOTS) & 1, nullptr);
+        return;
+    }
+
+    // ---------------------------------------------------- consumer warps
+    float *mg = reinterpret_cast<float *>(smem + C::OFF_M);
+    float *mml = reinterpret_cast<float *>(smem + C::OFF_ML);
+    const int quad = lane >> 2, pair = lane & 3;
+    // ldmatrix lane addresses (relative to a slot): rows and the swizzled
+    // 16-byte column; a k-step moves bits 5-6 of the column, a panel adds psz
+    const int psz = p.BR * 128;
+    uint32_t k_row[2], v_row[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int rk = t * 16 + (lane & 15);
+        const int rv = t * 16 + (lane & 7) + ((lane >> 4) & 1) * 8;
+        k_row[t] = (rk / p.BR) * (C::PANELS * psz) + (rk % p.BR) * 128 +
+                   ((((lane >> 4) & 1) ^ (lane & 7)) << 4);
+        v_row[t] = (rv / p.BR) * (C::PANELS * psz) + (rv % p.BR) * 128 +
+                   ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
+    }
+    const uint32_t k_base = ptx::smem_addr(smem + C::OFF_K), v_base = ptx::smem_addr(smem + C::OFF_V);
+
+    // after a timeout a warp computes nothing more but still walks the
+    // segments: the other warps meet it at their barriers, and every unit's
+    // ticket is counted up and reset as usual
+    int dead = 0;
+    do {
+        // ---- q of the unit's heads as MMA B operands (heads are columns)
+        uint32_t qf[NT][D / 16][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int h = nt * 8 + quad;
+            const T *qp = static_cast<const T *>(p.q) + w.b * p.q_sb +
+                          (long long)(w.kvh * p.G + h) * p.q_sh + pair * 2;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                qf[nt][kk][0] = h < p.G ? *reinterpret_cast<const uint32_t *>(qp + kk * 16) : 0u;
+                qf[nt][kk][1] = h < p.G ? *reinterpret_cast<const uint32_t *>(qp + kk * 16 + 8) : 0u;
+            }
+        }
+        float m[NT][2], l[NT][2], acc[NT][D / 16][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
+        }
+        int bad = dead;
+
+        const int f_end = f + w.cnt;
+        // this warp's chunks: the range's chunk number modulo the warps
+        for (int fc = f + ((warp - f) & (kCW - 1)); fc < f_end && !dead; fc += kCW) {
+            const int s = fc % C::SLOTS;
+            const uint32_t parity = (fc / C::SLOTS) & 1;
+            const int base = chunk_of(w.plan, w.v0 + (fc - f)) * kChunk;
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&ms->full_k[s], parity, p.err, abort))) {
+                bad = dead = 1;
+                break;
+            }
+            bad |= ms->bad[s];
+
+            // ---- S^T = K q^T
+            float sc[2][NT][4];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    sc[t][nt][0] = sc[t][nt][1] = sc[t][nt][2] = sc[t][nt][3] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    uint32_t a[4];
+                    ldsm4(a, k_base + s * C::TILE + (kk >> 2) * psz + (k_row[t] ^ ((kk & 3) << 5)));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma16816<F16>(sc[t][nt], a, qf[nt][kk][0], qf[nt][kk][1]);
+                }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&ms->empty_k[s]);
+
+            // ---- visibility of the chunk's 32 positions
+            unsigned vis;
+            {
+                const int pos = base + lane;
+                vis = __ballot_sync(0xffffffffu, pos < w.plan.len && (pos >= w.plan.lo || pos < w.plan.s_end));
+            }
+            // ---- online softmax (base 2) per head column
+            uint32_t ph[2][NT][2], pl[2][NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float x[2][4];
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[t][i] = (vis >> (t * 16 + quad + (i >> 1) * 8)) & 1u ? sc[t][nt][i] * p.c_log2
+                                                                               : -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float mx = fmaxf(fmaxf(x[0][j], x[0][j + 2]), fmaxf(x[1][j], x[1][j + 2]));
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1)
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                    const float mn = fmaxf(m[nt][j], mx);
+                    const float alpha = mn == -INFINITY ? 1.f : ptx::ex2(m[nt][j] - mn);
+                    m[nt][j] = mn;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int i = j; i < 4; i += 2) {
+                            const bool v = (vis >> (t * 16 + quad + (i >> 1) * 8)) & 1u;
+                            x[t][i] = v && mn != -INFINITY ? ptx::ex2(x[t][i] - mn) : 0.f;
+                            sum += x[t][i];
+                        }
+                    l[nt][j] = l[nt][j] * alpha + sum;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        acc[nt][i][j] *= alpha;
+                        acc[nt][i][j + 2] *= alpha;
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float a = x[t][2 * r], b = x[t][2 * r + 1];
+                        const uint32_t hi = H::pack(a, b);
+                        ph[t][nt][r] = transpose8x8(hi);
+                        pl[t][nt][r] = transpose8x8(H::pack(a - H::lo(hi), b - H::hi(hi)));
+                    }
+            }
+
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&ms->full_v[s], parity, p.err, abort))) {
+                bad = dead = 1;
+                break;
+            }
+            // ---- O^T += V^T P^T.  Rows that are not visible may hold anything
+            //      (NaN times a zero weight is NaN): their values are cleared.
+            const bool part = vis != 0xffffffffu;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+                if (part) {
+                    const unsigned v = vis >> (t * 16 + 2 * pair);
+                    keep0 = (v & 1u ? 0x0000ffffu : 0u) | (v & 2u ? 0xffff0000u : 0u);
+                    keep1 = (v & 0x100u ? 0x0000ffffu : 0u) | (v & 0x200u ? 0xffff0000u : 0u);
+                }
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    uint32_t a[4];
+                    ldsm4t(a, v_base + s * C::TILE + (i >> 2) * psz + (v_row[t] ^ ((i & 3) << 5)));
+                    if (part) {
+                        a[0] &= keep0;
+                        a[1] &= keep0;
+                        a[2] &= keep1;
+                        a[3] &= keep1;
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma16816<F16>(acc[nt][i], a, ph[t][nt][0], ph[t][nt][1]);
+                        mma16816<F16>(acc[nt][i], a, pl[t][nt][0], pl[t][nt][1]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&ms->empty_v[s]);
+        }
+        f = f_end;
+
+        // ---- the four warps' (max, sum, O) -> one per head
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1)
+                    l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], off);
+                const int h = nt * 8 + pair * 2 + j;
+                if (quad == 0) {
+                    mml[(warp * C::HP + h) * 2] = m[nt][j];
+                    mml[(warp * C::HP + h) * 2 + 1] = l[nt][j];
+                }
+                float *row = mg + (warp * C::HP + h) * C::LDM;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    row[i * 16 + quad] = acc[nt][i][j];
+                    row[i * 16 + 8 + quad] = acc[nt][i][j + 2];
+                }
+            }
+        if (lane == 0) ms->warp_bad[warp] = bad;
+        ptx::named_barrier_sync(1, kCW * 32);
+        bad = ms->warp_bad[0] | ms->warp_bad[1] | ms->warp_bad[2] | ms->warp_bad[3];
+
+        const bool whole = w.v0 == 0 && w.cnt == w.plan.n;
+        // a range holds at most one segment that starts inside its unit (slot 0)
+        // and one that starts at its unit's head and is cut (slot 1)
+        const int slot = 2 * cta + (w.v0 == 0 ? 1 : 0);
+        float *po = p.part_o + (size_t)slot * C::HP * D;
+        float *pml = p.part_ml + (size_t)slot * C::HP * 2;
+        for (int e = threadIdx.x; e < p.G * (D / 4); e += kCW * 32) {
+            const int h = e / (D / 4), d = (e % (D / 4)) * 4;
+            float M = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kCW; ++i) M = fmaxf(M, mml[(i * C::HP + h) * 2]);
+            float L = 0.f;
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kCW; ++i) {
+                const float mi = mml[(i * C::HP + h) * 2], li = mml[(i * C::HP + h) * 2 + 1];
+                // a warp that saw nothing, or only scores of -inf, adds nothing
+                // (its sum is zero, or NaN if one of its scores was)
+                const float wt = mi == -INFINITY ? 0.f : ptx::ex2(mi - M);
+                L += mi == -INFINITY ? li : wt * li;
+                const float4 x = *reinterpret_cast<const float4 *>(mg + (i * C::HP + h) * C::LDM + d);
+                O.x += wt * x.x;
+                O.y += wt * x.y;
+                O.z += wt * x.z;
+                O.w += wt * x.w;
+            }
+            if (whole) {
+                if (!bad) {
+                    const float inv = 1.f / L;
+                    T *dst = static_cast<T *>(p.o) + w.b * p.o_sb + (long long)(w.kvh * p.G + h) * p.o_sh + d;
+                    *reinterpret_cast<uint2 *>(dst) =
+                        make_uint2(H::pack(O.x * inv, O.y * inv), H::pack(O.z * inv, O.w * inv));
+                }
+            } else {
+                *reinterpret_cast<float4 *>(po + h * D + d) = O;
+                if (d == 0)                            // a NaN maximum marks a segment with a bad page
+                    *reinterpret_cast<float2 *>(pml + h * 2) = make_float2(bad ? NAN : M, L);
+            }
+        }
+        if (!whole) {
+            const int unit = w.b * p.Hkv + w.kvh;
+            const long long u0 = w.flat - w.v0;        // flat index of the unit's first chunk
+            const int c0 = int(u0 / per), c1 = int((u0 + w.plan.n - 1) / per);
+            __threadfence();
+            ptx::named_barrier_sync(1, kCW * 32);
+            if (threadIdx.x == 0) ms->last = atomicAdd(&p.tickets[unit], 1u) == unsigned(c1 - c0);
+            ptx::named_barrier_sync(1, kCW * 32);
+            if (ms->last) {
+                __threadfence();
+                for (int e = threadIdx.x; e < p.G * (D / 4); e += kCW * 32) {
+                    const int h = e / (D / 4), d = (e % (D / 4)) * 4;
+                    float M = -INFINITY, L = 0.f;
+                    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+                    bool skip = false;
+                    constexpr int U = 4;               // partials in flight
+                    for (int c = c0; c <= c1; c += U) {
+                        float2 ml[U];
+                        float4 x[U];
+#pragma unroll
+                        for (int i = 0; i < U; ++i) {
+                            ml[i] = make_float2(-INFINITY, 0.f);
+                            x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (c + i <= c1) {
+                                // the CTA that holds the unit's head left it in slot 1
+                                const size_t sl = 2 * size_t(c + i) + (c + i == c0 ? 1 : 0);
+                                ml[i] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + sl * C::HP * 2) + h);
+                                x[i] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + sl * C::HP * D + h * D + d));
+                            }
+                        }
+                        float mn = M;
+#pragma unroll
+                        for (int i = 0; i < U; ++i) {
+                            skip = skip || ml[i].x != ml[i].x;
+                            mn = fmaxf(mn, ml[i].x);
+                        }
+                        const float keep = M == -INFINITY ? 1.f : ptx::ex2(M - mn);
+                        L *= keep;
+                        O.x *= keep;
+                        O.y *= keep;
+                        O.z *= keep;
+                        O.w *= keep;
+                        M = mn;
+#pragma unroll
+                        for (int i = 0; i < U; ++i) {
+                            const float wt = ml[i].x == -INFINITY ? 0.f : ptx::ex2(ml[i].x - mn);
+                            L += ml[i].x == -INFINITY ? ml[i].y : wt * ml[i].y;
+                            O.x += wt * x[i].x;
+                            O.y += wt * x[i].y;
+                            O.z += wt * x[i].z;
+                            O.w += wt * x[i].w;
+                        }
+                    }
+                    if (!skip) {
+                        const float inv = 1.f / L;
+                        T *dst = static_cast<T *>(p.o) + w.b * p.o_sb +
+                                 (long long)(w.kvh * p.G + h) * p.o_sh + d;
+                        *reinterpret_cast<uint2 *>(dst) =
+                            make_uint2(H::pack(O.x * inv, O.y * inv), H::pack(O.z * inv, O.w * inv));
+                    }
+                }
+                if (threadIdx.x == 0) p.tickets[unit] = 0u;   // ready for the next call
+            }
+        }
+        ptx::named_barrier_sync(1, kCW * 32);          // the merge rows may be written again
+    } while (w.next());
+}
+
+// 5D map {64 channels, S rows, D / 64 panels, Hkv, pages} over a cache with
+// element strides (page, head, token); box: BR rows x D channels of one head,
+// stored as panels of BR 128-byte rows (128-byte swizzle).
+bool page_tmap(CUtensorMap *m, const void *base, int P, int Hkv, int S, int D, const long long st[3],
+               int BR, bool f16) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t gdim[5] = {64, cuuint64_t(S), cuuint64_t(D / 64), cuuint64_t(Hkv), cuuint64_t(P)};
+    const cuuint64_t gstride[4] = {cuuint64_t(st[2]) * 2, 128, cuuint64_t(st[1]) * 2, cuuint64_t(st[0]) * 2};
+    const cuuint32_t box[5] = {64, cuuint32_t(BR), cuuint32_t(D / 64), 1, 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+              const_cast<void *>(base), gdim, gstride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NT, bool F16>
+attn_status_t launch_paged(const Ctx &c, const CUtensorMap &tk, const CUtensorMap &tv,
+                           const PgParams &p) {
+    using C = PgCfg<D, NT>;
+    static int done_mask = 0;
+    auto kern = decode_paged_kernel<D, NT, F16>;
+    if (!ensure_smem_attr(reinterpret_cast<const void *>(kern), C::SMEM, c.device, &done_mask))
+        return ATTN_ERR_RESOURCE;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(imin(kCtasPerSm * c.sm_count, kMaxCtas));
+    cfg.blockDim = dim3(kNT);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = c.stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, tk, tv, p) != cudaSuccess) {
+        cudaGetLastError();
+        return ATTN_ERR_CUDA;
+    }
+    return launch_status(kFamDecodePaged);
+}
+
+size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
+
+}  // namespace
+
+size_t decode_paged_workspace_bytes(int B, int G, int Hkv, int D) {
+    const size_t hp = G <= 8 ? 8 : 16;
+    return align256(size_t(B) * Hkv * sizeof(unsigned)) +
+           align256(size_t(2) * kMaxCtas * hp * D * sizeof(float)) +
+           align256(size_t(2) * kMaxCtas * hp * 2 * sizeof(float));
+}
+
+attn_status_t decode_paged(const Ctx &c, attn_dtype_t dt, const PagedDecode &a) {
+    const bool f16 = dt == ATTN_F16;
+    PgParams p{};
+    p.BR = a.S % 32 == 0 ? 32 : a.S % 16 == 0 ? 16 : 8;
+    CUtensorMap tk, tv;
+    if (!page_tmap(&tk, a.k, a.P, a.Hkv, a.S, a.D, a.k_st, p.BR, f16) ||
+        !page_tmap(&tv, a.v, a.P, a.Hkv, a.S, a.D, a.v_st, p.BR, f16))
+        return ATTN_ERR_UNSUPPORTED;
+    p.q = a.q;
+    p.o = a.o;
+    p.q_sb = a.q_st[0]; p.q_sh = a.q_st[1];
+    p.o_sb = a.o_st[0]; p.o_sh = a.o_st[1];
+    p.table = a.table;
+    p.table_stride = a.table_stride;
+    p.seq_len = a.seq_len;
+    p.B = a.B; p.Hkv = a.Hkv; p.G = a.G;
+    p.S = a.S;
+    p.max_pages = a.max_pages; p.num_pages = a.P;
+    p.window = a.window; p.sinks = a.sinks;
+    p.c_log2 = a.scale * kLog2e;
+    const size_t hp = a.G <= 8 ? 8 : 16;
+    uint8_t *w = static_cast<uint8_t *>(a.ws);
+    p.tickets = reinterpret_cast<unsigned *>(w);
+    w += align256(size_t(a.B) * a.Hkv * sizeof(unsigned));
+    p.part_o = reinterpret_cast<float *>(w);
+    w += align256(size_t(2) * kMaxCtas * hp * a.D * sizeof(float));
+    p.part_ml = reinterpret_cast<float *>(w);
+    p.err = c.err;
+    if (a.D == 128) {
+        if (a.G <= 8) return f16 ? launch_paged<128, 1, true>(c, tk, tv, p) : launch_paged<128, 1, false>(c, tk, tv, p);
+        return f16 ? launch_paged<128, 2, true>(c, tk, tv, p) : launch_paged<128, 2, false>(c, tk, tv, p);
+    }
+    if (a.G <= 8) return f16 ? launch_paged<64, 1, true>(c, tk, tv, p) : launch_paged<64, 1, false>(c, tk, tv, p);
+    return f16 ? launch_paged<64, 2, true>(c, tk, tv, p) : launch_paged<64, 2, false>(c, tk, tv, p);
+}
+
+}  // namespace attn

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -26,7 +27,9 @@ enum KernelFamily : int {
     kFamTcNa = 5,
     kFamKvAppend = 6,
     kFamDebug = 7,
-    kFamCount = 8,
+    kFamDecodePaged = 8,
+    kFamKvPages = 9,
+    kFamCount = 10,
 };
 
 void count_launch(int family);
@@ -46,6 +49,7 @@ bool ensure_smem_attr(const void *func, size_t bytes, int device, int *done_mask
 bool make_tmap(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint32_t *box,
                bool f16 = false);
 bool tma_encode_available();
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();   // nullptr if the driver has none
 
 // Element strides of a [B, heads, N, D] tensor with D contiguous.
 struct TensorStrides {
@@ -80,6 +84,62 @@ attn_status_t decode_gqa(const Ctx &c, attn_dtype_t dt, const void *q, const voi
                          int Lmax, int D, float scale, void *ws, size_t ws_bytes,
                          bool ring = false);
 
+// Paged KV cache.  Strides are element strides; pages [P][Hkv][S][D] in any
+// order of (page, head, token) with D contiguous.
+struct PagedDecode {
+    const void *q, *k, *v;
+    void *o;
+    const int32_t *table, *seq_len;
+    int B, G, Hkv, D, P, S, max_pages;
+    long long table_stride;
+    long long q_st[2], o_st[2];          // (batch, head)
+    long long k_st[3], v_st[3];          // (page, head, token)
+    int window, sinks;
+    float scale;
+    void *ws;
+};
+size_t decode_paged_workspace_bytes(int B, int G, int Hkv, int D);
+attn_status_t decode_paged(const Ctx &c, attn_dtype_t dt, const PagedDecode &a);
+
+struct PagedAppend {
+    void *k, *v;
+    const void *kn, *vn;
+    const int32_t *table;
+    int32_t *seq_len;
+    const int32_t *new_len;              // nullptr: T rows for every sequence
+    int B, T, Hkv, D, P, S, max_pages;
+    long long table_stride;
+    long long k_st[3], v_st[3];          // (page, head, token)
+    long long kn_st[3], vn_st[3];        // (batch, head, token)
+    int advance;
+};
+attn_status_t kv_append_paged(const Ctx &c, attn_dtype_t dt, const PagedAppend &a);
+
+struct PagesCopy {
+    void *k, *v;
+    const int32_t *src, *dst, *count;    // count: nullptr for n
+    int n, layers, Hkv, S, D, P;
+    long long k_st[4], v_st[4];          // (layer, page, head, token)
+};
+attn_status_t kv_pages_copy(const Ctx &c, attn_dtype_t dt, const PagesCopy &a);
+
+struct PageTable {
+    int32_t *table;
+    long long stride;
+    int B, max_pages, P, S;
+};
+size_t kv_pages_workspace_bytes(int P);
+attn_status_t kv_pages_reserve(const Ctx &c, const PageTable &t, const int32_t *seq_len,
+                               const int32_t *add, int32_t *refs, void *ws);
+attn_status_t kv_pages_free(const Ctx &c, const PageTable &t, const int32_t *seq_len,
+                            int32_t *refs, int window, int sinks);
+attn_status_t kv_pages_fork(const Ctx &c, const PageTable &t, int32_t *seq_len, int32_t *refs,
+                            const int32_t *src, const int32_t *dst, int n, int32_t *copy_src,
+                            int32_t *copy_dst, void *ws);
+attn_status_t kv_pages_compact(const Ctx &c, const PageTable &t, const int32_t *refs,
+                               int32_t *new_table, long long new_stride, int32_t *new_refs,
+                               int32_t *copy_src, int32_t *copy_dst, int32_t *count, void *ws);
+
 // tcgen05 (tensor-core) flash attention, bf16 or f16: full and neighborhood.
 // st: strides of q, k, v, o (nullptr: contiguous).
 attn_status_t tc_full(const Ctx &c, attn_dtype_t dt, const void *q, const void *k, const void *v,
@@ -92,6 +152,14 @@ attn_status_t tc_causal_gqa(const Ctx &c, attn_dtype_t dt, const void *q, const 
 attn_status_t simt_causal_gqa(const Ctx &c, attn_dtype_t dt, const void *q, const void *k,
                               const void *v, void *o, int B, int Hq, int Hkv, int N, int D,
                               float scale, const TensorStrides *st = nullptr);
+// Sliding window with sinks: queries are the last Nq of Nkv positions.
+attn_status_t tc_causal_window(const Ctx &c, attn_dtype_t dt, const void *q, const void *k,
+                               const void *v, void *o, int B, int Hq, int Hkv, int Nq, int Nkv,
+                               int D, int window, int sinks, float scale, const TensorStrides *st);
+attn_status_t simt_causal_window(const Ctx &c, attn_dtype_t dt, const void *q, const void *k,
+                                 const void *v, void *o, int B, int Hq, int Hkv, int Nq, int Nkv,
+                                 int D, int window, int sinks, float scale,
+                                 const TensorStrides *st);
 attn_status_t tc_na3d(const Ctx &c, attn_dtype_t dt, const void *q, const void *k, const void *v,
                       void *o, int B, int H, int T, int Hg, int W, int D, const int kernel[3],
                       float scale);
