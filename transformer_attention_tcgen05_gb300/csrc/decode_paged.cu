@@ -466,7 +466,9 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
 #pragma unroll
                         for (int i = j; i < 4; i += 2) {
                             const bool v = (vis >> (t * 16 + quad + (i >> 1) * 8)) & 1u;
-                            x[t][i] = v && mn != -INFINITY ? ptx::ex2(x[t][i] - mn) : 0.f;
+                            // no finite score so far: -inf weighs nothing, NaN stays NaN
+                            x[t][i] = !v || (mn == -INFINITY && x[t][i] == -INFINITY)
+                                          ? 0.f : ptx::ex2(x[t][i] - mn);
                             sum += x[t][i];
                         }
                     l[nt][j] = l[nt][j] * alpha + sum;

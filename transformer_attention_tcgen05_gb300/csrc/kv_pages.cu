@@ -1,0 +1,821 @@
+// The pages of a paged KV cache: appending rows, and the allocator (reserve,
+// free, fork, compact) with the page copies it asks for.
+//
+// The allocator's whole state is on the device: page_table [B][max_pages]
+// (-1: no page) and page_refs [P], the number of table entries that name a
+// page (0: free).  The lowest free page is always taken first and requests are
+// served in (row, entry) order, so the result of a call depends on its inputs
+// alone, never on the order in which threads or atomics run, and a captured
+// graph can allocate.  Nothing here is read back by the host.
+//
+// These calls move a few kilobytes of tables, so they are bound by latency,
+// not bandwidth: a call that has to number its requests (reserve, fork,
+// compact) is one cluster of 8 CTAs whose barriers and distributed shared
+// memory replace a grid-wide scan in several launches.  An append and a page
+// copy move cache rows and are bound by HBM: 16-byte vectors, several in
+// flight per thread.
+#include "common.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace attn {
+namespace {
+
+// Launches with the programmatic-dependent attribute: the kernel may start
+// while the one before it finishes, and waits for it (griddep_wait) before its
+// first global access.
+template <typename... P, typename... A>
+attn_status_t launch_pdl(const Ctx &c, void (*kern)(P...), dim3 grid, int threads, int cluster,
+                         size_t smem, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = c.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kern, P(args)...) != cudaSuccess) {
+        cudaGetLastError();
+        return ATTN_ERR_CUDA;
+    }
+    return launch_status(kFamKvPages);
+}
+
+// ------------------------------------------------------------------ append
+
+struct AppendParams {
+    uint8_t *k, *v;
+    const uint8_t *kn, *vn;
+    const int32_t *table;
+    int32_t *seq_len;
+    const int32_t *new_len;
+    int T, Hkv, S, P, max_pages;
+    long long table_stride;
+    long long k_st[3], v_st[3], kn_st[3], vn_st[3];   // bytes
+    int vpr_log;                                      // log2 of the 16-byte vectors per row
+    int tiles;                                        // token tiles per sequence
+    int advance;
+    unsigned *err;
+};
+
+// Rows the call appends to sequence b at position `len`, or -1 if the request
+// does not fit the table.
+__device__ __forceinline__ int append_count(const AppendParams &p, int b, int len) {
+    const int n = p.new_len ? p.new_len[b] : p.T;
+    if (len < 0 || n < 0 || n > p.T || (long long)len + n > (long long)p.max_pages * p.S) return -1;
+    return n;
+}
+
+// One CTA copies a tile of TB tokens (all KV heads, K and V) of one sequence.
+// ONE: a single tile per sequence; the CTA that wrote it advances the length.
+template <int TB, bool ONE>
+__global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    __shared__ long long s_k[TB], s_v[TB];             // byte offset of a token's row of head 0, -1: none
+    __shared__ int s_bad;
+    const int b = blockIdx.x / p.tiles, t0 = (blockIdx.x % p.tiles) * TB;
+    const int len = p.seq_len[b];
+    const int n = append_count(p, b, len);
+    if (n < 0) {
+        if (threadIdx.x == 0 && t0 == 0) raise_device_error(p.err, kDevCheck);
+        return;
+    }
+    if (t0 >= n) return;
+    if (threadIdx.x == 0) s_bad = 0;
+    __syncthreads();
+    const int nt = imin(TB, n - t0);
+    if (threadIdx.x < TB) {
+        long long ok = -1, ov = -1;
+        if (int(threadIdx.x) < nt) {
+            const int pos = len + t0 + threadIdx.x;
+            const int page = p.table[b * p.table_stride + pos / p.S], row = pos % p.S;
+            if (page >= 0 && page < p.P) {
+                ok = page * p.k_st[0] + row * p.k_st[2];
+                ov = page * p.v_st[0] + row * p.v_st[2];
+            } else {
+                raise_device_error(p.err, kDevCheck);
+                s_bad = 1;
+            }
+        }
+        s_k[threadIdx.x] = ok;
+        s_v[threadIdx.x] = ov;
+    }
+    __syncthreads();
+    // vector e of the tile: column e % VPR of token (e / VPR) % TB of head e / (VPR TB)
+    const int vpr = 1 << p.vpr_log, total = (TB * p.Hkv) << p.vpr_log;
+    const uint8_t *kn = p.kn + b * p.kn_st[0] + (long long)t0 * p.kn_st[2];
+    const uint8_t *vn = p.vn + b * p.vn_st[0] + (long long)t0 * p.vn_st[2];
+    constexpr int U = 4;
+    for (int e0 = threadIdx.x; e0 < total; e0 += U * 256) {
+        uint4 xk[U], xv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int e = e0 + u * 256;
+            const int c = e & (vpr - 1), t = (e >> p.vpr_log) % TB, h = (e >> p.vpr_log) / TB;
+            if (e < total && s_k[t] >= 0) {
+                xk[u] = *reinterpret_cast<const uint4 *>(kn + h * p.kn_st[1] + t * p.kn_st[2] + c * 16);
+                xv[u] = *reinterpret_cast<const uint4 *>(vn + h * p.vn_st[1] + t * p.vn_st[2] + c * 16);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int e = e0 + u * 256;
+            const int c = e & (vpr - 1), t = (e >> p.vpr_log) % TB, h = (e >> p.vpr_log) / TB;
+            if (e < total && s_k[t] >= 0) {
+                *reinterpret_cast<uint4 *>(p.k + s_k[t] + h * p.k_st[1] + c * 16) = xk[u];
+                *reinterpret_cast<uint4 *>(p.v + s_v[t] + h * p.v_st[1] + c * 16) = xv[u];
+            }
+        }
+    }
+    if (ONE && p.advance && threadIdx.x == 0 && !s_bad) p.seq_len[b] = len + n;
+}
+
+// Advances the lengths after a tiled append (every tile has read them by now):
+// one warp per sequence, which stays where it was if one of its pages was bad.
+__global__ void __launch_bounds__(128) advance_kernel(const AppendParams p, int B) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int b = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (b >= B) return;
+    const int len = p.seq_len[b];
+    const int n = append_count(p, b, len);
+    if (n <= 0) return;
+    bool ok = true;
+    for (int i = len / p.S + lane; i <= (len + n - 1) / p.S; i += 32) {
+        const int page = p.table[b * p.table_stride + i];
+        ok = ok && page >= 0 && page < p.P;
+    }
+    if (__all_sync(0xffffffffu, ok) && lane == 0) p.seq_len[b] = len + n;
+}
+
+// -------------------------------------------------------------------- copy
+
+struct CopyParams {
+    uint8_t *k, *v;
+    const int32_t *src, *dst, *count;
+    int n, P;
+    int vecs;                                          // 16-byte vectors of a page side
+    int pieces;                                        // pieces of kPiece vectors per page side
+    int sides;                                         // layers * 2
+    int vpr, S;                                        // vectors per row, rows per head
+    long long k_st[4], v_st[4];                        // bytes (layer, page, head, token)
+    unsigned *err;
+};
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 4;
+constexpr int kPiece = kCopyThreads * kCopyUnroll;     // 16 KB
+
+// A persistent grid walks the pieces (16 KB of one page of one layer's K or V)
+// of all pairs.  DENSE: a page is one contiguous block.
+template <bool DENSE>
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int n = p.count ? imax(0, imin(*p.count, p.n)) : p.n;
+    const int per_pair = p.sides * p.pieces;
+    const long long total = (long long)n * per_pair;
+    for (long long it = blockIdx.x; it < total; it += gridDim.x) {
+        const int pair = int(it / per_pair), rest = int(it % per_pair);
+        const int side = rest / p.pieces, piece = rest % p.pieces;
+        const int s = p.src[pair], d = p.dst[pair];
+        if ((s == -1 && d == -1) || s == d) continue;
+        if (s < 0 || s >= p.P || d < 0 || d >= p.P) {
+            if (rest == 0 && threadIdx.x == 0) raise_device_error(p.err, kDevCheck);
+            continue;
+        }
+        const bool is_v = side & 1;
+        uint8_t *base = (is_v ? p.v : p.k) + (side >> 1) * (is_v ? p.v_st[0] : p.k_st[0]);
+        const long long pst = is_v ? p.v_st[1] : p.k_st[1];
+        const uint8_t *from = base + s * pst;
+        uint8_t *to = base + d * pst;
+        uint4 x[kCopyUnroll];
+        long long off[kCopyUnroll];
+#pragma unroll
+        for (int u = 0; u < kCopyUnroll; ++u) {
+            const int e = piece * kPiece + u * kCopyThreads + threadIdx.x;
+            if (DENSE) {
+                off[u] = (long long)e * 16;
+            } else {
+                const int row = e / p.vpr;
+                off[u] = (row / p.S) * (is_v ? p.v_st[2] : p.k_st[2]) +
+                         (row % p.S) * (is_v ? p.v_st[3] : p.k_st[3]) + (e % p.vpr) * 16;
+            }
+            if (e < p.vecs) x[u] = *reinterpret_cast<const uint4 *>(from + off[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kCopyUnroll; ++u)
+            if (piece * kPiece + u * kCopyThreads + int(threadIdx.x) < p.vecs)
+                *reinterpret_cast<uint4 *>(to + off[u]) = x[u];
+    }
+}
+
+// --------------------------------------------------------------- allocator
+
+constexpr int kClu = 8;                                // CTAs of the allocator's cluster
+constexpr int kAT = 512;                               // threads per CTA
+constexpr int kAW = kAT / 32;
+
+struct AllocShared {
+    int warp[kAW];
+    int val[8];                                        // one word per cluster exchange
+};
+
+// Exclusive prefix of x over the CTA's threads; *total: the CTA's sum.
+__device__ __forceinline__ int block_scan(AllocShared &sh, int x, int *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += up;
+    }
+    if (lane == 31) sh.warp[warp] = inc;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kAW; ++w) {
+        const int s = sh.warp[w];
+        if (w < warp) before += s;
+        all += s;
+    }
+    __syncthreads();
+    *total = all;
+    return before + inc - x;
+}
+
+__device__ __forceinline__ int block_sum(AllocShared &sh, int x) {
+    int all;
+    block_scan(sh, x, &all);
+    return all;
+}
+
+// Cluster barrier (arrive / wait are warp-collective); orders global and
+// distributed shared memory between the CTAs.
+__device__ __forceinline__ void cluster_barrier() {
+    __syncwarp();
+    ptx::cluster_sync();
+}
+
+// Publishes one word per CTA; after the cluster barrier that follows,
+// cluster_gather returns the sum over the lower ranks and over all.
+__device__ __forceinline__ void cluster_put(AllocShared &sh, int word, int x) {
+    if (threadIdx.x == 0) sh.val[word] = x;
+}
+__device__ __forceinline__ int cluster_gather(AllocShared &sh, int word, int rank, int *total) {
+    const uint32_t a = ptx::smem_addr(&sh.val[word]);
+    int before = 0, all = 0;
+#pragma unroll
+    for (int r = 0; r < kClu; ++r) {
+        const int x = __float_as_int(ptx::ld_cluster_f32(ptx::cluster_map(a, r)));
+        if (r < rank) before += x;
+        all += x;
+    }
+    *total = all;
+    return before;
+}
+
+struct AllocParams {
+    int32_t *table;
+    long long stride;
+    int B, M, P, S;
+    int32_t *seq_len;
+    const int32_t *add;
+    int32_t *refs;
+    const int32_t *src, *dst;
+    int n;
+    int32_t *copy_src, *copy_dst, *count;
+    int32_t *new_refs;
+    int32_t *ws;                                       // [P + 1]
+    unsigned *err;
+};
+
+// This CTA's share [i0, i1) of the pages (multiples of 4).
+__device__ __forceinline__ void page_share(int P, int rank, int *i0, int *i1) {
+    const int per = (cdiv(P, kClu) + 3) & ~3;
+    *i0 = imin(P, rank * per);
+    *i1 = imin(P, *i0 + per);
+}
+
+// This thread's part of the free pages of [i0, i1), 16 bytes per load.
+__device__ __forceinline__ int count_free(const int32_t *refs, int i0, int i1) {
+    int n = 0;
+#pragma unroll 4
+    for (int i = i0 + int(threadIdx.x) * 4; i < i1; i += kAT * 4) {
+        if (i + 4 <= i1) {
+            const int4 r = *reinterpret_cast<const int4 *>(refs + i);
+            n += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
+        } else {
+            for (int j = i; j < i1; ++j) n += refs[j] == 0;
+        }
+    }
+    return n;
+}
+
+// Takes the free pages of [i0, i1) whose rank (from `rank0` on, in page order)
+// is below `need`: list[rank] = page, refs[page] = 1.
+__device__ __forceinline__ void take_free(AllocShared &sh, int32_t *refs, int i0, int i1, int rank0,
+                                          int need, int32_t *list) {
+    for (int b = i0; b < i1 && rank0 < need; b += kAT * 4) {
+        const int i = b + int(threadIdx.x) * 4;
+        int r[4], n = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            r[j] = i + j < i1 ? refs[i + j] : 1;
+            n += r[j] == 0;
+        }
+        int all;
+        int k = rank0 + block_scan(sh, n, &all);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (r[j] == 0) {
+                if (k < need) {
+                    list[k] = i + j;
+                    refs[i + j] = 1;
+                }
+                ++k;
+            }
+        rank0 += all;
+    }
+}
+
+// Reserve: entry i of row b is needed if it covers a position of
+// [seq_len[b], seq_len[b] + add[b]) and holds no page yet.
+__global__ void __launch_bounds__(kAT) reserve_kernel(const AllocParams p) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    __shared__ AllocShared sh;
+    const int rank = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rows = cdiv(p.B, kClu), r0 = imin(p.B, rank * rows), r1 = imin(p.B, r0 + rows);
+
+    // ---- count: a warp per row, and the free pages of this CTA's share
+    int need = 0, bad = 0;
+    for (int b = r0 + warp; b < r1; b += kAW) {
+        const int len = p.seq_len[b], add = p.add[b];
+        if (len < 0 || add < 0 || (long long)len + add > (long long)p.M * p.S) {
+            bad = 1;
+            continue;
+        }
+        const int32_t *row = p.table + b * p.stride;
+        const int e1 = add > 0 ? (len + add - 1) / p.S + 1 : 0;
+#pragma unroll 4
+        for (int i = len / p.S + lane; i < e1; i += 32) need += row[i] < 0;
+    }
+    int i0, i1;
+    page_share(p.P, rank, &i0, &i1);
+    const int free_part = count_free(p.refs, i0, i1);
+    const int my_need = block_sum(sh, need), my_bad = block_sum(sh, bad);
+    const int my_free = block_sum(sh, free_part);
+    cluster_put(sh, 0, my_need);
+    cluster_put(sh, 1, my_bad);
+    cluster_put(sh, 2, my_free);
+    cluster_barrier();
+    int total, errors, avail;
+    int base = cluster_gather(sh, 0, rank, &total);
+    cluster_gather(sh, 1, rank, &errors);
+    const int free0 = cluster_gather(sh, 2, rank, &avail);
+    const bool refuse = errors > 0 || total > avail;   // the same in every CTA
+    if (!refuse) take_free(sh, p.refs, i0, i1, free0, total, p.ws);
+    cluster_barrier();                                 // the list is complete; no CTA left early
+    if (refuse) {
+        if (rank == 0 && threadIdx.x == 0) raise_device_error(p.err, kDevCheck);
+        return;
+    }
+    // ---- assign, rows in order: a tile of one row per warp
+    for (int b0 = r0; b0 < r1; b0 += kAW) {
+        const int b = b0 + warp;
+        int n = 0, e0 = 0, e1 = 0;
+        int32_t *row = p.table + (long long)b * p.stride;
+        if (b < r1) {
+            const int len = p.seq_len[b], add = p.add[b];
+            e0 = len / p.S;
+            e1 = add > 0 ? (len + add - 1) / p.S + 1 : 0;
+#pragma unroll 4
+            for (int i = e0 + lane; i < e1; i += 32) n += row[i] < 0;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
+        int all;
+        int k = base + block_scan(sh, lane == 0 ? n : 0, &all);
+        k = __shfl_sync(0xffffffffu, k, 0);
+        if (b < r1 && n > 0) {
+            for (int i = e0; i < e1; i += 32) {
+                const bool empty = i + lane < e1 && row[i + lane] < 0;
+                const unsigned bits = __ballot_sync(0xffffffffu, empty);
+                if (empty) row[i + lane] = p.ws[k + __popc(bits & ((1u << lane) - 1u))];
+                k += __popc(bits);
+            }
+        }
+        base += all;
+    }
+}
+
+// Free: an entry whose page holds no visible token of its row lets go of it.
+__global__ void __launch_bounds__(256) free_kernel(const AllocParams p, int blocks, int window,
+                                                   int sinks) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int b = blockIdx.x / blocks, j0 = (blockIdx.x % blocks) * 1024;
+    const int len = p.seq_len[b];
+    if (len < 0) {
+        if (threadIdx.x == 0 && j0 == 0) raise_device_error(p.err, kDevCheck);
+        return;
+    }
+    const int lo = window > 0 && len > window ? len - window : 0;
+    const int s_end = imin(sinks, len);
+    int32_t *row = p.table + b * p.stride;
+    int page[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int i = j0 + u * 256 + threadIdx.x;
+        page[u] = i < p.M ? row[i] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int i = j0 + u * 256 + threadIdx.x;
+        if (page[u] == -1) continue;
+        const long long at = (long long)i * p.S;
+        if (at < len && (at + p.S > lo || at < s_end)) continue;
+        if (page[u] < 0 || page[u] >= p.P) {
+            raise_device_error(p.err, kDevCheck);
+            continue;
+        }
+        if (atomicSub(&p.refs[page[u]], 1) <= 0) {     // not counted: the entry stays
+            atomicAdd(&p.refs[page[u]], 1);
+            raise_device_error(p.err, kDevCheck);
+            continue;
+        }
+        row[i] = -1;
+    }
+}
+
+// Fork: row dst[i] becomes a copy of row src[i].  Full pages are shared; a last
+// page that is partly filled gets a page of its own and a copy order.
+__global__ void __launch_bounds__(kAT) fork_kernel(const AllocParams p) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    __shared__ AllocShared sh;
+    extern __shared__ unsigned is_dst[];               // one bit per row
+    const int rank = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+    // ---- the lists: rows in range, no row twice a target, none target and source
+    int bad = 0;
+    const int words = (p.B + 31) / 32;
+    for (int i = threadIdx.x; i < words; i += kAT) is_dst[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.n; i += kAT) {
+        const int d = p.dst[i];
+        if (d < 0 || d >= p.B)
+            bad = 1;
+        else if (atomicOr(&is_dst[d >> 5], 1u << (d & 31)) >> (d & 31) & 1u)
+            bad = 1;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.n; i += kAT) {
+        const int s = p.src[i];
+        if (s < 0 || s >= p.B || (is_dst[s >> 5] >> (s & 31) & 1u)) {
+            bad = 1;
+        } else {
+            const int len = p.seq_len[s];
+            if (len < 0 || len > (long long)p.M * p.S) bad = 1;
+        }
+    }
+    bad = block_sum(sh, bad);                          // the same in every CTA
+    // ---- the entries: pages in range that are counted.  Work item: 128
+    //      entries of one fork, a warp each.
+    const int blocks = cdiv(p.M, 128);
+    const long long items = (long long)p.n * blocks;
+    const int w0 = rank * kAW + warp, wn = kClu * kAW;
+    int wrong = 0;
+    if (!bad)
+        for (long long it = w0; it < items; it += wn) {
+            const int f = int(it / blocks), j0 = int(it % blocks) * 128;
+            const int s = p.src[f], d = p.dst[f];
+            const int used = cdiv(p.seq_len[s], p.S);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int j = j0 + u * 32 + lane;
+                if (j >= p.M) continue;
+                const int old = p.table[d * p.stride + j], e = j < used ? p.table[s * p.stride + j] : -1;
+                if (old < -1 || old >= p.P || (old >= 0 && p.refs[old] <= 0)) wrong = 1;
+                if (e < -1 || e >= p.P || (e >= 0 && p.refs[e] <= 0)) wrong = 1;
+            }
+        }
+    wrong = block_sum(sh, wrong);
+    cluster_put(sh, 0, wrong);
+    cluster_barrier();
+    int any;
+    cluster_gather(sh, 0, rank, &any);
+    bool refuse = bad || any;
+    // ---- counts: the targets' old pages let go, the shared full pages taken
+    auto recount = [&](int sign) {
+        for (long long it = w0; it < items; it += wn) {
+            const int f = int(it / blocks), j0 = int(it % blocks) * 128;
+            const int s = p.src[f], d = p.dst[f];
+            const int full = p.seq_len[s] / p.S;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int j = j0 + u * 32 + lane;
+                if (j >= p.M) continue;
+                const int old = p.table[d * p.stride + j], e = j < full ? p.table[s * p.stride + j] : -1;
+                if (old >= 0) atomicSub(&p.refs[old], sign);
+                if (e >= 0) atomicAdd(&p.refs[e], sign);
+            }
+        }
+    };
+    if (!refuse) recount(1);
+    cluster_barrier();
+    // ---- pages of their own for the partly filled last pages, in list order;
+    //      CTA 0 leaves each fork's number in copy_dst
+    int i0, i1, tails = 0;
+    page_share(p.P, rank, &i0, &i1);
+    int my_free = 0;
+    if (!refuse) {
+        for (int b0 = 0; b0 < p.n; b0 += kAT) {
+            const int f = b0 + threadIdx.x;
+            int t = 0;
+            if (f < p.n) {
+                const int len = p.seq_len[p.src[f]];
+                t = len % p.S != 0 && p.table[p.src[f] * p.stride + len / p.S] >= 0;
+            }
+            int all;
+            const int k = tails + block_scan(sh, t, &all);
+            if (rank == 0 && f < p.n) p.copy_dst[f] = t ? k : -1;
+            tails += all;
+        }
+        my_free = block_sum(sh, count_free(p.refs, i0, i1));
+    }
+    cluster_put(sh, 1, my_free);
+    cluster_barrier();
+    int avail;
+    const int free0 = cluster_gather(sh, 1, rank, &avail);
+    if (!refuse && tails > avail) {
+        recount(-1);                                   // nothing has changed but the counts
+        refuse = true;
+    }
+    if (!refuse) take_free(sh, p.refs, i0, i1, free0, tails, p.ws);
+    cluster_barrier();
+    if (refuse) {
+        for (int i = rank * kAT + threadIdx.x; i < p.n; i += kClu * kAT) p.copy_src[i] = p.copy_dst[i] = -1;
+        if (rank == 0 && threadIdx.x == 0) raise_device_error(p.err, kDevCheck);
+        return;
+    }
+    // ---- the rows
+    for (long long it = w0; it < items; it += wn) {
+        const int f = int(it / blocks), j0 = int(it % blocks) * 128;
+        const int s = p.src[f], d = p.dst[f];
+        const int len = p.seq_len[s], full = len / p.S;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int j = j0 + u * 32 + lane;
+            if (j >= p.M) continue;
+            int e = j < full ? p.table[s * p.stride + j] : -1;
+            if (j == full) {                           // the last page, or the first entry behind it
+                const int k = p.copy_dst[f];
+                if (k >= 0) {
+                    e = p.ws[k];
+                    p.copy_src[f] = p.table[s * p.stride + j];
+                    p.copy_dst[f] = e;
+                } else {
+                    p.copy_src[f] = -1;
+                }
+            }
+            p.table[d * p.stride + j] = e;
+        }
+        if (j0 == 0 && lane == 0) {
+            p.seq_len[d] = len;
+            if (full == p.M) p.copy_src[f] = -1;       // no entry behind a full table
+        }
+    }
+}
+
+// Compact: with L live pages, the k-th live page at or above L moves to the
+// k-th free page below L.  Lists the moves, fills the map old -> new of the
+// pages at or above L (ws[page]; ws[P] = L) and writes the new counts.
+__global__ void __launch_bounds__(kAT) compact_kernel(const AllocParams p) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    __shared__ AllocShared sh;
+    const int rank = blockIdx.x;
+    const int cap = p.P / 2;
+    int i0, i1;
+    page_share(p.P, rank, &i0, &i1);
+    int live = 0;
+#pragma unroll 4
+    for (int i = i0 + threadIdx.x; i < i1; i += kAT) live += p.refs[i] > 0;
+    live = block_sum(sh, live);
+    cluster_put(sh, 0, live);
+    cluster_barrier();
+    int L;
+    cluster_gather(sh, 0, rank, &L);
+    // of this share: live pages at or above L (movers), free ones below (holes)
+    int n_mov = 0, n_hole = 0;
+#pragma unroll 4
+    for (int i = i0 + threadIdx.x; i < i1; i += kAT) {
+        const bool lv = p.refs[i] > 0;
+        n_mov += lv && i >= L;
+        n_hole += !lv && i < L;
+    }
+    n_mov = block_sum(sh, n_mov);
+    n_hole = block_sum(sh, n_hole);
+    cluster_put(sh, 1, n_mov);
+    cluster_put(sh, 2, n_hole);
+    cluster_barrier();
+    int moves, holes;
+    int km = cluster_gather(sh, 1, rank, &moves);
+    int kh = cluster_gather(sh, 2, rank, &holes);
+    for (int b = i0; b < i1; b += kAT) {
+        const int i = b + threadIdx.x;
+        const bool in = i < i1, lv = in && p.refs[i] > 0;
+        const int mov = lv && i >= L, hole = in && !lv && i < L;
+        int all;
+        const int pre = block_scan(sh, mov | (hole << 16), &all);
+        if (mov) p.copy_src[km + (pre & 0xffff)] = i;
+        if (hole) p.copy_dst[kh + (pre >> 16)] = i;
+        if (in && i >= L && !lv) p.ws[i] = -1;         // no live page: an entry naming it is wrong
+        km += all & 0xffff;
+        kh += all >> 16;
+    }
+    cluster_barrier();
+    const int t = rank * kAT + threadIdx.x;
+    for (int k = t; k < cap; k += kClu * kAT) {
+        if (k < moves) {
+            const int s = p.copy_src[k], d = p.copy_dst[k];
+            p.ws[s] = d;
+            p.new_refs[d] = p.refs[s];
+        } else {
+            p.copy_src[k] = p.copy_dst[k] = -1;
+        }
+    }
+    if (t == 0) {
+        *p.count = moves;
+        p.ws[p.P] = L;
+    }
+    cluster_barrier();                                 // the movers' counts have been read
+    for (int i = i0 + threadIdx.x; i < i1; i += kAT) {
+        if (i >= L)
+            p.new_refs[i] = 0;
+        else if (p.refs[i] > 0)
+            p.new_refs[i] = p.refs[i];
+    }
+}
+
+__global__ void __launch_bounds__(256) remap_kernel(const AllocParams p, int32_t *out,
+                                                    long long out_stride, int blocks) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int b = blockIdx.x / blocks, j0 = (blockIdx.x % blocks) * 1024;
+    const int L = p.ws[p.P];
+    int e[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int i = j0 + u * 256 + threadIdx.x;
+        e[u] = i < p.M ? p.table[b * p.stride + i] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int i = j0 + u * 256 + threadIdx.x;
+        if (i >= p.M) break;
+        if (e[u] >= L || e[u] < -1) {
+            e[u] = e[u] >= L && e[u] < p.P ? p.ws[e[u]] : -1;
+            if (e[u] < 0) raise_device_error(p.err, kDevCheck);
+        }
+        out[b * out_stride + i] = e[u];
+    }
+}
+
+AllocParams alloc_params(const Ctx &c, const PageTable &t) {
+    AllocParams p{};
+    p.table = t.table;
+    p.stride = t.stride;
+    p.B = t.B; p.M = t.max_pages; p.P = t.P; p.S = t.S;
+    p.err = c.err;
+    return p;
+}
+
+// A page is one block if its rows follow one another in either order.
+// st: element strides (head, token).
+bool dense_page(const long long *st, int Hkv, int S, int D) {
+    const long long h = st[0], t = st[1];
+    return (t == D && (Hkv == 1 || h == (long long)S * D)) ||
+           (h == D && t == (long long)Hkv * D);
+}
+
+}  // namespace
+
+attn_status_t kv_append_paged(const Ctx &c, attn_dtype_t dt, const PagedAppend &a) {
+    const int es = dt == ATTN_F32 ? 4 : 2;
+    AppendParams p{};
+    p.k = static_cast<uint8_t *>(a.k);
+    p.v = static_cast<uint8_t *>(a.v);
+    p.kn = static_cast<const uint8_t *>(a.kn);
+    p.vn = static_cast<const uint8_t *>(a.vn);
+    p.table = a.table;
+    p.seq_len = a.seq_len;
+    p.new_len = a.new_len;
+    p.T = a.T; p.Hkv = a.Hkv; p.S = a.S; p.P = a.P; p.max_pages = a.max_pages;
+    p.table_stride = a.table_stride;
+    for (int i = 0; i < 3; ++i) {
+        p.k_st[i] = a.k_st[i] * es;
+        p.v_st[i] = a.v_st[i] * es;
+        p.kn_st[i] = a.kn_st[i] * es;
+        p.vn_st[i] = a.vn_st[i] * es;
+    }
+    for (int vpr = a.D * es / 16; vpr > 1; vpr >>= 1) ++p.vpr_log;
+    p.advance = a.advance;
+    p.err = c.err;
+    if (a.T == 1) {
+        p.tiles = 1;
+        return launch_pdl(c, append_kernel<1, true>, dim3(a.B), 256, 1, 0, p);
+    }
+    constexpr int TB = 16;
+    p.tiles = cdiv(a.T, TB);
+    if ((long long)a.B * p.tiles > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
+    if (p.tiles == 1) return launch_pdl(c, append_kernel<TB, true>, dim3(a.B), 256, 1, 0, p);
+    const attn_status_t st = launch_pdl(c, append_kernel<TB, false>, dim3(a.B * p.tiles), 256, 1, 0, p);
+    if (st != ATTN_OK || !a.advance) return st;
+    return launch_pdl(c, advance_kernel, dim3(cdiv(a.B, 4)), 128, 1, 0, p, a.B);
+}
+
+attn_status_t kv_pages_copy(const Ctx &c, attn_dtype_t dt, const PagesCopy &a) {
+    const int es = dt == ATTN_F32 ? 4 : 2;
+    CopyParams p{};
+    p.k = static_cast<uint8_t *>(a.k);
+    p.v = static_cast<uint8_t *>(a.v);
+    p.src = a.src; p.dst = a.dst; p.count = a.count;
+    p.n = a.n; p.P = a.P;
+    p.vpr = a.D * es / 16;
+    p.S = a.S;
+    p.vecs = a.Hkv * a.S * p.vpr;
+    p.pieces = cdiv(p.vecs, kPiece);
+    p.sides = 2 * a.layers;
+    for (int i = 0; i < 4; ++i) {
+        p.k_st[i] = a.k_st[i] * es;
+        p.v_st[i] = a.v_st[i] * es;
+    }
+    p.err = c.err;
+    const long long items = (long long)a.n * p.sides * p.pieces;
+    const int grid = int(items < 8ll * c.sm_count ? items : 8ll * c.sm_count);
+    const bool dense = dense_page(a.k_st + 2, a.Hkv, a.S, a.D) && dense_page(a.v_st + 2, a.Hkv, a.S, a.D);
+    return dense ? launch_pdl(c, copy_kernel<true>, dim3(grid), kCopyThreads, 1, 0, p)
+                 : launch_pdl(c, copy_kernel<false>, dim3(grid), kCopyThreads, 1, 0, p);
+}
+
+size_t kv_pages_workspace_bytes(int P) { return ((size_t(P) + 1) * 4 + 255) & ~size_t(255); }
+
+attn_status_t kv_pages_reserve(const Ctx &c, const PageTable &t, const int32_t *seq_len,
+                               const int32_t *add, int32_t *refs, void *ws) {
+    AllocParams p = alloc_params(c, t);
+    p.seq_len = const_cast<int32_t *>(seq_len);        // read only
+    p.add = add;
+    p.refs = refs;
+    p.ws = static_cast<int32_t *>(ws);
+    return launch_pdl(c, reserve_kernel, dim3(kClu), kAT, kClu, 0, p);
+}
+
+attn_status_t kv_pages_free(const Ctx &c, const PageTable &t, const int32_t *seq_len, int32_t *refs,
+                            int window, int sinks) {
+    AllocParams p = alloc_params(c, t);
+    p.seq_len = const_cast<int32_t *>(seq_len);        // read only
+    p.refs = refs;
+    const int blocks = cdiv(t.max_pages, 1024);
+    if ((long long)t.B * blocks > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
+    return launch_pdl(c, free_kernel, dim3(t.B * blocks), 256, 1, 0, p, blocks, window, sinks);
+}
+
+attn_status_t kv_pages_fork(const Ctx &c, const PageTable &t, int32_t *seq_len, int32_t *refs,
+                            const int32_t *src, const int32_t *dst, int n, int32_t *copy_src,
+                            int32_t *copy_dst, void *ws) {
+    AllocParams p = alloc_params(c, t);
+    p.seq_len = seq_len;
+    p.refs = refs;
+    p.src = src; p.dst = dst; p.n = n;
+    p.copy_src = copy_src; p.copy_dst = copy_dst;
+    p.ws = static_cast<int32_t *>(ws);
+    return launch_pdl(c, fork_kernel, dim3(kClu), kAT, kClu, size_t(cdiv(t.B, 32)) * 4, p);
+}
+
+attn_status_t kv_pages_compact(const Ctx &c, const PageTable &t, const int32_t *refs,
+                               int32_t *new_table, long long new_stride, int32_t *new_refs,
+                               int32_t *copy_src, int32_t *copy_dst, int32_t *count, void *ws) {
+    AllocParams p = alloc_params(c, t);
+    p.refs = const_cast<int32_t *>(refs);              // written only where new_refs is the same array
+    p.new_refs = new_refs;
+    p.copy_src = copy_src; p.copy_dst = copy_dst; p.count = count;
+    p.ws = static_cast<int32_t *>(ws);
+    const int blocks = cdiv(t.max_pages, 1024);
+    if ((long long)t.B * blocks > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
+    const attn_status_t st = launch_pdl(c, compact_kernel, dim3(kClu), kAT, kClu, 0, p);
+    if (st != ATTN_OK) return st;
+    return launch_pdl(c, remap_kernel, dim3(t.B * blocks), 256, 1, 0, p, new_table, new_stride, blocks);
+}
+
+}  // namespace attn
