@@ -271,6 +271,197 @@ ATTN_API attn_status_t attn_decode_gqa_ring(const void *q, const void *k_cache,
                                             size_t workspace_bytes, void *stream);
 
 /*
+ * Causal grouped-query prefill with a sliding window and sinks.
+ *   q, o [B, Hq, Nq, D]; k, v [B, Hkv, Nkv, D]; Hq % Hkv == 0, Nq <= Nkv.  The
+ *   queries are the last Nq of the Nkv positions: query i sits at position
+ *   p = Nkv - Nq + i and attends to
+ *       { j <= p : j > p - window  or  j < sinks },
+ *   i.e. its newest `window` positions (itself among them) and the first
+ *   `sinks` tokens.  window <= 0: no window (plain causal attention).
+ *   sinks >= 0.  Nq < Nkv continues a prompt whose first keys are cached.
+ *   x_strides[3] as in attn_full_fwd_strided (NULL: contiguous).
+ *   A key that a query does not attend to does not change its output, whatever
+ *   it or its value holds (infinities and NaN included).
+ *   bf16 and f16 run on the tensor cores for D in {64, 128}; fp32 (and the
+ *   16-bit types with D = 32) on the exact-FFMA SIMT kernel.  Work grows with
+ *   Nq * (window + sinks), not with Nq * Nkv.
+ *   Requires Nkv <= 2^30.
+ * Passage: fak "GPU - the in-kernel forward pass", section 3 (Llama prefill
+ * of a grouped-query model); the window is that of attn_decode_gqa_paged.
+ */
+ATTN_API attn_status_t attn_causal_gqa_window_fwd(const void *q, const void *k, const void *v,
+                                                  void *o, int B, int Hq, int Hkv, int Nq,
+                                                  int Nkv, int D, const int64_t q_strides[3],
+                                                  const int64_t k_strides[3],
+                                                  const int64_t v_strides[3],
+                                                  const int64_t o_strides[3], int window,
+                                                  int sinks, attn_dtype_t dtype, float scale,
+                                                  void *stream);
+
+/*
+ * Paged KV cache.  Many sequences share one pool of pages of `page_size`
+ * tokens; a page table names each sequence's pages.  Conventions of all
+ * entries below:
+ *   k_pages, v_pages [num_pages, Hkv, page_size, D], any order of the three
+ *     outer axes given by k_strides / v_strides[3] = element strides of (page,
+ *     head, token); D is contiguous, strides are multiples of 16 bytes, a
+ *     stride whose extent is 1 is ignored, NULL means contiguous in the order
+ *     above.  page_size is a multiple of 8.
+ *   page_table: DEVICE int32 [B, max_pages], rows table_stride entries apart
+ *     (>= max_pages).  Position j of sequence b lives in row j % page_size of
+ *     page page_table[b][j / page_size]; -1 means no page.  Requires
+ *     max_pages * page_size < 2^31 and B <= 2^20.
+ *   seq_len: DEVICE int32 [B], tokens held by each sequence.
+ *   page_refs: DEVICE int32 [num_pages], 16-byte aligned: how many table
+ *     entries name the page; 0 means free.  A page named by several rows
+ *     (after a fork) is only read.  page_table and page_refs are the whole
+ *     state of the allocator; a new pool is refs = 0 and table = -1.
+ *   The values are read on the device when the call runs, so every call can be
+ *   captured in a CUDA graph and replayed as sequences grow.
+ */
+
+/*
+ * Appends the K and V rows of new tokens to the sequences' pages.
+ *   k_new, v_new [B, Hkv, T, D], element strides (batch, head, token) in
+ *   kn_strides / vn_strides[3] (NULL: contiguous), e.g. slices of a packed
+ *   projection.  new_len: DEVICE int32 [B], rows to append per sequence, 0 <=
+ *   new_len[b] <= T; NULL means T.  Row t goes to position seq_len[b] + t; if
+ *   advance != 0, seq_len[b] += new_len[b] afterwards.
+ *   The pages must exist (attn_kv_pages_reserve) and be named by this sequence
+ *   alone.  A request that does not fit the table writes nothing; a token whose
+ *   table entry is no page of the pool is not written; either sets
+ *   ATTN_ERR_DEVICE_CHECK and leaves that sequence's seq_len as it was.
+ *   The cache's (page, head, token) rows must be disjoint (checked).
+ *   dtype ATTN_F32, ATTN_BF16 or ATTN_F16; D in {32, 64, 128}.
+ * Passage: fak "GPU - the in-kernel forward pass", section 3b (the kernel-form
+ * KV append with a device-held position), on pages.
+ */
+ATTN_API attn_status_t attn_kv_append_paged(void *k_pages, void *v_pages, const void *k_new,
+                                            const void *v_new, const int32_t *page_table,
+                                            int32_t *seq_len, const int32_t *new_len, int B, int T,
+                                            int Hkv, int D, int num_pages, int page_size,
+                                            int max_pages, int64_t table_stride,
+                                            const int64_t k_strides[3], const int64_t v_strides[3],
+                                            const int64_t kn_strides[3],
+                                            const int64_t vn_strides[3], attn_dtype_t dtype,
+                                            int advance, void *stream);
+
+/*
+ * Single-token grouped-query decode attention over a paged KV cache.
+ *   q, o [B, Hq, D] with element strides (batch, head) in q_strides /
+ *   o_strides[2] (NULL: contiguous).  Query head hq of sequence b reads KV head
+ *   hq / (Hq / Hkv) and attends to the positions
+ *       { j < seq_len[b] : j >= seq_len[b] - window  or  j < sinks };
+ *   window <= 0: all of them.  sinks >= 0.
+ *   seq_len[b] == 0 (an idle slot) writes zeros.  Table entries of pages that
+ *   hold no visible position are not needed, so those pages may be free.  Rows of a page
+ *   behind seq_len[b], or outside the window, do not change the result,
+ *   whatever they hold.
+ *   A seq_len[b] outside [0, max_pages * page_size], or a needed entry that is
+ *   no page of the pool, sets ATTN_ERR_DEVICE_CHECK and leaves that sequence's
+ *   output unwritten; other sequences' are not affected.
+ *   Requires Hq % Hkv == 0, Hq / Hkv <= 16, D in {64, 128}, dtype ATTN_BF16 or
+ *   ATTN_F16 (q, pages and o alike).  For one set of inputs the result does not
+ *   depend on timing.
+ *   workspace: DEVICE scratch of attn_decode_gqa_paged_workspace_bytes(...)
+ *   bytes, 256-byte aligned, ZERO-FILLED before its first use.  Every call that
+ *   completes leaves it ready for the next one with the same B, Hq, Hkv and D
+ *   (for other sizes, zero it again or use another).  Calls that share a
+ *   workspace must not overlap on the GPU.
+ * Passage: fak "GPU - the in-kernel forward pass", section 4 (naive decode
+ * attention, "no flash/paged attention").
+ */
+ATTN_API attn_status_t attn_decode_gqa_paged(const void *q, const void *k_pages,
+                                             const void *v_pages, const int32_t *page_table,
+                                             const int32_t *seq_len, void *o, int B, int Hq,
+                                             int Hkv, int D, int num_pages, int page_size,
+                                             int max_pages, int64_t table_stride,
+                                             const int64_t q_strides[2],
+                                             const int64_t k_strides[3],
+                                             const int64_t v_strides[3],
+                                             const int64_t o_strides[2], int window, int sinks,
+                                             attn_dtype_t dtype, float scale, void *workspace,
+                                             size_t workspace_bytes, void *stream);
+
+ATTN_API size_t attn_decode_gqa_paged_workspace_bytes(int B, int Hq, int Hkv, int D);
+
+/*
+ * The page allocator.  Each call takes its pages lowest number first and
+ * serves requests in (row, entry) order, so its result depends on its inputs
+ * alone.  A request that cannot be met, or an argument on the device that is
+ * out of range, sets ATTN_ERR_DEVICE_CHECK and changes nothing (free: the
+ * entry in question stays; compact: an entry that names no live page becomes
+ * -1).  page_refs must count the table's entries, as these calls keep it; calls
+ * that change the same pool are ordered by their stream.
+ *   workspace: DEVICE scratch of attn_kv_pages_workspace_bytes(num_pages)
+ *   bytes, 256-byte aligned, contents irrelevant, not used by another call at
+ *   the same time.
+ *
+ * reserve: pages for the add_len[b] tokens (DEVICE int32 [B], >= 0) behind
+ *   seq_len[b]: every entry that covers a position in [seq_len[b], seq_len[b] +
+ *   add_len[b]) and holds no page gets one.
+ * free: lets go of every page that holds no token sequence b can still see:
+ *   entries whose positions are all >= seq_len[b], or (window > 0) all < seq_len[b] -
+ *   window and >= sinks.  With seq_len[b] = 0 that is the whole row.  Pages
+ *   reserved ahead of seq_len[b] are let go too.
+ * fork: for i < n, row dst[i] becomes a copy of row src[i] (DEVICE int32 [n]),
+ *   seq_len[dst[i]] = seq_len[src[i]]; what dst[i] held is let go first.  Full
+ *   pages are shared; a partly filled last page gets a page of its own, and
+ *   (copy_src[i], copy_dst[i]) (DEVICE int32 [n]) names the copy that
+ *   attn_kv_pages_copy must make before either row is appended to; (-1, -1) if
+ *   there is none.  No row may be a target twice, or both target and source; a
+ *   source may be named many times.  1 <= n <= B <= 262144.
+ * compact: moves the live pages to the lowest numbers.  With L live pages the
+ *   k-th live page >= L goes to the k-th free page < L.  Writes the new table
+ *   and counts to new_table (rows new_stride apart) and new_refs, either of
+ *   which may be the old array; copy_src / copy_dst (DEVICE int32
+ *   [num_pages / 2], NULL allowed only if num_pages is 1) hold *count (DEVICE
+ *   int32) moves and -1 behind them.
+ * copy: copies pages copy_src[i] -> copy_dst[i], i < n (and < *count, if count
+ *   is not NULL), K and V, in each of `layers` caches that share one table:
+ *   strides[4] of (layer, page, head, token), NULL = contiguous.  A pair
+ *   (-1, -1) is skipped; another number outside the pool sets
+ *   ATTN_ERR_DEVICE_CHECK and that pair is skipped.  The pairs are copied in no
+ *   order, so no page may be a target twice, or both target and source (the
+ *   lists of fork and compact are so).  All dtypes, D in {32, 64, 128}.
+ * Passage: fak "GPU - the in-kernel forward pass", section 3b (device KV of a
+ * dynamic capacity, named there as the follow-up).
+ */
+ATTN_API size_t attn_kv_pages_workspace_bytes(int num_pages);
+
+ATTN_API attn_status_t attn_kv_pages_reserve(int32_t *page_table, const int32_t *seq_len,
+                                             const int32_t *add_len, int32_t *page_refs, int B,
+                                             int num_pages, int page_size, int max_pages,
+                                             int64_t table_stride, void *workspace,
+                                             size_t workspace_bytes, void *stream);
+
+ATTN_API attn_status_t attn_kv_pages_free(int32_t *page_table, const int32_t *seq_len,
+                                          int32_t *page_refs, int B, int num_pages, int page_size,
+                                          int max_pages, int64_t table_stride, int window,
+                                          int sinks, void *stream);
+
+ATTN_API attn_status_t attn_kv_pages_fork(int32_t *page_table, int32_t *seq_len,
+                                          int32_t *page_refs, const int32_t *src,
+                                          const int32_t *dst, int n, int32_t *copy_src,
+                                          int32_t *copy_dst, int B, int num_pages, int page_size,
+                                          int max_pages, int64_t table_stride, void *workspace,
+                                          size_t workspace_bytes, void *stream);
+
+ATTN_API attn_status_t attn_kv_pages_compact(const int32_t *page_table, const int32_t *page_refs,
+                                             int32_t *new_table, int32_t *new_refs,
+                                             int32_t *copy_src, int32_t *copy_dst, int32_t *count,
+                                             int B, int num_pages, int max_pages,
+                                             int64_t table_stride, int64_t new_stride,
+                                             void *workspace, size_t workspace_bytes,
+                                             void *stream);
+
+ATTN_API attn_status_t attn_kv_pages_copy(void *k_pages, void *v_pages, const int32_t *copy_src,
+                                          const int32_t *copy_dst, int n, const int32_t *count,
+                                          int layers, int num_pages, int Hkv, int page_size, int D,
+                                          const int64_t k_strides[4], const int64_t v_strides[4],
+                                          attn_dtype_t dtype, void *stream);
+
+/*
  * 3D neighborhood attention with NATTEN boundary windows.
  *   q, k, v, o [B, heads, N, D] with N = T * Hg * W tokens in row-major
  *   (t, h, w) order.  kernel: HOST int[3], the requested window per axis; each
@@ -360,7 +551,8 @@ ATTN_API attn_status_t attn_device_status(void *stream);
  * family, for tests that must prove the path under test really ran.
  * ids: 0 = fp32/SIMT flash, 1 = tcgen05 flash, 2 = decode split-KV,
  *      3 = RoPE prologue, 4 = window-start export, 5 = tcgen05 neighborhood,
- *      6 = KV-cache append, 7 = bounded-wait check.
+ *      6 = KV-cache append, 7 = bounded-wait check, 8 = paged decode,
+ *      9 = paged append, page allocator and page copies.
  * Returns 0 for an unknown id.
  */
 ATTN_API uint64_t attn_launch_count(int kernel_family);

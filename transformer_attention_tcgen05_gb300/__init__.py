@@ -14,6 +14,11 @@ Entry points (names as in the C ABI, without the ``attn_`` prefix):
     na3d_window_starts(grid, kernel)
     kv_append(k_cache, v_cache, k_new, v_new, seq_len)   device-side position, graph-stable
     causal_gqa_fwd(q, k, v)                    q [B, Hq, N, D], k/v [B, Hkv, N, D], causal
+    causal_gqa_window_fwd(q, k, v, window, sinks)   causal with a sliding window and sinks
+Paged KV cache (pages [P, Hkv, page_size, D], page_table int32 [B, max_pages]):
+    decode_gqa_paged(q, k_pages, v_pages, page_table, seq_len, window, sinks)
+    kv_append_paged(k_pages, v_pages, k_new, v_new, page_table, seq_len, new_len)
+    kv_pages_reserve / kv_pages_free / kv_pages_fork / kv_pages_compact / kv_pages_copy
 """
 from __future__ import annotations
 
@@ -26,6 +31,9 @@ import torch
 __all__ = [
     "AttnError", "lib", "full_fwd", "full_fwd_strided", "causal_gqa_fwd_strided", "na3d_fwd_strided", "rope_joint_fwd", "decode_gqa", "na3d_fwd", "causal_gqa_fwd",
     "na3d_window_starts", "kv_append", "kv_append_ring", "decode_gqa_ring", "decode_workspace_bytes", "rope_joint_workspace_bytes",
+    "causal_gqa_window_fwd", "decode_gqa_paged", "decode_paged_workspace_bytes", "kv_append_paged",
+    "kv_pages_workspace_bytes", "kv_pages_reserve", "kv_pages_free", "kv_pages_fork",
+    "kv_pages_compact", "kv_pages_copy",
     "device_status", "debug_wait_test", "launch_count", "version", "FAMILIES", "LIB_PATH",
 ]
 
@@ -37,7 +45,7 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported configuration",
           6: "device-side check failed"}
 #: kernel families of attn_launch_count
 FAMILIES = {"simt": 0, "tc_flash": 1, "decode": 2, "rope": 3, "na_starts": 4, "tc_na": 5,
-            "kv_append": 6, "debug": 7}
+            "kv_append": 6, "debug": 7, "decode_paged": 8, "kv_pages": 9}
 
 
 class AttnError(RuntimeError):
@@ -80,6 +88,26 @@ def lib() -> ctypes.CDLL:
         L.attn_causal_gqa_fwd_strided.argtypes = L.attn_full_fwd_strided.argtypes
         L.attn_na3d_fwd_strided.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
                                             ctypes.POINTER(_i), _st, _st, _st, _st, _i, _f, _vp]
+        _i64 = ctypes.c_int64
+        L.attn_causal_gqa_window_fwd.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
+                                                 _st, _st, _st, _st, _i, _i, _i, _f, _vp]
+        L.attn_decode_gqa_paged.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
+                                            _i, _i64, _st, _st, _st, _st, _i, _i, _i, _f, _vp,
+                                            _sz, _vp]
+        L.attn_decode_gqa_paged_workspace_bytes.argtypes = [_i, _i, _i, _i]
+        L.attn_decode_gqa_paged_workspace_bytes.restype = _sz
+        L.attn_kv_append_paged.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i,
+                                           _i, _i, _i64, _st, _st, _st, _st, _i, _i, _vp]
+        L.attn_kv_pages_workspace_bytes.argtypes = [_i]
+        L.attn_kv_pages_workspace_bytes.restype = _sz
+        L.attn_kv_pages_reserve.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i64, _vp, _sz, _vp]
+        L.attn_kv_pages_free.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, _i64, _i, _i, _vp]
+        L.attn_kv_pages_fork.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i,
+                                         _i64, _vp, _sz, _vp]
+        L.attn_kv_pages_compact.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i64,
+                                            _i64, _vp, _sz, _vp]
+        L.attn_kv_pages_copy.argtypes = [_vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _st, _st,
+                                         _i, _vp]
         L.attn_status_string.argtypes = [_i]
         L.attn_status_string.restype = ctypes.c_char_p
         L.attn_device_status.argtypes = [_vp]
@@ -91,7 +119,10 @@ def lib() -> ctypes.CDLL:
                      "attn_na3d_window_starts", "attn_device_status", "attn_kv_append",
                      "attn_causal_gqa_fwd", "attn_full_fwd_strided", "attn_kv_append_ring",
                      "attn_causal_gqa_fwd_strided", "attn_na3d_fwd_strided",
-                     "attn_decode_gqa_ring"):
+                     "attn_decode_gqa_ring", "attn_causal_gqa_window_fwd",
+                     "attn_decode_gqa_paged", "attn_kv_append_paged", "attn_kv_pages_reserve",
+                     "attn_kv_pages_free", "attn_kv_pages_fork", "attn_kv_pages_compact",
+                     "attn_kv_pages_copy"):
             getattr(L, name).restype = _i
         _lib = L
     return _lib
@@ -304,6 +335,248 @@ def kv_append_ring(k_cache, v_cache, k_new, v_new, seq_len, advance=True):
     """Ring-cache append: row seq_len[b] % Lmax (the oldest token's row once
     the ring is full); with advance, seq_len[b] += 1 on the device."""
     kv_append(k_cache, v_cache, k_new, v_new, seq_len, advance, _ring=True)
+
+
+def causal_gqa_window_fwd(q, k, v, window, sinks=0, o=None, scale=None):
+    """Causal GQA prefill with a sliding window and sinks: q [B,Hq,Nq,D] are the
+    last Nq of the Nkv positions of k/v [B,Hkv,Nkv,D] (strided views, D
+    contiguous); position p attends to its newest ``window`` positions and the
+    first ``sinks`` tokens (window 0: all). o defaults to a new contiguous tensor."""
+    dev = _cuda(q, k, v, strided=True)
+    B, Hq, Nq, D = q.shape
+    Hkv, Nkv = k.shape[1], k.shape[2]
+    if k.shape != (B, Hkv, Nkv, D) or v.shape != k.shape or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("k/v must be [B, Hkv, Nkv, D] with q's dtype")
+    o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else o
+    _cuda(q, o, strided=True)
+    if o.shape != q.shape or o.dtype != q.dtype:
+        raise ValueError("o must be [B, Hq, Nq, D] with q's dtype")
+    with torch.cuda.device(dev):
+        _check(lib().attn_causal_gqa_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                                o.data_ptr(), B, Hq, Hkv, Nq, Nkv, D, _strides(q),
+                                                _strides(k), _strides(v), _strides(o),
+                                                int(window), int(sinks), _dtype(q), _scale(scale),
+                                                _stream(dev)),
+               "attn_causal_gqa_window_fwd")
+    return o
+
+
+def _outer_strides(t):
+    if t.stride(-1) != 1:
+        raise ValueError("the last (D) dimension must be contiguous")
+    return (ctypes.c_int64 * (t.dim() - 1))(*t.stride()[:-1])
+
+
+def _i32(dev, *pairs):
+    """Each (tensor, shape): contiguous int32 on dev."""
+    for t, shape in pairs:
+        if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
+            raise ValueError(f"expected an int32 tensor of shape {tuple(shape)}, got "
+                             f"{t.dtype} {tuple(t.shape)}")
+        if t.device != dev or not t.is_contiguous():
+            raise ValueError("index tensors must be contiguous and on the device of the pages")
+
+
+def _table(page_table):
+    """(B, max_pages, row stride) of an int32 page table whose rows are contiguous."""
+    if not page_table.is_cuda:
+        raise ValueError("libattn tensors must be on a CUDA device")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2:
+        raise ValueError("page_table must be int32 [B, max_pages]")
+    if page_table.shape[1] > 1 and page_table.stride(1) != 1:
+        raise ValueError("the rows of page_table must be contiguous")
+    B, M = page_table.shape
+    return B, M, page_table.stride(0) if B > 1 else M
+
+
+def _pages(k_pages, v_pages):
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+        raise ValueError("k_pages and v_pages must be [P, Hkv, page_size, D] of one dtype")
+    return _cuda(k_pages, v_pages, strided=True)
+
+
+def decode_paged_workspace_bytes(B, Hq, Hkv, D) -> int:
+    return int(lib().attn_decode_gqa_paged_workspace_bytes(B, Hq, Hkv, D))
+
+
+def decode_gqa_paged(q, k_pages, v_pages, page_table, seq_len, o=None, scale=None, window=0,
+                     sinks=0, workspace=None):
+    """GQA decode over a paged cache: q [B,Hq,D], pages [P,Hkv,S,D] (views of any
+    order with D contiguous), page_table int32 [B,max_pages], seq_len int32 [B]
+    -> o [B,Hq,D].  With window > 0 only the newest ``window`` positions and the
+    first ``sinks`` tokens are attended to; a sequence of length 0 gives zeros.
+
+    ``workspace`` (uint8, decode_paged_workspace_bytes(...) bytes) must be
+    zero-filled before its first use; calls of the same sizes leave it reusable.
+    If omitted a zeroed one is allocated for this call.
+    """
+    dev = _pages(k_pages, v_pages)
+    B, Hq, D = q.shape
+    P, Hkv, S, _ = k_pages.shape
+    Bt, M, ts = _table(page_table)
+    if k_pages.shape[3] != D or Bt != B or k_pages.dtype != q.dtype:
+        raise ValueError("q [B,Hq,D], pages [P,Hkv,S,D] of q's dtype and page_table [B,max_pages] required")
+    _i32(dev, (seq_len, (B,)))
+    o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else o
+    _cuda(k_pages, q, o, page_table, strided=True)
+    if o.shape != q.shape or o.dtype != q.dtype:
+        raise ValueError("o must be [B, Hq, D] with q's dtype")
+    if workspace is None:
+        workspace = torch.zeros(max(decode_paged_workspace_bytes(B, Hq, Hkv, D), 256),
+                                dtype=torch.uint8, device=dev)
+    _cuda(k_pages, workspace, strided=True)
+    with torch.cuda.device(dev):
+        _check(lib().attn_decode_gqa_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                           page_table.data_ptr(), seq_len.data_ptr(), o.data_ptr(),
+                                           B, Hq, Hkv, D, P, S, M, ts, _outer_strides(q),
+                                           _outer_strides(k_pages), _outer_strides(v_pages),
+                                           _outer_strides(o), int(window), int(sinks), _dtype(q),
+                                           _scale(scale), workspace.data_ptr(),
+                                           workspace.numel() * workspace.element_size(),
+                                           _stream(dev)),
+               "attn_decode_gqa_paged")
+    return o
+
+
+def kv_append_paged(k_pages, v_pages, k_new, v_new, page_table, seq_len, new_len=None,
+                    advance=True):
+    """Write rows [0, new_len[b]) of k_new/v_new [B,Hkv,T,D] (or [B,Hkv,D], one
+    token; strided views) to the positions behind seq_len[b] in the sequences'
+    pages; with advance, seq_len[b] += new_len[b] on the device.  new_len int32
+    [B] defaults to T for every sequence."""
+    dev = _pages(k_pages, v_pages)
+    if k_new.dim() == 3:
+        k_new, v_new = k_new.unsqueeze(2), v_new.unsqueeze(2)
+    B, Hkv, T, D = k_new.shape
+    P, _, S, _ = k_pages.shape
+    Bt, M, ts = _table(page_table)
+    if k_pages.shape[1] != Hkv or k_pages.shape[3] != D or v_new.shape != k_new.shape or Bt != B \
+            or k_new.dtype != k_pages.dtype or v_new.dtype != k_pages.dtype:
+        raise ValueError("pages [P,Hkv,S,D], new rows [B,Hkv,T,D] of one dtype, page_table [B,max_pages] required")
+    _cuda(k_pages, k_new, v_new, page_table, strided=True)
+    _i32(dev, (seq_len, (B,)), *([] if new_len is None else [(new_len, (B,))]))
+    with torch.cuda.device(dev):
+        _check(lib().attn_kv_append_paged(k_pages.data_ptr(), v_pages.data_ptr(), k_new.data_ptr(),
+                                          v_new.data_ptr(), page_table.data_ptr(),
+                                          seq_len.data_ptr(),
+                                          None if new_len is None else new_len.data_ptr(),
+                                          B, T, Hkv, D, P, S, M, ts, _outer_strides(k_pages),
+                                          _outer_strides(v_pages), _outer_strides(k_new),
+                                          _outer_strides(v_new), _dtype(k_pages),
+                                          1 if advance else 0, _stream(dev)),
+               "attn_kv_append_paged")
+
+
+def kv_pages_workspace_bytes(num_pages) -> int:
+    return int(lib().attn_kv_pages_workspace_bytes(num_pages))
+
+
+def _pages_workspace(workspace, P, dev):
+    if workspace is None:
+        return torch.empty(max(kv_pages_workspace_bytes(P), 256), dtype=torch.uint8, device=dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on the device of the table")
+    return workspace
+
+
+def kv_pages_reserve(page_table, seq_len, add_len, page_refs, page_size, workspace=None):
+    """Give every entry of page_table [B,max_pages] that covers the add_len[b]
+    positions behind seq_len[b] and holds no page the lowest free one
+    (page_refs int32 [P]: table entries per page, 0 = free)."""
+    B, M, ts = _table(page_table)
+    dev, P = page_table.device, page_refs.numel()
+    _i32(dev, (seq_len, (B,)), (add_len, (B,)), (page_refs, (P,)))
+    workspace = _pages_workspace(workspace, P, dev)
+    with torch.cuda.device(dev):
+        _check(lib().attn_kv_pages_reserve(page_table.data_ptr(), seq_len.data_ptr(),
+                                           add_len.data_ptr(), page_refs.data_ptr(), B, P,
+                                           int(page_size), M, ts, workspace.data_ptr(),
+                                           workspace.numel() * workspace.element_size(),
+                                           _stream(dev)),
+               "attn_kv_pages_reserve")
+
+
+def kv_pages_free(page_table, seq_len, page_refs, page_size, window=0, sinks=0):
+    """Let go of the pages that hold no token their sequence can still see: all
+    positions behind seq_len[b] (the whole row if it is 0) or, with window > 0,
+    before the newest ``window`` tokens and past the first ``sinks``."""
+    B, M, ts = _table(page_table)
+    dev, P = page_table.device, page_refs.numel()
+    _i32(dev, (seq_len, (B,)), (page_refs, (P,)))
+    with torch.cuda.device(dev):
+        _check(lib().attn_kv_pages_free(page_table.data_ptr(), seq_len.data_ptr(),
+                                        page_refs.data_ptr(), B, P, int(page_size), M, ts,
+                                        int(window), int(sinks), _stream(dev)),
+               "attn_kv_pages_free")
+
+
+def kv_pages_fork(page_table, seq_len, page_refs, src, dst, page_size, workspace=None):
+    """Make row dst[i] a copy of row src[i] (int32 [n]): full pages are shared, a
+    partly filled last page gets a page of its own.  Returns (copy_src,
+    copy_dst) int32 [n] for kv_pages_copy, -1 where nothing is to be copied."""
+    B, M, ts = _table(page_table)
+    dev, P, n = page_table.device, page_refs.numel(), src.numel()
+    _i32(dev, (seq_len, (B,)), (page_refs, (P,)), (src, (n,)), (dst, (n,)))
+    workspace = _pages_workspace(workspace, P, dev)
+    pairs = torch.empty((2, n), dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib().attn_kv_pages_fork(page_table.data_ptr(), seq_len.data_ptr(),
+                                        page_refs.data_ptr(), src.data_ptr(), dst.data_ptr(), n,
+                                        pairs[0].data_ptr(), pairs[1].data_ptr(), B, P,
+                                        int(page_size), M, ts, workspace.data_ptr(),
+                                        workspace.numel() * workspace.element_size(),
+                                        _stream(dev)),
+               "attn_kv_pages_fork")
+    return pairs[0], pairs[1]
+
+
+def kv_pages_compact(page_table, page_refs, new_table=None, new_refs=None, workspace=None):
+    """Move the live pages to the lowest numbers.  The new table and counts go to
+    new_table / new_refs (default: in place).  Returns (copy_src, copy_dst,
+    count) for kv_pages_copy."""
+    B, M, ts = _table(page_table)
+    dev, P = page_table.device, page_refs.numel()
+    new_table = page_table if new_table is None else new_table
+    new_refs = page_refs if new_refs is None else new_refs
+    Bn, Mn, ns = _table(new_table)
+    if (Bn, Mn) != (B, M) or new_table.device != dev:
+        raise ValueError("new_table must be like page_table")
+    _i32(dev, (page_refs, (P,)), (new_refs, (P,)))
+    workspace = _pages_workspace(workspace, P, dev)
+    lists = torch.empty(2 * (P // 2) + 1, dtype=torch.int32, device=dev)
+    src, dst, count = lists[:P // 2], lists[P // 2:2 * (P // 2)], lists[2 * (P // 2):]
+    with torch.cuda.device(dev):
+        _check(lib().attn_kv_pages_compact(page_table.data_ptr(), page_refs.data_ptr(),
+                                           new_table.data_ptr(), new_refs.data_ptr(),
+                                           src.data_ptr(), dst.data_ptr(), count.data_ptr(), B, P,
+                                           M, ts, ns, workspace.data_ptr(),
+                                           workspace.numel() * workspace.element_size(),
+                                           _stream(dev)),
+               "attn_kv_pages_compact")
+    return src, dst, count
+
+
+def kv_pages_copy(k_pages, v_pages, copy_src, copy_dst, count=None):
+    """Copy pages copy_src[i] -> copy_dst[i] of pages [P,Hkv,S,D], or of every
+    layer of [layers,P,Hkv,S,D] (views with D contiguous); pairs of -1, and
+    pairs from count[0] on, are skipped."""
+    if k_pages.dim() == 4:
+        k_pages, v_pages = k_pages.unsqueeze(0), v_pages.unsqueeze(0)
+    if k_pages.dim() != 5 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+        raise ValueError("pages [P,Hkv,S,D] or [layers,P,Hkv,S,D] of one dtype required")
+    dev = _cuda(k_pages, v_pages, strided=True)
+    layers, P, Hkv, S, D = k_pages.shape
+    n = copy_src.numel()
+    _i32(dev, (copy_src, (n,)), (copy_dst, (n,)), *([] if count is None else [(count, (1,))]))
+    if n == 0:
+        return
+    with torch.cuda.device(dev):
+        _check(lib().attn_kv_pages_copy(k_pages.data_ptr(), v_pages.data_ptr(), copy_src.data_ptr(),
+                                        copy_dst.data_ptr(), n,
+                                        None if count is None else count.data_ptr(), layers, P,
+                                        Hkv, S, D, _outer_strides(k_pages), _outer_strides(v_pages),
+                                        _dtype(k_pages), _stream(dev)),
+               "attn_kv_pages_copy")
 
 
 def na3d_fwd(q, k, v, grid, kernel, o=None, scale=None):

@@ -417,6 +417,294 @@ attn_status_t attn_kv_append_ring(void *k_cache, void *v_cache, const void *k_ne
                         stream, true);
 }
 
+// ------------------------------------------------- windowed causal prefill
+
+attn_status_t attn_causal_gqa_window_fwd(const void *q, const void *k, const void *v, void *o,
+                                         int B, int Hq, int Hkv, int Nq, int Nkv, int D,
+                                         const int64_t q_strides[3], const int64_t k_strides[3],
+                                         const int64_t v_strides[3], const int64_t o_strides[3],
+                                         int window, int sinks, attn_dtype_t dtype, float scale,
+                                         void *stream) {
+    if (!q || !k || !v || !o) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o))
+        return ATTN_ERR_INVALID_ARG;
+    if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Nkv < Nq || Hq % Hkv != 0 || !valid_d(D) ||
+        !valid_dtype(dtype) || sinks < 0)
+        return ATTN_ERR_INVALID_ARG;
+    if ((long long)B * Hq > 65535 || Nkv > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+    if (o == q || o == k || o == v) return ATTN_ERR_INVALID_ARG;
+    const int64_t dq[3] = {(int64_t)Hq * Nq * D, (int64_t)Nq * D, D};
+    const int64_t dkv[3] = {(int64_t)Hkv * Nkv * D, (int64_t)Nkv * D, D};
+    const int64_t *const in[4] = {q_strides ? q_strides : dq, k_strides ? k_strides : dkv,
+                                  v_strides ? v_strides : dkv, o_strides ? o_strides : dq};
+    TensorStrides st[4];
+    attn_status_t status = parse_strides(in, B, Hq, Hkv, Nq, Nkv, D, dtype, st);
+    if (status != ATTN_OK) return status;
+    Ctx c;
+    status = get_ctx(stream, &c);
+    if (status != ATTN_OK) return status;
+    const float sc = resolve_scale(scale, D);
+    // no window: as wide as the sequence; sinks beyond it change nothing
+    const int w = window > 0 && window < Nkv ? window : Nkv;
+    const int s = sinks < Nkv ? sinks : Nkv;
+    if (half_dtype(dtype) && tc_full_supported(B, Hq, Nq, Nkv, D)) {
+        status = tc_causal_window(c, dtype, q, k, v, o, B, Hq, Hkv, Nq, Nkv, D, w, s, sc, st);
+        if (status != ATTN_ERR_UNSUPPORTED) return status;
+    }
+    return simt_causal_window(c, dtype, q, k, v, o, B, Hq, Hkv, Nq, Nkv, D, w, s, sc, st);
+}
+
+// ---------------------------------------------------------- paged KV cache
+
+// `n` strides of an array with the given extents and contiguous rows of D
+// elements: in (or, if null, the contiguous ones of that order) -> out.  An
+// extent-1 axis is never stepped along and gets a valid stride.  disjoint: the
+// rows are written, so they must not overlap (sorted by stride, each axis'
+// stride covers the span of the axes below it).
+static bool row_strides(const int64_t *in, const long long *ext, int n, int D, attn_dtype_t dt,
+                        bool disjoint, long long *out) {
+    long long dense = D;
+    for (int a = n - 1; a >= 0; --a) {
+        out[a] = in ? (long long)in[a] : dense;
+        if (ext[a] == 1) out[a] = D;
+        if (!stride_ok(out[a], dt)) return false;
+        if (dense < (1ll << 40)) dense *= ext[a];
+    }
+    if (!disjoint) return true;
+    long long span = D;
+    bool used[4] = {false, false, false, false};
+    for (int step = 0; step < n; ++step) {
+        int best = -1;
+        for (int a = 0; a < n; ++a)
+            if (!used[a] && ext[a] > 1 && (best < 0 || out[a] < out[best])) best = a;
+        if (best < 0) break;
+        if (out[best] < span || out[best] > (1ll << 62) / ext[best]) return false;
+        span = out[best] * ext[best];
+        used[best] = true;
+    }
+    return true;
+}
+
+static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static attn_status_t check_pool(const void *table, int B, int num_pages, int page_size,
+                                int max_pages, int64_t table_stride) {
+    if (!table || !aligned4(table)) return ATTN_ERR_INVALID_ARG;
+    if (B < 1 || num_pages < 1 || page_size < 1 || max_pages < 1 || page_size % 8 != 0)
+        return ATTN_ERR_INVALID_ARG;
+    if (B > 1 && table_stride < max_pages) return ATTN_ERR_INVALID_ARG;
+    if ((long long)max_pages * page_size >= (1ll << 31) || B > (1 << 20) ||
+        num_pages > 0x7fff0000 || table_stride > (1ll << 40))
+        return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+size_t attn_decode_gqa_paged_workspace_bytes(int B, int Hq, int Hkv, int D) {
+    if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > 16 || (D != 64 && D != 128))
+        return 0;
+    return decode_paged_workspace_bytes(B, Hq / Hkv, Hkv, D);
+}
+
+attn_status_t attn_decode_gqa_paged(const void *q, const void *k_pages, const void *v_pages,
+                                    const int32_t *page_table, const int32_t *seq_len, void *o,
+                                    int B, int Hq, int Hkv, int D, int num_pages, int page_size,
+                                    int max_pages, int64_t table_stride,
+                                    const int64_t q_strides[2], const int64_t k_strides[3],
+                                    const int64_t v_strides[3], const int64_t o_strides[2],
+                                    int window, int sinks, attn_dtype_t dtype, float scale,
+                                    void *workspace, size_t workspace_bytes, void *stream) {
+    if (!q || !k_pages || !v_pages || !seq_len || !o || !workspace) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) ||
+        !aligned4(seq_len) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_pool(page_table, B, num_pages, page_size, max_pages, table_stride);
+    if (st != ATTN_OK) return st;
+    if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !valid_d(D) || !valid_dtype(dtype) || sinks < 0)
+        return ATTN_ERR_INVALID_ARG;
+    if (!half_dtype(dtype) || D == 32 || Hq / Hkv > 16 || Hkv > 65535 ||
+        (long long)B * Hkv > 0x7fffffffll)
+        return ATTN_ERR_UNSUPPORTED;
+    if (o == q || o == k_pages || o == v_pages) return ATTN_ERR_INVALID_ARG;
+    PagedDecode a{};
+    const long long qe[2] = {B, Hq}, pe[3] = {num_pages, Hkv, page_size};
+    if (!row_strides(q_strides, qe, 2, D, dtype, false, a.q_st) ||
+        !row_strides(o_strides, qe, 2, D, dtype, true, a.o_st) ||
+        !row_strides(k_strides, pe, 3, D, dtype, false, a.k_st) ||
+        !row_strides(v_strides, pe, 3, D, dtype, false, a.v_st))
+        return ATTN_ERR_INVALID_ARG;
+    if (workspace_bytes < decode_paged_workspace_bytes(B, Hq / Hkv, Hkv, D)) return ATTN_ERR_RESOURCE;
+    Ctx c;
+    st = get_ctx(stream, &c);
+    if (st != ATTN_OK) return st;
+    a.q = q; a.k = k_pages; a.v = v_pages; a.o = o;
+    a.table = page_table; a.seq_len = seq_len;
+    a.B = B; a.G = Hq / Hkv; a.Hkv = Hkv; a.D = D;
+    a.P = num_pages; a.S = page_size; a.max_pages = max_pages;
+    a.table_stride = B > 1 ? table_stride : max_pages;
+    a.window = window; a.sinks = sinks;
+    a.scale = resolve_scale(scale, D);
+    a.ws = workspace;
+    return decode_paged(c, dtype, a);
+}
+
+attn_status_t attn_kv_append_paged(void *k_pages, void *v_pages, const void *k_new,
+                                   const void *v_new, const int32_t *page_table, int32_t *seq_len,
+                                   const int32_t *new_len, int B, int T, int Hkv, int D,
+                                   int num_pages, int page_size, int max_pages,
+                                   int64_t table_stride, const int64_t k_strides[3],
+                                   const int64_t v_strides[3], const int64_t kn_strides[3],
+                                   const int64_t vn_strides[3], attn_dtype_t dtype, int advance,
+                                   void *stream) {
+    if (!k_pages || !v_pages || !k_new || !v_new || !seq_len) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_new) || !aligned16(v_new) ||
+        !aligned4(seq_len) || !aligned4(new_len))
+        return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_pool(page_table, B, num_pages, page_size, max_pages, table_stride);
+    if (st != ATTN_OK) return st;
+    if (T < 1 || Hkv < 1 || !valid_d(D) || !valid_dtype(dtype)) return ATTN_ERR_INVALID_ARG;
+    if (k_pages == v_pages || k_new == k_pages || v_new == v_pages || k_new == v_pages ||
+        v_new == k_pages || new_len == seq_len)
+        return ATTN_ERR_INVALID_ARG;
+    if (Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
+    PagedAppend a{};
+    const long long pe[3] = {num_pages, Hkv, page_size}, ne[3] = {B, Hkv, T};
+    if (!row_strides(k_strides, pe, 3, D, dtype, true, a.k_st) ||
+        !row_strides(v_strides, pe, 3, D, dtype, true, a.v_st) ||
+        !row_strides(kn_strides, ne, 3, D, dtype, false, a.kn_st) ||
+        !row_strides(vn_strides, ne, 3, D, dtype, false, a.vn_st))
+        return ATTN_ERR_INVALID_ARG;
+    Ctx c;
+    st = get_ctx(stream, &c);
+    if (st != ATTN_OK) return st;
+    a.k = k_pages; a.v = v_pages; a.kn = k_new; a.vn = v_new;
+    a.table = page_table; a.seq_len = seq_len; a.new_len = new_len;
+    a.B = B; a.T = T; a.Hkv = Hkv; a.D = D; a.P = num_pages; a.S = page_size;
+    a.max_pages = max_pages;
+    a.table_stride = B > 1 ? table_stride : max_pages;
+    a.advance = advance;
+    return kv_append_paged(c, dtype, a);
+}
+
+size_t attn_kv_pages_workspace_bytes(int num_pages) {
+    return num_pages < 1 ? 0 : kv_pages_workspace_bytes(num_pages);
+}
+
+static attn_status_t check_pages_ws(const void *ws, size_t bytes, int num_pages) {
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return ATTN_ERR_INVALID_ARG;
+    return bytes < kv_pages_workspace_bytes(num_pages) ? ATTN_ERR_RESOURCE : ATTN_OK;
+}
+
+attn_status_t attn_kv_pages_reserve(int32_t *page_table, const int32_t *seq_len,
+                                    const int32_t *add_len, int32_t *page_refs, int B,
+                                    int num_pages, int page_size, int max_pages,
+                                    int64_t table_stride, void *workspace, size_t workspace_bytes,
+                                    void *stream) {
+    if (!seq_len || !add_len || !page_refs || !aligned16(page_refs) || !aligned4(seq_len) ||
+        !aligned4(add_len))
+        return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_pool(page_table, B, num_pages, page_size, max_pages, table_stride);
+    if (st == ATTN_OK) st = check_pages_ws(workspace, workspace_bytes, num_pages);
+    if (st != ATTN_OK) return st;
+    Ctx c;
+    st = get_ctx(stream, &c);
+    if (st != ATTN_OK) return st;
+    const PageTable t{page_table, B > 1 ? table_stride : max_pages, B, max_pages, num_pages, page_size};
+    return kv_pages_reserve(c, t, seq_len, add_len, page_refs, workspace);
+}
+
+attn_status_t attn_kv_pages_free(int32_t *page_table, const int32_t *seq_len, int32_t *page_refs,
+                                 int B, int num_pages, int page_size, int max_pages,
+                                 int64_t table_stride, int window, int sinks, void *stream) {
+    if (!seq_len || !page_refs || !aligned16(page_refs) || !aligned4(seq_len) || sinks < 0)
+        return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_pool(page_table, B, num_pages, page_size, max_pages, table_stride);
+    if (st != ATTN_OK) return st;
+    Ctx c;
+    st = get_ctx(stream, &c);
+    if (st != ATTN_OK) return st;
+    const PageTable t{page_table, B > 1 ? table_stride : max_pages, B, max_pages, num_pages, page_size};
+    return kv_pages_free(c, t, seq_len, page_refs, window, sinks);
+}
+
+attn_status_t attn_kv_pages_fork(int32_t *page_table, int32_t *seq_len, int32_t *page_refs,
+                                 const int32_t *src, const int32_t *dst, int n, int32_t *copy_src,
+                                 int32_t *copy_dst, int B, int num_pages, int page_size,
+                                 int max_pages, int64_t table_stride, void *workspace,
+                                 size_t workspace_bytes, void *stream) {
+    if (!seq_len || !page_refs || !src || !dst || !copy_src || !copy_dst || copy_src == copy_dst)
+        return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(page_refs) || !aligned4(seq_len) || !aligned4(src) || !aligned4(dst) ||
+        !aligned4(copy_src) || !aligned4(copy_dst))
+        return ATTN_ERR_INVALID_ARG;
+    if (copy_src == src || copy_src == dst || copy_dst == src || copy_dst == dst)
+        return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_pool(page_table, B, num_pages, page_size, max_pages, table_stride);
+    if (st == ATTN_OK) st = check_pages_ws(workspace, workspace_bytes, num_pages);
+    if (st != ATTN_OK) return st;
+    if (n < 1 || n > B) return ATTN_ERR_INVALID_ARG;
+    if (B > 262144) return ATTN_ERR_UNSUPPORTED;
+    Ctx c;
+    st = get_ctx(stream, &c);
+    if (st != ATTN_OK) return st;
+    const PageTable t{page_table, B > 1 ? table_stride : max_pages, B, max_pages, num_pages, page_size};
+    return kv_pages_fork(c, t, seq_len, page_refs, src, dst, n, copy_src, copy_dst, workspace);
+}
+
+attn_status_t attn_kv_pages_compact(const int32_t *page_table, const int32_t *page_refs,
+                                    int32_t *new_table, int32_t *new_refs, int32_t *copy_src,
+                                    int32_t *copy_dst, int32_t *count, int B, int num_pages,
+                                    int max_pages, int64_t table_stride, int64_t new_stride,
+                                    void *workspace, size_t workspace_bytes, void *stream) {
+    if (!page_refs || !new_table || !new_refs || !count || !aligned16(page_refs) ||
+        !aligned16(new_refs) || !aligned4(new_table) || !aligned4(count) || !aligned4(copy_src) ||
+        !aligned4(copy_dst))
+        return ATTN_ERR_INVALID_ARG;
+    if (num_pages > 1 && (!copy_src || !copy_dst || copy_src == copy_dst)) return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_pool(page_table, B, num_pages, 8, max_pages, table_stride);
+    if (st == ATTN_OK) st = check_pages_ws(workspace, workspace_bytes, num_pages);
+    if (st != ATTN_OK) return st;
+    if (B > 1 && (new_stride < max_pages || new_stride > (1ll << 40))) return ATTN_ERR_INVALID_ARG;
+    if (new_table == page_table && B > 1 && new_stride != table_stride) return ATTN_ERR_INVALID_ARG;
+    Ctx c;
+    st = get_ctx(stream, &c);
+    if (st != ATTN_OK) return st;
+    const PageTable t{const_cast<int32_t *>(page_table), B > 1 ? table_stride : max_pages, B,
+                      max_pages, num_pages, 8};
+    return kv_pages_compact(c, t, page_refs, new_table, B > 1 ? new_stride : max_pages, new_refs,
+                            copy_src, copy_dst, count, workspace);
+}
+
+attn_status_t attn_kv_pages_copy(void *k_pages, void *v_pages, const int32_t *copy_src,
+                                 const int32_t *copy_dst, int n, const int32_t *count, int layers,
+                                 int num_pages, int Hkv, int page_size, int D,
+                                 const int64_t k_strides[4], const int64_t v_strides[4],
+                                 attn_dtype_t dtype, void *stream) {
+    if (!k_pages || !v_pages || !copy_src || !copy_dst || k_pages == v_pages)
+        return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned4(copy_src) || !aligned4(copy_dst) ||
+        !aligned4(count))
+        return ATTN_ERR_INVALID_ARG;
+    if (n < 1 || layers < 1 || num_pages < 1 || Hkv < 1 || page_size < 1 || page_size % 8 != 0 ||
+        !valid_d(D) || !valid_dtype(dtype))
+        return ATTN_ERR_INVALID_ARG;
+    // a page side's vector count and the pieces of one pair are 32-bit
+    if ((long long)Hkv * page_size * D >= (1ll << 31) || layers > 65535 ||
+        (long long)Hkv * page_size * layers >= (1ll << 30))
+        return ATTN_ERR_UNSUPPORTED;
+    PagesCopy a{};
+    const long long pe[4] = {layers, num_pages, Hkv, page_size};
+    if (!row_strides(k_strides, pe, 4, D, dtype, true, a.k_st) ||
+        !row_strides(v_strides, pe, 4, D, dtype, true, a.v_st))
+        return ATTN_ERR_INVALID_ARG;
+    Ctx c;
+    const attn_status_t st = get_ctx(stream, &c);
+    if (st != ATTN_OK) return st;
+    a.k = k_pages; a.v = v_pages;
+    a.src = copy_src; a.dst = copy_dst; a.count = count;
+    a.n = n; a.layers = layers; a.Hkv = Hkv; a.S = page_size; a.D = D; a.P = num_pages;
+    return kv_pages_copy(c, dtype, a);
+}
+
 static attn_status_t check_na(int T, int Hg, int W, const int kernel[3]) {
     if (!kernel || T < 1 || Hg < 1 || W < 1) return ATTN_ERR_INVALID_ARG;
     for (int a = 0; a < 3; ++a)

@@ -217,8 +217,9 @@ simt_flash_kernel(const SimtParams p) {
 #pragma unroll
             for (int c = 1; c < kChunk; ++c) cm = fmaxf(cm, s[c]);
             const float mn = fmaxf(m, cm);
-            if (mn != -INFINITY) {
-                const float alpha = exp2f(m - mn);   // m == -inf -> 0
+            if (WIN ? seen != 0 : mn != -INFINITY) {
+                // m == -inf -> 0 (WIN: no finite score yet, NaN ones included: 1)
+                const float alpha = WIN && mn == -INFINITY ? 1.f : exp2f(m - mn);
                 l *= alpha;
 #pragma unroll
                 for (int d = 0; d < 32; ++d) acc[d] *= alpha;
@@ -226,7 +227,7 @@ simt_flash_kernel(const SimtParams p) {
 #pragma unroll
                 for (int c = 0; c < kChunk; ++c) {
                     if (WIN && !((seen >> c) & 1u)) continue;
-                    const float pc = exp2f(s[c] - mn);
+                    const float pc = WIN && mn == -INFINITY && s[c] == -INFINITY ? 0.f : exp2f(s[c] - mn);
                     l += pc;
                     const float *vr = Vs + (c0 + c) * L::ROW + sl * L::SLICE;
 #pragma unroll
