@@ -1,0 +1,158 @@
+"""Causal prefill with a sliding window and sinks against a 64-bit softmax over
+exactly the keys each query sees."""
+import pytest
+import torch
+
+from tests.paged_ref import DT, attend, bound, visible
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ta():
+    from transformer_attention_tcgen05_gb300.build import build
+    build()
+    import transformer_attention_tcgen05_gb300 as ta
+    torch.cuda.set_device(0)
+    return ta
+
+
+def make(dt, B, heads, N, D, order, seed):
+    g = torch.Generator().manual_seed(seed)
+    if order == "token":
+        return torch.randn(B, N, heads, D, generator=g).to(DT[dt]).cuda().transpose(1, 2)
+    return torch.randn(B, heads, N, D, generator=g).to(DT[dt]).cuda()
+
+
+def p_eps(dt, D):
+    """Rounding of P before the P V product: to 16 bits on the tensor cores."""
+    return torch.finfo(DT[dt]).eps / 2 if dt != "f32" and D != 32 else 0.0
+
+
+def check(ta, dt, q, k, v, o, window, sinks, rows=None):
+    B, Hq, Nq, D = q.shape
+    Hkv, Nkv = k.shape[1], k.shape[2]
+    rows = list(range(Nq)) if rows is None else rows
+    see = visible(Nkv, [Nkv - Nq + r for r in rows], window, sinks)
+    for b in range(B):
+        for h in range(Hq):
+            hk = h // (Hq // Hkv)
+            ref, A, E, s1 = attend(q[b, h, rows].double().cpu(), k[b, hk].double().cpu(),
+                                   v[b, hk].double().cpu(), see)
+            got = o[b, h, rows].double().cpu()
+            lim = bound(dt, ref, A, E, s1, int(see.sum(1).max()), p_eps(dt, D))
+            bad = ~((got - ref).abs() <= lim)
+            assert not bad.any(), (b, h, torch.nonzero(bad)[:5].tolist(),
+                                   ((got - ref).abs() / lim).max().item())
+
+
+CASES = [
+    # dt, B, Hq, Hkv, Nq, Nkv, D, window, sinks, order
+    ("bf16", 1, 2, 1, 1, 1, 128, 1, 0, "head"),
+    ("bf16", 2, 3, 3, 1, 300, 64, 17, 2, "token"),
+    ("bf16", 1, 4, 2, 129, 129, 128, 1, 0, "head"),
+    ("bf16", 1, 4, 2, 300, 300, 128, 128, 4, "token"),
+    ("f16", 2, 4, 1, 300, 300, 64, 128, 4, "head"),
+    ("bf16", 1, 2, 1, 700, 700, 128, 100, 0, "head"),
+    ("bf16", 1, 2, 1, 700, 700, 64, 100, 130, "token"),     # sinks past a key tile
+    ("bf16", 1, 2, 2, 700, 700, 128, 256, 256, "head"),     # whole sink tiles
+    ("bf16", 1, 2, 1, 513, 1000, 128, 255, 3, "head"),      # queries continue a prompt
+    ("f16", 1, 2, 1, 130, 777, 128, 129, 1, "token"),
+    ("bf16", 1, 7, 1, 257, 900, 64, 384, 5, "head"),
+    ("bf16", 1, 2, 1, 400, 400, 128, 400, 0, "head"),       # the window covers everything
+    ("bf16", 1, 2, 1, 400, 400, 64, 100000, 7, "head"),
+    ("bf16", 1, 2, 1, 400, 500, 128, 0, 0, "head"),         # no window
+    ("bf16", 1, 2, 1, 400, 400, 64, 3, 1000, "head"),       # sinks cover everything
+    ("f32", 1, 4, 2, 200, 200, 64, 50, 4, "token"),
+    ("f32", 2, 2, 1, 65, 333, 128, 64, 70, "head"),
+    ("f32", 1, 1, 1, 1, 1, 32, 5, 5, "head"),
+    ("bf16", 1, 2, 1, 150, 150, 32, 33, 1, "head"),         # D = 32: SIMT kernel
+    ("f16", 1, 2, 2, 90, 200, 32, 70, 0, "token"),
+]
+
+
+@pytest.mark.parametrize("dt,B,Hq,Hkv,Nq,Nkv,D,window,sinks,order", CASES)
+def test_window_parity(ta, dt, B, Hq, Hkv, Nq, Nkv, D, window, sinks, order):
+    q = make(dt, B, Hq, Nq, D, order, 1)
+    k, v = make(dt, B, Hkv, Nkv, D, order, 2), make(dt, B, Hkv, Nkv, D, order, 3)
+    fam = "simt" if dt == "f32" or D == 32 else "tc_flash"
+    n0 = ta.launch_count(fam)
+    o = ta.causal_gqa_window_fwd(q, k, v, window, sinks)
+    assert ta.launch_count(fam) == n0 + 1
+    assert ta.device_status() == 0
+    check(ta, dt, q, k, v, o, window, sinks)
+
+
+def test_window_long_sampled_rows(ta):
+    q = make("bf16", 1, 8, 9000, 128, "token", 4)
+    k, v = make("bf16", 1, 2, 9000, 128, "token", 5), make("bf16", 1, 2, 9000, 128, "token", 6)
+    o = ta.causal_gqa_window_fwd(q, k, v, 2048, 4)
+    check(ta, "bf16", q, k, v, o, 2048, 4, rows=[0, 1, 127, 128, 2047, 2048, 2051, 2052, 5000, 8191, 8999])
+
+
+def test_window_scores_far_above_the_running_maximum(ta):
+    """Keys that grow along the sequence move the maximum in every tile."""
+    q = make("bf16", 1, 2, 600, 128, "head", 7)
+    k, v = make("bf16", 1, 2, 600, 128, "head", 8), make("bf16", 1, 2, 600, 128, "head", 9)
+    k = (k.float() * torch.linspace(0.1, 12, 600).cuda()[None, None, :, None]).bfloat16()
+    o = ta.causal_gqa_window_fwd(q, k, v, 300, 2)
+    check(ta, "bf16", q, k, v, o, 300, 2)
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 128), ("f16", 64), ("f32", 64), ("bf16", 32)])
+@pytest.mark.parametrize("what", ["v_nan", "v_inf", "k_nan", "k_inf"])
+def test_what_a_row_does_not_see_does_not_reach_it(ta, dt, D, what):
+    N, window, sinks, spots = 500, 90, 3, [0, 200, 333, 499]
+    q = make(dt, 1, 2, N, D, "head", 10)
+    k, v = make(dt, 1, 1, N, D, "head", 11), make(dt, 1, 1, N, D, "head", 12)
+    clean = ta.causal_gqa_window_fwd(q, k, v, window, sinks)
+    x = k if what[0] == "k" else v
+    x[:, :, spots, 5] = float("nan") if what.endswith("nan") else float("inf")
+    o = ta.causal_gqa_window_fwd(q, k, v, window, sinks)
+    assert ta.device_status() == 0
+    sees = visible(N, range(N), window, sinks)[:, spots].any(1).cuda()
+    check(ta, dt, q, k, v, o, window, sinks, rows=torch.nonzero(~sees)[:, 0].tolist())
+    if what.endswith("nan"):
+        assert torch.isnan(o[:, :, sees].float()).any(-1).all()
+    else:
+        # an infinite value: the rows that see it have it (or NaN) in channel 5
+        if what == "v_inf":
+            assert not torch.isfinite(o[:, :, sees, 5].float()).any()
+            other = [c for c in range(D) if c != 5]
+            assert torch.isfinite(o[:, :, sees][..., other].float()).all()
+    assert torch.isfinite(clean.float()).all()
+
+
+def test_window_output_view_and_sentinels(ta):
+    B, Hq, N, D = 2, 4, 200, 64
+    q, k, v = (make("bf16", B, h, N, D, "token", 20 + i) for i, h in enumerate((Hq, 2, 2)))
+    wide = torch.full((B, N, Hq + 2, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    o = wide[:, :, 1:1 + Hq].transpose(1, 2)
+    ta.causal_gqa_window_fwd(q, k, v, 33, 2, o=o)
+    assert torch.equal(o, ta.causal_gqa_window_fwd(q, k, v, 33, 2))
+    assert (wide[:, :, 0] == 7).all() and (wide[:, :, -1] == 7).all()
+
+
+def test_window_on_another_stream_and_in_a_graph(ta):
+    q, k, v = (make("bf16", 1, h, 300, 128, "head", 30 + i) for i, h in enumerate((4, 2, 2)))
+    want = ta.causal_gqa_window_fwd(q, k, v, 64, 1)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = ta.causal_gqa_window_fwd(q, k, v, 64, 1)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(got, want)
+    o = torch.zeros_like(q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ta.causal_gqa_window_fwd(q, k, v, 64, 1, o=o)
+    q.copy_(q.flip(2))
+    g.replay()
+    assert torch.equal(o, ta.causal_gqa_window_fwd(q, k, v, 64, 1))
+
+
+def test_no_window_agrees_with_the_causal_entry(ta):
+    q, k, v = (make("bf16", 1, h, 500, 128, "head", 40 + i) for i, h in enumerate((4, 2, 2)))
+    a, b = ta.causal_gqa_fwd(q, k, v), ta.causal_gqa_window_fwd(q, k, v, 0)
+    check(ta, "bf16", q, k, v, a, 0, 0)
+    check(ta, "bf16", q, k, v, b, 0, 0)
