@@ -426,12 +426,15 @@ def test_fork_refuses_what_it_cannot_do(ta):
     assert refs[15] == 0
     ta.kv_pages_fork(bad, m.len, refs, m.i32([0]), m.i32([3]), 8)
     assert ta.device_status() == 6 and torch.equal(refs, m.refs)
-    # no page left for the copies
-    m.reserve([0, 100 - 100, 0, 0, 0, 0])
-    while m.reserve([0, 8, 0, 0, 0, 0]):
-        m.append([0, 8, 0, 0, 0, 0])
-        if m.pool.len[1] >= 64:
-            break
+
+
+def test_fork_without_pages_for_the_copies_changes_nothing(ta):
+    m = Model(ta, 4, 8, 6, 8)
+    m.reserve([20, 16, 0, 0])                   # 3 + 2 of 6 pages
+    m.append([20, 16, 0, 0])
+    assert not m.fork([0, 0], [2, 3])           # two copies, one free page
+    m.check()
+    assert m.fork([0, 1], [2, 3])
     m.check()
 
 
@@ -549,7 +552,7 @@ def test_prefill_append_fork_decode(ta):
     sl = torch.zeros(B, dtype=torch.int32, device="cuda")
     n = torch.tensor([N - 1, 0, 0], dtype=torch.int32, device="cuda")
     ta.kv_pages_reserve(table, sl, n, refs, S)
-    ta.kv_append_paged(kp, vp, k.expand(B, -1, -1, -1), v.expand(B, -1, -1, -1), table, sl, n)
+    ta.kv_append_paged(kp, vp, k.repeat(B, 1, 1, 1), v.repeat(B, 1, 1, 1), table, sl, n)
     cs, cd = ta.kv_pages_fork(table, sl, refs, n.new_tensor([0, 0]), n.new_tensor([1, 2]), S)
     ta.kv_pages_copy(kp, vp, cs, cd)
     assert refs.max() == 3

@@ -102,7 +102,7 @@ def test_window_scores_far_above_the_running_maximum(ta):
 @pytest.mark.parametrize("dt,D", [("bf16", 128), ("f16", 64), ("f32", 64), ("bf16", 32)])
 @pytest.mark.parametrize("what", ["v_nan", "v_inf", "k_nan", "k_inf"])
 def test_what_a_row_does_not_see_does_not_reach_it(ta, dt, D, what):
-    N, window, sinks, spots = 500, 90, 3, [0, 200, 333, 499]
+    N, window, sinks, spots = 500, 90, 3, [200, 333, 499]
     q = make(dt, 1, 2, N, D, "head", 10)
     k, v = make(dt, 1, 1, N, D, "head", 11), make(dt, 1, 1, N, D, "head", 12)
     clean = ta.causal_gqa_window_fwd(q, k, v, window, sinks)
