@@ -125,6 +125,20 @@ def test_decode_paged_workspace_is_left_ready_and_results_repeat(ta):
         assert torch.equal(ta.decode_gqa_paged(q, kp, vp, table, sl, workspace=ws), first)
 
 
+@pytest.mark.parametrize("dt,D,S,order,G", [("bf16", 128, 16, "head", 2), ("f16", 64, 32, "token", 1),
+                                            ("bf16", 128, 8, "head", 9)])
+def test_decode_paged_ring_wraps_in_back_to_back_launches(ta, dt, D, S, order, G):
+    """Ten chunks and more per CTA: every ring slot is used several times, and the
+    next launch starts while the last CTAs finish."""
+    lens = [6000, 5500, 33, 7100]
+    q, kp, vp, table, sl, ks, vs = build_case(dt, lens, 4 * G, 4, D, S, 0, 0, order, 9)
+    ws = torch.zeros(ta.decode_paged_workspace_bytes(4, 4 * G, 4, D), dtype=torch.uint8, device="cuda")
+    outs = [ta.decode_gqa_paged(q, kp, vp, table, sl, workspace=ws) for _ in range(30)]
+    assert ta.device_status() == 0
+    check(dt, q, ks, vs, lens, outs[0], 0, 0)
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
 def test_decode_paged_strided_query_output_and_table(ta):
     lens = [50, 400, 33]
     q, kp, vp, table, sl, ks, vs = build_case("bf16", lens, 6, 2, 64, 16, 0, 0, "head", 4)

@@ -64,14 +64,17 @@ struct PgCfg {
     static constexpr int MISC = 1024;                       // barriers, flags
     static constexpr int BUDGET = 113 * 1024 - 1024;        // two CTAs per SM, alignment slack
     static constexpr int FIT = (BUDGET - MERGE - ML - MISC) / (2 * TILE);
-    static constexpr int SLOTS = FIT > 8 ? 8 : FIT;
+    // A multiple of the consumer warps: a slot always feeds the same warp, so
+    // a warp that waits for a slot's phase has itself seen the phase before
+    // complete (a parity wait cannot tell phase n - 2 from phase n).
+    static constexpr int SLOTS = FIT >= 8 ? 8 : FIT / kCW * kCW;
     static constexpr int OFF_K = 0;
     static constexpr int OFF_V = SLOTS * TILE;
     static constexpr int OFF_M = 2 * SLOTS * TILE;
     static constexpr int OFF_ML = OFF_M + MERGE;
     static constexpr int OFF_MISC = OFF_ML + ML;
     static constexpr int SMEM = OFF_MISC + MISC + 1024;
-    static_assert(SLOTS >= 4, "at least one slot per consumer warp");
+    static_assert(SLOTS >= kCW && SLOTS % kCW == 0, "every slot must always feed the same consumer warp");
 };
 
 struct PgParams {
