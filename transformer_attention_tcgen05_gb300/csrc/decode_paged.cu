@@ -51,7 +51,9 @@ constexpr int kCW = 4;            // consumer warps
 constexpr int kNT = (kCW + 2) * 32;
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxCtas = 2 * 192; // workspace slots (2 CTAs on up to 192 SMs)
-constexpr int kMinChunks = kCW;   // a CTA's range is at least one chunk per consumer warp
+// A CTA's range is at least one chunk per consumer warp, unless every unit is
+// shorter than that: then the units are spread over more CTAs.
+constexpr int kMinChunks = kCW;
 
 template <int D, int NT>
 struct PgCfg {
@@ -98,8 +100,9 @@ struct PgParams {
 struct Misc {
     uint64_t full_k[8], full_v[8], empty_k[8], empty_v[8];
     long long warp_sum[kNT / 32];
+    int warp_max[kNT / 32];
     long long start_off;
-    int start_b;
+    int start_b, start_len;
     int abort;
     unsigned last;
     int bad[8];                            // per slot: a page id of the chunk is out of range
@@ -140,9 +143,12 @@ struct Walk {
     long long left;                        // chunks of the range from this segment on
     long long flat;                        // flat index of the segment's first chunk
 
-    __device__ Walk(const PgParams &pp, int b0, long long off, long long f0, long long count)
+    int ahead;                             // seq_len[b + 1], loaded before it is needed
+
+    __device__ Walk(const PgParams &pp, int b0, int len0, long long off, long long f0, long long count)
         : p(pp), b(b0), left(count), flat(f0) {
-        plan = make_plan(p, p.seq_len[b]);
+        plan = make_plan(p, len0);
+        ahead = b + 1 < p.B ? p.seq_len[b + 1] : 0;
         kvh = int(off / plan.n);
         v0 = int(off % plan.n);
         cnt = int(left < plan.n - v0 ? left : plan.n - v0);
@@ -155,7 +161,9 @@ struct Walk {
         if (++kvh == p.Hkv) {
             kvh = 0;
             do {                            // the range ends inside the list: b stays below B
-                plan = make_plan(p, p.seq_len[++b]);
+                plan = make_plan(p, ahead);
+                ++b;
+                ahead = b + 1 < p.B ? p.seq_len[b + 1] : 0;
             } while (plan.n == 0);
         }
         cnt = int(left < plan.n ? left : plan.n);
@@ -193,6 +201,14 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Takes the next ticket: releases what this CTA wrote, acquires what the
+// holders of the earlier tickets wrote.
+__device__ __forceinline__ unsigned ticket_add(unsigned *t) {
+    unsigned old;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(t) : "memory");
+    return old;
+}
+
 template <int D, int NT, bool F16>
 __global__ void __launch_bounds__(kNT, kCtasPerSm)
 decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -226,67 +242,87 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     //      Sequences with nothing to attend to are dealt out over the CTAs:
     //      length 0 writes zeros, a length outside the table is reported and
     //      its output left as it was.
-    long long total = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kNT) {
-        const int b = b0 + threadIdx.x;
-        if (b < p.B) {
-            const int len = p.seq_len[b];
-            const Plan r = make_plan(p, len);
-            total += r.n;
-            if (r.n == 0 && b % ctas == cta) {
-                if (len != 0) {
-                    raise_device_error(p.err, kDevCheck);
-                } else {
-                    for (int h = 0; h < p.Hkv * p.G; ++h) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + b * p.o_sb +
-                                                               h * p.o_sh);
-                        for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-                    }
+    const bool one_tile = p.B <= kNT;                  // a thread per sequence: read once
+    long long inc = 0;
+    int n_mine = 0, len_mine = 0, n_max = 0;
+    for (int b = threadIdx.x; b < p.B; b += kNT) {
+        len_mine = p.seq_len[b];
+        n_mine = make_plan(p, len_mine).n;
+        inc += n_mine;
+        n_max = imax(n_max, n_mine);
+        if (n_mine == 0 && b % ctas == cta) {
+            if (len_mine != 0) {
+                raise_device_error(p.err, kDevCheck);
+            } else {
+                for (int h = 0; h < p.Hkv * p.G; ++h) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + b * p.o_sb + h * p.o_sh);
+                    for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
                 }
             }
         }
     }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-    if (lane == 0) ms->warp_sum[warp] = total;
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += up;
+        n_max = imax(n_max, __shfl_xor_sync(0xffffffffu, n_max, off));
+    }
+    if (lane == 31) {
+        ms->warp_sum[warp] = inc;
+        ms->warp_max[warp] = n_max;
+    }
     __syncthreads();
-    total = 0;
-    for (int w = 0; w < kNT / 32; ++w) total += ms->warp_sum[w];
-    __syncthreads();
+    long long total = 0, before = inc - n_mine;        // before: chunks of the sequences ahead (one tile)
+#pragma unroll
+    for (int w = 0; w < kNT / 32; ++w) {
+        if (w < warp) before += ms->warp_sum[w];
+        total += ms->warp_sum[w];
+        n_max = imax(n_max, ms->warp_max[w]);
+    }
     total *= p.Hkv;
     long long per = (total + ctas - 1) / ctas;
-    if (per < kMinChunks) per = kMinChunks;
+    if (per < imin(kMinChunks, n_max)) per = imin(kMinChunks, n_max);
     const long long f0 = per * cta;
     if (f0 >= total) return;
     const long long f1 = f0 + per < total ? f0 + per : total;
-    long long carry = 0;                               // chunks of the sequences before this tile
-    for (int b0 = 0; b0 < p.B; b0 += kNT) {
-        const int b = b0 + threadIdx.x;
-        const long long n = b < p.B ? make_plan(p, p.seq_len[b]).n : 0;
-        long long inc = n;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long up = __shfl_up_sync(0xffffffffu, inc, off);
-            if (lane >= off) inc += up;
-        }
-        if (lane == 31) ms->warp_sum[warp] = inc;
-        __syncthreads();
-        long long before = carry, tile = 0;
-        for (int w = 0; w < kNT / 32; ++w) {
-            if (w < warp) before += ms->warp_sum[w];
-            tile += ms->warp_sum[w];
-        }
-        before += inc - n;
-        if (n > 0 && f0 >= before * p.Hkv && f0 < (before + n) * p.Hkv) {
-            ms->start_b = b;
+    if (one_tile) {
+        if (n_mine > 0 && f0 >= before * p.Hkv && f0 < (before + n_mine) * p.Hkv) {
+            ms->start_b = threadIdx.x;
+            ms->start_len = len_mine;
             ms->start_off = f0 - before * p.Hkv;
         }
-        carry += tile;
         __syncthreads();
-        if (carry * p.Hkv > f0) break;
+    } else {
+        long long carry = 0;                           // chunks of the sequences before this tile
+        for (int b0 = 0; b0 < p.B; b0 += kNT) {
+            __syncthreads();
+            const int b = b0 + threadIdx.x;
+            const int len = b < p.B ? p.seq_len[b] : 0;
+            const int n = make_plan(p, len).n;
+            inc = n;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long up = __shfl_up_sync(0xffffffffu, inc, off);
+                if (lane >= off) inc += up;
+            }
+            if (lane == 31) ms->warp_sum[warp] = inc;
+            __syncthreads();
+            before = carry + inc - n;
+            for (int w = 0; w < kNT / 32; ++w) {
+                if (w < warp) before += ms->warp_sum[w];
+                carry += ms->warp_sum[w];
+            }
+            if (n > 0 && f0 >= before * p.Hkv && f0 < (before + n) * p.Hkv) {
+                ms->start_b = b;
+                ms->start_len = len;
+                ms->start_off = f0 - before * p.Hkv;
+            }
+            if (carry * p.Hkv > f0) break;
+        }
+        __syncthreads();
     }
 
-    Walk w(p, ms->start_b, ms->start_off, f0, f1 - f0);
+    Walk w(p, ms->start_b, ms->start_len, ms->start_off, f0, f1 - f0);
     int f = 0;                                         // chunk number within the CTA's range
 
     if (warp >= kCW) {
@@ -380,9 +416,10 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     // segments: the other warps meet it at their barriers, and every unit's
     // ticket is counted up and reset as usual
     int dead = 0;
-    do {
-        // ---- q of the unit's heads as MMA B operands (heads are columns)
-        uint32_t qf[NT][D / 16][2];
+    // q of the unit's heads as MMA B operands (heads are columns); the next
+    // segment's are requested before this one's results are merged
+    uint32_t qf[NT][D / 16][2];
+    auto load_q = [&]() {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int h = nt * 8 + quad;
@@ -394,6 +431,9 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
                 qf[nt][kk][1] = h < p.G ? *reinterpret_cast<const uint32_t *>(qp + kk * 16 + 8) : 0u;
             }
         }
+    };
+    load_q();
+    for (bool more = true; more;) {
         float m[NT][2], l[NT][2], acc[NT][D / 16][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -529,6 +569,13 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         }
         f = f_end;
 
+        // this segment (the walk goes on to the next one)
+        const int seg_b = w.b, seg_kvh = w.kvh, seg_v0 = w.v0, seg_cnt = w.cnt, seg_n = w.plan.n;
+        const long long u0 = w.flat - w.v0;            // flat index of the unit's first chunk
+        more = w.next();
+        if (more) load_q();
+        T *const o_unit = static_cast<T *>(p.o) + seg_b * p.o_sb + (long long)seg_kvh * p.G * p.o_sh;
+
         // ---- the four warps' (max, sum, O) -> one per head
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -553,10 +600,10 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         ptx::named_barrier_sync(1, kCW * 32);
         bad = ms->warp_bad[0] | ms->warp_bad[1] | ms->warp_bad[2] | ms->warp_bad[3];
 
-        const bool whole = w.v0 == 0 && w.cnt == w.plan.n;
+        const bool whole = seg_v0 == 0 && seg_cnt == seg_n;
         // a range holds at most one segment that starts inside its unit (slot 0)
         // and one that starts at its unit's head and is cut (slot 1)
-        const int slot = 2 * cta + (w.v0 == 0 ? 1 : 0);
+        const int slot = 2 * cta + (seg_v0 == 0 ? 1 : 0);
         float *po = p.part_o + (size_t)slot * C::HP * D;
         float *pml = p.part_ml + (size_t)slot * C::HP * 2;
         for (int e = threadIdx.x; e < p.G * (D / 4); e += kCW * 32) {
@@ -582,7 +629,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
             if (whole) {
                 if (!bad) {
                     const float inv = 1.f / L;
-                    T *dst = static_cast<T *>(p.o) + w.b * p.o_sb + (long long)(w.kvh * p.G + h) * p.o_sh + d;
+                    T *dst = o_unit + h * p.o_sh + d;
                     *reinterpret_cast<uint2 *>(dst) =
                         make_uint2(H::pack(O.x * inv, O.y * inv), H::pack(O.z * inv, O.w * inv));
                 }
@@ -593,15 +640,14 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
             }
         }
         if (!whole) {
-            const int unit = w.b * p.Hkv + w.kvh;
-            const long long u0 = w.flat - w.v0;        // flat index of the unit's first chunk
-            const int c0 = int(u0 / per), c1 = int((u0 + w.plan.n - 1) / per);
-            __threadfence();
+            const int unit = seg_b * p.Hkv + seg_kvh;
+            const int c0 = int(u0 / per), c1 = int((u0 + seg_n - 1) / per);
+            // the barrier puts the CTA's partial before thread 0's release; its
+            // acquire and the second barrier put the other CTAs' before the reads
             ptx::named_barrier_sync(1, kCW * 32);
-            if (threadIdx.x == 0) ms->last = atomicAdd(&p.tickets[unit], 1u) == unsigned(c1 - c0);
+            if (threadIdx.x == 0) ms->last = ticket_add(&p.tickets[unit]) == unsigned(c1 - c0);
             ptx::named_barrier_sync(1, kCW * 32);
             if (ms->last) {
-                __threadfence();
                 for (int e = threadIdx.x; e < p.G * (D / 4); e += kCW * 32) {
                     const int h = e / (D / 4), d = (e % (D / 4)) * 4;
                     float M = -INFINITY, L = 0.f;
@@ -647,8 +693,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
                     }
                     if (!skip) {
                         const float inv = 1.f / L;
-                        T *dst = static_cast<T *>(p.o) + w.b * p.o_sb +
-                                 (long long)(w.kvh * p.G + h) * p.o_sh + d;
+                        T *dst = o_unit + h * p.o_sh + d;
                         *reinterpret_cast<uint2 *>(dst) =
                             make_uint2(H::pack(O.x * inv, O.y * inv), H::pack(O.z * inv, O.w * inv));
                     }
@@ -657,7 +702,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
             }
         }
         ptx::named_barrier_sync(1, kCW * 32);          // the merge rows may be written again
-    } while (w.next());
+    }
 }
 
 // 5D map {64 channels, S rows, D / 64 panels, Hkv, pages} over a cache with
