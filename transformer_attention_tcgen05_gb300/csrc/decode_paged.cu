@@ -19,19 +19,22 @@
 //  * A CTA whose range cuts a unit writes a partial (max, sum, O) per head to
 //    the workspace; the last CTA of the unit to arrive (ticket) joins the
 //    partials in CTA order, so the result does not depend on who is last.
-//  * Two producer warps (K, V) stream chunks with TMA into a shared-memory
-//    ring: a box of up to 32 rows x D channels per copy, the page and
-//    the KV head being coordinates of one 5D tensor map, so either memory
-//    order of a page costs nothing and addresses are 64-bit.  The 32 lanes
-//    look up 32 boxes' pages at once.
-//  * Four consumer warps, one chunk each: S^T = K q^T (rows x heads) and
-//    O^T += V^T P^T with mma.sync m16n8k16.  With at most 16 query heads per
-//    KV head the product is 8 or 16 columns wide; the warp-level instruction
-//    takes the heads as its n = 8 columns, leaves the softmax statistics in
-//    registers and P^T one 8 x 8 transpose away from the next operand, where a
-//    tcgen05 tile would need 128 rows, a round trip through tensor memory and
-//    P staged in shared memory, for a tensor pipe that is mostly idle either
-//    way.
+//  * Every warp streams chunks of its own (chunk f of the range goes to warp
+//    f % CW) into shared memory of its own with TMA: a box of up to 32 rows x D
+//    channels per copy, the page and the KV head being coordinates of one 5D
+//    tensor map, so either memory order of a page costs nothing and addresses
+//    are 64-bit.  A warp asks for its next K right after it has read this one
+//    and for its next V after this one's P V; no warp waits for another inside
+//    a unit.  The 32 lanes look up 32 boxes' pages at once, one group ahead, also
+//    across units.  (With a producer warp for K and one for V the first four
+//    chunks went out one after the other, 0.3 us each.)
+//  * S^T = K q^T (rows x heads) and O^T += V^T P^T with mma.sync m16n8k16.
+//    With at most 16 query heads per KV head the product is 8 or 16 columns
+//    wide; the warp-level instruction takes the heads as its n = 8 columns,
+//    leaves the softmax statistics in registers and P^T one 8 x 8 transpose
+//    away from the next operand, where a tcgen05 tile would need 128 rows, a
+//    round trip through tensor memory and P staged in shared memory, for a
+//    tensor pipe that is mostly idle either way.
 //  * P is split into two 16-bit terms (P = hi + lo), so the P V product keeps
 //    ~16 bits of P instead of 8 (bf16): a second MMA on operands that are in
 //    registers already.  Sums and statistics are fp32; the output is rounded
@@ -47,36 +50,28 @@ namespace attn {
 namespace {
 
 constexpr int kChunk = 32;        // positions per chunk
-constexpr int kCW = 4;            // consumer warps
-constexpr int kNT = (kCW + 2) * 32;
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxCtas = 2 * 192; // workspace slots (2 CTAs on up to 192 SMs)
-// A CTA's range is at least one chunk per consumer warp, unless every unit is
-// shorter than that: then the units are spread over more CTAs.
-constexpr int kMinChunks = kCW;
 
 template <int D, int NT>
 struct PgCfg {
+    static constexpr int CW = 4;  // warps
+    static constexpr int NS = D == 64 ? 2 : 1;              // chunks in flight per warp
+    static constexpr int THREADS = CW * 32;
     static constexpr int HP = NT * 8;                       // padded heads per KV head
     static constexpr int PANELS = D / 64;
     static constexpr int TILE = kChunk * D * 2;             // K (or V) bytes of a chunk
     static constexpr int LDM = D + 4;                       // floats per merge row (bank spread)
-    static constexpr int MERGE = kCW * HP * LDM * 4;
-    static constexpr int ML = kCW * HP * 2 * 4;
-    static constexpr int MISC = 1024;                       // barriers, flags
-    static constexpr int BUDGET = 113 * 1024 - 1024;        // two CTAs per SM, alignment slack
-    static constexpr int FIT = (BUDGET - MERGE - ML - MISC) / (2 * TILE);
-    // A multiple of the consumer warps: a slot always feeds the same warp, so
-    // a warp that waits for a slot's phase has itself seen the phase before
-    // complete (a parity wait cannot tell phase n - 2 from phase n).
-    static constexpr int SLOTS = FIT >= 8 ? 8 : FIT / kCW * kCW;
+    static constexpr int MERGE = CW * HP * LDM * 4;
+    static constexpr int ML = CW * HP * 2 * 4;
+    static constexpr int MISC = 512;                        // barriers, flags
     static constexpr int OFF_K = 0;
-    static constexpr int OFF_V = SLOTS * TILE;
-    static constexpr int OFF_M = 2 * SLOTS * TILE;
+    static constexpr int OFF_V = CW * NS * TILE;
+    static constexpr int OFF_M = 2 * CW * NS * TILE;
     static constexpr int OFF_ML = OFF_M + MERGE;
     static constexpr int OFF_MISC = OFF_ML + ML;
     static constexpr int SMEM = OFF_MISC + MISC + 1024;
-    static_assert(SLOTS >= kCW && SLOTS % kCW == 0, "every slot must always feed the same consumer warp");
+    static_assert(kCtasPerSm * (SMEM + 1024) <= 228 * 1024, "the CTAs of an SM must fit its shared memory");
 };
 
 struct PgParams {
@@ -97,18 +92,19 @@ struct PgParams {
     unsigned *err;
 };
 
+constexpr int kMaxWarps = 8;
+
 struct Misc {
-    uint64_t full_k[8], full_v[8], empty_k[8], empty_v[8];
-    long long warp_sum[kNT / 32];
-    int warp_max[kNT / 32];
+    uint64_t full_k[kMaxWarps * 2], full_v[kMaxWarps * 2];   // [warp][slot]
+    long long warp_sum[kMaxWarps];
+    int warp_max[kMaxWarps];
     long long start_off;
     int start_b, start_len;
     int abort;
     unsigned last;
-    int bad[8];                            // per slot: a page id of the chunk is out of range
-    int warp_bad[kCW];
+    int warp_bad[kMaxWarps];
 };
-static_assert(sizeof(Misc) <= 1024, "barrier block must fit its reserved bytes");
+static_assert(sizeof(Misc) <= 512, "barrier block must fit its reserved bytes");
 
 // The chunks of one sequence that hold a visible position: chunks [0, n1) for
 // the sinks and [c2, ...) for the window (one run from 0 where they touch).
@@ -209,13 +205,22 @@ __device__ __forceinline__ unsigned ticket_add(unsigned *t) {
     return old;
 }
 
+// The pages of one warp's next chunks, box by box: lane i holds box i % nb of
+// chunk i / nb of the group.
+struct Group {
+    int page, row;                         // this lane's box
+    unsigned needs, bads;                  // boxes to copy; boxes whose entry is no page
+    int kvh, cnt;                          // KV head; chunks in the group (0: the range is done)
+};
+
 template <int D, int NT, bool F16>
-__global__ void __launch_bounds__(kNT, kCtasPerSm)
+__global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, kCtasPerSm)
 decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                     const PgParams p) {
     using C = PgCfg<D, NT>;
     using H = H16<F16>;
     using T = typename H::T;
+    constexpr int CW = C::CW, NS = C::NS, kNT = C::THREADS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (ptx::smem_addr(smem_raw) & 1023)) & 1023);
     Misc *ms = reinterpret_cast<Misc *>(smem + C::OFF_MISC);
@@ -224,14 +229,14 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     const int cta = blockIdx.x, ctas = gridDim.x;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::SLOTS; ++s) {
+        for (int s = 0; s < CW * NS; ++s) {
             ptx::mbar_init(&ms->full_k[s], 1);
             ptx::mbar_init(&ms->full_v[s], 1);
-            ptx::mbar_init(&ms->empty_k[s], 1);
-            ptx::mbar_init(&ms->empty_v[s], 1);
         }
         ptx::fence_barrier_init();
         ms->abort = 0;
+        ptx::prefetch_tmap(&tk);
+        ptx::prefetch_tmap(&tv);
     }
     // programmatic dependent launch: nothing global is read or written before
     // the previous kernel (an append, say) has completed
@@ -281,7 +286,9 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     }
     total *= p.Hkv;
     long long per = (total + ctas - 1) / ctas;
-    if (per < imin(kMinChunks, n_max)) per = imin(kMinChunks, n_max);
+    // at least one chunk per warp, unless every unit is shorter than that: then
+    // the units are spread over more CTAs
+    if (per < imin(CW, n_max)) per = imin(CW, n_max);
     const long long f0 = per * cta;
     if (f0 >= total) return;
     const long long f1 = f0 + per < total ? f0 + per : total;
@@ -325,75 +332,100 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     Walk w(p, ms->start_b, ms->start_len, ms->start_off, f0, f1 - f0);
     int f = 0;                                         // chunk number within the CTA's range
 
-    if (warp >= kCW) {
-        // ------------------------------------------------ producer warps
-        const bool is_k = warp == kCW;
-        const CUtensorMap *tm = is_k ? &tk : &tv;
-        uint64_t *full = is_k ? ms->full_k : ms->full_v;
-        uint64_t *empty = is_k ? ms->empty_k : ms->empty_v;
-        uint8_t *ring = smem + (is_k ? C::OFF_K : C::OFF_V);
-        if (lane == 0) ptx::prefetch_tmap(tm);
-        const uint64_t pol = ptx::l2_policy_evict_first();
-        const int nb = kChunk / p.BR;                  // boxes per chunk: 1, 2 or 4
-        const unsigned bits = (1u << nb) - 1u;
-        const int box_bytes = p.BR * D * 2;
-        const int group = 32 / nb;                     // chunks whose boxes the lanes look up at once
-        bool ok = true;
-        do {
-            const int32_t *row = p.table + (long long)w.b * p.table_stride;
-            for (int g0 = 0; ok && g0 < w.cnt; g0 += group) {
-                const int gi = g0 + lane / nb;
-                int page = 0, prow = 0;
-                bool need = false;
-                if (gi < w.cnt) {
-                    const int pos = chunk_of(w.plan, w.v0 + gi) * kChunk + (lane % nb) * p.BR;
-                    // a box without a visible position is not read: its page
-                    // may not exist (past the end) or may be free again
-                    need = pos < w.plan.len && (pos + p.BR > w.plan.lo || pos < w.plan.s_end);
-                    if (need) {
-                        page = row[pos / p.S];
-                        prow = pos % p.S;
-                    }
-                }
-                const bool bad = need && (page < 0 || page >= p.num_pages);
-                if (bad) {
-                    raise_device_error(p.err, kDevCheck);
-                    page = p.num_pages;                // outside the map: the copy fills zeros
-                }
-                const unsigned needs = __ballot_sync(0xffffffffu, need);
-                const unsigned bads = __ballot_sync(0xffffffffu, bad);
-                const int in_group = imin(group, w.cnt - g0);
-                for (int i = 0; i < in_group; ++i, ++f) {
-                    const int s = f % C::SLOTS;
-                    if (f >= C::SLOTS &&
-                        !__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(
-                                                     &empty[s], ((f / C::SLOTS) - 1) & 1, p.err, abort))) {
-                        ok = false;
-                        break;
-                    }
-                    const unsigned mine = (needs >> (i * nb)) & bits;
-                    if (lane == 0) {
-                        if (is_k) ms->bad[s] = ((bads >> (i * nb)) & bits) != 0;
-                        ptx::mbar_arrive_expect_tx(&full[s], __popc(mine) * box_bytes);
-                    }
-                    __syncwarp();
-                    const int pg = __shfl_sync(0xffffffffu, page, i * nb + lane % nb);
-                    const int pr = __shfl_sync(0xffffffffu, prow, i * nb + lane % nb);
-                    if (lane < nb && ((mine >> lane) & 1u))
-                        ptx::tma_load_5d(ring + s * C::TILE + lane * box_bytes, tm, 0, pr, 0, w.kvh, pg,
-                                         &full[s], pol);
-                }
+    // ---- loads: a walk of its own that runs NS chunks (and a group of page
+    //      lookups) ahead of the computation
+    const int nb = kChunk / p.BR;                      // boxes per chunk: 1, 2 or 4
+    const unsigned bits = (1u << nb) - 1u;
+    const int box_bytes = p.BR * D * 2;
+    const int group = 32 / nb;
+    const uint64_t pol = ptx::l2_policy_evict_first();
+    uint64_t *full_k = ms->full_k + warp * NS, *full_v = ms->full_v + warp * NS;
+    uint8_t *ring_k = smem + C::OFF_K + warp * NS * C::TILE, *ring_v = smem + C::OFF_V + warp * NS * C::TILE;
+    Walk lw = w;
+    int l_next = (warp + CW - f % CW) % CW;            // this warp's next chunk within lw's segment
+    int l_f = 0;                                       // chunk number of lw's segment start
+    bool l_more = true;
+    auto lookup = [&]() -> Group {
+        Group g;
+        g.page = g.row = 0;
+        g.needs = g.bads = 0;
+        g.kvh = g.cnt = 0;
+        while (l_more && l_next >= lw.cnt) {           // no (more) chunk of this warp in the segment
+            l_f += lw.cnt;
+            l_more = lw.next();
+            l_next = (warp + CW - l_f % CW) % CW;
+        }
+        if (!l_more) return g;
+        g.kvh = lw.kvh;
+        g.cnt = imin(group, (lw.cnt - l_next + CW - 1) / CW);
+        bool need = false;
+        if (lane / nb < g.cnt) {
+            const int v = lw.v0 + l_next + (lane / nb) * CW;
+            const int pos = chunk_of(lw.plan, v) * kChunk + (lane % nb) * p.BR;
+            // a box without a visible position is not read: its page may not
+            // exist (past the end) or may be free again
+            need = pos < lw.plan.len && (pos + p.BR > lw.plan.lo || pos < lw.plan.s_end);
+            if (need) {
+                g.page = p.table[(long long)lw.b * p.table_stride + pos / p.S];
+                g.row = pos % p.S;
             }
-        } while (ok && w.next());
-        // after a timeout: let the copies already issued land (bounded) before
-        // the CTA's shared memory is released
-        if (!ok && lane == 0)
-            for (int i = imax(0, f - C::SLOTS); i < f; ++i)
-                ptx::mbar_wait(&full[i % C::SLOTS], (i / C::SLOTS) & 1, nullptr);
-        return;
-    }
+        }
+        g.needs = __ballot_sync(0xffffffffu, need);
+        l_next += g.cnt * CW;
+        return g;
+    };
+    // checks the entries (when they have arrived) before the group's first copy
+    auto check = [&](Group &g) {
+        const bool bad = ((g.needs >> lane) & 1u) && (g.page < 0 || g.page >= p.num_pages);
+        if (bad) {
+            raise_device_error(p.err, kDevCheck);
+            g.page = p.num_pages;                      // outside the map: the copy fills zeros
+        }
+        g.bads = __ballot_sync(0xffffffffu, bad);
+    };
+    Group cur = lookup(), nxt = lookup();
+    check(cur);
+    int gi = 0;                                        // chunk within cur
+    // this warp's chunks: K asked for, K and V asked for, computed
+    int k_out = 0, issued = 0, taken = 0;
+    unsigned bad_bits = 0;                             // bit i % 32: chunk i has a bad page
+    int pg = 0, pr = 0, kvh_v = 0;                     // the chunk whose K went out last
+    unsigned mine = 0;
+    auto issue_k = [&]() -> bool {                     // K of this warp's next chunk, if there is one
+        if (gi == cur.cnt) {
+            cur = nxt;
+            gi = 0;
+            if (cur.cnt == 0) return false;
+            check(cur);
+            nxt = lookup();
+        }
+        const int s = issued % NS;
+        mine = (cur.needs >> (gi * nb)) & bits;
+        const unsigned b = (cur.bads >> (gi * nb)) & bits;
+        bad_bits = (bad_bits & ~(1u << (issued & 31))) | (unsigned(b != 0) << (issued & 31));
+        pg = __shfl_sync(0xffffffffu, cur.page, gi * nb + lane % nb);
+        pr = __shfl_sync(0xffffffffu, cur.row, gi * nb + lane % nb);
+        kvh_v = cur.kvh;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&full_k[s], __popc(mine) * box_bytes);
+        __syncwarp();
+        if (lane < nb && ((mine >> lane) & 1u))
+            ptx::tma_load_5d(ring_k + s * C::TILE + lane * box_bytes, &tk, 0, pr, 0, kvh_v, pg, &full_k[s], pol);
+        ++k_out;
+        return true;
+    };
+    auto issue_v = [&]() {                             // V of the same chunk
+        const int s = issued % NS;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&full_v[s], __popc(mine) * box_bytes);
+        __syncwarp();
+        if (lane < nb && ((mine >> lane) & 1u))
+            ptx::tma_load_5d(ring_v + s * C::TILE + lane * box_bytes, &tv, 0, pr, 0, kvh_v, pg, &full_v[s], pol);
+        ++issued;
+        ++gi;
+    };
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+        if (issue_k()) issue_v();
 
-    // ---------------------------------------------------- consumer warps
     float *mg = reinterpret_cast<float *>(smem + C::OFF_M);
     float *mml = reinterpret_cast<float *>(smem + C::OFF_ML);
     const int quad = lane >> 2, pair = lane & 3;
@@ -410,7 +442,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         v_row[t] = (rv / p.BR) * (C::PANELS * psz) + (rv % p.BR) * 128 +
                    ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
     }
-    const uint32_t k_base = ptx::smem_addr(smem + C::OFF_K), v_base = ptx::smem_addr(smem + C::OFF_V);
+    const uint32_t k_base = ptx::smem_addr(ring_k), v_base = ptx::smem_addr(ring_v);
 
     // after a timeout a warp computes nothing more but still walks the
     // segments: the other warps meet it at their barriers, and every unit's
@@ -447,17 +479,18 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
 
         const int f_end = f + w.cnt;
         // this warp's chunks: the range's chunk number modulo the warps
-        for (int fc = f + ((warp - f) & (kCW - 1)); fc < f_end && !dead; fc += kCW) {
-            const int s = fc % C::SLOTS;
-            const uint32_t parity = (fc / C::SLOTS) & 1;
+        for (int fc = f + (warp + CW - f % CW) % CW; fc < f_end && !dead; fc += CW) {
+            const int s = taken % NS;
+            const uint32_t parity = (taken / NS) & 1;
             const int base = chunk_of(w.plan, w.v0 + (fc - f)) * kChunk;
-            if (!__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&ms->full_k[s], parity, p.err, abort))) {
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&full_k[s], parity, p.err, abort))) {
                 bad = dead = 1;
                 break;
             }
-            bad |= ms->bad[s];
+            bad |= (bad_bits >> (taken & 31)) & 1u;
 
             // ---- S^T = K q^T
+            //      a panel's fragments first, then its MMAs
             float sc[2][NT][4];
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -465,17 +498,25 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
                 for (int nt = 0; nt < NT; ++nt)
                     sc[t][nt][0] = sc[t][nt][1] = sc[t][nt][2] = sc[t][nt][3] = 0.f;
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
+            for (int pn = 0; pn < C::PANELS; ++pn) {
+                uint32_t a[4][2][4];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    uint32_t a[4];
-                    ldsm4(a, k_base + s * C::TILE + (kk >> 2) * psz + (k_row[t] ^ ((kk & 3) << 5)));
+                for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma16816<F16>(sc[t][nt], a, qf[nt][kk][0], qf[nt][kk][1]);
-                }
+                    for (int t = 0; t < 2; ++t)
+                        ldsm4(a[kk][t], k_base + s * C::TILE + pn * psz + (k_row[t] ^ (kk << 5)));
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816<F16>(sc[t][nt], a[kk][t], qf[nt][pn * 4 + kk][0],
+                                          qf[nt][pn * 4 + kk][1]);
+            }
+            // every lane's fragments have been read: the slot takes the next K
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&ms->empty_k[s]);
+            const bool more_loads = issue_k();
 
             // ---- visibility of the chunk's 32 positions
             unsigned vis;
@@ -532,7 +573,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
                     }
             }
 
-            if (!__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&ms->full_v[s], parity, p.err, abort))) {
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&full_v[s], parity, p.err, abort))) {
                 bad = dead = 1;
                 break;
             }
@@ -548,24 +589,34 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
                     keep1 = (v & 0x100u ? 0x0000ffffu : 0u) | (v & 0x200u ? 0xffff0000u : 0u);
                 }
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    uint32_t a[4];
-                    ldsm4t(a, v_base + s * C::TILE + (i >> 2) * psz + (v_row[t] ^ ((i & 3) << 5)));
-                    if (part) {
-                        a[0] &= keep0;
-                        a[1] &= keep0;
-                        a[2] &= keep1;
-                        a[3] &= keep1;
-                    }
+                for (int pn = 0; pn < C::PANELS; ++pn) {
+                    uint32_t a[4][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        ldsm4t(a[i], v_base + s * C::TILE + pn * psz + (v_row[t] ^ (i << 5)));
+                    if (part)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            a[i][0] &= keep0;
+                            a[i][1] &= keep0;
+                            a[i][2] &= keep1;
+                            a[i][3] &= keep1;
+                        }
+                    // the two terms of P in separate rounds: no MMA waits for the one before
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        mma16816<F16>(acc[nt][i], a, ph[t][nt][0], ph[t][nt][1]);
-                        mma16816<F16>(acc[nt][i], a, pl[t][nt][0], pl[t][nt][1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma16816<F16>(acc[nt][pn * 4 + i], a[i], ph[t][nt][0], ph[t][nt][1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma16816<F16>(acc[nt][pn * 4 + i], a[i], pl[t][nt][0], pl[t][nt][1]);
                     }
                 }
             }
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&ms->empty_v[s]);
+            if (more_loads) issue_v();
+            ++taken;
         }
         f = f_end;
 
@@ -576,7 +627,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         if (more) load_q();
         T *const o_unit = static_cast<T *>(p.o) + seg_b * p.o_sb + (long long)seg_kvh * p.G * p.o_sh;
 
-        // ---- the four warps' (max, sum, O) -> one per head
+        // ---- the warps' (max, sum, O) -> one per head
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -597,8 +648,9 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
                 }
             }
         if (lane == 0) ms->warp_bad[warp] = bad;
-        ptx::named_barrier_sync(1, kCW * 32);
-        bad = ms->warp_bad[0] | ms->warp_bad[1] | ms->warp_bad[2] | ms->warp_bad[3];
+        ptx::named_barrier_sync(1, kNT);
+        #pragma unroll
+        for (int i = 0; i < CW; ++i) bad |= ms->warp_bad[i];
 
         const bool whole = seg_v0 == 0 && seg_cnt == seg_n;
         // a range holds at most one segment that starts inside its unit (slot 0)
@@ -606,15 +658,15 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         const int slot = 2 * cta + (seg_v0 == 0 ? 1 : 0);
         float *po = p.part_o + (size_t)slot * C::HP * D;
         float *pml = p.part_ml + (size_t)slot * C::HP * 2;
-        for (int e = threadIdx.x; e < p.G * (D / 4); e += kCW * 32) {
+        for (int e = threadIdx.x; e < p.G * (D / 4); e += kNT) {
             const int h = e / (D / 4), d = (e % (D / 4)) * 4;
             float M = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < kCW; ++i) M = fmaxf(M, mml[(i * C::HP + h) * 2]);
+            for (int i = 0; i < CW; ++i) M = fmaxf(M, mml[(i * C::HP + h) * 2]);
             float L = 0.f;
             float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < kCW; ++i) {
+            for (int i = 0; i < CW; ++i) {
                 const float mi = mml[(i * C::HP + h) * 2], li = mml[(i * C::HP + h) * 2 + 1];
                 // a warp that saw nothing, or only scores of -inf, adds nothing
                 // (its sum is zero, or NaN if one of its scores was)
@@ -644,11 +696,11 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
             const int c0 = int(u0 / per), c1 = int((u0 + seg_n - 1) / per);
             // the barrier puts the CTA's partial before thread 0's release; its
             // acquire and the second barrier put the other CTAs' before the reads
-            ptx::named_barrier_sync(1, kCW * 32);
+            ptx::named_barrier_sync(1, kNT);
             if (threadIdx.x == 0) ms->last = ticket_add(&p.tickets[unit]) == unsigned(c1 - c0);
-            ptx::named_barrier_sync(1, kCW * 32);
+            ptx::named_barrier_sync(1, kNT);
             if (ms->last) {
-                for (int e = threadIdx.x; e < p.G * (D / 4); e += kCW * 32) {
+                for (int e = threadIdx.x; e < p.G * (D / 4); e += kNT) {
                     const int h = e / (D / 4), d = (e % (D / 4)) * 4;
                     float M = -INFINITY, L = 0.f;
                     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -701,7 +753,13 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
                 if (threadIdx.x == 0) p.tickets[unit] = 0u;   // ready for the next call
             }
         }
-        ptx::named_barrier_sync(1, kCW * 32);          // the merge rows may be written again
+        ptx::named_barrier_sync(1, kNT);          // the merge rows may be written again
+    }
+    // after a timeout: let the copies this warp asked for land (bounded) before
+    // the CTA's shared memory is released
+    if (dead && lane == 0) {
+        for (int i = taken; i < k_out; ++i) ptx::mbar_wait(&full_k[i % NS], (i / NS) & 1, nullptr);
+        for (int i = taken; i < issued; ++i) ptx::mbar_wait(&full_v[i % NS], (i / NS) & 1, nullptr);
     }
 }
 
@@ -732,7 +790,7 @@ attn_status_t launch_paged(const Ctx &c, const CUtensorMap &tk, const CUtensorMa
         return ATTN_ERR_RESOURCE;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(imin(kCtasPerSm * c.sm_count, kMaxCtas));
-    cfg.blockDim = dim3(kNT);
+    cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = c.stream;
     cudaLaunchAttribute attr;
