@@ -361,7 +361,7 @@ ATTN_API attn_status_t attn_kv_append_paged(void *k_pages, void *v_pages, const 
  *   no page of the pool, sets ATTN_ERR_DEVICE_CHECK and leaves that sequence's
  *   output unwritten; other sequences' are not affected.
  *   Requires Hq % Hkv == 0, Hq / Hkv <= 16, D in {64, 128}, dtype ATTN_BF16 or
- *   ATTN_F16 (q, pages and o alike).  For one set of inputs the result does not
+ *   ATTN_F16 (q, pages and o alike), B * Hkv * (max_pages * page_size + 32) < 2^36.  For one set of inputs the result does not
  *   depend on timing.
  *   workspace: DEVICE scratch of attn_decode_gqa_paged_workspace_bytes(...)
  *   bytes, 256-byte aligned, ZERO-FILLED before its first use.  Every call that

@@ -102,6 +102,10 @@ CASES = [
     ("f16", [900, 20], 2, 1, 128, 16, 100000, 4, "head"),          # window beyond the length
     ("bf16", [900, 20], 2, 1, 64, 16, 16, 5000, "head"),           # sinks beyond it
     ("bf16", [3, 9, 30] * 70, 2, 2, 64, 16, 0, 0, "head"),         # more rows than threads
+    ("bf16", [250, 7, 0, 100] * 25, 16, 8, 128, 16, 0, 0, "head"), # units dealt out warp by warp
+    ("f16", [250, 1, 0, 33, 64, 0] * 50, 12, 4, 64, 8, 0, 0, "token"),
+    ("bf16", [900, 40, 0, 129] * 30, 27, 3, 128, 48, 100, 20, "head"),
+    ("bf16", [1200, 300, 700] * 12, 8, 4, 64, 16, 0, 0, "head"),   # ranges that end inside units
 ]
 
 
@@ -181,6 +185,16 @@ def test_decode_paged_bad_pages_and_lengths_are_reported_per_sequence(ta):
         assert ta.device_status() == 6
         assert (o[:3] == 9).all()
         check("bf16", q, ks, vs, lens, o, 0, 0, only=[3])
+        # units dealt out warp by warp
+        lens2 = [40, 100, 250, 16] * 40
+        q, kp, vp, table, sl, ks, vs = build_case("bf16", lens2, 8, 4, 128, 16, 0, 0, "head", 8)
+        table[1, 3] = entry
+        sl[2] = -1
+        o = torch.full_like(q, 9.0)
+        ta.decode_gqa_paged(q, kp, vp, table, sl, o=o)
+        assert ta.device_status() == 6
+        assert (o[1:3] == 9).all()
+        check("bf16", q, ks, vs, lens2, o, 0, 0, only=[0] + list(range(3, 160, 9)))
         # the workspace serves the next call
         q, kp, vp, table, sl, ks, vs = build_case("bf16", lens, 4, 2, 128, 16, 0, 0, "head", 7)
         o = ta.decode_gqa_paged(q, kp, vp, table, sl, workspace=ws)

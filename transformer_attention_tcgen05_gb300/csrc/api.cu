@@ -522,7 +522,7 @@ attn_status_t attn_decode_gqa_paged(const void *q, const void *k_pages, const vo
     if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !valid_d(D) || !valid_dtype(dtype) || sinks < 0)
         return ATTN_ERR_INVALID_ARG;
     if (!half_dtype(dtype) || D == 32 || Hq / Hkv > 16 || Hkv > 65535 ||
-        (long long)B * Hkv > 0x7fffffffll)
+        double(B) * Hkv * (double(max_pages) * page_size + 32.0) >= 68719476736.0)
         return ATTN_ERR_UNSUPPORTED;
     if (o == q || o == k_pages || o == v_pages) return ATTN_ERR_INVALID_ARG;
     PagedDecode a{};

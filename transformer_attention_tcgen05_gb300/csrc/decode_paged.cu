@@ -19,6 +19,10 @@
 //  * A CTA whose range cuts a unit writes a partial (max, sum, O) per head to
 //    the workspace; the last CTA of the unit to arrive (ticket) joins the
 //    partials in CTA order, so the result does not depend on who is last.
+//    (Drawing the tickets of a range's cut units only at its end, so that the
+//    next unit need not wait, measured 1 us slower: 8 x 4096 tokens 28.1 us.)
+//  * Many short units (more units than CTAs, none longer than 8 chunks) are
+//    dealt out whole, warp by warp: no joining, no barrier.
 //  * Every warp streams chunks of its own (chunk f of the range goes to warp
 //    f % CW) into shared memory of its own with TMA: a box of up to 32 rows x D
 //    channels per copy, the page and the KV head being coordinates of one 5D
@@ -74,6 +78,10 @@ struct PgCfg {
     static_assert(kCtasPerSm * (SMEM + 1024) <= 228 * 1024, "the CTAs of an SM must fit its shared memory");
 };
 
+// The chunk counts of a call fit 31 bits (checked by the entry), so the work
+// list is kept in ints.  Every launch starts with a cold instruction cache: the
+// code is kept short (one copy of each step, no 64-bit or run-time division in
+// the loop), which is worth 2 us of a 10 us call.
 struct PgParams {
     const void *q;
     void *o;
@@ -82,7 +90,8 @@ struct PgParams {
     long long table_stride;
     const int32_t *seq_len;
     int B, Hkv, G;
-    int S, BR;                             // page size, rows per TMA box
+    int S, nb, br_log;                     // page size, TMA boxes per chunk and log2 of their rows
+    unsigned s_mul, s_sh;                  // division by S (div_s)
     int max_pages, num_pages;
     int window, sinks;
     float c_log2;
@@ -92,14 +101,16 @@ struct PgParams {
     unsigned *err;
 };
 
-constexpr int kMaxWarps = 8;
+constexpr int kMaxWarps = 4;
+constexpr int kWarpUnit = 8;      // longest unit (chunks) that one warp takes alone
 
 struct Misc {
     uint64_t full_k[kMaxWarps * 2], full_v[kMaxWarps * 2];   // [warp][slot]
-    long long warp_sum[kMaxWarps];
-    int warp_max[kMaxWarps];
-    long long start_off;
-    int start_b, start_len;
+    int warp_sum[kMaxWarps];
+    int warp_max[kMaxWarps], warp_units[kMaxWarps];
+    // where the CTA's range, or each warp's (and the one behind), starts
+    int start_flat[kMaxWarps + 1];
+    int start_b[kMaxWarps + 1], start_len[kMaxWarps + 1], start_kvh[kMaxWarps + 1], start_v[kMaxWarps + 1];
     int abort;
     unsigned last;
     int warp_bad[kMaxWarps];
@@ -127,6 +138,12 @@ __device__ __forceinline__ Plan make_plan(const PgParams &p, int len) {
     return r;
 }
 
+// n / S for 0 <= n < 2^31 by a multiplication (S >= 2)
+__device__ __forceinline__ int div_s(const PgParams &p, int n) {
+    const unsigned t = __umulhi(p.s_mul, unsigned(n));
+    return int((t + ((unsigned(n) - t) >> 1)) >> p.s_sh);
+}
+
 __device__ __forceinline__ int chunk_of(const Plan &r, int v) {
     return v < r.n1 ? v : v - r.n1 + r.c2;
 }
@@ -136,33 +153,33 @@ struct Walk {
     const PgParams &p;
     Plan plan;
     int b, kvh, v0, cnt;
-    long long left;                        // chunks of the range from this segment on
-    long long flat;                        // flat index of the segment's first chunk
+    int left;                              // chunks of the range from this segment on
+    int flat;                              // flat index of the segment's first chunk
 
     int ahead;                             // seq_len[b + 1], loaded before it is needed
 
-    __device__ Walk(const PgParams &pp, int b0, int len0, long long off, long long f0, long long count)
-        : p(pp), b(b0), left(count), flat(f0) {
+    __device__ Walk(const PgParams &pp, int b0, int len0, int kvh0, int v, int f0, int count)
+        : p(pp), b(b0), kvh(kvh0), v0(v), left(count), flat(f0) {
         plan = make_plan(p, len0);
         ahead = b + 1 < p.B ? p.seq_len[b + 1] : 0;
-        kvh = int(off / plan.n);
-        v0 = int(off % plan.n);
-        cnt = int(left < plan.n - v0 ? left : plan.n - v0);
+        if (kvh == p.Hkv) next_sequence();
+        cnt = imin(left, plan.n - v0);
+    }
+    __device__ void next_sequence() {       // the range ends inside the list: b stays below B
+        kvh = 0;
+        do {
+            plan = make_plan(p, ahead);
+            ++b;
+            ahead = b + 1 < p.B ? p.seq_len[b + 1] : 0;
+        } while (plan.n == 0);
     }
     __device__ bool next() {
         left -= cnt;
         flat += cnt;
         if (left <= 0) return false;
         v0 = 0;
-        if (++kvh == p.Hkv) {
-            kvh = 0;
-            do {                            // the range ends inside the list: b stays below B
-                plan = make_plan(p, ahead);
-                ++b;
-                ahead = b + 1 < p.B ? p.seq_len[b + 1] : 0;
-            } while (plan.n == 0);
-        }
-        cnt = int(left < plan.n ? left : plan.n);
+        if (++kvh == p.Hkv) next_sequence();
+        cnt = imin(left, plan.n);
         return true;
     }
 };
@@ -248,101 +265,128 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     //      length 0 writes zeros, a length outside the table is reported and
     //      its output left as it was.
     const bool one_tile = p.B <= kNT;                  // a thread per sequence: read once
-    long long inc = 0;
-    int n_mine = 0, len_mine = 0, n_max = 0;
+    int inc = 0, n_mine = 0, len_mine = 0, n_max = 0, units = 0;
+#pragma unroll 1
     for (int b = threadIdx.x; b < p.B; b += kNT) {
         len_mine = p.seq_len[b];
         n_mine = make_plan(p, len_mine).n;
         inc += n_mine;
         n_max = imax(n_max, n_mine);
+        units += n_mine > 0;
         if (n_mine == 0 && b % ctas == cta) {
-            if (len_mine != 0) {
-                raise_device_error(p.err, kDevCheck);
-            } else {
-                for (int h = 0; h < p.Hkv * p.G; ++h) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + b * p.o_sb + h * p.o_sh);
-                    for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-                }
-            }
+            if (len_mine != 0) raise_device_error(p.err, kDevCheck);
+#pragma unroll 1
+            for (int i = 0; i < p.Hkv * p.G * (D / 8) && len_mine == 0; ++i)
+                *reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + b * p.o_sb + (i / (D / 8)) * p.o_sh +
+                                           (i % (D / 8)) * 8) = make_uint4(0u, 0u, 0u, 0u);
         }
     }
-#pragma unroll
+#pragma unroll 1
     for (int off = 1; off < 32; off <<= 1) {
-        const long long up = __shfl_up_sync(0xffffffffu, inc, off);
+        const int up = __shfl_up_sync(0xffffffffu, inc, off);
         if (lane >= off) inc += up;
         n_max = imax(n_max, __shfl_xor_sync(0xffffffffu, n_max, off));
+        units += __shfl_xor_sync(0xffffffffu, units, off);
     }
     if (lane == 31) {
         ms->warp_sum[warp] = inc;
         ms->warp_max[warp] = n_max;
+        ms->warp_units[warp] = units;
     }
     __syncthreads();
-    long long total = 0, before = inc - n_mine;        // before: chunks of the sequences ahead (one tile)
+    int total = 0, before = inc - n_mine;              // before: chunks of the sequences ahead (one tile)
+    units = 0;
 #pragma unroll
-    for (int w = 0; w < kNT / 32; ++w) {
+    for (int w = 0; w < CW; ++w) {
         if (w < warp) before += ms->warp_sum[w];
         total += ms->warp_sum[w];
         n_max = imax(n_max, ms->warp_max[w]);
+        units += ms->warp_units[w];
     }
     total *= p.Hkv;
-    long long per = (total + ctas - 1) / ctas;
+    // team: the warps that share a range (all of the CTA's, or each its own)
+    const bool alone = n_max <= kWarpUnit && (long long)units * p.Hkv > ctas;
+    const int team = alone ? 1 : CW, rank = alone ? 0 : warp;
+    const int teams = alone ? ctas * CW : ctas;
+    int per = int((unsigned(total) + teams - 1) / unsigned(teams));
     // at least one chunk per warp, unless every unit is shorter than that: then
     // the units are spread over more CTAs
-    if (per < imin(CW, n_max)) per = imin(CW, n_max);
-    const long long f0 = per * cta;
-    if (f0 >= total) return;
-    const long long f1 = f0 + per < total ? f0 + per : total;
-    if (one_tile) {
-        if (n_mine > 0 && f0 >= before * p.Hkv && f0 < (before + n_mine) * p.Hkv) {
-            ms->start_b = threadIdx.x;
-            ms->start_len = len_mine;
-            ms->start_off = f0 - before * p.Hkv;
+    if (!alone) per = imax(per, imin(CW, n_max));
+    const long long f0l = (long long)per * (alone ? cta * CW : cta);
+    if (f0l >= total) return;
+    const int f0 = int(f0l);
+    // boundary i of this CTA: f0, or the first unit that starts at or behind
+    // f0 + i per (each warp's range is a run of whole units)
+    const int marks = alone ? CW + 1 : 1;
+    auto mark = [&](int b, int len, int n, int before) {
+        const int lo = before * p.Hkv, hi = lo + n * p.Hkv;
+#pragma unroll 1
+        for (int i = 0; i < marks; ++i) {
+            const unsigned x = unsigned(f0) + unsigned(i * per);
+            if (x < unsigned(lo) || x >= unsigned(hi)) continue;
+            int kvh = int((x - lo) / unsigned(n)), v = int(x - lo) - kvh * n;
+            if (alone && v > 0) {
+                ++kvh;                                 // may be Hkv: the next sequence's first
+                v = 0;
+            }
+            ms->start_b[i] = b;
+            ms->start_len[i] = len;
+            ms->start_kvh[i] = kvh;
+            ms->start_v[i] = v;
+            ms->start_flat[i] = lo + kvh * n + v;
         }
-        __syncthreads();
-    } else {
-        long long carry = 0;                           // chunks of the sequences before this tile
-        for (int b0 = 0; b0 < p.B; b0 += kNT) {
-            __syncthreads();
-            const int b = b0 + threadIdx.x;
-            const int len = b < p.B ? p.seq_len[b] : 0;
-            const int n = make_plan(p, len).n;
-            inc = n;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const long long up = __shfl_up_sync(0xffffffffu, inc, off);
-                if (lane >= off) inc += up;
-            }
-            if (lane == 31) ms->warp_sum[warp] = inc;
-            __syncthreads();
-            before = carry + inc - n;
-            for (int w = 0; w < kNT / 32; ++w) {
-                if (w < warp) before += ms->warp_sum[w];
-                carry += ms->warp_sum[w];
-            }
-            if (n > 0 && f0 >= before * p.Hkv && f0 < (before + n) * p.Hkv) {
-                ms->start_b = b;
-                ms->start_len = len;
-                ms->start_off = f0 - before * p.Hkv;
-            }
-            if (carry * p.Hkv > f0) break;
-        }
-        __syncthreads();
+    };
+    if (threadIdx.x < marks && f0l + (long long)threadIdx.x * per >= total) ms->start_flat[threadIdx.x] = total;
+    int carry = 0, b0 = 0;                             // chunks of the sequences before this tile
+    if (!one_tile) {                                   // a long batch is read again, tile by tile
+        b0 = -kNT;
+        n_mine = 0;
     }
+#pragma unroll 1
+    for (;;) {
+        mark(b0 + threadIdx.x, len_mine, n_mine, before);
+        b0 += kNT;
+        if (b0 >= p.B) break;
+        __syncthreads();
+        const int b = b0 + threadIdx.x;
+        len_mine = b < p.B ? p.seq_len[b] : 0;
+        n_mine = make_plan(p, len_mine).n;
+        inc = n_mine;
+#pragma unroll 1
+        for (int off = 1; off < 32; off <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += up;
+        }
+        if (lane == 31) ms->warp_sum[warp] = inc;
+        __syncthreads();
+        before = carry + inc - n_mine;
+#pragma unroll
+        for (int w = 0; w < CW; ++w) {
+            if (w < warp) before += ms->warp_sum[w];
+            carry += ms->warp_sum[w];
+        }
+    }
+    __syncthreads();
+    const int at = alone ? warp : 0;
+    const int start = ms->start_flat[at];
+    const int count = alone ? ms->start_flat[warp + 1] - start : imin(per, total - f0);
+    if (count <= 0) return;                            // alone: no unit starts in this warp's share
 
-    Walk w(p, ms->start_b, ms->start_len, ms->start_off, f0, f1 - f0);
-    int f = 0;                                         // chunk number within the CTA's range
+    Walk w(p, ms->start_b[at], ms->start_len[at], ms->start_kvh[at], ms->start_v[at], start, count);
+    int f = 0;                                         // chunk number within the range
 
     // ---- loads: a walk of its own that runs NS chunks (and a group of page
     //      lookups) ahead of the computation
-    const int nb = kChunk / p.BR;                      // boxes per chunk: 1, 2 or 4
+    const int nb = p.nb, BR = 1 << p.br_log;           // boxes per chunk (1, 2 or 4), their rows
     const unsigned bits = (1u << nb) - 1u;
-    const int box_bytes = p.BR * D * 2;
-    const int group = 32 / nb;
+    const int box_bytes = BR * D * 2;
+    const int group = BR;                              // chunks whose boxes the lanes look up: 32 / nb
+    const int sub = lane >> (5 - p.br_log), box = lane & (nb - 1);
     const uint64_t pol = ptx::l2_policy_evict_first();
     uint64_t *full_k = ms->full_k + warp * NS, *full_v = ms->full_v + warp * NS;
     uint8_t *ring_k = smem + C::OFF_K + warp * NS * C::TILE, *ring_v = smem + C::OFF_V + warp * NS * C::TILE;
     Walk lw = w;
-    int l_next = (warp + CW - f % CW) % CW;            // this warp's next chunk within lw's segment
+    int l_next = rank;                                 // this warp's next chunk within lw's segment
     int l_f = 0;                                       // chunk number of lw's segment start
     bool l_more = true;
     auto lookup = [&]() -> Group {
@@ -353,25 +397,26 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         while (l_more && l_next >= lw.cnt) {           // no (more) chunk of this warp in the segment
             l_f += lw.cnt;
             l_more = lw.next();
-            l_next = (warp + CW - l_f % CW) % CW;
+            l_next = (rank - l_f) & (team - 1);
         }
         if (!l_more) return g;
         g.kvh = lw.kvh;
-        g.cnt = imin(group, (lw.cnt - l_next + CW - 1) / CW);
+        g.cnt = imin(group, (lw.cnt - l_next + team - 1) >> (alone ? 0 : 2));
         bool need = false;
-        if (lane / nb < g.cnt) {
-            const int v = lw.v0 + l_next + (lane / nb) * CW;
-            const int pos = chunk_of(lw.plan, v) * kChunk + (lane % nb) * p.BR;
+        if (sub < g.cnt) {
+            const int v = lw.v0 + l_next + sub * team;
+            const int pos = chunk_of(lw.plan, v) * kChunk + box * BR;
             // a box without a visible position is not read: its page may not
             // exist (past the end) or may be free again
-            need = pos < lw.plan.len && (pos + p.BR > lw.plan.lo || pos < lw.plan.s_end);
+            need = pos < lw.plan.len && (pos + BR > lw.plan.lo || pos < lw.plan.s_end);
             if (need) {
-                g.page = p.table[(long long)lw.b * p.table_stride + pos / p.S];
-                g.row = pos % p.S;
+                const int e = div_s(p, pos);
+                g.page = p.table[(long long)lw.b * p.table_stride + e];
+                g.row = pos - e * p.S;
             }
         }
         g.needs = __ballot_sync(0xffffffffu, need);
-        l_next += g.cnt * CW;
+        l_next += g.cnt * team;
         return g;
     };
     // checks the entries (when they have arrived) before the group's first copy
@@ -383,8 +428,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         }
         g.bads = __ballot_sync(0xffffffffu, bad);
     };
-    Group cur = lookup(), nxt = lookup();
-    check(cur);
+    Group cur{}, nxt{};
     int gi = 0;                                        // chunk within cur
     // this warp's chunks: K asked for, K and V asked for, computed
     int k_out = 0, issued = 0, taken = 0;
@@ -392,19 +436,20 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     int pg = 0, pr = 0, kvh_v = 0;                     // the chunk whose K went out last
     unsigned mine = 0;
     auto issue_k = [&]() -> bool {                     // K of this warp's next chunk, if there is one
-        if (gi == cur.cnt) {
+#pragma unroll 1
+        while (gi == cur.cnt && (nxt.cnt > 0 || l_more)) {
             cur = nxt;
             gi = 0;
-            if (cur.cnt == 0) return false;
-            check(cur);
             nxt = lookup();
+            check(cur);
         }
+        if (gi == cur.cnt) return false;
         const int s = issued % NS;
         mine = (cur.needs >> (gi * nb)) & bits;
         const unsigned b = (cur.bads >> (gi * nb)) & bits;
         bad_bits = (bad_bits & ~(1u << (issued & 31))) | (unsigned(b != 0) << (issued & 31));
-        pg = __shfl_sync(0xffffffffu, cur.page, gi * nb + lane % nb);
-        pr = __shfl_sync(0xffffffffu, cur.row, gi * nb + lane % nb);
+        pg = __shfl_sync(0xffffffffu, cur.page, gi * nb + box);
+        pr = __shfl_sync(0xffffffffu, cur.row, gi * nb + box);
         kvh_v = cur.kvh;
         if (lane == 0) ptx::mbar_arrive_expect_tx(&full_k[s], __popc(mine) * box_bytes);
         __syncwarp();
@@ -422,24 +467,20 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         ++issued;
         ++gi;
     };
-#pragma unroll
-    for (int i = 0; i < NS; ++i)
-        if (issue_k()) issue_v();
-
     float *mg = reinterpret_cast<float *>(smem + C::OFF_M);
     float *mml = reinterpret_cast<float *>(smem + C::OFF_ML);
     const int quad = lane >> 2, pair = lane & 3;
     // ldmatrix lane addresses (relative to a slot): rows and the swizzled
     // 16-byte column; a k-step moves bits 5-6 of the column, a panel adds psz
-    const int psz = p.BR * 128;
+    const int psz = BR * 128;
     uint32_t k_row[2], v_row[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const int rk = t * 16 + (lane & 15);
         const int rv = t * 16 + (lane & 7) + ((lane >> 4) & 1) * 8;
-        k_row[t] = (rk / p.BR) * (C::PANELS * psz) + (rk % p.BR) * 128 +
+        k_row[t] = (rk >> p.br_log) * (C::PANELS * psz) + (rk & (BR - 1)) * 128 +
                    ((((lane >> 4) & 1) ^ (lane & 7)) << 4);
-        v_row[t] = (rv / p.BR) * (C::PANELS * psz) + (rv % p.BR) * 128 +
+        v_row[t] = (rv >> p.br_log) * (C::PANELS * psz) + (rv & (BR - 1)) * 128 +
                    ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
     }
     const uint32_t k_base = ptx::smem_addr(ring_k), v_base = ptx::smem_addr(ring_v);
@@ -447,7 +488,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     // after a timeout a warp computes nothing more but still walks the
     // segments: the other warps meet it at their barriers, and every unit's
     // ticket is counted up and reset as usual
-    int dead = 0;
+    int dead = 0, warm = 0;
     // q of the unit's heads as MMA B operands (heads are columns); the next
     // segment's are requested before this one's results are merged
     uint32_t qf[NT][D / 16][2];
@@ -478,45 +519,54 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         int bad = dead;
 
         const int f_end = f + w.cnt;
-        // this warp's chunks: the range's chunk number modulo the warps
-        for (int fc = f + (warp + CW - f % CW) % CW; fc < f_end && !dead; fc += CW) {
+        // this warp's chunks: the range's chunk number modulo the team.  The
+        // first NS rounds of all only ask for chunks.
+        int fc = f + ((rank - f) & (team - 1));
+#pragma unroll 1
+        while ((warm < NS || fc < f_end) && !dead) {
             const int s = taken % NS;
             const uint32_t parity = (taken / NS) & 1;
-            const int base = chunk_of(w.plan, w.v0 + (fc - f)) * kChunk;
-            if (!__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&full_k[s], parity, p.err, abort))) {
-                bad = dead = 1;
-                break;
-            }
-            bad |= (bad_bits >> (taken & 31)) & 1u;
-
-            // ---- S^T = K q^T
-            //      a panel's fragments first, then its MMAs
+            const bool go = warm == NS;
             float sc[2][NT][4];
+            if (go) {
+                if (!__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&full_k[s], parity, p.err, abort))) {
+                    bad = dead = 1;
+                    break;
+                }
+                bad |= (bad_bits >> (taken & 31)) & 1u;
+                // ---- S^T = K q^T, a panel's fragments first, then its MMAs
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    sc[t][nt][0] = sc[t][nt][1] = sc[t][nt][2] = sc[t][nt][3] = 0.f;
+                    for (int nt = 0; nt < NT; ++nt)
+                        sc[t][nt][0] = sc[t][nt][1] = sc[t][nt][2] = sc[t][nt][3] = 0.f;
 #pragma unroll
-            for (int pn = 0; pn < C::PANELS; ++pn) {
-                uint32_t a[4][2][4];
+                for (int pn = 0; pn < C::PANELS; ++pn) {
+                    uint32_t a[4][2][4];
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
+                    for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        ldsm4(a[kk][t], k_base + s * C::TILE + pn * psz + (k_row[t] ^ (kk << 5)));
+                        for (int t = 0; t < 2; ++t)
+                            ldsm4(a[kk][t], k_base + s * C::TILE + pn * psz + (k_row[t] ^ (kk << 5)));
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
+                    for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
+                        for (int t = 0; t < 2; ++t)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma16816<F16>(sc[t][nt], a[kk][t], qf[nt][pn * 4 + kk][0],
-                                          qf[nt][pn * 4 + kk][1]);
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816<F16>(sc[t][nt], a[kk][t], qf[nt][pn * 4 + kk][0],
+                                              qf[nt][pn * 4 + kk][1]);
+                }
             }
             // every lane's fragments have been read: the slot takes the next K
             __syncwarp();
             const bool more_loads = issue_k();
+            if (!go) {
+                if (more_loads) issue_v();
+                ++warm;
+                continue;
+            }
+            const int base = chunk_of(w.plan, w.v0 + (fc - f)) * kChunk;
 
             // ---- visibility of the chunk's 32 positions
             unsigned vis;
@@ -579,29 +629,24 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
             }
             // ---- O^T += V^T P^T.  Rows that are not visible may hold anything
             //      (NaN times a zero weight is NaN): their values are cleared.
-            const bool part = vis != 0xffffffffu;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-                if (part) {
-                    const unsigned v = vis >> (t * 16 + 2 * pair);
-                    keep0 = (v & 1u ? 0x0000ffffu : 0u) | (v & 2u ? 0xffff0000u : 0u);
-                    keep1 = (v & 0x100u ? 0x0000ffffu : 0u) | (v & 0x200u ? 0xffff0000u : 0u);
-                }
+                const unsigned v = vis >> (t * 16 + 2 * pair);
+                const uint32_t keep0 = (v & 1u ? 0x0000ffffu : 0u) | (v & 2u ? 0xffff0000u : 0u);
+                const uint32_t keep1 = (v & 0x100u ? 0x0000ffffu : 0u) | (v & 0x200u ? 0xffff0000u : 0u);
 #pragma unroll
                 for (int pn = 0; pn < C::PANELS; ++pn) {
                     uint32_t a[4][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         ldsm4t(a[i], v_base + s * C::TILE + pn * psz + (v_row[t] ^ (i << 5)));
-                    if (part)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            a[i][0] &= keep0;
-                            a[i][1] &= keep0;
-                            a[i][2] &= keep1;
-                            a[i][3] &= keep1;
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        a[i][0] &= keep0;
+                        a[i][1] &= keep0;
+                        a[i][2] &= keep1;
+                        a[i][3] &= keep1;
+                    }
                     // the two terms of P in separate rounds: no MMA waits for the one before
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
@@ -617,12 +662,13 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
             __syncwarp();
             if (more_loads) issue_v();
             ++taken;
+            fc += team;
         }
         f = f_end;
 
         // this segment (the walk goes on to the next one)
         const int seg_b = w.b, seg_kvh = w.kvh, seg_v0 = w.v0, seg_cnt = w.cnt, seg_n = w.plan.n;
-        const long long u0 = w.flat - w.v0;            // flat index of the unit's first chunk
+        const int u0 = w.flat - w.v0;                  // flat index of the unit's first chunk
         more = w.next();
         if (more) load_q();
         T *const o_unit = static_cast<T *>(p.o) + seg_b * p.o_sb + (long long)seg_kvh * p.G * p.o_sh;
@@ -647,9 +693,24 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
                     row[i * 16 + 8 + quad] = acc[nt][i][j + 2];
                 }
             }
+        if (alone) {
+            // a whole unit in one warp's registers: through its own merge rows
+            // to 8-byte stores
+            __syncwarp();
+#pragma unroll 1
+            for (int e = lane; e < p.G * (D / 4) && !bad; e += 32) {
+                const int h = e / (D / 4), d = (e % (D / 4)) * 4;
+                const float inv = 1.f / mml[(warp * C::HP + h) * 2 + 1];
+                const float4 x = *reinterpret_cast<const float4 *>(mg + (warp * C::HP + h) * C::LDM + d);
+                *reinterpret_cast<uint2 *>(o_unit + h * p.o_sh + d) =
+                    make_uint2(H::pack(x.x * inv, x.y * inv), H::pack(x.z * inv, x.w * inv));
+            }
+            __syncwarp();
+            continue;
+        }
         if (lane == 0) ms->warp_bad[warp] = bad;
         ptx::named_barrier_sync(1, kNT);
-        #pragma unroll
+#pragma unroll
         for (int i = 0; i < CW; ++i) bad |= ms->warp_bad[i];
 
         const bool whole = seg_v0 == 0 && seg_cnt == seg_n;
@@ -658,6 +719,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         const int slot = 2 * cta + (seg_v0 == 0 ? 1 : 0);
         float *po = p.part_o + (size_t)slot * C::HP * D;
         float *pml = p.part_ml + (size_t)slot * C::HP * 2;
+#pragma unroll 1
         for (int e = threadIdx.x; e < p.G * (D / 4); e += kNT) {
             const int h = e / (D / 4), d = (e % (D / 4)) * 4;
             float M = -INFINITY;
@@ -693,19 +755,21 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         }
         if (!whole) {
             const int unit = seg_b * p.Hkv + seg_kvh;
-            const int c0 = int(u0 / per), c1 = int((u0 + seg_n - 1) / per);
+            const int c0 = int(unsigned(u0) / unsigned(per)), c1 = int(unsigned(u0 + seg_n - 1) / unsigned(per));
             // the barrier puts the CTA's partial before thread 0's release; its
             // acquire and the second barrier put the other CTAs' before the reads
             ptx::named_barrier_sync(1, kNT);
             if (threadIdx.x == 0) ms->last = ticket_add(&p.tickets[unit]) == unsigned(c1 - c0);
             ptx::named_barrier_sync(1, kNT);
             if (ms->last) {
+#pragma unroll 1
                 for (int e = threadIdx.x; e < p.G * (D / 4); e += kNT) {
                     const int h = e / (D / 4), d = (e % (D / 4)) * 4;
                     float M = -INFINITY, L = 0.f;
                     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
                     bool skip = false;
-                    constexpr int U = 4;               // partials in flight
+                    constexpr int U = 8;                   // partials in flight
+#pragma unroll 1
                     for (int c = c0; c <= c1; c += U) {
                         float2 ml[U];
                         float4 x[U];
@@ -745,15 +809,14 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
                     }
                     if (!skip) {
                         const float inv = 1.f / L;
-                        T *dst = o_unit + h * p.o_sh + d;
-                        *reinterpret_cast<uint2 *>(dst) =
+                        *reinterpret_cast<uint2 *>(o_unit + h * p.o_sh + d) =
                             make_uint2(H::pack(O.x * inv, O.y * inv), H::pack(O.z * inv, O.w * inv));
                     }
                 }
                 if (threadIdx.x == 0) p.tickets[unit] = 0u;   // ready for the next call
             }
         }
-        ptx::named_barrier_sync(1, kNT);          // the merge rows may be written again
+        ptx::named_barrier_sync(1, kNT);               // the merge rows may be written again
     }
     // after a timeout: let the copies this warp asked for land (bounded) before
     // the CTA's shared memory is released
@@ -819,10 +882,18 @@ size_t decode_paged_workspace_bytes(int B, int G, int Hkv, int D) {
 attn_status_t decode_paged(const Ctx &c, attn_dtype_t dt, const PagedDecode &a) {
     const bool f16 = dt == ATTN_F16;
     PgParams p{};
-    p.BR = a.S % 32 == 0 ? 32 : a.S % 16 == 0 ? 16 : 8;
+    const int BR = a.S % 32 == 0 ? 32 : a.S % 16 == 0 ? 16 : 8;
+    p.nb = kChunk / BR;
+    p.br_log = BR == 32 ? 5 : BR == 16 ? 4 : 3;
+    // n / S = (t + (n - t) / 2) >> s_sh with t = high word of s_mul n, for
+    // l = ceil(log2 S), s_mul = floor(2^32 (2^l - S) / S) + 1, s_sh = l - 1
+    int l = 0;
+    while ((1ll << l) < a.S) ++l;
+    p.s_mul = unsigned((((1ull << l) - a.S) << 32) / unsigned(a.S) + 1);
+    p.s_sh = l - 1;
     CUtensorMap tk, tv;
-    if (!page_tmap(&tk, a.k, a.P, a.Hkv, a.S, a.D, a.k_st, p.BR, f16) ||
-        !page_tmap(&tv, a.v, a.P, a.Hkv, a.S, a.D, a.v_st, p.BR, f16))
+    if (!page_tmap(&tk, a.k, a.P, a.Hkv, a.S, a.D, a.k_st, BR, f16) ||
+        !page_tmap(&tv, a.v, a.P, a.Hkv, a.S, a.D, a.v_st, BR, f16))
         return ATTN_ERR_UNSUPPORTED;
     p.q = a.q;
     p.o = a.o;
