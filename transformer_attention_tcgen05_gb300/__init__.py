@@ -2,8 +2,8 @@
 
 Every step of the attention path runs in the CUDA library; this module checks
 tensor arguments, allocates outputs with PyTorch (PyTorch provides device
-memory and streams, nothing else) and calls the C ABI through ctypes on the
-current CUDA stream.  There is no fallback: if the library is not built, or
+memory and streams, nothing else) and calls the C ABI, through ctypes or (the
+paged and windowed entries) a native module, on the current CUDA stream.  There is no fallback: if the library is not built, or
 the tensors are not on a CUDA device, calls raise.
 
 Entry points (names as in the C ABI, without the ``attn_`` prefix):
@@ -23,7 +23,7 @@ Paged KV cache (pages [P, Hkv, page_size, D], page_table int32 [B, max_pages]):
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import os
 from typing import Optional, Sequence
 
@@ -339,73 +339,26 @@ def kv_append_ring(k_cache, v_cache, k_new, v_new, seq_len, advance=True):
 
 
 # The entry points below are called once per layer and token by a serving loop,
-# where a kernel takes a few microseconds: their checks read each attribute
-# once, contiguous tensors pass NULL strides, the stride arrays of views are
-# made once per set of strides, and the device is switched only if it has to be.
+# where a kernel takes a few microseconds: their arguments are checked and
+# marshalled by a native module (csrc/binding.cpp) instead of ctypes.
 
-_I32 = torch.int32
-
-
-@functools.lru_cache(maxsize=1024)
-def _stride_array(st):
-    return (ctypes.c_int64 * len(st))(*st)
+_native_mod = None
 
 
-def _outer(t):
-    """The element strides of all axes but the last (None: contiguous)."""
-    if t.is_contiguous():
-        return None
-    st = t.stride()
-    if st[-1] != 1:
-        raise ValueError("the last (D) dimension must be contiguous")
-    return _stride_array(st[:-1])
-
-
-def _index(*ts):
-    """The CUDA device index that all tensors share."""
-    i = ts[0].get_device()
-    for t in ts:
-        if t.get_device() != i or not t.is_cuda:
-            if not t.is_cuda:
-                raise ValueError("libattn tensors must be on a CUDA device")
-            raise ValueError("all tensors must be on the same device")
-    return i
-
-
-def _run(entry, index, *args):
-    """Calls attn_<entry>(*args, stream) on device `index` and its current stream."""
-    f = getattr(_lib or lib(), entry)
-    if torch.cuda.current_device() == index:
-        st = f(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with torch.cuda.device(index):
-            st = f(*args, torch._C._cuda_getCurrentRawStream(index))
-    if st != 0:
-        raise AttnError(st, entry)
-
-
-def _like(t):
-    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
-
-
-def _i32(t, shape):
-    if t.dtype is not _I32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"expected a contiguous int32 tensor of shape {tuple(shape)}, got "
-                         f"{t.dtype} {tuple(t.shape)}")
-
-
-def _table(page_table):
-    """(B, max_pages, row stride) of an int32 page table whose rows are contiguous."""
-    if page_table.dtype is not _I32 or page_table.dim() != 2:
-        raise ValueError("page_table must be int32 [B, max_pages]")
-    B, M = page_table.shape
-    ts, one = page_table.stride()
-    if M > 1 and one != 1:
-        raise ValueError("the rows of page_table must be contiguous")
-    return B, M, ts if B > 1 else M
-
-
-_DTYPES = {torch.float32: ATTN_F32, torch.bfloat16: ATTN_BF16, torch.float16: ATTN_F16}
+def _native():
+    global _native_mod
+    if _native_mod is None:
+        lib()                                    # the same library instance, its errors first
+        path = os.path.join(os.path.dirname(LIB_PATH), "_attn_native.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"the native binding is not built ({path} missing): run "
+                               "`python -m transformer_attention_tcgen05_gb300.build`")
+        spec = importlib.util.spec_from_file_location("_attn_native", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.set_error(AttnError)
+        _native_mod = mod
+    return _native_mod
 
 
 def causal_gqa_window_fwd(q, k, v, window, sinks=0, o=None, scale=None):
@@ -413,20 +366,7 @@ def causal_gqa_window_fwd(q, k, v, window, sinks=0, o=None, scale=None):
     last Nq of the Nkv positions of k/v [B,Hkv,Nkv,D] (strided views, D
     contiguous); position p attends to its newest ``window`` positions and the
     first ``sinks`` tokens (window 0: all). o defaults to a new contiguous tensor."""
-    index = _index(q, k, v)
-    B, Hq, Nq, D = q.shape
-    Bk, Hkv, Nkv, Dk = k.shape
-    dt = q.dtype
-    if Bk != B or Dk != D or v.shape != k.shape or k.dtype is not dt or v.dtype is not dt:
-        raise ValueError("k/v must be [B, Hkv, Nkv, D] with q's dtype")
-    if o is None:
-        o = _like(q)
-    elif o.shape != q.shape or o.dtype is not dt or _index(q, o) != index:
-        raise ValueError("o must be [B, Hq, Nq, D] with q's dtype")
-    _run("attn_causal_gqa_window_fwd", index, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-         o.data_ptr(), B, Hq, Hkv, Nq, Nkv, D, _outer(q), _outer(k), _outer(v), _outer(o),
-         int(window), int(sinks), _DTYPES[dt] if dt in _DTYPES else _dtype(q), _scale(scale))
-    return o
+    return (_native_mod or _native()).causal_gqa_window_fwd(q, k, v, window, sinks, o, scale)
 
 
 def decode_paged_workspace_bytes(B, Hq, Hkv, D) -> int:
@@ -444,30 +384,8 @@ def decode_gqa_paged(q, k_pages, v_pages, page_table, seq_len, o=None, scale=Non
     zero-filled before its first use; calls of the same sizes leave it reusable.
     If omitted a zeroed one is allocated for this call.
     """
-    index = _index(q, k_pages, v_pages, page_table, seq_len)
-    B, Hq, D = q.shape
-    P, Hkv, S, Dk = k_pages.shape
-    Bt, M, ts = _table(page_table)
-    dt = q.dtype
-    if Dk != D or Bt != B or v_pages.shape != k_pages.shape or k_pages.dtype is not dt \
-            or v_pages.dtype is not dt:
-        raise ValueError("q [B,Hq,D], pages [P,Hkv,S,D] of q's dtype and page_table [B,max_pages] required")
-    _i32(seq_len, (B,))
-    if o is None:
-        o = _like(q)
-    elif o.shape != q.shape or o.dtype is not dt or _index(q, o) != index:
-        raise ValueError("o must be [B, Hq, D] with q's dtype")
-    if workspace is None:
-        workspace = torch.zeros(max(decode_paged_workspace_bytes(B, Hq, Hkv, D), 256),
-                                dtype=torch.uint8, device=q.device)
-    elif not workspace.is_contiguous() or _index(q, workspace) != index:
-        raise ValueError("the workspace must be contiguous")
-    _run("attn_decode_gqa_paged", index, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-         page_table.data_ptr(), seq_len.data_ptr(), o.data_ptr(), B, Hq, Hkv, D, P, S, M, ts,
-         _outer(q), _outer(k_pages), _outer(v_pages), _outer(o), int(window), int(sinks),
-         _DTYPES[dt] if dt in _DTYPES else _dtype(q), _scale(scale), workspace.data_ptr(),
-         workspace.nbytes)
-    return o
+    return (_native_mod or _native()).decode_gqa_paged(q, k_pages, v_pages, page_table, seq_len, o,
+                                                       scale, window, sinks, workspace)
 
 
 def kv_append_paged(k_pages, v_pages, k_new, v_new, page_table, seq_len, new_len=None,
@@ -476,136 +394,50 @@ def kv_append_paged(k_pages, v_pages, k_new, v_new, page_table, seq_len, new_len
     token; strided views) to the positions behind seq_len[b] in the sequences'
     pages; with advance, seq_len[b] += new_len[b] on the device.  new_len int32
     [B] defaults to T for every sequence."""
-    index = _index(k_pages, v_pages, k_new, v_new, page_table, seq_len)
-    if k_new.dim() == 3:
-        k_new, v_new = k_new.unsqueeze(2), v_new.unsqueeze(2)
-    B, Hkv, T, D = k_new.shape
-    P, Hp, S, Dp = k_pages.shape
-    Bt, M, ts = _table(page_table)
-    dt = k_pages.dtype
-    if Hp != Hkv or Dp != D or v_pages.shape != k_pages.shape or v_new.shape != k_new.shape \
-            or Bt != B or v_pages.dtype is not dt or k_new.dtype is not dt or v_new.dtype is not dt:
-        raise ValueError("pages [P,Hkv,S,D], new rows [B,Hkv,T,D] of one dtype, page_table [B,max_pages] required")
-    _i32(seq_len, (B,))
-    if new_len is not None:
-        _i32(new_len, (B,))
-        _index(k_pages, new_len)
-    _run("attn_kv_append_paged", index, k_pages.data_ptr(), v_pages.data_ptr(), k_new.data_ptr(),
-         v_new.data_ptr(), page_table.data_ptr(), seq_len.data_ptr(),
-         None if new_len is None else new_len.data_ptr(), B, T, Hkv, D, P, S, M, ts,
-         _outer(k_pages), _outer(v_pages), _outer(k_new), _outer(v_new),
-         _DTYPES[dt] if dt in _DTYPES else _dtype(k_pages), 1 if advance else 0)
+    (_native_mod or _native()).kv_append_paged(k_pages, v_pages, k_new, v_new, page_table, seq_len,
+                                               new_len, advance)
 
 
 def kv_pages_workspace_bytes(num_pages) -> int:
     return int(lib().attn_kv_pages_workspace_bytes(num_pages))
 
 
-def _pages_workspace(workspace, page_refs):
-    if workspace is None:
-        return torch.empty(max(kv_pages_workspace_bytes(page_refs.numel()), 256),
-                           dtype=torch.uint8, device=page_refs.device)
-    if not workspace.is_contiguous():
-        raise ValueError("the workspace must be contiguous")
-    _index(page_refs, workspace)
-    return workspace
-
-
 def kv_pages_reserve(page_table, seq_len, add_len, page_refs, page_size, workspace=None):
     """Give every entry of page_table [B,max_pages] that covers the add_len[b]
     positions behind seq_len[b] and holds no page the lowest free one
     (page_refs int32 [P]: table entries per page, 0 = free)."""
-    index = _index(page_table, seq_len, add_len, page_refs)
-    B, M, ts = _table(page_table)
-    P = page_refs.numel()
-    _i32(seq_len, (B,))
-    _i32(add_len, (B,))
-    _i32(page_refs, (P,))
-    workspace = _pages_workspace(workspace, page_refs)
-    _run("attn_kv_pages_reserve", index, page_table.data_ptr(), seq_len.data_ptr(),
-         add_len.data_ptr(), page_refs.data_ptr(), B, P, int(page_size), M, ts,
-         workspace.data_ptr(), workspace.nbytes)
+    (_native_mod or _native()).kv_pages_reserve(page_table, seq_len, add_len, page_refs, page_size,
+                                                workspace)
 
 
 def kv_pages_free(page_table, seq_len, page_refs, page_size, window=0, sinks=0):
     """Let go of the pages that hold no token their sequence can still see: all
     positions behind seq_len[b] (the whole row if it is 0) or, with window > 0,
     before the newest ``window`` tokens and past the first ``sinks``."""
-    index = _index(page_table, seq_len, page_refs)
-    B, M, ts = _table(page_table)
-    P = page_refs.numel()
-    _i32(seq_len, (B,))
-    _i32(page_refs, (P,))
-    _run("attn_kv_pages_free", index, page_table.data_ptr(), seq_len.data_ptr(),
-         page_refs.data_ptr(), B, P, int(page_size), M, ts, int(window), int(sinks))
+    (_native_mod or _native()).kv_pages_free(page_table, seq_len, page_refs, page_size, window, sinks)
 
 
 def kv_pages_fork(page_table, seq_len, page_refs, src, dst, page_size, workspace=None):
     """Make row dst[i] a copy of row src[i] (int32 [n]): full pages are shared, a
     partly filled last page gets a page of its own.  Returns (copy_src,
     copy_dst) int32 [n] for kv_pages_copy, -1 where nothing is to be copied."""
-    index = _index(page_table, seq_len, page_refs, src, dst)
-    B, M, ts = _table(page_table)
-    P, n = page_refs.numel(), src.numel()
-    _i32(seq_len, (B,))
-    _i32(page_refs, (P,))
-    _i32(src, (n,))
-    _i32(dst, (n,))
-    workspace = _pages_workspace(workspace, page_refs)
-    copy_src, copy_dst = torch.empty_like(src), torch.empty_like(dst)
-    _run("attn_kv_pages_fork", index, page_table.data_ptr(), seq_len.data_ptr(),
-         page_refs.data_ptr(), src.data_ptr(), dst.data_ptr(), n, copy_src.data_ptr(),
-         copy_dst.data_ptr(), B, P, int(page_size), M, ts, workspace.data_ptr(), workspace.nbytes)
-    return copy_src, copy_dst
+    return (_native_mod or _native()).kv_pages_fork(page_table, seq_len, page_refs, src, dst,
+                                                    page_size, workspace)
 
 
 def kv_pages_compact(page_table, page_refs, new_table=None, new_refs=None, workspace=None):
     """Move the live pages to the lowest numbers.  The new table and counts go to
     new_table / new_refs (default: in place).  Returns (copy_src, copy_dst,
     count) for kv_pages_copy."""
-    index = _index(page_table, page_refs)
-    B, M, ts = _table(page_table)
-    P = page_refs.numel()
-    new_table = page_table if new_table is None else new_table
-    new_refs = page_refs if new_refs is None else new_refs
-    _index(page_table, new_table, new_refs)
-    Bn, Mn, ns = _table(new_table)
-    if (Bn, Mn) != (B, M):
-        raise ValueError("new_table must be like page_table")
-    _i32(page_refs, (P,))
-    _i32(new_refs, (P,))
-    workspace = _pages_workspace(workspace, page_refs)
-    src = torch.empty(P // 2, dtype=_I32, device=page_refs.device)
-    dst = torch.empty_like(src)
-    count = src.new_empty(1)
-    _run("attn_kv_pages_compact", index, page_table.data_ptr(), page_refs.data_ptr(),
-         new_table.data_ptr(), new_refs.data_ptr(), src.data_ptr(), dst.data_ptr(),
-         count.data_ptr(), B, P, M, ts, ns, workspace.data_ptr(), workspace.nbytes)
-    return src, dst, count
+    return (_native_mod or _native()).kv_pages_compact(page_table, page_refs, new_table, new_refs,
+                                                       workspace)
 
 
 def kv_pages_copy(k_pages, v_pages, copy_src, copy_dst, count=None):
     """Copy pages copy_src[i] -> copy_dst[i] of pages [P,Hkv,S,D], or of every
     layer of [layers,P,Hkv,S,D] (views with D contiguous); pairs of -1, and
     pairs from count[0] on, are skipped."""
-    index = _index(k_pages, v_pages, copy_src, copy_dst)
-    if k_pages.dim() == 4:
-        k_pages, v_pages = k_pages.unsqueeze(0), v_pages.unsqueeze(0)
-    dt = k_pages.dtype
-    if k_pages.dim() != 5 or v_pages.shape != k_pages.shape or v_pages.dtype is not dt:
-        raise ValueError("pages [P,Hkv,S,D] or [layers,P,Hkv,S,D] of one dtype required")
-    layers, P, Hkv, S, D = k_pages.shape
-    n = copy_src.numel()
-    _i32(copy_src, (n,))
-    _i32(copy_dst, (n,))
-    if count is not None:
-        _i32(count, (1,))
-        _index(k_pages, count)
-    if n == 0:
-        return
-    _run("attn_kv_pages_copy", index, k_pages.data_ptr(), v_pages.data_ptr(), copy_src.data_ptr(),
-         copy_dst.data_ptr(), n, None if count is None else count.data_ptr(), layers, P, Hkv, S, D,
-         _outer(k_pages), _outer(v_pages), _DTYPES[dt] if dt in _DTYPES else _dtype(k_pages))
+    (_native_mod or _native()).kv_pages_copy(k_pages, v_pages, copy_src, copy_dst, count)
 
 
 def na3d_fwd(q, k, v, grid, kernel, o=None, scale=None):

@@ -1,10 +1,13 @@
-"""Builds libattn.so (the CUDA library behind include/libattn.h) in-tree.
+"""Builds libattn.so (the CUDA library behind include/libattn.h) and the native
+part of the Python binding (_attn_native.so) in-tree.
 
     python -m transformer_attention_tcgen05_gb300.build [--force] [--verbose]
 
 Each .cu under csrc/ compiles in parallel with nvcc for sm_103a only, then
 links into transformer_attention_tcgen05_gb300/_build/libattn.so with the
-CUDA runtime linked statically.  Rebuilds only what changed.
+CUDA runtime linked statically.  The binding (csrc/binding.cpp) compiles with
+the host compiler against the installed torch and Python headers and links to
+libattn.so beside it.  Rebuilds only what changed.
 """
 from __future__ import annotations
 
@@ -14,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libattn.so")
+BINDING = os.path.join(OUT, "_attn_native.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -48,8 +53,36 @@ def _compile(src: str, obj: str, verbose: bool) -> str:
     return r.stderr
 
 
+def _compile_binding(obj: str) -> str:
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-I", INCLUDE, "-isystem", os.path.join(t, "include"),
+           "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda,
+           "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on binding.cpp:\n{r.stderr}")
+    return r.stderr
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", OUT, "-lattn", "-L", lib,
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile (if stale) and link libattn.so; returns its path."""
+    """Compile (if stale) and link libattn.so and the binding; returns libattn.so's path."""
     os.makedirs(OUT, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     hdr_time = max([os.path.getmtime(h) for h in _headers()] + [0.0])
@@ -59,11 +92,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if force or verbose or not os.path.exists(o) or \
                 os.path.getmtime(o) < max(os.path.getmtime(s), hdr_time):
             jobs.append((s, o))
-    if jobs:
-        with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
+    bsrc, bobj = os.path.join(CSRC, "binding.cpp"), os.path.join(OUT, "binding.o")
+    bind = force or not os.path.exists(bobj) or \
+        os.path.getmtime(bobj) < max(os.path.getmtime(bsrc), hdr_time)
+    if jobs or bind:
+        with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs) + 1)) as ex:
+            bound = ex.submit(_compile_binding, bobj) if bind else None
             for (s, _), log in zip(jobs, ex.map(lambda j: _compile(j[0], j[1], verbose), jobs)):
                 if verbose and log:
                     sys.stderr.write(f"== {os.path.basename(s)}\n{log}")
+            if bound:
+                bound.result()
     objs = [os.path.join(OUT, os.path.basename(s)[:-3] + ".o") for s in srcs]
     if jobs or not os.path.exists(LIB) or \
             os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
@@ -73,6 +112,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}")
         os.replace(tmp, LIB)
+    if bind or not os.path.exists(BINDING) or os.path.getmtime(BINDING) < os.path.getmtime(bobj):
+        _link_binding(bobj)
     return LIB
 
 
