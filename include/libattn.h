@@ -395,7 +395,7 @@ ATTN_API size_t attn_decode_gqa_paged_workspace_bytes(int B, int Hq, int Hkv, in
  * that change the same pool are ordered by their stream.
  *   workspace: DEVICE scratch of attn_kv_pages_workspace_bytes(num_pages)
  *   bytes, 256-byte aligned, contents irrelevant, not used by another call at
- *   the same time.
+ *   the same time.  reserve and fork take B <= 16384.
  *
  * reserve: pages for the add_len[b] tokens (DEVICE int32 [B], >= 0) behind
  *   seq_len[b]: every entry that covers a position in [seq_len[b], seq_len[b] +
@@ -410,7 +410,7 @@ ATTN_API size_t attn_decode_gqa_paged_workspace_bytes(int B, int Hq, int Hkv, in
  *   (copy_src[i], copy_dst[i]) (DEVICE int32 [n]) names the copy that
  *   attn_kv_pages_copy must make before either row is appended to; (-1, -1) if
  *   there is none.  No row may be a target twice, or both target and source; a
- *   source may be named many times.  1 <= n <= B <= 262144.
+ *   source may be named many times.  1 <= n <= B, n <= 8192.
  * compact: moves the live pages to the lowest numbers.  With L live pages the
  *   k-th live page >= L goes to the k-th free page < L.  Writes the new table
  *   and counts to new_table (rows new_stride apart) and new_refs, either of

@@ -82,6 +82,7 @@ def test_allocator_refusals(L):
     assert reserve(refs=ctypes.c_void_p(0x40004)) == reserve(S=9) == reserve(ts=3) == INVALID
     assert reserve(w=None) == reserve(w=ctypes.c_void_p(0x90004)) == INVALID
     assert reserve(n=8) == RESOURCE
+    assert reserve(B=20000) == UNSUPPORTED
 
     def free(t=A, sl=Bp, refs=Cp, sinks=0, B=2, S=8):
         return L.attn_kv_pages_free(t, sl, refs, B, 10, S, 4, 4, 5, sinks, None)
@@ -91,7 +92,7 @@ def test_allocator_refusals(L):
         return L.attn_kv_pages_fork(A, Bp, Cp, src, dst, n, cs, cd, B, 10, 8, 4, 4, w, nb, None)
     assert fork(src=None) == fork(dst=None) == fork(n=0) == fork(n=3) == fork(cs=None) == INVALID
     assert fork(cd=Fp) == fork(cs=Dp) == fork(cd=Ep) == INVALID
-    assert fork(B=300000) == UNSUPPORTED
+    assert fork(B=20000) == UNSUPPORTED
     assert fork(nb=8) == RESOURCE
 
     def compact(nt=Cp, ns=4, cs=Ep, cd=Fp, cnt=ctypes.c_void_p(0x70000), t=A, ts=4):

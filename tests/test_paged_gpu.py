@@ -388,16 +388,18 @@ class Model:
             assert torch.equal(got_v.permute(1, 2, 0, 3), want - off)
 
 
-@pytest.mark.parametrize("S,P,B,seed", [(8, 60, 6, 0), (16, 41, 5, 1), (24, 200, 9, 2), (8, 1300, 40, 3)])
+@pytest.mark.parametrize("S,P,B,seed", [(8, 60, 6, 0), (16, 41, 5, 1), (24, 200, 9, 2), (8, 1300, 40, 3),
+                                        (8, 20011, 7, 4), (8, 17003, 1100, 5)])
 def test_allocator_against_the_model(ta, S, P, B, seed):
     rng = np.random.default_rng(seed)
-    m = Model(ta, B, M=max(12, P // 8), P=P, S=S, seed=seed)
+    m = Model(ta, B, M=min(2000, max(12, P // 8)), P=P, S=S, seed=seed, layers=1 if P > 5000 else 2)
     refused = 0
-    for step in range(40):
+    long_row = 500 * S if P > 5000 else 4 * S     # several entries per thread in a large pool
+    for step in range(40 if B < 100 else 12):
         op = rng.choice(["grow", "grow", "grow", "fork", "drop", "slide", "compact"])
         if op == "grow":
             room = m.table.shape[1] * S - m.pool.len
-            add = [int(min(room[b], rng.integers(0, 4 * S) if rng.random() < 0.6 else 0)) for b in range(B)]
+            add = [int(min(room[b], rng.integers(0, long_row if b < 8 else 4 * S) if rng.random() < 0.6 else 0)) for b in range(B)]
             if m.reserve(add):
                 m.append(add)
             else:

@@ -605,6 +605,7 @@ attn_status_t attn_kv_pages_reserve(int32_t *page_table, const int32_t *seq_len,
     attn_status_t st = check_pool(page_table, B, num_pages, page_size, max_pages, table_stride);
     if (st == ATTN_OK) st = check_pages_ws(workspace, workspace_bytes, num_pages);
     if (st != ATTN_OK) return st;
+    if (B > 16384) return ATTN_ERR_UNSUPPORTED;
     Ctx c;
     st = get_ctx(stream, &c);
     if (st != ATTN_OK) return st;
@@ -642,7 +643,7 @@ attn_status_t attn_kv_pages_fork(int32_t *page_table, int32_t *seq_len, int32_t 
     if (st == ATTN_OK) st = check_pages_ws(workspace, workspace_bytes, num_pages);
     if (st != ATTN_OK) return st;
     if (n < 1 || n > B) return ATTN_ERR_INVALID_ARG;
-    if (B > 262144) return ATTN_ERR_UNSUPPORTED;
+    if (B > 16384 || n > 8192) return ATTN_ERR_UNSUPPORTED;
     Ctx c;
     st = get_ctx(stream, &c);
     if (st != ATTN_OK) return st;

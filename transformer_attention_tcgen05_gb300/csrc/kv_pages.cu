@@ -10,8 +10,8 @@
 //
 // These calls move a few kilobytes of tables, so they are bound by latency,
 // not bandwidth: a call that has to number its requests (reserve, fork,
-// compact) is one cluster of 8 CTAs whose barriers and distributed shared
-// memory replace a grid-wide scan in several launches.  An append and a page
+// compact) is one CTA, or for a large pool one cluster of 8, whose barriers and
+// distributed shared memory replace a grid-wide scan in several launches.  An append and a page
 // copy move cache rows and are bound by HBM: 16-byte vectors, several in
 // flight per thread.
 #include "common.cuh"
@@ -220,12 +220,13 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p) 
 
 // --------------------------------------------------------------- allocator
 
-constexpr int kClu = 8;                                // CTAs of the allocator's cluster
-constexpr int kAT = 512;                               // threads per CTA
-constexpr int kAW = kAT / 32;
+constexpr int kClu = 8;                                // CTAs of a large call's cluster
+constexpr int kAT = 1024;                              // threads per CTA
+constexpr int kMaxRows = 16384;                        // rows of a table (shared-memory prefix)
+constexpr int kMaxForks = 8192;
 
 struct AllocShared {
-    int warp[kAW];
+    int warp[3][32];
     int val[8];                                        // one word per cluster exchange
 };
 
@@ -238,31 +239,47 @@ __device__ __forceinline__ int block_scan(AllocShared &sh, int x, int *total) {
         const int up = __shfl_up_sync(0xffffffffu, inc, off);
         if (lane >= off) inc += up;
     }
-    if (lane == 31) sh.warp[warp] = inc;
+    if (lane == 31) sh.warp[0][warp] = inc;
     __syncthreads();
-    int before = 0, all = 0;
+    const int s = sh.warp[0][lane];
+    int ws = s;
 #pragma unroll
-    for (int w = 0; w < kAW; ++w) {
-        const int s = sh.warp[w];
-        if (w < warp) before += s;
-        all += s;
+    for (int off = 1; off < 32; off <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, ws, off);
+        if (lane >= off) ws += up;
     }
     __syncthreads();
-    *total = all;
-    return before + inc - x;
+    *total = __shfl_sync(0xffffffffu, ws, 31);
+    return __shfl_sync(0xffffffffu, ws - s, warp) + inc - x;
 }
 
-__device__ __forceinline__ int block_sum(AllocShared &sh, int x) {
-    int all;
-    block_scan(sh, x, &all);
-    return all;
+// Sums of three words over the CTA.
+__device__ __forceinline__ void block_sum3(AllocShared &sh, int &x, int &y, int &z) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    x = __reduce_add_sync(0xffffffffu, x);
+    y = __reduce_add_sync(0xffffffffu, y);
+    z = __reduce_add_sync(0xffffffffu, z);
+    if (lane == 0) {
+        sh.warp[0][warp] = x;
+        sh.warp[1][warp] = y;
+        sh.warp[2][warp] = z;
+    }
+    __syncthreads();
+    x = __reduce_add_sync(0xffffffffu, sh.warp[0][lane]);
+    y = __reduce_add_sync(0xffffffffu, sh.warp[1][lane]);
+    z = __reduce_add_sync(0xffffffffu, sh.warp[2][lane]);
+    __syncthreads();
 }
 
 // Cluster barrier (arrive / wait are warp-collective); orders global and
-// distributed shared memory between the CTAs.
+// distributed shared memory between the CTAs.  A small call is one CTA.
 __device__ __forceinline__ void cluster_barrier() {
-    __syncwarp();
-    ptx::cluster_sync();
+    if (gridDim.x == 1) {
+        __syncthreads();
+    } else {
+        __syncwarp();
+        ptx::cluster_sync();
+    }
 }
 
 // Publishes one word per CTA; after the cluster barrier that follows,
@@ -270,17 +287,15 @@ __device__ __forceinline__ void cluster_barrier() {
 __device__ __forceinline__ void cluster_put(AllocShared &sh, int word, int x) {
     if (threadIdx.x == 0) sh.val[word] = x;
 }
-__device__ __forceinline__ int cluster_gather(AllocShared &sh, int word, int rank, int *total) {
+__device__ __forceinline__ int cluster_gather(AllocShared &sh, int word, int *total) {
+    const int rank = blockIdx.x, ranks = gridDim.x, lane = threadIdx.x & 31;
     const uint32_t a = ptx::smem_addr(&sh.val[word]);
-    int before = 0, all = 0;
-#pragma unroll
-    for (int r = 0; r < kClu; ++r) {
-        const int x = __float_as_int(ptx::ld_cluster_f32(ptx::cluster_map(a, r)));
-        if (r < rank) before += x;
-        all += x;
-    }
-    *total = all;
-    return before;
+    int x = 0;
+    if (lane < ranks)
+        x = ranks == 1 ? sh.val[word] : __float_as_int(ptx::ld_cluster_f32(ptx::cluster_map(a, lane)));
+    __syncwarp();
+    *total = __reduce_add_sync(0xffffffffu, x);
+    return __reduce_add_sync(0xffffffffu, lane < rank ? x : 0);
 }
 
 struct AllocParams {
@@ -298,11 +313,11 @@ struct AllocParams {
     unsigned *err;
 };
 
-// This CTA's share [i0, i1) of the pages (multiples of 4).
-__device__ __forceinline__ void page_share(int P, int rank, int *i0, int *i1) {
-    const int per = (cdiv(P, kClu) + 3) & ~3;
-    *i0 = imin(P, rank * per);
-    *i1 = imin(P, *i0 + per);
+// This CTA's share [i0, i1) of n items in units of g.
+__device__ __forceinline__ void share(int n, int g, int *i0, int *i1) {
+    const long long per = ((long long)(n + gridDim.x - 1) / gridDim.x + g - 1) / g * g;
+    *i0 = int(per * blockIdx.x < n ? per * blockIdx.x : n);
+    *i1 = int(*i0 + per < n ? *i0 + per : n);
 }
 
 // This thread's part of the free pages of [i0, i1), 16 bytes per load.
@@ -324,96 +339,107 @@ __device__ __forceinline__ int count_free(const int32_t *refs, int i0, int i1) {
 // is below `need`: list[rank] = page, refs[page] = 1.
 __device__ __forceinline__ void take_free(AllocShared &sh, int32_t *refs, int i0, int i1, int rank0,
                                           int need, int32_t *list) {
-    for (int b = i0; b < i1 && rank0 < need; b += kAT * 4) {
-        const int i = b + int(threadIdx.x) * 4;
-        int r[4], n = 0;
+    constexpr int E = 8;                               // pages per thread and round
+    for (int b = i0; b < i1 && rank0 < need; b += kAT * E) {
+        const int i = b + int(threadIdx.x) * E;
+        unsigned is_free = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            r[j] = i + j < i1 ? refs[i + j] : 1;
-            n += r[j] == 0;
-        }
+        for (int j = 0; j < E; ++j)
+            if (i + j < i1 && refs[i + j] == 0) is_free |= 1u << j;
         int all;
-        int k = rank0 + block_scan(sh, n, &all);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (r[j] == 0) {
-                if (k < need) {
-                    list[k] = i + j;
-                    refs[i + j] = 1;
-                }
-                ++k;
-            }
+        int k = rank0 + block_scan(sh, __popc(is_free), &all);
+        for (; is_free && k < need; is_free &= is_free - 1, ++k) {
+            const int page = i + __ffs(is_free) - 1;
+            list[k] = page;
+            refs[page] = 1;
+        }
         rank0 += all;
     }
 }
 
 // Reserve: entry i of row b is needed if it covers a position of
-// [seq_len[b], seq_len[b] + add[b]) and holds no page yet.
-__global__ void __launch_bounds__(kAT) reserve_kernel(const AllocParams p) {
+// [seq_len[b], seq_len[b] + add[b]) and holds no page yet.  The entries that
+// the rows ask about, one after the other, are numbered by a prefix over the
+// rows and dealt out evenly over the threads, however long the rows are.
+__global__ void __launch_bounds__(kAT, 1) reserve_kernel(const AllocParams p) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     __shared__ AllocShared sh;
-    const int rank = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int rows = cdiv(p.B, kClu), r0 = imin(p.B, rank * rows), r1 = imin(p.B, r0 + rows);
-
-    // ---- count: a warp per row, and the free pages of this CTA's share
-    int need = 0, bad = 0;
-    for (int b = r0 + warp; b < r1; b += kAW) {
-        const int len = p.seq_len[b], add = p.add[b];
-        if (len < 0 || add < 0 || (long long)len + add > (long long)p.M * p.S) {
-            bad = 1;
-            continue;
-        }
-        const int32_t *row = p.table + b * p.stride;
-        const int e1 = add > 0 ? (len + add - 1) / p.S + 1 : 0;
-#pragma unroll 4
-        for (int i = len / p.S + lane; i < e1; i += 32) need += row[i] < 0;
-    }
+    extern __shared__ int dyn[];
+    int *const pre = dyn, *const e0 = dyn + p.B + 1;   // entries before row b; its first entry
     int i0, i1;
-    page_share(p.P, rank, &i0, &i1);
-    const int free_part = count_free(p.refs, i0, i1);
-    const int my_need = block_sum(sh, need), my_bad = block_sum(sh, bad);
-    const int my_free = block_sum(sh, free_part);
-    cluster_put(sh, 0, my_need);
-    cluster_put(sh, 1, my_bad);
+    share(p.P, 4, &i0, &i1);
+    int my_free = count_free(p.refs, i0, i1);
+    int bad = 0, ask = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kAT) {
+        const int b = b0 + threadIdx.x;
+        int n = 0, first = 0;
+        if (b < p.B) {
+            const int len = p.seq_len[b], add = p.add[b];
+            if (len < 0 || add < 0 || (long long)len + add > (long long)p.M * p.S) {
+                bad = 1;
+            } else if (add > 0) {
+                first = len / p.S;
+                n = (len + add - 1) / p.S + 1 - first;
+            }
+        }
+        int all;
+        const int at = ask + block_scan(sh, n, &all);
+        if (b < p.B) {
+            pre[b] = at;
+            e0[b] = first;
+        }
+        ask += all;
+    }
+    if (threadIdx.x == 0) pre[p.B] = ask;
+    __syncthreads();
+    // the table entry of number x: the last row whose entries start at or before it
+    auto entry = [&](int x) -> int32_t * {
+        int lo = 0, hi = p.B;                          // pre[lo] <= x < pre[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid] <= x)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        return p.table + lo * p.stride + e0[lo] + (x - pre[lo]);
+    };
+    int x0, x1;
+    share(ask, 1, &x0, &x1);
+    int need = 0;
+    if (x1 - x0 <= kAT) {
+        if (x0 + int(threadIdx.x) < x1) need = *entry(x0 + threadIdx.x) < 0;
+    } else {
+        for (int x = x0 + threadIdx.x; x < x1; x += kAT) need += *entry(x) < 0;
+    }
+    const int mine = need;
+    block_sum3(sh, need, bad, my_free);
+    cluster_put(sh, 0, need);
+    cluster_put(sh, 1, bad);
     cluster_put(sh, 2, my_free);
     cluster_barrier();
     int total, errors, avail;
-    int base = cluster_gather(sh, 0, rank, &total);
-    cluster_gather(sh, 1, rank, &errors);
-    const int free0 = cluster_gather(sh, 2, rank, &avail);
+    int base = cluster_gather(sh, 0, &total);
+    cluster_gather(sh, 1, &errors);
+    const int free0 = cluster_gather(sh, 2, &avail);
     const bool refuse = errors > 0 || total > avail;   // the same in every CTA
     if (!refuse) take_free(sh, p.refs, i0, i1, free0, total, p.ws);
     cluster_barrier();                                 // the list is complete; no CTA left early
     if (refuse) {
-        if (rank == 0 && threadIdx.x == 0) raise_device_error(p.err, kDevCheck);
+        if (blockIdx.x == 0 && threadIdx.x == 0) raise_device_error(p.err, kDevCheck);
         return;
     }
-    // ---- assign, rows in order: a tile of one row per warp
-    for (int b0 = r0; b0 < r1; b0 += kAW) {
-        const int b = b0 + warp;
-        int n = 0, e0 = 0, e1 = 0;
-        int32_t *row = p.table + (long long)b * p.stride;
-        if (b < r1) {
-            const int len = p.seq_len[b], add = p.add[b];
-            e0 = len / p.S;
-            e1 = add > 0 ? (len + add - 1) / p.S + 1 : 0;
-#pragma unroll 4
-            for (int i = e0 + lane; i < e1; i += 32) n += row[i] < 0;
+    for (int x = x0; x < x1; x += kAT) {
+        int32_t *e = nullptr;
+        int n = 0;
+        if (x + int(threadIdx.x) < x1) {
+            e = entry(x + threadIdx.x);
+            n = x1 - x0 <= kAT ? mine : *e < 0;
         }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
         int all;
-        int k = base + block_scan(sh, lane == 0 ? n : 0, &all);
-        k = __shfl_sync(0xffffffffu, k, 0);
-        if (b < r1 && n > 0) {
-            for (int i = e0; i < e1; i += 32) {
-                const bool empty = i + lane < e1 && row[i + lane] < 0;
-                const unsigned bits = __ballot_sync(0xffffffffu, empty);
-                if (empty) row[i + lane] = p.ws[k + __popc(bits & ((1u << lane) - 1u))];
-                k += __popc(bits);
-            }
-        }
+        const int k = base + block_scan(sh, n, &all);
+        if (n) *e = p.ws[k];
         base += all;
     }
 }
@@ -459,139 +485,152 @@ __global__ void __launch_bounds__(256) free_kernel(const AllocParams p, int bloc
 
 // Fork: row dst[i] becomes a copy of row src[i].  Full pages are shared; a last
 // page that is partly filled gets a page of its own and a copy order.
-__global__ void __launch_bounds__(kAT) fork_kernel(const AllocParams p) {
+__global__ void __launch_bounds__(kAT, 1) fork_kernel(const AllocParams p) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     __shared__ AllocShared sh;
-    extern __shared__ unsigned is_dst[];               // one bit per row
+    extern __shared__ int dyn[];
+    int *const s_src = dyn, *const s_dst = dyn + p.n, *const s_len = dyn + 2 * p.n;
+    unsigned *const is_dst = reinterpret_cast<unsigned *>(dyn + 3 * p.n);   // one bit per row
     const int rank = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
     // ---- the lists: rows in range, no row twice a target, none target and source
-    int bad = 0;
-    const int words = (p.B + 31) / 32;
-    for (int i = threadIdx.x; i < words; i += kAT) is_dst[i] = 0;
+    int bad = 0, zero = 0, one = 0;
+    for (int i = threadIdx.x; i < (p.B + 31) / 32; i += kAT) is_dst[i] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < p.n; i += kAT) {
-        const int d = p.dst[i];
-        if (d < 0 || d >= p.B)
-            bad = 1;
-        else if (atomicOr(&is_dst[d >> 5], 1u << (d & 31)) >> (d & 31) & 1u)
-            bad = 1;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < p.n; i += kAT) {
-        const int s = p.src[i];
-        if (s < 0 || s >= p.B || (is_dst[s >> 5] >> (s & 31) & 1u)) {
+        const int s = p.src[i], d = p.dst[i];
+        int len = 0;
+        if (s < 0 || s >= p.B || d < 0 || d >= p.B) {
             bad = 1;
         } else {
-            const int len = p.seq_len[s];
+            if (atomicOr(&is_dst[d >> 5], 1u << (d & 31)) >> (d & 31) & 1u) bad = 1;
+            len = p.seq_len[s];
             if (len < 0 || len > (long long)p.M * p.S) bad = 1;
         }
+        s_src[i] = s;
+        s_dst[i] = d;
+        s_len[i] = len;
     }
-    bad = block_sum(sh, bad);                          // the same in every CTA
-    // ---- the entries: pages in range that are counted.  Work item: 128
-    //      entries of one fork, a warp each.
+    __syncthreads();
+    if (!bad)
+        for (int i = threadIdx.x; i < p.n; i += kAT) {
+            const int s = s_src[i];
+            if (s >= 0 && s < p.B && (is_dst[s >> 5] >> (s & 31) & 1u)) bad = 1;
+        }
+    block_sum3(sh, bad, zero, one);                    // the same in every CTA
+    // ---- counts: the targets' old pages let go, the shared full pages taken.
+    //      Work item: 128 entries of one fork, a warp each.  An entry that is no
+    //      counted page makes the call fail; the counts are put back then.
     const int blocks = cdiv(p.M, 128);
     const long long items = (long long)p.n * blocks;
-    const int w0 = rank * kAW + warp, wn = kClu * kAW;
+    const int w0 = rank * (kAT / 32) + warp, wn = int(gridDim.x) * (kAT / 32);
     int wrong = 0;
-    if (!bad)
-        for (long long it = w0; it < items; it += wn) {
-            const int f = int(it / blocks), j0 = int(it % blocks) * 128;
-            const int s = p.src[f], d = p.dst[f];
-            const int used = cdiv(p.seq_len[s], p.S);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int j = j0 + u * 32 + lane;
-                if (j >= p.M) continue;
-                const int old = p.table[d * p.stride + j], e = j < used ? p.table[s * p.stride + j] : -1;
-                if (old < -1 || old >= p.P || (old >= 0 && p.refs[old] <= 0)) wrong = 1;
-                if (e < -1 || e >= p.P || (e >= 0 && p.refs[e] <= 0)) wrong = 1;
-            }
-        }
-    wrong = block_sum(sh, wrong);
-    cluster_put(sh, 0, wrong);
-    cluster_barrier();
-    int any;
-    cluster_gather(sh, 0, rank, &any);
-    bool refuse = bad || any;
-    // ---- counts: the targets' old pages let go, the shared full pages taken
     auto recount = [&](int sign) {
         for (long long it = w0; it < items; it += wn) {
             const int f = int(it / blocks), j0 = int(it % blocks) * 128;
-            const int s = p.src[f], d = p.dst[f];
-            const int full = p.seq_len[s] / p.S;
+            const int32_t *rs = p.table + s_src[f] * p.stride, *rd = p.table + s_dst[f] * p.stride;
+            const int full = s_len[f] / p.S;
+            int old[4], e[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int j = j0 + u * 32 + lane;
-                if (j >= p.M) continue;
-                const int old = p.table[d * p.stride + j], e = j < full ? p.table[s * p.stride + j] : -1;
-                if (old >= 0) atomicSub(&p.refs[old], sign);
-                if (e >= 0) atomicAdd(&p.refs[e], sign);
+                old[u] = j < p.M ? rd[j] : -1;
+                e[u] = j < full ? rs[j] : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (old[u] < -1 || old[u] >= p.P)
+                    wrong = 1;
+                else if (old[u] >= 0 && atomicSub(&p.refs[old[u]], sign) <= 0 && sign > 0)
+                    wrong = 1;
+                if (e[u] < -1 || e[u] >= p.P)
+                    wrong = 1;
+                else if (e[u] >= 0 && atomicAdd(&p.refs[e[u]], sign) <= 0 && sign > 0)
+                    wrong = 1;
             }
         }
     };
-    if (!refuse) recount(1);
-    cluster_barrier();
-    // ---- pages of their own for the partly filled last pages, in list order;
-    //      CTA 0 leaves each fork's number in copy_dst
-    int i0, i1, tails = 0;
-    page_share(p.P, rank, &i0, &i1);
-    int my_free = 0;
-    if (!refuse) {
-        for (int b0 = 0; b0 < p.n; b0 += kAT) {
-            const int f = b0 + threadIdx.x;
-            int t = 0;
-            if (f < p.n) {
-                const int len = p.seq_len[p.src[f]];
-                t = len % p.S != 0 && p.table[p.src[f] * p.stride + len / p.S] >= 0;
-            }
-            int all;
-            const int k = tails + block_scan(sh, t, &all);
-            if (rank == 0 && f < p.n) p.copy_dst[f] = t ? k : -1;
-            tails += all;
+    if (!bad) recount(1);
+    // the partly filled last pages, in list order: how many come before this
+    // thread's fork; CTA 0 leaves each fork's number in copy_dst
+    int tails = 0;
+    for (int b0 = 0; b0 < p.n && !bad; b0 += kAT) {
+        const int f = b0 + threadIdx.x;
+        int t = 0;
+        if (f < p.n && s_len[f] % p.S != 0) {
+            const int e = p.table[s_src[f] * p.stride + s_len[f] / p.S];
+            if (e < -1 || e >= p.P)
+                wrong = 1;
+            else
+                t = e >= 0;
         }
-        my_free = block_sum(sh, count_free(p.refs, i0, i1));
+        int all;
+        const int k = tails + block_scan(sh, t, &all);
+        if (rank == 0 && f < p.n) p.copy_dst[f] = t ? k : -1;
+        tails += all;
     }
-    cluster_put(sh, 1, my_free);
+    cluster_barrier();                                 // every count is in
+    int i0, i1;
+    share(p.P, 4, &i0, &i1);
+    int my_free = bad ? 0 : count_free(p.refs, i0, i1);
+    // a last page to be copied from must be counted
+    if (!bad)
+        for (int f = rank * kAT + threadIdx.x; f < p.n; f += int(gridDim.x) * kAT)
+            if (s_len[f] % p.S != 0) {
+                const int e = p.table[s_src[f] * p.stride + s_len[f] / p.S];
+                if (e >= 0 && e < p.P && p.refs[e] <= 0) wrong = 1;
+            }
+    block_sum3(sh, my_free, wrong, zero);
+    cluster_put(sh, 0, my_free);
+    cluster_put(sh, 1, wrong);
     cluster_barrier();
-    int avail;
-    const int free0 = cluster_gather(sh, 1, rank, &avail);
-    if (!refuse && tails > avail) {
-        recount(-1);                                   // nothing has changed but the counts
-        refuse = true;
+    int avail, errors;
+    const int free0 = cluster_gather(sh, 0, &avail);
+    cluster_gather(sh, 1, &errors);
+    const bool refuse = bad || errors || tails > avail;
+    if (refuse) {
+        if (!bad) recount(-1);                         // nothing has changed but the counts
+    } else {
+        take_free(sh, p.refs, i0, i1, free0, tails, p.ws);
     }
-    if (!refuse) take_free(sh, p.refs, i0, i1, free0, tails, p.ws);
     cluster_barrier();
     if (refuse) {
-        for (int i = rank * kAT + threadIdx.x; i < p.n; i += kClu * kAT) p.copy_src[i] = p.copy_dst[i] = -1;
+        for (int i = rank * kAT + threadIdx.x; i < p.n; i += int(gridDim.x) * kAT)
+            p.copy_src[i] = p.copy_dst[i] = -1;
         if (rank == 0 && threadIdx.x == 0) raise_device_error(p.err, kDevCheck);
         return;
     }
     // ---- the rows
     for (long long it = w0; it < items; it += wn) {
         const int f = int(it / blocks), j0 = int(it % blocks) * 128;
-        const int s = p.src[f], d = p.dst[f];
-        const int len = p.seq_len[s], full = len / p.S;
+        const int32_t *rs = p.table + s_src[f] * p.stride;
+        int32_t *rd = p.table + s_dst[f] * p.stride;
+        const int full = s_len[f] / p.S;
+        int e[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int j = j0 + u * 32 + lane;
+            e[u] = j < full ? rs[j] : -1;
+        }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int j = j0 + u * 32 + lane;
             if (j >= p.M) continue;
-            int e = j < full ? p.table[s * p.stride + j] : -1;
             if (j == full) {                           // the last page, or the first entry behind it
                 const int k = p.copy_dst[f];
                 if (k >= 0) {
-                    e = p.ws[k];
-                    p.copy_src[f] = p.table[s * p.stride + j];
-                    p.copy_dst[f] = e;
+                    e[u] = p.ws[k];
+                    p.copy_src[f] = rs[j];
+                    p.copy_dst[f] = e[u];
                 } else {
                     p.copy_src[f] = -1;
                 }
             }
-            p.table[d * p.stride + j] = e;
+            rd[j] = e[u];
         }
         if (j0 == 0 && lane == 0) {
-            p.seq_len[d] = len;
+            p.seq_len[s_dst[f]] = s_len[f];
             if (full == p.M) p.copy_src[f] = -1;       // no entry behind a full table
         }
     }
@@ -600,22 +639,21 @@ __global__ void __launch_bounds__(kAT) fork_kernel(const AllocParams p) {
 // Compact: with L live pages, the k-th live page at or above L moves to the
 // k-th free page below L.  Lists the moves, fills the map old -> new of the
 // pages at or above L (ws[page]; ws[P] = L) and writes the new counts.
-__global__ void __launch_bounds__(kAT) compact_kernel(const AllocParams p) {
+__global__ void __launch_bounds__(kAT, 1) compact_kernel(const AllocParams p) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     __shared__ AllocShared sh;
-    const int rank = blockIdx.x;
     const int cap = p.P / 2;
-    int i0, i1;
-    page_share(p.P, rank, &i0, &i1);
-    int live = 0;
+    int i0, i1, zero = 0;
+    share(p.P, 4, &i0, &i1);
+    int live = 0, one = 0;
 #pragma unroll 4
     for (int i = i0 + threadIdx.x; i < i1; i += kAT) live += p.refs[i] > 0;
-    live = block_sum(sh, live);
+    block_sum3(sh, live, zero, one);
     cluster_put(sh, 0, live);
     cluster_barrier();
     int L;
-    cluster_gather(sh, 0, rank, &L);
+    cluster_gather(sh, 0, &L);
     // of this share: live pages at or above L (movers), free ones below (holes)
     int n_mov = 0, n_hole = 0;
 #pragma unroll 4
@@ -624,29 +662,35 @@ __global__ void __launch_bounds__(kAT) compact_kernel(const AllocParams p) {
         n_mov += lv && i >= L;
         n_hole += !lv && i < L;
     }
-    n_mov = block_sum(sh, n_mov);
-    n_hole = block_sum(sh, n_hole);
+    block_sum3(sh, n_mov, n_hole, zero);
     cluster_put(sh, 1, n_mov);
     cluster_put(sh, 2, n_hole);
     cluster_barrier();
     int moves, holes;
-    int km = cluster_gather(sh, 1, rank, &moves);
-    int kh = cluster_gather(sh, 2, rank, &holes);
-    for (int b = i0; b < i1; b += kAT) {
-        const int i = b + threadIdx.x;
-        const bool in = i < i1, lv = in && p.refs[i] > 0;
-        const int mov = lv && i >= L, hole = in && !lv && i < L;
+    int km = cluster_gather(sh, 1, &moves);
+    int kh = cluster_gather(sh, 2, &holes);
+    constexpr int E = 8;                               // pages per thread and round
+    for (int b = i0; b < i1; b += kAT * E) {
+        const int i = b + int(threadIdx.x) * E;
+        unsigned mov = 0, hole = 0;
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            if (i + j >= i1) break;
+            const bool lv = p.refs[i + j] > 0;
+            if (lv && i + j >= L) mov |= 1u << j;
+            if (!lv && i + j < L) hole |= 1u << j;
+            if (!lv && i + j >= L) p.ws[i + j] = -1;   // no live page: an entry naming it is wrong
+        }
         int all;
-        const int pre = block_scan(sh, mov | (hole << 16), &all);
-        if (mov) p.copy_src[km + (pre & 0xffff)] = i;
-        if (hole) p.copy_dst[kh + (pre >> 16)] = i;
-        if (in && i >= L && !lv) p.ws[i] = -1;         // no live page: an entry naming it is wrong
+        const int pre = block_scan(sh, __popc(mov) | (__popc(hole) << 16), &all);
+        for (int k = km + (pre & 0xffff); mov; mov &= mov - 1, ++k) p.copy_src[k] = i + __ffs(mov) - 1;
+        for (int k = kh + (pre >> 16); hole; hole &= hole - 1, ++k) p.copy_dst[k] = i + __ffs(hole) - 1;
         km += all & 0xffff;
         kh += all >> 16;
     }
     cluster_barrier();
-    const int t = rank * kAT + threadIdx.x;
-    for (int k = t; k < cap; k += kClu * kAT) {
+    const int t = blockIdx.x * kAT + threadIdx.x, step = int(gridDim.x) * kAT;
+    for (int k = t; k < cap; k += step) {
         if (k < moves) {
             const int s = p.copy_src[k], d = p.copy_dst[k];
             p.ws[s] = d;
@@ -700,6 +744,10 @@ AllocParams alloc_params(const Ctx &c, const PageTable &t) {
     p.err = c.err;
     return p;
 }
+
+// CTAs of a call that scans n words: one CTA reads 16,384 in about the time of
+// the cluster barriers that a larger call needs.
+int cluster_size(long long n) { return n <= 16384 ? 1 : kClu; }
 
 // A page is one block if its rows follow one another in either order.
 // st: element strides (head, token).
@@ -778,7 +826,13 @@ attn_status_t kv_pages_reserve(const Ctx &c, const PageTable &t, const int32_t *
     p.add = add;
     p.refs = refs;
     p.ws = static_cast<int32_t *>(ws);
-    return launch_pdl(c, reserve_kernel, dim3(kClu), kAT, kClu, 0, p);
+    if (t.B > kMaxRows) return ATTN_ERR_UNSUPPORTED;
+    static int done_mask = 0;
+    if (!ensure_smem_attr(reinterpret_cast<const void *>(reserve_kernel), (2 * kMaxRows + 1) * 4, c.device,
+                          &done_mask))
+        return ATTN_ERR_RESOURCE;
+    const int ctas = cluster_size(t.P);
+    return launch_pdl(c, reserve_kernel, dim3(ctas), kAT, ctas, size_t(2 * t.B + 1) * 4, p);
 }
 
 attn_status_t kv_pages_free(const Ctx &c, const PageTable &t, const int32_t *seq_len, int32_t *refs,
@@ -800,7 +854,13 @@ attn_status_t kv_pages_fork(const Ctx &c, const PageTable &t, int32_t *seq_len, 
     p.src = src; p.dst = dst; p.n = n;
     p.copy_src = copy_src; p.copy_dst = copy_dst;
     p.ws = static_cast<int32_t *>(ws);
-    return launch_pdl(c, fork_kernel, dim3(kClu), kAT, kClu, size_t(cdiv(t.B, 32)) * 4, p);
+    if (t.B > kMaxRows || n > kMaxForks) return ATTN_ERR_UNSUPPORTED;
+    static int done_mask = 0;
+    if (!ensure_smem_attr(reinterpret_cast<const void *>(fork_kernel), 3 * kMaxForks * 4 + kMaxRows / 8, c.device,
+                          &done_mask))
+        return ATTN_ERR_RESOURCE;
+    const int ctas = cluster_size((long long)n * t.max_pages + t.P);
+    return launch_pdl(c, fork_kernel, dim3(ctas), kAT, ctas, size_t(3 * n + cdiv(t.B, 32)) * 4, p);
 }
 
 attn_status_t kv_pages_compact(const Ctx &c, const PageTable &t, const int32_t *refs,
@@ -813,7 +873,8 @@ attn_status_t kv_pages_compact(const Ctx &c, const PageTable &t, const int32_t *
     p.ws = static_cast<int32_t *>(ws);
     const int blocks = cdiv(t.max_pages, 1024);
     if ((long long)t.B * blocks > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
-    const attn_status_t st = launch_pdl(c, compact_kernel, dim3(kClu), kAT, kClu, 0, p);
+    const int ctas = cluster_size(t.P);
+    const attn_status_t st = launch_pdl(c, compact_kernel, dim3(ctas), kAT, ctas, 0, p);
     if (st != ATTN_OK) return st;
     return launch_pdl(c, remap_kernel, dim3(t.B * blocks), 256, 1, 0, p, new_table, new_stride, blocks);
 }
