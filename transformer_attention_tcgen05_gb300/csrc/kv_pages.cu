@@ -491,23 +491,31 @@ __global__ void __launch_bounds__(kAT, 1) fork_kernel(const AllocParams p) {
     __shared__ AllocShared sh;
     extern __shared__ int dyn[];
     int *const s_src = dyn, *const s_dst = dyn + p.n, *const s_len = dyn + 2 * p.n;
-    unsigned *const is_dst = reinterpret_cast<unsigned *>(dyn + 3 * p.n);   // one bit per row
+    int *const s_tail = dyn + 3 * p.n, *const s_rank = dyn + 4 * p.n;       // last page, its number
+    unsigned *const is_dst = reinterpret_cast<unsigned *>(dyn + 5 * p.n);   // one bit per row
     const int rank = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
     // ---- the lists: rows in range, no row twice a target, none target and source
-    int bad = 0, zero = 0, one = 0;
+    int bad = 0, zero = 0, wrong = 0;
     for (int i = threadIdx.x; i < (p.B + 31) / 32; i += kAT) is_dst[i] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < p.n; i += kAT) {
         const int s = p.src[i], d = p.dst[i];
-        int len = 0;
+        int len = 0, tail = -1;
         if (s < 0 || s >= p.B || d < 0 || d >= p.B) {
             bad = 1;
         } else {
             if (atomicOr(&is_dst[d >> 5], 1u << (d & 31)) >> (d & 31) & 1u) bad = 1;
             len = p.seq_len[s];
-            if (len < 0 || len > (long long)p.M * p.S) bad = 1;
+            if (len < 0 || len > (long long)p.M * p.S) {
+                bad = 1;
+            } else if (len % p.S != 0) {
+                // a partly filled last page, to be copied from: it must be counted
+                tail = p.table[s * p.stride + len / p.S];
+                if (tail < -1 || tail >= p.P || (tail >= 0 && p.refs[tail] <= 0)) bad = 1;
+            }
         }
+        s_tail[i] = tail;
         s_src[i] = s;
         s_dst[i] = d;
         s_len[i] = len;
@@ -518,14 +526,13 @@ __global__ void __launch_bounds__(kAT, 1) fork_kernel(const AllocParams p) {
             const int s = s_src[i];
             if (s >= 0 && s < p.B && (is_dst[s >> 5] >> (s & 31) & 1u)) bad = 1;
         }
-    block_sum3(sh, bad, zero, one);                    // the same in every CTA
+    block_sum3(sh, bad, zero, wrong);                  // the same in every CTA
     // ---- counts: the targets' old pages let go, the shared full pages taken.
     //      Work item: 128 entries of one fork, a warp each.  An entry that is no
     //      counted page makes the call fail; the counts are put back then.
     const int blocks = cdiv(p.M, 128);
     const long long items = (long long)p.n * blocks;
     const int w0 = rank * (kAT / 32) + warp, wn = int(gridDim.x) * (kAT / 32);
-    int wrong = 0;
     auto recount = [&](int sign) {
         for (long long it = w0; it < items; it += wn) {
             const int f = int(it / blocks), j0 = int(it % blocks) * 128;
@@ -552,43 +559,27 @@ __global__ void __launch_bounds__(kAT, 1) fork_kernel(const AllocParams p) {
         }
     };
     if (!bad) recount(1);
-    // the partly filled last pages, in list order: how many come before this
-    // thread's fork; CTA 0 leaves each fork's number in copy_dst
-    int tails = 0;
+    int tails = 0;                                     // last pages to copy, numbered in list order
     for (int b0 = 0; b0 < p.n && !bad; b0 += kAT) {
         const int f = b0 + threadIdx.x;
-        int t = 0;
-        if (f < p.n && s_len[f] % p.S != 0) {
-            const int e = p.table[s_src[f] * p.stride + s_len[f] / p.S];
-            if (e < -1 || e >= p.P)
-                wrong = 1;
-            else
-                t = e >= 0;
-        }
+        const int t = f < p.n && s_tail[f] >= 0;
         int all;
         const int k = tails + block_scan(sh, t, &all);
-        if (rank == 0 && f < p.n) p.copy_dst[f] = t ? k : -1;
+        if (f < p.n) s_rank[f] = k;
         tails += all;
     }
     cluster_barrier();                                 // every count is in
     int i0, i1;
     share(p.P, 4, &i0, &i1);
     int my_free = bad ? 0 : count_free(p.refs, i0, i1);
-    // a last page to be copied from must be counted
-    if (!bad)
-        for (int f = rank * kAT + threadIdx.x; f < p.n; f += int(gridDim.x) * kAT)
-            if (s_len[f] % p.S != 0) {
-                const int e = p.table[s_src[f] * p.stride + s_len[f] / p.S];
-                if (e >= 0 && e < p.P && p.refs[e] <= 0) wrong = 1;
-            }
     block_sum3(sh, my_free, wrong, zero);
     cluster_put(sh, 0, my_free);
-    cluster_put(sh, 1, wrong);
+    cluster_put(sh, 1, wrong + bad);
     cluster_barrier();
     int avail, errors;
     const int free0 = cluster_gather(sh, 0, &avail);
     cluster_gather(sh, 1, &errors);
-    const bool refuse = bad || errors || tails > avail;
+    const bool refuse = errors || tails > avail;       // the same in every CTA
     if (refuse) {
         if (!bad) recount(-1);                         // nothing has changed but the counts
     } else {
@@ -618,20 +609,15 @@ __global__ void __launch_bounds__(kAT, 1) fork_kernel(const AllocParams p) {
             const int j = j0 + u * 32 + lane;
             if (j >= p.M) continue;
             if (j == full) {                           // the last page, or the first entry behind it
-                const int k = p.copy_dst[f];
-                if (k >= 0) {
-                    e[u] = p.ws[k];
-                    p.copy_src[f] = rs[j];
-                    p.copy_dst[f] = e[u];
-                } else {
-                    p.copy_src[f] = -1;
-                }
+                if (s_tail[f] >= 0) e[u] = p.ws[s_rank[f]];
+                p.copy_src[f] = s_tail[f];
+                p.copy_dst[f] = e[u];
             }
             rd[j] = e[u];
         }
         if (j0 == 0 && lane == 0) {
             p.seq_len[s_dst[f]] = s_len[f];
-            if (full == p.M) p.copy_src[f] = -1;       // no entry behind a full table
+            if (full == p.M) p.copy_src[f] = p.copy_dst[f] = -1;   // no entry behind a full table
         }
     }
 }
@@ -856,11 +842,11 @@ attn_status_t kv_pages_fork(const Ctx &c, const PageTable &t, int32_t *seq_len, 
     p.ws = static_cast<int32_t *>(ws);
     if (t.B > kMaxRows || n > kMaxForks) return ATTN_ERR_UNSUPPORTED;
     static int done_mask = 0;
-    if (!ensure_smem_attr(reinterpret_cast<const void *>(fork_kernel), 3 * kMaxForks * 4 + kMaxRows / 8, c.device,
+    if (!ensure_smem_attr(reinterpret_cast<const void *>(fork_kernel), 5 * kMaxForks * 4 + kMaxRows / 8, c.device,
                           &done_mask))
         return ATTN_ERR_RESOURCE;
     const int ctas = cluster_size((long long)n * t.max_pages + t.P);
-    return launch_pdl(c, fork_kernel, dim3(ctas), kAT, ctas, size_t(3 * n + cdiv(t.B, 32)) * 4, p);
+    return launch_pdl(c, fork_kernel, dim3(ctas), kAT, ctas, size_t(5 * n + cdiv(t.B, 32)) * 4, p);
 }
 
 attn_status_t kv_pages_compact(const Ctx &c, const PageTable &t, const int32_t *refs,
