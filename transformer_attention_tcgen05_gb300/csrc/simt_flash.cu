@@ -38,8 +38,6 @@ struct SimtParams {
     int nbh, nbw;            // boxes along h and w
     // causal grouped-query prefill (group > 1: KV head = query head / group)
     int causal, group;
-    // sliding window with sinks: query i sits at position off + i
-    int off, window, sinks;
     // H query heads: block row bh is batch bh / H, head bh % H; element
     // strides (batch, head, row) of q, k, v, o with D contiguous
     int H;
@@ -68,9 +66,7 @@ template <> __device__ __forceinline__ float4 load4<__half>(const __half *p) {
     return make_float4(f16_lo(u.x), f16_hi(u.x), f16_lo(u.y), f16_hi(u.y));
 }
 
-// WIN: causal with a sliding window and sinks; only the sink keys and the tile's
-// window are streamed, and a key a row does not see never enters its sums.
-template <typename T, int D, bool NA, bool WIN = false>
+template <typename T, int D, bool NA>
 __global__ void __launch_bounds__(SimtLayout<D>::NT)
 simt_flash_kernel(const SimtParams p) {
     using L = SimtLayout<D>;
@@ -96,7 +92,6 @@ simt_flash_kernel(const SimtParams p) {
     int wst = 0, wsh = 0, wsw = 0;                 // this query's window starts
     int u0t = 0, u0h = 0, u0w = 0, uh = 1, uw = 1;  // union box origin / extents
     int nkeys;
-    int kb0 = 0, win0 = 0, sink1 = 0;               // WIN: first key, window start, end of the sinks
     if (NA) {
         const int nb_hw = p.nbh * p.nbw;
         const int t0 = (tile / nb_hw) * p.bt;
@@ -126,12 +121,6 @@ simt_flash_kernel(const SimtParams p) {
         qvalid = qi < p.Nq;
         // causal: keys past the tile's last query are seen by no row of it
         nkeys = p.causal ? imin(p.Nkv, (tile + 1) * kRows) : p.Nkv;
-        if (WIN) {
-            nkeys = imin(p.Nkv, p.off + (tile + 1) * kRows);
-            win0 = imax(0, p.off + tile * kRows - p.window + 1);
-            sink1 = imin(p.sinks, win0);
-            kb0 = sink1 > 0 ? 0 : win0;
-        }
     }
 
     float qv[32], acc[32];
@@ -147,10 +136,7 @@ simt_flash_kernel(const SimtParams p) {
     }
     float m = -INFINITY, l = 0.f;
 
-    auto next_tile = [&](int kb) {
-        return WIN && kb + kKT >= sink1 ? imax(kb + kKT, win0) : kb + kKT;
-    };
-    for (int kb = kb0; kb < nkeys; kb = next_tile(kb)) {
+    for (int kb = 0; kb < nkeys; kb += kKT) {
         // ---- stage one key tile (K and V, converted to fp32) in shared memory
         for (int e = tid; e < kKT * D / 4; e += L::NT) {
             const int kk = (e * 4) / D, d0 = (e * 4) % D;
@@ -181,7 +167,6 @@ simt_flash_kernel(const SimtParams p) {
 #pragma unroll 1
         for (int c0 = 0; c0 < kKT; c0 += kChunk) {
             float s[kChunk];
-            unsigned seen = 0;                       // WIN: keys of the chunk this row sees
 #pragma unroll
             for (int c = 0; c < kChunk; ++c) {
                 const float *kr = Ks + (c0 + c) * L::ROW + sl * L::SLICE;
@@ -198,13 +183,7 @@ simt_flash_kernel(const SimtParams p) {
                 for (int off = 1; off < L::TPR; off <<= 1)
                     part += __shfl_xor_sync(0xffffffffu, part, off);
                 bool ok = kb + c0 + c < nkeys;
-                if (WIN) {
-                    const int key = kb + c0 + c, pos = p.off + qi;
-                    ok = ok && key <= pos && (key > pos - p.window || key < p.sinks);
-                    seen |= unsigned(ok) << c;
-                } else if (!NA && p.causal) {
-                    ok = ok && kb + c0 + c <= qi;
-                }
+                if (!NA && p.causal) ok = ok && kb + c0 + c <= qi;
                 if (NA) {
                     const int4 kq = kc[c0 + c];
                     ok = ok && unsigned(kq.x - wst) < unsigned(p.et) &&
@@ -217,17 +196,15 @@ simt_flash_kernel(const SimtParams p) {
 #pragma unroll
             for (int c = 1; c < kChunk; ++c) cm = fmaxf(cm, s[c]);
             const float mn = fmaxf(m, cm);
-            if (WIN ? seen != 0 : mn != -INFINITY) {
-                // m == -inf -> 0 (WIN: no finite score yet, NaN ones included: 1)
-                const float alpha = WIN && mn == -INFINITY ? 1.f : exp2f(m - mn);
+            if (mn != -INFINITY) {
+                const float alpha = exp2f(m - mn);   // m == -inf -> 0
                 l *= alpha;
 #pragma unroll
                 for (int d = 0; d < 32; ++d) acc[d] *= alpha;
                 m = mn;
 #pragma unroll
                 for (int c = 0; c < kChunk; ++c) {
-                    if (WIN && !((seen >> c) & 1u)) continue;
-                    const float pc = WIN && mn == -INFINITY && s[c] == -INFINITY ? 0.f : exp2f(s[c] - mn);
+                    const float pc = exp2f(s[c] - mn);
                     l += pc;
                     const float *vr = Vs + (c0 + c) * L::ROW + sl * L::SLICE;
 #pragma unroll
@@ -294,11 +271,11 @@ void choose_box(int T, int Hg, int W, const int kern[3], int rows, int box[3]) {
             }
 }
 
-template <typename T, int D, bool NA, bool WIN>
+template <typename T, int D, bool NA>
 attn_status_t launch(const Ctx &c, const SimtParams &p, int tiles, int BH) {
     using L = SimtLayout<D>;
     static int done_mask = 0;
-    auto kern = simt_flash_kernel<T, D, NA, WIN>;
+    auto kern = simt_flash_kernel<T, D, NA>;
     if (!ensure_smem_attr(reinterpret_cast<const void *>(kern), L::SMEM, c.device, &done_mask))
         return ATTN_ERR_RESOURCE;
     if (BH > 65535) return ATTN_ERR_UNSUPPORTED;
@@ -306,21 +283,21 @@ attn_status_t launch(const Ctx &c, const SimtParams &p, int tiles, int BH) {
     return launch_status(kFamSimt);
 }
 
-template <bool NA, bool WIN = false>
+template <bool NA>
 attn_status_t dispatch(const Ctx &c, attn_dtype_t dt, int D, const SimtParams &p, int tiles,
                        int BH) {
     if (dt == ATTN_F32) {
-        if (D == 32) return launch<float, 32, NA, WIN>(c, p, tiles, BH);
-        if (D == 64) return launch<float, 64, NA, WIN>(c, p, tiles, BH);
-        if (D == 128) return launch<float, 128, NA, WIN>(c, p, tiles, BH);
+        if (D == 32) return launch<float, 32, NA>(c, p, tiles, BH);
+        if (D == 64) return launch<float, 64, NA>(c, p, tiles, BH);
+        if (D == 128) return launch<float, 128, NA>(c, p, tiles, BH);
     } else if (dt == ATTN_F16) {
-        if (D == 32) return launch<__half, 32, NA, WIN>(c, p, tiles, BH);
-        if (D == 64) return launch<__half, 64, NA, WIN>(c, p, tiles, BH);
-        if (D == 128) return launch<__half, 128, NA, WIN>(c, p, tiles, BH);
+        if (D == 32) return launch<__half, 32, NA>(c, p, tiles, BH);
+        if (D == 64) return launch<__half, 64, NA>(c, p, tiles, BH);
+        if (D == 128) return launch<__half, 128, NA>(c, p, tiles, BH);
     } else {
-        if (D == 32) return launch<__nv_bfloat16, 32, NA, WIN>(c, p, tiles, BH);
-        if (D == 64) return launch<__nv_bfloat16, 64, NA, WIN>(c, p, tiles, BH);
-        if (D == 128) return launch<__nv_bfloat16, 128, NA, WIN>(c, p, tiles, BH);
+        if (D == 32) return launch<__nv_bfloat16, 32, NA>(c, p, tiles, BH);
+        if (D == 64) return launch<__nv_bfloat16, 64, NA>(c, p, tiles, BH);
+        if (D == 128) return launch<__nv_bfloat16, 128, NA>(c, p, tiles, BH);
     }
     return ATTN_ERR_UNSUPPORTED;
 }
@@ -363,25 +340,6 @@ attn_status_t simt_causal_gqa(const Ctx &c, attn_dtype_t dt, const void *q, cons
     p.sv = st ? st[2] : dense(Hkv, N, D);
     p.so = st ? st[3] : dense(Hq, N, D);
     return dispatch<false>(c, dt, D, p, cdiv(N, kRows), B * Hq);
-}
-
-attn_status_t simt_causal_window(const Ctx &c, attn_dtype_t dt, const void *q, const void *k,
-                                 const void *v, void *o, int B, int Hq, int Hkv, int Nq, int Nkv,
-                                 int D, int window, int sinks, float scale,
-                                 const TensorStrides *st) {
-    SimtParams p{};
-    p.q = q; p.k = k; p.v = v; p.o = o;
-    p.Nq = Nq;
-    p.Nkv = Nkv;
-    p.qscale = scale * kLog2e;
-    p.causal = 1;
-    p.group = Hq / Hkv;
-    p.off = Nkv - Nq;
-    p.window = window;
-    p.sinks = sinks;
-    p.H = Hq;
-    p.sq = st[0]; p.sk = st[1]; p.sv = st[2]; p.so = st[3];
-    return dispatch<false, true>(c, dt, D, p, cdiv(Nq, kRows), B * Hq);
 }
 
 attn_status_t simt_na3d(const Ctx &c, attn_dtype_t dt, const void *q, const void *k,
