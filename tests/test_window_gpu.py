@@ -90,6 +90,22 @@ def test_window_long_sampled_rows(ta):
     check(ta, "bf16", q, k, v, o, 2048, 4, rows=[0, 1, 127, 128, 2047, 2048, 2051, 2052, 5000, 8191, 8999])
 
 
+@pytest.mark.parametrize("dt,B,Hq,Hkv,Nq,Nkv,D,window,sinks", [
+    ("bf16", 2, 40, 8, 1200, 1200, 128, 300, 4),     # several pairs per CTA and single tiles behind them
+    ("f16", 3, 36, 4, 1100, 1500, 64, 130, 140),
+    ("bf16", 1, 152, 8, 300, 300, 128, 64, 0),       # whole rounds, a second tile of 44 rows
+    ("bf16", 1, 77, 7, 520, 520, 64, 0, 0)])         # a last pair whose second tile is empty
+def test_window_persistent_items(ta, dt, B, Hq, Hkv, Nq, Nkv, D, window, sinks):
+    q = make(dt, B, Hq, Nq, D, "token", 50)
+    k, v = make(dt, B, Hkv, Nkv, D, "head", 51), make(dt, B, Hkv, Nkv, D, "head", 52)
+    o = ta.causal_gqa_window_fwd(q, k, v, window, sinks)
+    again = [ta.causal_gqa_window_fwd(q, k, v, window, sinks) for _ in range(5)]
+    assert ta.device_status() == 0
+    assert all(torch.equal(a, o) for a in again)
+    check(ta, dt, q, k, v, o, window, sinks,
+          rows=sorted({0, 1, 127, 128, 255, 256, Nq // 2, Nq - 2, Nq - 1} & set(range(Nq))))
+
+
 def test_window_scores_far_above_the_running_maximum(ta):
     """Keys that grow along the sequence move the maximum in every tile."""
     q = make("bf16", 1, 2, 600, 128, "head", 7)

@@ -79,9 +79,9 @@ struct PgCfg {
 };
 
 // The chunk counts of a call fit 31 bits (checked by the entry), so the work
-// list is kept in ints.  Every launch starts with a cold instruction cache: the
-// code is kept short (one copy of each step, no 64-bit or run-time division in
-// the loop), which is worth 2 us of a 10 us call.
+// list is kept in ints; the steps of the loop are kept to one copy each and its
+// divisions by the page size are multiplications (the kernel is short: a call
+// of a few microseconds fetches most of its code once).
 struct PgParams {
     const void *q;
     void *o;

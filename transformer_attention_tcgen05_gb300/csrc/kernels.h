@@ -56,6 +56,10 @@ struct TensorStrides {
     long long b, h, n;
 };
 
+// 4D map {D, N, heads, B} over such a tensor; 128-byte swizzle, box {64, 128, 1, 1}.
+bool make_tmap4(CUtensorMap *m, const void *base, int D, int N, int heads, int B,
+                const TensorStrides &st, bool f16);
+
 // fp32 / generic SIMT flash attention (exact FFMA for fp32 storage).
 attn_status_t simt_full(const Ctx &c, attn_dtype_t dt, const void *q, const void *k,
                         const void *v, void *o, int B, int H, int Nq, int Nkv, int D,

@@ -118,12 +118,6 @@ struct TcParams {
     // element strides (batch, head, row), D contiguous
     int H;                   // query heads (the batch of block row bh is bh / H)
     long long o_sb, o_sh, o_sn;
-    // sliding window with sinks: query i sits at position off + i and sees the
-    // keys j <= off + i with j > off + i - window or j < sinks
-    int off, window, sinks;
-    // operands and element strides for rows redone outside the tensor cores
-    const void *q, *k, *v;
-    TensorStrides sq, sk, sv;
 };
 
 // Barrier block at OFF_BAR.
@@ -153,65 +147,10 @@ __device__ __forceinline__ T pick(const T (&a)[kNQ], int t) {
     return r;
 }
 
-// One row of windowed attention by one warp, in fp32 (every lane D / 32
-// channels): row qi of (batch b, query head h, KV head hk).  A row whose tensor-core
-// result is not finite comes here: a key that the row does not see has weight
-// zero in the P V product, but zero times an infinite or NaN value is NaN.
-// Only the row's own keys are read here, so such a value spoils exactly the
-// rows that see it.
-template <int D, bool F16>
-__device__ __forceinline__ void window_row(const TcParams &p, int b, int h, int hk, int qi) {
-    using H = H16<F16>;
-    using T = typename H::T;
-    constexpr int CW = D / 64;                       // 32-bit words per lane
-    const int lane = threadIdx.x & 31;
-    auto load = [&](const void *base, const TensorStrides &st, int head, int n, float (&x)[2 * CW]) {
-        const uint32_t *g = reinterpret_cast<const uint32_t *>(
-            static_cast<const T *>(base) + b * st.b + head * st.h + n * st.n) + lane * CW;
-#pragma unroll
-        for (int i = 0; i < CW; ++i) {
-            const uint32_t w = g[i];
-            x[2 * i] = H::lo(w);
-            x[2 * i + 1] = H::hi(w);
-        }
-    };
-    float q[2 * CW], acc[2 * CW], m = -INFINITY, l = 0.f;
-    load(p.q, p.sq, h, qi, q);
-#pragma unroll
-    for (int i = 0; i < 2 * CW; ++i) acc[i] = 0.f;
-    const int pos = p.off + qi;
-    const int lo = pos >= p.window ? pos - p.window + 1 : 0;
-    const int s_end = imin(p.sinks, lo);
-#pragma unroll 1
-    for (int j = s_end > 0 ? 0 : lo; j <= pos; j = j + 1 == s_end ? lo : j + 1) {
-        float x[2 * CW], s = 0.f;
-        load(p.k, p.sk, hk, j, x);
-#pragma unroll
-        for (int i = 0; i < 2 * CW; ++i) s = fmaf(q[i], x[i], s);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        s *= p.c_log2;
-        const float mn = fmaxf(m, s);
-        const float f = mn == -INFINITY ? 1.f : ptx::ex2(m - mn);
-        const float w = s == -INFINITY && mn == -INFINITY ? 0.f : ptx::ex2(s - mn);
-        load(p.v, p.sv, hk, j, x);
-        m = mn;
-        l = l * f + w;
-#pragma unroll
-        for (int i = 0; i < 2 * CW; ++i) acc[i] = fmaf(w, x[i], acc[i] * f);
-    }
-    const float inv = 1.f / l;
-    uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<T *>(p.o) + b * p.o_sb + h * p.o_sh +
-                                               qi * p.o_sn) + lane * CW;
-#pragma unroll
-    for (int i = 0; i < CW; ++i) o[i] = H::pack(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-}
-
 // CAUSAL: grouped-query causal prefill (query tile t sees key tiles up to its
-// diagonal).  WIN (with CAUSAL): sliding window with sinks; a CTA streams the
-// sink tiles and the tiles of its two query tiles' windows only.  F16: inputs, P and output in f16 instead of bf16 (same layouts;
+// diagonal).  F16: inputs, P and output in f16 instead of bf16 (same layouts;
 // the MMA operand format flips).
-template <int D, bool CAUSAL, bool F16, bool WIN = false>
+template <int D, bool CAUSAL, bool F16>
 __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
 tc_attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                const __grid_constant__ CUtensorMap tv, const TcParams p) {
@@ -232,29 +171,11 @@ tc_attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
     const int fkh = CAUSAL ? fh / p.group : fh;
 
     // ---- per-CTA work description (identical in every role)
-    // query tile t works in steps [f_t, n_t) of the CTA's key tile list
     int n_t[kNQ];
-    int f_t[kNQ] = {0, 0};
     int steps;
     int q0;
-    int w_lo = 0, w_sk = 0;        // first window tile, sink tiles before it
     constexpr int BNt = C::BN;     // keys per tile
-    if constexpr (WIN) {
-        q0 = (gridDim.x - 1 - blockIdx.x) * (kNQ * kBM);
-        const int pos = p.off + q0;
-        const bool two = q0 + kBM < p.Nq;
-        const int ns = cdiv(p.sinks, kBN);
-        w_lo = imax(0, pos - p.window + 1) / kBN;
-        const int lo1 = imax(0, pos + kBM - p.window + 1) / kBN;
-        w_sk = imin(ns, w_lo);
-        // The second query tile's window starts one key tile later: that tile
-        // goes first, for the first query tile alone, so that each query tile
-        // works in consecutive steps.
-        f_t[1] = two && lo1 > w_lo && w_lo >= ns ? 1 : 0;
-        n_t[0] = w_sk + (p.off + imin(q0 + kBM, p.Nq) - 1) / kBN - w_lo + 1;
-        n_t[1] = two ? w_sk + (p.off + imin(q0 + 2 * kBM, p.Nq) - 1) / kBN - w_lo + 1 : 0;
-        steps = imax(n_t[0], n_t[1]);
-    } else if constexpr (CAUSAL) {
+    if constexpr (CAUSAL) {
         // heaviest query blocks first; query tile t sees key tiles 0 .. its diagonal
         q0 = (gridDim.x - 1 - blockIdx.x) * (kNQ * kBM);
         const int all = cdiv(p.Nkv, kBN);
@@ -267,14 +188,6 @@ tc_attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         steps = cdiv(p.Nkv, kBN);
         n_t[0] = n_t[1] = steps;
     }
-
-    // key tile of step j: the leading tile of the first query tile (if any),
-    // the sink tiles, the window
-    auto tile_of = [&](int j) -> int {
-        if constexpr (!WIN) return j;
-        const int i = j - f_t[1];
-        return i < 0 ? w_lo : i < w_sk ? i : w_lo + j - w_sk;
-    };
 
     if (warp == C::W_INIT && lane == 0) {
         ptx::mbar_init(&bars->q_full, 1);
@@ -345,7 +258,7 @@ tc_attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 ptx::mbar_arrive_expect_tx(&full[s], C::KV_BYTES);
                 for (int pn = 0; pn < C::PANELS; ++pn)
                     ptx::tma_load_4d(smem + (which == 0 ? C::k_off(s) : C::v_off(s)) + pn * C::PANEL_KV, tm,
-                                     pn * 64, tile_of(j) * kBN, fkh, fb, &full[s], pol_kv);
+                                     pn * 64, j * kBN, fkh, fb, &full[s], pol_kv);
             }
             // after a timeout elsewhere: let the copies this thread issued land
             // (bounded) before the CTA's shared memory is released
@@ -386,7 +299,7 @@ tc_attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                 for (int kk = 0; kk < nkv; ++kk)
                     ptx::mma_ts(tmem + C::tm_o(t), a0 + kk * 8,
                                 ptx::desc_join(b0 + uint32_t(kk * (2048 >> 4)), HI128), id_pv,
-                                (j > pick(f_t, t) || kk > 0) ? 1u : 0u);
+                                (j > 0 || kk > 0) ? 1u : 0u);
                 ptx::tc_commit(&bars->o_done[t]);
             };
             bool ok = ptx::mbar_wait_or_abort(&bars->q_full, 0, p.err, abort) &&
@@ -412,8 +325,8 @@ tc_attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             // S(jprev) in registers; P over S: after P V (jprev), issued before)
             auto next_qk = [&](int t, int jn, int jprev) {
                 if (jn < pick(n_t, t)) {
-                    if (C::SEP_P && jn > pick(f_t, t))
-                        ok = ok && ptx::mbar_wait_or_abort(&bars->s_free[t], (jprev - pick(f_t, t)) & 1, p.err, abort);
+                    if (C::SEP_P)
+                        ok = ok && ptx::mbar_wait_or_abort(&bars->s_free[t], jprev & 1, p.err, abort);
                     wait_k(jn);
                     if (!ok) return;
                     ptx::tc_fence_after();
@@ -424,8 +337,8 @@ tc_attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             };
             // P V of key tile j for tile t
             auto this_pv = [&](int t, int j) {
-                if (j < pick(n_t, t) && j >= pick(f_t, t)) {
-                    ok = ok && ptx::mbar_wait_or_abort(&bars->p_ready[t], (j - pick(f_t, t)) & 1, p.err, abort);
+                if (j < pick(n_t, t)) {
+                    ok = ok && ptx::mbar_wait_or_abort(&bars->p_ready[t], j & 1, p.err, abort);
                     wait_v(j);
                     if (!ok) return;
                     ptx::tc_fence_after();
@@ -437,7 +350,7 @@ tc_attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             if (ok) {
 #pragma unroll
                 for (int t = 0; t < kNQ; ++t)
-                    if (n_t[t] > 0 && f_t[t] == 0) issue_qk(t, 0);
+                    if (n_t[t] > 0) issue_qk(t, 0);
                 if (steps > 0) ptx::tc_commit(&bars->k_empty[0]);
             }
             for (int j = 0; ok && j < steps; ++j) {
@@ -481,7 +394,7 @@ tc_attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         const uint32_t s_addr = lane_base + C::tm_s(t);
         const uint32_t p_addr = lane_base + C::tm_p(t);
         const float cl = p.c_log2;
-        const int nt = pick(n_t, t) - pick(f_t, t);   // this query tile's key tiles
+        const int nt = pick(n_t, t);
         const bool qvalid = q0 + t * kBM + row < p.Nq;
 
         // waits for the P V product of key tile jj of this query tile (and so
@@ -518,19 +431,7 @@ tc_attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
             //      position), key e is visible to row `row` iff e <= row
             {
                 int valid = p.Nkv - j * BNt;
-                if constexpr (WIN) {
-                    // rows at positions pos + row; only tiles on an edge of the
-                    // window are masked per element
-                    const int k0 = tile_of(j + pick(f_t, t)) * BNt, pos = p.off + q0 + t * kBM;
-                    if (k0 + BNt - 1 > pos ||
-                        (k0 + p.window < pos + kBM && k0 + BNt > p.sinks)) {
-                        const int hi = pos + row - k0, lo = hi - p.window + 1, sk = p.sinks - k0;
-#pragma unroll
-                        for (int e = 0; e < BNt; ++e)
-                            if (e > hi || (e < lo && e >= sk)) sv[e] = -INFINITY;
-                    }
-                    valid = BNt;
-                } else if constexpr (CAUSAL) {
+                if constexpr (CAUSAL) {
                     if (j == nt - 1) {
 #pragma unroll
                         for (int e = 0; e < BNt; ++e)
@@ -656,7 +557,6 @@ tc_attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         if (ok && nt > 0 && wait_pv(nt - 1)) {
             const float inv = 1.f / l;
             typename H16<F16>::T *orow = nullptr;
-            bool finite = true;
             if (qvalid)
                 orow = static_cast<typename H16<F16>::T *>(p.o) +
                        size_t(fb * p.o_sb + fh * p.o_sh + (long long)(q0 + t * kBM + row) * p.o_sn);
@@ -675,19 +575,6 @@ tc_attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
                     uint4 *dst = reinterpret_cast<uint4 *>(orow + c * 32);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) dst[e] = w4[e];
-                    if constexpr (WIN)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            finite = finite && fabsf(__uint_as_float(ov[e]) * inv) < INFINITY;
-                }
-            }
-            if constexpr (WIN) {
-                unsigned redo = __ballot_sync(0xffffffffu, !finite);
-                while (redo) {
-                    const int r = __ffs(redo) - 1;
-                    redo &= redo - 1;
-                    __syncwarp();
-                    window_row<D, F16>(p, fb, fh, fkh, q0 + t * kBM + quarter * 32 + r);
                 }
             }
         }
@@ -824,13 +711,13 @@ tc_selftest_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     }
 }
 
-template <int D, bool CAUSAL = false, bool F16 = false, bool WIN = false>
+template <int D, bool CAUSAL = false, bool F16 = false>
 attn_status_t launch_tc(const Ctx &c, const CUtensorMap &tq, const CUtensorMap &tk,
                         const CUtensorMap &tv, const TcParams &p, dim3 grid) {
     using C = TcCfg<D>;
     static int done_mask = 0;
     static int regs = -1;
-    auto kern = tc_attn_kernel<D, CAUSAL, F16, WIN>;
+    auto kern = tc_attn_kernel<D, CAUSAL, F16>;
     if (!ensure_smem_attr(reinterpret_cast<const void *>(kern), C::SMEM, c.device, &done_mask))
         return ATTN_ERR_RESOURCE;
     // The warpgroups re-split the launch's register file with setmaxnreg; the
@@ -983,39 +870,6 @@ attn_status_t tc_causal_gqa(const Ctx &c, attn_dtype_t dt, const void *q, const 
         return D == 128 ? launch_tc<128, true, true>(c, tq, tk, tv, p, grid)
                         : launch_tc<64, true, true>(c, tq, tk, tv, p, grid);
     return D == 128 ? launch_tc<128, true>(c, tq, tk, tv, p, grid) : launch_tc<64, true>(c, tq, tk, tv, p, grid);
-}
-
-attn_status_t tc_causal_window(const Ctx &c, attn_dtype_t dt, const void *q, const void *k,
-                               const void *v, void *o, int B, int Hq, int Hkv, int Nq, int Nkv,
-                               int D, int window, int sinks, float scale, const TensorStrides *st) {
-    const bool f16 = dt == ATTN_F16;
-    CUtensorMap tq, tk, tv;
-    // a layout the tensor-map encoder refuses goes to the strided SIMT kernel
-    if (!make_tmap4(&tq, q, D, Nq, Hq, B, st[0], f16) || !make_tmap4(&tk, k, D, Nkv, Hkv, B, st[1], f16) ||
-        !make_tmap4(&tv, v, D, Nkv, Hkv, B, st[2], f16))
-        return ATTN_ERR_UNSUPPORTED;
-    TcParams p{};
-    p.Nq = Nq;
-    p.Nkv = Nkv;
-    p.c_log2 = scale * kLog2e;
-    p.o = o;
-    p.err = c.err;
-    p.Hq = Hq;
-    p.Hkv = Hkv;
-    p.group = Hq / Hkv;
-    p.H = Hq;
-    p.o_sb = st[3].b; p.o_sh = st[3].h; p.o_sn = st[3].n;
-    p.off = Nkv - Nq;
-    p.window = window;
-    p.sinks = sinks;
-    p.q = q; p.k = k; p.v = v;
-    p.sq = st[0]; p.sk = st[1]; p.sv = st[2];
-    const dim3 grid(cdiv(Nq, kNQ * kBM), B * Hq);
-    if (f16)
-        return D == 128 ? launch_tc<128, true, true, true>(c, tq, tk, tv, p, grid)
-                        : launch_tc<64, true, true, true>(c, tq, tk, tv, p, grid);
-    return D == 128 ? launch_tc<128, true, false, true>(c, tq, tk, tv, p, grid)
-                    : launch_tc<64, true, false, true>(c, tq, tk, tv, p, grid);
 }
 
 attn_status_t tc_selftest(const Ctx &c, const void *q, const void *k, const void *v,

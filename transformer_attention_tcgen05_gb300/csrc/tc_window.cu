@@ -1,0 +1,724 @@
+// Tensor-core (tcgen05 + TMEM + TMA) causal grouped-query attention with a
+// sliding window and sinks, bf16 and f16, sm_103a.
+//
+// Query i sits at position p = off + i and sees the keys j <= p with
+// j > p - window or j < sinks.  The tile arithmetic is that of the flash kernel
+// (tc_flash.cu): a CTA's two 128-row query tiles share a stream of 128-key tiles,
+// S and O live in tensor memory, P goes back there in 16 bits (over S at
+// D = 128), thread = query row in two softmax warpgroups, one thread issues every
+// MMA.  Bound by the exponentials and the tensor pipe at about 1.4 us per step of
+// two tiles, plus about 8 us per CTA (set-up, first loads, masked tiles, last
+// P V and epilogue), which is what a short window pays for.  What differs:
+//
+//  * Key tile list.  A CTA streams the sink tiles and the tiles of its windows
+//    only; tiles on an edge (diagonal, window start, sinks) are masked per
+//    element, nearly always by one bound.
+//  * Pairs of heads.  The two query tiles are the same rows of two query heads
+//    of one KV head: one key range, no step that serves one tile alone.  (Pairs
+//    of row tiles, which odd groups use, see windows one key tile apart: the
+//    leading tile goes first, for the first query tile alone, so that each
+//    works in consecutive steps.)  4096 tokens, 32 heads on 8, window 1024,
+//    sinks 4, D 128: 86.1 us with row pairs and one general mask, 74.4 us so.
+//  * The pairs that do not fill a last round of the SMs are split into single
+//    query tiles, so that the round ends sooner.
+//  * One CTA per item.  A persistent form (K and V of the next pair streaming in
+//    behind the current one's, its first scores computed during the epilogue)
+//    measured slower: 81 against 74.4 us at 4096 tokens, 1580 against 1467 us at
+//    32768 tokens with a window of 4096 (1406 TFLOP/s).
+//
+// A key that a row does not see does not change its output even if its value is
+// infinite or NaN: such a row is redone from its own keys (window_row).
+//
+// All spin-waits are bounded (1 s); on a timeout the CTA raises the device
+// error word, drains what it issued, frees TMEM and exits.
+#include <cuda.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kBM = 128;      // query rows per tile (MMA M)
+constexpr int kNQ = 2;        // query tiles per CTA
+constexpr int kBN = 128;      // keys per key tile (MMA N of S)
+
+template <int D>
+struct WnCfg {
+    static constexpr int BN = kBN;                         // keys per key tile
+    static constexpr int PANELS = D / 64;                  // 128-byte swizzle panels
+    static constexpr int PANEL_Q = kBM * 128;              // bytes per Q panel
+    static constexpr int PANEL_KV = BN * 128;              // bytes per K/V panel
+    static constexpr int Q_BYTES = PANELS * PANEL_Q;
+    static constexpr int KV_BYTES = PANELS * PANEL_KV;     // one K (or V) stage
+    static constexpr int BUDGET = 227 * 1024 - 2048;
+    static constexpr int NS_ALL = (BUDGET - kNQ * Q_BYTES) / KV_BYTES;
+    // K and V rings of equal depth (a third K stage at D = 128 measured slower)
+    static constexpr int KS = NS_ALL / 2 > 4 ? 4 : NS_ALL / 2;               // K stages
+    static constexpr int VS = NS_ALL - NS_ALL / 2 > 4 ? 4 : NS_ALL - NS_ALL / 2;  // V stages
+    static_assert(KS >= 2 && VS >= 2, "at least two K and two V stages");
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = kNQ * Q_BYTES;
+    static constexpr int OFF_V = OFF_K + KS * KV_BYTES;
+    static constexpr int OFF_BAR = OFF_V + VS * KV_BYTES;
+    static constexpr int SMEM = OFF_BAR + 512 + 1024;      // barriers + 1024 B alignment slack
+    // Tensor memory (512 columns): S_t at t BN, O_t at kNQ BN + t D; P (16-bit,
+    // two per column) over the first half of S_t (D = 128) or in columns of
+    // its own after the O's (D = 64).
+    static constexpr bool SEP_P = kNQ * (BN + D + BN / 2) <= 512;
+    static constexpr uint32_t tm_s(int t) { return t * BN; }
+    static constexpr uint32_t tm_o(int t) { return kNQ * BN + t * D; }
+    static constexpr uint32_t tm_p(int t) { return SEP_P ? kNQ * BN + kNQ * D + t * (BN / 2) : t * BN; }
+    static constexpr uint32_t TM_COLS = 512;
+    static_assert(tm_o(kNQ - 1) + D <= TM_COLS && (!SEP_P || tm_p(kNQ) <= TM_COLS),
+                  "tensor-memory layout must fit 512 columns");
+    static constexpr int NSOFT = 4 * kNQ;
+    static constexpr int W_MMA = NSOFT;                   // MMA issuer, TMEM owner
+    static constexpr int W_LOAD = NSOFT + 1;              // Q and K copies
+    static constexpr int W_LOADV = NSOFT + 2;             // V copies
+    static constexpr int W_INIT = NSOFT + 3;              // barrier set-up
+    static constexpr int NT = (NSOFT + 4) * 32;            // 3 warpgroups
+    // register split: launch 168 x 384 = 64512; 2 x 128 x 216 + 128 x 72 = 64512
+    static constexpr int REGS_LAUNCH = 168;
+    static constexpr int REGS_SOFTMAX = 216;
+    static constexpr int REGS_OTHER = 72;
+    static_assert(2 * 128 * REGS_SOFTMAX + 128 * REGS_OTHER <= NT * REGS_LAUNCH,
+                  "setmaxnreg split must fit the launch's register file share");
+    static constexpr int k_off(int s) { return OFF_K + s * KV_BYTES; }
+    static constexpr int v_off(int s) { return OFF_V + s * KV_BYTES; }
+};
+
+struct WnParams {
+    int Nq, Nkv;             // query / key tokens per (batch, head)
+    int off, window, sinks;  // query i sits at position off + i
+    float c_log2;            // scale * log2(e)
+    unsigned *err;
+    int H, group, BH;        // query heads, query heads per KV head, batch * heads
+    int pairs;               // query tile pairs
+    int G;                   // SMs: pairs per round
+    int by_head;             // a pair is two heads of one KV head (else two row tiles)
+    // operands and element strides (rows redone outside the tensor cores; o)
+    const void *q, *k, *v;
+    void *o;
+    TensorStrides sq, sk, sv;
+    long long o_sb, o_sh, o_sn;
+};
+
+// Barrier block at OFF_BAR.
+template <int KS, int VS>
+struct Bars {
+    uint64_t q_full;
+    uint64_t k_full[KS], k_empty[KS], v_full[VS], v_empty[VS];
+    // per query tile t: s_full its Q K^T has completed, p_ready the softmax
+    // has written P, o_done the P V product that read P has completed,
+    // s_free (separate P, D = 64) the softmax holds S_t in registers
+    uint64_t s_full[kNQ], p_ready[kNQ], o_done[kNQ], s_free[kNQ];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+};
+
+// a[t] for a per-query-tile array and a run-time t, by selects
+template <typename T>
+__device__ __forceinline__ T pick(const T (&a)[kNQ], int t) { return t == 0 ? a[0] : a[1]; }
+
+// One work item: a pair of query tiles, or one tile alone.  Query tile t (rows
+// q0 + t dq, head fh + t dh) works in steps [f[t], n[t]) of the item's key tile
+// list.
+struct Item {
+    int q0, fb, fh, fkh, dq, dh;
+    int n[kNQ], f[kNQ], steps;
+    int w_lo, w_sk;                // first window tile, sink tiles before it
+
+    // key tile of step j: the leading tile of the first query tile (if any),
+    // the sink tiles, the window
+    __device__ __forceinline__ int tile(int j) const {
+        const int i = j - f[1];
+        return i < 0 ? w_lo : i < w_sk ? i : w_lo + j - w_sk;
+    }
+};
+
+// This CTA's item.  Rounds of whole pairs, late queries first, then the rest as
+// single tiles.
+__device__ __forceinline__ Item get_item(const WnParams &p) {
+    Item w;
+    const int G = p.G, k = blockIdx.x / G, c = blockIdx.x - k * G;
+    const int rounds = p.pairs / G;
+    int pair, half = -1;
+    if (k < rounds) {
+        pair = k * G + c;
+    } else {
+        const int s = (k - rounds) * G + c;
+        pair = rounds * G + (s >> 1);
+        half = s & 1;
+    }
+    const int hp = p.by_head ? p.BH / 2 : p.BH;          // pairs (or heads) per row block
+    const int qb = (p.pairs / hp - 1) - pair / hp, bh = (pair % hp) * (p.by_head ? 2 : 1);
+    w.dq = p.by_head ? 0 : kBM;
+    w.dh = p.by_head ? 1 : 0;
+    w.fb = bh / p.H;
+    w.fh = bh % p.H + (half > 0 ? w.dh : 0);
+    w.fkh = w.fh / p.group;
+    w.q0 = qb * (p.by_head ? kBM : kNQ * kBM) + (half > 0 ? w.dq : 0);
+    const int pos = p.off + w.q0;
+    const bool one = w.q0 < p.Nq, two = half < 0 && w.q0 + w.dq < p.Nq;
+    const int ns = cdiv(p.sinks, kBN);
+    w.w_lo = imax(0, pos - p.window + 1) / kBN;
+    const int lo1 = imax(0, pos + w.dq - p.window + 1) / kBN;
+    w.w_sk = imin(ns, w.w_lo);
+    w.f[0] = 0;
+    w.f[1] = two && lo1 > w.w_lo && w.w_lo >= ns ? 1 : 0;
+    // (a single second row tile past the sequence's end has no step)
+    w.n[0] = one ? w.w_sk + (p.off + imin(w.q0 + kBM, p.Nq) - 1) / kBN - w.w_lo + 1 : 0;
+    w.n[1] = two ? w.w_sk + (p.off + imin(w.q0 + w.dq + kBM, p.Nq) - 1) / kBN - w.w_lo + 1 : 0;
+    w.steps = imax(w.n[0], w.n[1]);
+    return w;
+}
+
+// One row of windowed attention by one warp, in fp32 (every lane D / 32
+// channels): row qi of (batch b, query head h, KV head hk).  A row whose tensor-core
+// result is not finite comes here: a key that the row does not see has weight
+// zero in the P V product, but zero times an infinite or NaN value is NaN.
+// Only the row's own keys are read here, so such a value spoils exactly the
+// rows that see it.
+template <int D, bool F16>
+__device__ __forceinline__ void window_row(const WnParams &p, int b, int h, int hk, int qi) {
+    using H = H16<F16>;
+    using T = typename H::T;
+    constexpr int CW = D / 64;                       // 32-bit words per lane
+    const int lane = threadIdx.x & 31;
+    auto load = [&](const void *base, const TensorStrides &st, int head, int n, float (&x)[2 * CW]) {
+        const uint32_t *g = reinterpret_cast<const uint32_t *>(
+            static_cast<const T *>(base) + b * st.b + head * st.h + n * st.n) + lane * CW;
+#pragma unroll
+        for (int i = 0; i < CW; ++i) {
+            const uint32_t w = g[i];
+            x[2 * i] = H::lo(w);
+            x[2 * i + 1] = H::hi(w);
+        }
+    };
+    float q[2 * CW], acc[2 * CW], m = -INFINITY, l = 0.f;
+    load(p.q, p.sq, h, qi, q);
+#pragma unroll
+    for (int i = 0; i < 2 * CW; ++i) acc[i] = 0.f;
+    const int pos = p.off + qi;
+    const int lo = pos >= p.window ? pos - p.window + 1 : 0;
+    const int s_end = imin(p.sinks, lo);
+#pragma unroll 1
+    for (int j = s_end > 0 ? 0 : lo; j <= pos; j = j + 1 == s_end ? lo : j + 1) {
+        float x[2 * CW], s = 0.f;
+        load(p.k, p.sk, hk, j, x);
+#pragma unroll
+        for (int i = 0; i < 2 * CW; ++i) s = fmaf(q[i], x[i], s);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        s *= p.c_log2;
+        const float mn = fmaxf(m, s);
+        const float f = mn == -INFINITY ? 1.f : ptx::ex2(m - mn);
+        const float w = s == -INFINITY && mn == -INFINITY ? 0.f : ptx::ex2(s - mn);
+        load(p.v, p.sv, hk, j, x);
+        m = mn;
+        l = l * f + w;
+#pragma unroll
+        for (int i = 0; i < 2 * CW; ++i) acc[i] = fmaf(w, x[i], acc[i] * f);
+    }
+    const float inv = 1.f / l;
+    uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<T *>(p.o) + b * p.o_sb + h * p.o_sh +
+                                               qi * p.o_sn) + lane * CW;
+#pragma unroll
+    for (int i = 0; i < CW; ++i) o[i] = H::pack(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(WnCfg<D>::NT, 1)
+tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                 const __grid_constant__ CUtensorMap tv, const WnParams p) {
+    using C = WnCfg<D>;
+    using BarsT = Bars<C::KS, C::VS>;
+    static_assert(sizeof(BarsT) <= 512, "barrier block must fit its reserved bytes");
+    extern __shared__ uint8_t smem_raw[];
+    // 1024-byte alignment for the 128-byte swizzle atoms
+    uint8_t *smem = smem_raw + ((1024 - (ptx::smem_addr(smem_raw) & 1023)) & 1023);
+    BarsT *bars = reinterpret_cast<BarsT *>(smem + C::OFF_BAR);
+    volatile int *abort = &bars->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int BNt = C::BN;     // keys per tile
+
+    if (warp == C::W_INIT && lane == 0) {
+        ptx::mbar_init(&bars->q_full, 1);
+        for (int s = 0; s < C::KS; ++s) {
+            ptx::mbar_init(&bars->k_full[s], 1);
+            ptx::mbar_init(&bars->k_empty[s], 1);
+        }
+        for (int s = 0; s < C::VS; ++s) {
+            ptx::mbar_init(&bars->v_full[s], 1);
+            ptx::mbar_init(&bars->v_empty[s], 1);
+        }
+        for (int t = 0; t < kNQ; ++t) {
+            ptx::mbar_init(&bars->s_full[t], 1);
+            ptx::mbar_init(&bars->p_ready[t], 128);
+            ptx::mbar_init(&bars->o_done[t], 1);
+            ptx::mbar_init(&bars->s_free[t], 128);
+        }
+        ptx::mbar_init(&bars->drain, 1);
+        bars->abort = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == C::W_MMA) {
+        ptx::tmem_alloc(&bars->tmem_base, C::TM_COLS);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    // programmatic dependent launch: the set-up above touches nothing global
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+
+    if (warp >= C::NSOFT) {
+        ptx::regs_decrease<C::REGS_OTHER>();
+        if ((warp == C::W_LOAD || warp == C::W_LOADV) && lane == 0) {
+            // ============================================= TMA loaders: one
+            // thread streams Q and the K ring, another the V ring
+            const int which = warp == C::W_LOAD ? 0 : 1;
+            const CUtensorMap *tm = which == 0 ? &tk : &tv;
+            uint64_t *full = which == 0 ? bars->k_full : bars->v_full;
+            uint64_t *empty = which == 0 ? bars->k_empty : bars->v_empty;
+            const int NS = which == 0 ? C::KS : C::VS;   // depth of this ring
+            const Item w = get_item(p);
+            ptx::prefetch_tmap(tm);
+            const uint64_t pol_kv = ptx::l2_policy_evict_last();
+            if (which == 0 && w.steps > 0) {
+                ptx::prefetch_tmap(&tq);
+                const uint64_t pol_q = ptx::l2_policy_evict_first();
+                const int tiles = w.n[1] > 0 ? kNQ : 1;
+                ptx::mbar_arrive_expect_tx(&bars->q_full, tiles * C::Q_BYTES);
+                for (int t = 0; t < tiles; ++t)
+                    for (int pn = 0; pn < C::PANELS; ++pn)
+                        ptx::tma_load_4d(smem + C::OFF_Q + t * C::Q_BYTES + pn * C::PANEL_Q, &tq, pn * 64,
+                                         w.q0 + t * w.dq, w.fh + t * w.dh, w.fb, &bars->q_full, pol_q);
+            }
+            int issued = 0;
+            for (int j = 0; j < w.steps; ++j) {
+                const int s = j % NS;
+                if (j >= NS && !ptx::mbar_wait_or_abort(&empty[s], ((j / NS) - 1) & 1, p.err, abort)) break;
+                issued = j + 1;
+                ptx::mbar_arrive_expect_tx(&full[s], C::KV_BYTES);
+                for (int pn = 0; pn < C::PANELS; ++pn)
+                    ptx::tma_load_4d(smem + (which == 0 ? C::k_off(s) : C::v_off(s)) + pn * C::PANEL_KV, tm,
+                                     pn * 64, w.tile(j) * kBN, w.fkh, w.fb, &full[s], pol_kv);
+            }
+            // after a timeout elsewhere: let the copies this thread issued land
+            // (bounded) before the CTA's shared memory is released
+            if (*abort) {
+                if (which == 0 && w.steps > 0) ptx::mbar_wait(&bars->q_full, 0, nullptr);
+                for (int j = imax(0, issued - NS); j < issued; ++j)
+                    ptx::mbar_wait(&full[j % NS], (j / NS) & 1, nullptr);
+            }
+        } else if (warp == C::W_MMA && lane == 0) {
+            // ============================================= MMA issuer
+            const uint32_t id_qk = ptx::idesc_16_f32(kBM, BNt, false, F16);
+            const uint32_t id_pv = ptx::idesc_16_f32(kBM, D, true, F16);
+            // descriptors are built once; a k-step, a stage or a tile only moves
+            // the start-address field
+            constexpr uint32_t HI128 = ptx::desc_hi_sw128(1024);
+            const uint32_t dq0 = ptx::desc_lo_sw128(ptx::smem_addr(smem + C::OFF_Q), 16);
+            const uint32_t dk0 = ptx::desc_lo_sw128(ptx::smem_addr(smem + C::k_off(0)), 16);
+            const uint32_t dv0 = ptx::desc_lo_sw128(ptx::smem_addr(smem + C::v_off(0)), C::PANEL_KV);
+            constexpr int nkv = BNt / 16;                // k-steps of P V
+            auto issue_qk = [&](int t, int gk) {
+                const uint32_t a0 = dq0 + uint32_t((t * C::Q_BYTES) >> 4);
+                const uint32_t b0 = dk0 + uint32_t(((gk % C::KS) * C::KV_BYTES) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t oa = ((kk >> 2) * C::PANEL_Q + (kk & 3) * 32) >> 4;
+                    const uint32_t ob = ((kk >> 2) * C::PANEL_KV + (kk & 3) * 32) >> 4;
+                    ptx::mma_ss(tmem + C::tm_s(t), ptx::desc_join(a0 + oa, HI128),
+                                ptx::desc_join(b0 + ob, HI128), id_qk, kk > 0);
+                }
+                ptx::tc_commit(&bars->s_full[t]);
+            };
+            auto issue_pv = [&](int t, int gv, bool first) {
+                const uint32_t b0 = dv0 + uint32_t(((gv % C::VS) * C::KV_BYTES) >> 4);
+                const uint32_t a0 = tmem + C::tm_p(t);
+#pragma unroll
+                for (int kk = 0; kk < nkv; ++kk)
+                    ptx::mma_ts(tmem + C::tm_o(t), a0 + kk * 8,
+                                ptx::desc_join(b0 + uint32_t(kk * (2048 >> 4)), HI128), id_pv,
+                                (!first || kk > 0) ? 1u : 0u);
+                ptx::tc_commit(&bars->o_done[t]);
+            };
+            const Item w = get_item(p);
+            bool ok = w.steps > 0, k_seen = false, v_seen = false;
+            // a stage barrier is waited on once per step (a completed wait still
+            // costs this thread a round trip to shared memory)
+            auto wait_k = [&](int j) {
+                if (!k_seen) {
+                    ok = ok && ptx::mbar_wait_or_abort(&bars->k_full[j % C::KS], (j / C::KS) & 1, p.err, abort);
+                    k_seen = true;
+                }
+            };
+            auto wait_v = [&](int j) {
+                if (!v_seen) {
+                    ok = ok && ptx::mbar_wait_or_abort(&bars->v_full[j % C::VS], (j / C::VS) & 1, p.err, abort);
+                    v_seen = true;
+                }
+            };
+            // Q K^T of step j for tile t, once the softmax no longer needs the S it
+            // overwrites (separate P: as soon as the softmax holds the S before in
+            // registers; P over S: after the P V before, issued already)
+            auto qk = [&](int t, int j) {
+                wait_k(j);
+                if (j >= w.n[t] || j < w.f[t]) return;
+                if (C::SEP_P && j > w.f[t])
+                    ok = ok && ptx::mbar_wait_or_abort(&bars->s_free[t], (j - 1 - w.f[t]) & 1, p.err, abort);
+                if (!ok) return;
+                ptx::tc_fence_after();
+                issue_qk(t, j);
+            };
+            // P V of step j for tile t
+            auto pv = [&](int t, int j) {
+                wait_v(j);
+                if (j >= w.n[t] || j < w.f[t]) return;
+                ok = ok && ptx::mbar_wait_or_abort(&bars->p_ready[t], (j - w.f[t]) & 1, p.err, abort);
+                if (!ok) return;
+                ptx::tc_fence_after();
+                issue_pv(t, j, j == w.f[t]);
+            };
+            ok = ok && ptx::mbar_wait_or_abort(&bars->q_full, 0, p.err, abort);
+#pragma unroll
+            for (int t = 0; t < kNQ; ++t)
+                if (ok) qk(t, 0);
+            if (ok) ptx::tc_commit(&bars->k_empty[0]);
+            for (int j = 0; ok && j < w.steps; ++j) {
+                const int jn = j + 1;
+                k_seen = v_seen = false;
+                if constexpr (C::SEP_P) {
+#pragma unroll
+                    for (int t = 0; t < kNQ; ++t)
+                        if (ok && jn < w.steps) qk(t, jn);
+#pragma unroll
+                    for (int t = 0; t < kNQ; ++t)
+                        if (ok) pv(t, j);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < kNQ; ++t) {
+                        if (ok) pv(t, j);
+                        if (ok && jn < w.steps) qk(t, jn);
+                    }
+                }
+                if (!ok) break;
+                if (jn < w.steps) ptx::tc_commit(&bars->k_empty[jn % C::KS]);
+                ptx::tc_commit(&bars->v_empty[j % C::VS]);
+            }
+            // drain: every MMA has completed before TMEM is freed
+            ptx::tc_commit(&bars->drain);
+            ptx::mbar_wait(&bars->drain, 0, p.err);
+        }
+    } else {
+        // ================================================= softmax warpgroups
+        ptx::regs_increase<C::REGS_SOFTMAX>();
+        const int t = warp >> 2;                 // query tile
+        const int quarter = warp & 3;            // TMEM lanes [32 quarter, 32 quarter + 32)
+        const int row = quarter * 32 + lane;     // query row within the tile
+        const uint32_t lane_base = tmem + (uint32_t(quarter * 32) << 16);
+        const uint32_t o_addr = lane_base + C::tm_o(t);
+        const uint32_t s_addr = lane_base + C::tm_s(t);
+        const uint32_t p_addr = lane_base + C::tm_p(t);
+        const float cl = p.c_log2;
+        bool ok = true;
+        const Item w = get_item(p);
+        const int f = pick(w.f, t), nt = pick(w.n, t) - f;   // this query tile's key tiles
+        const int pos = p.off + w.q0 + w.dq * t;             // position of its first row
+
+        // waits for the P V product of key tile jj of this query tile (and so
+        // for every earlier one: one thread's MMAs complete in issue order)
+        auto wait_pv = [&](int jj) -> bool {
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&bars->o_done[t], jj & 1, p.err, abort)))
+                return false;
+            ptx::tc_fence_after();
+            return true;
+        };
+
+        float m = -INFINITY, l = 0.f;
+        for (int j = 0; j < nt; ++j) {
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&bars->s_full[t], j & 1, p.err, abort))) {
+                ok = false;
+                break;
+            }
+            ptx::tc_fence_after();
+
+            float sv[BNt];
+#pragma unroll
+            for (int c = 0; c < BNt / 32; ++c)
+                ptx::tmem_ld32(s_addr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[c * 32]));
+            ptx::tmem_wait_ld();
+            if constexpr (C::SEP_P) {
+                // S_t is in registers: the next QK_t may overwrite it
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&bars->s_free[t]);
+            }
+
+            // ---- masks: rows at positions pos + row; only tiles on an edge of
+            //      the window are masked per element
+            {
+                const int k0 = w.tile(f + j) * BNt;
+                const bool late = k0 + BNt - 1 > pos;                    // a key behind the first row
+                const bool early = k0 + p.window < pos + kBM;            // one before the last row's window
+                if (late || (early && k0 + BNt > p.sinks)) {
+                    // key e of the tile is seen iff e <= hi and (e >= lo or e < sk);
+                    // all but tiny windows need only one bound per tile: the
+                    // diagonal's, the end of the sinks, or the window's start
+                    const int hi = pos + row - k0, lo = hi - p.window + 1, sk = p.sinks - k0;
+                    if (!early || (!late && k0 + p.window + BNt <= pos + 1)) {
+                        const int last = early ? sk - 1 : hi;
+#pragma unroll
+                        for (int e = 0; e < BNt; ++e)
+                            if (e > last) sv[e] = -INFINITY;
+                    } else if (!late && sk <= 0) {
+#pragma unroll
+                        for (int e = 0; e < BNt; ++e)
+                            if (e < lo) sv[e] = -INFINITY;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < BNt; ++e)
+                            if (e > hi || (e < lo && e >= sk)) sv[e] = -INFINITY;
+                    }
+                }
+            }
+
+            // P = 2^(x - m) in 16-bit into TMEM; returns the tile's row sum (fp32)
+            auto emit_p = [&](float nmu) -> float {
+                float acc[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+#pragma unroll
+                for (int c = 0; c < BNt / 32; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float x0, x1;
+                        ptx::ffma2(x0, x1, sv[c * 32 + 2 * e], sv[c * 32 + 2 * e + 1], cl, cl, nmu, nmu);
+                        const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+                        ptx::fadd2(acc[(2 * e) & 7], acc[(2 * e + 1) & 7], acc[(2 * e) & 7],
+                                   acc[(2 * e + 1) & 7], p0, p1);
+                        pk[e] = H16<F16>::pack(p0, p1);
+                    }
+                    ptx::tmem_st16(p_addr + c * 16, pk);
+                }
+                return ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+            };
+
+            // ---- P in columns of its own: the P V product that last read them
+            //      (key tile j - 1) must be done.  P over S needs no wait: the
+            //      Q K^T that wrote this S was issued after the P V that read the
+            //      P last held here, and MMAs complete in issue order.
+            bool prev_done = false;              // P V of tile j - 1 observed complete
+            if (C::SEP_P && j >= 1) {
+                if (!wait_pv(j - 1)) {
+                    ok = false;
+                    break;
+                }
+                prev_done = true;
+            }
+
+            // ---- fast path: exponentiate against the running maximum m as it
+            //      stands, with no tile maximum.  P only has to stay finite in its
+            //      16-bit type, not below 1: a tile whose row sum exceeds 2^24 (2^15
+            //      for f16, whose largest finite value is 65504) or is not finite
+            //      is redone below against its own maximum.  After the first tiles
+            //      m is close to the row maximum and the redo almost never runs.
+            bool fast = j > 0 && __all_sync(0xffffffffu, m != -INFINITY);
+            if (fast) {
+                const float lt = emit_p(-m);
+                if (__any_sync(0xffffffffu, !(lt <= (F16 ? 32768.f : 16777216.f))))
+                    fast = false;                 // redo the tile (P is rewritten below)
+                else
+                    l += lt;
+            }
+
+            if (!fast) {
+                // ---- tile maximum
+                float mx[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < BNt; e += 8) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) mx[i] = fmaxf(mx[i], sv[e + i]);
+                }
+                const float tmax = fmaxf(ptx::fmax3(ptx::fmax3(mx[0], mx[1], mx[2]), ptx::fmax3(mx[3], mx[4], mx[5]),
+                                                    mx[6]),
+                                         mx[7]);
+                const float mt = tmax * cl;      // cl > 0: max commutes with the scaling
+
+                // ---- the previous P V must be done before O is rescaled
+                const bool want = j == 0 || mt > m + 8.f;   // this row moves its maximum
+                const bool any_want = __any_sync(0xffffffffu, want);
+                if (j > 0 && any_want && !prev_done) {
+                    if (!wait_pv(j - 1)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                // ---- running maximum (moved lazily) and O rescale in TMEM
+                if (j == 0) {
+                    m = mt;
+                } else if (any_want) {
+                    // rows that move m scale their O row; the others multiply by 1
+                    const float f = want ? ptx::ex2(m - mt) : 1.f;   // m == -inf -> 0
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t ov[32];
+                        ptx::tmem_ld32(o_addr + c * 32, ov);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float a0, a1;
+                            ptx::ffma2(a0, a1, __uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), f,
+                                       f, 0.f, 0.f);
+                            ov[e] = __float_as_uint(a0);
+                            ov[e + 1] = __float_as_uint(a1);
+                        }
+                        ptx::tmem_st32(o_addr + c * 32, ov);
+                    }
+                    if (want) {
+                        l *= f;
+                        m = mt;
+                    }
+                }
+                l += emit_p((m == -INFINITY) ? 0.f : -m);
+            }
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&bars->p_ready[t]);
+        }
+
+
+        // ---- epilogue: O / l -> 16-bit -> global
+        if (ok && nt > 0 && wait_pv(nt - 1)) {
+            const float inv = 1.f / l;
+            const int qi = w.q0 + t * w.dq + row, qh = w.fh + t * w.dh;
+            const bool qvalid = qi < p.Nq;
+            bool finite = true;
+            typename H16<F16>::T *orow = nullptr;
+            if (qvalid)
+                orow = static_cast<typename H16<F16>::T *>(p.o) +
+                       size_t(w.fb * p.o_sb + qh * p.o_sh + (long long)qi * p.o_sn);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t ov[32];
+                ptx::tmem_ld32(o_addr + c * 32, ov);
+                ptx::tmem_wait_ld();
+                if (qvalid) {
+                    uint4 w4[4];
+                    uint32_t *wp = reinterpret_cast<uint32_t *>(w4);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        wp[e] = H16<F16>::pack(__uint_as_float(ov[2 * e]) * inv,
+                                               __uint_as_float(ov[2 * e + 1]) * inv);
+                    uint4 *dst = reinterpret_cast<uint4 *>(orow + c * 32);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dst[e] = w4[e];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        finite = finite && fabsf(__uint_as_float(ov[e]) * inv) < INFINITY;
+                }
+            }
+            unsigned redo = __ballot_sync(0xffffffffu, !finite);
+            while (redo) {
+                const int r = __ffs(redo) - 1;
+                redo &= redo - 1;
+                __syncwarp();
+                window_row<D, F16>(p, w.fb, qh, w.fkh, w.q0 + t * w.dq + quarter * 32 + r);
+            }
+        }
+    }
+
+    // ---- teardown: all TMEM traffic done before the owner warp frees it
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == C::W_MMA) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, C::TM_COLS);
+    }
+}
+
+template <int D, bool F16>
+attn_status_t launch_window(const Ctx &c, const CUtensorMap &tq, const CUtensorMap &tk,
+                            const CUtensorMap &tv, const WnParams &p) {
+    using C = WnCfg<D>;
+    static int done_mask = 0;
+    static int regs = -1;
+    auto kern = tc_window_kernel<D, F16>;
+    if (!ensure_smem_attr(reinterpret_cast<const void *>(kern), C::SMEM, c.device, &done_mask))
+        return ATTN_ERR_RESOURCE;
+    // the setmaxnreg split is only valid for the per-thread count it was computed for
+    if (regs < 0) {
+        cudaFuncAttributes fa;
+        if (cudaFuncGetAttributes(&fa, reinterpret_cast<const void *>(kern)) != cudaSuccess) {
+            cudaGetLastError();
+            return ATTN_ERR_CUDA;
+        }
+        regs = fa.numRegs;
+    }
+    if (regs != C::REGS_LAUNCH) return ATTN_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.pairs / p.G * p.G + 2 * (p.pairs % p.G));
+    cfg.blockDim = dim3(C::NT);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = c.stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p) != cudaSuccess) {
+        cudaGetLastError();
+        return ATTN_ERR_CUDA;
+    }
+    return launch_status(kFamTcFlash);
+}
+
+}  // namespace
+
+attn_status_t tc_causal_window(const Ctx &c, attn_dtype_t dt, const void *q, const void *k,
+                               const void *v, void *o, int B, int Hq, int Hkv, int Nq, int Nkv,
+                               int D, int window, int sinks, float scale, const TensorStrides *st) {
+    const bool f16 = dt == ATTN_F16;
+    // Two heads of a KV head make a pair with one key range: no step for one
+    // tile alone, and 128-row blocks.  An odd group pairs row tiles instead.
+    const bool by_head = (Hq / Hkv) % 2 == 0;
+    const long long pairs = by_head ? (long long)cdiv(Nq, kBM) * (B * Hq / 2)
+                                    : (long long)cdiv(Nq, kNQ * kBM) * B * Hq;
+    if (pairs > (1 << 29)) return ATTN_ERR_UNSUPPORTED;
+    CUtensorMap tq, tk, tv;
+    // a layout the tensor-map encoder refuses goes to the strided SIMT kernel
+    if (!make_tmap4(&tq, q, D, Nq, Hq, B, st[0], f16) || !make_tmap4(&tk, k, D, Nkv, Hkv, B, st[1], f16) ||
+        !make_tmap4(&tv, v, D, Nkv, Hkv, B, st[2], f16))
+        return ATTN_ERR_UNSUPPORTED;
+    WnParams p{};
+    p.Nq = Nq;
+    p.Nkv = Nkv;
+    p.off = Nkv - Nq;
+    p.window = window;
+    p.sinks = sinks;
+    p.c_log2 = scale * kLog2e;
+    p.err = c.err;
+    p.H = Hq;
+    p.group = Hq / Hkv;
+    p.BH = B * Hq;
+    p.pairs = int(pairs);
+    p.by_head = by_head;
+    p.G = imax(1, c.sm_count);
+    p.q = q; p.k = k; p.v = v; p.o = o;
+    p.sq = st[0]; p.sk = st[1]; p.sv = st[2];
+    p.o_sb = st[3].b; p.o_sh = st[3].h; p.o_sn = st[3].n;
+    if (D == 128)
+        return f16 ? launch_window<128, true>(c, tq, tk, tv, p) : launch_window<128, false>(c, tq, tk, tv, p);
+    return f16 ? launch_window<64, true>(c, tq, tk, tv, p) : launch_window<64, false>(c, tq, tk, tv, p);
+}
+
+}  // namespace attn
