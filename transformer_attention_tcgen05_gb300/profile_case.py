@@ -12,6 +12,10 @@ KERNEL is one of:
           (attn_decode_gqa)
   causal  causal GQA prefill, B 1, 32 query / 8 KV heads, 4096 tokens, D 128
           (attn_causal_gqa_fwd)
+  window  the causal case with a sliding window of 1024 and 4 sinks
+          (attn_causal_gqa_window_fwd)
+  decode_paged  the decode case over scattered pages of 16 tokens
+          (attn_decode_gqa_paged)
 
 The inputs are the benchmark's seeded bf16 draws.  W untimed launches run
 first, then N more; the process exits non-zero if the device reports an
@@ -70,12 +74,37 @@ def build_case(kernel: str, frames: int, dev):
         v = torch.randn(1, 8, 4096, 128, generator=g).bfloat16().to(dev)
         o = torch.empty_like(q)
         return lambda: ta.causal_gqa_fwd(q, k, v, o=o)
+    if kernel == "window":
+        g = torch.Generator(device="cpu").manual_seed(1007)
+        q = torch.randn(1, 32, 4096, 128, generator=g).bfloat16().to(dev)
+        k = torch.randn(1, 8, 4096, 128, generator=g).bfloat16().to(dev)
+        v = torch.randn(1, 8, 4096, 128, generator=g).bfloat16().to(dev)
+        o = torch.empty_like(q)
+        return lambda: ta.causal_gqa_window_fwd(q, k, v, 1024, 4, o=o)
+    if kernel == "decode_paged":
+        w, S = WORKLOADS["gqa_decode"], 16
+        h = make_inputs(w)
+        q = _dev(h["q"], dev)
+        # [B, Hkv, L, D] rows dealt out to pages in a scattered order
+        perm = torch.randperm(w.B * w.Lmax // S, generator=torch.Generator().manual_seed(1008))
+        pages = []
+        for n in "kv":
+            x = _dev(h[n], dev).view(w.B, w.Hkv, w.Lmax // S, S, w.D).transpose(1, 2).flatten(0, 1)
+            y = torch.empty_like(x)
+            y[perm.to(dev)] = x
+            pages.append(y)
+        table = perm.view(w.B, w.Lmax // S).int().to(dev)
+        sl = torch.from_numpy(h["seq_len"]).to(dev)
+        o = torch.empty_like(q)
+        ws = torch.zeros(ta.decode_paged_workspace_bytes(w.B, w.H, w.Hkv, w.D), dtype=torch.uint8,
+                         device=dev)
+        return lambda: ta.decode_gqa_paged(q, *pages, table, sl, o=o, workspace=ws)
     raise SystemExit(f"unknown kernel {kernel!r}")
 
 
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
-    ap.add_argument("kernel", choices=["joint", "na3d", "decode", "causal"])
+    ap.add_argument("kernel", choices=["joint", "na3d", "decode", "causal", "window", "decode_paged"])
     ap.add_argument("--frames", type=int, default=0, help="na3d: T extent (default 21)")
     ap.add_argument("--warmup", type=int, default=2)
     ap.add_argument("--launches", type=int, default=1)
