@@ -3,8 +3,8 @@
 //
 // Query i sits at position p = off + i and sees the keys j <= p with
 // j > p - window or j < sinks.  One CTA owns 32 query rows of one (batch, head)
-// and streams the key tiles (64 keys) that hold a key one of them sees: the
-// sinks, then the window.
+// and streams the keys that one of them sees, the sinks and the window, as one
+// list in tiles of 64.
 //
 // Both products are register-tiled: a thread holds 4 rows x 4 keys of S and 4
 // rows x D / 16 channels of O, so that 8 shared-memory vectors feed 64 FMAs
@@ -12,13 +12,16 @@
 // entries use reads one vector per 4 FMAs and has a quarter of the warps.
 // Bound by the FMA pipe and, for short prompts, by latency: 32-row tiles give a
 // 515-token prompt of 16 heads 272 CTAs (B 2, 8 heads on 2 KV heads, D 64,
-// window 128, sinks 4: 27.9 us, 57 us in the one-row-per-thread form; 2048
-// tokens, 8 heads, D 128, window 512: 229 us = 16.6 TFLOP/s, was 334 us).
+// window 128, sinks 4: 21.8 us, 57 us in the one-row-per-thread form; 2048
+// tokens, 8 heads, D 128, window 512: 188 us = 20.2 TFLOP/s, was 334 us).
+// Sinks and window as two runs of tiles cost one tile more (27.9 us), synchronous
+// copies 22.9 us.
 //
 // Every product is an fp32 FMA (never TF32), statistics and sums are fp32 and
 // the output is rounded once.  A key that a row does not see never enters the
-// row's sums, whatever its value holds: its weight is marked negative and left
-// out of the P V product on the tiles that are masked at all.
+// row's sums, whatever its value holds: on a masked tile that holds an infinite
+// or NaN value (noticed when it is loaded) its weight is left out of the P V
+// product instead of multiplying by zero.
 #include <math.h>
 
 #include "common.cuh"
@@ -59,6 +62,18 @@ template <> __device__ __forceinline__ float4 load4<__half>(const __half *p) {
     const uint2 u = *reinterpret_cast<const uint2 *>(p);
     return make_float4(f16_lo(u.x), f16_hi(u.x), f16_lo(u.y), f16_hi(u.y));
 }
+
+// 16 bytes global -> shared without passing registers; src is read only if `take`
+// (zeros otherwise).
+__device__ __forceinline__ void cp_async16(float *dst, const void *src, bool take) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(take ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// waits until at most one group of this thread is outstanding
+__device__ __forceinline__ void cp_wait1() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 
 // Thread (ty, tx) = (tid / 16, tid % 16): rows 4 ty + i, keys tx + 16 c,
 // channels tx * D / 16 + e.
@@ -102,21 +117,33 @@ __global__ void __launch_bounds__(kThreads) simt_window_kernel(const WinParams p
         for (int e = 0; e < CH; ++e) acc[i][e] = 0.f;
     }
 
-    int kb = sink1 > 0 ? 0 : win0;
-    while (kb < end) {
-        __syncthreads();                               // the tile before has been read
-        // (not unrolled further: 8 vectors of K and V in flight per thread)
+    // key u of the list: the sinks before the window, then the window
+    const int total = sink1 + end - win0;
+    auto key_of = [&](int u) { return u < sink1 ? u : u - sink1 + win0; };
+    // One tile of K or V.  fp32 goes to shared memory asynchronously: the next
+    // K while this tile's P V runs, the next V while the next S does.
+    auto stage = [&](float *dst, const T *base, long long sn, int kb) {
+        const int keys = imin(kBN, total - kb);
 #pragma unroll 4
         for (int e = tid; e < kBN * D / 4; e += kThreads) {
             const int r = (e * 4) / D, d = (e * 4) % D;
-            float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
-            if (kb + r < end) {
-                kx = load4<T>(kg + (kb + r) * p.sk.n + d);
-                vx = load4<T>(vg + (kb + r) * p.sv.n + d);
+            const bool in = r < keys;
+            const T *src = base + (in ? key_of(kb + r) * sn + d : 0);
+            if constexpr (sizeof(T) == 4) {
+                cp_async16(dst + r * S::LD + d, src, in);
+            } else {
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (in) x = load4<T>(src);
+                *reinterpret_cast<float4 *>(dst + r * S::LD + d) = x;
             }
-            *reinterpret_cast<float4 *>(Ks + r * S::LD + d) = kx;
-            *reinterpret_cast<float4 *>(Vs + r * S::LD + d) = vx;
         }
+        cp_commit();
+    };
+    stage(Ks, kg, p.sk.n, 0);
+    stage(Vs, vg, p.sv.n, 0);
+    for (int kb = 0; kb < total; kb += kBN) {
+        const int keys = imin(kBN, total - kb);
+        cp_wait1();                                    // K is here
         __syncthreads();
 
         // ---- S: 4 rows x 4 keys per thread
@@ -143,10 +170,26 @@ __global__ void __launch_bounds__(kThreads) simt_window_kernel(const WinParams p
                 }
         }
 
-        // ---- masks (the tile is inside every row's window or among the sinks,
-        //      or it is tested key by key) and online softmax
-        const bool edge = kb + kBN - 1 > pos0 ||
-                          (kb < pos0 + kBM - p.window && kb + kBN > p.sinks);
+        __syncthreads();                               // K has been read
+        if (kb + kBN < total)
+            stage(Ks, kg, p.sk.n, kb + kBN);
+        else
+            cp_commit();
+        cp_wait1();                                    // V is here
+        int wild = 0;                                  // an infinite or NaN value in the tile
+#pragma unroll 4
+        for (int e = tid; e < kBN * D / 4; e += kThreads) {
+            const float4 v = *reinterpret_cast<const float4 *>(Vs + (e * 4) / D * S::LD + (e * 4) % D);
+            wild |= !(fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY && fabsf(v.z) < INFINITY &&
+                      fabsf(v.w) < INFINITY);
+        }
+        wild = __syncthreads_or(wild);
+
+        // ---- masks (every row sees the whole tile, or it is tested key by key)
+        //      and online softmax
+        const int k_first = key_of(kb), k_last = key_of(kb + keys - 1);
+        const bool edge = keys < kBN || k_last > pos0 ||
+                          (k_first <= pos0 + kBM - 1 - p.window && k_last >= p.sinks);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int pos = pos0 + 4 * ty + i;
@@ -155,8 +198,8 @@ __global__ void __launch_bounds__(kThreads) simt_window_kernel(const WinParams p
                 seen = 0;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const int key = kb + tx + 16 * c;
-                    const bool ok = key <= pos && key < end && (key > pos - p.window || key < p.sinks);
+                    const int u = tx + 16 * c, key = key_of(kb + u);
+                    const bool ok = u < keys && key <= pos && (key > pos - p.window || key < p.sinks);
                     seen |= unsigned(ok) << c;
                     if (!ok) s[i][c] = -INFINITY;
                 }
@@ -174,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) simt_window_kernel(const WinParams p
                 // no finite score yet: -inf weighs nothing, NaN stays NaN
                 const float w = mn == -INFINITY && s[i][c] == -INFINITY ? 0.f : exp2f(s[i][c] - mn);
                 if (ok) sum += w;
-                s[i][c] = ok ? w : -1.f;
+                s[i][c] = ok ? w : (wild ? -1.f : 0.f);
             }
 #pragma unroll
             for (int off = 1; off < 16; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -190,9 +233,8 @@ __global__ void __launch_bounds__(kThreads) simt_window_kernel(const WinParams p
         __syncwarp();
 
         // ---- O += P V
-        const int keys = imin(kBN, end - kb);
-        if (edge) {
-#pragma unroll 2
+        if (edge && wild) {
+#pragma unroll 1
             for (int c = 0; c < keys; ++c) {
                 const float4 w = *reinterpret_cast<const float4 *>(Ps + c * S::LP + 4 * ty);
                 const float wv[4] = {w.x, w.y, w.z, w.w};
@@ -206,7 +248,7 @@ __global__ void __launch_bounds__(kThreads) simt_window_kernel(const WinParams p
             }
         } else {
 #pragma unroll 4
-            for (int c = 0; c < kBN; ++c) {
+            for (int c = 0; c < keys; ++c) {
                 const float4 w = *reinterpret_cast<const float4 *>(Ps + c * S::LP + 4 * ty);
                 float v[CH];
                 if constexpr (CH == 2) {
@@ -232,8 +274,11 @@ __global__ void __launch_bounds__(kThreads) simt_window_kernel(const WinParams p
                 }
             }
         }
-        kb += kBN;
-        if (kb >= sink1) kb = imax(kb, win0);          // past the sinks: on to the window
+        __syncthreads();                               // V has been read
+        if (kb + kBN < total)
+            stage(Vs, vg, p.sv.n, kb + kBN);
+        else
+            cp_commit();
     }
 
 #pragma unroll
