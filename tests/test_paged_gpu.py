@@ -106,6 +106,9 @@ CASES = [
     ("f16", [250, 1, 0, 33, 64, 0] * 50, 12, 4, 64, 8, 0, 0, "token"),
     ("bf16", [900, 40, 0, 129] * 30, 27, 3, 128, 48, 100, 20, "head"),
     ("bf16", [1200, 300, 700] * 12, 8, 4, 64, 16, 0, 0, "head"),   # ranges that end inside units
+    ("bf16", [3000, 1, 0, 40, 257, 256, 7], 8, 8, 64, 16, 0, 0, "head"),   # short units beside long ones
+    ("f16", ([1] * 40 + [900, 0]) * 4, 4, 2, 128, 32, 0, 0, "token"),
+    ("bf16", [5000, 3] + [300, 64] * 30, 3, 3, 64, 8, 200, 10, "head"),
 ]
 
 

@@ -21,8 +21,10 @@
 //    partials in CTA order, so the result does not depend on who is last.
 //    (Drawing the tickets of a range's cut units only at its end, so that the
 //    next unit need not wait, measured 1 us slower: 8 x 4096 tokens 28.1 us.)
-//  * Many short units (more units than CTAs, none longer than 8 chunks) are
-//    dealt out whole, warp by warp: no joining, no barrier.
+//  * Short units (up to 8 chunks) beside long ones, or more of them than CTAs,
+//    are dealt out whole, warp by warp, to a share of the CTAs that their work
+//    deserves: no joining, no barrier.  (In the list of the long ones each
+//    would cost its CTA a merge of four warps, 1.3 us, for a chunk or two.)
 //  * Every warp streams chunks of its own (chunk f of the range goes to warp
 //    f % CW) into shared memory of its own with TMA: a box of up to 32 rows x D
 //    channels per copy, the page and the KV head being coordinates of one 5D
@@ -102,11 +104,11 @@ struct PgParams {
 };
 
 constexpr int kMaxWarps = 4;
-constexpr int kWarpUnit = 8;      // longest unit (chunks) that one warp takes alone
+constexpr int kWarpUnit = 8;      // longest unit (chunks) that counts as short
 
 struct Misc {
     uint64_t full_k[kMaxWarps * 2], full_v[kMaxWarps * 2];   // [warp][slot]
-    int warp_sum[kMaxWarps];
+    int warp_long[kMaxWarps], warp_short[kMaxWarps];
     int warp_max[kMaxWarps], warp_units[kMaxWarps];
     // where the CTA's range, or each warp's (and the one behind), starts
     int start_flat[kMaxWarps + 1];
@@ -144,6 +146,13 @@ __device__ __forceinline__ int div_s(const PgParams &p, int n) {
     return int((t + ((unsigned(n) - t) >> 1)) >> p.s_sh);
 }
 
+// The plan of a sequence if it belongs to the list of the short (or long) ones.
+__device__ __forceinline__ Plan plan_in(const PgParams &p, int len, bool in_short) {
+    Plan r = make_plan(p, len);
+    if ((r.n <= kWarpUnit) != in_short) r.n = 0;
+    return r;
+}
+
 __device__ __forceinline__ int chunk_of(const Plan &r, int v) {
     return v < r.n1 ? v : v - r.n1 + r.c2;
 }
@@ -151,6 +160,7 @@ __device__ __forceinline__ int chunk_of(const Plan &r, int v) {
 // One CTA's range of the flat chunk list, a segment (part of one unit) at a time.
 struct Walk {
     const PgParams &p;
+    bool in_short;                         // the list: short or long units
     Plan plan;
     int b, kvh, v0, cnt;
     int left;                              // chunks of the range from this segment on
@@ -158,8 +168,8 @@ struct Walk {
 
     int ahead;                             // seq_len[b + 1], loaded before it is needed
 
-    __device__ Walk(const PgParams &pp, int b0, int len0, int kvh0, int v, int f0, int count)
-        : p(pp), b(b0), kvh(kvh0), v0(v), left(count), flat(f0) {
+    __device__ Walk(const PgParams &pp, bool list, int b0, int len0, int kvh0, int v, int f0, int count)
+        : p(pp), in_short(list), b(b0), kvh(kvh0), v0(v), left(count), flat(f0) {
         plan = make_plan(p, len0);
         ahead = b + 1 < p.B ? p.seq_len[b + 1] : 0;
         if (kvh == p.Hkv) next_sequence();
@@ -168,7 +178,7 @@ struct Walk {
     __device__ void next_sequence() {       // the range ends inside the list: b stays below B
         kvh = 0;
         do {
-            plan = make_plan(p, ahead);
+            plan = plan_in(p, ahead, in_short);
             ++b;
             ahead = b + 1 < p.B ? p.seq_len[b + 1] : 0;
         } while (plan.n == 0);
@@ -260,19 +270,23 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
 
-    // ---- the flat list's length, this CTA's range and where it starts.
+    // ---- the lists' lengths, this CTA's range and where it starts.
     //      Sequences with nothing to attend to are dealt out over the CTAs:
     //      length 0 writes zeros, a length outside the table is reported and
     //      its output left as it was.
     const bool one_tile = p.B <= kNT;                  // a thread per sequence: read once
-    int inc = 0, n_mine = 0, len_mine = 0, n_max = 0, units = 0;
+    int inc_l = 0, inc_s = 0, n_mine = 0, len_mine = 0, n_max = 0, units = 0;
 #pragma unroll 1
     for (int b = threadIdx.x; b < p.B; b += kNT) {
         len_mine = p.seq_len[b];
         n_mine = make_plan(p, len_mine).n;
-        inc += n_mine;
         n_max = imax(n_max, n_mine);
-        units += n_mine > 0;
+        if (n_mine <= kWarpUnit) {
+            inc_s += n_mine;
+            units += n_mine > 0;
+        } else {
+            inc_l += n_mine;
+        }
         if (n_mine == 0 && b % ctas == cta) {
             if (len_mine != 0) raise_device_error(p.err, kDevCheck);
 #pragma unroll 1
@@ -283,36 +297,58 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     }
 #pragma unroll 1
     for (int off = 1; off < 32; off <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, inc, off);
-        if (lane >= off) inc += up;
+        const int up_l = __shfl_up_sync(0xffffffffu, inc_l, off), up_s = __shfl_up_sync(0xffffffffu, inc_s, off);
+        if (lane >= off) {
+            inc_l += up_l;
+            inc_s += up_s;
+        }
         n_max = imax(n_max, __shfl_xor_sync(0xffffffffu, n_max, off));
         units += __shfl_xor_sync(0xffffffffu, units, off);
     }
     if (lane == 31) {
-        ms->warp_sum[warp] = inc;
+        ms->warp_long[warp] = inc_l;
+        ms->warp_short[warp] = inc_s;
         ms->warp_max[warp] = n_max;
         ms->warp_units[warp] = units;
     }
     __syncthreads();
-    int total = 0, before = inc - n_mine;              // before: chunks of the sequences ahead (one tile)
+    int total_l = 0, total_s = 0, before_l = inc_l, before_s = inc_s;
     units = 0;
 #pragma unroll
     for (int w = 0; w < CW; ++w) {
-        if (w < warp) before += ms->warp_sum[w];
-        total += ms->warp_sum[w];
+        if (w < warp) {
+            before_l += ms->warp_long[w];
+            before_s += ms->warp_short[w];
+        }
+        total_l += ms->warp_long[w];
+        total_s += ms->warp_short[w];
         n_max = imax(n_max, ms->warp_max[w]);
         units += ms->warp_units[w];
     }
-    total *= p.Hkv;
+    total_l *= p.Hkv;
+    total_s *= p.Hkv;
+    units *= p.Hkv;                                    // of the short list
+    // this CTA's list, its number c among the nc CTAs of that list
+    bool in_short = total_l == 0, alone = in_short && units > ctas;
+    int c = cta, nc = ctas;
+    if (total_l > 0 && total_s > 0) {
+        const float cost = float(total_s) + float(units);   // a unit costs about a chunk more
+        const int ns = imax(1, imin(ctas - 1, int(ctas * (cost / (cost + float(total_l)))) + 1));
+        in_short = alone = cta >= ctas - ns;
+        nc = in_short ? ns : ctas - ns;
+        c = in_short ? cta - (ctas - ns) : cta;
+    }
+    const int total = in_short ? total_s : total_l;
+    if ((n_mine <= kWarpUnit) != in_short) n_mine = 0;
+    int before = (in_short ? before_s : before_l) - n_mine;   // chunks of the sequences ahead (one tile)
     // team: the warps that share a range (all of the CTA's, or each its own)
-    const bool alone = n_max <= kWarpUnit && (long long)units * p.Hkv > ctas;
     const int team = alone ? 1 : CW, rank = alone ? 0 : warp;
-    const int teams = alone ? ctas * CW : ctas;
+    const int teams = alone ? nc * CW : nc;
     int per = int((unsigned(total) + teams - 1) / unsigned(teams));
     // at least one chunk per warp, unless every unit is shorter than that: then
     // the units are spread over more CTAs
     if (!alone) per = imax(per, imin(CW, n_max));
-    const long long f0l = (long long)per * (alone ? cta * CW : cta);
+    const long long f0l = (long long)per * (alone ? c * CW : c);
     if (f0l >= total) return;
     const int f0 = int(f0l);
     // boundary i of this CTA: f0, or the first unit that starts at or behind
@@ -350,20 +386,20 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         __syncthreads();
         const int b = b0 + threadIdx.x;
         len_mine = b < p.B ? p.seq_len[b] : 0;
-        n_mine = make_plan(p, len_mine).n;
-        inc = n_mine;
+        n_mine = plan_in(p, len_mine, in_short).n;
+        int inc = n_mine;
 #pragma unroll 1
         for (int off = 1; off < 32; off <<= 1) {
             const int up = __shfl_up_sync(0xffffffffu, inc, off);
             if (lane >= off) inc += up;
         }
-        if (lane == 31) ms->warp_sum[warp] = inc;
+        if (lane == 31) ms->warp_long[warp] = inc;
         __syncthreads();
         before = carry + inc - n_mine;
 #pragma unroll
         for (int w = 0; w < CW; ++w) {
-            if (w < warp) before += ms->warp_sum[w];
-            carry += ms->warp_sum[w];
+            if (w < warp) before += ms->warp_long[w];
+            carry += ms->warp_long[w];
         }
     }
     __syncthreads();
@@ -372,7 +408,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     const int count = alone ? ms->start_flat[warp + 1] - start : imin(per, total - f0);
     if (count <= 0) return;                            // alone: no unit starts in this warp's share
 
-    Walk w(p, ms->start_b[at], ms->start_len[at], ms->start_kvh[at], ms->start_v[at], start, count);
+    Walk w(p, in_short, ms->start_b[at], ms->start_len[at], ms->start_kvh[at], ms->start_v[at], start, count);
     int f = 0;                                         // chunk number within the range
 
     // ---- loads: a walk of its own that runs NS chunks (and a group of page
