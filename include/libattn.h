@@ -365,9 +365,9 @@ ATTN_API attn_status_t attn_kv_append_paged(void *k_pages, void *v_pages, const 
  *   depend on timing.
  *   workspace: DEVICE scratch of attn_decode_gqa_paged_workspace_bytes(...)
  *   bytes, 256-byte aligned, ZERO-FILLED before its first use.  Every call that
- *   completes leaves it ready for the next one with the same B, Hq, Hkv and D
- *   (for other sizes, zero it again or use another).  Calls that share a
- *   workspace must not overlap on the GPU.
+ *   completes leaves it ready for the next one, of any sizes it is large enough
+ *   for.  Calls (and replays of captured ones) that share a workspace must not
+ *   overlap on the GPU.
  * Passage: fak "GPU - the in-kernel forward pass", section 4 (naive decode
  * attention, "no flash/paged attention").
  */

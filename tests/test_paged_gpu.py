@@ -146,6 +146,31 @@ def test_decode_paged_ring_wraps_in_back_to_back_launches(ta, dt, D, S, order, G
     assert all(torch.equal(o, outs[0]) for o in outs)
 
 
+def test_one_workspace_serves_calls_of_several_sizes(ta):
+    sizes = [([2000, 5], 4, 2, 128), ([900] * 9, 16, 1, 64), ([3000], 8, 8, 128), ([70, 800, 9], 27, 3, 128)]
+    ws = torch.zeros(ta.decode_paged_workspace_bytes(9, 64, 8, 128), dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        for i, (lens, Hq, Hkv, D) in enumerate(sizes):
+            q, kp, vp, table, sl, ks, vs = build_case("bf16", lens, Hq, Hkv, D, 16, 0, 0, "head", 30 + i)
+            o = ta.decode_gqa_paged(q, kp, vp, table, sl, workspace=ws)
+            check("bf16", q, ks, vs, lens, o, 0, 0)
+    assert ta.device_status() == 0
+
+
+def test_empty_fork_list_and_zero_rows(ta):
+    table = torch.full((2, 4), -1, dtype=torch.int32, device="cuda")
+    refs, sl = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (8, 2))
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    cs, cd = ta.kv_pages_fork(table, sl, refs, none, none, 8)
+    assert cs.numel() == cd.numel() == 0
+    k = torch.zeros(8, 1, 8, 64, dtype=torch.bfloat16, device="cuda")
+    ta.kv_pages_copy(k, k.clone(), cs, cd)
+    ta.kv_pages_reserve(table, sl, sl, refs, 8)
+    assert ta.device_status() == 0 and (table == -1).all() and (refs == 0).all()
+    with pytest.raises(ta.AttnError):
+        ta.decode_gqa_paged(k[:0, 0, :1], k, k.clone(), table[:0], sl[:0])
+
+
 def test_decode_paged_strided_query_output_and_table(ta):
     lens = [50, 400, 33]
     q, kp, vp, table, sl, ks, vs = build_case("bf16", lens, 6, 2, 64, 16, 0, 0, "head", 4)
@@ -481,12 +506,13 @@ def test_free_reports_pages_that_are_not_counted(ta):
 
 
 def test_compact_drops_entries_of_free_pages(ta):
-    table = torch.tensor([[5, 3, -1, 4, 99]], dtype=torch.int32, device="cuda")
+    # 4 and 1 name free pages (1 below the live count: another page moves there)
+    table = torch.tensor([[5, 3, -1, 4, 99, 1]], dtype=torch.int32, device="cuda")
     refs = torch.tensor([0, 0, 0, 1, 0, 1], dtype=torch.int32, device="cuda")
     cs, cd, n = ta.kv_pages_compact(table, refs)
     assert ta.device_status() == 6
     assert n.item() == 2 and cs.tolist() == [3, 5, -1] and cd.tolist() == [0, 1, -1]
-    assert table.tolist() == [[1, 0, -1, -1, -1]] and refs.tolist() == [1, 1, 0, 0, 0, 0]
+    assert table.tolist() == [[1, 0, -1, -1, -1, -1]] and refs.tolist() == [1, 1, 0, 0, 0, 0]
 
 
 @pytest.mark.parametrize("order", ["head", "token", "packed"])

@@ -381,8 +381,8 @@ def decode_gqa_paged(q, k_pages, v_pages, page_table, seq_len, o=None, scale=Non
     first ``sinks`` tokens are attended to; a sequence of length 0 gives zeros.
 
     ``workspace`` (uint8, decode_paged_workspace_bytes(...) bytes) must be
-    zero-filled before its first use; calls of the same sizes leave it reusable.
-    If omitted a zeroed one is allocated for this call.
+    zero-filled before its first use; calls leave it reusable, for any sizes it
+    is large enough for.  If omitted a zeroed one is allocated for this call.
     """
     return (_native_mod or _native()).decode_gqa_paged(q, k_pages, v_pages, page_table, seq_len, o,
                                                        scale, window, sinks, workspace)

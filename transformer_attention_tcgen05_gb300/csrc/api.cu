@@ -502,7 +502,7 @@ static attn_status_t check_pool(const void *table, int B, int num_pages, int pag
 size_t attn_decode_gqa_paged_workspace_bytes(int B, int Hq, int Hkv, int D) {
     if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > 16 || (D != 64 && D != 128))
         return 0;
-    return decode_paged_workspace_bytes(B, Hq / Hkv, Hkv, D);
+    return decode_paged_workspace_bytes(B, Hkv);
 }
 
 attn_status_t attn_decode_gqa_paged(const void *q, const void *k_pages, const void *v_pages,
@@ -532,7 +532,7 @@ attn_status_t attn_decode_gqa_paged(const void *q, const void *k_pages, const vo
         !row_strides(k_strides, pe, 3, D, dtype, false, a.k_st) ||
         !row_strides(v_strides, pe, 3, D, dtype, false, a.v_st))
         return ATTN_ERR_INVALID_ARG;
-    if (workspace_bytes < decode_paged_workspace_bytes(B, Hq / Hkv, Hkv, D)) return ATTN_ERR_RESOURCE;
+    if (workspace_bytes < decode_paged_workspace_bytes(B, Hkv)) return ATTN_ERR_RESOURCE;
     Ctx c;
     st = get_ctx(stream, &c);
     if (st != ATTN_OK) return st;

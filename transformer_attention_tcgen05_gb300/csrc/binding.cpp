@@ -282,10 +282,11 @@ PyObject *kv_pages_fork(PyObject *const *a) {
     const int32_t *src = c.ints(a[3], "src", n), *dst = c.ints(a[4], "dst", n);
     const Workspace ws(c, a[6], attn_kv_pages_workspace_bytes(P), false, r);
     const at::Tensor cs = at::empty({n}, r.options()), cd = at::empty({n}, r.options());
-    done(attn_kv_pages_fork(t.p, sl, refs, src, dst, n, static_cast<int32_t *>(cs.data_ptr()),
-                            static_cast<int32_t *>(cd.data_ptr()), t.B, P, integer(a[5]), t.M, t.stride,
-                            ws.ptr(), ws.bytes(), c.stream()),
-         "attn_kv_pages_fork");
+    if (n > 0)
+        done(attn_kv_pages_fork(t.p, sl, refs, src, dst, n, static_cast<int32_t *>(cs.data_ptr()),
+                                static_cast<int32_t *>(cd.data_ptr()), t.B, P, integer(a[5]), t.M, t.stride,
+                                ws.ptr(), ws.bytes(), c.stream()),
+             "attn_kv_pages_fork");
     return Py_BuildValue("(NN)", wrap(cs), wrap(cd));
 }
 

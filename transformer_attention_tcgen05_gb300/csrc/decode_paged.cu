@@ -908,11 +908,14 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 }  // namespace
 
-size_t decode_paged_workspace_bytes(int B, int G, int Hkv, int D) {
-    const size_t hp = G <= 8 ? 8 : 16;
-    return align256(size_t(B) * Hkv * sizeof(unsigned)) +
-           align256(size_t(2) * kMaxCtas * hp * D * sizeof(float)) +
-           align256(size_t(2) * kMaxCtas * hp * 2 * sizeof(float));
+// The partials come first, at their largest size, so that the tickets lie at one
+// place whatever the call's sizes: one workspace serves calls of several sizes.
+constexpr size_t kPartBytes = size_t(2) * kMaxCtas * 16 * 128 * sizeof(float);
+constexpr size_t kMlBytes = size_t(2) * kMaxCtas * 16 * 2 * sizeof(float);
+static_assert(kPartBytes % 256 == 0 && kMlBytes % 256 == 0, "aligned workspace parts");
+
+size_t decode_paged_workspace_bytes(int B, int Hkv) {
+    return kPartBytes + kMlBytes + align256(size_t(B) * Hkv * sizeof(unsigned));
 }
 
 attn_status_t decode_paged(const Ctx &c, attn_dtype_t dt, const PagedDecode &a) {
@@ -943,13 +946,10 @@ attn_status_t decode_paged(const Ctx &c, attn_dtype_t dt, const PagedDecode &a) 
     p.max_pages = a.max_pages; p.num_pages = a.P;
     p.window = a.window; p.sinks = a.sinks;
     p.c_log2 = a.scale * kLog2e;
-    const size_t hp = a.G <= 8 ? 8 : 16;
     uint8_t *w = static_cast<uint8_t *>(a.ws);
-    p.tickets = reinterpret_cast<unsigned *>(w);
-    w += align256(size_t(a.B) * a.Hkv * sizeof(unsigned));
     p.part_o = reinterpret_cast<float *>(w);
-    w += align256(size_t(2) * kMaxCtas * hp * a.D * sizeof(float));
-    p.part_ml = reinterpret_cast<float *>(w);
+    p.part_ml = reinterpret_cast<float *>(w + kPartBytes);
+    p.tickets = reinterpret_cast<unsigned *>(w + kPartBytes + kMlBytes);
     p.err = c.err;
     if (a.D == 128) {
         if (a.G <= 8) return f16 ? launch_paged<128, 1, true>(c, tk, tv, p) : launch_paged<128, 1, false>(c, tk, tv, p);

@@ -102,7 +102,7 @@ struct PagedDecode {
     float scale;
     void *ws;
 };
-size_t decode_paged_workspace_bytes(int B, int G, int Hkv, int D);
+size_t decode_paged_workspace_bytes(int B, int Hkv);
 attn_status_t decode_paged(const Ctx &c, attn_dtype_t dt, const PagedDecode &a);
 
 struct PagedAppend {

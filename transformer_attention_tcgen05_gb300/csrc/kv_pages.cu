@@ -309,7 +309,7 @@ struct AllocParams {
     int n;
     int32_t *copy_src, *copy_dst, *count;
     int32_t *new_refs;
-    int32_t *ws;                                       // [P + 1]
+    int32_t *ws;                                       // [P]
     unsigned *err;
 };
 
@@ -623,8 +623,8 @@ __global__ void __launch_bounds__(kAT, 1) fork_kernel(const AllocParams p) {
 }
 
 // Compact: with L live pages, the k-th live page at or above L moves to the
-// k-th free page below L.  Lists the moves, fills the map old -> new of the
-// pages at or above L (ws[page]; ws[P] = L) and writes the new counts.
+// k-th free page below L.  Lists the moves, fills the map old -> new (ws[page],
+// -1 for a page that is not live) and writes the new counts.
 __global__ void __launch_bounds__(kAT, 1) compact_kernel(const AllocParams p) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -665,7 +665,8 @@ __global__ void __launch_bounds__(kAT, 1) compact_kernel(const AllocParams p) {
             const bool lv = p.refs[i + j] > 0;
             if (lv && i + j >= L) mov |= 1u << j;
             if (!lv && i + j < L) hole |= 1u << j;
-            if (!lv && i + j >= L) p.ws[i + j] = -1;   // no live page: an entry naming it is wrong
+            // no live page: an entry that names it is wrong
+            if (!lv || i + j < L) p.ws[i + j] = lv ? i + j : -1;
         }
         int all;
         const int pre = block_scan(sh, __popc(mov) | (__popc(hole) << 16), &all);
@@ -687,7 +688,6 @@ __global__ void __launch_bounds__(kAT, 1) compact_kernel(const AllocParams p) {
     }
     if (t == 0) {
         *p.count = moves;
-        p.ws[p.P] = L;
     }
     cluster_barrier();                                 // the movers' counts have been read
     for (int i = i0 + threadIdx.x; i < i1; i += kAT) {
@@ -703,7 +703,6 @@ __global__ void __launch_bounds__(256) remap_kernel(const AllocParams p, int32_t
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int b = blockIdx.x / blocks, j0 = (blockIdx.x % blocks) * 1024;
-    const int L = p.ws[p.P];
     int e[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -714,8 +713,8 @@ __global__ void __launch_bounds__(256) remap_kernel(const AllocParams p, int32_t
     for (int u = 0; u < 4; ++u) {
         const int i = j0 + u * 256 + threadIdx.x;
         if (i >= p.M) break;
-        if (e[u] >= L || e[u] < -1) {
-            e[u] = e[u] >= L && e[u] < p.P ? p.ws[e[u]] : -1;
+        if (e[u] != -1) {
+            e[u] = e[u] >= 0 && e[u] < p.P ? p.ws[e[u]] : -1;
             if (e[u] < 0) raise_device_error(p.err, kDevCheck);
         }
         out[b * out_stride + i] = e[u];
@@ -803,7 +802,7 @@ attn_status_t kv_pages_copy(const Ctx &c, attn_dtype_t dt, const PagesCopy &a) {
                  : launch_pdl(c, copy_kernel<false>, dim3(grid), kCopyThreads, 1, 0, p);
 }
 
-size_t kv_pages_workspace_bytes(int P) { return ((size_t(P) + 1) * 4 + 255) & ~size_t(255); }
+size_t kv_pages_workspace_bytes(int P) { return (size_t(P) * 4 + 255) & ~size_t(255); }
 
 attn_status_t kv_pages_reserve(const Ctx &c, const PageTable &t, const int32_t *seq_len,
                                const int32_t *add, int32_t *refs, void *ws) {
