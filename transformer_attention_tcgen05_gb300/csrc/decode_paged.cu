@@ -104,15 +104,18 @@ struct PgParams {
 };
 
 constexpr int kMaxWarps = 4;
+constexpr int kMaxAligned = 16;   // longest range (chunks) that is fitted to its units
 constexpr int kWarpUnit = 8;      // longest unit (chunks) that counts as short
 
 struct Misc {
     uint64_t full_k[kMaxWarps * 2], full_v[kMaxWarps * 2];   // [warp][slot]
     int warp_long[kMaxWarps], warp_short[kMaxWarps];
-    int warp_max[kMaxWarps], warp_units[kMaxWarps];
+    int warp_parts[kMaxWarps];
+    int warp_max[kMaxWarps], warp_units[kMaxWarps], warp_units_l[kMaxWarps];
     // where the CTA's range, or each warp's (and the one behind), starts
     int start_flat[kMaxWarps + 1];
     int start_b[kMaxWarps + 1], start_len[kMaxWarps + 1], start_kvh[kMaxWarps + 1], start_v[kMaxWarps + 1];
+    int start_count;
     int abort;
     unsigned last;
     int warp_bad[kMaxWarps];
@@ -240,6 +243,72 @@ struct Group {
     int kvh, cnt;                          // KV head; chunks in the group (0: the range is done)
 };
 
+// Rare steps are functions of their own, out of the way of the code that every
+// launch fetches.
+
+// A sequence with nothing to attend to: zeros (length 0) or a report.
+template <int D, typename T>
+__device__ __noinline__ void idle_sequence(const PgParams &p, int b, int len) {
+    if (len != 0) raise_device_error(p.err, kDevCheck);
+#pragma unroll 1
+    for (int i = 0; i < p.Hkv * p.G * (D / 8) && len == 0; ++i)
+        *reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + b * p.o_sb + (i / (D / 8)) * p.o_sh +
+                                   (i % (D / 8)) * 8) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// Where this CTA's range starts (mark i: f0, or the first unit that starts at or
+// behind f0 + i per), looked for by the thread of one sequence: n chunks per
+// unit of this list, `before` chunks per KV head ahead of it.
+__device__ __forceinline__ void mark_starts(const PgParams &p, Misc *ms, int marks, int f0, int per, int b,
+                                            int len, int n, int before) {
+    const int lo = before * p.Hkv, hi = lo + n * p.Hkv;
+#pragma unroll 1
+    for (int i = 0; i < marks; ++i) {
+        const unsigned x = unsigned(f0) + unsigned(i * per);
+        if (x < unsigned(lo) || x >= unsigned(hi)) continue;
+        int kvh = int((x - lo) / unsigned(n)), v = int(x - lo) - kvh * n;
+        if (marks > 1 && v > 0) {
+            ++kvh;                                     // may be Hkv: the next sequence's first
+            v = 0;
+        }
+        ms->start_b[i] = b;
+        ms->start_len[i] = len;
+        ms->start_kvh[i] = kvh;
+        ms->start_v[i] = v;
+        ms->start_flat[i] = lo + kvh * n + v;
+    }
+}
+
+// The same for a batch of more sequences than threads, read again tile by tile.
+template <int CW>
+__device__ __noinline__ void mark_long_batch(const PgParams &p, Misc *ms, int marks, int f0, int per,
+                                             bool in_short) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int carry = 0;                                     // chunks of the sequences before this tile
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.B; b0 += CW * 32) {
+        __syncthreads();
+        const int b = b0 + threadIdx.x;
+        const int len = b < p.B ? p.seq_len[b] : 0;
+        const int n = plan_in(p, len, in_short).n;
+        int inc = n;
+#pragma unroll 1
+        for (int off = 1; off < 32; off <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += up;
+        }
+        if (lane == 31) ms->warp_long[warp] = inc;
+        __syncthreads();
+        int before = carry + inc - n;
+#pragma unroll
+        for (int w = 0; w < CW; ++w) {
+            if (w < warp) before += ms->warp_long[w];
+            carry += ms->warp_long[w];
+        }
+        if (n > 0) mark_starts(p, ms, marks, f0, per, b, len, n, before);
+    }
+}
+
 template <int D, int NT, bool F16>
 __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, kCtasPerSm)
 decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -275,7 +344,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     //      length 0 writes zeros, a length outside the table is reported and
     //      its output left as it was.
     const bool one_tile = p.B <= kNT;                  // a thread per sequence: read once
-    int inc_l = 0, inc_s = 0, n_mine = 0, len_mine = 0, n_max = 0, units = 0;
+    int inc_l = 0, inc_s = 0, n_mine = 0, len_mine = 0, n_max = 0, units = 0, units_l = 0;
 #pragma unroll 1
     for (int b = threadIdx.x; b < p.B; b += kNT) {
         len_mine = p.seq_len[b];
@@ -286,14 +355,9 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
             units += n_mine > 0;
         } else {
             inc_l += n_mine;
+            ++units_l;
         }
-        if (n_mine == 0 && b % ctas == cta) {
-            if (len_mine != 0) raise_device_error(p.err, kDevCheck);
-#pragma unroll 1
-            for (int i = 0; i < p.Hkv * p.G * (D / 8) && len_mine == 0; ++i)
-                *reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + b * p.o_sb + (i / (D / 8)) * p.o_sh +
-                                           (i % (D / 8)) * 8) = make_uint4(0u, 0u, 0u, 0u);
-        }
+        if (n_mine == 0 && b % ctas == cta) idle_sequence<D, T>(p, b, len_mine);
     }
 #pragma unroll 1
     for (int off = 1; off < 32; off <<= 1) {
@@ -304,16 +368,18 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         }
         n_max = imax(n_max, __shfl_xor_sync(0xffffffffu, n_max, off));
         units += __shfl_xor_sync(0xffffffffu, units, off);
+        units_l += __shfl_xor_sync(0xffffffffu, units_l, off);
     }
     if (lane == 31) {
         ms->warp_long[warp] = inc_l;
         ms->warp_short[warp] = inc_s;
         ms->warp_max[warp] = n_max;
         ms->warp_units[warp] = units;
+        ms->warp_units_l[warp] = units_l;
     }
     __syncthreads();
     int total_l = 0, total_s = 0, before_l = inc_l, before_s = inc_s;
-    units = 0;
+    units = units_l = 0;
 #pragma unroll
     for (int w = 0; w < CW; ++w) {
         if (w < warp) {
@@ -324,10 +390,12 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         total_s += ms->warp_short[w];
         n_max = imax(n_max, ms->warp_max[w]);
         units += ms->warp_units[w];
+        units_l += ms->warp_units_l[w];
     }
     total_l *= p.Hkv;
     total_s *= p.Hkv;
     units *= p.Hkv;                                    // of the short list
+    units_l *= p.Hkv;
     // this CTA's list, its number c among the nc CTAs of that list
     bool in_short = total_l == 0, alone = in_short && units > ctas;
     int c = cta, nc = ctas;
@@ -348,64 +416,63 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     // at least one chunk per warp, unless every unit is shorter than that: then
     // the units are spread over more CTAs
     if (!alone) per = imax(per, imin(CW, n_max));
-    const long long f0l = (long long)per * (alone ? c * CW : c);
-    if (f0l >= total) return;
-    const int f0 = int(f0l);
-    // boundary i of this CTA: f0, or the first unit that starts at or behind
-    // f0 + i per (each warp's range is a run of whole units)
-    const int marks = alone ? CW + 1 : 1;
-    auto mark = [&](int b, int len, int n, int before) {
-        const int lo = before * p.Hkv, hi = lo + n * p.Hkv;
-#pragma unroll 1
-        for (int i = 0; i < marks; ++i) {
-            const unsigned x = unsigned(f0) + unsigned(i * per);
-            if (x < unsigned(lo) || x >= unsigned(hi)) continue;
-            int kvh = int((x - lo) / unsigned(n)), v = int(x - lo) - kvh * n;
-            if (alone && v > 0) {
-                ++kvh;                                 // may be Hkv: the next sequence's first
-                v = 0;
-            }
-            ms->start_b[i] = b;
-            ms->start_len[i] = len;
-            ms->start_kvh[i] = kvh;
-            ms->start_v[i] = v;
-            ms->start_flat[i] = lo + kvh * n + v;
-        }
-    };
-    if (threadIdx.x < marks && f0l + (long long)threadIdx.x * per >= total) ms->start_flat[threadIdx.x] = total;
-    int carry = 0, b0 = 0;                             // chunks of the sequences before this tile
-    if (!one_tile) {                                   // a long batch is read again, tile by tile
-        b0 = -kNT;
-        n_mine = 0;
-    }
-#pragma unroll 1
-    for (;;) {
-        mark(b0 + threadIdx.x, len_mine, n_mine, before);
-        b0 += kNT;
-        if (b0 >= p.B) break;
-        __syncthreads();
-        const int b = b0 + threadIdx.x;
-        len_mine = b < p.B ? p.seq_len[b] : 0;
-        n_mine = plan_in(p, len_mine, in_short).n;
-        int inc = n_mine;
+    // Where at most two more chunks per range allow it, a range holds part of one
+    // unit only, and its CTA merges and joins once instead of twice: with q =
+    // CTAs / units, parts of the longest unit's q-th give no more parts than
+    // CTAs.  The list is read as if each unit filled whole parts.  (Equal units
+    // that fill whole ranges need no such thing.  8 x 1024 tokens: 13.3 us
+    // without, 11.6 with; longer ranges lose more than a merge.)
+    int parts = 0, parts_before = 0, parts_total = 0;
+    const int n_units = in_short ? units : units_l;
+    const int fit = n_units <= nc ? imax(per, cdiv(n_max, nc / imax(n_units, 1))) : 0;
+    if (!alone && one_tile && fit > 0 && fit <= per + 2 && per <= kMaxAligned && n_max > per &&
+        !(n_max % per == 0 && (long long)n_units * n_max == total)) {
+        per = fit;
+        parts = int(unsigned(n_mine + per - 1) / unsigned(per));
+        int inc = parts;
 #pragma unroll 1
         for (int off = 1; off < 32; off <<= 1) {
             const int up = __shfl_up_sync(0xffffffffu, inc, off);
             if (lane >= off) inc += up;
         }
-        if (lane == 31) ms->warp_long[warp] = inc;
+        if (lane == 31) ms->warp_parts[warp] = inc;
         __syncthreads();
-        before = carry + inc - n_mine;
+        parts_before = inc - parts;
 #pragma unroll
         for (int w = 0; w < CW; ++w) {
-            if (w < warp) before += ms->warp_long[w];
-            carry += ms->warp_long[w];
+            if (w < warp) parts_before += ms->warp_parts[w];
+            parts_total += ms->warp_parts[w];
         }
+        parts_total *= p.Hkv;
+    }
+    const bool aligned = parts_total > 0;
+    const long long f0l = (long long)per * (alone ? c * CW : c);
+    if (aligned ? c >= parts_total : f0l >= total) return;
+    const int f0 = int(f0l);
+    // each warp's range is a run of whole units, between two marks
+    const int marks = alone ? CW + 1 : 1;
+    if (aligned) {
+        const int x = c - parts_before * p.Hkv;        // among the parts of this thread's sequence
+        if (parts > 0 && x >= 0 && x < parts * p.Hkv) {
+            const int kvh = int(unsigned(x) / unsigned(parts)), v = (x - kvh * parts) * per;
+            ms->start_b[0] = threadIdx.x;
+            ms->start_len[0] = len_mine;
+            ms->start_kvh[0] = kvh;
+            ms->start_v[0] = v;
+            ms->start_flat[0] = f0;
+            ms->start_count = imin(per, n_mine - v);
+        }
+    } else {
+        if (threadIdx.x < marks && f0l + (long long)threadIdx.x * per >= total) ms->start_flat[threadIdx.x] = total;
+        if (!one_tile)
+            mark_long_batch<CW>(p, ms, marks, f0, per, in_short);
+        else if (n_mine > 0)
+            mark_starts(p, ms, marks, f0, per, threadIdx.x, len_mine, n_mine, before);
     }
     __syncthreads();
     const int at = alone ? warp : 0;
     const int start = ms->start_flat[at];
-    const int count = alone ? ms->start_flat[warp + 1] - start : imin(per, total - f0);
+    const int count = alone ? ms->start_flat[warp + 1] - start : aligned ? ms->start_count : imin(per, total - f0);
     if (count <= 0) return;                            // alone: no unit starts in this warp's share
 
     Walk w(p, in_short, ms->start_b[at], ms->start_len[at], ms->start_kvh[at], ms->start_v[at], start, count);
