@@ -356,7 +356,8 @@ ATTN_API attn_status_t attn_kv_append_paged(void *k_pages, void *v_pages, const 
  *   seq_len[b] == 0 (an idle slot) writes zeros.  Table entries of pages that
  *   hold no visible position are not needed, so those pages may be free.  Rows of a page
  *   behind seq_len[b], or outside the window, do not change the result,
- *   whatever they hold.
+ *   whatever they hold.  An infinity or NaN that is visible makes what it
+ *   reaches infinite or NaN.
  *   A seq_len[b] outside [0, max_pages * page_size], or a needed entry that is
  *   no page of the pool, sets ATTN_ERR_DEVICE_CHECK and leaves that sequence's
  *   output unwritten; other sequences' are not affected.
@@ -390,12 +391,12 @@ ATTN_API size_t attn_decode_gqa_paged_workspace_bytes(int B, int Hq, int Hkv, in
  * serves requests in (row, entry) order, so its result depends on its inputs
  * alone.  A request that cannot be met, or an argument on the device that is
  * out of range, sets ATTN_ERR_DEVICE_CHECK and changes nothing (free: the
- * entry in question stays; compact: an entry that names no live page becomes
+ * entry, or the row of that seq_len, stays; compact: an entry that names no live page becomes
  * -1).  page_refs must count the table's entries, as these calls keep it; calls
  * that change the same pool are ordered by their stream.
  *   workspace: DEVICE scratch of attn_kv_pages_workspace_bytes(num_pages)
  *   bytes, 256-byte aligned, contents irrelevant, not used by another call at
- *   the same time.  reserve and fork take B <= 16384.
+ *   the same time.  reserve and fork take B <= 16384, reserve B * max_pages < 2^31.
  *
  * reserve: pages for the add_len[b] tokens (DEVICE int32 [B], >= 0) behind
  *   seq_len[b]: every entry that covers a position in [seq_len[b], seq_len[b] +

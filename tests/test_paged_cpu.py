@@ -83,6 +83,7 @@ def test_allocator_refusals(L):
     assert reserve(w=None) == reserve(w=ctypes.c_void_p(0x90004)) == INVALID
     assert reserve(n=8) == RESOURCE
     assert reserve(B=20000) == UNSUPPORTED
+    assert reserve(B=16384, M=1 << 17, ts=1 << 17) == UNSUPPORTED      # 2^31 entries
 
     def free(t=A, sl=Bp, refs=Cp, sinks=0, B=2, S=8):
         return L.attn_kv_pages_free(t, sl, refs, B, 10, S, 4, 4, 5, sinks, None)

@@ -505,6 +505,24 @@ def test_free_reports_pages_that_are_not_counted(ta):
     assert table.tolist() == [[-1, 1, -1, 7]] and refs.tolist() == [0, 0, 1, 0]
 
 
+def test_free_leaves_rows_of_impossible_lengths(ta):
+    table = torch.tensor([[0, 1], [2, -1], [3, 4]], dtype=torch.int32, device="cuda")
+    refs = torch.ones(5, dtype=torch.int32, device="cuda")
+    sl = torch.tensor([17, 0, -1], dtype=torch.int32, device="cuda")     # 16 positions per row
+    ta.kv_pages_free(table, sl, refs, 8, window=1)
+    assert ta.device_status() == 6
+    assert table.tolist() == [[0, 1], [-1, -1], [3, 4]] and refs.tolist() == [1, 1, 0, 1, 1]
+
+
+def test_copy_reports_a_pair_of_equal_numbers_outside_the_pool(ta):
+    k, v = torch.randn(2, 1, 8, 64, device="cuda"), torch.randn(2, 1, 8, 64, device="cuda")
+    k0 = k.clone()
+    pair = torch.tensor([2], dtype=torch.int32, device="cuda")
+    ta.kv_pages_copy(k, v, pair, pair)
+    assert ta.device_status() == 6
+    assert torch.equal(k, k0)
+
+
 def test_compact_drops_entries_of_free_pages(ta):
     # 4 and 1 name free pages (1 below the live count: another page moves there)
     table = torch.tensor([[5, 3, -1, 4, 99, 1]], dtype=torch.int32, device="cuda")

@@ -139,6 +139,16 @@ def test_what_a_row_does_not_see_does_not_reach_it(ta, dt, D, what):
     assert torch.isfinite(clean.float()).all()
 
 
+@pytest.mark.parametrize("which", ["q", "k", "v"])
+def test_window_of_nothing_but_nan(ta, which):
+    t = dict(q=make("bf16", 1, 2, 2000, 128, "head", 10), k=make("bf16", 1, 1, 2000, 128, "head", 11),
+             v=make("bf16", 1, 1, 2000, 128, "head", 12))
+    t[which].fill_(float("nan"))
+    o = ta.causal_gqa_window_fwd(t["q"], t["k"], t["v"], 0)
+    assert ta.device_status() == 0
+    assert torch.isnan(o).all()
+
+
 def test_window_output_view_and_sentinels(ta):
     B, Hq, N, D = 2, 4, 200, 64
     q, k, v = (make("bf16", B, h, N, D, "token", 20 + i) for i, h in enumerate((Hq, 2, 2)))

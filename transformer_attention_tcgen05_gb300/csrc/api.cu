@@ -605,7 +605,8 @@ attn_status_t attn_kv_pages_reserve(int32_t *page_table, const int32_t *seq_len,
     attn_status_t st = check_pool(page_table, B, num_pages, page_size, max_pages, table_stride);
     if (st == ATTN_OK) st = check_pages_ws(workspace, workspace_bytes, num_pages);
     if (st != ATTN_OK) return st;
-    if (B > 16384) return ATTN_ERR_UNSUPPORTED;
+    // the entries asked about are numbered in 32 bits
+    if (B > 16384 || (long long)B * max_pages >= (1ll << 31)) return ATTN_ERR_UNSUPPORTED;
     Ctx c;
     st = get_ctx(stream, &c);
     if (st != ATTN_OK) return st;

@@ -187,11 +187,12 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p) 
         const int pair = int(it / per_pair), rest = int(it % per_pair);
         const int side = rest / p.pieces, piece = rest % p.pieces;
         const int s = p.src[pair], d = p.dst[pair];
-        if ((s == -1 && d == -1) || s == d) continue;
+        if (s == -1 && d == -1) continue;
         if (s < 0 || s >= p.P || d < 0 || d >= p.P) {
             if (rest == 0 && threadIdx.x == 0) raise_device_error(p.err, kDevCheck);
             continue;
         }
+        if (s == d) continue;
         const bool is_v = side & 1;
         uint8_t *base = (is_v ? p.v : p.k) + (side >> 1) * (is_v ? p.v_st[0] : p.k_st[0]);
         const long long pst = is_v ? p.v_st[1] : p.k_st[1];
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(256) free_kernel(const AllocParams p, int bloc
     ptx::griddep_launch_dependents();
     const int b = blockIdx.x / blocks, j0 = (blockIdx.x % blocks) * 1024;
     const int len = p.seq_len[b];
-    if (len < 0) {
+    if (len < 0 || len > (long long)p.M * p.S) {
         if (threadIdx.x == 0 && j0 == 0) raise_device_error(p.err, kDevCheck);
         return;
     }

@@ -222,6 +222,11 @@ __device__ __forceinline__ void window_row(const WnParams &p, int b, int h, int 
         l = l * f + w;
 #pragma unroll
         for (int i = 0; i < 2 * CW; ++i) acc[i] = fmaf(w, x[i], acc[i] * f);
+        // NaN in every channel (a NaN in q, say) stays: no need to read on
+        bool lost = true;
+#pragma unroll
+        for (int i = 0; i < 2 * CW; ++i) lost = lost && acc[i] != acc[i];
+        if (__all_sync(0xffffffffu, lost)) break;
     }
     const float inv = 1.f / l;
     uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<T *>(p.o) + b * p.o_sb + h * p.o_sh +
