@@ -43,6 +43,7 @@ namespace {
 constexpr int kBM = 128;      // query rows per tile (MMA M)
 constexpr int kNQ = 2;        // query tiles per CTA
 constexpr int kBN = 128;      // keys per key tile (MMA N of S)
+constexpr int kFew = 32;      // keys of the tile that holds a few sinks only
 
 template <int D>
 struct WnCfg {
@@ -130,6 +131,7 @@ struct Item {
     int q0, fb, fh, fkh, dq, dh;
     int n[kNQ], f[kNQ], steps;
     int w_lo, w_sk;                // first window tile, sink tiles before it
+    bool few;                      // step 0 is the sinks' tile and holds at most kFew keys
 
     // key tile of step j: the leading tile of the first query tile (if any),
     // the sink tiles, the window
@@ -167,8 +169,10 @@ __device__ __forceinline__ Item get_item(const WnParams &p) {
     w.w_lo = imax(0, pos - p.window + 1) / kBN;
     const int lo1 = imax(0, pos + w.dq - p.window + 1) / kBN;
     w.w_sk = imin(ns, w.w_lo);
+    w.few = w.w_sk > 0 && p.sinks <= kFew;
     w.f[0] = 0;
     w.f[1] = two && lo1 > w.w_lo && w.w_lo >= ns ? 1 : 0;
+    w.few = w.few && w.f[1] == 0;
     // (a single second row tile past the sequence's end has no step)
     w.n[0] = one ? w.w_sk + (p.off + imin(w.q0 + kBM, p.Nq) - 1) / kBN - w.w_lo + 1 : 0;
     w.n[1] = two ? w.w_sk + (p.off + imin(w.q0 + w.dq + kBM, p.Nq) - 1) / kBN - w.w_lo + 1 : 0;
@@ -325,6 +329,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         } else if (warp == C::W_MMA && lane == 0) {
             // ============================================= MMA issuer
             const uint32_t id_qk = ptx::idesc_16_f32(kBM, BNt, false, F16);
+            const uint32_t id_few = ptx::idesc_16_f32(kBM, kFew, false, F16);
             const uint32_t id_pv = ptx::idesc_16_f32(kBM, D, true, F16);
             // descriptors are built once; a k-step, a stage or a tile only moves
             // the start-address field
@@ -333,7 +338,9 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             const uint32_t dk0 = ptx::desc_lo_sw128(ptx::smem_addr(smem + C::k_off(0)), 16);
             const uint32_t dv0 = ptx::desc_lo_sw128(ptx::smem_addr(smem + C::v_off(0)), C::PANEL_KV);
             constexpr int nkv = BNt / 16;                // k-steps of P V
+            const Item w = get_item(p);
             auto issue_qk = [&](int t, int gk) {
+                const uint32_t id = w.few && gk == 0 ? id_few : id_qk;
                 const uint32_t a0 = dq0 + uint32_t((t * C::Q_BYTES) >> 4);
                 const uint32_t b0 = dk0 + uint32_t(((gk % C::KS) * C::KV_BYTES) >> 4);
 #pragma unroll
@@ -341,7 +348,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                     const uint32_t oa = ((kk >> 2) * C::PANEL_Q + (kk & 3) * 32) >> 4;
                     const uint32_t ob = ((kk >> 2) * C::PANEL_KV + (kk & 3) * 32) >> 4;
                     ptx::mma_ss(tmem + C::tm_s(t), ptx::desc_join(a0 + oa, HI128),
-                                ptx::desc_join(b0 + ob, HI128), id_qk, kk > 0);
+                                ptx::desc_join(b0 + ob, HI128), id, kk > 0);
                 }
                 ptx::tc_commit(&bars->s_full[t]);
             };
@@ -349,13 +356,14 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 const uint32_t b0 = dv0 + uint32_t(((gv % C::VS) * C::KV_BYTES) >> 4);
                 const uint32_t a0 = tmem + C::tm_p(t);
 #pragma unroll
-                for (int kk = 0; kk < nkv; ++kk)
+                for (int kk = 0; kk < nkv; ++kk) {
+                    if (kk == kFew / 16 && w.few && gv == 0) break;
                     ptx::mma_ts(tmem + C::tm_o(t), a0 + kk * 8,
                                 ptx::desc_join(b0 + uint32_t(kk * (2048 >> 4)), HI128), id_pv,
                                 (!first || kk > 0) ? 1u : 0u);
+                }
                 ptx::tc_commit(&bars->o_done[t]);
             };
-            const Item w = get_item(p);
             bool ok = w.steps > 0, k_seen = false, v_seen = false;
             // a stage barrier is waited on once per step (a completed wait still
             // costs this thread a round trip to shared memory)
@@ -448,7 +456,42 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         };
 
         float m = -INFINITY, l = 0.f;
-        for (int j = 0; j < nt; ++j) {
+        int j = 0;
+        // ---- a first tile of a few sinks, which every row sees: kFew columns
+        if (w.few && nt > 0) {
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&bars->s_full[t], 0, p.err, abort));
+            if (ok) {
+                ptx::tc_fence_after();
+                float x[kFew];
+                ptx::tmem_ld32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+                ptx::tmem_wait_ld();
+                if constexpr (C::SEP_P) {
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(&bars->s_free[t]);
+                }
+                float mx = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < kFew; ++e) {
+                    if (e >= p.sinks) x[e] = -INFINITY;
+                    mx = fmaxf(mx, x[e]);
+                }
+                m = mx * cl;
+                const float nmu = m == -INFINITY ? 0.f : -m;
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < kFew; e += 2) {
+                    const float p0 = ptx::ex2(fmaf(x[e], cl, nmu)), p1 = ptx::ex2(fmaf(x[e + 1], cl, nmu));
+                    l += p0 + p1;
+                    pk[e / 2] = H16<F16>::pack(p0, p1);
+                }
+                ptx::tmem_st16(p_addr, pk);
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&bars->p_ready[t]);
+                j = 1;
+            }
+        }
+        for (; ok && j < nt; ++j) {
             if (!__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&bars->s_full[t], j & 1, p.err, abort))) {
                 ok = false;
                 break;
