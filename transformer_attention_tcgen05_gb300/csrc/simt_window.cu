@@ -6,16 +6,18 @@
 // and streams the keys that one of them sees, the sinks and the window, as one
 // list in tiles of 64.
 //
-// Both products are register-tiled: a thread holds 4 rows x 4 keys of S and 4
-// rows x D / 16 channels of O, so that 8 shared-memory vectors feed 64 FMAs
-// (S) and 2 feed 16 (P V); the one-row-per-thread kernel that the unwindowed
-// entries use reads one vector per 4 FMAs and has a quarter of the warps.
-// Bound by the FMA pipe and, for short prompts, by latency: 32-row tiles give a
+// Both products are register-tiled: a thread holds 8 rows x 2 keys of S and 8
+// rows x D / 32 channels of O and multiplies in pairs (two FMAs an instruction:
+// even and odd channels of S, two rows of O), the vectors of the next step read
+// ahead.  A warp owns 8 rows, so what it shares (q, P) is read as broadcasts.
+// Bound by shared-memory latency and the FMA pipe (3.4 cycles per pair
+// instruction and warp, 2 at best) and, for short prompts, by the three or four
+// tiles that each CTA goes through one after the other: 32-row tiles give a
 // 515-token prompt of 16 heads 272 CTAs (B 2, 8 heads on 2 KV heads, D 64,
-// window 128, sinks 4: 21.8 us, 57 us in the one-row-per-thread form; 2048
-// tokens, 8 heads, D 128, window 512: 188 us = 20.2 TFLOP/s, was 334 us).
-// Sinks and window as two runs of tiles cost one tile more (27.9 us), synchronous
-// copies 22.9 us.
+// window 128, sinks 4: 15.4 us; 2048 tokens, 8 heads, D 128, window 512: 121 us
+// = 31.4 TFLOP/s).  4 rows x 4 keys per thread, scalar FMAs and nothing read
+// ahead: 20.6 and 187 us; 4 rows x 2 keys in twice the warps: 17.6 and 146 us;
+// one row per thread, as in the entries without a window: 57 and 334 us.
 //
 // Every product is an fp32 FMA (never TF32), statistics and sums are fp32 and
 // the output is rounded once.  A key that a row does not see never enters the
@@ -26,6 +28,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "ptx.cuh"
 
 namespace attn {
 namespace {
@@ -33,12 +36,13 @@ namespace {
 constexpr int kBM = 32;      // query rows per CTA
 constexpr int kBN = 64;      // keys per tile
 constexpr int kThreads = 128;
+constexpr int kR = 8;        // query rows per warp
 
 struct WinParams {
     const void *q, *k, *v;
     void *o;
     int Nq, Nkv, off, window, sinks, H, group;
-    float qscale;            // scale * log2(e), folded into q
+    float qscale;            // scale * log2(e)
     TensorStrides sq, sk, sv, so;
 };
 
@@ -75,15 +79,40 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 // waits until at most one group of this thread is outstanding
 __device__ __forceinline__ void cp_wait1() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 
-// Thread (ty, tx) = (tid / 16, tid % 16): rows 4 ty + i, keys tx + 16 c,
-// channels tx * D / 16 + e.
+// the largest x of a warp (NaN ignored)
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// N consecutive floats of shared memory (the widest load that fits)
+template <int N> __device__ __forceinline__ void read(const float *p, float (&x)[N]) {
+    if constexpr (N == 1) {
+        x[0] = *p;
+    } else if constexpr (N == 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(p);
+        x[0] = v.x;
+        x[1] = v.y;
+    } else {
+        const float4 v = *reinterpret_cast<const float4 *>(p);
+        x[0] = v.x;
+        x[1] = v.y;
+        x[2] = v.z;
+        x[3] = v.w;
+    }
+}
+
+// Warp w owns rows 8 w .. 8 w + 7; a lane keys lane and lane + 32 of a tile and
+// channels lane CH .. lane CH + CH - 1 of O.  What all lanes read (q, P) costs
+// shared memory one cycle a vector, what each reads for itself (k, V) four.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) simt_window_kernel(const WinParams p) {
+__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) simt_window_kernel(const WinParams p) {
     using S = WinSmem<D>;
-    constexpr int CH = D / 16;
+    constexpr int CH = D / 32;
     extern __shared__ float sm[];
     float *Qs = sm + S::Q, *Ks = sm + S::K, *Vs = sm + S::V, *Ps = sm + S::P;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int tid = threadIdx.x, lane = tid & 31, row0 = (tid >> 5) * kR;
     const int q0 = (gridDim.x - 1 - blockIdx.x) * kBM;
     const long long b = blockIdx.y / p.H, h = blockIdx.y % p.H, hk = h / p.group;
     const T *qg = static_cast<const T *>(p.q) + (b * p.sq.b + h * p.sq.h);
@@ -97,20 +126,19 @@ __global__ void __launch_bounds__(kThreads) simt_window_kernel(const WinParams p
     const int win0 = imax(0, pos0 - p.window + 1);
     const int sink1 = imin(p.sinks, win0);
 
+#pragma unroll
     for (int e = tid; e < kBM * D / 4; e += kThreads) {
         const int r = (e * 4) / D, d = (e * 4) % D;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < rows) x = load4<T>(qg + (q0 + r) * p.sq.n + d);
-        x.x *= p.qscale;
-        x.y *= p.qscale;
-        x.z *= p.qscale;
-        x.w *= p.qscale;
-        *reinterpret_cast<float4 *>(Qs + r * S::LD + d) = x;
+        const T *src = qg + (r < rows ? (q0 + r) * p.sq.n + d : 0);
+        if constexpr (sizeof(T) == 4)
+            cp_async16(Qs + r * S::LD + d, src, r < rows);
+        else
+            *reinterpret_cast<float4 *>(Qs + r * S::LD + d) = r < rows ? load4<T>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 
-    float acc[4][CH], m[4], l[4];
+    float acc[kR][CH], m[kR], l[kR];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kR; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
@@ -123,18 +151,21 @@ __global__ void __launch_bounds__(kThreads) simt_window_kernel(const WinParams p
     // One tile of K or V.  fp32 goes to shared memory asynchronously: the next
     // K while this tile's P V runs, the next V while the next S does.
     auto stage = [&](float *dst, const T *base, long long sn, int kb) {
-        const int keys = imin(kBN, total - kb);
-#pragma unroll 4
-        for (int e = tid; e < kBN * D / 4; e += kThreads) {
-            const int r = (e * 4) / D, d = (e * 4) % D;
-            const bool in = r < keys;
-            const T *src = base + (in ? key_of(kb + r) * sn + d : 0);
+        constexpr int VPR = D / 4, STEP = kThreads / VPR;      // vectors per row, rows per round
+        const int r0 = tid / VPR, d = (tid % VPR) * 4;
+        float *to = dst + r0 * S::LD + d;
+        const T *from = base + d;
+#pragma unroll 8
+        for (int r = 0; r < kBN; r += STEP) {
+            const int u = kb + r0 + r;
+            const bool in = u < total;
+            const T *src = from + (in ? key_of(u) : 0) * sn;
             if constexpr (sizeof(T) == 4) {
-                cp_async16(dst + r * S::LD + d, src, in);
+                cp_async16(to + r * S::LD, src, in);
             } else {
                 float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (in) x = load4<T>(src);
-                *reinterpret_cast<float4 *>(dst + r * S::LD + d) = x;
+                *reinterpret_cast<float4 *>(to + r * S::LD) = x;
             }
         }
         cp_commit();
@@ -146,28 +177,40 @@ __global__ void __launch_bounds__(kThreads) simt_window_kernel(const WinParams p
         cp_wait1();                                    // K is here
         __syncthreads();
 
-        // ---- S: 4 rows x 4 keys per thread
-        float s[4][4];
+        // ---- S: kR rows x 2 keys per thread, sums over even and odd channels;
+        //      the next step's vectors are read while this one's are multiplied
+        float s[kR][2], s2[kR][2][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kR; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s[i][c] = 0.f;
+            for (int c = 0; c < 2; ++c) s2[i][c][0] = s2[i][c][1] = 0.f;
+        float qn[kR][4], kn[2][4];
+        auto read_qk = [&](int d) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) read<4>(Ks + (lane + 32 * c) * S::LD + d, kn[c]);
+#pragma unroll
+            for (int i = 0; i < kR; ++i) read<4>(Qs + (row0 + i) * S::LD + d, qn[i]);
+        };
+        read_qk(0);
 #pragma unroll 4
         for (int d = 0; d < D; d += 4) {
-            float4 qv[4], kv[4];
+            float qv[kR][4], kv[2][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4 *>(Qs + (4 * ty + i) * S::LD + d);
+            for (int x = 0; x < 4; ++x) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) kv[c] = *reinterpret_cast<const float4 *>(Ks + (tx + 16 * c) * S::LD + d);
+                for (int i = 0; i < kR; ++i) qv[i][x] = qn[i][x];
+                kv[0][x] = kn[0][x];
+                kv[1][x] = kn[1][x];
+            }
+            read_qk(d + 4);                            // the last one reads the rows' padding
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int x = 0; x < 4; x += 2)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    s[i][c] = fmaf(qv[i].x, kv[c].x, s[i][c]);
-                    s[i][c] = fmaf(qv[i].y, kv[c].y, s[i][c]);
-                    s[i][c] = fmaf(qv[i].z, kv[c].z, s[i][c]);
-                    s[i][c] = fmaf(qv[i].w, kv[c].w, s[i][c]);
-                }
+                for (int i = 0; i < kR; ++i)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        ptx::ffma2(s2[i][c][0], s2[i][c][1], qv[i][x], qv[i][x + 1], kv[c][x], kv[c][x + 1],
+                                   s2[i][c][0], s2[i][c][1]);
         }
 
         __syncthreads();                               // K has been read
@@ -176,102 +219,116 @@ __global__ void __launch_bounds__(kThreads) simt_window_kernel(const WinParams p
         else
             cp_commit();
         cp_wait1();                                    // V is here
-        int wild = 0;                                  // an infinite or NaN value in the tile
-#pragma unroll 4
-        for (int e = tid; e < kBN * D / 4; e += kThreads) {
-            const float4 v = *reinterpret_cast<const float4 *>(Vs + (e * 4) / D * S::LD + (e * 4) % D);
-            wild |= !(fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY && fabsf(v.z) < INFINITY &&
-                      fabsf(v.w) < INFINITY);
-        }
-        wild = __syncthreads_or(wild);
-
-        // ---- masks (every row sees the whole tile, or it is tested key by key)
-        //      and online softmax
         const int k_first = key_of(kb), k_last = key_of(kb + keys - 1);
         const bool edge = keys < kBN || k_last > pos0 ||
                           (k_first <= pos0 + kBM - 1 - p.window && k_last >= p.sinks);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int pos = pos0 + 4 * ty + i;
-            unsigned seen = 0xfu;
-            if (edge) {
-                seen = 0;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int u = tx + 16 * c, key = key_of(kb + u);
-                    const bool ok = u < keys && key <= pos && (key > pos - p.window || key < p.sinks);
-                    seen |= unsigned(ok) << c;
-                    if (!ok) s[i][c] = -INFINITY;
-                }
+        // an infinite or NaN value in a masked tile: 0 x is not 0
+        float z0 = 0.f, z1 = 0.f;
+        if (edge)
+#pragma unroll 4
+            for (int e = tid; e < kBN * D / 4; e += kThreads) {
+                const float4 v = *reinterpret_cast<const float4 *>(Vs + (e * 4) / D * S::LD + (e * 4) % D);
+                ptx::ffma2(z0, z1, v.x, v.y, 0.f, 0.f, z0, z1);
+                ptx::ffma2(z0, z1, v.z, v.w, 0.f, 0.f, z0, z1);
             }
-            float mx = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
+        const int wild = __syncthreads_or(z0 + z1 != 0.f);
+
+        // ---- masks (every row sees the whole tile, or it is tested key by key)
+        //      and online softmax
+        unsigned seen = 0xffffu;                       // bit kR c + i
+        if (edge) {
+            seen = 0;
 #pragma unroll
-            for (int off = 1; off < 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            const float mn = fmaxf(m[i], mx);
-            const float alpha = mn == -INFINITY ? 1.f : exp2f(m[i] - mn);
+            for (int c = 0; c < 2; ++c) {
+                const int u = lane + 32 * c, key = key_of(kb + u), ahead = key - (pos0 + row0);
+#pragma unroll
+                for (int i = 0; i < kR; ++i)
+                    seen |= unsigned(u < keys && ahead <= i && (ahead > i - p.window || key < p.sinks))
+                            << (kR * c + i);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                s[i][c] = (seen >> (kR * c + i)) & 1u ? (s2[i][c][0] + s2[i][c][1]) * p.qscale : -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+            const float mn = fmaxf(m[i], warp_max(fmaxf(s[i][0], s[i][1])));
+            const float alpha = mn == -INFINITY ? 1.f : ptx::ex2(m[i] - mn);
             m[i] = mn;
-            float sum = 0.f;
+            l[i] *= alpha;                             // of this lane's keys; joined at the end
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const bool ok = (seen >> c) & 1u;
+            for (int c = 0; c < 2; ++c) {
                 // no finite score yet: -inf weighs nothing, NaN stays NaN
-                const float w = mn == -INFINITY && s[i][c] == -INFINITY ? 0.f : exp2f(s[i][c] - mn);
-                if (ok) sum += w;
-                s[i][c] = ok ? w : (wild ? -1.f : 0.f);
+                const float w = s[i][c] == -INFINITY ? 0.f : ptx::ex2(s[i][c] - mn);
+                l[i] += w;
+                s[i][c] = wild && !((seen >> (kR * c + i)) & 1u) ? -1.f : w;
             }
-#pragma unroll
-            for (int off = 1; off < 16; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            l[i] = l[i] * alpha + sum;
 #pragma unroll
             for (int e = 0; e < CH; ++e) acc[i][e] *= alpha;
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<float4 *>(Ps + (tx + 16 * c) * S::LP + 4 * ty) =
-                make_float4(s[0][c], s[1][c], s[2][c], s[3][c]);
-        // rows 4 ty .. 4 ty + 3 of P are written and read by the same half warp
-        __syncwarp();
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < kR; i += 4)
+                *reinterpret_cast<float4 *>(Ps + (lane + 32 * c) * S::LP + row0 + i) =
+                    make_float4(s[i][c], s[i + 1][c], s[i + 2][c], s[i + 3][c]);
+        __syncwarp();                                  // a warp reads its own rows of P
 
-        // ---- O += P V
-        if (edge && wild) {
+        // ---- O += P V, two rows per FFMA2
+        if (wild) {
 #pragma unroll 1
             for (int c = 0; c < keys; ++c) {
-                const float4 w = *reinterpret_cast<const float4 *>(Ps + c * S::LP + 4 * ty);
-                const float wv[4] = {w.x, w.y, w.z, w.w};
+                float v[CH];
+                read<CH>(Vs + c * S::LD + lane * CH, v);
 #pragma unroll
-                for (int e = 0; e < CH; ++e) {
-                    const float v = Vs[c * S::LD + tx * CH + e];
+                for (int i = 0; i < kR; ++i) {
+                    const float w = Ps[c * S::LP + row0 + i];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (!(wv[i] < 0.f)) acc[i][e] = fmaf(wv[i], v, acc[i][e]);
+                    for (int e = 0; e < CH; ++e)
+                        if (!(w < 0.f)) acc[i][e] = fmaf(w, v[e], acc[i][e]);
                 }
             }
         } else {
-#pragma unroll 4
-            for (int c = 0; c < keys; ++c) {
-                const float4 w = *reinterpret_cast<const float4 *>(Ps + c * S::LP + 4 * ty);
-                float v[CH];
-                if constexpr (CH == 2) {
-                    const float2 x = *reinterpret_cast<const float2 *>(Vs + c * S::LD + tx * 2);
-                    v[0] = x.x;
-                    v[1] = x.y;
-                } else {
+            // NK keys at a time, the next NK read ahead; weights (and V) of
+            // keys past the end are zeros
+            constexpr int NK = 4;
+            float wn[NK][kR], vn[NK][CH];
+            auto read_pv = [&](int c) {
 #pragma unroll
-                    for (int e = 0; e < CH; e += 4) {
-                        const float4 x = *reinterpret_cast<const float4 *>(Vs + c * S::LD + tx * CH + e);
-                        v[e] = x.x;
-                        v[e + 1] = x.y;
-                        v[e + 2] = x.z;
-                        v[e + 3] = x.w;
+                for (int k = 0; k < NK; ++k) {
+                    read<CH>(Vs + (c + k) * S::LD + lane * CH, vn[k]);
+#pragma unroll
+                    for (int i = 0; i < kR; i += 4) {
+                        float x[4];
+                        read<4>(Ps + (c + k) * S::LP + row0 + i, x);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) wn[k][i + e] = x[e];
                     }
                 }
+            };
+            read_pv(0);
+#pragma unroll 2
+            for (int c = 0; c < keys; c += NK) {
+                float w[NK][kR], v[NK][CH];
 #pragma unroll
-                for (int e = 0; e < CH; ++e) {
-                    acc[0][e] = fmaf(w.x, v[e], acc[0][e]);
-                    acc[1][e] = fmaf(w.y, v[e], acc[1][e]);
-                    acc[2][e] = fmaf(w.z, v[e], acc[2][e]);
-                    acc[3][e] = fmaf(w.w, v[e], acc[3][e]);
+                for (int k = 0; k < NK; ++k) {
+#pragma unroll
+                    for (int i = 0; i < kR; ++i) w[k][i] = wn[k][i];
+#pragma unroll
+                    for (int e = 0; e < CH; ++e) v[k][e] = vn[k][e];
                 }
+                read_pv(imin(c + NK, kBN - NK));
+#pragma unroll
+                for (int k = 0; k < NK; ++k)
+#pragma unroll
+                    for (int e = 0; e < CH; ++e)
+#pragma unroll
+                        for (int i = 0; i < kR; i += 2)
+                            ptx::ffma2(acc[i][e], acc[i + 1][e], w[k][i], w[k][i + 1], v[k][e], v[k][e], acc[i][e],
+                                       acc[i + 1][e]);
             }
         }
         __syncthreads();                               // V has been read
@@ -282,13 +339,25 @@ __global__ void __launch_bounds__(kThreads) simt_window_kernel(const WinParams p
     }
 
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 4 * ty + i;
-        if (r >= rows) continue;
-        const float inv = 1.f / l[i];
-        T *orow = og + (q0 + r) * p.so.n + tx * CH;
+    for (int off = 1; off < 32; off <<= 1)
 #pragma unroll
-        for (int e = 0; e < CH; ++e) Elem<T>::store(orow + e, acc[i][e] * inv);
+        for (int i = 0; i < kR; ++i) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
+#pragma unroll
+    for (int i = 0; i < kR; ++i) {
+        if (row0 + i >= rows) continue;
+        const float inv = 1.f / l[i];
+        T *orow = og + (q0 + row0 + i) * p.so.n + lane * CH;
+        alignas(16) T x[CH];
+#pragma unroll
+        for (int e = 0; e < CH; ++e) Elem<T>::store(x + e, acc[i][e] * inv);
+        if constexpr (CH * sizeof(T) == 16)
+            *reinterpret_cast<uint4 *>(orow) = *reinterpret_cast<const uint4 *>(x);
+        else if constexpr (CH * sizeof(T) == 8)
+            *reinterpret_cast<uint2 *>(orow) = *reinterpret_cast<const uint2 *>(x);
+        else if constexpr (CH * sizeof(T) == 4)
+            *reinterpret_cast<uint32_t *>(orow) = *reinterpret_cast<const uint32_t *>(x);
+        else
+            *orow = x[0];
     }
 }
 
