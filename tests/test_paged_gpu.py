@@ -446,6 +446,65 @@ def test_allocator_against_the_model(ta, S, P, B, seed):
         m.check()
 
 
+@pytest.mark.parametrize("P", [262143, 600001])
+def test_allocator_on_pools_of_several_spans(ta, P):
+    """More pages than the CTAs of a call hold at once: numbers run on from one
+    span of the pool to the next."""
+    rng = np.random.default_rng(P)
+    B, S, M = 40, 8, P // 16
+    held = rng.permutation(P)[:P * 3 // 5].astype(np.int32)
+    per = len(held) // B
+    table = np.full((B, M), -1, dtype=np.int32)
+    table[:, :per] = held[:per * B].reshape(B, per)
+    refs = np.zeros(P, dtype=np.int32)
+    refs[table[:, :per].ravel()] = 1
+    length = np.full(B, per * S, dtype=np.int32)
+    dt, dr, dl = (torch.from_numpy(x.copy()).cuda() for x in (table, refs, length))
+    # compact, out of place
+    L = int((refs > 0).sum())
+    src, dst = L + np.flatnonzero(refs[L:] > 0), np.flatnonzero(refs[:L] == 0)
+    place = np.where(refs > 0, np.arange(P), -1)
+    place[src] = dst
+    nt, nr = torch.empty_like(dt), torch.empty_like(dr)
+    cs, cd, n = ta.kv_pages_compact(dt, dr, new_table=nt, new_refs=nr)
+    assert n.item() == len(src) == len(dst)
+    assert np.array_equal(cs.cpu().numpy()[:len(src)], src) and np.array_equal(cd.cpu().numpy()[:len(src)], dst)
+    assert (cs[len(src):] == -1).all() and (cd[len(src):] == -1).all()
+    want = np.where(table >= 0, place[table], -1)
+    assert np.array_equal(nt.cpu().numpy(), want)
+    assert np.array_equal(nr.cpu().numpy(), (np.arange(P) < L).astype(np.int32))
+    # reserve nine tenths of what is free, some rows nothing
+    free = np.flatnonzero(refs == 0)
+    add = np.zeros(B, dtype=np.int32)
+    add[1::2] = len(free) * 9 // 10 // (B // 2) * S
+    for b in range(1, B, 2):
+        k = add[b] // S
+        table[b, per:per + k] = free[:k]
+        free = free[k:]
+    refs[table[table >= 0]] = 1
+    ta.kv_pages_reserve(dt, dl, torch.from_numpy(add).cuda(), dr, S)
+    assert ta.device_status() == 0
+    assert np.array_equal(dt.cpu().numpy(), table) and np.array_equal(dr.cpu().numpy(), refs)
+    # one page more than there are
+    add[:] = 0
+    add[0] = (len(free) + 1) * S
+    assert per + len(free) + 1 <= M
+    ta.kv_pages_reserve(dt, dl, torch.from_numpy(add).cuda(), dr, S)
+    assert ta.device_status() == 6
+    assert np.array_equal(dt.cpu().numpy(), table) and np.array_equal(dr.cpu().numpy(), refs)
+    # fork: row 2 (its last page partly filled) over row 4, whose pages are let go
+    dl[2] -= 3
+    ta.kv_pages_fork(dt, dl, dr, torch.tensor([2], dtype=torch.int32, device="cuda"),
+                     torch.tensor([4], dtype=torch.int32, device="cuda"), S)
+    assert ta.device_status() == 0
+    refs[table[4, :per]] -= 1
+    refs[table[2, :per - 1]] += 1
+    table[4, :per - 1] = table[2, :per - 1]
+    table[4, per - 1] = np.flatnonzero(refs == 0)[0]
+    refs[table[4, per - 1]] = 1
+    assert np.array_equal(dt.cpu().numpy(), table) and np.array_equal(dr.cpu().numpy(), refs)
+
+
 def test_reserve_is_all_or_nothing(ta):
     m = Model(ta, 3, 8, 10, 8)
     assert m.reserve([30, 0, 20])               # 4 + 3 pages

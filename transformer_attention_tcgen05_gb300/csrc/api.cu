@@ -494,7 +494,7 @@ static attn_status_t check_pool(const void *table, int B, int num_pages, int pag
         return ATTN_ERR_INVALID_ARG;
     if (B > 1 && table_stride < max_pages) return ATTN_ERR_INVALID_ARG;
     if ((long long)max_pages * page_size >= (1ll << 31) || B > (1 << 20) ||
-        num_pages > 0x7fff0000 || table_stride > (1ll << 40))
+        num_pages > 0x7ff00000 || table_stride > (1ll << 40))
         return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
 }
