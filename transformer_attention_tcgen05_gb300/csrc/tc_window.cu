@@ -19,8 +19,8 @@
 //    leading tile goes first, for the first query tile alone, so that each
 //    works in consecutive steps.)  4096 tokens, 32 heads on 8, window 1024,
 //    sinks 4, D 128: 86.1 us with row pairs and one general mask, 74.4 us so.
-//  * The pairs that do not fill a last round of the SMs are split into single
-//    query tiles, so that the round ends sooner.
+//  * The pairs of a last round that takes at most half of the SMs are split into
+//    single query tiles, so that the round ends sooner.
 //  * One CTA per item.  A persistent form (K and V of the next pair streaming in
 //    behind the current one's, its first scores computed during the epilogue)
 //    measured slower: 81 against 74.4 us at 4096 tokens, 1580 against 1467 us at
@@ -97,7 +97,7 @@ struct WnParams {
     unsigned *err;
     int H, group, BH;        // query heads, query heads per KV head, batch * heads
     int pairs;               // query tile pairs
-    int G;                   // SMs: pairs per round
+    int whole;               // pairs that are not split
     int by_head;             // a pair is two heads of one KV head (else two row tiles)
     // operands and element strides (rows redone outside the tensor cores; o)
     const void *q, *k, *v;
@@ -141,20 +141,12 @@ struct Item {
     }
 };
 
-// This CTA's item.  Rounds of whole pairs, late queries first, then the rest as
-// single tiles.
+// This CTA's item: whole pairs, late queries first, then the rest as single
+// tiles.
 __device__ __forceinline__ Item get_item(const WnParams &p) {
     Item w;
-    const int G = p.G, k = blockIdx.x / G, c = blockIdx.x - k * G;
-    const int rounds = p.pairs / G;
-    int pair, half = -1;
-    if (k < rounds) {
-        pair = k * G + c;
-    } else {
-        const int s = (k - rounds) * G + c;
-        pair = rounds * G + (s >> 1);
-        half = s & 1;
-    }
+    const int s = int(blockIdx.x) - p.whole;
+    const int pair = s < 0 ? int(blockIdx.x) : p.whole + (s >> 1), half = s < 0 ? -1 : s & 1;
     const int hp = p.by_head ? p.BH / 2 : p.BH;          // pairs (or heads) per row block
     const int qb = (p.pairs / hp - 1) - pair / hp, bh = (pair % hp) * (p.by_head ? 2 : 1);
     w.dq = p.by_head ? 0 : kBM;
@@ -714,7 +706,7 @@ attn_status_t launch_window(const Ctx &c, const CUtensorMap &tq, const CUtensorM
     }
     if (regs != C::REGS_LAUNCH) return ATTN_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.pairs / p.G * p.G + 2 * (p.pairs % p.G));
+    cfg.gridDim = dim3(p.whole + 2 * (p.pairs - p.whole));
     cfg.blockDim = dim3(C::NT);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = c.stream;
@@ -760,7 +752,10 @@ attn_status_t tc_causal_window(const Ctx &c, attn_dtype_t dt, const void *q, con
     p.BH = B * Hq;
     p.pairs = int(pairs);
     p.by_head = by_head;
-    p.G = imax(1, c.sm_count);
+    // the pairs of a last round that takes at most half of the SMs go out as
+    // single tiles, on twice as many
+    const int rest = p.pairs % imax(1, c.sm_count);
+    p.whole = 2 * rest <= c.sm_count ? p.pairs - rest : p.pairs;
     p.q = q; p.k = k; p.v = v; p.o = o;
     p.sq = st[0]; p.sk = st[1]; p.sv = st[2];
     p.o_sb = st[3].b; p.o_sh = st[3].h; p.o_sn = st[3].n;
