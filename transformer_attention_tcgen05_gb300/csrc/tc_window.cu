@@ -7,8 +7,10 @@
 // S and O live in tensor memory, P goes back there in 16 bits (over S at
 // D = 128), thread = query row in two softmax warpgroups, one thread issues every
 // MMA.  Bound by the exponentials and the tensor pipe at about 1.4 us per step of
-// two tiles, plus about 8 us per CTA (set-up, first loads, masked tiles, last
-// P V and epilogue), which is what a short window pays for.  What differs:
+// two tiles, plus about 6 us per CTA (set-up, first loads, masked tiles, last
+// P V and epilogue), which is what a short window pays for: 4096 tokens, 32 heads
+// on 8, window 1024, sinks 4, D 128: 65.7 us = 918 TFLOP/s; 32768 tokens, window
+// 4096: 1440 us = 1433 TFLOP/s.  What differs:
 //
 //  * Key tile list.  A CTA streams the sink tiles and the tiles of its windows
 //    only; tiles on an edge (diagonal, window start, sinks) are masked per
@@ -17,10 +19,16 @@
 //    of one KV head: one key range, no step that serves one tile alone.  (Pairs
 //    of row tiles, which odd groups use, see windows one key tile apart: the
 //    leading tile goes first, for the first query tile alone, so that each
-//    works in consecutive steps.)  4096 tokens, 32 heads on 8, window 1024,
-//    sinks 4, D 128: 86.1 us with row pairs and one general mask, 74.4 us so.
+//    works in consecutive steps.)  The 4096 tokens above: 86.1 us with row pairs
+//    and one general mask, 74.4 us so.
 //  * The pairs of a last round that takes at most half of the SMs are split into
-//    single query tiles, so that the round ends sooner.
+//    single query tiles, so that the round ends sooner (1024 tokens, window 256:
+//    19.2 us with any remainder split, 13.0 us so).
+//  * A tile that holds a few sinks only (32 at most) is a step of 32 keys
+//    (74.0 -> 71.4 us), output rows leave through shared memory as whole rows
+//    (70.0 -> 66.7 us), and what the first scores wait for comes first: the
+//    loaders' item and tensor maps during the set-up, then one query tile and one
+//    key tile (66.7 -> 65.7 us; 5 tokens 4.7 -> 4.1 us).
 //  * One CTA per item.  A persistent form (K and V of the next pair streaming in
 //    behind the current one's, its first scores computed during the epilogue)
 //    measured slower: 81 against 74.4 us at 4096 tokens, 1580 against 1467 us at
@@ -109,7 +117,7 @@ struct WnParams {
 // Barrier block at OFF_BAR.
 template <int KS, int VS>
 struct Bars {
-    uint64_t q_full;
+    uint64_t q_full[kNQ];
     uint64_t k_full[KS], k_empty[KS], v_full[VS], v_empty[VS];
     // per query tile t: s_full its Q K^T has completed, p_ready the softmax
     // has written P, o_done the P V product that read P has completed,
@@ -247,7 +255,6 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     constexpr int BNt = C::BN;     // keys per tile
 
     if (warp == C::W_INIT && lane == 0) {
-        ptx::mbar_init(&bars->q_full, 1);
         for (int s = 0; s < C::KS; ++s) {
             ptx::mbar_init(&bars->k_full[s], 1);
             ptx::mbar_init(&bars->k_empty[s], 1);
@@ -257,6 +264,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             ptx::mbar_init(&bars->v_empty[s], 1);
         }
         for (int t = 0; t < kNQ; ++t) {
+            ptx::mbar_init(&bars->q_full[t], 1);
             ptx::mbar_init(&bars->s_full[t], 1);
             ptx::mbar_init(&bars->p_ready[t], 128);
             ptx::mbar_init(&bars->o_done[t], 1);
@@ -269,6 +277,12 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     if (warp == C::W_MMA) {
         ptx::tmem_alloc(&bars->tmem_base, C::TM_COLS);
         ptx::tmem_relinquish();
+    }
+    Item load_item;                                    // the loaders', while the rest is set up
+    if (warp == C::W_LOAD || warp == C::W_LOADV) {
+        ptx::prefetch_tmap(warp == C::W_LOAD ? &tk : &tv);
+        if (warp == C::W_LOAD) ptx::prefetch_tmap(&tq);
+        load_item = get_item(p);
     }
     ptx::tc_fence_before();
     __syncthreads();
@@ -288,20 +302,18 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             uint64_t *full = which == 0 ? bars->k_full : bars->v_full;
             uint64_t *empty = which == 0 ? bars->k_empty : bars->v_empty;
             const int NS = which == 0 ? C::KS : C::VS;   // depth of this ring
-            const Item w = get_item(p);
-            ptx::prefetch_tmap(tm);
-            const uint64_t pol_kv = ptx::l2_policy_evict_last();
-            if (which == 0 && w.steps > 0) {
-                ptx::prefetch_tmap(&tq);
-                const uint64_t pol_q = ptx::l2_policy_evict_first();
-                const int tiles = w.n[1] > 0 ? kNQ : 1;
-                ptx::mbar_arrive_expect_tx(&bars->q_full, tiles * C::Q_BYTES);
-                for (int t = 0; t < tiles; ++t)
-                    for (int pn = 0; pn < C::PANELS; ++pn)
-                        ptx::tma_load_4d(smem + C::OFF_Q + t * C::Q_BYTES + pn * C::PANEL_Q, &tq, pn * 64,
-                                         w.q0 + t * w.dq, w.fh + t * w.dh, w.fb, &bars->q_full, pol_q);
-            }
-            int issued = 0;
+            const uint64_t pol_kv = ptx::l2_policy_evict_last(), pol_q = ptx::l2_policy_evict_first();
+            const Item w = load_item;
+            int q_out = 0, issued = 0;
+            auto load_q = [&](int t) {
+                if (t >= (w.n[1] > 0 ? kNQ : 1)) return;
+                ++q_out;
+                ptx::mbar_arrive_expect_tx(&bars->q_full[t], C::Q_BYTES);
+                for (int pn = 0; pn < C::PANELS; ++pn)
+                    ptx::tma_load_4d(smem + C::OFF_Q + t * C::Q_BYTES + pn * C::PANEL_Q, &tq, pn * 64,
+                                     w.q0 + t * w.dq, w.fh + t * w.dh, w.fb, &bars->q_full[t], pol_q);
+            };
+            if (which == 0 && w.steps > 0) load_q(0);
             for (int j = 0; j < w.steps; ++j) {
                 const int s = j % NS;
                 if (j >= NS && !ptx::mbar_wait_or_abort(&empty[s], ((j / NS) - 1) & 1, p.err, abort)) break;
@@ -310,11 +322,13 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 for (int pn = 0; pn < C::PANELS; ++pn)
                     ptx::tma_load_4d(smem + (which == 0 ? C::k_off(s) : C::v_off(s)) + pn * C::PANEL_KV, tm,
                                      pn * 64, w.tile(j) * kBN, w.fkh, w.fb, &full[s], pol_kv);
+                // the first scores need one query tile and the first keys
+                if (which == 0 && j == 0) load_q(1);
             }
             // after a timeout elsewhere: let the copies this thread issued land
             // (bounded) before the CTA's shared memory is released
             if (*abort) {
-                if (which == 0 && w.steps > 0) ptx::mbar_wait(&bars->q_full, 0, nullptr);
+                for (int t = 0; t < q_out; ++t) ptx::mbar_wait(&bars->q_full[t], 0, nullptr);
                 for (int j = imax(0, issued - NS); j < issued; ++j)
                     ptx::mbar_wait(&full[j % NS], (j / NS) & 1, nullptr);
             }
@@ -392,10 +406,11 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 ptx::tc_fence_after();
                 issue_pv(t, j, j == w.f[t]);
             };
-            ok = ok && ptx::mbar_wait_or_abort(&bars->q_full, 0, p.err, abort);
 #pragma unroll
-            for (int t = 0; t < kNQ; ++t)
+            for (int t = 0; t < kNQ; ++t) {
+                if (w.n[t] > 0) ok = ok && ptx::mbar_wait_or_abort(&bars->q_full[t], 0, p.err, abort);
                 if (ok) qk(t, 0);
+            }
             if (ok) ptx::tc_commit(&bars->k_empty[0]);
             for (int j = 0; ok && j < w.steps; ++j) {
                 const int jn = j + 1;
@@ -640,39 +655,49 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         // ---- epilogue: O / l -> 16-bit -> global
         if (ok && nt > 0 && wait_pv(nt - 1)) {
             const float inv = 1.f / l;
-            const int qi = w.q0 + t * w.dq + row, qh = w.fh + t * w.dh;
-            const bool qvalid = qi < p.Nq;
+            int ln = threadIdx.x & 31;           // opaque: nothing of the epilogue is computed ahead
+            asm volatile("" : "+r"(ln));
+            const int q_first = w.q0 + t * w.dq + quarter * 32, qh = w.fh + t * w.dh;   // the warp's first row
+            constexpr int CH = D / 8;            // 16-byte columns of a row
+            // the warp's 32 rows pass through the query tile's memory (every Q K^T
+            // has completed), column c of row r at c ^ (r & 7), so that whole rows
+            // go out instead of 32 rows' 16 bytes
+            uint8_t *stage = smem + C::OFF_Q + t * C::Q_BYTES + quarter * 32 * D * 2;
             bool finite = true;
-            typename H16<F16>::T *orow = nullptr;
-            if (qvalid)
-                orow = static_cast<typename H16<F16>::T *>(p.o) +
-                       size_t(w.fb * p.o_sb + qh * p.o_sh + (long long)qi * p.o_sn);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t ov[32];
-                ptx::tmem_ld32(o_addr + c * 32, ov);
+            for (int half = 0; half < D / 64; ++half) {
+                float ov[64];
+                ptx::tmem_ld32(o_addr + half * 64, *reinterpret_cast<uint32_t(*)[32]>(&ov[0]));
+                ptx::tmem_ld32(o_addr + half * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&ov[32]));
                 ptx::tmem_wait_ld();
-                if (qvalid) {
-                    uint4 w4[4];
-                    uint32_t *wp = reinterpret_cast<uint32_t *>(w4);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        wp[e] = H16<F16>::pack(__uint_as_float(ov[2 * e]) * inv,
-                                               __uint_as_float(ov[2 * e + 1]) * inv);
-                    uint4 *dst = reinterpret_cast<uint4 *>(orow + c * 32);
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t x[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) dst[e] = w4[e];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        finite = finite && fabsf(__uint_as_float(ov[e]) * inv) < INFINITY;
+                    for (int e = 0; e < 4; ++e) {
+                        const float x0 = ov[c * 8 + 2 * e] * inv, x1 = ov[c * 8 + 2 * e + 1] * inv;
+                        finite = finite && fabsf(x0) < INFINITY && fabsf(x1) < INFINITY;
+                        x[e] = H16<F16>::pack(x0, x1);
+                    }
+                    *reinterpret_cast<uint4 *>(stage + (ln * CH + half * 8 + (c ^ (ln & 7))) * 16) =
+                        make_uint4(x[0], x[1], x[2], x[3]);
                 }
             }
-            unsigned redo = __ballot_sync(0xffffffffu, !finite);
+            __syncwarp();
+            unsigned redo = __ballot_sync(0xffffffffu, !finite && q_first + ln < p.Nq);
+            typename H16<F16>::T *const o0 = static_cast<typename H16<F16>::T *>(p.o) + w.fb * p.o_sb + qh * p.o_sh;
+            const int col = ln % CH;
+#pragma unroll
+            for (int r0 = 0; r0 < 32; r0 += 32 / CH) {
+                const int r = r0 + ln / CH;
+                const uint4 x = *reinterpret_cast<const uint4 *>(stage + (r * CH + (col ^ (r & 7))) * 16);
+                if (q_first + r < p.Nq && !((redo >> r) & 1u))
+                    *reinterpret_cast<uint4 *>(o0 + (q_first + r) * p.o_sn + col * 8) = x;
+            }
             while (redo) {
                 const int r = __ffs(redo) - 1;
                 redo &= redo - 1;
-                __syncwarp();
-                window_row<D, F16>(p, w.fb, qh, w.fkh, w.q0 + t * w.dq + quarter * 32 + r);
+                window_row<D, F16>(p, w.fb, qh, w.fkh, q_first + r);
             }
         }
     }
