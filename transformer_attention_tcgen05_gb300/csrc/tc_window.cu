@@ -34,6 +34,10 @@
 //    measured slower: 81 against 74.4 us at 4096 tokens, 1580 against 1467 us at
 //    32768 tokens with a window of 4096 (1406 TFLOP/s).
 //
+// Roundings: S, the statistics, row sums and O are fp32.  P is rounded to the 16-bit
+// type (half a step of each weight) because the tensor core takes it as an
+// operand beside V; the sum takes the weights before that.  O is rounded once.
+//
 // A key that a row does not see does not change its output even if its value is
 // infinite or NaN: such a row is redone from its own keys (window_row).
 //
