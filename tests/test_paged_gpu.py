@@ -564,6 +564,28 @@ def test_free_reports_pages_that_are_not_counted(ta):
     assert table.tolist() == [[-1, 1, -1, 7]] and refs.tolist() == [0, 0, 1, 0]
 
 
+@pytest.mark.parametrize("M", [3, 1500])           # tables written by the call's first and second kernel
+def test_compact_of_the_smallest_pools(ta, M):
+    for P, live in ((1, [0]), (1, []), (2, [1]), (3, [2]), (5, [1, 3, 4])):
+        table = torch.full((2, M), -1, dtype=torch.int32, device="cuda")
+        refs = torch.zeros(P, dtype=torch.int32, device="cuda")
+        for i, page in enumerate(live):
+            table[i % 2, M - 1 - i // 2] = page
+            refs[page] = 1
+        place = {}
+        holes = [x for x in range(len(live)) if x not in live]
+        for page in live:
+            place[page] = page if page < len(live) else holes.pop(0)
+        want = torch.tensor([[place.get(x, -1) for x in row] for row in table.tolist()], dtype=torch.int32)
+        cs, cd, n = ta.kv_pages_compact(table, refs)
+        assert ta.device_status() == 0
+        moves = [(x, y) for x, y in place.items() if x != y]
+        assert len(cs) == len(cd) == P // 2 and n.tolist() == [len(moves)]
+        assert list(zip(cs.tolist(), cd.tolist()))[:len(moves)] == moves
+        assert torch.equal(table.cpu(), want)
+        assert refs.tolist() == [1] * len(live) + [0] * (P - len(live))
+
+
 def test_free_leaves_rows_of_impossible_lengths(ta):
     table = torch.tensor([[0, 1], [2, -1], [3, 4]], dtype=torch.int32, device="cuda")
     refs = torch.ones(5, dtype=torch.int32, device="cuda")

@@ -160,6 +160,15 @@ PyObject *done(attn_status_t st, const char *where) {
     throw PyFail();
 }
 
+// n entries of a one-axis tensor from `at` on: an output of its own that shares
+// an allocation (an allocation costs as much as a launch).
+at::Tensor part(const at::Tensor &t, int64_t at, int64_t n) {
+    at::Tensor x = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(t.storage()), t.key_set(), t.dtype());
+    x.unsafeGetTensorImpl()->set_storage_offset(at);
+    x.unsafeGetTensorImpl()->set_sizes_contiguous(n);
+    return x;
+}
+
 PyObject *wrap(const at::Tensor &t) { return THPVariable_Wrap(t); }
 
 // The output: the caller's (checked by the shape and dtype of `like`) or a new
@@ -281,7 +290,8 @@ PyObject *kv_pages_fork(PyObject *const *a) {
     const int n = to_int(c.take(a[3], "src").numel());
     const int32_t *src = c.ints(a[3], "src", n), *dst = c.ints(a[4], "dst", n);
     const Workspace ws(c, a[6], attn_kv_pages_workspace_bytes(P), false, r);
-    const at::Tensor cs = at::empty({n}, r.options()), cd = at::empty({n}, r.options());
+    const at::Tensor lists = at::empty({2 * int64_t(n)}, r.options());
+    const at::Tensor cs = part(lists, 0, n), cd = part(lists, n, n);
     if (n > 0)
         done(attn_kv_pages_fork(t.p, sl, refs, src, dst, n, static_cast<int32_t *>(cs.data_ptr()),
                                 static_cast<int32_t *>(cd.data_ptr()), t.B, P, integer(a[5]), t.M, t.stride,
@@ -301,8 +311,9 @@ PyObject *kv_pages_compact(PyObject *const *a) {
     const int32_t *refs = c.ints(a[1], "page_refs", P);
     int32_t *nr = c.ints(a[3] == Py_None ? a[1] : a[3], "new_refs", P);
     const Workspace ws(c, a[4], attn_kv_pages_workspace_bytes(P), false, r);
-    const at::Tensor cs = at::empty({P / 2}, r.options()), cd = at::empty({P / 2}, r.options()),
-                     n = at::empty({1}, r.options());
+    const int64_t cap = P / 2;
+    const at::Tensor lists = at::empty({2 * cap + 1}, r.options());
+    const at::Tensor cs = part(lists, 0, cap), cd = part(lists, cap, cap), n = part(lists, 2 * cap, 1);
     done(attn_kv_pages_compact(t.p, refs, nt.p, nr, static_cast<int32_t *>(cs.data_ptr()),
                                static_cast<int32_t *>(cd.data_ptr()), static_cast<int32_t *>(n.data_ptr()),
                                t.B, P, t.M, t.stride, nt.stride, ws.ptr(), ws.bytes(), c.stream()),

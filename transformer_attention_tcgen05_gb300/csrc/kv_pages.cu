@@ -312,7 +312,8 @@ struct AllocParams {
     const int32_t *src, *dst;
     int n;
     int32_t *copy_src, *copy_dst, *count;
-    int32_t *new_refs;
+    int32_t *new_refs, *new_table;
+    long long new_stride;
     int32_t *ws;                                       // [P]
     int quads;                                         // 16-byte reads of a chunk's counts per lane
     unsigned *err;
@@ -774,9 +775,19 @@ __global__ void __launch_bounds__(kAT, 1) fork_kernel(const AllocParams p) {
     }
 }
 
+// A table entry behind a compaction (the map is complete).
+__device__ __forceinline__ int moved(const AllocParams &p, int e) {
+    if (e == -1) return -1;
+    const int to = e >= 0 && e < p.P ? p.ws[e] : -1;
+    if (to < 0) raise_device_error(p.err, kDevCheck);
+    return to;
+}
+
 // Compact: with L live pages, the k-th live page at or above L moves to the
 // k-th free page below L.  Lists the moves, fills the map old -> new (ws[page],
-// -1 for a page that is not live) and writes the new counts.
+// -1 for a page that is not live) and writes the new counts, and the new table
+// too if it is short (TABLE).
+template <bool TABLE>
 __global__ void __launch_bounds__(kAT, 1) compact_kernel(const AllocParams p) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -844,10 +855,28 @@ __global__ void __launch_bounds__(kAT, 1) compact_kernel(const AllocParams p) {
         else if (p.refs[i] > 0)
             p.new_refs[i] = p.refs[i];
     }
+    if (TABLE) {
+        constexpr int U = 2;                           // entries per thread
+        const int n = p.B * p.M;
+        for (int x0 = t; x0 < n; x0 += U * step) {
+            int e[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int x = x0 + u * step;
+                e[u] = x < n ? p.table[x / p.M * p.stride + x % p.M] : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int x = x0 + u * step;
+                e[u] = moved(p, e[u]);
+                if (x < n) p.new_table[x / p.M * p.new_stride + x % p.M] = e[u];
+            }
+        }
+    }
 }
 
-__global__ void __launch_bounds__(256) remap_kernel(const AllocParams p, int32_t *out,
-                                                    long long out_stride, int blocks) {
+// The table of a large call.
+__global__ void __launch_bounds__(256) remap_kernel(const AllocParams p, int blocks) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int b = blockIdx.x / blocks, j0 = (blockIdx.x % blocks) * 1024;
@@ -860,12 +889,7 @@ __global__ void __launch_bounds__(256) remap_kernel(const AllocParams p, int32_t
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         const int i = j0 + u * 256 + threadIdx.x;
-        if (i >= p.M) break;
-        if (e[u] != -1) {
-            e[u] = e[u] >= 0 && e[u] < p.P ? p.ws[e[u]] : -1;
-            if (e[u] < 0) raise_device_error(p.err, kDevCheck);
-        }
-        out[b * out_stride + i] = e[u];
+        if (i < p.M) p.new_table[b * p.new_stride + i] = moved(p, e[u]);
     }
 }
 
@@ -1015,9 +1039,16 @@ attn_status_t kv_pages_compact(const Ctx &c, const PageTable &t, const int32_t *
     if ((long long)t.B * blocks > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
     const int ctas = cluster_size(t.P);
     p.quads = chunk_quads(t.P, ctas);
-    const attn_status_t st = launch_pdl(c, compact_kernel, dim3(ctas), kAT, ctas, 0, p);
+    p.new_table = new_table;
+    p.new_stride = new_stride;
+    // a table of up to 2 entries per thread saves a launch (host side of a call
+    // 7.2 -> 5.5 us); with 8 each the launch is faster (72.3 against 75.5 us with
+    // the copy of 1440 pages)
+    if ((long long)t.B * t.max_pages <= 2ll * kAT * ctas)
+        return launch_pdl(c, compact_kernel<true>, dim3(ctas), kAT, ctas, 0, p);
+    const attn_status_t st = launch_pdl(c, compact_kernel<false>, dim3(ctas), kAT, ctas, 0, p);
     if (st != ATTN_OK) return st;
-    return launch_pdl(c, remap_kernel, dim3(t.B * blocks), 256, 1, 0, p, new_table, new_stride, blocks);
+    return launch_pdl(c, remap_kernel, dim3(t.B * blocks), 256, 1, 0, p, blocks);
 }
 
 }  // namespace attn
