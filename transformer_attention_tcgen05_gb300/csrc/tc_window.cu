@@ -6,11 +6,11 @@
 // (tc_flash.cu): a CTA's two 128-row query tiles share a stream of 128-key tiles,
 // S and O live in tensor memory, P goes back there in 16 bits (over S at
 // D = 128), thread = query row in two softmax warpgroups, one thread issues every
-// MMA.  Bound by the exponentials and the tensor pipe at about 1.4 us per step of
+// MMA.  Bound by the exponentials and the tensor pipe at about 1.2 us per step of
 // two tiles, plus about 6 us per CTA (set-up, first loads, masked tiles, last
 // P V and epilogue), which is what a short window pays for: 4096 tokens, 32 heads
-// on 8, window 1024, sinks 4, D 128: 65.7 us = 918 TFLOP/s; 32768 tokens, window
-// 4096: 1440 us = 1433 TFLOP/s.  What differs:
+// on 8, window 1024, sinks 4, D 128: 59.3 us = 1018 TFLOP/s; 32768 tokens, window
+// 4096: 1249 us = 1652 TFLOP/s.  What differs:
 //
 //  * Key tile list.  A CTA streams the sink tiles and the tiles of its windows
 //    only; tiles on an edge (diagonal, window start, sinks) are masked per
@@ -336,8 +336,12 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 for (int j = imax(0, issued - NS); j < issued; ++j)
                     ptx::mbar_wait(&full[j % NS], (j / NS) & 1, nullptr);
             }
-        } else if (warp == C::W_MMA && lane == 0) {
-            // ============================================= MMA issuer
+        } else if (warp == C::W_MMA) {
+            // ============================================= MMA issuer: the whole
+            // warp walks the steps, so that all it computes is uniform, and one
+            // thread issues (with a single thread in the branch the operands of every
+            // MMA passed through vector registers: 65.3 and 1435 us)
+            const bool lead = ptx::elect_one();
             const uint32_t id_qk = ptx::idesc_16_f32(kBM, BNt, false, F16);
             const uint32_t id_few = ptx::idesc_16_f32(kBM, kFew, false, F16);
             const uint32_t id_pv = ptx::idesc_16_f32(kBM, D, true, F16);
@@ -350,6 +354,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             constexpr int nkv = BNt / 16;                // k-steps of P V
             const Item w = get_item(p);
             auto issue_qk = [&](int t, int gk) {
+                if (!lead) return;
                 const uint32_t id = w.few && gk == 0 ? id_few : id_qk;
                 const uint32_t a0 = dq0 + uint32_t((t * C::Q_BYTES) >> 4);
                 const uint32_t b0 = dk0 + uint32_t(((gk % C::KS) * C::KV_BYTES) >> 4);
@@ -363,6 +368,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 ptx::tc_commit(&bars->s_full[t]);
             };
             auto issue_pv = [&](int t, int gv, bool first) {
+                if (!lead) return;
                 const uint32_t b0 = dv0 + uint32_t(((gv % C::VS) * C::KV_BYTES) >> 4);
                 const uint32_t a0 = tmem + C::tm_p(t);
 #pragma unroll
@@ -415,7 +421,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 if (w.n[t] > 0) ok = ok && ptx::mbar_wait_or_abort(&bars->q_full[t], 0, p.err, abort);
                 if (ok) qk(t, 0);
             }
-            if (ok) ptx::tc_commit(&bars->k_empty[0]);
+            if (ok && lead) ptx::tc_commit(&bars->k_empty[0]);
             for (int j = 0; ok && j < w.steps; ++j) {
                 const int jn = j + 1;
                 k_seen = v_seen = false;
@@ -434,11 +440,13 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                     }
                 }
                 if (!ok) break;
-                if (jn < w.steps) ptx::tc_commit(&bars->k_empty[jn % C::KS]);
-                ptx::tc_commit(&bars->v_empty[j % C::VS]);
+                if (lead) {
+                    if (jn < w.steps) ptx::tc_commit(&bars->k_empty[jn % C::KS]);
+                    ptx::tc_commit(&bars->v_empty[j % C::VS]);
+                }
             }
             // drain: every MMA has completed before TMEM is freed
-            ptx::tc_commit(&bars->drain);
+            if (lead) ptx::tc_commit(&bars->drain);
             ptx::mbar_wait(&bars->drain, 0, p.err);
         }
     } else {
