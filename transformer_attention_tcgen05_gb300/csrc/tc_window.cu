@@ -9,8 +9,8 @@
 // MMA.  Bound by the exponentials and the tensor pipe at about 1.2 us per step of
 // two tiles, plus about 6 us per CTA (set-up, first loads, masked tiles, last
 // P V and epilogue), which is what a short window pays for: 4096 tokens, 32 heads
-// on 8, window 1024, sinks 4, D 128: 59.3 us = 1018 TFLOP/s; 32768 tokens, window
-// 4096: 1249 us = 1652 TFLOP/s.  What differs:
+// on 8, window 1024, sinks 4, D 128: 58.9 us = 1024 TFLOP/s; 32768 tokens, window
+// 4096: 1225 us = 1684 TFLOP/s.  What differs:
 //
 //  * Key tile list.  A CTA streams the sink tiles and the tiles of its windows
 //    only; tiles on an edge (diagonal, window start, sinks) are masked per
@@ -102,15 +102,34 @@ struct WnCfg {
     static constexpr int v_off(int s) { return OFF_V + s * KV_BYTES; }
 };
 
+// Division by a number that a launch knows: n / d by a multiplication (every CTA
+// starts with three of them, and everything waits for its loaders).
+struct Div {
+    unsigned mul;
+    int sh, d;
+    Div() = default;
+    explicit Div(int n) : d(n) {
+        int l = 0;
+        while ((1ll << l) < d) ++l;
+        mul = unsigned((((1ull << l) - d) << 32) / unsigned(d) + 1);
+        sh = l - 1;
+    }
+    __device__ __forceinline__ int operator()(int n) const {
+        const unsigned t = __umulhi(mul, unsigned(n));
+        return d == 1 ? n : int((t + ((unsigned(n) - t) >> 1)) >> sh);
+    }
+};
+
 struct WnParams {
     int Nq, Nkv;             // query / key tokens per (batch, head)
     int off, window, sinks;  // query i sits at position off + i
     float c_log2;            // scale * log2(e)
     unsigned *err;
-    int H, group, BH;        // query heads, query heads per KV head, batch * heads
     int pairs;               // query tile pairs
     int whole;               // pairs that are not split
     int by_head;             // a pair is two heads of one KV head (else two row tiles)
+    int blocks;              // row blocks
+    Div by_hp, by_h, by_group;   // pairs (or heads) per row block, heads, heads per KV head
     // operands and element strides (rows redone outside the tensor cores; o)
     const void *q, *k, *v;
     void *o;
@@ -159,13 +178,13 @@ __device__ __forceinline__ Item get_item(const WnParams &p) {
     Item w;
     const int s = int(blockIdx.x) - p.whole;
     const int pair = s < 0 ? int(blockIdx.x) : p.whole + (s >> 1), half = s < 0 ? -1 : s & 1;
-    const int hp = p.by_head ? p.BH / 2 : p.BH;          // pairs (or heads) per row block
-    const int qb = (p.pairs / hp - 1) - pair / hp, bh = (pair % hp) * (p.by_head ? 2 : 1);
+    const int block = p.by_hp(pair), qb = p.blocks - 1 - block;
+    const int bh = (pair - block * p.by_hp.d) * (p.by_head ? 2 : 1);
     w.dq = p.by_head ? 0 : kBM;
     w.dh = p.by_head ? 1 : 0;
-    w.fb = bh / p.H;
-    w.fh = bh % p.H + (half > 0 ? w.dh : 0);
-    w.fkh = w.fh / p.group;
+    w.fb = p.by_h(bh);
+    w.fh = bh - w.fb * p.by_h.d + (half > 0 ? w.dh : 0);
+    w.fkh = p.by_group(w.fh);
     w.q0 = qb * (p.by_head ? kBM : kNQ * kBM) + (half > 0 ? w.dq : 0);
     const int pos = p.off + w.q0;
     const bool one = w.q0 < p.Nq, two = half < 0 && w.q0 + w.dq < p.Nq;
@@ -784,9 +803,10 @@ attn_status_t tc_causal_window(const Ctx &c, attn_dtype_t dt, const void *q, con
     p.sinks = sinks;
     p.c_log2 = scale * kLog2e;
     p.err = c.err;
-    p.H = Hq;
-    p.group = Hq / Hkv;
-    p.BH = B * Hq;
+    p.blocks = cdiv(Nq, by_head ? kBM : kNQ * kBM);
+    p.by_hp = Div(by_head ? B * Hq / 2 : B * Hq);
+    p.by_h = Div(Hq);
+    p.by_group = Div(Hq / Hkv);
     p.pairs = int(pairs);
     p.by_head = by_head;
     // the pairs of a last round that takes at most half of the SMs go out as
