@@ -9,8 +9,8 @@
 // MMA.  Bound by the exponentials and the tensor pipe at about 1.2 us per step of
 // two tiles, plus about 6 us per CTA (set-up, first loads, masked tiles, last
 // P V and epilogue), which is what a short window pays for: 4096 tokens, 32 heads
-// on 8, window 1024, sinks 4, D 128: 58.9 us = 1024 TFLOP/s; 32768 tokens, window
-// 4096: 1225 us = 1684 TFLOP/s.  What differs:
+// on 8, window 1024, sinks 4, D 128: 58.8 us = 1026 TFLOP/s; 32768 tokens, window
+// 4096: 1220 us = 1692 TFLOP/s.  What differs:
 //
 //  * Key tile list.  A CTA streams the sink tiles and the tiles of its windows
 //    only; tiles on an edge (diagonal, window start, sinks) are masked per
@@ -31,8 +31,11 @@
 //    key tile (66.7 -> 65.7 us; 5 tokens 4.7 -> 4.1 us).
 //  * One CTA per item.  A persistent form (K and V of the next pair streaming in
 //    behind the current one's, its first scores computed during the epilogue)
-//    measured slower: 81 against 74.4 us at 4096 tokens, 1580 against 1467 us at
-//    32768 tokens with a window of 4096 (1406 TFLOP/s).
+//    measured slower: 60.1 against 58.8 us at 4096 tokens, 1272 against 1220 us at
+//    32768 tokens with a window of 4096: both query tiles end together, and their
+//    epilogue keeps the softmax warps from the next pair.
+//  * One thread per row.  Two (16 softmax warps, half of the keys each) took 63.2
+//    against 59.3 us, P V in two halves behind the exponentials 58.8 against 58.3.
 //
 // Roundings: S, the statistics, row sums and O are fp32.  P is rounded to the 16-bit
 // type (half a step of each weight) because the tensor core takes it as an
