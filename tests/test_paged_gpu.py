@@ -122,6 +122,22 @@ def test_decode_paged_parity(ta, dt, lens, Hq, Hkv, D, S, window, sinks, order):
     check(dt, q, ks, vs, lens, o, window, sinks)
 
 
+@pytest.mark.parametrize("dt,lens,Hq,Hkv,D,S,window,sinks", [
+    ("bf16", [700], 16, 8, 128, 16, 0, 0),
+    ("f16", [700, 0, 650], 8, 8, 64, 16, 0, 0),
+    ("bf16", [1024, 1023, 1025, 993, 600, 289, 1100, 800], 16, 8, 128, 32, 0, 0),
+    ("bf16", [2000] * 8, 8, 8, 64, 16, 0, 0),
+    ("bf16", [1500, 20, 1400, 0, 3], 12, 4, 128, 16, 0, 0),      # short units beside them
+    ("bf16", [5000, 900, 700], 8, 8, 64, 24, 650, 33),
+])
+def test_decode_paged_ranges_fitted_to_units(ta, dt, lens, Hq, Hkv, D, S, window, sinks):
+    """A few long units: a range holds part of one of them."""
+    q, kp, vp, table, sl, ks, vs = build_case(dt, lens, Hq, Hkv, D, S, window, sinks, "head", 5)
+    o = ta.decode_gqa_paged(q, kp, vp, table, sl, window=window, sinks=sinks)
+    assert ta.device_status() == 0
+    check(dt, q, ks, vs, lens, o, window, sinks)
+
+
 def test_decode_paged_workspace_is_left_ready_and_results_repeat(ta):
     lens = [3000, 1, 0, 777]
     q, kp, vp, table, sl, ks, vs = build_case("bf16", lens, 8, 2, 128, 16, 0, 0, "head", 3)

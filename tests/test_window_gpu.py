@@ -139,6 +139,41 @@ def test_what_a_row_does_not_see_does_not_reach_it(ta, dt, D, what):
     assert torch.isfinite(clean.float()).all()
 
 
+@pytest.mark.parametrize("dt,B,Hq,Hkv,Nq,Nkv,D,window,sinks,order", [
+    ("bf16", 1, 4, 2, 300, 1300, 128, 200, 32, "head"),     # 32 sinks: the widest narrow tile
+    ("bf16", 1, 4, 2, 300, 1300, 64, 200, 33, "token"),     # 33: a whole one
+    ("f16", 1, 2, 1, 260, 1300, 128, 128, 1, "token"),
+    ("f16", 2, 6, 2, 260, 700, 64, 129, 31, "head"),        # an odd group: pairs of row tiles
+    ("bf16", 1, 24, 8, 520, 520, 128, 100, 5, "token"),
+    ("f32", 1, 4, 2, 130, 900, 128, 140, 70, "token"),
+    ("f32", 1, 3, 3, 33, 97, 32, 31, 1, "head"),
+    ("f16", 1, 4, 4, 65, 300, 32, 64, 64, "token"),
+])
+def test_window_few_sinks(ta, dt, B, Hq, Hkv, Nq, Nkv, D, window, sinks, order):
+    q = make(dt, B, Hq, Nq, D, order, 1)
+    k, v = make(dt, B, Hkv, Nkv, D, order, 2), make(dt, B, Hkv, Nkv, D, order, 3)
+    o = ta.causal_gqa_window_fwd(q, k, v, window, sinks)
+    assert ta.device_status() == 0
+    check(ta, dt, q, k, v, o, window, sinks)
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 128), ("f16", 64), ("f32", 64)])
+@pytest.mark.parametrize("spot", [0, 3, 4, 20, 40])
+def test_window_sinks_of_extreme_values(ta, dt, D, spot):
+    """A sink (0, 3) or a key behind the sinks in their tile (4, 20, 40), far from
+    the others: scores of its own scale, or values that no row may see."""
+    N, window, sinks = 400, 60, 4
+    q = make(dt, 1, 2, N, D, "head", 20)
+    k, v = make(dt, 1, 1, N, D, "head", 21), make(dt, 1, 1, N, D, "head", 22)
+    k[:, :, spot] *= 8
+    rows = [r for r in range(N) if spot < sinks or r < spot or r >= spot + window]
+    if spot >= sinks:
+        v[:, :, spot] = float("nan")
+    o = ta.causal_gqa_window_fwd(q, k, v, window, sinks)
+    assert ta.device_status() == 0
+    check(ta, dt, q, k, v, o, window, sinks, rows=rows)
+
+
 @pytest.mark.parametrize("which", ["q", "k", "v"])
 def test_window_of_nothing_but_nan(ta, which):
     t = dict(q=make("bf16", 1, 2, 2000, 128, "head", 10), k=make("bf16", 1, 1, 2000, 128, "head", 11),
