@@ -104,7 +104,7 @@ struct PgParams {
 };
 
 constexpr int kMaxWarps = 4;
-constexpr int kMaxAligned = 16;   // longest range (chunks) that is fitted to its units
+constexpr int kFitted = 64;       // chunks up to which a range is fitted to its units at any price
 constexpr int kWarpUnit = 8;      // longest unit (chunks) that counts as short
 
 struct Misc {
@@ -416,16 +416,19 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     // at least one chunk per warp, unless every unit is shorter than that: then
     // the units are spread over more CTAs
     if (!alone) per = imax(per, imin(CW, n_max));
-    // Where at most two more chunks per range allow it, a range holds part of one
-    // unit only, and its CTA merges and joins once instead of twice: with q =
-    // CTAs / units, parts of the longest unit's q-th give no more parts than
-    // CTAs.  The list is read as if each unit filled whole parts.  (Equal units
-    // that fill whole ranges need no such thing.  8 x 1024 tokens: 13.3 us
-    // without, 11.6 with; longer ranges lose more than a merge.)
+    // Where a quarter more chunks per range allow it, or ranges are short, a range
+    // holds part of one unit only, and its CTA merges and joins once instead of
+    // twice: with q = CTAs / units, parts of the longest unit's q-th give no more
+    // parts than CTAs.  The list is read as if each unit filled whole parts.
+    // (Equal units that fill whole ranges need no such thing.  8 x 1024 tokens:
+    // 13.3 us without, 11.6 with; 8 x 4096 27.2 and 25.4; 30 x 600 18.8 and 15.7;
+    // 8 x 8192 47.0 and 44.1; 8 x 32768 159 and 154.
+    // With longer ranges at any price, up to 128 chunks, 64 sequences of 1 to 4000
+    // tokens took 36.6 us instead of 25.5.)
     int parts = 0, parts_before = 0, parts_total = 0;
     const int n_units = in_short ? units : units_l;
     const int fit = n_units <= nc ? imax(per, cdiv(n_max, nc / imax(n_units, 1))) : 0;
-    if (!alone && one_tile && fit > 0 && fit <= per + 2 && per <= kMaxAligned && n_max > per &&
+    if (!alone && one_tile && fit > 0 && fit <= imax(kFitted, per + per / 4) && n_max > per && total < (1 << 30) &&
         !(n_max % per == 0 && (long long)n_units * n_max == total)) {
         per = fit;
         parts = int(unsigned(n_mine + per - 1) / unsigned(per));
