@@ -21,8 +21,8 @@
 //    partials in CTA order, so the result does not depend on who is last.
 //    (Drawing the tickets of a range's cut units only at its end, so that the
 //    next unit need not wait, measured 1 us slower: 8 x 4096 tokens 28.1 us.)
-//  * Short units (up to 8 chunks) beside long ones, or more of them than CTAs,
-//    are dealt out whole, warp by warp, to a share of the CTAs that their work
+//  * Short units (up to 5 chunks) beside long ones, or units of up to 8 chunks if
+//    there are more of them than CTAs and no longer ones, are dealt out whole, warp by warp, to a share of the CTAs that their work
 //    deserves: no joining, no barrier.  (In the list of the long ones each
 //    would cost its CTA a merge of four warps, 1.3 us, for a chunk or two.)
 //  * Every warp streams chunks of its own (chunk f of the range goes to warp
@@ -105,7 +105,10 @@ struct PgParams {
 
 constexpr int kMaxWarps = 4;
 constexpr int kFitted = 64;       // chunks up to which a range is fitted to its units at any price
-constexpr int kWarpUnit = 8;      // longest unit (chunks) that counts as short
+// The longest unit (chunks) that counts as short: beside long ones (40 sequences of
+// 1 to 900 tokens 11.7 us, 13.7 with 8, 11.8 with 4) and in a call without longer
+// ones (100 x 250 tokens 20.2 us, 23.1 with 5).
+constexpr int kWarpUnit = 5, kAllShort = 8;
 
 struct Misc {
     uint64_t full_k[kMaxWarps * 2], full_v[kMaxWarps * 2];   // [warp][slot]
@@ -149,10 +152,11 @@ __device__ __forceinline__ int div_s(const PgParams &p, int n) {
     return int((t + ((unsigned(n) - t) >> 1)) >> p.s_sh);
 }
 
-// The plan of a sequence if it belongs to the list of the short (or long) ones.
-__device__ __forceinline__ Plan plan_in(const PgParams &p, int len, bool in_short) {
+// The plan of a sequence if it belongs to a list of the call: the units of up to
+// `list` chunks, or (negative) those of more than -list.
+__device__ __forceinline__ Plan plan_in(const PgParams &p, int len, int list) {
     Plan r = make_plan(p, len);
-    if ((r.n <= kWarpUnit) != in_short) r.n = 0;
+    if ((r.n <= abs(list)) != (list > 0)) r.n = 0;
     return r;
 }
 
@@ -163,7 +167,7 @@ __device__ __forceinline__ int chunk_of(const Plan &r, int v) {
 // One CTA's range of the flat chunk list, a segment (part of one unit) at a time.
 struct Walk {
     const PgParams &p;
-    bool in_short;                         // the list: short or long units
+    int list;
     Plan plan;
     int b, kvh, v0, cnt;
     int left;                              // chunks of the range from this segment on
@@ -171,8 +175,8 @@ struct Walk {
 
     int ahead;                             // seq_len[b + 1], loaded before it is needed
 
-    __device__ Walk(const PgParams &pp, bool list, int b0, int len0, int kvh0, int v, int f0, int count)
-        : p(pp), in_short(list), b(b0), kvh(kvh0), v0(v), left(count), flat(f0) {
+    __device__ Walk(const PgParams &pp, int l, int b0, int len0, int kvh0, int v, int f0, int count)
+        : p(pp), list(l), b(b0), kvh(kvh0), v0(v), left(count), flat(f0) {
         plan = make_plan(p, len0);
         ahead = b + 1 < p.B ? p.seq_len[b + 1] : 0;
         if (kvh == p.Hkv) next_sequence();
@@ -181,7 +185,7 @@ struct Walk {
     __device__ void next_sequence() {       // the range ends inside the list: b stays below B
         kvh = 0;
         do {
-            plan = plan_in(p, ahead, in_short);
+            plan = plan_in(p, ahead, list);
             ++b;
             ahead = b + 1 < p.B ? p.seq_len[b + 1] : 0;
         } while (plan.n == 0);
@@ -282,7 +286,7 @@ __device__ __forceinline__ void mark_starts(const PgParams &p, Misc *ms, int mar
 // The same for a batch of more sequences than threads, read again tile by tile.
 template <int CW>
 __device__ __noinline__ void mark_long_batch(const PgParams &p, Misc *ms, int marks, int f0, int per,
-                                             bool in_short) {
+                                             int list) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int carry = 0;                                     // chunks of the sequences before this tile
 #pragma unroll 1
@@ -290,7 +294,7 @@ __device__ __noinline__ void mark_long_batch(const PgParams &p, Misc *ms, int ma
         __syncthreads();
         const int b = b0 + threadIdx.x;
         const int len = b < p.B ? p.seq_len[b] : 0;
-        const int n = plan_in(p, len, in_short).n;
+        const int n = plan_in(p, len, list).n;
         int inc = n;
 #pragma unroll 1
         for (int off = 1; off < 32; off <<= 1) {
@@ -392,6 +396,12 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         units += ms->warp_units[w];
         units_l += ms->warp_units_l[w];
     }
+    if (n_max <= kAllShort) {                          // no long ones: one list
+        total_s += total_l;
+        before_s += before_l;
+        units += units_l;
+        total_l = units_l = 0;
+    }
     total_l *= p.Hkv;
     total_s *= p.Hkv;
     units *= p.Hkv;                                    // of the short list
@@ -407,7 +417,8 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         c = in_short ? cta - (ctas - ns) : cta;
     }
     const int total = in_short ? total_s : total_l;
-    if ((n_mine <= kWarpUnit) != in_short) n_mine = 0;
+    const int limit = n_max <= kAllShort ? kAllShort : kWarpUnit, list = in_short ? limit : -limit;
+    if ((n_mine <= limit) != in_short) n_mine = 0;
     int before = (in_short ? before_s : before_l) - n_mine;   // chunks of the sequences ahead (one tile)
     // team: the warps that share a range (all of the CTA's, or each its own)
     const int team = alone ? 1 : CW, rank = alone ? 0 : warp;
@@ -468,7 +479,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     } else {
         if (threadIdx.x < marks && f0l + (long long)threadIdx.x * per >= total) ms->start_flat[threadIdx.x] = total;
         if (!one_tile)
-            mark_long_batch<CW>(p, ms, marks, f0, per, in_short);
+            mark_long_batch<CW>(p, ms, marks, f0, per, list);
         else if (n_mine > 0)
             mark_starts(p, ms, marks, f0, per, threadIdx.x, len_mine, n_mine, before);
     }
@@ -478,7 +489,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     const int count = alone ? ms->start_flat[warp + 1] - start : aligned ? ms->start_count : imin(per, total - f0);
     if (count <= 0) return;                            // alone: no unit starts in this warp's share
 
-    Walk w(p, in_short, ms->start_b[at], ms->start_len[at], ms->start_kvh[at], ms->start_v[at], start, count);
+    Walk w(p, list, ms->start_b[at], ms->start_len[at], ms->start_kvh[at], ms->start_v[at], start, count);
     int f = 0;                                         // chunk number within the range
 
     // ---- loads: a walk of its own that runs NS chunks (and a group of page
