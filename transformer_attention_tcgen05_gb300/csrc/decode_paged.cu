@@ -22,8 +22,9 @@
 //    (Drawing the tickets of a range's cut units only at its end, so that the
 //    next unit need not wait, measured 1 us slower: 8 x 4096 tokens 28.1 us.)
 //  * Short units (up to 5 chunks) beside long ones, or units of up to 8 chunks if
-//    there are more of them than CTAs and no longer ones, are dealt out whole, warp by warp, to a share of the CTAs that their work
-//    deserves: no joining, no barrier.  (In the list of the long ones each
+//    there are more of them than CTAs and no longer ones, are dealt out whole,
+//    warp by warp, to a share of the CTAs that their work deserves: no joining, no
+//    barrier.  (In the list of the long ones each
 //    would cost its CTA a merge of four warps, 1.3 us, for a chunk or two.)
 //  * Every warp streams chunks of its own (chunk f of the range goes to warp
 //    f % CW) into shared memory of its own with TMA: a box of up to 32 rows x D
