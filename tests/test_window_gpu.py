@@ -217,3 +217,74 @@ def test_no_window_agrees_with_the_causal_entry(ta):
     a, b = ta.causal_gqa_fwd(q, k, v), ta.causal_gqa_window_fwd(q, k, v, 0)
     check(ta, "bf16", q, k, v, a, 0, 0)
     check(ta, "bf16", q, k, v, b, 0, 0)
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 128), ("f16", 128), ("bf16", 64), ("f16", 64), ("f32", 64), ("bf16", 32)])
+@pytest.mark.parametrize("Hq,Nq,Nkv,window,sinks", [
+    (2, 700, 700, 90, 3),          # pairs of heads; a narrow tile of sinks
+    (3, 700, 777, 300, 40),        # pairs of row tiles, queries off the tiles' grid
+    (3, 600, 600, 130, 0),
+    (1, 333, 700, 200, 130),       # a second tile of sinks
+])
+@pytest.mark.parametrize("what", ["v_nan", "v_inf", "k_nan", "k_inf"])
+def test_what_a_row_does_not_see_leaves_every_bit_of_it(ta, dt, D, Hq, Nq, Nkv, window, sinks, what):
+    """Not within a tolerance: the output row is the same row.  An infinite or NaN
+    value spoils its own channel of the rows that see it and nothing else."""
+    q = make(dt, 1, Hq, Nq, D, "head", 60)
+    k, v = make(dt, 1, 1, Nkv, D, "head", 61), make(dt, 1, 1, Nkv, D, "head", 62)
+    clean = ta.causal_gqa_window_fwd(q, k, v, window, sinks)
+    bad = float("nan") if what.endswith("nan") else float("inf")
+    for spots in ([Nkv - 1], [Nkv - 200], [Nkv - 256, Nkv - 129, Nkv - 127], [sinks], [sinks + 5, 127], [129],
+                  [0] if sinks else [Nkv // 2], [Nkv - 300, 20, Nkv - 64]):
+        k2, v2 = k.clone(), v.clone()
+        (k2 if what[0] == "k" else v2)[:, :, spots, 5] = bad
+        o = ta.causal_gqa_window_fwd(q, k2, v2, window, sinks)
+        assert ta.device_status() == 0
+        see = visible(Nkv, range(Nkv - Nq, Nkv), window, sinks)[:, spots].any(1).cuda()
+        assert torch.equal(o[:, :, ~see], clean[:, :, ~see]), spots
+        if what[0] == "v":
+            assert not torch.isfinite(o[:, :, see, 5].float()).any(), spots
+            assert torch.equal(o[:, :, see, :5], clean[:, :, see, :5])
+            assert torch.equal(o[:, :, see, 6:], clean[:, :, see, 6:])
+        else:
+            # an infinite key: infinite scores of either sign; +inf makes the row NaN
+            lost = see if what == "k_nan" else see & (q[0, :, :, 5].float() > 0).all(0)
+            assert torch.isnan(o[:, :, lost].float()).all(), spots
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 128), ("f16", 64)])
+def test_infinite_values_cost_little(ta, dt, D):
+    """One infinite channel of a sink that nearly every row sees, or of a key behind
+    the sinks that none of them sees, over a long prompt: the rows are not
+    computed again key by key.  The work is that of the clean call and, for the
+    row blocks with the value in a tile on an edge, one more look at such tiles
+    (a few of hundreds of steps): less than three times the clean call."""
+    N, window, sinks = 16384, 2048, 4
+    q = make(dt, 1, 8, N, D, "head", 70)
+    k, v = make(dt, 1, 2, N, D, "head", 71), make(dt, 1, 2, N, D, "head", 72)
+    clean = ta.causal_gqa_window_fwd(q, k, v, window, sinks)
+
+    def took():
+        best = 1e9
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            o = ta.causal_gqa_window_fwd(q, k, v, window, sinks)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best, o
+
+    limit = 3 * took()[0]
+    for spot in (2, 20, N // 2):
+        keep = v[:, :, spot].clone()
+        v[:, :, spot, 5] = float("inf")
+        ms, o = took()
+        v[:, :, spot] = keep
+        assert ta.device_status() == 0
+        see = torch.arange(N, device="cuda")
+        see = (see >= spot) & ((see < spot + window) | (spot < sinks))
+        assert not torch.isfinite(o[:, :, see, 5].float()).any()
+        o[:, :, see, 5] = clean[:, :, see, 5]
+        assert torch.equal(o, clean)
+        assert ms < limit, (spot, ms, limit / 3)

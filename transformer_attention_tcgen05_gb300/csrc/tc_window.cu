@@ -41,8 +41,16 @@
 // type (half a step of each weight) because the tensor core takes it as an
 // operand beside V; the sum takes the weights before that.  O is rounded once.
 //
-// A key that a row does not see does not change its output even if its value is
-// infinite or NaN: such a row is redone from its own keys (window_row).
+// A key that a row does not see does not change its output, whatever it or its
+// value holds: a masked score is -inf before anything is made of it, and the
+// tensor cores meet no infinite or NaN value that one of their rows does not see (0 x inf is NaN).  V
+// of the sinks comes through a map that ends behind them (zeros follow); in the
+// other tiles on an edge a warp that has nothing else to do looks the values over
+// while the scores are computed and clears what is not finite, and the rows that
+// do see such a value get it back in the epilogue (spoil_rows).  With finite
+// inputs 4096 tokens take 58.4 us (58.1 without any of it), 32768 tokens 1226
+// (1222); with one infinite value 8192 tokens, 8 heads on 2, window 2048, took
+// 58 ms as long as rows that were not finite were computed again key by key.
 //
 // All spin-waits are bounded (1 s); on a timeout the CTA raises the device
 // error word, drains what it issued, frees TMEM and exits.
@@ -133,10 +141,9 @@ struct WnParams {
     int by_head;             // a pair is two heads of one KV head (else two row tiles)
     int blocks;              // row blocks
     Div by_hp, by_h, by_group;   // pairs (or heads) per row block, heads, heads per KV head
-    // operands and element strides (rows redone outside the tensor cores; o)
-    const void *q, *k, *v;
+    const void *v;           // with element strides: values cleared from an edge tile
+    TensorStrides sv;
     void *o;
-    TensorStrides sq, sk, sv;
     long long o_sb, o_sh, o_sn;
 };
 
@@ -144,14 +151,15 @@ struct WnParams {
 template <int KS, int VS>
 struct Bars {
     uint64_t q_full[kNQ];
-    uint64_t k_full[KS], k_empty[KS], v_full[VS], v_empty[VS];
+    // v_in: the stage's copies have landed; v_full: the checking warp has passed it on
+    uint64_t k_full[KS], k_empty[KS], v_in[VS], v_full[VS], v_empty[VS];
     // per query tile t: s_full its Q K^T has completed, p_ready the softmax
     // has written P, o_done the P V product that read P has completed,
     // s_free (separate P, D = 64) the softmax holds S_t in registers
     uint64_t s_full[kNQ], p_ready[kNQ], o_done[kNQ], s_free[kNQ];
-    uint64_t drain;
+    uint64_t drain, checked;       // checked: every edge tile has been looked over
     uint32_t tmem_base;
-    int abort;
+    int abort, wild;               // wild: a value was cleared from one of them
 };
 
 // a[t] for a per-query-tile array and a run-time t, by selects
@@ -166,12 +174,19 @@ struct Item {
     int n[kNQ], f[kNQ], steps;
     int w_lo, w_sk;                // first window tile, sink tiles before it
     bool few;                      // step 0 is the sinks' tile and holds at most kFew keys
+    int e0, e1, e2;                // steps of the tiles on an edge: [e0, e1), [e2, steps), a leading one
 
     // key tile of step j: the leading tile of the first query tile (if any),
     // the sink tiles, the window
     __device__ __forceinline__ int tile(int j) const {
         const int i = j - f[1];
         return i < 0 ? w_lo : i < w_sk ? i : w_lo + j - w_sk;
+    }
+    // step j is a tile of sinks in front of every row's window
+    __device__ __forceinline__ bool sink_tile(int j) const { return j >= f[1] && j < f[1] + w_sk; }
+    // some row does not see all keys of step j's tile (sink tiles left out)
+    __device__ __forceinline__ bool edge(int j) const {
+        return j >= e2 || (j >= e0 && j < e1) || j < f[1];
     }
 };
 
@@ -203,72 +218,125 @@ __device__ __forceinline__ Item get_item(const WnParams &p) {
     w.n[0] = one ? w.w_sk + (p.off + imin(w.q0 + kBM, p.Nq) - 1) / kBN - w.w_lo + 1 : 0;
     w.n[1] = two ? w.w_sk + (p.off + imin(w.q0 + w.dq + kBM, p.Nq) - 1) / kBN - w.w_lo + 1 : 0;
     w.steps = imax(w.n[0], w.n[1]);
+    // the window of the last query tile starts behind its first key, or the first
+    // one's diagonal comes before its last
+    const int lead = two ? pos + w.dq : pos;
+    w.e0 = w.w_sk + w.f[1];
+    w.e1 = w.w_sk + cdiv(imax(0, lead + kBM - p.window), kBN) - w.w_lo;
+    w.e2 = w.w_sk + imax(0, (pos + 1) / kBN - w.w_lo);
     return w;
 }
 
-// One row of windowed attention by one warp, in fp32 (every lane D / 32
-// channels): row qi of (batch b, query head h, KV head hk).  A row whose tensor-core
-// result is not finite comes here: a key that the row does not see has weight
-// zero in the P V product, but zero times an infinite or NaN value is NaN.
-// Only the row's own keys are read here, so such a value spoils exactly the
-// rows that see it.
+// The bits of a 16-bit value that are all ones if it is infinite or NaN.
+template <bool F16> constexpr uint32_t kWild = F16 ? 0x7c00u : 0x7f80u;
+
+template <bool F16>
+__device__ __forceinline__ bool wild_pair(uint32_t w) {
+    constexpr uint32_t lo = kWild<F16>, hi = lo << 16;
+    return (w & lo) == lo || (w & hi) == hi;
+}
+
+// a + 0 x in both halves: NaN where x is infinite or NaN.
+template <bool F16>
+__device__ __forceinline__ uint32_t add_zero_times(uint32_t a, uint32_t x) {
+    uint32_t r;
+    if constexpr (F16)
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(a));
+    else
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(a));
+    return r;
+}
+
+// Clears the infinite and NaN values of a V stage; returns whether there were
+// any.  One warp; the writes are visible to the tensor cores behind the barrier
+// that follows.
 template <int D, bool F16>
-__device__ __forceinline__ void window_row(const WnParams &p, int b, int h, int hk, int qi) {
-    using H = H16<F16>;
-    using T = typename H::T;
-    constexpr int CW = D / 64;                       // 32-bit words per lane
-    const int lane = threadIdx.x & 31;
-    auto load = [&](const void *base, const TensorStrides &st, int head, int n, float (&x)[2 * CW]) {
-        const uint32_t *g = reinterpret_cast<const uint32_t *>(
-            static_cast<const T *>(base) + b * st.b + head * st.h + n * st.n) + lane * CW;
+__device__ __forceinline__ bool clear_wild(uint8_t *stage) {
+    constexpr int VECS = kBN * D / 8, U = 8;
+    constexpr uint32_t lo = kWild<F16>, hi = lo << 16;
+    uint4 *at = reinterpret_cast<uint4 *>(stage) + (threadIdx.x & 31);
+    uint32_t z[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 2
+    for (int i = 0; i < VECS; i += U * 32) {
+        uint4 x[U];
 #pragma unroll
-        for (int i = 0; i < CW; ++i) {
-            const uint32_t w = g[i];
-            x[2 * i] = H::lo(w);
-            x[2 * i + 1] = H::hi(w);
+        for (int u = 0; u < U; ++u) x[u] = at[i + u * 32];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            z[0] = add_zero_times<F16>(z[0], x[u].x);
+            z[1] = add_zero_times<F16>(z[1], x[u].y);
+            z[2] = add_zero_times<F16>(z[2], x[u].z);
+            z[3] = add_zero_times<F16>(z[3], x[u].w);
         }
-    };
-    float q[2 * CW], acc[2 * CW], m = -INFINITY, l = 0.f;
-    load(p.q, p.sq, h, qi, q);
-#pragma unroll
-    for (int i = 0; i < 2 * CW; ++i) acc[i] = 0.f;
-    const int pos = p.off + qi;
-    const int lo = pos >= p.window ? pos - p.window + 1 : 0;
-    const int s_end = imin(p.sinks, lo);
-#pragma unroll 1
-    for (int j = s_end > 0 ? 0 : lo; j <= pos; j = j + 1 == s_end ? lo : j + 1) {
-        float x[2 * CW], s = 0.f;
-        load(p.k, p.sk, hk, j, x);
-#pragma unroll
-        for (int i = 0; i < 2 * CW; ++i) s = fmaf(q[i], x[i], s);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        s *= p.c_log2;
-        const float mn = fmaxf(m, s);
-        const float f = mn == -INFINITY ? 1.f : ptx::ex2(m - mn);
-        const float w = s == -INFINITY && mn == -INFINITY ? 0.f : ptx::ex2(s - mn);
-        load(p.v, p.sv, hk, j, x);
-        m = mn;
-        l = l * f + w;
-#pragma unroll
-        for (int i = 0; i < 2 * CW; ++i) acc[i] = fmaf(w, x[i], acc[i] * f);
-        // NaN in every channel (a NaN in q, say) stays: no need to read on
-        bool lost = true;
-#pragma unroll
-        for (int i = 0; i < 2 * CW; ++i) lost = lost && acc[i] != acc[i];
-        if (__all_sync(0xffffffffu, lost)) break;
     }
-    const float inv = 1.f / l;
-    uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<T *>(p.o) + b * p.o_sb + h * p.o_sh +
-                                               qi * p.o_sn) + lane * CW;
+    const bool any = ((z[0] | z[1] | z[2] | z[3]) & 0x7fff7fffu) != 0;   // 0 x is +-0
+    if (any) {
+#pragma unroll 1
+        for (int e = 0; e < VECS / 32 * 4; ++e) {
+            uint32_t *y = reinterpret_cast<uint32_t *>(at + (e >> 2) * 32) + (e & 3);
+            uint32_t w = *y;
+            if ((w & lo) == lo) w &= 0xffff0000u;
+            if ((w & hi) == hi) w &= 0x0000ffffu;
+            *y = w;
+        }
+        ptx::fence_proxy_async_smem();
+    }
+    return __any_sync(0xffffffffu, any);
+}
+
+// Adds the infinite and NaN values that were cleared from the item's edge tiles to
+// the warp's staged output rows that see them: whatever its (positive) weight,
+// such a value makes its channel of the row infinite or NaN.  Rare, so the
+// values are read again from memory, a row of V at a time.
+template <int D, bool F16>
+__device__ __noinline__ void spoil_rows(const WnParams &p, uint8_t *stage, int first_pos, int rows) {
+    const Item w = get_item(p);                      // (handed over it would live in memory)
+    using H = H16<F16>;
+    constexpr int CW = D / 64;                       // 32-bit words (two channels) per lane
+    constexpr int CH = D / 8, U = 8;
+    const int lane = threadIdx.x & 31;
+    const uint32_t *v = reinterpret_cast<const uint32_t *>(static_cast<const typename H::T *>(p.v) +
+                                                           w.fb * p.sv.b + w.fkh * p.sv.h) + lane * CW;
+    for (int j = 0; j < w.steps; ++j) {
+        if (!w.edge(j)) continue;
+        const int k0 = w.tile(j) * kBN, keys = imin(kBN, p.Nkv - k0);
+        for (int i = 0; i < keys; i += U) {
+            uint32_t x[U][CW];
 #pragma unroll
-    for (int i = 0; i < CW; ++i) o[i] = H::pack(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int c = 0; c < CW; ++c) x[u][c] = i + u < keys ? v[(k0 + i + u) * (p.sv.n / 2) + c] : 0u;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                bool here = false;
+#pragma unroll
+                for (int c = 0; c < CW; ++c) here = here || wild_pair<F16>(x[u][c]);
+                if (!__any_sync(0xffffffffu, here)) continue;
+                const int key = k0 + i + u;
+#pragma unroll 1
+                for (int r = 0; r < rows; ++r) {
+                    const int pos = first_pos + r;
+                    if (key > pos || (key <= pos - p.window && key >= p.sinks)) continue;
+                    uint32_t *y = reinterpret_cast<uint32_t *>(
+                                      stage + (r * CH + ((lane * CW / 4) ^ (r & 7))) * 16) + lane * CW % 4;
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) {
+                        const float a = H::lo(x[u][c]), b = H::hi(x[u][c]);
+                        y[c] = H::pack(fabsf(a) < INFINITY ? H::lo(y[c]) : H::lo(y[c]) + a,
+                                       fabsf(b) < INFINITY ? H::hi(y[c]) : H::hi(y[c]) + b);
+                    }
+                }
+            }
+        }
+    }
+    __syncwarp();
 }
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(WnCfg<D>::NT, 1)
 tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                 const __grid_constant__ CUtensorMap tv, const WnParams p) {
+                 const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tvs,
+                 const WnParams p) {
     using C = WnCfg<D>;
     using BarsT = Bars<C::KS, C::VS>;
     static_assert(sizeof(BarsT) <= 512, "barrier block must fit its reserved bytes");
@@ -286,6 +354,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             ptx::mbar_init(&bars->k_empty[s], 1);
         }
         for (int s = 0; s < C::VS; ++s) {
+            ptx::mbar_init(&bars->v_in[s], 1);
             ptx::mbar_init(&bars->v_full[s], 1);
             ptx::mbar_init(&bars->v_empty[s], 1);
         }
@@ -297,7 +366,8 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             ptx::mbar_init(&bars->s_free[t], 128);
         }
         ptx::mbar_init(&bars->drain, 1);
-        bars->abort = 0;
+        ptx::mbar_init(&bars->checked, 1);
+        bars->abort = bars->wild = 0;
         ptx::fence_barrier_init();
     }
     if (warp == C::W_MMA) {
@@ -309,6 +379,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         ptx::prefetch_tmap(warp == C::W_LOAD ? &tk : &tv);
         if (warp == C::W_LOAD) ptx::prefetch_tmap(&tq);
         load_item = get_item(p);
+        if (warp == C::W_LOADV && load_item.w_sk > 0) ptx::prefetch_tmap(&tvs);
     }
     ptx::tc_fence_before();
     __syncthreads();
@@ -325,7 +396,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             // thread streams Q and the K ring, another the V ring
             const int which = warp == C::W_LOAD ? 0 : 1;
             const CUtensorMap *tm = which == 0 ? &tk : &tv;
-            uint64_t *full = which == 0 ? bars->k_full : bars->v_full;
+            uint64_t *full = which == 0 ? bars->k_full : bars->v_in;
             uint64_t *empty = which == 0 ? bars->k_empty : bars->v_empty;
             const int NS = which == 0 ? C::KS : C::VS;   // depth of this ring
             const uint64_t pol_kv = ptx::l2_policy_evict_last(), pol_q = ptx::l2_policy_evict_first();
@@ -346,8 +417,8 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 issued = j + 1;
                 ptx::mbar_arrive_expect_tx(&full[s], C::KV_BYTES);
                 for (int pn = 0; pn < C::PANELS; ++pn)
-                    ptx::tma_load_4d(smem + (which == 0 ? C::k_off(s) : C::v_off(s)) + pn * C::PANEL_KV, tm,
-                                     pn * 64, w.tile(j) * kBN, w.fkh, w.fb, &full[s], pol_kv);
+                    ptx::tma_load_4d(smem + (which == 0 ? C::k_off(s) : C::v_off(s)) + pn * C::PANEL_KV,
+                                     which == 1 && w.sink_tile(j) ? &tvs : tm, pn * 64, w.tile(j) * kBN, w.fkh, w.fb, &full[s], pol_kv);
                 // the first scores need one query tile and the first keys
                 if (which == 0 && j == 0) load_q(1);
             }
@@ -470,6 +541,23 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             // drain: every MMA has completed before TMEM is freed
             if (lead) ptx::tc_commit(&bars->drain);
             ptx::mbar_wait(&bars->drain, 0, p.err);
+        } else if (warp == C::W_INIT) {
+            // ============================================= the V of edge tiles is
+            // looked over as it arrives, while the tile's scores are computed and
+            // exponentiated; other tiles are passed on at once
+            const Item w = get_item(p);
+            for (int j = 0; j < w.steps; ++j) {
+                const int s = j % C::VS;
+                if (!__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&bars->v_in[s], (j / C::VS) & 1, p.err, abort)))
+                    break;
+                const bool any = w.edge(j) && clear_wild<D, F16>(smem + C::v_off(s));
+                __syncwarp();
+                if (lane == 0) {
+                    if (any) bars->wild = 1;
+                    ptx::mbar_arrive(&bars->v_full[s]);
+                }
+            }
+            if (lane == 0) ptx::mbar_arrive(&bars->checked);
         }
     } else {
         // ================================================= softmax warpgroups
@@ -697,7 +785,6 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             // has completed), column c of row r at c ^ (r & 7), so that whole rows
             // go out instead of 32 rows' 16 bytes
             uint8_t *stage = smem + C::OFF_Q + t * C::Q_BYTES + quarter * 32 * D * 2;
-            bool finite = true;
 #pragma unroll
             for (int half = 0; half < D / 64; ++half) {
                 float ov[64];
@@ -708,30 +795,24 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 for (int c = 0; c < 8; ++c) {
                     uint32_t x[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float x0 = ov[c * 8 + 2 * e] * inv, x1 = ov[c * 8 + 2 * e + 1] * inv;
-                        finite = finite && fabsf(x0) < INFINITY && fabsf(x1) < INFINITY;
-                        x[e] = H16<F16>::pack(x0, x1);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        x[e] = H16<F16>::pack(ov[c * 8 + 2 * e] * inv, ov[c * 8 + 2 * e + 1] * inv);
                     *reinterpret_cast<uint4 *>(stage + (ln * CH + half * 8 + (c ^ (ln & 7))) * 16) =
                         make_uint4(x[0], x[1], x[2], x[3]);
                 }
             }
             __syncwarp();
-            unsigned redo = __ballot_sync(0xffffffffu, !finite && q_first + ln < p.Nq);
+            if (__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&bars->checked, 0, p.err, abort)) &&
+                *reinterpret_cast<volatile int *>(&bars->wild))
+                spoil_rows<D, F16>(p, stage, p.off + q_first, imin(32, p.Nq - q_first));
             typename H16<F16>::T *const o0 = static_cast<typename H16<F16>::T *>(p.o) + w.fb * p.o_sb + qh * p.o_sh;
             const int col = ln % CH;
 #pragma unroll
             for (int r0 = 0; r0 < 32; r0 += 32 / CH) {
                 const int r = r0 + ln / CH;
                 const uint4 x = *reinterpret_cast<const uint4 *>(stage + (r * CH + (col ^ (r & 7))) * 16);
-                if (q_first + r < p.Nq && !((redo >> r) & 1u))
+                if (q_first + r < p.Nq)
                     *reinterpret_cast<uint4 *>(o0 + (q_first + r) * p.o_sn + col * 8) = x;
-            }
-            while (redo) {
-                const int r = __ffs(redo) - 1;
-                redo &= redo - 1;
-                window_row<D, F16>(p, w.fb, qh, w.fkh, q_first + r);
             }
         }
     }
@@ -747,7 +828,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
 
 template <int D, bool F16>
 attn_status_t launch_window(const Ctx &c, const CUtensorMap &tq, const CUtensorMap &tk,
-                            const CUtensorMap &tv, const WnParams &p) {
+                            const CUtensorMap &tv, const CUtensorMap &tvs, const WnParams &p) {
     using C = WnCfg<D>;
     static int done_mask = 0;
     static int regs = -1;
@@ -774,7 +855,7 @@ attn_status_t launch_window(const Ctx &c, const CUtensorMap &tq, const CUtensorM
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, tvs, p) != cudaSuccess) {
         cudaGetLastError();
         return ATTN_ERR_CUDA;
     }
@@ -793,10 +874,12 @@ attn_status_t tc_causal_window(const Ctx &c, attn_dtype_t dt, const void *q, con
     const long long pairs = by_head ? (long long)cdiv(Nq, kBM) * (B * Hq / 2)
                                     : (long long)cdiv(Nq, kNQ * kBM) * B * Hq;
     if (pairs > (1 << 29)) return ATTN_ERR_UNSUPPORTED;
-    CUtensorMap tq, tk, tv;
+    CUtensorMap tq, tk, tv, tvs;
     // a layout the tensor-map encoder refuses goes to the strided SIMT kernel
     if (!make_tmap4(&tq, q, D, Nq, Hq, B, st[0], f16) || !make_tmap4(&tk, k, D, Nkv, Hkv, B, st[1], f16) ||
-        !make_tmap4(&tv, v, D, Nkv, Hkv, B, st[2], f16))
+        !make_tmap4(&tv, v, D, Nkv, Hkv, B, st[2], f16) ||
+        // of the sinks' values only: rows behind them are read as zeros
+        !make_tmap4(&tvs, v, D, sinks > 0 ? sinks : Nkv, Hkv, B, st[2], f16))
         return ATTN_ERR_UNSUPPORTED;
     WnParams p{};
     p.Nq = Nq;
@@ -816,12 +899,12 @@ attn_status_t tc_causal_window(const Ctx &c, attn_dtype_t dt, const void *q, con
     // single tiles, on twice as many
     const int rest = p.pairs % imax(1, c.sm_count);
     p.whole = 2 * rest <= c.sm_count ? p.pairs - rest : p.pairs;
-    p.q = q; p.k = k; p.v = v; p.o = o;
-    p.sq = st[0]; p.sk = st[1]; p.sv = st[2];
+    p.v = v; p.o = o;
+    p.sv = st[2];
     p.o_sb = st[3].b; p.o_sh = st[3].h; p.o_sn = st[3].n;
     if (D == 128)
-        return f16 ? launch_window<128, true>(c, tq, tk, tv, p) : launch_window<128, false>(c, tq, tk, tv, p);
-    return f16 ? launch_window<64, true>(c, tq, tk, tv, p) : launch_window<64, false>(c, tq, tk, tv, p);
+        return f16 ? launch_window<128, true>(c, tq, tk, tv, tvs, p) : launch_window<128, false>(c, tq, tk, tv, tvs, p);
+    return f16 ? launch_window<64, true>(c, tq, tk, tv, tvs, p) : launch_window<64, false>(c, tq, tk, tv, tvs, p);
 }
 
 }  // namespace attn
