@@ -280,8 +280,9 @@ ATTN_API attn_status_t attn_decode_gqa_ring(const void *q, const void *k_cache,
  *   `sinks` tokens.  window <= 0: no window (plain causal attention).
  *   sinks >= 0.  Nq < Nkv continues a prompt whose first keys are cached.
  *   x_strides[3] as in attn_full_fwd_strided (NULL: contiguous).
- *   A key that a query does not attend to does not change its output, whatever
- *   it or its value holds (infinities and NaN included).
+ *   A key that a query does not attend to does not change a bit of its output,
+ *   whatever it or its value holds (infinities and NaN included).  An infinity
+ *   or NaN that it does attend to makes what it reaches infinite or NaN.
  *   bf16 and f16 run on the tensor cores for D in {64, 128}; fp32 (and the
  *   16-bit types with D = 32) on the exact-FFMA SIMT kernel.  Work grows with
  *   Nq * (window + sinks), not with Nq * Nkv.

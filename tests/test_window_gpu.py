@@ -288,3 +288,21 @@ def test_infinite_values_cost_little(ta, dt, D):
         o[:, :, see, 5] = clean[:, :, see, 5]
         assert torch.equal(o, clean)
         assert ms < limit, (spot, ms, limit / 3)
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 128), ("f16", 128), ("bf16", 64), ("f16", 64)])
+@pytest.mark.parametrize("Hq", [2, 3])
+@pytest.mark.parametrize("spot", [100, 271, 400, 530, 599])
+def test_a_key_that_other_rows_see_leaves_every_bit_of_a_row(ta, dt, D, Hq, spot):
+    """Keys that grow along the sequence, so that maxima are due to move, and a NaN
+    among them: rows next to those that see it keep theirs as without it."""
+    N, window = 600, 300
+    q = make(dt, 1, Hq, N, D, "head", 63)
+    k, v = make(dt, 1, 1, N, D, "head", 64), make(dt, 1, 1, N, D, "head", 65)
+    k = (k.float() * torch.linspace(0.1, 9, N).cuda()[None, None, :, None]).to(DT[dt])
+    clean = ta.causal_gqa_window_fwd(q, k, v, window, 2)
+    k[:, :, spot, 5] = float("nan")
+    o = ta.causal_gqa_window_fwd(q, k, v, window, 2)
+    see = visible(N, range(N), window, 2)[:, spot].cuda()
+    assert torch.isnan(o[:, :, see].float()).all()
+    assert torch.equal(o[:, :, ~see], clean[:, :, ~see])

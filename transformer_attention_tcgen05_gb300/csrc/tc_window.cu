@@ -42,8 +42,9 @@
 // operand beside V; the sum takes the weights before that.  O is rounded once.
 //
 // A key that a row does not see does not change its output, whatever it or its
-// value holds: a masked score is -inf before anything is made of it, and the
-// tensor cores meet no infinite or NaN value that one of their rows does not see (0 x inf is NaN).  V
+// value holds: a masked score is -inf before anything is made of it, a row's
+// running maximum moves by its own scores alone, and the tensor cores meet no
+// infinite or NaN value that one of their rows does not see (0 x inf is NaN).  V
 // of the sinks comes through a map that ends behind them (zeros follow); in the
 // other tiles on an edge a warp that has nothing else to do looks the values over
 // while the scores are computed and clears what is not finite, and the rows that
@@ -586,6 +587,10 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
 
         float m = -INFINITY, l = 0.f;
         int j = 0;
+        // the key tile from which on every row of the warp has seen a key before: of
+        // the first one the last rows may see nothing, and then see the next
+        const int k_first = w.tile(f) * kBN;
+        const int seen_from = k_first < p.sinks || pos + quarter * 32 + 32 - p.window < k_first + kBN ? 1 : 2;
         // ---- a first tile of a few sinks, which every row sees: kFew columns
         if (w.few && nt > 0) {
             ok = __all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&bars->s_full[t], 0, p.err, abort));
@@ -707,13 +712,12 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             //      for f16, whose largest finite value is 65504) or is not finite
             //      is redone below against its own maximum.  After the first tiles
             //      m is close to the row maximum and the redo almost never runs.
-            bool fast = j > 0 && __all_sync(0xffffffffu, m != -INFINITY);
-            if (fast) {
-                const float lt = emit_p(-m);
-                if (__any_sync(0xffffffffu, !(lt <= (F16 ? 32768.f : 16777216.f))))
-                    fast = false;                 // redo the tile (P is rewritten below)
-                else
-                    l += lt;
+            bool fast = false, keep = false;      // this row's maximum may stay
+            if (j >= seen_from) {
+                const float lt = emit_p(-m);      // infinite or NaN if m is still -inf
+                keep = lt <= (F16 ? 32768.f : 16777216.f);
+                fast = __all_sync(0xffffffffu, keep);   // else redo the tile (P is rewritten below)
+                if (fast) l += lt;
             }
 
             if (!fast) {
@@ -732,7 +736,8 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 const float mt = tmax * cl;      // cl > 0: max commutes with the scaling
 
                 // ---- the previous P V must be done before O is rescaled
-                const bool want = j == 0 || mt > m + 8.f;   // this row moves its maximum
+                // (a row that a redo for other rows' sake takes along keeps it)
+                const bool want = j == 0 || (!keep && mt > m + 8.f);   // this row moves its maximum
                 const bool any_want = __any_sync(0xffffffffu, want);
                 if (j > 0 && any_want && !prev_done) {
                     if (!wait_pv(j - 1)) {
