@@ -114,7 +114,7 @@ constexpr int kWarpUnit = 5, kAllShort = 8;
 struct Misc {
     uint64_t full_k[kMaxWarps * 2], full_v[kMaxWarps * 2];   // [warp][slot]
     int warp_long[kMaxWarps], warp_short[kMaxWarps];
-    int warp_parts[kMaxWarps];
+    int warp_parts[kMaxWarps], warp_idle[kMaxWarps];
     int warp_max[kMaxWarps], warp_units[kMaxWarps], warp_units_l[kMaxWarps];
     // where the CTA's range, or each warp's (and the one behind), starts
     int start_flat[kMaxWarps + 1];
@@ -251,14 +251,21 @@ struct Group {
 // Rare steps are functions of their own, out of the way of the code that every
 // launch fetches.
 
-// A sequence with nothing to attend to: zeros (length 0) or a report.
+// The sequences with nothing to attend to among this CTA's share (b0 and every
+// step-th from it on): zeros (length 0) by all of its threads, or a report.  4
+// sequences of 128 to 700 tokens, 32 heads, D 128, beside 4 idle slots: 8.8 us,
+// 8.7 without the slots (45.8 us with one thread writing a slot's zeros).
 template <int D, typename T>
-__device__ __noinline__ void idle_sequence(const PgParams &p, int b, int len) {
-    if (len != 0) raise_device_error(p.err, kDevCheck);
+__device__ __noinline__ void idle_sequences(const PgParams &p, int b0, int step) {
 #pragma unroll 1
-    for (int i = 0; i < p.Hkv * p.G * (D / 8) && len == 0; ++i)
-        *reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + b * p.o_sb + (i / (D / 8)) * p.o_sh +
-                                   (i % (D / 8)) * 8) = make_uint4(0u, 0u, 0u, 0u);
+    for (int b = b0; b < p.B; b += step) {
+        const int len = p.seq_len[b];
+        if (len != 0 && make_plan(p, len).n == 0 && threadIdx.x == 0) raise_device_error(p.err, kDevCheck);
+        if (len != 0) continue;
+        for (int i = threadIdx.x; i < p.Hkv * p.G * (D / 8); i += blockDim.x)
+            *reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + b * p.o_sb + (i / (D / 8)) * p.o_sh +
+                                       (i % (D / 8)) * 8) = make_uint4(0u, 0u, 0u, 0u);
+    }
 }
 
 // Where this CTA's range starts (mark i: f0, or the first unit that starts at or
@@ -345,11 +352,13 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     ptx::griddep_launch_dependents();
 
     // ---- the lists' lengths, this CTA's range and where it starts.
-    //      Sequences with nothing to attend to are dealt out over the CTAs:
-    //      length 0 writes zeros, a length outside the table is reported and
-    //      its output left as it was.
+    //      Sequences with nothing to attend to are dealt out over the CTAs, the
+    //      last first (a short call leaves those without a range): length 0
+    //      writes zeros, a length outside the table is reported and its output
+    //      left as it was.
     const bool one_tile = p.B <= kNT;                  // a thread per sequence: read once
     int inc_l = 0, inc_s = 0, n_mine = 0, len_mine = 0, n_max = 0, units = 0, units_l = 0;
+    bool idle = false;
 #pragma unroll 1
     for (int b = threadIdx.x; b < p.B; b += kNT) {
         len_mine = p.seq_len[b];
@@ -362,7 +371,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
             inc_l += n_mine;
             ++units_l;
         }
-        if (n_mine == 0 && b % ctas == cta) idle_sequence<D, T>(p, b, len_mine);
+        idle = idle || (n_mine == 0 && b % ctas == ctas - 1 - cta);
     }
 #pragma unroll 1
     for (int off = 1; off < 32; off <<= 1) {
@@ -375,7 +384,9 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         units += __shfl_xor_sync(0xffffffffu, units, off);
         units_l += __shfl_xor_sync(0xffffffffu, units_l, off);
     }
+    idle = __any_sync(0xffffffffu, idle);
     if (lane == 31) {
+        ms->warp_idle[warp] = idle;
         ms->warp_long[warp] = inc_l;
         ms->warp_short[warp] = inc_s;
         ms->warp_max[warp] = n_max;
@@ -396,7 +407,9 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         n_max = imax(n_max, ms->warp_max[w]);
         units += ms->warp_units[w];
         units_l += ms->warp_units_l[w];
+        idle = idle || ms->warp_idle[w];
     }
+    if (idle) idle_sequences<D, T>(p, ctas - 1 - cta, ctas);
     if (n_max <= kAllShort) {                          // no long ones: one list
         total_s += total_l;
         before_s += before_l;
