@@ -804,3 +804,18 @@ def test_idle_slots_cost_little(ta):
     a call of 8 to 9: the limit leaves them four."""
     busy = [700, 300, 512, 128]
     assert decode_us(ta, busy + [0] * 60) < 1.5 * decode_us(ta, busy)
+
+
+@pytest.mark.parametrize("a,b,Hq,Hkv", [([2048], [200] * 24, 32, 8), ([2000], [300] * 100, 16, 2)])
+def test_one_longer_sequence_does_not_hold_up_the_others(ta, a, b, Hq, Hkv):
+    """One call over both batches takes no longer than a call for each of them."""
+    assert decode_us(ta, a + b, Hq, Hkv) < decode_us(ta, a, Hq, Hkv) + decode_us(ta, b, Hq, Hkv)
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv", [([2000] + [300] * 12, 16, 8), ([170 + i * 830 // 39 for i in range(40)], 8, 2),
+                                         ([2000] + [500] * 15, 8, 8), ([2048] + [200] * 24, 8, 8)])
+def test_decode_paged_ranges_of_mixed_units(ta, lens, Hq, Hkv):
+    q, kp, vp, table, sl, ks, vs = build_case("bf16", lens, Hq, Hkv, 128, 16, 0, 0, "head", 17)
+    o = ta.decode_gqa_paged(q, kp, vp, table, sl)
+    assert ta.device_status() == 0
+    check("bf16", q, ks, vs, lens, o, 0, 0)

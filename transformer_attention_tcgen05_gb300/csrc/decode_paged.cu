@@ -105,7 +105,7 @@ struct PgParams {
 };
 
 constexpr int kMaxWarps = 4;
-constexpr int kFitted = 64;       // chunks up to which a range is fitted to its units at any price
+constexpr int kFitted = 20;       // chunks by which a range may grow to be fitted to its units
 // The longest unit (chunks) that counts as short: beside long ones (40 sequences of
 // 1 to 900 tokens 11.7 us, 13.7 with 8, 11.8 with 4) and in a call without longer
 // ones (100 x 250 tokens 20.2 us, 23.1 with 5).
@@ -441,19 +441,27 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     // at least one chunk per warp, unless every unit is shorter than that: then
     // the units are spread over more CTAs
     if (!alone) per = imax(per, imin(CW, n_max));
-    // Where a quarter more chunks per range allow it, or ranges are short, a range
-    // holds part of one unit only, and its CTA merges and joins once instead of
-    // twice: with q = CTAs / units, parts of the longest unit's q-th give no more
-    // parts than CTAs.  The list is read as if each unit filled whole parts.
-    // (Equal units that fill whole ranges need no such thing.  8 x 1024 tokens:
-    // 13.3 us without, 11.6 with; 8 x 4096 27.2 and 25.4; 30 x 600 18.8 and 15.7;
-    // 8 x 8192 47.0 and 44.1; 8 x 32768 159 and 154.
-    // With longer ranges at any price, up to 128 chunks, 64 sequences of 1 to 4000
-    // tokens took 36.6 us instead of 25.5.)
+    // Where a quarter more chunks per range allow it, or 20, a range holds part of
+    // one unit only, and its CTA merges and joins once instead of twice: with q =
+    // CTAs / units, parts of the longest unit's q-th give no more parts than CTAs.
+    // The list is read as if each unit filled whole parts.  (Equal units that fill
+    // whole ranges need no such thing.)  That saves 2 to 3 us and costs what the
+    // longest range gains.  Chunks longer: us without and with (32 heads on 8, D 128)
+    //    1   8 x 1024 tokens 13.3, 11.6
+    //    4   30 x 600 18.3, 15.7
+    //    5   8 x 4096 27.2, 25.4
+    //   13   40 of 1 to 900 19.6, 17.4
+    //   16   30 of 200 to 1000 19.2, 17.4
+    //   17   120 of 170 to 1000, 16 heads on 2: 20.2, 17.6
+    //   24   one of 2000 beside 15 of 500 14.4, 16.0
+    //   30   36 of 170 to 2000 31.3, 30.4
+    //   31   20 of 300 to 1500 18.7, 20.1
+    //   51   one of 2000 beside 36 of 300 15.8, 24.2
+    //   57   one of 2048 beside 24 of 200 13.3, 22.8
     int parts = 0, parts_before = 0, parts_total = 0;
     const int n_units = in_short ? units : units_l;
     const int fit = n_units <= nc ? imax(per, cdiv(n_max, nc / imax(n_units, 1))) : 0;
-    if (!alone && one_tile && fit > 0 && fit <= imax(kFitted, per + per / 4) && n_max > per && total < (1 << 30) &&
+    if (!alone && one_tile && fit > 0 && fit <= per + imax(kFitted, per / 4) && n_max > per && total < (1 << 30) &&
         !(n_max % per == 0 && (long long)n_units * n_max == total)) {
         per = fit;
         parts = int(unsigned(n_mine + per - 1) / unsigned(per));
