@@ -819,3 +819,32 @@ def test_decode_paged_ranges_of_mixed_units(ta, lens, Hq, Hkv):
     o = ta.decode_gqa_paged(q, kp, vp, table, sl)
     assert ta.device_status() == 0
     check("bf16", q, ks, vs, lens, o, 0, 0)
+
+
+@pytest.mark.parametrize("P", [300, 30000])         # one CTA, a cluster
+@pytest.mark.parametrize("what", ["tail", "full", "two targets"])
+def test_fork_refuses_pages_counted_too_low_every_time(ta, P, what):
+    """A page that a source and a target row name but that is counted once is let go
+    by the target: it must not be handed out, whichever thread comes first."""
+    S, M, B = 8, 40, 6
+    table = torch.full((B, M), -1, dtype=torch.int32, device="cuda")
+    n = [20 * 8 + 3, 0, 0, 0, 9 * 8, 0]
+    table[0, :21] = torch.arange(21, dtype=torch.int32)
+    table[4, :9] = torch.arange(50, 59, dtype=torch.int32)
+    refs = torch.zeros(P, dtype=torch.int32, device="cuda")
+    refs[:21] = 1
+    refs[50:59] = 1
+    if what == "tail":                               # row 0's last page, partly filled
+        table[1, 2] = 20
+    elif what == "full":
+        table[1, 0] = 7
+    else:
+        table[1, 5] = table[2, 39] = 55
+    sl = torch.tensor(n, dtype=torch.int32, device="cuda")
+    src, dst = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 4], [1, 2]))
+    before = [x.clone() for x in (table, refs, sl)]
+    for _ in range(50):
+        cs, cd = ta.kv_pages_fork(table, sl, refs, src, dst, S)
+        assert ta.device_status() == 6
+        assert cs.tolist() == cd.tolist() == [-1, -1]
+        assert all(torch.equal(a, b) for a, b in zip(before, (table, refs, sl)))

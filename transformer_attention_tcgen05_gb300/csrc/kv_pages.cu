@@ -663,9 +663,9 @@ __global__ void __launch_bounds__(kAT, 1) fork_kernel(const AllocParams p) {
             if (len < 0 || len > (long long)p.M * p.S) {
                 bad = 1;
             } else if (len % p.S != 0) {
-                // a partly filled last page, to be copied from: it must be counted
+                // a partly filled last page, to be copied from
                 tail = p.table[s * p.stride + len / p.S];
-                if (tail < -1 || tail >= p.P || (tail >= 0 && p.refs[tail] <= 0)) bad = 1;
+                if (tail < -1 || tail >= p.P) bad = 1;
             }
         }
         s_tail[i] = tail;
@@ -680,39 +680,34 @@ __global__ void __launch_bounds__(kAT, 1) fork_kernel(const AllocParams p) {
             if (s >= 0 && s < p.B && (is_dst[s >> 5] >> (s & 31) & 1u)) bad = 1;
         }
     block_sum3(sh, bad, zero, wrong);                  // the same in every CTA
-    // ---- counts: the targets' old pages let go, the shared full pages taken.
-    //      Work item: 128 entries of one fork, a warp each.  An entry that is no
-    //      counted page makes the call fail; the counts are put back then.
+    // ---- counts: the targets' old pages are let go, and what is left is looked
+    //      at: a page that a source names must still be counted, or it would be
+    //      handed out.  An entry that is no counted page makes the call fail; the
+    //      counts are put back then.  No count rises before all have fallen, so
+    //      the verdict does not depend on which CTA is first.
+    //      Work item: 128 entries of one fork, a warp each.
     const int blocks = cdiv(p.M, 128);
     const long long items = (long long)p.n * blocks;
     const int w0 = warp * int(gridDim.x) + rank, wn = int(gridDim.x) * (kAT / 32);
-    auto recount = [&](int sign) {
+    auto let_go = [&](int sign) {
         for (long long it = w0; it < items; it += wn) {
             const int f = int(it / blocks), j0 = int(it % blocks) * 128;
-            const int32_t *rs = p.table + s_src[f] * p.stride, *rd = p.table + s_dst[f] * p.stride;
-            const int full = s_len[f] / p.S;
-            int old[4], e[4];
+            const int32_t *rd = p.table + s_dst[f] * p.stride;
+            int old[4], was[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int j = j0 + u * 32 + lane;
                 old[u] = j < p.M ? rd[j] : -1;
-                e[u] = j < full ? rs[j] : -1;
             }
-            // the eight counts change together; what they were is looked at behind
-            int was[8];
+            // the counts change together; what they were is looked at behind
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                was[u] = add_if(old[u] >= 0 && old[u] < p.P, p.refs + old[u], -sign);
-                was[4 + u] = add_if(e[u] >= 0 && e[u] < p.P, p.refs + e[u], sign);
-            }
+            for (int u = 0; u < 4; ++u) was[u] = add_if(old[u] >= 0 && old[u] < p.P, p.refs + old[u], -sign);
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                if (old[u] < -1 || old[u] >= p.P || e[u] < -1 || e[u] >= p.P ||
-                    (sign > 0 && (was[u] <= 0 || was[4 + u] <= 0)))
-                    wrong = 1;
+                if (old[u] < -1 || old[u] >= p.P || (sign > 0 && was[u] <= 0)) wrong = 1;
         }
     };
-    if (!bad) recount(1);
+    if (!bad) let_go(1);
     int tails = 0;                                     // last pages to copy, numbered in list order
     for (int b0 = 0; b0 < p.n && !bad; b0 += kAT) {
         const int f = b0 + threadIdx.x;
@@ -722,7 +717,23 @@ __global__ void __launch_bounds__(kAT, 1) fork_kernel(const AllocParams p) {
         if (f < p.n) s_rank[f] = k;
         tails += all;
     }
-    cluster_barrier();                                 // every count is in
+    cluster_barrier();                                 // every page is let go
+    for (long long it = w0; it < items && !bad; it += wn) {
+        const int f = int(it / blocks), j0 = int(it % blocks) * 128;
+        const int32_t *rs = p.table + s_src[f] * p.stride;
+        const int full = s_len[f] / p.S;
+        int e[4], n[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int j = j0 + u * 32 + lane;
+            e[u] = j < full ? rs[j] : j == full ? s_tail[f] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) n[u] = e[u] >= 0 && e[u] < p.P ? p.refs[e[u]] : 1;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (e[u] < -1 || e[u] >= p.P || n[u] <= 0) wrong = 1;
+    }
     unsigned bits = 0;
     int my_free = bad ? 0 : count_free(p, &bits);
     put_chunk(sh, 0, bits);
@@ -734,7 +745,7 @@ __global__ void __launch_bounds__(kAT, 1) fork_kernel(const AllocParams p) {
     const int free0 = exchange(sh, sum, &none);
     const bool refuse = sum[1] || tails > sum[2];      // the same in every CTA
     if (refuse) {
-        if (!bad) recount(-1);                         // nothing has changed but the counts
+        if (!bad) let_go(-1);                          // nothing has changed but the counts
     } else {
         take_free(p, sh, tails, bits, free0);
     }
@@ -760,6 +771,7 @@ __global__ void __launch_bounds__(kAT, 1) fork_kernel(const AllocParams p) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int j = j0 + u * 32 + lane;
+            if (e[u] >= 0) atomicAdd(&p.refs[e[u]], 1);     // a shared full page
             if (j >= p.M) continue;
             if (j == full) {                           // the last page, or the first entry behind it
                 if (s_tail[f] >= 0) e[u] = p.ws[s_rank[f]];
