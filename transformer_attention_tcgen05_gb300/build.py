@@ -7,7 +7,9 @@ Each .cu under csrc/ compiles in parallel with nvcc for sm_103a only, then
 links into transformer_attention_tcgen05_gb300/_build/libattn.so with the
 CUDA runtime linked statically.  The binding (csrc/binding.cpp) compiles with
 the host compiler against the installed torch and Python headers and links to
-libattn.so beside it.  Rebuilds only what changed.
+libattn.so beside it.  The library does not need the binding: where the binding
+cannot be built, libattn.so is, and the entry points that go through the binding
+raise.  Rebuilds only what changed.
 """
 from __future__ import annotations
 
@@ -18,6 +20,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -82,7 +85,9 @@ def _link_binding(obj: str) -> None:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile (if stale) and link libattn.so and the binding; returns libattn.so's path."""
+    """Compile (if stale) and link libattn.so and the binding; returns libattn.so's path.
+
+    Raises if libattn.so cannot be built; a binding that cannot be is a warning."""
     os.makedirs(OUT, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     hdr_time = max([os.path.getmtime(h) for h in _headers()] + [0.0])
@@ -95,6 +100,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     bsrc, bobj = os.path.join(CSRC, "binding.cpp"), os.path.join(OUT, "binding.o")
     bind = force or not os.path.exists(bobj) or \
         os.path.getmtime(bobj) < max(os.path.getmtime(bsrc), hdr_time)
+    failed = None                                # why there is no binding
     if jobs or bind:
         with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs) + 1)) as ex:
             bound = ex.submit(_compile_binding, bobj) if bind else None
@@ -102,7 +108,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 if verbose and log:
                     sys.stderr.write(f"== {os.path.basename(s)}\n{log}")
             if bound:
-                bound.result()
+                failed = bound.exception()
     objs = [os.path.join(OUT, os.path.basename(s)[:-3] + ".o") for s in srcs]
     if jobs or not os.path.exists(LIB) or \
             os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
@@ -112,8 +118,18 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}")
         os.replace(tmp, LIB)
-    if bind or not os.path.exists(BINDING) or os.path.getmtime(BINDING) < os.path.getmtime(bobj):
-        _link_binding(bobj)
+    if not failed and (bind or not os.path.exists(BINDING) or
+                       os.path.getmtime(BINDING) < os.path.getmtime(bobj)):
+        try:
+            _link_binding(bobj)
+        except Exception as e:
+            failed = e
+    if failed:
+        for old in (BINDING, bobj):              # what an earlier build left does not fit these sources
+            if os.path.exists(old):
+                os.remove(old)
+        warnings.warn(f"the native binding was not built, its entry points will raise: {failed}",
+                      RuntimeWarning, stacklevel=2)
     return LIB
 
 
