@@ -45,3 +45,24 @@ def test_libattn_is_built_where_the_binding_cannot_be(fresh, monkeypatch):
     monkeypatch.delenv("CXX")
     b.build()
     assert os.path.exists(b.BINDING)
+
+
+@pytest.mark.parametrize("other", ["torch", "python"])
+def test_the_binding_is_built_again_for_another_torch_or_python(fresh, monkeypatch, other):
+    import sysconfig
+
+    import torch
+    b.build()
+    at = os.path.getmtime(b.BINDING), os.path.getmtime(b.LIB)
+    b.build()
+    assert at == (os.path.getmtime(b.BINDING), os.path.getmtime(b.LIB))
+    if other == "torch":
+        monkeypatch.setattr(torch, "__version__", "0.0.0+other")
+    else:
+        real = sysconfig.get_config_var
+        monkeypatch.setattr(sysconfig, "get_config_var", lambda n: "other" if n == "SOABI" else real(n))
+    b.build()
+    assert os.path.getmtime(b.BINDING) > at[0] and os.path.getmtime(b.LIB) == at[1]
+    again = os.path.getmtime(b.BINDING)
+    b.build()
+    assert os.path.getmtime(b.BINDING) == again

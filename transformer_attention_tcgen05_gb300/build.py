@@ -9,7 +9,7 @@ CUDA runtime linked statically.  The binding (csrc/binding.cpp) compiles with
 the host compiler against the installed torch and Python headers and links to
 libattn.so beside it.  The library does not need the binding: where the binding
 cannot be built, libattn.so is, and the entry points that go through the binding
-raise.  Rebuilds only what changed.
+raise.  Rebuilds only what changed, the binding also for another torch or Python.
 """
 from __future__ import annotations
 
@@ -72,6 +72,12 @@ def _compile_binding(obj: str) -> str:
     return r.stderr
 
 
+def _binding_for() -> str:
+    """What a binding is built for: it fits no other torch or Python."""
+    import torch
+    return f"torch {torch.__version__} {torch._C._GLIBCXX_USE_CXX11_ABI} python {sysconfig.get_config_var('SOABI')}"
+
+
 def _link_binding(obj: str) -> None:
     import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
@@ -98,7 +104,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 os.path.getmtime(o) < max(os.path.getmtime(s), hdr_time):
             jobs.append((s, o))
     bsrc, bobj = os.path.join(CSRC, "binding.cpp"), os.path.join(OUT, "binding.o")
-    bind = force or not os.path.exists(bobj) or \
+    stamp = bobj + ".for"                        # written once the binding is built
+    made_for = open(stamp).read() if os.path.exists(stamp) else ""
+    bind = force or not os.path.exists(bobj) or made_for != _binding_for() or \
         os.path.getmtime(bobj) < max(os.path.getmtime(bsrc), hdr_time)
     failed = None                                # why there is no binding
     if jobs or bind:
@@ -122,6 +130,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
                        os.path.getmtime(BINDING) < os.path.getmtime(bobj)):
         try:
             _link_binding(bobj)
+            with open(stamp, "w") as f:
+                f.write(_binding_for())
         except Exception as e:
             failed = e
     if failed:
