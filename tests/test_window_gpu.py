@@ -306,3 +306,41 @@ def test_a_key_that_other_rows_see_leaves_every_bit_of_a_row(ta, dt, D, Hq, spot
     see = visible(N, range(N), window, 2)[:, spot].cuda()
     assert torch.isnan(o[:, :, see].float()).all()
     assert torch.equal(o[:, :, ~see], clean[:, :, ~see])
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 128), ("f16", 64)])
+@pytest.mark.parametrize("rest", ["split", "whole", "none", "odd group"])
+def test_window_last_round_of_items(ta, dt, D, rest):
+    """Items are pairs of query tiles, one per CTA; those of a last round that takes
+    at most half of the SMs go out as single tiles.  Chosen by the SM count: a
+    remainder that is split, one that is not, none, and (pairs of row tiles, split)
+    a last pair whose second tile lies behind the queries."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    N, window, sinks = 129, 40, 3
+    if rest == "odd group":
+        # three heads per KV head, one pair of row tiles each, 100 queries: the second is empty
+        Hkv = next(h for h in range(1, 400) if 0 < 2 * (3 * h % sms) <= sms and 3 * h > sms)
+        Hq, N = 3 * Hkv, 100
+        pairs = Hq
+    else:
+        want = {"split": lambda r: 0 < 2 * r <= sms, "whole": lambda r: 2 * r > sms, "none": lambda r: r == 0}[rest]
+        # two row blocks, two heads per KV head: two pairs per KV head
+        Hkv = next(h for h in range(1, 2 * sms) if want(2 * h % sms) and (rest != "split" or 2 * h > sms))
+        Hq, pairs = 2 * Hkv, 2 * Hkv
+    r = pairs % sms
+    assert (0 < 2 * r <= sms) == (rest in ("split", "odd group"))
+    q = make(dt, 1, Hq, N, D, "head", 80)
+    k, v = make(dt, 1, Hkv, N, D, "head", 81), make(dt, 1, Hkv, N, D, "head", 82)
+    wide = torch.full((1, Hq, N + 60, D), 7.0, dtype=DT[dt], device="cuda")
+    o = wide[:, :, :N]
+    ta.causal_gqa_window_fwd(q, k, v, window, sinks, o=o)
+    assert ta.device_status() == 0
+    assert (wide[:, :, N:] == 7).all()
+    heads = sorted({0, 1, 2, Hq // 2, Hq - 3, Hq - 2, Hq - 1})
+    g = Hq // Hkv
+    for h in heads:
+        check(ta, dt, q[:, h:h + 1], k[:, h // g:h // g + 1], v[:, h // g:h // g + 1], o[:, h:h + 1], window, sinks)
+    # the other heads: each as it comes out of a call of its own
+    for h in range(0, Hkv, 7):
+        one = ta.causal_gqa_window_fwd(q[:, h * g:(h + 1) * g], k[:, h:h + 1], v[:, h:h + 1], window, sinks)
+        assert torch.equal(one, o[:, h * g:(h + 1) * g])
