@@ -390,7 +390,8 @@ ATTN_API size_t attn_decode_gqa_paged_workspace_bytes(int B, int Hq, int Hkv, in
 /*
  * The page allocator.  Each call takes its pages lowest number first and
  * serves requests in (row, entry) order, so its result depends on its inputs
- * alone.  A request that cannot be met, or an argument on the device that is
+ * alone (but for free where a page's count is too low: which of the entries that
+ * name it keep it).  A request that cannot be met, or an argument on the device that is
  * out of range, sets ATTN_ERR_DEVICE_CHECK and changes nothing (free: the
  * entry, or the row of that seq_len, stays; compact: an entry that names no live page becomes
  * -1).  page_refs must count the table's entries, as these calls keep it; calls

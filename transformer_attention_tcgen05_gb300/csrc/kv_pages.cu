@@ -1032,8 +1032,8 @@ attn_status_t kv_pages_fork(const Ctx &c, const PageTable &t, int32_t *seq_len, 
     if (!ensure_smem_attr(reinterpret_cast<const void *>(fork_kernel), 5 * kMaxForks * 4 + kMaxRows / 8, c.device,
                           &done_mask))
         return ATTN_ERR_RESOURCE;
-    // an entry is read twice and costs two atomics on the counts (16 rows of 250
-    // entries: 12.2 us in one CTA, 11.2 in eight; 21 of 52: 10.4 and 10.8)
+    // an entry is read three times and costs two atomics on the counts (16 rows of
+    // 254 entries: 12.4 us in one CTA, 9.8 in eight; 21 of 52: 9.4 and 9.5)
     const int ctas = cluster_size(8ll * n * t.max_pages + t.P);
     p.quads = chunk_quads(t.P, ctas);
     return launch_pdl(c, fork_kernel, dim3(ctas), kAT, ctas, size_t(5 * n + cdiv(t.B, 32)) * 4, p);

@@ -9,8 +9,10 @@
 // MMA.  Bound by the exponentials and the tensor pipe at about 1.2 us per step of
 // two tiles, plus about 6 us per CTA (set-up, first loads, masked tiles, last
 // P V and epilogue), which is what a short window pays for: 4096 tokens, 32 heads
-// on 8, window 1024, sinks 4, D 128: 58.8 us = 1026 TFLOP/s; 32768 tokens, window
-// 4096: 1220 us = 1692 TFLOP/s.  What differs:
+// on 8, window 1024, sinks 4, D 128: 58.1 us = 1039 TFLOP/s; 32768 tokens, window
+// 4096: 1225 us = 1684 TFLOP/s for the first 20 calls in a row, then 1310 to 1335 us
+// at the clock that the power cap leaves.  (The steps on record below were timed in
+// short runs, against the kernel of their time.)  What differs:
 //
 //  * Key tile list.  A CTA streams the sink tiles and the tiles of its windows
 //    only; tiles on an edge (diagonal, window start, sinks) are masked per
@@ -49,8 +51,8 @@
 // other tiles on an edge a warp that has nothing else to do looks the values over
 // while the scores are computed and clears what is not finite, and the rows that
 // do see such a value get it back in the epilogue (spoil_rows).  With finite
-// inputs 4096 tokens take 58.4 us (58.1 without any of it), 32768 tokens 1226
-// (1222); with one infinite value 8192 tokens, 8 heads on 2, window 2048, took
+// inputs 4096 tokens take 58.4 us where 58.1 go without any of it, 32768 tokens
+// 1226 and 1222; with one infinite value 8192 tokens, 8 heads on 2, window 2048, took
 // 58 ms as long as rows that were not finite were computed again key by key.
 //
 // All spin-waits are bounded (1 s); on a timeout the CTA raises the device
