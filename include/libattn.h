@@ -57,6 +57,13 @@ typedef enum {
 } attn_dtype_t;
 
 typedef enum {
+    ATTN_ROPE_UNSCALED = 0,
+    ATTN_ROPE_LINEAR = 1,
+    ATTN_ROPE_NTK = 2,
+    ATTN_ROPE_BY_PARTS = 3
+} attn_rope_scaling_t;
+
+typedef enum {
     ATTN_OK = 0,
     ATTN_ERR_INVALID_ARG = 1,   /* null pointer, bad shape, bad kernel, ...       */
     ATTN_ERR_UNSUPPORTED = 2,   /* valid request this build has no kernel for     */
@@ -300,6 +307,38 @@ ATTN_API attn_status_t attn_causal_gqa_window_fwd(const void *q, const void *k, 
                                                   void *stream);
 
 /*
+ * Causal grouped-query attention over packed sequences of different lengths.
+ *   q, o [Nq, Hq, D], k, v [Nkv, Hkv, D], element strides (token, head) in
+ *   x_strides[2] (NULL: contiguous).  cu_q, cu_k: DEVICE int32 [B + 1]: sequence b
+ *   has the queries [cu_q[b], cu_q[b + 1]) and the keys [cu_k[b], cu_k[b + 1]);
+ *   cu_k may be cu_q.  The queries of a sequence are the last of its positions,
+ *   as in attn_causal_gqa_window_fwd, whose window, sinks and rules for infinities
+ *   and NaN hold within each sequence: what lies in other sequences' rows, or
+ *   between them, does not change a bit of its output.
+ *   Sequences may be empty, and so may cu_q's (keys without queries).  Rows of o
+ *   outside every sequence are left as they were.  A sequence with more queries
+ *   than keys, or whose starts do not rise or pass Nq / Nkv, sets
+ *   ATTN_ERR_DEVICE_CHECK and its rows of o are left as they were (but for rows
+ *   that another sequence, whose own starts rise, claims as well).
+ *   The lengths are read on the device: Nq and Nkv are the arrays' extents, and
+ *   a captured call serves any lengths within them.  bf16 and f16 run on the
+ *   tensor cores for D in {64, 128}; fp32 (and the 16-bit types with D = 32) on
+ *   the exact-FFMA SIMT kernel.  B <= 65535, Nq and Nkv <= 2^30.
+ * Passage: fak "GPU - the in-kernel forward pass", section 3 (Llama prefill of
+ * a grouped-query model), for a batch of prompts without padding.
+ */
+ATTN_API attn_status_t attn_causal_gqa_varlen_fwd(const void *q, const void *k, const void *v,
+                                                  void *o, const int32_t *cu_q,
+                                                  const int32_t *cu_k, int B, int Nq, int Nkv,
+                                                  int Hq, int Hkv, int D,
+                                                  const int64_t q_strides[2],
+                                                  const int64_t k_strides[2],
+                                                  const int64_t v_strides[2],
+                                                  const int64_t o_strides[2], int window,
+                                                  int sinks, attn_dtype_t dtype, float scale,
+                                                  void *stream);
+
+/*
  * Paged KV cache.  Many sequences share one pool of pages of `page_size`
  * tokens; a page table names each sequence's pages.  Conventions of all
  * entries below:
@@ -386,6 +425,154 @@ ATTN_API attn_status_t attn_decode_gqa_paged(const void *q, const void *k_pages,
                                              size_t workspace_bytes, void *stream);
 
 ATTN_API size_t attn_decode_gqa_paged_workspace_bytes(int B, int Hq, int Hkv, int D);
+
+/*
+ * Rotary positions.  The first rotary_dim channels of a row at position t are
+ * rotated in pairs (a, b) by the angle t theta_i, i < rotary_dim / 2:
+ *     a' = m (a cos - b sin),   b' = m (b cos + a sin);
+ * pair i is channels (i, i + rotary_dim / 2), or (2i, 2i + 1) if interleaved.
+ * The other channels are copied.  rotary_dim is a multiple of 16, at most D.
+ *   freq: DEVICE uint64 [rotary_dim / 2], theta_i as a fraction of a turn per
+ *     position, 2^64 theta_i / (2 pi) (8-byte aligned).  The angle is the product
+ *     modulo 2^64, so it is as exact at position 2^31 - 1 as at 0.
+ *   mscale: the factor m (1 for plain rotary positions; not for the copied
+ *     channels).  Must be finite.
+ *
+ * attn_rope_frequencies fills freq (HOST memory here; the caller copies it to
+ * the device, once) with theta_i = theta^(-2i / rotary_dim), scaled for contexts
+ * `factor` times the original length:
+ *   ATTN_ROPE_UNSCALED  as it is;
+ *   ATTN_ROPE_LINEAR    theta_i / factor;
+ *   ATTN_ROPE_NTK       with theta factor^(rotary_dim / (rotary_dim - 2)) in
+ *                       the place of theta;
+ *   ATTN_ROPE_BY_PARTS  (1 - g) theta_i / factor + g theta_i, where a pair that
+ *                       makes r = original_len theta_i / (2 pi) turns within the
+ *                       original length has g = (r - alpha) / (beta - alpha),
+ *                       held to [0, 1].
+ *   theta > 0 and factor > 0 finite; by parts also original_len > 0 and beta >
+ *   alpha.  A theta_i of half a turn or more is refused.
+ *
+ * attn_rope_fwd: y = the rotated rows of x, both [B, H, N, D] with element
+ *   strides (batch, head, token) in x_strides / y_strides[3] (NULL: contiguous).
+ *   positions: DEVICE int32 [B, N], rows pos_stride entries apart (0: one row for
+ *   all batches); any value, negative ones too.  inverse != 0: the transposed
+ *   rotation (angles negated), which is the gradient of the call with respect
+ *   to x.  y may be x itself, with x's strides (in place); it must not overlap x
+ *   otherwise.  All dtypes, D in {32, 64, 128}; fp32 arithmetic, rounded once.
+ * Passage: iris.c issue #15 "CUDA codepath !" (custom RoPE kernel) and fak
+ * "GPU - the in-kernel forward pass", section 3 (the rotary step of a Llama
+ * layer); the scalings are published extensions of it.
+ */
+ATTN_API attn_status_t attn_rope_frequencies(uint64_t *freq, int rotary_dim, double theta,
+                                             attn_rope_scaling_t scaling, double factor,
+                                             double original_len, double alpha, double beta);
+
+ATTN_API attn_status_t attn_rope_fwd(const void *x, void *y, const uint64_t *freq,
+                                     const int32_t *positions, int64_t pos_stride, int B, int H,
+                                     int N, int D, int rotary_dim, int interleaved, int inverse,
+                                     float mscale, const int64_t x_strides[3],
+                                     const int64_t y_strides[3], attn_dtype_t dtype, void *stream);
+
+/*
+ * attn_kv_append_paged for packed new tokens, K rotated on the way.
+ *   k_new, v_new [N, Hkv, D] (read), q, q_out [N, Hq, D], element strides (token,
+ *   head) in kn_strides / vn_strides / q_strides / qo_strides[2] (NULL: contiguous),
+ *   e.g. column blocks of one packed projection.
+ *   cu_new: DEVICE int32 [B + 1], sequence b's new tokens are rows [cu_new[b],
+ *   cu_new[b + 1]); rows outside every sequence are not touched.  NULL: one token
+ *   per sequence, row b (N == B).
+ *   Row cu_new[b] + t goes to position seq_len[b] + t: K is rotated for that
+ *   position (freq, rotary_dim, interleaved and mscale as in attn_rope_fwd) and
+ *   rounded once, V is copied.  q, if not NULL, is rotated likewise into q_out
+ *   (which may be q itself, with q's strides).  If advance != 0, seq_len[b] +=
+ *   the sequence's new tokens afterwards.
+ *   Pages, errors and their effects as for attn_kv_append_paged: a request that
+ *   does not fit the table, or starts that do not rise or pass N, writes nothing
+ *   for that sequence (its rows of q_out neither); a token whose entry is no
+ *   page is not written.  Either sets ATTN_ERR_DEVICE_CHECK and leaves that
+ *   sequence's seq_len as it was.
+ *   All dtypes, D in {32, 64, 128}; Hkv and Hq at most 65535.
+ * Passage: fak "GPU - the in-kernel forward pass", section 3b (kernel-form KV
+ * append), with the rotary step before it.
+ */
+ATTN_API attn_status_t attn_kv_append_paged_rope(
+    void *k_pages, void *v_pages, const void *k_new, const void *v_new, const void *q, void *q_out,
+    const int32_t *page_table, int32_t *seq_len, const int32_t *cu_new, const uint64_t *freq, int B,
+    int N, int Hq, int Hkv, int D, int rotary_dim, int interleaved, float mscale, int num_pages,
+    int page_size, int max_pages, int64_t table_stride, const int64_t k_strides[3],
+    const int64_t v_strides[3], const int64_t kn_strides[2], const int64_t vn_strides[2],
+    const int64_t q_strides[2], const int64_t qo_strides[2], attn_dtype_t dtype, int advance,
+    void *stream);
+
+/*
+ * Paged KV cache held in 4 bits.  One array kv_pages holds K and V: a page is
+ * [Hkv, page_size] rows of attn_kv_q4_row_bytes(D) = D + D / 8 bytes, one token
+ * and KV head each; the rows of a (page, head) are contiguous, pages_strides[2]
+ * are the BYTE strides of (page, head) (NULL: contiguous), multiples of 16.
+ * Page table, lengths and allocator are those of the paged cache above.
+ *   Values are held in groups of 32 channels as s (n - 8), n in [0, 15].  With
+ *   x* the group's largest or its least value, whichever is further from zero
+ *   (the largest if both are), s = -x* / 8, rounded to `dtype` (ATTN_BF16 or
+ *   ATTN_F16; below 2^-126: 0), and n = rint(x (1 / s)) + 8, held to [0, 15], in
+ *   fp32 (s = 0: n = 8).  A group that holds an infinity or NaN, or whose s does
+ *   not fit, is NaN throughout.  A cache is read with the dtype it was written with.
+ *   A row is: the codes of K (D / 2 bytes), those of V (D / 2), the scales of K's
+ *   groups (D / 16), those of V's (D / 16).  The codes of four consecutive channels
+ *   form a 16-bit word, channel i's at bit 4 i, rotated right by two bits
+ *   (little-endian).  Channel c = 32 g + r: K's word lies at byte (r / 8) D / 8 +
+ *   4 g + 2 (r / 4 mod 2), V's at D / 2 + (r / 4) D / 16 + 2 g.
+ *   D in {64, 128}, dtype ATTN_BF16 or ATTN_F16.
+ *
+ * attn_kv_append_paged_q4: attn_kv_append_paged_rope into such pages.  freq NULL
+ *   (rotary_dim 0): neither K nor q is rotated (q is copied to q_out).
+ * attn_kv_gather_paged_q4: the reader.  k, v [N, Hkv, D] (written, strides (token,
+ *   head)); row cu_len[b] + t receives position start[b] + t of sequence b
+ *   (DEVICE int32; start NULL: 0), t < cu_len[b + 1] - cu_len[b], rounded once to
+ *   dtype.  Rows outside every sequence are left as they were.  A position
+ *   outside the table, or whose entry is no page, is left as it was and sets
+ *   ATTN_ERR_DEVICE_CHECK; so are all rows of a sequence whose starts do not
+ *   rise or pass N.  It gives the cached keys and values of a prompt
+ *   that is continued to attn_causal_gqa_varlen_fwd.
+ * attn_kv_pages_copy_q4: attn_kv_pages_copy for such pages; strides[3]: BYTE
+ *   strides of (layer, page, head) (NULL: contiguous).
+ * attn_decode_gqa_paged_q4: attn_decode_gqa_paged over such pages: the same
+ *   arguments, visibility, errors and workspace rules, with a workspace of
+ *   attn_decode_gqa_paged_q4_workspace_bytes(...) bytes.  Codes are multiplied as they are and
+ *   scaled in fp32; a weight times its value's scale is rounded to 11 bits for
+ *   the P V product.  Outputs are finite for scales of up to 2^100.
+ * Passage: fak "GPU - the in-kernel forward pass", section 3b (the device KV
+ * cache), section 4 (decode attention), and candle PR #11's int8 rows with a scale
+ * for the idea of holding rows in fewer bits.
+ */
+ATTN_API size_t attn_kv_q4_row_bytes(int D);
+
+ATTN_API attn_status_t attn_kv_append_paged_q4(
+    void *kv_pages, const void *k_new, const void *v_new, const void *q, void *q_out,
+    const int32_t *page_table, int32_t *seq_len, const int32_t *cu_new, const uint64_t *freq, int B,
+    int N, int Hq, int Hkv, int D, int rotary_dim, int interleaved, float mscale, int num_pages,
+    int page_size, int max_pages, int64_t table_stride, const int64_t pages_strides[2],
+    const int64_t kn_strides[2], const int64_t vn_strides[2], const int64_t q_strides[2],
+    const int64_t qo_strides[2], attn_dtype_t dtype, int advance, void *stream);
+
+ATTN_API attn_status_t attn_kv_gather_paged_q4(
+    const void *kv_pages, const int32_t *page_table, const int32_t *start, const int32_t *cu_len,
+    void *k, void *v, int B, int N, int Hkv, int D, int num_pages, int page_size, int max_pages,
+    int64_t table_stride, const int64_t pages_strides[2], const int64_t k_strides[2],
+    const int64_t v_strides[2], attn_dtype_t dtype, void *stream);
+
+ATTN_API attn_status_t attn_kv_pages_copy_q4(void *kv_pages, const int32_t *copy_src,
+                                             const int32_t *copy_dst, int n, const int32_t *count,
+                                             int layers, int num_pages, int Hkv, int page_size,
+                                             int D, const int64_t strides[3], void *stream);
+
+ATTN_API attn_status_t attn_decode_gqa_paged_q4(
+    const void *q, const void *kv_pages, const int32_t *page_table, const int32_t *seq_len, void *o,
+    int B, int Hq, int Hkv, int D, int num_pages, int page_size, int max_pages,
+    int64_t table_stride, const int64_t q_strides[2], const int64_t pages_strides[2],
+    const int64_t o_strides[2], int window, int sinks, attn_dtype_t dtype, float scale,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+ATTN_API size_t attn_decode_gqa_paged_q4_workspace_bytes(int B, int Hq, int Hkv, int D);
 
 /*
  * The page allocator.  Each call takes its pages lowest number first and

@@ -19,6 +19,12 @@ Paged KV cache (pages [P, Hkv, page_size, D], page_table int32 [B, max_pages]):
     decode_gqa_paged(q, k_pages, v_pages, page_table, seq_len, window, sinks)
     kv_append_paged(k_pages, v_pages, k_new, v_new, page_table, seq_len, new_len)
     kv_pages_reserve / kv_pages_free / kv_pages_fork / kv_pages_compact / kv_pages_copy
+Packed sequences (rows [N, H, D] of many sequences, starts cu int32 [B + 1]):
+    rope_fwd(x, freq, positions)               rotary positions (freq = rope_frequencies(...))
+    causal_gqa_varlen_fwd(q, k, v, cu_q, cu_k, window, sinks)
+    kv_append_paged_rope(k_pages, v_pages, k_new, v_new, page_table, seq_len, freq, cu_new, q)
+Paged KV cache held in 4 bits (kv_pages uint8 [P, Hkv, page_size, D + D / 8]):
+    kv_append_paged_q4 / kv_gather_paged_q4 / kv_pages_copy_q4 / decode_gqa_paged_q4
 """
 from __future__ import annotations
 
@@ -35,6 +41,9 @@ __all__ = [
     "causal_gqa_window_fwd", "decode_gqa_paged", "decode_paged_workspace_bytes", "kv_append_paged",
     "kv_pages_workspace_bytes", "kv_pages_reserve", "kv_pages_free", "kv_pages_fork",
     "kv_pages_compact", "kv_pages_copy",
+    "rope_frequencies", "rope_fwd", "causal_gqa_varlen_fwd", "kv_append_paged_rope", "kv_append_paged_q4",
+    "kv_gather_paged_q4", "kv_pages_copy_q4", "kv_q4_row_bytes", "decode_gqa_paged_q4",
+    "decode_paged_q4_workspace_bytes",
     "device_status", "debug_wait_test", "launch_count", "version", "FAMILIES", "LIB_PATH",
 ]
 
@@ -109,6 +118,22 @@ def lib() -> ctypes.CDLL:
                                             _i64, _vp, _sz, _vp]
         L.attn_kv_pages_copy.argtypes = [_vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _st, _st,
                                          _i, _vp]
+        _d = ctypes.c_double
+        L.attn_rope_frequencies.argtypes = [_vp, _i, _d, _i, _d, _d, _d, _d]
+        L.attn_rope_fwd.argtypes = [_vp, _vp, _vp, _vp, _i64, _i, _i, _i, _i, _i, _i, _i, _f, _st, _st, _i, _vp]
+        L.attn_kv_append_paged_rope.argtypes = [_vp] * 10 + [_i] * 7 + [_f, _i, _i, _i, _i64] + [_st] * 6 + \
+            [_i, _i, _vp]
+        L.attn_kv_append_paged_q4.argtypes = [_vp] * 9 + [_i] * 7 + [_f, _i, _i, _i, _i64] + [_st] * 5 + \
+            [_i, _i, _vp]
+        L.attn_kv_gather_paged_q4.argtypes = [_vp] * 6 + [_i] * 7 + [_i64, _st, _st, _st, _i, _vp]
+        L.attn_kv_pages_copy_q4.argtypes = [_vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _st, _vp]
+        L.attn_decode_gqa_paged_q4.argtypes = [_vp] * 5 + [_i] * 7 + [_i64, _st, _st, _st, _i, _i, _i, _f, _vp,
+                                                                      _sz, _vp]
+        L.attn_decode_gqa_paged_q4_workspace_bytes.argtypes = [_i, _i, _i, _i]
+        L.attn_decode_gqa_paged_q4_workspace_bytes.restype = _sz
+        L.attn_kv_q4_row_bytes.argtypes = [_i]
+        L.attn_kv_q4_row_bytes.restype = _sz
+        L.attn_causal_gqa_varlen_fwd.argtypes = [_vp] * 6 + [_i] * 6 + [_st] * 4 + [_i, _i, _i, _f, _vp]
         L.attn_status_string.argtypes = [_i]
         L.attn_status_string.restype = ctypes.c_char_p
         L.attn_device_status.argtypes = [_vp]
@@ -123,7 +148,10 @@ def lib() -> ctypes.CDLL:
                      "attn_decode_gqa_ring", "attn_causal_gqa_window_fwd",
                      "attn_decode_gqa_paged", "attn_kv_append_paged", "attn_kv_pages_reserve",
                      "attn_kv_pages_free", "attn_kv_pages_fork", "attn_kv_pages_compact",
-                     "attn_kv_pages_copy"):
+                     "attn_kv_pages_copy", "attn_rope_frequencies", "attn_rope_fwd",
+                     "attn_kv_append_paged_rope", "attn_kv_append_paged_q4",
+                     "attn_kv_gather_paged_q4", "attn_kv_pages_copy_q4",
+                     "attn_decode_gqa_paged_q4", "attn_causal_gqa_varlen_fwd"):
             getattr(L, name).restype = _i
         _lib = L
     return _lib
@@ -438,6 +466,104 @@ def kv_pages_copy(k_pages, v_pages, copy_src, copy_dst, count=None):
     layer of [layers,P,Hkv,S,D] (views with D contiguous); pairs of -1, and
     pairs from count[0] on, are skipped."""
     (_native_mod or _native()).kv_pages_copy(k_pages, v_pages, copy_src, copy_dst, count)
+
+
+SCALINGS = {None: 0, "linear": 1, "ntk": 2, "by_parts": 3}
+
+
+def rope_frequencies(rotary_dim, theta=10000.0, scaling=None, factor=1.0, original_len=0, alpha=1.0,
+                     beta=32.0, device=None):
+    """The angles per position of rotary_dim / 2 channel pairs, as the int64 table
+    (64-bit fractions of a turn) that rope_fwd and the appends take; made once.
+
+    theta_i = theta^(-2i / rotary_dim), for contexts ``factor`` times as long:
+    scaling None; "linear": theta_i / factor; "ntk": a larger theta; "by_parts":
+    pairs that turn less than ``alpha`` times within ``original_len`` positions
+    are divided by factor, those that turn more than ``beta`` times are kept, a
+    linear mixture between (the customary mscale is then 0.1 ln(factor) + 1)."""
+    if scaling not in SCALINGS:
+        raise ValueError(f"scaling must be one of {list(SCALINGS)}")
+    rotary_dim = int(rotary_dim)
+    if rotary_dim < 16 or rotary_dim > 128:
+        raise ValueError("rotary_dim must be a multiple of 16 up to 128")
+    t = torch.empty(rotary_dim // 2, dtype=torch.int64)
+    _check(lib().attn_rope_frequencies(t.data_ptr(), rotary_dim, float(theta), SCALINGS[scaling], float(factor),
+                                       float(original_len), float(alpha), float(beta)),
+           "attn_rope_frequencies")
+    return t.to(torch.device("cuda", torch.cuda.current_device()) if device is None else device)
+
+
+def rope_fwd(x, freq, positions, interleaved=False, inverse=False, mscale=1.0, o=None):
+    """Rotary positions of rows x [N,H,D] (packed tokens) or [B,H,N,D] (strided
+    views, D contiguous); positions int32 [N], or [B,N] beside a 4-D x.  The first
+    2 len(freq) channels turn in pairs (i, i + len(freq)), or (2i, 2i + 1) if
+    ``interleaved``, and are multiplied by mscale; the others are copied.
+    ``inverse``: the transposed rotation, which is the gradient with respect to
+    x.  o defaults to a new contiguous tensor and may be x."""
+    return (_native_mod or _native()).rope_fwd(x, freq, positions, interleaved, inverse, mscale, o)
+
+
+def causal_gqa_varlen_fwd(q, k, v, cu_q, cu_k=None, window=0, sinks=0, o=None, scale=None):
+    """Causal GQA over packed sequences: q [Nq,Hq,D], k/v [Nkv,Hkv,D] (strided
+    views, D contiguous), starts cu_q / cu_k int32 [B+1] (cu_k defaults to cu_q).
+    A sequence's queries are the last of its positions; window and sinks as in
+    causal_gqa_window_fwd.  Rows of o outside every sequence are left as they
+    were.  o defaults to a new contiguous tensor."""
+    return (_native_mod or _native()).causal_gqa_varlen_fwd(q, k, v, cu_q, cu_k, window, sinks, o, scale)
+
+
+def kv_append_paged_rope(k_pages, v_pages, k_new, v_new, page_table, seq_len, freq, cu_new=None, q=None,
+                         q_out=None, interleaved=False, mscale=1.0, advance=True):
+    """Rotate the keys of packed new tokens k_new/v_new [N,Hkv,D] (strided views)
+    for their positions and write them behind seq_len[b] in the sequences' pages:
+    sequence b brings rows [cu_new[b], cu_new[b+1]), or row b alone if cu_new is
+    None.  q [N,Hq,D] is rotated for the same positions; returns it (in q_out,
+    which may be q; default a new contiguous tensor), or None without q.  With
+    advance, seq_len[b] grows on the device."""
+    return (_native_mod or _native()).kv_append_paged_rope(k_pages, v_pages, k_new, v_new, page_table, seq_len,
+                                                           freq, cu_new, q, q_out, interleaved, mscale, advance)
+
+
+def kv_q4_row_bytes(D) -> int:
+    """Bytes of one token and KV head in a cache held in 4 bits: D + D / 8."""
+    return int(lib().attn_kv_q4_row_bytes(D))
+
+
+def kv_append_paged_q4(kv_pages, k_new, v_new, page_table, seq_len, freq=None, cu_new=None, q=None, q_out=None,
+                       interleaved=False, mscale=1.0, advance=True):
+    """kv_append_paged_rope into pages held in 4 bits, kv_pages uint8
+    [P,Hkv,S,D + D/8] (the rows of a (page, head) contiguous): groups of 32
+    channels share a scale of k_new's dtype.  freq None: nothing is rotated."""
+    return (_native_mod or _native()).kv_append_paged_q4(kv_pages, k_new, v_new, page_table, seq_len, freq, cu_new,
+                                                         q, q_out, interleaved, mscale, advance)
+
+
+def kv_gather_paged_q4(kv_pages, page_table, cu_len, k, v, start=None):
+    """Read rows of a 4-bit cache into k/v [N,Hkv,D] (strided views): rows
+    [cu_len[b], cu_len[b+1]) receive positions start[b], start[b] + 1, ... of
+    sequence b (start None: from 0).  Returns (k, v)."""
+    return (_native_mod or _native()).kv_gather_paged_q4(kv_pages, page_table, cu_len, k, v, start)
+
+
+def kv_pages_copy_q4(kv_pages, copy_src, copy_dst, count=None):
+    """kv_pages_copy for pages held in 4 bits, [P,Hkv,S,R] or [layers,P,Hkv,S,R]."""
+    (_native_mod or _native()).kv_pages_copy_q4(kv_pages, copy_src, copy_dst, count)
+
+
+def decode_paged_q4_workspace_bytes(B, Hq, Hkv, D) -> int:
+    return int(lib().attn_decode_gqa_paged_q4_workspace_bytes(B, Hq, Hkv, D))
+
+
+def decode_gqa_paged_q4(q, kv_pages, page_table, seq_len, o=None, scale=None, window=0, sinks=0,
+                        workspace=None):
+    """GQA decode over a paged cache held in 4 bits: q [B,Hq,D] of the dtype the
+    cache was written with, the other arguments as in decode_gqa_paged.
+
+    ``workspace`` (uint8, decode_paged_q4_workspace_bytes(...) bytes) must be
+    zero-filled before its first use; calls leave it reusable, for any sizes it
+    is large enough for.  If omitted a zeroed one is allocated for this call."""
+    return (_native_mod or _native()).decode_gqa_paged_q4(q, kv_pages, page_table, seq_len, o, scale, window,
+                                                          sinks, workspace)
 
 
 def na3d_fwd(q, k, v, grid, kernel, o=None, scale=None):

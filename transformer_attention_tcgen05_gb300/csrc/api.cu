@@ -585,6 +585,311 @@ attn_status_t attn_kv_append_paged(void *k_pages, void *v_pages, const void *k_n
     return kv_append_paged(c, dtype, a);
 }
 
+// ---------------------------------------------- rotary positions, 4-bit pages
+
+static bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+attn_status_t attn_rope_frequencies(uint64_t *freq, int rotary_dim, double theta, attn_rope_scaling_t scaling,
+                                    double factor, double original_len, double alpha, double beta) {
+    if (!freq || rotary_dim < 16 || rotary_dim % 16 != 0 || rotary_dim > 128) return ATTN_ERR_INVALID_ARG;
+    if (!(theta > 0) || !isfinite(theta) || !(factor > 0) || !isfinite(factor)) return ATTN_ERR_INVALID_ARG;
+    if (scaling != ATTN_ROPE_UNSCALED && scaling != ATTN_ROPE_LINEAR && scaling != ATTN_ROPE_NTK &&
+        scaling != ATTN_ROPE_BY_PARTS)
+        return ATTN_ERR_INVALID_ARG;
+    if (scaling == ATTN_ROPE_BY_PARTS &&
+        (!(original_len > 0) || !isfinite(original_len) || !isfinite(alpha) || !isfinite(beta) || !(beta > alpha)))
+        return ATTN_ERR_INVALID_ARG;
+    return rope_frequencies(freq, rotary_dim, theta, scaling, factor, original_len, alpha, beta);
+}
+
+static bool check_rotary(const uint64_t *freq, int rot, int D, float mscale) {
+    return freq && aligned8(freq) && rot >= 16 && rot % 16 == 0 && rot <= D && isfinite(mscale);
+}
+
+attn_status_t attn_rope_fwd(const void *x, void *y, const uint64_t *freq, const int32_t *positions,
+                            int64_t pos_stride, int B, int H, int N, int D, int rotary_dim, int interleaved,
+                            int inverse, float mscale, const int64_t x_strides[3], const int64_t y_strides[3],
+                            attn_dtype_t dtype, void *stream) {
+    if (!x || !y || !positions || !aligned16(x) || !aligned16(y) || !aligned4(positions))
+        return ATTN_ERR_INVALID_ARG;
+    if (B < 1 || H < 1 || N < 1 || !valid_d(D) || !valid_dtype(dtype) || !check_rotary(freq, rotary_dim, D, mscale))
+        return ATTN_ERR_INVALID_ARG;
+    if (B > 1 && (pos_stride < 0 || (pos_stride > 0 && pos_stride < N) || pos_stride > (1ll << 40)))
+        return ATTN_ERR_INVALID_ARG;
+    if ((const void *)positions == y || (const void *)freq == y) return ATTN_ERR_INVALID_ARG;
+    const long long ext[3] = {B, H, N};
+    long long sx[3], sy[3];
+    if (!row_strides(x_strides, ext, 3, D, dtype, false, sx) || !row_strides(y_strides, ext, 3, D, dtype, true, sy))
+        return ATTN_ERR_INVALID_ARG;
+    // in place every row is rotated where it lies
+    if (x == y && (sx[0] != sy[0] || sx[1] != sy[1] || sx[2] != sy[2])) return ATTN_ERR_INVALID_ARG;
+    Ctx c;
+    const attn_status_t st = get_ctx(stream, &c);
+    if (st != ATTN_OK) return st;
+    return rope_rows(c, dtype, x, y, positions, B > 1 ? pos_stride : 0, B, H, N, D,
+                     TensorStrides{sx[0], sx[1], sx[2]}, TensorStrides{sy[0], sy[1], sy[2]},
+                     RotaryArgs{freq, rotary_dim, interleaved != 0, inverse != 0, mscale});
+}
+
+// What the appends of packed rows share; a.k and a.v are checked by the caller.
+static attn_status_t check_rows_append(RowsAppend &a, const uint64_t *freq, int rotary_dim, int interleaved,
+                                       float mscale, int64_t table_stride, const int64_t *kn_strides,
+                                       const int64_t *vn_strides, const int64_t *q_strides,
+                                       const int64_t *qo_strides, attn_dtype_t dtype) {
+    if (!a.kn || !a.vn || !a.seq_len || !aligned16(a.kn) || !aligned16(a.vn) || !aligned4(a.seq_len) ||
+        !aligned4(a.cu))
+        return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_pool(a.table, a.B, a.P, a.S, a.max_pages, table_stride);
+    if (st != ATTN_OK) return st;
+    if (a.N < 1 || a.Hkv < 1 || (!a.cu && a.N != a.B) || a.cu == a.seq_len) return ATTN_ERR_INVALID_ARG;
+    if (a.kn == a.k || a.vn == a.k || a.kn == a.v || a.vn == a.v) return ATTN_ERR_INVALID_ARG;
+    if (a.Hkv > 65535 || a.N > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+    const long long ne[2] = {a.N, a.Hkv};
+    if (!row_strides(kn_strides, ne, 2, a.D, dtype, false, a.kn_st) ||
+        !row_strides(vn_strides, ne, 2, a.D, dtype, false, a.vn_st))
+        return ATTN_ERR_INVALID_ARG;
+    if (a.q) {
+        if (!a.qo || !aligned16(a.q) || !aligned16(a.qo) || a.Hq < 1) return ATTN_ERR_INVALID_ARG;
+        if (a.qo == a.kn || a.qo == a.vn || a.qo == a.k || a.qo == a.v || a.q == a.k || a.q == a.v)
+            return ATTN_ERR_INVALID_ARG;
+        if (a.Hq > 65535) return ATTN_ERR_UNSUPPORTED;
+        const long long qe[2] = {a.N, a.Hq};
+        if (!row_strides(q_strides, qe, 2, a.D, dtype, false, a.q_st) ||
+            !row_strides(qo_strides, qe, 2, a.D, dtype, true, a.qo_st))
+            return ATTN_ERR_INVALID_ARG;
+        if (a.q == a.qo && (a.q_st[0] != a.qo_st[0] || a.q_st[1] != a.qo_st[1])) return ATTN_ERR_INVALID_ARG;
+    }
+    a.table_stride = a.B > 1 ? table_stride : a.max_pages;
+    a.rot = RotaryArgs{freq, rotary_dim, interleaved != 0, 0, mscale};
+    return ATTN_OK;
+}
+
+attn_status_t attn_kv_append_paged_rope(
+    void *k_pages, void *v_pages, const void *k_new, const void *v_new, const void *q, void *q_out,
+    const int32_t *page_table, int32_t *seq_len, const int32_t *cu_new, const uint64_t *freq, int B, int N, int Hq,
+    int Hkv, int D, int rotary_dim, int interleaved, float mscale, int num_pages, int page_size, int max_pages,
+    int64_t table_stride, const int64_t k_strides[3], const int64_t v_strides[3], const int64_t kn_strides[2],
+    const int64_t vn_strides[2], const int64_t q_strides[2], const int64_t qo_strides[2], attn_dtype_t dtype,
+    int advance, void *stream) {
+    if (!k_pages || !v_pages || !aligned16(k_pages) || !aligned16(v_pages) || k_pages == v_pages || !valid_d(D) ||
+        !valid_dtype(dtype) || !check_rotary(freq, rotary_dim, D, mscale))
+        return ATTN_ERR_INVALID_ARG;
+    RowsAppend a{};
+    a.k = k_pages; a.v = v_pages; a.kn = k_new; a.vn = v_new; a.q = q; a.qo = q_out;
+    a.table = page_table; a.seq_len = seq_len; a.cu = cu_new;
+    a.B = B; a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.D = D;
+    a.P = num_pages; a.S = page_size; a.max_pages = max_pages;
+    a.advance = advance != 0;
+    attn_status_t st = check_rows_append(a, freq, rotary_dim, interleaved, mscale, table_stride, kn_strides,
+                                         vn_strides, q_strides, qo_strides, dtype);
+    if (st != ATTN_OK) return st;
+    const long long pe[3] = {num_pages, Hkv, page_size};
+    if (!row_strides(k_strides, pe, 3, D, dtype, true, a.k_st) || !row_strides(v_strides, pe, 3, D, dtype, true, a.v_st))
+        return ATTN_ERR_INVALID_ARG;
+    Ctx c;
+    st = get_ctx(stream, &c);
+    if (st != ATTN_OK) return st;
+    return append_rows(c, dtype, a);
+}
+
+size_t attn_kv_q4_row_bytes(int D) { return D == 64 || D == 128 ? size_t(D + D / 8) : 0; }
+
+// The byte strides of n outer axes (extents ext) over blocks of `block` bytes:
+// in (null: contiguous) -> out.  The blocks must be disjoint where they are written.
+static bool block_strides(const int64_t *in, const long long *ext, int n, long long block, bool disjoint,
+                          long long *out) {
+    long long dense = block;
+    for (int a = n - 1; a >= 0; --a) {
+        out[a] = in ? (long long)in[a] : dense;
+        if (ext[a] == 1) out[a] = block;
+        if (out[a] < 16 || out[a] % 16 != 0 || out[a] >= (1ll << 40)) return false;
+        if (dense < (1ll << 40)) dense *= ext[a];
+    }
+    if (!disjoint) return true;
+    long long span = block;
+    bool used[3] = {false, false, false};
+    for (int step = 0; step < n; ++step) {
+        int best = -1;
+        for (int a = 0; a < n; ++a)
+            if (!used[a] && ext[a] > 1 && (best < 0 || out[a] < out[best])) best = a;
+        if (best < 0) break;
+        if (out[best] < span || out[best] > (1ll << 62) / ext[best]) return false;
+        span = out[best] * ext[best];
+        used[best] = true;
+    }
+    return true;
+}
+
+static bool valid_q4(int D, attn_dtype_t dtype) { return half_dtype(dtype) && D != 32; }
+
+attn_status_t attn_kv_append_paged_q4(
+    void *kv_pages, const void *k_new, const void *v_new, const void *q, void *q_out, const int32_t *page_table,
+    int32_t *seq_len, const int32_t *cu_new, const uint64_t *freq, int B, int N, int Hq, int Hkv, int D,
+    int rotary_dim, int interleaved, float mscale, int num_pages, int page_size, int max_pages,
+    int64_t table_stride, const int64_t pages_strides[2], const int64_t kn_strides[2], const int64_t vn_strides[2],
+    const int64_t q_strides[2], const int64_t qo_strides[2], attn_dtype_t dtype, int advance, void *stream) {
+    if (!kv_pages || !aligned16(kv_pages) || !valid_d(D) || !valid_dtype(dtype)) return ATTN_ERR_INVALID_ARG;
+    if (freq ? !check_rotary(freq, rotary_dim, D, mscale) : rotary_dim != 0) return ATTN_ERR_INVALID_ARG;
+    if (!valid_q4(D, dtype)) return ATTN_ERR_UNSUPPORTED;
+    RowsAppend a{};
+    a.k = kv_pages; a.kn = k_new; a.vn = v_new; a.q = q; a.qo = q_out;
+    a.table = page_table; a.seq_len = seq_len; a.cu = cu_new;
+    a.B = B; a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.D = D;
+    a.P = num_pages; a.S = page_size; a.max_pages = max_pages;
+    a.advance = advance != 0;
+    a.q4 = true;
+    attn_status_t st = check_rows_append(a, freq, rotary_dim, interleaved, mscale, table_stride, kn_strides,
+                                         vn_strides, q_strides, qo_strides, dtype);
+    if (st != ATTN_OK) return st;
+    const long long pe[2] = {num_pages, Hkv};
+    const long long row = (long long)attn_kv_q4_row_bytes(D);
+    if (!block_strides(pages_strides, pe, 2, page_size * row, true, a.k_st)) return ATTN_ERR_INVALID_ARG;
+    a.k_st[2] = row;
+    Ctx c;
+    st = get_ctx(stream, &c);
+    if (st != ATTN_OK) return st;
+    return append_rows(c, dtype, a);
+}
+
+attn_status_t attn_kv_gather_paged_q4(const void *kv_pages, const int32_t *page_table, const int32_t *start,
+                                      const int32_t *cu_len, void *k, void *v, int B, int N, int Hkv, int D,
+                                      int num_pages, int page_size, int max_pages, int64_t table_stride,
+                                      const int64_t pages_strides[2], const int64_t k_strides[2],
+                                      const int64_t v_strides[2], attn_dtype_t dtype, void *stream) {
+    if (!kv_pages || !cu_len || !k || !v || !aligned16(kv_pages) || !aligned16(k) || !aligned16(v) ||
+        !aligned4(start) || !aligned4(cu_len))
+        return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_pool(page_table, B, num_pages, page_size, max_pages, table_stride);
+    if (st != ATTN_OK) return st;
+    if (N < 1 || Hkv < 1 || !valid_d(D) || !valid_dtype(dtype)) return ATTN_ERR_INVALID_ARG;
+    if (k == v || k == kv_pages || v == kv_pages) return ATTN_ERR_INVALID_ARG;
+    if (!valid_q4(D, dtype) || Hkv > 65535 || N > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+    RowsGather a{};
+    const long long pe[2] = {num_pages, Hkv}, ne[2] = {N, Hkv};
+    if (!block_strides(pages_strides, pe, 2, page_size * (long long)attn_kv_q4_row_bytes(D), false, a.p_st) ||
+        !row_strides(k_strides, ne, 2, D, dtype, true, a.k_st) || !row_strides(v_strides, ne, 2, D, dtype, true, a.v_st))
+        return ATTN_ERR_INVALID_ARG;
+    Ctx c;
+    st = get_ctx(stream, &c);
+    if (st != ATTN_OK) return st;
+    a.pages = kv_pages; a.table = page_table; a.start = start; a.cu = cu_len;
+    a.k = k; a.v = v;
+    a.B = B; a.N = N; a.Hkv = Hkv; a.D = D;
+    a.P = num_pages; a.S = page_size; a.max_pages = max_pages;
+    a.table_stride = B > 1 ? table_stride : max_pages;
+    return gather_rows(c, dtype, a);
+}
+
+attn_status_t attn_kv_pages_copy_q4(void *kv_pages, const int32_t *copy_src, const int32_t *copy_dst, int n,
+                                    const int32_t *count, int layers, int num_pages, int Hkv, int page_size, int D,
+                                    const int64_t strides[3], void *stream) {
+    if (!kv_pages || !copy_src || !copy_dst || !aligned16(kv_pages) || !aligned4(copy_src) || !aligned4(copy_dst) ||
+        !aligned4(count))
+        return ATTN_ERR_INVALID_ARG;
+    if (n < 1 || layers < 1 || num_pages < 1 || Hkv < 1 || page_size < 1 || page_size % 8 != 0 || !valid_d(D))
+        return ATTN_ERR_INVALID_ARG;
+    if (D == 32) return ATTN_ERR_UNSUPPORTED;
+    // a page's bytes and the pieces of one pair are 32-bit
+    if ((long long)Hkv * page_size * D >= (1ll << 30) || layers > 65535 ||
+        (long long)Hkv * page_size * layers >= (1ll << 30))
+        return ATTN_ERR_UNSUPPORTED;
+    PagesCopyQ4 a{};
+    const long long pe[3] = {layers, num_pages, Hkv};
+    a.block = page_size * (long long)attn_kv_q4_row_bytes(D);
+    if (!block_strides(strides, pe, 3, a.block, true, a.st)) return ATTN_ERR_INVALID_ARG;
+    Ctx c;
+    const attn_status_t st = get_ctx(stream, &c);
+    if (st != ATTN_OK) return st;
+    a.pages = kv_pages; a.src = copy_src; a.dst = copy_dst; a.count = count;
+    a.n = n; a.layers = layers; a.Hkv = Hkv; a.P = num_pages;
+    return kv_pages_copy_q4(c, a);
+}
+
+size_t attn_decode_gqa_paged_q4_workspace_bytes(int B, int Hq, int Hkv, int D) {
+    if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > 16 || (D != 64 && D != 128)) return 0;
+    return decode_paged_q4_workspace_bytes(B, Hkv);
+}
+
+attn_status_t attn_decode_gqa_paged_q4(const void *q, const void *kv_pages, const int32_t *page_table,
+                                       const int32_t *seq_len, void *o, int B, int Hq, int Hkv, int D,
+                                       int num_pages, int page_size, int max_pages, int64_t table_stride,
+                                       const int64_t q_strides[2], const int64_t pages_strides[2],
+                                       const int64_t o_strides[2], int window, int sinks, attn_dtype_t dtype,
+                                       float scale, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!q || !kv_pages || !seq_len || !o || !workspace) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(kv_pages) || !aligned16(o) || !aligned4(seq_len) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_pool(page_table, B, num_pages, page_size, max_pages, table_stride);
+    if (st != ATTN_OK) return st;
+    if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !valid_d(D) || !valid_dtype(dtype) || sinks < 0)
+        return ATTN_ERR_INVALID_ARG;
+    if (!valid_q4(D, dtype) || Hq / Hkv > 16 || Hkv > 65535 ||
+        double(B) * Hkv * (double(max_pages) * page_size + 32.0) >= 68719476736.0)
+        return ATTN_ERR_UNSUPPORTED;
+    if (o == q || o == kv_pages) return ATTN_ERR_INVALID_ARG;
+    PagedDecodeQ4 a{};
+    const long long qe[2] = {B, Hq}, pe[2] = {num_pages, Hkv};
+    if (!row_strides(q_strides, qe, 2, D, dtype, false, a.q_st) ||
+        !row_strides(o_strides, qe, 2, D, dtype, true, a.o_st) ||
+        !block_strides(pages_strides, pe, 2, page_size * (long long)attn_kv_q4_row_bytes(D), false, a.p_st))
+        return ATTN_ERR_INVALID_ARG;
+    if (workspace_bytes < decode_paged_q4_workspace_bytes(B, Hkv)) return ATTN_ERR_RESOURCE;
+    Ctx c;
+    st = get_ctx(stream, &c);
+    if (st != ATTN_OK) return st;
+    a.q = q; a.pages = kv_pages; a.o = o;
+    a.table = page_table; a.seq_len = seq_len;
+    a.B = B; a.G = Hq / Hkv; a.Hkv = Hkv; a.D = D;
+    a.P = num_pages; a.S = page_size; a.max_pages = max_pages;
+    a.table_stride = B > 1 ? table_stride : max_pages;
+    a.window = window; a.sinks = sinks;
+    a.scale = resolve_scale(scale, D);
+    a.ws = workspace;
+    return decode_paged_q4(c, dtype, a);
+}
+
+// ------------------------------------------------ packed causal attention
+
+attn_status_t attn_causal_gqa_varlen_fwd(const void *q, const void *k, const void *v, void *o, const int32_t *cu_q,
+                                         const int32_t *cu_k, int B, int Nq, int Nkv, int Hq, int Hkv, int D,
+                                         const int64_t q_strides[2], const int64_t k_strides[2],
+                                         const int64_t v_strides[2], const int64_t o_strides[2], int window,
+                                         int sinks, attn_dtype_t dtype, float scale, void *stream) {
+    if (!q || !k || !v || !o || !cu_q || !cu_k || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) ||
+        !aligned4(cu_q) || !aligned4(cu_k))
+        return ATTN_ERR_INVALID_ARG;
+    if (B < 1 || Nq < 1 || Nkv < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !valid_d(D) || !valid_dtype(dtype) ||
+        sinks < 0)
+        return ATTN_ERR_INVALID_ARG;
+    if (B > 65535 || Hq > 65535 || Nq > (1 << 30) || Nkv > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+    if (o == q || o == k || o == v) return ATTN_ERR_INVALID_ARG;
+    VarlenArgs a{};
+    const int64_t *const in[4] = {q_strides, k_strides, v_strides, o_strides};
+    for (int i = 0; i < 4; ++i) {
+        const bool qo = i == 0 || i == 3;
+        const long long ext[2] = {qo ? Nq : Nkv, qo ? Hq : Hkv};
+        long long st[2];
+        if (!row_strides(in[i], ext, 2, D, dtype, i == 3, st)) return ATTN_ERR_INVALID_ARG;
+        a.st[i] = TensorStrides{D, st[1], st[0]};
+    }
+    Ctx c;
+    attn_status_t status = get_ctx(stream, &c);
+    if (status != ATTN_OK) return status;
+    a.q = q; a.k = k; a.v = v; a.o = o;
+    a.cu_q = cu_q; a.cu_k = cu_k;
+    a.B = B; a.Nq = Nq; a.Nkv = Nkv; a.Hq = Hq; a.Hkv = Hkv; a.D = D;
+    // no window: wider than the sequences and a block of rows behind them
+    a.window = window > 0 && window < Nkv ? window : Nkv + 256;
+    a.sinks = sinks < Nkv ? sinks : Nkv;
+    a.scale = resolve_scale(scale, D);
+    if (half_dtype(dtype) && D != 32) {
+        status = tc_causal_varlen(c, dtype, a);
+        if (status != ATTN_ERR_UNSUPPORTED) return status;
+    }
+    return simt_causal_varlen(c, dtype, a);
+}
+
 size_t attn_kv_pages_workspace_bytes(int num_pages) {
     return num_pages < 1 ? 0 : kv_pages_workspace_bytes(num_pages);
 }

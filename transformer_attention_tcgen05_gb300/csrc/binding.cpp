@@ -253,6 +253,239 @@ PyObject *kv_append_paged(PyObject *const *a) {
                 "attn_kv_append_paged");
 }
 
+// A table of rope_frequencies (None: no rotation).
+struct Rotary {
+    const uint64_t *freq = nullptr;
+    int dim = 0;
+    Rotary(Call &c, PyObject *o) {
+        if (o == Py_None) return;
+        const at::Tensor &t = c.take(o, "freq");
+        if (t.scalar_type() != at::kLong || t.dim() != 1 || !t.is_contiguous())
+            value_error("freq must be a contiguous int64 tensor [rotary_dim / 2] (rope_frequencies)");
+        freq = static_cast<const uint64_t *>(t.data_ptr());
+        dim = to_int(2 * t.size(0));
+    }
+};
+
+int truth(PyObject *o) {
+    const int x = PyObject_IsTrue(o);
+    if (x < 0) throw PyFail();
+    return x;
+}
+
+// x, freq, positions, interleaved, inverse, mscale, o
+PyObject *rope_fwd(PyObject *const *a) {
+    Call c;
+    const at::Tensor &x = c.take(a[0], "x");
+    const Rotary rot(c, a[1]);
+    const at::Tensor &pos = c.take(a[2], "positions");
+    if (x.dim() != 3 && x.dim() != 4) value_error("x must be [N, H, D] or [B, H, N, D]");
+    const bool packed = x.dim() == 3;
+    const int64_t B = packed ? 1 : x.size(0), H = x.size(1), N = packed ? x.size(0) : x.size(2);
+    const bool rows = !packed && pos.dim() == 2;
+    if (pos.scalar_type() != at::kInt || (rows ? pos.size(0) != B || pos.size(1) != N : pos.dim() != 1 || pos.size(0) != N) ||
+        (N > 1 && pos.stride(pos.dim() - 1) != 1))
+        value_error("positions must be int32 [N] (or [B, N] beside a 4-D x), rows contiguous");
+    const at::Tensor o = output(c, a[6], x);
+    const Outer sx(x), so(o);
+    // (batch, head, token) of packed rows
+    const int64_t D = x.size(x.dim() - 1);
+    const int64_t px[3] = {D, x.stride(1), x.stride(0)}, po[3] = {D, o.stride(1), o.stride(0)};
+    const float mscale = float(PyFloat_AsDouble(a[5]));
+    if (PyErr_Occurred()) throw PyFail();
+    done(attn_rope_fwd(x.data_ptr(), o.data_ptr(), rot.freq, static_cast<const int32_t *>(pos.data_ptr()),
+                       rows ? (B > 1 ? pos.stride(0) : 0) : 0, to_int(B), to_int(H), to_int(N), to_int(D), rot.dim,
+                       truth(a[3]), truth(a[4]), mscale, packed ? px : sx.p, packed ? po : so.p, dtype_of(x),
+                       c.stream()),
+         "attn_rope_fwd");
+    return returned(a[6], o);
+}
+
+// New tokens' rows as the two appends of packed rows take them.
+struct NewRows {
+    const at::Tensor &kn, &vn;
+    at::Tensor q, qo;
+    const int32_t *cu;
+    int64_t N, Hkv, D;
+    Outer skn, svn;
+    NewRows(Call &c, PyObject *k, PyObject *v, PyObject *q_, PyObject *qo_, PyObject *cu_, int B)
+        : kn(c.take(k, "k_new")), vn(c.take(v, "v_new")), skn(kn), svn(vn) {
+        if (kn.dim() != 3 || vn.sizes() != kn.sizes() || vn.scalar_type() != kn.scalar_type())
+            value_error("k_new and v_new must be [N, Hkv, D] of one dtype");
+        N = kn.size(0);
+        Hkv = kn.size(1);
+        D = kn.size(2);
+        cu = cu_ == Py_None ? nullptr : c.ints(cu_, "cu_new", int64_t(B) + 1);
+        if (!cu && N != B) value_error("without cu_new there is one new token per sequence");
+        if (q_ != Py_None) {
+            q = c.take(q_, "q");
+            if (q.dim() != 3 || q.size(0) != N || q.size(2) != D || q.scalar_type() != kn.scalar_type())
+                value_error("q must be [N, Hq, D] of k_new's dtype");
+            if (qo_ == Py_None) {
+                qo = at::empty(q.sizes(), q.options());
+            } else {
+                qo = c.take(qo_, "q_out");
+                if (qo.sizes() != q.sizes() || qo.scalar_type() != q.scalar_type())
+                    value_error("q_out must have q's shape and dtype");
+            }
+        } else if (qo_ != Py_None) {
+            value_error("q_out without q");
+        }
+    }
+    const void *q_ptr() const { return q.defined() ? q.data_ptr() : nullptr; }
+    void *qo_ptr() const { return qo.defined() ? qo.data_ptr() : nullptr; }
+    int Hq() const { return q.defined() ? to_int(q.size(1)) : 0; }
+    PyObject *result(PyObject *qo_) const {
+        if (!qo.defined()) Py_RETURN_NONE;
+        return returned(qo_, qo);
+    }
+};
+
+// k_pages, v_pages, k_new, v_new, page_table, seq_len, freq, cu_new, q, q_out, interleaved, mscale, advance
+PyObject *kv_append_paged_rope(PyObject *const *a) {
+    Call c;
+    const at::Tensor &k = c.take(a[0], "k_pages"), &v = c.take(a[1], "v_pages");
+    const Table t(c, a[4]);
+    const NewRows n(c, a[2], a[3], a[8], a[9], a[7], t.B);
+    if (k.dim() != 4 || v.sizes() != k.sizes() || n.Hkv != k.size(1) || n.D != k.size(3) ||
+        v.scalar_type() != k.scalar_type() || n.kn.scalar_type() != k.scalar_type())
+        value_error("pages [P,Hkv,S,D] and new rows [N,Hkv,D] of one dtype required");
+    int32_t *sl = c.ints(a[5], "seq_len", t.B);
+    const Rotary rot(c, a[6]);
+    const Outer sk(k), sv(v), sq(n.q.defined() ? n.q : n.kn), sqo(n.qo.defined() ? n.qo : n.kn);
+    const double mscale = PyFloat_AsDouble(a[11]);
+    if (PyErr_Occurred()) throw PyFail();
+    done(attn_kv_append_paged_rope(k.data_ptr(), v.data_ptr(), n.kn.data_ptr(), n.vn.data_ptr(), n.q_ptr(),
+                                   n.qo_ptr(), t.p, sl, n.cu, rot.freq, t.B, to_int(n.N), n.Hq(), to_int(n.Hkv),
+                                   to_int(n.D), rot.dim, truth(a[10]), float(mscale), to_int(k.size(0)),
+                                   to_int(k.size(2)), t.M, t.stride, sk.p, sv.p, n.skn.p, n.svn.p, sq.p, sqo.p,
+                                   dtype_of(k), truth(a[12]), c.stream()),
+         "attn_kv_append_paged_rope");
+    return n.result(a[9]);
+}
+
+// A cache held in 4 bits: uint8 [(layers,) P, Hkv, S, D + D / 8], the rows of a
+// (page, head) contiguous.
+struct PagesQ4 {
+    const at::Tensor &t;
+    int P, Hkv, S, D, layers = 1;
+    int64_t st[3];                                     // of all axes but the last two
+    const int64_t *p = nullptr;
+    PagesQ4(Call &c, PyObject *o, bool with_layers = false) : t(c.take(o, "kv_pages")) {
+        const int64_t n = t.dim();
+        if (t.scalar_type() != at::kByte || (n != 4 && !(with_layers && n == 5)))
+            value_error("kv_pages must be uint8 [P, Hkv, S, D + D / 8]");
+        const int64_t row = t.size(n - 1);
+        D = row == 72 ? 64 : row == 144 ? 128 : 0;
+        if (D == 0) value_error("a row of kv_pages has D + D / 8 bytes, D 64 or 128");
+        P = to_int(t.size(n - 4));
+        Hkv = to_int(t.size(n - 3));
+        S = to_int(t.size(n - 2));
+        if (n == 5) layers = to_int(t.size(0));
+        if (t.is_contiguous()) return;
+        if (t.stride(n - 1) != 1 || (S > 1 && t.stride(n - 2) != row))
+            value_error("the rows of a (page, head) of kv_pages must be contiguous");
+        for (int i = 0; i < n - 2; ++i) st[i + (with_layers && n == 4)] = t.stride(i);
+        if (with_layers && n == 4) st[0] = 16;         // one layer: not stepped along
+        p = st;
+    }
+};
+
+// kv_pages, k_new, v_new, page_table, seq_len, freq, cu_new, q, q_out, interleaved, mscale, advance
+PyObject *kv_append_paged_q4(PyObject *const *a) {
+    Call c;
+    const PagesQ4 pg(c, a[0]);
+    const Table t(c, a[3]);
+    const NewRows n(c, a[1], a[2], a[7], a[8], a[6], t.B);
+    if (n.Hkv != pg.Hkv || n.D != pg.D) value_error("new rows [N,Hkv,D] must have the pages' heads and channels");
+    int32_t *sl = c.ints(a[4], "seq_len", t.B);
+    const Rotary rot(c, a[5]);
+    const Outer sq(n.q.defined() ? n.q : n.kn), sqo(n.qo.defined() ? n.qo : n.kn);
+    const double mscale = PyFloat_AsDouble(a[10]);
+    if (PyErr_Occurred()) throw PyFail();
+    done(attn_kv_append_paged_q4(pg.t.data_ptr(), n.kn.data_ptr(), n.vn.data_ptr(), n.q_ptr(), n.qo_ptr(), t.p, sl,
+                                 n.cu, rot.freq, t.B, to_int(n.N), n.Hq(), pg.Hkv, pg.D, rot.dim, truth(a[9]),
+                                 float(mscale), pg.P, pg.S, t.M, t.stride, pg.p, n.skn.p, n.svn.p, sq.p, sqo.p,
+                                 dtype_of(n.kn), truth(a[11]), c.stream()),
+         "attn_kv_append_paged_q4");
+    return n.result(a[8]);
+}
+
+// kv_pages, page_table, cu_len, k, v, start
+PyObject *kv_gather_paged_q4(PyObject *const *a) {
+    Call c;
+    const PagesQ4 pg(c, a[0]);
+    const Table t(c, a[1]);
+    const int32_t *cu = c.ints(a[2], "cu_len", int64_t(t.B) + 1);
+    const at::Tensor &k = c.take(a[3], "k"), &v = c.take(a[4], "v");
+    const int32_t *start = a[5] == Py_None ? nullptr : c.ints(a[5], "start", t.B);
+    if (k.dim() != 3 || v.sizes() != k.sizes() || v.scalar_type() != k.scalar_type() || k.size(1) != pg.Hkv ||
+        k.size(2) != pg.D)
+        value_error("k and v must be [N, Hkv, D] of one dtype with the pages' heads and channels");
+    const Outer sk(k), sv(v);
+    done(attn_kv_gather_paged_q4(pg.t.data_ptr(), t.p, start, cu, k.data_ptr(), v.data_ptr(), t.B, to_int(k.size(0)),
+                                 pg.Hkv, pg.D, pg.P, pg.S, t.M, t.stride, pg.p, sk.p, sv.p, dtype_of(k), c.stream()),
+         "attn_kv_gather_paged_q4");
+    Py_INCREF(a[3]);
+    Py_INCREF(a[4]);
+    return Py_BuildValue("(NN)", a[3], a[4]);
+}
+
+// kv_pages, copy_src, copy_dst, count
+PyObject *kv_pages_copy_q4(PyObject *const *a) {
+    Call c;
+    const PagesQ4 pg(c, a[0], true);
+    const int n = to_int(c.take(a[1], "copy_src").numel());
+    const int32_t *src = c.ints(a[1], "copy_src", n), *dst = c.ints(a[2], "copy_dst", n);
+    const int32_t *count = a[3] == Py_None ? nullptr : c.ints(a[3], "count", 1);
+    if (n == 0) Py_RETURN_NONE;
+    return done(attn_kv_pages_copy_q4(pg.t.data_ptr(), src, dst, n, count, pg.layers, pg.P, pg.Hkv, pg.S, pg.D, pg.p,
+                                      c.stream()),
+                "attn_kv_pages_copy_q4");
+}
+
+// q, kv_pages, page_table, seq_len, o, scale, window, sinks, workspace
+PyObject *decode_gqa_paged_q4(PyObject *const *a) {
+    Call c;
+    const at::Tensor &q = c.take(a[0], "q");
+    const PagesQ4 pg(c, a[1]);
+    const Table t(c, a[2]);
+    if (q.dim() != 3 || q.size(0) != t.B || q.size(2) != pg.D)
+        value_error("q [B,Hq,D], kv_pages [P,Hkv,S,D + D / 8] and page_table [B,max_pages] required");
+    const int32_t *sl = c.ints(a[3], "seq_len", t.B);
+    const int Hq = to_int(q.size(1));
+    const at::Tensor o = output(c, a[4], q);
+    const Workspace ws(c, a[8], attn_decode_gqa_paged_q4_workspace_bytes(t.B, Hq, pg.Hkv, pg.D), true, q);
+    const Outer sq(q), so(o);
+    done(attn_decode_gqa_paged_q4(q.data_ptr(), pg.t.data_ptr(), t.p, sl, o.data_ptr(), t.B, Hq, pg.Hkv, pg.D, pg.P,
+                                  pg.S, t.M, t.stride, sq.p, pg.p, so.p, tokens(a[6]), tokens(a[7]), dtype_of(q),
+                                  scale_of(a[5]), ws.ptr(), ws.bytes(), c.stream()),
+         "attn_decode_gqa_paged_q4");
+    return returned(a[4], o);
+}
+
+// q, k, v, cu_q, cu_k, window, sinks, o, scale
+PyObject *causal_gqa_varlen_fwd(PyObject *const *a) {
+    Call c;
+    const at::Tensor &q = c.take(a[0], "q"), &k = c.take(a[1], "k"), &v = c.take(a[2], "v");
+    if (q.dim() != 3 || k.dim() != 3 || k.size(2) != q.size(2) || v.sizes() != k.sizes() ||
+        k.scalar_type() != q.scalar_type() || v.scalar_type() != q.scalar_type())
+        value_error("q must be [Nq, Hq, D], k and v [Nkv, Hkv, D] with q's dtype");
+    const at::Tensor &cq = c.take(a[3], "cu_q");
+    const int64_t n = cq.numel();
+    if (n < 2) value_error("cu_q must be int32 [B + 1]");
+    const int32_t *cu_q = c.ints(a[3], "cu_q", n);
+    const int32_t *cu_k = a[4] == Py_None ? cu_q : c.ints(a[4], "cu_k", n);
+    const at::Tensor o = output(c, a[7], q);
+    const Outer sq(q), sk(k), sv(v), so(o);
+    done(attn_causal_gqa_varlen_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), cu_q, cu_k,
+                                    to_int(n - 1), to_int(q.size(0)), to_int(k.size(0)), to_int(q.size(1)),
+                                    to_int(k.size(1)), to_int(q.size(2)), sq.p, sk.p, sv.p, so.p, tokens(a[5]),
+                                    tokens(a[6]), dtype_of(q), scale_of(a[8]), c.stream()),
+         "attn_causal_gqa_varlen_fwd");
+    return returned(a[7], o);
+}
+
 // page_table, seq_len, add_len, page_refs, page_size, workspace
 PyObject *kv_pages_reserve(PyObject *const *a) {
     Call c;
@@ -372,7 +605,10 @@ PyObject *set_error(PyObject *, PyObject *cls) {
 PyMethodDef g_methods[] = {
     ENTRY(causal_gqa_window_fwd, 7), ENTRY(decode_gqa_paged, 10), ENTRY(kv_append_paged, 8),
     ENTRY(kv_pages_reserve, 6),      ENTRY(kv_pages_free, 6),     ENTRY(kv_pages_fork, 7),
-    ENTRY(kv_pages_compact, 5),      ENTRY(kv_pages_copy, 5),     {"set_error", set_error, METH_O, nullptr},
+    ENTRY(kv_pages_compact, 5),      ENTRY(kv_pages_copy, 5),     ENTRY(rope_fwd, 7),
+    ENTRY(kv_append_paged_rope, 13), ENTRY(kv_append_paged_q4, 12), ENTRY(kv_gather_paged_q4, 6),
+    ENTRY(kv_pages_copy_q4, 4),      ENTRY(decode_gqa_paged_q4, 9), ENTRY(causal_gqa_varlen_fwd, 9),
+    {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_attn_native", nullptr, -1, g_methods, nullptr, nullptr, nullptr,
                         nullptr};

@@ -75,6 +75,18 @@ attn_status_t rope_rotate_qk(const Ctx &c, attn_dtype_t dt, const void *q, const
                              void *qr, void *kr, int BH, int N, int D, const int32_t *pos,
                              const int axes_dim[4], float theta);
 
+// Rotary positions (rotary.cu): freq DEVICE [rot / 2], 64-bit fractions of a turn.
+struct RotaryArgs {
+    const uint64_t *freq;
+    int rot, interleaved, inverse;       // rot 0: no rotation
+    float mscale;
+};
+attn_status_t rope_rows(const Ctx &c, attn_dtype_t dt, const void *x, void *y, const int32_t *pos,
+                        long long pos_stride, int B, int H, int N, int D, const TensorStrides &sx,
+                        const TensorStrides &sy, const RotaryArgs &rot);
+attn_status_t rope_frequencies(uint64_t *freq, int rot, double theta, attn_rope_scaling_t scaling, double factor,
+                               double original_len, double alpha, double beta);
+
 // KV-cache append at the device-side position seq_len[b] (optionally advancing it);
 // ring: the cache keeps the last Lmax tokens, token t in row t % Lmax.
 attn_status_t kv_append(const Ctx &c, attn_dtype_t dt, void *kc, void *vc, const void *kn,
@@ -118,6 +130,62 @@ struct PagedAppend {
     int advance;
 };
 attn_status_t kv_append_paged(const Ctx &c, attn_dtype_t dt, const PagedAppend &a);
+
+// Rows of packed new tokens into pages, K (and q) rotated on the way.  q4: k is a
+// cache held in 4 bits (v unused), its strides in bytes.
+struct RowsAppend {
+    void *k, *v;
+    const void *kn, *vn, *q;             // q null: none
+    void *qo;
+    const int32_t *table;
+    int32_t *seq_len;
+    const int32_t *cu;                   // nullptr: token b is the next one of sequence b
+    int B, N, Hq, Hkv, D, P, S, max_pages;
+    long long table_stride;
+    long long k_st[3], v_st[3];          // (page, head, token)
+    long long kn_st[2], vn_st[2], q_st[2], qo_st[2];   // (token, head)
+    RotaryArgs rot;
+    int advance;
+    bool q4;
+};
+attn_status_t append_rows(const Ctx &c, attn_dtype_t dt, const RowsAppend &a);
+
+// Rows of a cache held in 4 bits, as 16-bit K and V rows of packed sequences.
+struct RowsGather {
+    const void *pages;
+    const int32_t *table, *start, *cu;   // start nullptr: 0
+    void *k, *v;
+    int B, N, Hkv, D, P, S, max_pages;
+    long long table_stride;
+    long long p_st[2];                   // bytes (page, head)
+    long long k_st[2], v_st[2];          // (token, head)
+};
+attn_status_t gather_rows(const Ctx &c, attn_dtype_t dt, const RowsGather &a);
+
+// Decode over pages held in 4 bits; p_st: bytes (page, head).
+struct PagedDecodeQ4 {
+    const void *q, *pages;
+    void *o;
+    const int32_t *table, *seq_len;
+    int B, G, Hkv, D, P, S, max_pages;
+    long long table_stride;
+    long long q_st[2], o_st[2], p_st[2];
+    int window, sinks;
+    float scale;
+    void *ws;
+};
+size_t decode_paged_q4_workspace_bytes(int B, int Hkv);
+attn_status_t decode_paged_q4(const Ctx &c, attn_dtype_t dt, const PagedDecodeQ4 &a);
+
+// Pages of a cache held in 4 bits, strides in bytes (layer, page, head).
+struct PagesCopyQ4 {
+    void *pages;
+    const int32_t *src, *dst, *count;
+    int n, layers, Hkv, P;
+    long long block;                     // bytes of one head's rows of a page
+    long long st[3];
+};
+attn_status_t kv_pages_copy_q4(const Ctx &c, const PagesCopyQ4 &a);
 
 struct PagesCopy {
     void *k, *v;
@@ -164,6 +232,18 @@ attn_status_t simt_causal_window(const Ctx &c, attn_dtype_t dt, const void *q, c
                                  const void *v, void *o, int B, int Hq, int Hkv, int Nq, int Nkv,
                                  int D, int window, int sinks, float scale,
                                  const TensorStrides *st);
+// Causal attention over packed sequences; st: (b unused, head, token).
+struct VarlenArgs {
+    const void *q, *k, *v;
+    void *o;
+    const int32_t *cu_q, *cu_k;
+    int B, Nq, Nkv, Hq, Hkv, D;
+    TensorStrides st[4];
+    int window, sinks;                   // window: wider than any sequence for none
+    float scale;
+};
+attn_status_t tc_causal_varlen(const Ctx &c, attn_dtype_t dt, const VarlenArgs &a);
+attn_status_t simt_causal_varlen(const Ctx &c, attn_dtype_t dt, const VarlenArgs &a);
 attn_status_t tc_na3d(const Ctx &c, attn_dtype_t dt, const void *q, const void *k, const void *v,
                       void *o, int B, int H, int T, int Hg, int W, int D, const int kernel[3],
                       float scale);

@@ -164,7 +164,7 @@ struct CopyParams {
     int n, P;
     int vecs;                                          // 16-byte vectors of a page side
     int pieces;                                        // pieces of kPiece vectors per page side
-    int sides;                                         // layers * 2
+    int sides, two;                                    // layers * 2; two: K and V are arrays of their own
     int vpr, S;                                        // vectors per row, rows per head
     long long k_st[4], v_st[4];                        // bytes (layer, page, head, token)
     unsigned *err;
@@ -193,8 +193,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p) 
             continue;
         }
         if (s == d) continue;
-        const bool is_v = side & 1;
-        uint8_t *base = (is_v ? p.v : p.k) + (side >> 1) * (is_v ? p.v_st[0] : p.k_st[0]);
+        const bool is_v = side & p.two;
+        uint8_t *base = (is_v ? p.v : p.k) + (side >> p.two) * (is_v ? p.v_st[0] : p.k_st[0]);
         const long long pst = is_v ? p.v_st[1] : p.k_st[1];
         const uint8_t *from = base + s * pst;
         uint8_t *to = base + d * pst;
@@ -977,6 +977,7 @@ attn_status_t kv_pages_copy(const Ctx &c, attn_dtype_t dt, const PagesCopy &a) {
     p.vecs = a.Hkv * a.S * p.vpr;
     p.pieces = cdiv(p.vecs, kPiece);
     p.sides = 2 * a.layers;
+    p.two = 1;
     for (int i = 0; i < 4; ++i) {
         p.k_st[i] = a.k_st[i] * es;
         p.v_st[i] = a.v_st[i] * es;
@@ -987,6 +988,26 @@ attn_status_t kv_pages_copy(const Ctx &c, attn_dtype_t dt, const PagesCopy &a) {
     const bool dense = dense_page(a.k_st + 2, a.Hkv, a.S, a.D) && dense_page(a.v_st + 2, a.Hkv, a.S, a.D);
     return dense ? launch_pdl(c, copy_kernel<true>, dim3(grid), kCopyThreads, 1, 0, p)
                  : launch_pdl(c, copy_kernel<false>, dim3(grid), kCopyThreads, 1, 0, p);
+}
+
+// A (page, head) of a cache held in 4 bits is one block of bytes: one row of the
+// copy above, in one array.
+attn_status_t kv_pages_copy_q4(const Ctx &c, const PagesCopyQ4 &a) {
+    CopyParams p{};
+    p.k = p.v = static_cast<uint8_t *>(a.pages);
+    p.src = a.src; p.dst = a.dst; p.count = a.count;
+    p.n = a.n; p.P = a.P;
+    p.vpr = int(a.block / 16);
+    p.S = 1;
+    p.vecs = a.Hkv * p.vpr;
+    p.pieces = cdiv(p.vecs, kPiece);
+    p.sides = a.layers;
+    for (int i = 0; i < 3; ++i) p.k_st[i] = p.v_st[i] = a.st[i];
+    p.err = c.err;
+    const long long items = (long long)a.n * p.sides * p.pieces;
+    const int grid = int(items < 8ll * c.sm_count ? items : 8ll * c.sm_count);
+    return a.Hkv == 1 || a.st[2] == a.block ? launch_pdl(c, copy_kernel<true>, dim3(grid), kCopyThreads, 1, 0, p)
+                                            : launch_pdl(c, copy_kernel<false>, dim3(grid), kCopyThreads, 1, 0, p);
 }
 
 size_t kv_pages_workspace_bytes(int P) { return (size_t(P) * 4 + 255) & ~size_t(255); }

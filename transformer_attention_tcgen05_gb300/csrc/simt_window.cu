@@ -28,6 +28,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "packed.cuh"
 #include "ptx.cuh"
 
 namespace attn {
@@ -43,6 +44,8 @@ struct WinParams {
     void *o;
     int Nq, Nkv, off, window, sinks, H, group;
     float qscale;            // scale * log2(e)
+    PackedSeqs seqs;         // packed: the sequences' starts (Nq, Nkv, off unused)
+    unsigned *err;
     TensorStrides sq, sk, sv, so;
 };
 
@@ -103,22 +106,40 @@ template <int N> __device__ __forceinline__ void read(const float *p, float (&x)
 // Warp w owns rows 8 w .. 8 w + 7; a lane keys lane and lane + 32 of a tile and
 // channels lane CH .. lane CH + CH - 1 of O.  What all lanes read (q, P) costs
 // shared memory one cycle a vector, what each reads for itself (k, V) four.
-template <typename T, int D>
+// PACKED: sequences of different lengths one behind the other; every warp finds the
+// CTA's block of rows (packed.cuh).
+template <typename T, int D, bool PACKED>
 __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) simt_window_kernel(const WinParams p) {
     using S = WinSmem<D>;
     constexpr int CH = D / 32;
     extern __shared__ float sm[];
     float *Qs = sm + S::Q, *Ks = sm + S::K, *Vs = sm + S::V, *Ps = sm + S::P;
     const int tid = threadIdx.x, lane = tid & 31, row0 = (tid >> 5) * kR;
-    const int q0 = (gridDim.x - 1 - blockIdx.x) * kBM;
-    const long long b = blockIdx.y / p.H, h = blockIdx.y % p.H, hk = h / p.group;
-    const T *qg = static_cast<const T *>(p.q) + (b * p.sq.b + h * p.sq.h);
-    const T *kg = static_cast<const T *>(p.k) + (b * p.sk.b + hk * p.sk.h);
-    const T *vg = static_cast<const T *>(p.v) + (b * p.sv.b + hk * p.sv.h);
-    T *og = static_cast<T *>(p.o) + (b * p.so.b + h * p.so.h);
+    const long long b = PACKED ? 0 : blockIdx.y / p.H, h = PACKED ? blockIdx.y : blockIdx.y % p.H;
+    const long long hk = h / p.group;
+    int q0, nq, off;
+    long long q_row = 0, k_row = 0;
+    if constexpr (PACKED) {
+        const BlockFinder finder(p.seqs, 5, blockIdx.x == 0 && h == 0 && tid < 32, p.err);
+        if (int(blockIdx.x) >= finder.total) return;
+        const PackedBlock at = finder.find(blockIdx.x);
+        q0 = at.q0;
+        nq = at.nq;
+        off = at.nkv - at.nq;
+        q_row = at.q_row;
+        k_row = at.k_row;
+    } else {
+        q0 = (gridDim.x - 1 - blockIdx.x) * kBM;
+        nq = p.Nq;
+        off = p.off;
+    }
+    const T *qg = static_cast<const T *>(p.q) + (b * p.sq.b + h * p.sq.h + q_row * p.sq.n);
+    const T *kg = static_cast<const T *>(p.k) + (b * p.sk.b + hk * p.sk.h + k_row * p.sk.n);
+    const T *vg = static_cast<const T *>(p.v) + (b * p.sv.b + hk * p.sv.h + k_row * p.sv.n);
+    T *og = static_cast<T *>(p.o) + (b * p.so.b + h * p.so.h + q_row * p.so.n);
 
-    const int pos0 = p.off + q0;                       // position of the first row
-    const int rows = imin(kBM, p.Nq - q0);
+    const int pos0 = off + q0;                         // position of the first row
+    const int rows = imin(kBM, nq - q0);
     const int end = pos0 + rows;                       // keys past the last row are seen by none
     const int win0 = imax(0, pos0 - p.window + 1);
     const int sink1 = imin(p.sinks, win0);
@@ -358,21 +379,28 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) simt_window_kernel
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool PACKED>
 attn_status_t launch_win(const Ctx &c, const WinParams &p, int tiles, int BH) {
     static int done_mask = 0;
-    auto kern = simt_window_kernel<T, D>;
+    auto kern = simt_window_kernel<T, D, PACKED>;
     if (!ensure_smem_attr(reinterpret_cast<const void *>(kern), WinSmem<D>::BYTES, c.device, &done_mask))
         return ATTN_ERR_RESOURCE;
     kern<<<dim3(tiles, BH), kThreads, WinSmem<D>::BYTES, c.stream>>>(p);
     return launch_status(kFamSimt);
 }
 
-template <typename T>
-attn_status_t dispatch_win(const Ctx &c, int D, const WinParams &p, int tiles, int BH) {
-    if (D == 32) return launch_win<T, 32>(c, p, tiles, BH);
-    if (D == 64) return launch_win<T, 64>(c, p, tiles, BH);
-    return launch_win<T, 128>(c, p, tiles, BH);
+template <typename T, bool PACKED>
+attn_status_t dispatch_d(const Ctx &c, int D, const WinParams &p, int tiles, int BH) {
+    if (D == 32) return launch_win<T, 32, PACKED>(c, p, tiles, BH);
+    if (D == 64) return launch_win<T, 64, PACKED>(c, p, tiles, BH);
+    return launch_win<T, 128, PACKED>(c, p, tiles, BH);
+}
+
+template <bool PACKED>
+attn_status_t dispatch_win(const Ctx &c, attn_dtype_t dt, int D, const WinParams &p, int tiles, int BH) {
+    if (dt == ATTN_F32) return dispatch_d<float, PACKED>(c, D, p, tiles, BH);
+    if (dt == ATTN_F16) return dispatch_d<__half, PACKED>(c, D, p, tiles, BH);
+    return dispatch_d<__nv_bfloat16, PACKED>(c, D, p, tiles, BH);
 }
 
 }  // namespace
@@ -392,10 +420,23 @@ attn_status_t simt_causal_window(const Ctx &c, attn_dtype_t dt, const void *q, c
     p.group = Hq / Hkv;
     p.qscale = scale * kLog2e;
     p.sq = st[0]; p.sk = st[1]; p.sv = st[2]; p.so = st[3];
-    const int tiles = cdiv(Nq, kBM);
-    if (dt == ATTN_F32) return dispatch_win<float>(c, D, p, tiles, B * Hq);
-    if (dt == ATTN_F16) return dispatch_win<__half>(c, D, p, tiles, B * Hq);
-    return dispatch_win<__nv_bfloat16>(c, D, p, tiles, B * Hq);
+    return dispatch_win<false>(c, dt, D, p, cdiv(Nq, kBM), B * Hq);
+}
+
+attn_status_t simt_causal_varlen(const Ctx &c, attn_dtype_t dt, const VarlenArgs &a) {
+    WinParams p{};
+    p.q = a.q; p.k = a.k; p.v = a.v; p.o = a.o;
+    p.seqs = PackedSeqs{a.cu_q, a.cu_k, a.B, a.Nq, a.Nkv};
+    p.window = a.window;
+    p.sinks = a.sinks;
+    p.H = a.Hq;
+    p.group = a.Hq / a.Hkv;
+    p.qscale = a.scale * kLog2e;
+    p.err = c.err;
+    p.sq = a.st[0]; p.sk = a.st[1]; p.sv = a.st[2]; p.so = a.st[3];
+    // the most blocks that sequences of Nq queries together can have
+    const long long blocks = (a.Nq + (long long)imin(a.B, a.Nq) * (kBM - 1)) / kBM;
+    return dispatch_win<true>(c, dt, a.D, p, int(blocks), a.Hq);
 }
 
 }  // namespace attn

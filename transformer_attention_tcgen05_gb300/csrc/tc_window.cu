@@ -61,6 +61,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "packed.cuh"
 #include "ptx.cuh"
 
 namespace attn {
@@ -144,10 +145,47 @@ struct WnParams {
     int by_head;             // a pair is two heads of one KV head (else two row tiles)
     int blocks;              // row blocks
     Div by_hp, by_h, by_group;   // pairs (or heads) per row block, heads, heads per KV head
+    PackedSeqs seqs;         // packed: the sequences' starts (Nq, Nkv, off, pairs, whole, blocks unused)
+    int sms;                 // packed: SMs
     const void *v;           // with element strides: values cleared from an edge tile
     TensorStrides sv;
     void *o;
     long long o_sb, o_sh, o_sn;
+};
+
+// a[t] for a per-query-tile array and a run-time t, by selects
+template <typename T>
+__device__ __forceinline__ T pick(const T (&a)[kNQ], int t) { return t == 0 ? a[0] : a[1]; }
+
+// One work item: a pair of query tiles, or one tile alone.  Query tile t (rows
+// q0 + t dq, head fh + t dh) works in steps [f[t], n[t]) of the item's key tile
+// list.
+struct Item {
+    int q0, fb, fh, fkh, dq, dh;
+    int n[kNQ], f[kNQ], steps;
+    int w_lo, w_sk;                // first window tile, sink tiles before it
+    bool few;                      // step 0 is the sinks' tile and holds at most kFew keys
+    int nq, nkv, off;              // the sequence's lengths, its first query's position
+    int q_row, k_row;              // packed: its rows in the arrays
+    int e0, e1, e2;                // steps of the tiles on an edge: [e0, e1), [e2, steps), a leading one
+
+    // key tile of step j: the leading tile of the first query tile (if any),
+    // the sink tiles, the window
+    __device__ __forceinline__ int tile(int j) const {
+        const int i = j - f[1];
+        return i < 0 ? w_lo : i < w_sk ? i : w_lo + j - w_sk;
+    }
+    // step j is a tile of sinks in front of every row's window
+    __device__ __forceinline__ bool sink_tile(int j) const { return j >= f[1] && j < f[1] + w_sk; }
+    // some row does not see all keys of step j's tile (sink tiles left out)
+    __device__ __forceinline__ bool edge(int j) const {
+        return j >= e2 || (j >= e0 && j < e1) || j < f[1];
+    }
+    // step j's values are looked over (packed: no tensor map ends behind a
+    // sequence's sinks)
+    template <bool PACKED> __device__ __forceinline__ bool checked(int j) const {
+        return edge(j) || (PACKED && sink_tile(j));
+    }
 };
 
 // Barrier block at OFF_BAR.
@@ -163,35 +201,33 @@ struct Bars {
     uint64_t drain, checked;       // checked: every edge tile has been looked over
     uint32_t tmem_base;
     int abort, wild;               // wild: a value was cleared from one of them
+    Item item;                     // packed: the CTA's item
 };
 
-// a[t] for a per-query-tile array and a run-time t, by selects
-template <typename T>
-__device__ __forceinline__ T pick(const T (&a)[kNQ], int t) { return t == 0 ? a[0] : a[1]; }
-
-// One work item: a pair of query tiles, or one tile alone.  Query tile t (rows
-// q0 + t dq, head fh + t dh) works in steps [f[t], n[t]) of the item's key tile
-// list.
-struct Item {
-    int q0, fb, fh, fkh, dq, dh;
-    int n[kNQ], f[kNQ], steps;
-    int w_lo, w_sk;                // first window tile, sink tiles before it
-    bool few;                      // step 0 is the sinks' tile and holds at most kFew keys
-    int e0, e1, e2;                // steps of the tiles on an edge: [e0, e1), [e2, steps), a leading one
-
-    // key tile of step j: the leading tile of the first query tile (if any),
-    // the sink tiles, the window
-    __device__ __forceinline__ int tile(int j) const {
-        const int i = j - f[1];
-        return i < 0 ? w_lo : i < w_sk ? i : w_lo + j - w_sk;
-    }
-    // step j is a tile of sinks in front of every row's window
-    __device__ __forceinline__ bool sink_tile(int j) const { return j >= f[1] && j < f[1] + w_sk; }
-    // some row does not see all keys of step j's tile (sink tiles left out)
-    __device__ __forceinline__ bool edge(int j) const {
-        return j >= e2 || (j >= e0 && j < e1) || j < f[1];
-    }
-};
+// Completes an item of query rows q0 of one sequence: its heads are w.fh, of the
+// pair or (half >= 0) one tile of it.
+__device__ __forceinline__ void plan_item(const WnParams &p, Item &w, int half) {
+    const int pos = w.off + w.q0;
+    const bool one = w.q0 < w.nq, two = half < 0 && w.q0 + w.dq < w.nq;
+    const int ns = cdiv(p.sinks, kBN);
+    w.w_lo = imax(0, pos - p.window + 1) / kBN;
+    const int lo1 = imax(0, pos + w.dq - p.window + 1) / kBN;
+    w.w_sk = imin(ns, w.w_lo);
+    w.few = w.w_sk > 0 && p.sinks <= kFew;
+    w.f[0] = 0;
+    w.f[1] = two && lo1 > w.w_lo && w.w_lo >= ns ? 1 : 0;
+    w.few = w.few && w.f[1] == 0;
+    // (a single second row tile past the sequence's end has no step)
+    w.n[0] = one ? w.w_sk + (w.off + imin(w.q0 + kBM, w.nq) - 1) / kBN - w.w_lo + 1 : 0;
+    w.n[1] = two ? w.w_sk + (w.off + imin(w.q0 + w.dq + kBM, w.nq) - 1) / kBN - w.w_lo + 1 : 0;
+    w.steps = imax(w.n[0], w.n[1]);
+    // the window of the last query tile starts behind its first key, or the first
+    // one's diagonal comes before its last
+    const int lead = two ? pos + w.dq : pos;
+    w.e0 = w.w_sk + w.f[1];
+    w.e1 = w.w_sk + cdiv(imax(0, lead + kBM - p.window), kBN) - w.w_lo;
+    w.e2 = w.w_sk + imax(0, (pos + 1) / kBN - w.w_lo);
+}
 
 // This CTA's item: whole pairs, late queries first, then the rest as single
 // tiles.
@@ -207,26 +243,43 @@ __device__ __forceinline__ Item get_item(const WnParams &p) {
     w.fh = bh - w.fb * p.by_h.d + (half > 0 ? w.dh : 0);
     w.fkh = p.by_group(w.fh);
     w.q0 = qb * (p.by_head ? kBM : kNQ * kBM) + (half > 0 ? w.dq : 0);
-    const int pos = p.off + w.q0;
-    const bool one = w.q0 < p.Nq, two = half < 0 && w.q0 + w.dq < p.Nq;
-    const int ns = cdiv(p.sinks, kBN);
-    w.w_lo = imax(0, pos - p.window + 1) / kBN;
-    const int lo1 = imax(0, pos + w.dq - p.window + 1) / kBN;
-    w.w_sk = imin(ns, w.w_lo);
-    w.few = w.w_sk > 0 && p.sinks <= kFew;
-    w.f[0] = 0;
-    w.f[1] = two && lo1 > w.w_lo && w.w_lo >= ns ? 1 : 0;
-    w.few = w.few && w.f[1] == 0;
-    // (a single second row tile past the sequence's end has no step)
-    w.n[0] = one ? w.w_sk + (p.off + imin(w.q0 + kBM, p.Nq) - 1) / kBN - w.w_lo + 1 : 0;
-    w.n[1] = two ? w.w_sk + (p.off + imin(w.q0 + w.dq + kBM, p.Nq) - 1) / kBN - w.w_lo + 1 : 0;
-    w.steps = imax(w.n[0], w.n[1]);
-    // the window of the last query tile starts behind its first key, or the first
-    // one's diagonal comes before its last
-    const int lead = two ? pos + w.dq : pos;
-    w.e0 = w.w_sk + w.f[1];
-    w.e1 = w.w_sk + cdiv(imax(0, lead + kBM - p.window), kBN) - w.w_lo;
-    w.e2 = w.w_sk + imax(0, (pos + 1) / kBN - w.w_lo);
+    w.nq = p.Nq;
+    w.nkv = p.Nkv;
+    w.off = p.off;
+    w.q_row = w.k_row = 0;
+    plan_item(p, w, half);
+    return w;
+}
+
+// The same for packed sequences (one warp): the blocks of all sequences by falling
+// level (packed.cuh), the pairs of a last round split by the same rule.  A CTA
+// behind the last item has one without steps.
+__device__ __forceinline__ Item find_item(const WnParams &p) {
+    const BlockFinder finder(p.seqs, p.by_head ? 7 : 8, blockIdx.x == 0, p.err);
+    const int pairs = finder.total * p.by_hp.d, rest = pairs % p.sms;
+    const int whole = 2 * rest <= p.sms ? pairs - rest : pairs;
+    const int s = int(blockIdx.x) - whole;
+    const int pair = s < 0 ? int(blockIdx.x) : whole + (s >> 1), half = s < 0 ? -1 : s & 1;
+    Item w;
+    w.n[0] = w.n[1] = w.f[0] = w.f[1] = w.steps = 0;
+    w.w_lo = w.w_sk = w.e0 = w.e1 = w.e2 = 0;
+    w.few = false;
+    w.q0 = w.nq = w.nkv = w.off = w.q_row = w.k_row = 0;
+    w.fb = w.fh = w.fkh = 0;
+    w.dq = p.by_head ? 0 : kBM;
+    w.dh = p.by_head ? 1 : 0;
+    if (pair >= pairs) return w;
+    const int block = p.by_hp(pair);
+    const PackedBlock b = finder.find(block);
+    w.fh = (pair - block * p.by_hp.d) * (p.by_head ? 2 : 1) + (half > 0 ? w.dh : 0);
+    w.fkh = p.by_group(w.fh);
+    w.q0 = b.q0 + (half > 0 ? w.dq : 0);
+    w.nq = b.nq;
+    w.nkv = b.nkv;
+    w.off = b.nkv - b.nq;
+    w.q_row = b.q_row;
+    w.k_row = b.k_row;
+    plan_item(p, w, half);
     return w;
 }
 
@@ -291,18 +344,20 @@ __device__ __forceinline__ bool clear_wild(uint8_t *stage) {
 // the warp's staged output rows that see them: whatever its (positive) weight,
 // such a value makes its channel of the row infinite or NaN.  Rare, so the
 // values are read again from memory, a row of V at a time.
-template <int D, bool F16>
-__device__ __noinline__ void spoil_rows(const WnParams &p, uint8_t *stage, int first_pos, int rows) {
-    const Item w = get_item(p);                      // (handed over it would live in memory)
+template <int D, bool F16, bool PACKED>
+__device__ __noinline__ void spoil_rows(const WnParams &p, const Item *packed, uint8_t *stage, int first_pos,
+                                        int rows) {
+    const Item w = PACKED ? *packed : get_item(p);   // (handed over it would live in memory)
     using H = H16<F16>;
     constexpr int CW = D / 64;                       // 32-bit words (two channels) per lane
     constexpr int CH = D / 8, U = 8;
     const int lane = threadIdx.x & 31;
     const uint32_t *v = reinterpret_cast<const uint32_t *>(static_cast<const typename H::T *>(p.v) +
-                                                           w.fb * p.sv.b + w.fkh * p.sv.h) + lane * CW;
+                                                           w.fb * p.sv.b + w.fkh * p.sv.h +
+                                                           w.k_row * p.sv.n) + lane * CW;
     for (int j = 0; j < w.steps; ++j) {
-        if (!w.edge(j)) continue;
-        const int k0 = w.tile(j) * kBN, keys = imin(kBN, p.Nkv - k0);
+        if (!w.template checked<PACKED>(j)) continue;
+        const int k0 = w.tile(j) * kBN, keys = imin(kBN, w.nkv - k0);
         for (int i = 0; i < keys; i += U) {
             uint32_t x[U][CW];
 #pragma unroll
@@ -335,7 +390,9 @@ __device__ __noinline__ void spoil_rows(const WnParams &p, uint8_t *stage, int f
     __syncwarp();
 }
 
-template <int D, bool F16>
+// PACKED: q, k, v and o hold sequences of different lengths one behind the other
+// (p.seqs); a warp finds the CTA's item while the rest is set up.
+template <int D, bool F16, bool PACKED>
 __global__ void __launch_bounds__(WnCfg<D>::NT, 1)
 tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                  const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tvs,
@@ -381,8 +438,16 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     if (warp == C::W_LOAD || warp == C::W_LOADV) {
         ptx::prefetch_tmap(warp == C::W_LOAD ? &tk : &tv);
         if (warp == C::W_LOAD) ptx::prefetch_tmap(&tq);
-        load_item = get_item(p);
-        if (warp == C::W_LOADV && load_item.w_sk > 0) ptx::prefetch_tmap(&tvs);
+        if constexpr (PACKED) {
+            if (warp == C::W_LOAD) {
+                ptx::griddep_wait();                   // the starts may be the previous kernel's
+                load_item = find_item(p);
+                if (lane == 0) bars->item = load_item;
+            }
+        } else {
+            load_item = get_item(p);
+            if (warp == C::W_LOADV && load_item.w_sk > 0) ptx::prefetch_tmap(&tvs);
+        }
     }
     ptx::tc_fence_before();
     __syncthreads();
@@ -391,6 +456,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     // programmatic dependent launch: the set-up above touches nothing global
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
+    auto my_item = [&]() -> Item { return PACKED ? bars->item : get_item(p); };
 
     if (warp >= C::NSOFT) {
         ptx::regs_decrease<C::REGS_OTHER>();
@@ -403,7 +469,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             uint64_t *empty = which == 0 ? bars->k_empty : bars->v_empty;
             const int NS = which == 0 ? C::KS : C::VS;   // depth of this ring
             const uint64_t pol_kv = ptx::l2_policy_evict_last(), pol_q = ptx::l2_policy_evict_first();
-            const Item w = load_item;
+            const Item w = PACKED && which == 1 ? bars->item : load_item;
             int q_out = 0, issued = 0;
             auto load_q = [&](int t) {
                 if (t >= (w.n[1] > 0 ? kNQ : 1)) return;
@@ -411,7 +477,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 ptx::mbar_arrive_expect_tx(&bars->q_full[t], C::Q_BYTES);
                 for (int pn = 0; pn < C::PANELS; ++pn)
                     ptx::tma_load_4d(smem + C::OFF_Q + t * C::Q_BYTES + pn * C::PANEL_Q, &tq, pn * 64,
-                                     w.q0 + t * w.dq, w.fh + t * w.dh, w.fb, &bars->q_full[t], pol_q);
+                                     w.q_row + w.q0 + t * w.dq, w.fh + t * w.dh, w.fb, &bars->q_full[t], pol_q);
             };
             if (which == 0 && w.steps > 0) load_q(0);
             for (int j = 0; j < w.steps; ++j) {
@@ -421,7 +487,8 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 ptx::mbar_arrive_expect_tx(&full[s], C::KV_BYTES);
                 for (int pn = 0; pn < C::PANELS; ++pn)
                     ptx::tma_load_4d(smem + (which == 0 ? C::k_off(s) : C::v_off(s)) + pn * C::PANEL_KV,
-                                     which == 1 && w.sink_tile(j) ? &tvs : tm, pn * 64, w.tile(j) * kBN, w.fkh, w.fb, &full[s], pol_kv);
+                                     !PACKED && which == 1 && w.sink_tile(j) ? &tvs : tm, pn * 64,
+                                     w.k_row + w.tile(j) * kBN, w.fkh, w.fb, &full[s], pol_kv);
                 // the first scores need one query tile and the first keys
                 if (which == 0 && j == 0) load_q(1);
             }
@@ -448,7 +515,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             const uint32_t dk0 = ptx::desc_lo_sw128(ptx::smem_addr(smem + C::k_off(0)), 16);
             const uint32_t dv0 = ptx::desc_lo_sw128(ptx::smem_addr(smem + C::v_off(0)), C::PANEL_KV);
             constexpr int nkv = BNt / 16;                // k-steps of P V
-            const Item w = get_item(p);
+            const Item w = my_item();
             auto issue_qk = [&](int t, int gk) {
                 if (!lead) return;
                 const uint32_t id = w.few && gk == 0 ? id_few : id_qk;
@@ -548,12 +615,12 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             // ============================================= the V of edge tiles is
             // looked over as it arrives, while the tile's scores are computed and
             // exponentiated; other tiles are passed on at once
-            const Item w = get_item(p);
+            const Item w = my_item();
             for (int j = 0; j < w.steps; ++j) {
                 const int s = j % C::VS;
                 if (!__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&bars->v_in[s], (j / C::VS) & 1, p.err, abort)))
                     break;
-                const bool any = w.edge(j) && clear_wild<D, F16>(smem + C::v_off(s));
+                const bool any = w.template checked<PACKED>(j) && clear_wild<D, F16>(smem + C::v_off(s));
                 __syncwarp();
                 if (lane == 0) {
                     if (any) bars->wild = 1;
@@ -574,9 +641,9 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         const uint32_t p_addr = lane_base + C::tm_p(t);
         const float cl = p.c_log2;
         bool ok = true;
-        const Item w = get_item(p);
+        const Item w = my_item();
         const int f = pick(w.f, t), nt = pick(w.n, t) - f;   // this query tile's key tiles
-        const int pos = p.off + w.q0 + w.dq * t;             // position of its first row
+        const int pos = w.off + w.q0 + w.dq * t;             // position of its first row
 
         // waits for the P V product of key tile jj of this query tile (and so
         // for every earlier one: one thread's MMAs complete in issue order)
@@ -811,15 +878,15 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             __syncwarp();
             if (__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&bars->checked, 0, p.err, abort)) &&
                 *reinterpret_cast<volatile int *>(&bars->wild))
-                spoil_rows<D, F16>(p, stage, p.off + q_first, imin(32, p.Nq - q_first));
+                spoil_rows<D, F16, PACKED>(p, &bars->item, stage, w.off + q_first, imin(32, w.nq - q_first));
             typename H16<F16>::T *const o0 = static_cast<typename H16<F16>::T *>(p.o) + w.fb * p.o_sb + qh * p.o_sh;
             const int col = ln % CH;
 #pragma unroll
             for (int r0 = 0; r0 < 32; r0 += 32 / CH) {
                 const int r = r0 + ln / CH;
                 const uint4 x = *reinterpret_cast<const uint4 *>(stage + (r * CH + (col ^ (r & 7))) * 16);
-                if (q_first + r < p.Nq)
-                    *reinterpret_cast<uint4 *>(o0 + (q_first + r) * p.o_sn + col * 8) = x;
+                if (q_first + r < w.nq)
+                    *reinterpret_cast<uint4 *>(o0 + (w.q_row + q_first + r) * p.o_sn + col * 8) = x;
             }
         }
     }
@@ -833,13 +900,13 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     }
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool PACKED>
 attn_status_t launch_window(const Ctx &c, const CUtensorMap &tq, const CUtensorMap &tk,
-                            const CUtensorMap &tv, const CUtensorMap &tvs, const WnParams &p) {
+                            const CUtensorMap &tv, const CUtensorMap &tvs, const WnParams &p, int grid) {
     using C = WnCfg<D>;
     static int done_mask = 0;
     static int regs = -1;
-    auto kern = tc_window_kernel<D, F16>;
+    auto kern = tc_window_kernel<D, F16, PACKED>;
     if (!ensure_smem_attr(reinterpret_cast<const void *>(kern), C::SMEM, c.device, &done_mask))
         return ATTN_ERR_RESOURCE;
     // the setmaxnreg split is only valid for the per-thread count it was computed for
@@ -853,7 +920,7 @@ attn_status_t launch_window(const Ctx &c, const CUtensorMap &tq, const CUtensorM
     }
     if (regs != C::REGS_LAUNCH) return ATTN_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.whole + 2 * (p.pairs - p.whole));
+    cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(C::NT);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = c.stream;
@@ -909,9 +976,45 @@ attn_status_t tc_causal_window(const Ctx &c, attn_dtype_t dt, const void *q, con
     p.v = v; p.o = o;
     p.sv = st[2];
     p.o_sb = st[3].b; p.o_sh = st[3].h; p.o_sn = st[3].n;
+    const int grid = p.whole + 2 * (p.pairs - p.whole);
     if (D == 128)
-        return f16 ? launch_window<128, true>(c, tq, tk, tv, tvs, p) : launch_window<128, false>(c, tq, tk, tv, tvs, p);
-    return f16 ? launch_window<64, true>(c, tq, tk, tv, tvs, p) : launch_window<64, false>(c, tq, tk, tv, tvs, p);
+        return f16 ? launch_window<128, true, false>(c, tq, tk, tv, tvs, p, grid)
+                   : launch_window<128, false, false>(c, tq, tk, tv, tvs, p, grid);
+    return f16 ? launch_window<64, true, false>(c, tq, tk, tv, tvs, p, grid)
+               : launch_window<64, false, false>(c, tq, tk, tv, tvs, p, grid);
+}
+
+attn_status_t tc_causal_varlen(const Ctx &c, attn_dtype_t dt, const VarlenArgs &a) {
+    const bool f16 = dt == ATTN_F16;
+    const bool by_head = (a.Hq / a.Hkv) % 2 == 0;
+    const int bs = by_head ? kBM : kNQ * kBM, hp = by_head ? a.Hq / 2 : a.Hq;
+    // the most blocks that sequences of Nq queries together can have
+    const long long blocks = (a.Nq + (long long)imin(a.B, a.Nq) * (bs - 1)) / bs;
+    if (blocks * hp > (1 << 29)) return ATTN_ERR_UNSUPPORTED;
+    CUtensorMap tq, tk, tv;
+    if (!make_tmap4(&tq, a.q, a.D, a.Nq, a.Hq, 1, a.st[0], f16) ||
+        !make_tmap4(&tk, a.k, a.D, a.Nkv, a.Hkv, 1, a.st[1], f16) ||
+        !make_tmap4(&tv, a.v, a.D, a.Nkv, a.Hkv, 1, a.st[2], f16))
+        return ATTN_ERR_UNSUPPORTED;
+    WnParams p{};
+    p.seqs = PackedSeqs{a.cu_q, a.cu_k, a.B, a.Nq, a.Nkv};
+    p.sms = imax(1, c.sm_count);
+    p.window = a.window;
+    p.sinks = a.sinks;
+    p.c_log2 = a.scale * kLog2e;
+    p.err = c.err;
+    p.by_hp = Div(hp);
+    p.by_group = Div(a.Hq / a.Hkv);
+    p.by_head = by_head;
+    p.v = a.v; p.o = a.o;
+    p.sv = a.st[2];
+    p.o_sh = a.st[3].h; p.o_sn = a.st[3].n;
+    const int grid = int(blocks * hp) + p.sms / 2;     // and the halves of a split last round
+    if (a.D == 128)
+        return f16 ? launch_window<128, true, true>(c, tq, tk, tv, tv, p, grid)
+                   : launch_window<128, false, true>(c, tq, tk, tv, tv, p, grid);
+    return f16 ? launch_window<64, true, true>(c, tq, tk, tv, tv, p, grid)
+               : launch_window<64, false, true>(c, tq, tk, tv, tv, p, grid);
 }
 
 }  // namespace attn
