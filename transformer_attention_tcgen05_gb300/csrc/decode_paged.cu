@@ -130,7 +130,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
 
     // ---- loads: a walk of its own that runs NS chunks (and a group of page
     //      lookups) ahead of the computation
-    const int nb = p.nb, BR = 1 << p.br_log;           // boxes per chunk (1, 2 or 4), their rows
+    const int BR = 1 << p.br_log;                      // rows of a box (1, 2 or 4 boxes per chunk)
     const int box_bytes = BR * D * 2;
     const uint64_t pol = ptx::l2_policy_evict_first();
     uint64_t *full_k = bars->full_k + warp * NS, *full_v = bars->full_v + warp * NS;
@@ -145,9 +145,10 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         bad_bits = (bad_bits & ~(1u << (issued & 31))) | (unsigned(feed.bad != 0) << (issued & 31));
         if (lane == 0) ptx::mbar_arrive_expect_tx(&full_k[s], __popc(feed.mine) * box_bytes);
         __syncwarp();
-        if (lane < nb && ((feed.mine >> lane) & 1u))
-            ptx::tma_load_5d(ring_k + s * C::TILE + lane * box_bytes, &tk, 0, feed.row, 0, feed.kvh, feed.page,
-                             &full_k[s], pol);
+        const int box = feed.box(feed.mine);
+        if (box >= 0)
+            ptx::tma_load_5d(ring_k + s * C::TILE + box * box_bytes, &tk, 0, feed.cur.row, 0, feed.cur.kvh,
+                             feed.cur.page, &full_k[s], pol);
         ++k_out;
         return true;
     };
@@ -155,9 +156,10 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         const int s = issued % NS;
         if (lane == 0) ptx::mbar_arrive_expect_tx(&full_v[s], __popc(feed.mine) * box_bytes);
         __syncwarp();
-        if (lane < nb && ((feed.mine >> lane) & 1u))
-            ptx::tma_load_5d(ring_v + s * C::TILE + lane * box_bytes, &tv, 0, feed.row, 0, feed.kvh, feed.page,
-                             &full_v[s], pol);
+        const int box = feed.box(feed.mine);
+        if (box >= 0)
+            ptx::tma_load_5d(ring_v + s * C::TILE + box * box_bytes, &tv, 0, feed.cur.row, 0, feed.cur.kvh,
+                             feed.cur.page, &full_v[s], pol);
         ++issued;
     };
     float *mg = reinterpret_cast<float *>(smem + C::OFF_M);

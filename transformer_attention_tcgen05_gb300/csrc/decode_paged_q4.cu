@@ -21,8 +21,8 @@
 //    per token for K, one 8-byte read for V, no ldmatrix, no swizzle.
 //  * V's scale belongs to the token, so it is multiplied into the weight:
 //    w_jg = p_j s_jg is the P operand of channel group g, f16 (a rounding of 2^-12 of
-//    each weight), and one MMA per group of a matrix of -24 (16 + 8) and -264 (256
-//    + 8) takes the constants out again with the very same rounded weights.  The running
+//    each weight), and a second MMA with a matrix of -24 (16 + 8) and -264 (256 + 8)
+//    takes the constants out again with the very same rounded weights.  The running
 //    reference of the softmax is the maximum of x_j + log2 max_g |s_jg|, which keeps
 //    every w_jg below 1 in any cache (below 2^8: the reference moves only when it must).
 //  * The rows of a (page, head) are contiguous: a chunk of 32 tokens is one to four
@@ -125,7 +125,7 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
     int f = 0;                                         // chunk number within the range
 
     // ---- loads: NS chunks ahead of the computation
-    const int nb = p.nb, box_bytes = (1 << p.br_log) * C::ROW;
+    const int box_bytes = (1 << p.br_log) * C::ROW;
     const uint64_t pol = ptx::l2_policy_evict_first();
     uint64_t *full = bars->full + warp * 4;
     uint8_t *ring = smem + warp * NS * C::TILE;
@@ -138,16 +138,14 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
         bad_bits = (bad_bits & ~(1u << (issued & 31))) | (unsigned(feed.bad != 0) << (issued & 31));
         if (lane == 0) ptx::mbar_arrive_expect_tx(&full[slot_in], __popc(go) * box_bytes);
         __syncwarp();
-        if (lane < nb && ((go >> lane) & 1u))
-            ptx::bulk_g2s(ring + slot_in * C::TILE + lane * box_bytes,
-                          pages.base + feed.page * pages.page + feed.kvh * pages.head + feed.row * C::ROW, box_bytes,
-                          &full[slot_in], pol);
+        const int box = feed.box(go);
+        if (box >= 0)
+            ptx::bulk_g2s(ring + slot_in * C::TILE + box * box_bytes,
+                          pages.base + feed.cur.page * pages.page + feed.cur.kvh * pages.head + feed.cur.row * C::ROW,
+                          box_bytes, &full[slot_in], pol);
         ++issued;
         slot_in = slot_in + 1 == NS ? 0 : slot_in + 1;
     };
-#pragma unroll 1
-    for (int i = 0; i < NS; ++i) issue();
-
     float *mg = reinterpret_cast<float *>(smem + C::OFF_M);
     float *mml = reinterpret_cast<float *>(smem + C::OFF_ML);
     const int quad = lane >> 2, pair = lane & 3;
@@ -213,26 +211,36 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
     // after a timeout a warp computes nothing more but still walks the
     // segments: the other warps meet it at their barriers, and every unit's
     // ticket is counted up and reset as usual
-    int dead = 0, s = 0;
+    int dead = 0, s = 0, warm = 0;
     uint32_t parity = 0;
-    load_q();
     for (bool more = true; more;) {
-        float m[NT][2], l[NT][2], acc[NT][2 * NG][4], cor[NT][NG][4];
+        // m: the running reference, and what weights are taken against (0 while it is -inf)
+        float m[NT][2], mu[NT][2], l[NT][2], acc[NT][2 * NG][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = -INFINITY;
-            l[nt][0] = l[nt][1] = 0.f;
+            mu[nt][0] = mu[nt][1] = l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
             for (int i = 0; i < 2 * NG; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
-#pragma unroll
-            for (int g = 0; g < NG; ++g) cor[nt][g][0] = cor[nt][g][1] = cor[nt][g][2] = cor[nt][g][3] = 0.f;
         }
         int bad = dead;
 
         const int f_end = f + w.cnt;
-        // this warp's chunks: the range's chunk number modulo the team
+        // this warp's chunks: the range's chunk number modulo the team.  The first
+        // NS rounds of all only ask for chunks; then come the segment's queries.
+        int fc = f + ((rank - f) & (team - 1));
+        bool have_q = false;
 #pragma unroll 1
-        for (int fc = f + ((rank - f) & (team - 1)); fc < f_end && !dead; fc += team) {
+        while ((warm < NS || fc < f_end) && !dead) {
+            if (warm < NS) {
+                issue();
+                ++warm;
+                continue;
+            }
+            if (!have_q) {
+                load_q();
+                have_q = true;
+            }
             if (!__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&full[s], parity, p.err, abort))) {
                 bad = dead = 1;
                 break;
@@ -240,10 +248,6 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
             bad |= (bad_bits >> (taken & 31)) & 1u;
             const uint8_t *tile = ring + s * C::TILE;
             const int base = chunk_of(w.plan, w.v0 + (fc - f)) * kChunk;
-
-            // ---- visibility of the chunk's 32 positions
-            const unsigned vis = __ballot_sync(0xffffffffu, base + lane < w.plan.len &&
-                                               (base + lane >= w.plan.lo || base + lane < w.plan.s_end));
 
             // ---- S^T = K q^T, group by group; x in base-2 exponents
             float x[2][NT][4];
@@ -280,69 +284,65 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
                     }
                 }
             }
-            // ---- the reference of a token: the power of two of its largest scale
+            // ---- the reference of a token: the logarithm of its largest scale
             float ref[2][2];
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    float top = 0.f;
-#pragma unroll
-                    for (int g = 0; g < NG / 2; ++g)
-                        top = fmaxf(top, fmaxf(fabsf(H::lo(vs[t][r][g])), fabsf(H::hi(vs[t][r][g]))));
+                    float top = fmaxf(fabsf(H::lo(vs[t][r][0])), fabsf(H::hi(vs[t][r][0])));
+                    if constexpr (NG == 4)
+                        top = ptx::fmax3(fabsf(H::lo(vs[t][r][NG / 2 - 1])), fabsf(H::hi(vs[t][r][NG / 2 - 1])), top);
                     ref[t][r] = fmaxf(ptx::lg2(top), -60.f);
                 }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[t][nt][i] *= qs[nt][i & 1];
-            if (vis != 0xffffffffu) {                  // scales of rows that are not seen may be NaN
+            // ---- positions that are not seen: their scales may be NaN
+            if (base + kChunk > w.plan.len || (base < w.plan.lo && base + kChunk > w.plan.s_end)) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        if (!((vis >> (t * 16 + r * 8 + tok)) & 1u)) {
+                    for (int r = 0; r < 2; ++r) {
+                        const int pos = base + t * 16 + r * 8 + tok;
+                        if (pos >= w.plan.len || (pos < w.plan.lo && pos >= w.plan.s_end)) {
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) x[t][nt][2 * r] = x[t][nt][2 * r + 1] = -INFINITY;
 #pragma unroll
                             for (int g = 0; g < NG / 2; ++g) vs[t][r][g] = 0u;
                         }
+                    }
             }
             // ---- the running reference moves if a weight could pass 2^8, or is NaN
+            float mx[NT][2];
             bool far = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float mx = fmaxf(fmaxf(x[0][nt][j] + ref[0][0], x[0][nt][j + 2] + ref[0][1]),
-                                     fmaxf(x[1][nt][j] + ref[1][0], x[1][nt][j + 2] + ref[1][1]));
-                    far = far || !(mx <= m[nt][j] + 8.f) || m[nt][j] == -INFINITY;
+                    float y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        y[i] = fmaf(x[i >> 1][nt][j + (i & 1) * 2], qs[nt][j], ref[i >> 1][i & 1]);
+                    mx[nt][j] = fmaxf(ptx::fmax3(y[0], y[1], y[2]), y[3]);
+                    // (fmax leaves NaN out: a NaN score shows in its weight)
+                    far = far || !(mx[nt][j] <= m[nt][j] + 8.f) || m[nt][j] == -INFINITY;
                 }
             if (__any_sync(0xffffffffu, far)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float mx = fmaxf(fmaxf(x[0][nt][j] + ref[0][0], x[0][nt][j + 2] + ref[0][1]),
-                                         fmaxf(x[1][nt][j] + ref[1][0], x[1][nt][j + 2] + ref[1][1]));
+                        float top = mx[nt][j];
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1)
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                        const float mn = fmaxf(m[nt][j], mx);
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                        const float mn = fmaxf(m[nt][j], top);
                         const float alpha = mn == -INFINITY ? 1.f : ptx::ex2(m[nt][j] - mn);
                         m[nt][j] = mn;
+                        mu[nt][j] = mn == -INFINITY ? 0.f : mn;
                         l[nt][j] *= alpha;
 #pragma unroll
                         for (int i = 0; i < 2 * NG; ++i) {
                             acc[nt][i][j] *= alpha;
                             acc[nt][i][j + 2] *= alpha;
-                        }
-#pragma unroll
-                        for (int g = 0; g < NG; ++g) {
-                            cor[nt][g][j] *= alpha;
-                            cor[nt][g][j + 2] *= alpha;
                         }
                     }
             }
@@ -353,9 +353,8 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float e = x[t][nt][i] == -INFINITY ? 0.f : ptx::ex2(x[t][nt][i] - m[nt][i & 1]);
-                        x[t][nt][i] = e;
-                        l[nt][i & 1] += e;
+                        x[t][nt][i] = ptx::ex2(fmaf(x[t][nt][i], qs[nt][i & 1], -mu[nt][i & 1]));
+                        l[nt][i & 1] += x[t][nt][i];
                     }
             // ---- O^T += V^T P^T, a weight's scale in P
 #pragma unroll
@@ -385,7 +384,8 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
                         const uint32_t b1 = ptx::transpose8x8(pack_f16x2(x[t][nt][2] * s1, x[t][nt][3] * s1));
                         ptx::mma16816<true>(acc[nt][2 * g], a0, b0, b1);
                         ptx::mma16816<true>(acc[nt][2 * g + 1], a1, b0, b1);
-                        ptx::mma16816<true>(cor[nt][g], minus, b0, b1);
+                        ptx::mma16816<true>(acc[nt][2 * g], minus, b0, b1);
+                        ptx::mma16816<true>(acc[nt][2 * g + 1], minus, b0, b1);
                     }
                 }
             }
@@ -393,6 +393,7 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
             __syncwarp();
             issue();
             ++taken;
+            fc += team;
             s = s + 1 == NS ? 0 : s + 1;
             parity ^= s == 0;
         }
@@ -402,7 +403,6 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
         const int seg_b = w.b, seg_kvh = w.kvh, seg_v0 = w.v0, seg_cnt = w.cnt, seg_n = w.plan.n;
         const int u0 = w.flat - w.v0;                  // flat index of the unit's first chunk
         more = w.next();
-        if (more) load_q();
         T *const o_unit = static_cast<T *>(p.o) + seg_b * p.o_sb + (long long)seg_kvh * p.G * p.o_sh;
 
         // ---- the warps' (reference, sum, O) -> one per head
@@ -421,9 +421,8 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
                     *reinterpret_cast<float4 *>(row + g * 32) =
-                        make_float4(acc[nt][2 * g][j] + cor[nt][g][j], acc[nt][2 * g][j + 2] + cor[nt][g][j + 2],
-                                    acc[nt][2 * g + 1][j] + cor[nt][g][j],
-                                    acc[nt][2 * g + 1][j + 2] + cor[nt][g][j + 2]);
+                        make_float4(acc[nt][2 * g][j], acc[nt][2 * g][j + 2], acc[nt][2 * g + 1][j],
+                                    acc[nt][2 * g + 1][j + 2]);
             }
         if (alone)
             store_alone<D, C::HP, C::LDM, F16>(p, mg, mml, bad, o_unit);

@@ -430,9 +430,10 @@ struct Group {
 
 // The chunks that one warp copies, in order: a walk that runs ahead of the
 // computation.  The 32 lanes look up the pages of 32 boxes at once, one group
-// ahead.  After next(), for the boxes of the chunk: which to copy (`mine`), which
-// of them have an entry that is no page (`bad`); lane i has box i % nb's page (one
-// behind the pool for a bad one) and first row.
+// ahead, and keep them: after next(), the chunk's boxes are those of the nb lanes
+// from `first` on, which have each its page (one behind the pool where the entry is
+// no page) and row in cur, and copy their boxes themselves.  Bits from 0 on: the
+// boxes to copy (`mine`), those without a page (`bad`).
 struct Feed {
     const PgParams &p;
     Walk w;
@@ -441,11 +442,11 @@ struct Feed {
     Group cur, nxt;
     int gi;                                // chunk within cur
     unsigned mine, bad;
-    int page, row, kvh;
+    int first;
 
     __device__ __forceinline__ Feed(const PgParams &pp, const Walk &walk, const Range &r)
         : p(pp), w(walk), team(r.team), step(r.alone ? 0 : 2), next_chunk(r.rank), base(0), more(true), cur{},
-          nxt{}, gi(0), mine(0), bad(0), page(0), row(0), kvh(0), rank(r.rank) {}
+          nxt{}, gi(0), mine(0), bad(0), first(0), rank(r.rank) {}
     __device__ __forceinline__ Group lookup() {
         const int lane = threadIdx.x & 31, BR = 1 << p.br_log;
         const int sub = lane >> (5 - p.br_log), box = lane & (p.nb - 1);
@@ -497,14 +498,16 @@ struct Feed {
         }
         if (gi == cur.cnt) return false;
         const unsigned bits = (1u << p.nb) - 1u;
-        const int box = threadIdx.x & (p.nb - 1);
-        mine = (cur.needs >> (gi * p.nb)) & bits;
-        bad = (cur.bads >> (gi * p.nb)) & bits;
-        page = __shfl_sync(0xffffffffu, cur.page, gi * p.nb + box);
-        row = __shfl_sync(0xffffffffu, cur.row, gi * p.nb + box);
-        kvh = cur.kvh;
+        first = gi * p.nb;
+        mine = (cur.needs >> first) & bits;
+        bad = (cur.bads >> first) & bits;
         ++gi;
         return true;
+    }
+    // this lane's box of the chunk, if it is one to copy (`of`: mine, or some of it), else -1
+    __device__ __forceinline__ int box(unsigned of) const {
+        const unsigned i = (threadIdx.x & 31) - unsigned(first);
+        return i < 32u && ((of >> i) & 1u) ? int(i) : -1;
     }
 
   private:

@@ -2,14 +2,14 @@
 // their way into a paged cache, 16-bit / fp32 or held in 4 bits, with the reader
 // that gives a 4-bit cache's rows back.
 //
-// All of it is bound by memory: 16 or 32 bytes per thread and load, several loads
-// in flight.  A thread keeps its token and channels and walks the heads, so the
-// angles of a (token, pair) are computed once for all heads where there are
-// tokens enough to fill the GPU; a short call spreads its heads over the threads
-// of a CTA instead and computes them several times over.  A thread reads its
-// partners' channels beside its own (a second read of a line that is in L1),
-// so no row passes through shared memory, and a row may be rotated in place: the
-// lanes of one warp own it, and all of them read before any writes.
+// All of it is bound by memory: a thread owns two times eight channels of a row
+// (both halves of eight pairs, two 16-byte vectors of a 16-bit type), walks the heads
+// of its token and has the vectors of four rows in flight.  A row belongs to D / 16
+// lanes and nothing of it passes through shared memory, so it may be rotated in place.
+// The angles of a tile of tokens are computed once into shared memory while the first
+// rows arrive.  (Eight channels per thread with the partners read a second time, and
+// the angles computed by every thread for itself, executed four times the
+// instructions: 8192 x 32 rows of D 128 took 29.2 us, prompts of 23 000 tokens 193 us.)
 #include <math.h>
 
 #include "kernels.h"
@@ -39,25 +39,43 @@ attn_status_t launch(const Ctx &c, int family, void (*kern)(P...), dim3 grid, A.
     return launch_status(family);
 }
 
-// How a CTA's threads are laid over a tile: D / 8 lanes per row, 2^tb_log tokens,
+constexpr int kPerSm = 3;                              // CTAs
+constexpr int kTile = 16;                              // most tokens of a tile
+
+// How a CTA's threads are laid over a tile: 2^lane_log lanes per row, 2^tb_log tokens,
 // the rest over heads.
 struct Tile {
-    int vpr_log, tb_log;
-    __host__ __device__ int vec(int t) const { return t & ((1 << vpr_log) - 1); }
-    __host__ __device__ int token(int t) const { return (t >> vpr_log) & ((1 << tb_log) - 1); }
-    __host__ __device__ int lane(int t) const { return t >> (vpr_log + tb_log); }
-    __host__ __device__ int lanes() const { return kThreads >> (vpr_log + tb_log); }
+    int lane_log, tb_log;
+    __host__ __device__ int vec(int t) const { return t & ((1 << lane_log) - 1); }
+    __host__ __device__ int token(int t) const { return (t >> lane_log) & ((1 << tb_log) - 1); }
+    __host__ __device__ int lane(int t) const { return t >> (lane_log + tb_log); }
+    __host__ __device__ int lanes() const { return kThreads >> (lane_log + tb_log); }
     __host__ __device__ int tokens() const { return 1 << tb_log; }
+    // rows of 8 channels per lane instead of 16
+    __host__ __device__ Tile finer() const { return Tile{lane_log + 1, tb_log}; }
 };
 
 // The most tokens per CTA (fewest angles computed) that leave `want` CTAs.
 Tile make_tile(int D, long long tokens, long long want) {
     Tile t;
-    t.vpr_log = D == 128 ? 4 : D == 64 ? 3 : 2;
-    t.tb_log = 8 - t.vpr_log;
+    t.lane_log = D == 128 ? 3 : D == 64 ? 2 : 1;
+    t.tb_log = 4;
     while (t.tb_log > 0 && (tokens >> t.tb_log) < want) --t.tb_log;
     return t;
 }
+
+// The channels of a thread: [a, a + 8) and [b, b + 8), its row's pairs 8 vec .. 8 vec + 7
+// if they are rotated.
+struct Channels {
+    int a, b;
+    bool turns;
+    __device__ __forceinline__ Channels(const Rotation &r, int vec) {
+        turns = vec * 16 < r.rot;
+        const bool half = turns && !r.interleaved;
+        a = half ? vec * 8 : vec * 16;
+        b = half ? a + r.rot / 2 : a + 8;
+    }
+};
 
 // -------------------------------------------------------------------- rope
 
@@ -67,52 +85,56 @@ struct RopeRows {
     const int32_t *pos;
     long long pos_stride;                              // between batches
     TensorStrides sx, sy;
-    int H, N, D, slice;                                // slice: heads per CTA
+    int H, N, slice;                                   // slice: heads per CTA
     long long tokens;                                  // B * N
     Rotation rot;
     Tile tile;
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) rope_rows_kernel(const RopeRows p) {
+__global__ void __launch_bounds__(kThreads, kPerSm) rope_rows_kernel(const RopeRows p) {
     constexpr int U = sizeof(T) == 4 ? 2 : 4;
+    __shared__ __align__(16) float2 tab[kTile * 64];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int tid = threadIdx.x, c0 = p.tile.vec(tid) * 8, hl = p.tile.lanes();
-    const long long t = ((long long)blockIdx.x << p.tile.tb_log) + p.tile.token(tid);
-    const bool here = t < p.tokens, turns = c0 < p.rot.rot;
+    const int tid = threadIdx.x, hl = p.tile.lanes(), tl = p.tile.token(tid);
+    const Channels ch(p.rot, p.tile.vec(tid));
+    const long long t0 = (long long)blockIdx.x << p.tile.tb_log, t = t0 + tl;
+    const bool here = t < p.tokens;
     const long long b = here ? t / p.N : 0, n = here ? t % p.N : 0;
     const int h_end = imin(p.H, (blockIdx.y + 1) * p.slice);
     const T *x = static_cast<const T *>(p.x) + b * p.sx.b + n * p.sx.n;
-    T *y = static_cast<T *>(p.y) + b * p.sy.b + n * p.sy.n + c0;
-    const bool inter = p.rot.interleaved;
-    Turn tr;
-    bool ready = false;
+    T *y = static_cast<T *>(p.y) + b * p.sy.b + n * p.sy.n;
+    Row8<T> va[U], vb[U];
+    auto load = [&](int h0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (here && h0 + u * hl < h_end) {
+                const T *src = x + (h0 + u * hl) * p.sx.h;
+                va[u].load(src + ch.a);
+                vb[u].load(src + ch.b);
+            }
+    };
+    int h = blockIdx.y * p.slice + p.tile.lane(tid);
+    load(h);                                           // on the way while the angles are computed
+    fill_turns(p.rot, tab, p.tile.tokens(), [&](int i) {
+        const long long u = t0 + i < p.tokens ? t0 + i : 0;
+        return p.pos[u / p.N * p.pos_stride + u % p.N];
+    });
+    __syncthreads();
+    const int step = p.rot.rot / 16;                   // lanes that rotate
+    const float4 *turns = reinterpret_cast<const float4 *>(tab) + tl * (p.rot.rot / 4) + p.tile.vec(tid);
 #pragma unroll 1
-    for (int h0 = blockIdx.y * p.slice; h0 < h_end; h0 += U * hl) {
-        Row8<T> own[U], other[U];
-        const int h = h0 + p.tile.lane(tid);
-        if (!ready)
-            tr.partner = inter ? c0 : c0 < p.rot.rot / 2 ? c0 + p.rot.rot / 2 : c0 - p.rot.rot / 2;
+    for (; h < h_end; h += U * hl) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (here && h + u * hl < h_end) {
-                own[u].load(x + (h + u * hl) * p.sx.h + c0);
-                if (turns && !inter) other[u].load(x + (h + u * hl) * p.sx.h + tr.partner);
+                if (ch.turns) rotate16<T>(turns, step, p.rot.interleaved, va[u], vb[u]);
+                T *dst = y + (h + u * hl) * p.sy.h;
+                va[u].store(dst + ch.a);
+                vb[u].store(dst + ch.b);
             }
-        if (!ready && turns && here) make_turn(p.rot, p.pos[b * p.pos_stride + n], c0, tr);
-        ready = true;
-        __syncwarp();                                  // the row has been read by all its lanes
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (here && h + u * hl < h_end) {
-                if (turns) {
-                    float z[8];
-                    rotate8<T>(tr, own[u], other[u], inter, z);
-                    own[u].set(z);
-                }
-                own[u].store(y + (h + u * hl) * p.sy.h);
-            }
+        if (h + U * hl < h_end) load(h + U * hl);
     }
 }
 
@@ -136,19 +158,20 @@ struct AppendRows {
 
 // Where a tile's tokens go.
 struct Dest {
-    int seq[64], first[64], count[64];                 // sequence (-1: none), its first row and rows
-    int pos[64];                                       // position (-1: the request does not fit)
-    int page[64], row[64];                             // page -1: none
+    int seq[kTile], first[kTile], count[kTile];        // sequence (-1: none), its first row and rows
+    int pos[kTile];                                    // length so far or first position, then the
+                                                       // position (-1: the request does not fit)
+    int page[kTile], row[kTile];                       // page -1: none
 };
 
 // Sequence, first row and row count of the tile's tokens [t0, t0 + n), from the
-// starts cu[0..B] of the packed sequences.
-__device__ __forceinline__ void find_sequences(Dest &d, const int32_t *cu, int B, int N, int t0, int n,
-                                               unsigned *err) {
-    if (threadIdx.x < 64) d.seq[threadIdx.x] = -1;
+// starts cu[0..B] of the packed sequences, and the sequence's `base` (null: 0).
+__device__ __forceinline__ void find_sequences(Dest &d, const int32_t *cu, const int32_t *base, int B, int N, int t0,
+                                               int n, unsigned *err) {
+    if (threadIdx.x < kTile) d.seq[threadIdx.x] = -1;
     __syncthreads();
     for (int b = threadIdx.x; b < B; b += kThreads) {
-        const int lo = cu[b], hi = cu[b + 1];
+        const int lo = cu[b], hi = cu[b + 1], from = base ? base[b] : 0;
         if (lo < 0 || hi < lo || hi > N) {
             if (blockIdx.x == 0) raise_device_error(err, kDevCheck);
             continue;
@@ -157,6 +180,7 @@ __device__ __forceinline__ void find_sequences(Dest &d, const int32_t *cu, int B
             d.seq[t - t0] = b;
             d.first[t - t0] = lo;
             d.count[t - t0] = hi - lo;
+            d.pos[t - t0] = from;
         }
     }
     __syncthreads();
@@ -166,49 +190,52 @@ __device__ __forceinline__ bool append_fits(const AppendRows &p, int len, int n)
     return len >= 0 && (long long)len + n <= (long long)p.max_pages * p.S;
 }
 
+// Rows of q, and of K and V into a 16-bit or fp32 cache: D / 16 lanes each.  Rows of K
+// and V into a cache held in 4 bits: D / 8 lanes, so that 4 neighbours hold a group of
+// 32 channels; the partners of a rotated half are read a second time.
 template <typename T, bool Q4>
-__global__ void __launch_bounds__(kThreads) append_rows_kernel(const AppendRows p) {
+__global__ void __launch_bounds__(kThreads, kPerSm) append_rows_kernel(const AppendRows p) {
     constexpr int U = sizeof(T) == 4 ? 2 : 4;
     __shared__ Dest d;
+    __shared__ __align__(16) float2 tab[kTile * 64];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int tid = threadIdx.x, TB = p.tile.tokens(), hl = p.tile.lanes();
     const int t0 = blockIdx.x * TB, tl = p.tile.token(tid), t = t0 + tl;
-    const int vec = p.tile.vec(tid), c0 = vec * 8;
-    const bool in = t < p.N, turns = c0 < p.rot.rot, inter = p.rot.interleaved;
-    const int other_c = inter ? c0 : c0 < p.rot.rot / 2 ? c0 + p.rot.rot / 2 : c0 - p.rot.rot / 2;
-    const int heads = p.Hq + 2 * p.Hkv;                // of q, then K, then V
-    // the first rows are read while their places are looked up
-    Row8<T> own[U], other[U];
+    const bool in = t < p.N;
+    const Channels ch(p.rot, p.tile.vec(tid));
+    const int heads = Q4 ? p.Hq : p.Hq + 2 * p.Hkv;    // of q, then K, then V
+    // row h is at base + h stride of its tensor
+    const T *const sq = static_cast<const T *>(p.q) + t * p.q_st[0] + ch.a;
+    const T *const sk = static_cast<const T *>(p.kn) + t * p.kn_st[0] - p.Hq * p.kn_st[1] + ch.a;
+    const T *const sv = static_cast<const T *>(p.vn) + t * p.vn_st[0] - (p.Hq + p.Hkv) * p.vn_st[1] + ch.a;
+    const int apart = ch.b - ch.a;
+    Row8<T> va[U], vb[U];
     auto load = [&](int h0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int h = h0 + u * hl;
             if (!in || h >= heads) continue;
-            const T *src;
-            if (h < p.Hq)
-                src = static_cast<const T *>(p.q) + t * p.q_st[0] + h * p.q_st[1];
-            else if (h < p.Hq + p.Hkv)
-                src = static_cast<const T *>(p.kn) + t * p.kn_st[0] + (h - p.Hq) * p.kn_st[1];
-            else
-                src = static_cast<const T *>(p.vn) + t * p.vn_st[0] + (h - p.Hq - p.Hkv) * p.vn_st[1];
-            own[u].load(src + c0);
-            if (turns && !inter && h < p.Hq + p.Hkv) other[u].load(src + other_c);
+            const bool is_q = Q4 || h < p.Hq, is_k = h < p.Hq + p.Hkv;
+            const T *src = (is_q ? sq : is_k ? sk : sv) + h * (is_q ? p.q_st[1] : is_k ? p.kn_st[1] : p.vn_st[1]);
+            va[u].load(src);
+            vb[u].load(src + apart);
         }
     };
-    load(p.tile.lane(tid));
+    load(p.tile.lane(tid));                            // on the way while their places are looked up
     if (p.cu) {
-        find_sequences(d, p.cu, p.B, p.N, t0, TB, p.err);
+        find_sequences(d, p.cu, p.seq_len, p.B, p.N, t0, TB, p.err);
     } else if (tid < TB) {
         d.seq[tid] = t0 + tid < p.N ? t0 + tid : -1;
         d.first[tid] = t0 + tid;
         d.count[tid] = 1;
+        if (t0 + tid < p.N) d.pos[tid] = p.seq_len[t0 + tid];
     }
     if (tid < TB) {
         int pos = -1, page = -1, row = 0;
         const int b = d.seq[tid];
         if (b >= 0) {
-            const int len = p.seq_len[b];
+            const int len = d.pos[tid];
             if (append_fits(p, len, d.count[tid])) {
                 pos = len + t0 + tid - d.first[tid];
                 row = pos % p.S;
@@ -222,52 +249,95 @@ __global__ void __launch_bounds__(kThreads) append_rows_kernel(const AppendRows 
         d.row[tid] = row;
     }
     __syncthreads();
-    const int pos = d.pos[tl], page = d.page[tl], row = d.row[tl];
-    const bool known = in && pos >= 0, stored = in && page >= 0;
-    Turn tr;
-    if (turns && known) make_turn(p.rot, pos, c0, tr);
-    for (int h0 = 0; h0 < heads; h0 += U * hl) {
-        const int hb = h0 + p.tile.lane(tid);
-        if (h0 > 0) load(hb);
-        __syncwarp();                                  // the rows have been read by all their lanes
+    if (p.rot.rot > 0) {
+        fill_turns(p.rot, tab, TB, [&](int i) { return d.pos[i]; });
+        __syncthreads();
+    }
+    const bool known = in && d.pos[tl] >= 0;
+    const long long page = d.page[tl], row = d.row[tl];
+    const bool stored = in && page >= 0;
+    const int step = p.rot.rot / 16;                   // lanes that rotate
+    const float4 *turns = reinterpret_cast<const float4 *>(tab) + tl * (p.rot.rot / 4) + p.tile.vec(tid);
+    T *const dq = static_cast<T *>(p.qo) + t * p.qo_st[0] + ch.a;
+    T *const dk = static_cast<T *>(p.k) + page * p.k_st[0] + row * p.k_st[2] - p.Hq * p.k_st[1] + ch.a;
+    T *const dv = static_cast<T *>(p.v) + page * p.v_st[0] + row * p.v_st[2] - (p.Hq + p.Hkv) * p.v_st[1] + ch.a;
+#pragma unroll 1
+    for (int h0 = p.tile.lane(tid); h0 < heads; h0 += U * hl) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int h = hb + u * hl;
-            const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-            const int hk = is_v ? h - p.Hq - p.Hkv : h - p.Hq;
-            float z[8];
-            if (known && h < heads && turns && !is_v) {
-                rotate8<T>(tr, own[u], other[u], inter, z);
-                if (!Q4 || is_q) own[u].set(z);
-            } else if (Q4) {
-                own[u].get(z);
+            const int h = h0 + u * hl;
+            const bool is_q = Q4 || h < p.Hq, is_k = h < p.Hq + p.Hkv;
+            if (h >= heads || !(is_q ? known : stored)) continue;
+            if (ch.turns && (is_q || is_k)) rotate16<T>(turns, step, p.rot.interleaved, va[u], vb[u]);
+            T *dst = (is_q ? dq : is_k ? dk : dv) + h * (is_q ? p.qo_st[1] : is_k ? p.k_st[1] : p.v_st[1]);
+            va[u].store(dst);
+            vb[u].store(dst + apart);
+        }
+        if (h0 + U * hl < heads) load(h0 + U * hl);
+    }
+    if constexpr (Q4) {
+        const Tile fine = p.tile.finer();
+        const int vec = fine.vec(tid), c0 = vec * 8, g = vec >> 2, pl = vec & 3, fl = fine.token(tid);
+        const bool rotated = c0 < p.rot.rot, inter = p.rot.interleaved;
+        const bool upper = !inter && c0 >= p.rot.rot / 2;
+        const int other = inter ? c0 : upper ? c0 - p.rot.rot / 2 : c0 + p.rot.rot / 2;
+        // y = x c + partner s, s of either sign
+        float c[8], s[8];
+        if (rotated) {
+            const float2 *w = tab + fl * (p.rot.rot / 2);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 x = w[turn_at(p.rot.rot, inter ? (c0 + i) / 2 : (upper ? other : c0) + i)];
+                c[i] = x.x;
+                s[i] = (inter ? i & 1 : upper) ? x.y : -x.y;
             }
-            if (is_q && known && h < heads)
-                own[u].store(static_cast<T *>(p.qo) + t * p.qo_st[0] + h * p.qo_st[1] + c0);
-            if constexpr (!Q4) {
-                if (!is_q && stored && h < heads)
-                    own[u].store(static_cast<T *>(is_v ? p.v : p.k) + page * (is_v ? p.v_st[0] : p.k_st[0]) +
-                                 hk * (is_v ? p.v_st[1] : p.k_st[1]) + row * (is_v ? p.v_st[2] : p.k_st[2]) + c0);
-            } else if (__any_sync(0xffffffffu, !is_q && h < heads)) {
-                float inv;
-                const T s = q4_scale<T>(z, inv);
-                const uint32_t w = q4_codes(z, inv);
-                // V: this lane's words of two neighbouring groups, one of its own and one
-                // of the lane of the other group (which holds the same four channels)
-                const int g = vec >> 2, pl = vec & 3;
-                const uint32_t o = __shfl_xor_sync(0xffffffffu, w, 4);
-                if (!is_q && stored && h < heads) {
-                    uint8_t *to = static_cast<uint8_t *>(p.k) + page * p.k_st[0] + hk * p.k_st[1] + row * p.k_st[2];
-                    if (!is_v)
-                        *reinterpret_cast<uint32_t *>(to + pl * (p.D / 8) + 4 * g) = w;
-                    else if (g & 1)
-                        *reinterpret_cast<uint32_t *>(to + p.D / 2 + (2 * pl + 1) * (p.D / 16) + 2 * (g - 1)) =
-                            (o >> 16) | (w & 0xffff0000u);
-                    else
-                        *reinterpret_cast<uint32_t *>(to + p.D / 2 + 2 * pl * (p.D / 16) + 2 * g) =
-                            (w & 0xffffu) | (o << 16);
-                    if (pl == 0)
-                        *reinterpret_cast<T *>(to + p.D + (is_v ? p.D / 16 : 0) + 2 * g) = s;
+        }
+        const int tf = t0 + fl;
+        const long long fp = d.page[fl];
+        const bool keep = tf < p.N && fp >= 0;
+        uint8_t *to = static_cast<uint8_t *>(p.k) + (keep ? fp * p.k_st[0] + d.row[fl] * p.k_st[2] : 0);
+        const T *kn = static_cast<const T *>(p.kn) + tf * p.kn_st[0], *vn = static_cast<const T *>(p.vn) + tf * p.vn_st[0];
+        // every lane takes every step: its neighbours' values pass by shuffles
+        constexpr int V = 2;
+        for (int h0 = 0; h0 < p.Hkv; h0 += V * fine.lanes()) {
+            Row8<T> k[V], kp[V], v[V];
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                const int h = h0 + fine.lane(tid) + u * fine.lanes();
+                if (!keep || h >= p.Hkv) continue;
+                k[u].load(kn + h * p.kn_st[1] + c0);
+                if (rotated && !inter) kp[u].load(kn + h * p.kn_st[1] + other);
+                v[u].load(vn + h * p.vn_st[1] + c0);
+            }
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                const int h = h0 + fine.lane(tid) + u * fine.lanes();
+                float x[8], y[8], inv;
+                k[u].get(x);
+                if (rotated) {
+                    float z[8];
+                    if (!inter) kp[u].get(y);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) z[i] = fmaf(inter ? x[i ^ 1] : y[i], s[i], x[i] * c[i]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = z[i];
+                }
+                const T sk = q4_scale<T>(x, inv);
+                const uint32_t wk = q4_codes(x, inv);
+                v[u].get(x);
+                const T sv = q4_scale<T>(x, inv);
+                const uint32_t wv = q4_codes(x, inv);
+                // V: words of two neighbouring groups, one of this lane's own and one of the
+                // lane of the other group that holds the same channels of it
+                const uint32_t o = __shfl_xor_sync(0xffffffffu, wv, 4);
+                if (!keep || h >= p.Hkv) continue;
+                uint8_t *r = to + h * p.k_st[1];
+                *reinterpret_cast<uint32_t *>(r + pl * (p.D / 8) + 4 * g) = wk;
+                *reinterpret_cast<uint32_t *>(r + p.D / 2 + (2 * pl + (g & 1)) * (p.D / 16) + 2 * (g & ~1)) =
+                    g & 1 ? __byte_perm(o, wv, 0x7632) : __byte_perm(wv, o, 0x5410);
+                if (pl == 0) {
+                    *reinterpret_cast<T *>(r + p.D + 2 * g) = sk;
+                    *reinterpret_cast<T *>(r + p.D + p.D / 16 + 2 * g) = sv;
                 }
             }
         }
@@ -319,12 +389,12 @@ __global__ void __launch_bounds__(kThreads) gather_rows_kernel(const GatherRows 
     ptx::griddep_launch_dependents();
     const int tid = threadIdx.x, TB = p.tile.tokens(), hl = p.tile.lanes();
     const int t0 = blockIdx.x * TB, tl = p.tile.token(tid);
-    find_sequences(d, p.cu, p.B, p.N, t0, TB, p.err);
+    find_sequences(d, p.cu, p.start, p.B, p.N, t0, TB, p.err);
     if (tid < TB) {
         int page = -1, row = 0;
         const int b = d.seq[tid];
         if (b >= 0) {
-            const long long pos = (long long)(p.start ? p.start[b] : 0) + (t0 + tid - d.first[tid]);
+            const long long pos = (long long)d.pos[tid] + (t0 + tid - d.first[tid]);
             if (pos >= 0 && pos < (long long)p.max_pages * p.S) {
                 page = p.table[b * p.table_stride + int(pos) / p.S];
                 row = int(pos) % p.S;
@@ -364,15 +434,12 @@ __global__ void __launch_bounds__(kThreads) gather_rows_kernel(const GatherRows 
             // a lane of an even group has read the first four channels of both
             // groups, the lane of the odd one the last four
             const uint32_t o = __shfl_xor_sync(0xffffffffu, vw[u], 4);
-            const uint32_t w = g & 1 ? (o >> 16) | (vw[u] & 0xffff0000u) : (vw[u] & 0xffffu) | (o << 16);
+            const uint32_t w = g & 1 ? __byte_perm(o, vw[u], 0x7632) : __byte_perm(vw[u], o, 0x5410);
             if (here && h < p.Hkv) {
-                float z[8];
                 Row8<T> r;
-                q4_values(kw[u], Elem<T>::load(&ks[u]), z);
-                r.set(z);
+                r.u = q4_values<T>(kw[u], ks[u]);
                 r.store(static_cast<T *>(p.k) + (t0 + tl) * p.k_st[0] + h * p.k_st[1] + vec * 8);
-                q4_values(w, Elem<T>::load(&vs[u]), z);
-                r.set(z);
+                r.u = q4_values<T>(w, vs[u]);
                 r.store(static_cast<T *>(p.v) + (t0 + tl) * p.v_st[0] + h * p.v_st[1] + vec * 8);
             }
         }
@@ -391,14 +458,14 @@ attn_status_t rope_rows(const Ctx &c, attn_dtype_t dt, const void *x, void *y, c
     RopeRows p{};
     p.x = x; p.y = y; p.pos = pos; p.pos_stride = pos_stride;
     p.sx = sx; p.sy = sy;
-    p.H = H; p.N = N; p.D = D;
+    p.H = H; p.N = N;
     p.tokens = (long long)B * N;
     p.rot = rotation_of(rot);
     // as many tokens per CTA as the heads, cut into slices, leave CTAs enough
-    p.tile = make_tile(D, p.tokens * H, 4ll * c.sm_count);
+    p.tile = make_tile(D, p.tokens, 8ll * c.sm_count);
     const long long cols = (p.tokens + p.tile.tokens() - 1) >> p.tile.tb_log;
     int slices = 1;
-    while (slices < H && slices < 32768 && cols * slices < 8ll * c.sm_count) slices *= 2;
+    while (slices < H && slices < 32768 && cols * slices < 2ll * c.sm_count) slices *= 2;
     p.slice = cdiv(H, slices);
     if (cols > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
     const dim3 grid(unsigned(cols), unsigned(cdiv(H, p.slice)));
@@ -427,7 +494,8 @@ attn_status_t append_rows(const Ctx &c, attn_dtype_t dt, const RowsAppend &a) {
     p.S = a.S; p.P = a.P; p.max_pages = a.max_pages;
     p.advance = a.advance;
     p.rot = rotation_of(a.rot);
-    p.tile = make_tile(a.D, a.N, 2ll * c.sm_count);
+    // (a 4-bit row costs more per token than its angles do)
+    p.tile = make_tile(a.D, a.N, (a.q4 ? 2ll : 8ll) * c.sm_count);
     p.err = c.err;
     const dim3 grid(unsigned(cdiv(a.N, p.tile.tokens())));
     attn_status_t st;
@@ -456,7 +524,7 @@ attn_status_t gather_rows(const Ctx &c, attn_dtype_t dt, const RowsGather &a) {
     }
     p.B = a.B; p.N = a.N; p.Hkv = a.Hkv; p.D = a.D;
     p.S = a.S; p.P = a.P; p.max_pages = a.max_pages;
-    p.tile = make_tile(a.D, a.N, 2ll * c.sm_count);
+    p.tile = make_tile(a.D, a.N, 2ll * c.sm_count).finer();
     p.err = c.err;
     const dim3 grid(unsigned(cdiv(a.N, p.tile.tokens())));
     return dt == ATTN_F16 ? launch(c, kFamKvPages, gather_rows_kernel<__half>, grid, p)

@@ -6,8 +6,8 @@
 // position 2^31 as at 0 (an fp32 product is off by half a radian at position
 // 10^7).  What is left is the quarter turn and a rest of at most an eighth.
 //
-// Every thread owns 8 consecutive channels of a row, so a group of 32 channels
-// belongs to 4 neighbouring lanes and a row to D / 8.
+// The angles of a tile of tokens are computed once, into shared memory, whatever
+// the number of heads that turn by them.
 #pragma once
 
 #include "common.cuh"
@@ -34,34 +34,22 @@ struct Rotation {
     float mscale;
 };
 
-// What a thread needs to rotate its channels [c0, c0 + 8): y = x cs + partner sn.
-struct Turn {
-    float cs[8], sn[8];
-    int partner;                                       // first channel of the partners (interleaved: c0)
-};
+// Where (cos, sin) of a pair stands among its token's rot / 2: the pairs 8 j .. 8 j + 7
+// of neighbouring lanes j side by side, two pairs (16 bytes) at a time.
+__device__ __forceinline__ int turn_at(int rot, int pair) {
+    return (((pair & 7) >> 1) * (rot >> 4) + (pair >> 3)) * 2 + (pair & 1);
+}
 
-__device__ __forceinline__ void make_turn(const Rotation &r, int pos, int c0, Turn &t) {
-    if (r.interleaved) {
-        t.partner = c0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float c, s;
-            turn_by(pos, r.freq[c0 / 2 + i], r.mscale, c, s);
-            s = r.inverse ? -s : s;
-            t.cs[2 * i] = t.cs[2 * i + 1] = c;
-            t.sn[2 * i] = -s;
-            t.sn[2 * i + 1] = s;
-        }
-    } else {
-        const bool upper = c0 >= r.rot / 2;
-        t.partner = upper ? c0 - r.rot / 2 : c0 + r.rot / 2;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float c, s;
-            turn_by(pos, r.freq[(upper ? t.partner : c0) + i], r.mscale, c, s);
-            t.cs[i] = c;
-            t.sn[i] = upper != bool(r.inverse) ? s : -s;
-        }
+// (cos, sin) of every pair of the tile's tokens, for the positions pos(token).  All
+// threads of the CTA; a barrier must follow.
+template <typename F>
+__device__ __forceinline__ void fill_turns(const Rotation &r, float2 *tab, int tokens, F pos) {
+    const int pairs = r.rot / 2;
+    for (int e = threadIdx.x; e < tokens * pairs; e += blockDim.x) {
+        const int t = e / pairs, pair = e - t * pairs;
+        float c, s;
+        turn_by(pos(t), r.freq[pair], r.mscale, c, s);
+        tab[t * pairs + turn_at(r.rot, pair)] = make_float2(c, r.inverse ? -s : s);
     }
 }
 
@@ -106,16 +94,38 @@ template <bool F16> struct Row8H {
 template <> struct Row8<__nv_bfloat16> : Row8H<false> {};
 template <> struct Row8<__half> : Row8H<true> {};
 
-// The rotated channels in fp32 (x: the thread's own, y: its partners').
+// Two times eight channels: eight pairs, (a_i, b_i) or interleaved (a_2i, a_2i+1) and
+// (b_2i, b_2i+1).  tab: the lane's first (cos, sin), `step` float4s from one two to the
+// next.
 template <typename T>
-__device__ __forceinline__ void rotate8(const Turn &t, const Row8<T> &x, const Row8<T> &y, bool interleaved,
-                                        float (&out)[8]) {
-    float a[8], b[8];
-    x.get(a);
-    y.get(b);
+__device__ __forceinline__ void rotate16(const float4 *tab, int step, bool interleaved, Row8<T> &a, Row8<T> &b) {
+    float x[8], y[8];
+    a.get(x);
+    b.get(y);
+    auto turn = [](float &u, float &v, float c, float s) {
+        const float u0 = u;
+        u = fmaf(-v, s, u0 * c);
+        v = fmaf(u0, s, v * c);
+    };
+    if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        out[i] = fmaf(interleaved ? a[i ^ 1] : b[i], t.sn[i], a[i] * t.cs[i]);
+        for (int i = 0; i < 2; ++i) {
+            const float4 p = tab[i * step], q = tab[(i + 2) * step];
+            turn(x[4 * i], x[4 * i + 1], p.x, p.y);
+            turn(x[4 * i + 2], x[4 * i + 3], p.z, p.w);
+            turn(y[4 * i], y[4 * i + 1], q.x, q.y);
+            turn(y[4 * i + 2], y[4 * i + 3], q.z, q.w);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 p = tab[i * step];
+            turn(x[2 * i], y[2 * i], p.x, p.y);
+            turn(x[2 * i + 1], y[2 * i + 1], p.z, p.w);
+        }
+    }
+    a.set(x);
+    b.set(y);
 }
 
 // ------------------------------------------------------- rows held in 4 bits
@@ -165,22 +175,65 @@ __device__ __forceinline__ T q4_scale(const float (&x)[8], float &inv) {
     return s;
 }
 
-// The two 16-bit words of 8 channels' codes, the first in the low half.
+// Pairs of the 16-bit types.
+template <typename T> struct H16F;
+template <> struct H16F<__half> {
+    static constexpr bool f16 = true;
+    static __device__ __forceinline__ uint32_t minus24(uint32_t x) {
+        const __half2 r = __hsub2(*reinterpret_cast<__half2 *>(&x), __floats2half2_rn(24.f, 24.f));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+    static __device__ __forceinline__ uint32_t mul(uint32_t x, __half s) {
+        const __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&x), __half2half2(s));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+};
+template <> struct H16F<__nv_bfloat16> {
+    static constexpr bool f16 = false;
+    static __device__ __forceinline__ uint32_t minus24(uint32_t x) {
+        const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&x), __floats2bfloat162_rn(24.f, 24.f));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+    static __device__ __forceinline__ uint32_t mul(uint32_t x, __nv_bfloat16 s) {
+        const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&x), __bfloat162bfloat162(s));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+};
+
+// The two 16-bit words of 8 channels' codes, the first in the low half.  1.5 2^23 + 8
+// is added so that rint(x inv) + 8 stands in the sum's last bits.
 __device__ __forceinline__ uint32_t q4_codes(const float (&x)[8], float inv) {
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int n = int(fminf(fmaxf(rintf(x[i] * inv) + 8.f, 0.f), 15.f));
-        w |= uint32_t(n) << (4 * i);
+        const float n = fminf(fmaxf(x[i] * inv, -8.f), 7.f);       // NaN: -8
+        w += __float_as_uint(n + 12582920.f) << (4 * i);
     }
+    w -= 0x4b400000u * 0x11111111u;
     return ((w >> 2) & 0x3fff3fffu) | ((w << 14) & 0xc000c000u);
 }
 
-// The values of 8 codes.
-__device__ __forceinline__ void q4_values(uint32_t w, float s, float (&x)[8]) {
-    w = ((w << 2) & 0xfffcfffcu) | ((w >> 14) & 0x00030003u);
+// The values of 8 codes in the 16-bit type: n - 8 is exact in either, so one product
+// rounds once.
+template <typename T>
+__device__ __forceinline__ uint4 q4_values(uint32_t w, T scale) {
+    const uint32_t y = __byte_perm(w, 0, 0x2301);
+    uint32_t c[4];                                     // channels (i, i + 4) as 16 + n
+    if constexpr (H16F<T>::f16) {
+        c[0] = (y & 0x03c003c0u) | 0x4c004c00u;
+        c[1] = ((w << 4) & 0x03c003c0u) | 0x4c004c00u;
+        c[2] = (w & 0x03c003c0u) | 0x4c004c00u;
+        c[3] = ((y << 4) & 0x03c003c0u) | 0x4c004c00u;
+    } else {
+        c[0] = ((y >> 3) & 0x00780078u) | 0x41804180u;
+        c[1] = ((w << 1) & 0x00780078u) | 0x41804180u;
+        c[2] = ((w >> 3) & 0x00780078u) | 0x41804180u;
+        c[3] = ((y << 1) & 0x00780078u) | 0x41804180u;
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = float(int((w >> (4 * i)) & 15u) - 8) * s;
+    for (int i = 0; i < 4; ++i) c[i] = H16F<T>::mul(H16F<T>::minus24(c[i]), scale);
+    return make_uint4(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410),
+                      __byte_perm(c[0], c[1], 0x7632), __byte_perm(c[2], c[3], 0x7632));
 }
 
 }  // namespace attn
