@@ -389,10 +389,10 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
                 }
             }
         if (alone) {
-            store_alone<D, C::HP, C::LDM, F16>(p, mg, mml, bad, o_unit);
+            store_alone<D, C::HP, C::LDM, 1, F16>(p, mg, mml, bad, o_unit);
             continue;
         }
-        join_segment<D, CW, C::HP, C::LDM, F16>(p, ms, mg, mml, range, seg_b * p.Hkv + seg_kvh, seg_v0, seg_cnt,
+        join_segment<D, CW, C::HP, C::LDM, 1, F16>(p, ms, mg, mml, range, seg_b * p.Hkv + seg_kvh, seg_v0, seg_cnt,
                                                 seg_n, u0, bad, o_unit);
     }
     // after a timeout: let the copies this warp asked for land (bounded) before

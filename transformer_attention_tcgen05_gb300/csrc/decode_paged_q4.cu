@@ -44,8 +44,8 @@ constexpr int kMaxSms = 192;               // workspace slots
 template <int D, int NT>
 struct Q4Cfg {
     static constexpr int CW = 4;                            // warps
-    static constexpr int PER_SM = NT == 1 ? 3 : 2;          // CTAs
-    static constexpr int NS = D == 64 ? 4 : 3;              // chunks in flight per warp
+    static constexpr int PER_SM = 3;                        // CTAs (168 registers per thread)
+    static constexpr int NS = D == 64 ? 4 : 2;              // chunks in flight per warp
     static constexpr int THREADS = CW * 32;
     static constexpr int HP = NT * 8;                       // padded heads per KV head
     static constexpr int NG = D / 32;                       // groups of channels with a scale each
@@ -54,23 +54,48 @@ struct Q4Cfg {
     static constexpr int LDM = D + 4;                       // floats per merge row (bank spread)
     static constexpr int MERGE = CW * HP * LDM * 4;
     static constexpr int ML = CW * HP * 2 * 4;
-    static constexpr int MISC = 512;
+    static constexpr int MISC = 2560;
     static constexpr int OFF_M = CW * NS * TILE;
     static constexpr int OFF_ML = OFF_M + MERGE;
     static constexpr int OFF_MISC = OFF_ML + ML;
-    static constexpr int SMEM = OFF_MISC + MISC + 128;
+    static constexpr int OFF_ZERO = OFF_MISC + MISC;        // SPLIT: zeros in the place of queries
+    static constexpr int SMEM = OFF_ZERO + NG * 512 + 128;
+    static_assert(NT * NG * 32 * 24 <= HP * LDM * 4, "the queries must fit a warp's merge rows");
     static_assert(PER_SM * (SMEM + 1024) <= 228 * 1024, "the CTAs of an SM must fit its shared memory");
+};
+
+// What a warp keeps of its range apart from the chunk it computes: where the loads
+// are, where the computation is (both change once in many chunks), and the visible
+// positions of the chunks asked for.
+struct WarpRange {
+    WalkState feed, work;
+    int feed_next, feed_base, feed_more;   // the next chunk within feed's segment, its start in the range
+    int work_f;                            // start of work's segment in the range
+    uint32_t seen[64];                     // of chunk i at i % 64: a bit per position; 0: it has a bad page
 };
 
 struct MiscQ4 {
     uint64_t full[kMaxWarps * 4];          // [warp][slot]
+    WarpRange warp[kMaxWarps];
     Schedule sched;
 };
-static_assert(sizeof(MiscQ4) <= 512, "barrier block must fit its reserved bytes");
+static_assert(sizeof(MiscQ4) <= 2560, "barrier block must fit its reserved bytes");
 
-// Fields of two 16-bit words as f16 pairs: bits 6-9 as 16 + n, bits 2-5 as 256 + n.
-__device__ __forceinline__ uint32_t code16(uint32_t w) { return (w & 0x03c003c0u) | 0x4c004c00u; }
-__device__ __forceinline__ uint32_t code256(uint32_t w) { return (w & 0x003c003cu) | 0x5c005c00u; }
+// The visible positions of the 32 from `base` on.
+__device__ __forceinline__ uint32_t seen_bits(const Plan &r, int base) {
+    auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+    return below(r.len - base) & (~below(r.lo - base) | below(r.s_end - base));
+}
+
+// Fields of two 16-bit words as f16 pairs: bits 6-9 as 16 + n, bits 2-5 as 256 + n;
+// one instruction each.
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(x), "r"(mask), "r"(bits));
+    return d;
+}
+__device__ __forceinline__ uint32_t code16(uint32_t w) { return and_or(w, 0x03c003c0u, 0x4c004c00u); }
+__device__ __forceinline__ uint32_t code256(uint32_t w) { return and_or(w, 0x003c003cu, 0x5c005c00u); }
 constexpr uint32_t kMinus24 = 0xce00ce00u, kMinus264 = 0xdc20dc20u;   // f16 pairs
 
 // N 32-bit words of shared memory (the widest load that fits)
@@ -91,13 +116,19 @@ struct PagesQ4 {
     long long page, head;                  // byte strides
 };
 
-template <int D, int NT, bool F16>
+// SPLIT (up to 4 heads per KV head): the 8 columns are the heads of the first 16
+// tokens of a chunk and, again, of the other 16.  The queries of the columns that a
+// token is not for are zeros, so that one accumulator fragment holds all 32 tokens and
+// a lane has the scores, scales and weights of 4 instead of 8 pairs of token and head.
+template <int D, int NT, bool SPLIT, bool F16>
 __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::PER_SM)
 decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
     using C = Q4Cfg<D, NT>;
     using H = H16<F16>;
     using T = typename H::T;
+    static_assert(!SPLIT || NT == 1, "two halves of 8 columns");
     constexpr int CW = C::CW, NS = C::NS, NG = C::NG;
+    constexpr int TT = SPLIT ? 1 : 2;                  // blocks of 16 tokens that a lane has weights of
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((128 - (ptx::smem_addr(smem_raw) & 127)) & 127);
     MiscQ4 *bars = reinterpret_cast<MiscQ4 *>(smem + C::OFF_MISC);
@@ -111,6 +142,9 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
         ptx::fence_barrier_init();
         ms->abort = 0;
     }
+    if constexpr (SPLIT)
+        for (int i = threadIdx.x; i < NG * 32; i += C::THREADS)
+            reinterpret_cast<uint4 *>(smem + C::OFF_ZERO)[i] = make_uint4(0u, 0u, 0u, 0u);
     // programmatic dependent launch: nothing global is read or written before
     // the previous kernel (an append, say) has completed
     ptx::griddep_wait();
@@ -120,51 +154,115 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
     if (!find_range<D, CW, T>(p, ms, range)) return;
     const bool alone = range.alone;
     const int team = range.team, rank = range.rank, at = range.at;
-    Walk w(p, range.list, ms->start_b[at], ms->start_len[at], ms->start_kvh[at], ms->start_v[at], range.start,
-           range.count);
-    int f = 0;                                         // chunk number within the range
+    WarpRange *mine = &bars->warp[warp];
+    {
+        const Walk w(p, range.list, ms->start_b[at], ms->start_len[at], ms->start_kvh[at], ms->start_v[at],
+                     range.start, range.count);
+        if (lane == 0) {
+            mine->feed = mine->work = w;
+            mine->feed_next = rank;
+            mine->feed_base = mine->work_f = 0;
+            mine->feed_more = 1;
+        }
+        __syncwarp();
+    }
 
-    // ---- loads: NS chunks ahead of the computation
-    const int box_bytes = (1 << p.br_log) * C::ROW;
+    // ---- loads: NS chunks ahead of the computation.  The lanes look up the pages of
+    //      32 boxes (of up to 32 chunks of one segment) at once and keep their own box
+    const int step = alone ? 0 : 2;                    // log2 of the team
     const uint64_t pol = ptx::l2_policy_evict_first();
     uint64_t *full = bars->full + warp * 4;
     uint8_t *ring = smem + warp * NS * C::TILE;
-    Feed feed(p, w, range);
     int issued = 0, taken = 0, slot_in = 0;            // this warp's chunks: asked for, computed; issued % NS
-    unsigned bad_bits = 0;                             // bit i % 32: chunk i has a bad page
-    auto issue = [&]() {
-        if (!feed.next()) return;
-        const unsigned go = feed.mine & ~feed.bad;
-        bad_bits = (bad_bits & ~(1u << (issued & 31))) | (unsigned(feed.bad != 0) << (issued & 31));
-        if (lane == 0) ptx::mbar_arrive_expect_tx(&full[slot_in], __popc(go) * box_bytes);
+    int left = 0;                                      // chunks of the group not asked for yet
+    int first = 0;                                     // lane of the next one's first box
+    const uint8_t *src = nullptr;                      // this lane's box; null: none
+    int bytes = 0;                                     // of its chunk's boxes
+    auto lookup = [&]() {
+        Walk w(p, mine->feed);
+        int next = mine->feed_next, base = mine->feed_base;
+        bool more = mine->feed_more != 0;
+        while (more && next >= w.cnt) {                // no (more) chunk of this warp in the segment
+            base += w.cnt;
+            more = w.next();
+            next = (rank - base) & (team - 1);
+        }
+        left = first = 0;
+        if (more) {
+            const int BR = 1 << p.br_log, sub = lane >> (5 - p.br_log), box = lane & (p.nb - 1);
+            left = imin(BR, (w.cnt - next + team - 1) >> step);   // 32 / nb = BR chunks at most
+            const int at = chunk_of(w.plan, w.v0 + next + sub * team) * kChunk, pos = at + box * BR;
+            // a box without a visible position is not read: its page may not
+            // exist (past the end) or may be free again
+            const bool need = sub < left && pos < w.plan.len && (pos + BR > w.plan.lo || pos < w.plan.s_end);
+            int page = 0, row = 0;
+            if (need) {
+                const int e = div_s(p, pos);
+                page = p.table[(long long)w.b * p.table_stride + e];
+                row = pos - e * p.S;
+            }
+            const bool wrong = page < 0 || page >= p.num_pages;
+            if (wrong) raise_device_error(p.err, kDevCheck);
+            const unsigned bits = (1u << p.nb) - 1u, chunk0 = lane & ~(p.nb - 1);
+            const unsigned bad = (__ballot_sync(0xffffffffu, wrong) >> chunk0) & bits;
+            const unsigned go = (__ballot_sync(0xffffffffu, need && !wrong) >> chunk0) & bits;
+            if (sub < left && box == 0) mine->seen[(issued + sub) & 63] = bad ? 0u : seen_bits(w.plan, at);
+            bytes = __popc(go) * (C::ROW << p.br_log);
+            src = need && !wrong ? pages.base + page * pages.page + w.kvh * pages.head + row * C::ROW : nullptr;
+            next += left * team;
+        }
         __syncwarp();
-        const int box = feed.box(go);
-        if (box >= 0)
-            ptx::bulk_g2s(ring + slot_in * C::TILE + box * box_bytes,
-                          pages.base + feed.cur.page * pages.page + feed.cur.kvh * pages.head + feed.cur.row * C::ROW,
-                          box_bytes, &full[slot_in], pol);
+        if (lane == 0) {
+            mine->feed = w;
+            mine->feed_next = next;
+            mine->feed_base = base;
+            mine->feed_more = more;
+        }
+        __syncwarp();
+    };
+    auto issue = [&]() {
+        if (left == 0) lookup();
+        if (left == 0) return;
+        const unsigned box = lane - first;
+        if (box == 0) ptx::mbar_arrive_expect_tx(&full[slot_in], bytes);
+        __syncwarp();
+        if (box < unsigned(p.nb) && src)
+            ptx::bulk_g2s(ring + slot_in * C::TILE + box * (C::ROW << p.br_log), src, C::ROW << p.br_log,
+                          &full[slot_in], pol);
+        --left;
+        first += p.nb;
         ++issued;
         slot_in = slot_in + 1 == NS ? 0 : slot_in + 1;
     };
+
     float *mg = reinterpret_cast<float *>(smem + C::OFF_M);
     float *mml = reinterpret_cast<float *>(smem + C::OFF_ML);
     const int quad = lane >> 2, pair = lane & 3;
 
-    // q of the unit's heads as MMA B operands (heads are columns), the constants of
-    // the codes times q per group, and what turns sums into base-2 exponents
-    uint32_t qf[NT][NG][4];
-    float qb[NT][NG][2], qs[NT][2];
+    // q of the unit's heads as MMA B operands (heads are columns) and the constants of
+    // the codes times q per group, which wait in the warp's merge rows (they are read
+    // again for every chunk: a register more per thread is a warp less per SM); and
+    // what turns sums into base-2 exponents
+    float qs[NT][2];
+    uint4 *const qf = reinterpret_cast<uint4 *>(mg + warp * C::HP * C::LDM) + lane;              // [nt][g][lane]
+    float2 *const qb = reinterpret_cast<float2 *>(mg + warp * C::HP * C::LDM + NT * NG * 128) + lane;
+    // what the lane multiplies the first 16 tokens by, and the others
+    const uint4 *const zero = reinterpret_cast<const uint4 *>(smem + C::OFF_ZERO);
+    const uint4 *const q0 = SPLIT && quad >= 4 ? zero : qf, *const q1 = SPLIT && quad < 4 ? zero : qf;
+    const uint32_t keep0 = quad < 4 ? 0xffffffffu : 0u, keep1 = ~keep0;
+    const int own = SPLIT ? (pair >> 1) * 16 : 0;      // the lane's tokens of a chunk: block (t * 16 + own)
     auto load_q = [&]() {
+        const int b = mine->work.b, kvh = mine->work.kvh;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int h = nt * 8 + quad;
-            const T *qp = static_cast<const T *>(p.q) + w.b * p.q_sb + (long long)(w.kvh * p.G + h) * p.q_sh + pair * 8;
-            uint4 u[NG];
+            const int h = SPLIT ? quad & 3 : nt * 8 + quad;
+            const T *qp = static_cast<const T *>(p.q) + b * p.q_sb + (long long)(kvh * p.G + h) * p.q_sh + pair * 8;
+            uint4 raw[NG];
             float top = 0.f;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                u[g] = h < p.G ? *reinterpret_cast<const uint4 *>(qp + g * 32) : make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t v[4] = {u[g].x, u[g].y, u[g].z, u[g].w};
+                raw[g] = h < p.G ? *reinterpret_cast<const uint4 *>(qp + g * 32) : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t v[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(H::lo(v[i])), fabsf(H::hi(v[i]))));
             }
@@ -176,30 +274,32 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
             float sum[NG];
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                const uint32_t v[4] = {u[g].x, u[g].y, u[g].z, u[g].w};
+                const uint32_t v[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
                 float x[8];
+                uint32_t u[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     x[2 * i] = H::lo(v[i]) * up;
                     x[2 * i + 1] = H::hi(v[i]) * up;
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) qf[nt][g][i] = pack_f16x2(x[i], x[i + 4]);
+                for (int i = 0; i < 4; ++i) u[i] = pack_f16x2(x[i], x[i + 4]);
+                qf[(nt * NG + g) * 32] = make_uint4(u[0], u[1], u[2], u[3]);
                 sum[g] = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    sum[g] = fmaf(i & 1 ? -264.f : -24.f, f16_lo(qf[nt][g][i]) + f16_hi(qf[nt][g][i]), sum[g]);
+                    sum[g] = fmaf(i & 1 ? -264.f : -24.f, f16_lo(u[i]) + f16_hi(u[i]), sum[g]);
 #pragma unroll
                 for (int off = 1; off < 4; off <<= 1) sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], off);
             }
             const float sc = p.c_log2 * __uint_as_float(unsigned(127 - 13 + e) << 23);
             // of the lane's two columns
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                qs[nt][j] = __shfl_sync(0xffffffffu, sc, (pair * 2 + j) * 4);
+            for (int j = 0; j < 2; ++j) qs[nt][j] = __shfl_sync(0xffffffffu, sc, (pair * 2 + j) * 4);
 #pragma unroll
-                for (int g = 0; g < NG; ++g) qb[nt][g][j] = __shfl_sync(0xffffffffu, sum[g], (pair * 2 + j) * 4);
-            }
+            for (int g = 0; g < NG; ++g)
+                qb[(nt * NG + g) * 32] = make_float2(__shfl_sync(0xffffffffu, sum[g], pair * 8),
+                                                     __shfl_sync(0xffffffffu, sum[g], pair * 8 + 4));
         }
     };
     // a lane's row of a block of 8 tokens in K and its two rows in V: with these the
@@ -225,13 +325,12 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
         }
         int bad = dead;
 
-        const int f_end = f + w.cnt;
-        // this warp's chunks: the range's chunk number modulo the team.  The first
-        // NS rounds of all only ask for chunks; then come the segment's queries.
-        int fc = f + ((rank - f) & (team - 1));
+        // this warp's chunks of the segment: the range's chunk number modulo the team.
+        // The first NS rounds of all only ask for chunks; then come the segment's queries.
+        int todo = (mine->work.cnt - ((rank - mine->work_f) & (team - 1)) + team - 1) >> step;
         bool have_q = false;
 #pragma unroll 1
-        while ((warm < NS || fc < f_end) && !dead) {
+        while ((warm < NS || todo > 0) && !dead) {
             if (warm < NS) {
                 issue();
                 ++warm;
@@ -245,49 +344,68 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
                 bad = dead = 1;
                 break;
             }
-            bad |= (bad_bits >> (taken & 31)) & 1u;
+            const uint32_t seen = mine->seen[taken & 63];
             const uint8_t *tile = ring + s * C::TILE;
-            const int base = chunk_of(w.plan, w.v0 + (fc - f)) * kChunk;
 
             // ---- S^T = K q^T, group by group; x in base-2 exponents
-            float x[2][NT][4];
-            uint32_t vs[2][2][NG / 2];                 // V's scales of the lane's four tokens
+            float x[TT][NT][4];
+            uint32_t vs[TT][2][NG / 2];                // V's scales of the lane's tokens
+            {
+                uint32_t kw[2][2][NG], ks[TT][2][NG / 2];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                uint32_t kw[2][NG], ks[2][NG / 2];
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const uint8_t *row = tile + (t * 16 + r * 8 + tok) * C::ROW;
-                    read_words<NG>(row + pair * (D / 8), kw[r]);
-                    read_words<NG / 2>(row + D, ks[r]);
-                    read_words<NG / 2>(row + D + D / 16, vs[t][r]);
-                }
+                    for (int r = 0; r < 2; ++r)
+                        read_words<NG>(tile + (t * 16 + r * 8 + tok) * C::ROW + pair * (D / 8), kw[t][r]);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) x[t][nt][0] = x[t][nt][1] = x[t][nt][2] = x[t][nt][3] = 0.f;
+                for (int t = 0; t < TT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint8_t *row = tile + (t * 16 + own + r * 8 + tok) * C::ROW;
+                        read_words<NG / 2>(row + D, ks[t][r]);
+                        read_words<NG / 2>(row + D + D / 16, vs[t][r]);
+                    }
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) x[t][nt][0] = x[t][nt][1] = x[t][nt][2] = x[t][nt][3] = 0.f;
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    const uint32_t y0 = __byte_perm(kw[0][g], 0, 0x2301), y1 = __byte_perm(kw[1][g], 0, 0x2301);
-                    const uint32_t a0[4] = {code16(y0), code16(y1), code256(kw[0][g]), code256(kw[1][g])};
-                    const uint32_t a1[4] = {code16(kw[0][g]), code16(kw[1][g]), code256(y0), code256(y1)};
-                    const float s0 = g & 1 ? H::hi(ks[0][g / 2]) : H::lo(ks[0][g / 2]);
-                    const float s1 = g & 1 ? H::hi(ks[1][g / 2]) : H::lo(ks[1][g / 2]);
+                    uint32_t a0[2][4], a1[2][4];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const uint32_t w0 = kw[t][0][g], w1 = kw[t][1][g];
+                        const uint32_t y0 = __byte_perm(w0, 0, 0x2301), y1 = __byte_perm(w1, 0, 0x2301);
+                        a0[t][0] = code16(y0); a0[t][1] = code16(y1); a0[t][2] = code256(w0); a0[t][3] = code256(w1);
+                        a1[t][0] = code16(w0); a1[t][1] = code16(w1); a1[t][2] = code256(y0); a1[t][3] = code256(y1);
+                    }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float c[4];
-                        ptx::mma16816_f16(c, a0, qf[nt][g][0], qf[nt][g][1], qb[nt][g][0], qb[nt][g][1], qb[nt][g][0],
-                                          qb[nt][g][1]);
-                        ptx::mma16816<true>(c, a1, qf[nt][g][2], qf[nt][g][3]);
-                        x[t][nt][0] = fmaf(s0, c[0], x[t][nt][0]);
-                        x[t][nt][1] = fmaf(s0, c[1], x[t][nt][1]);
-                        x[t][nt][2] = fmaf(s1, c[2], x[t][nt][2]);
-                        x[t][nt][3] = fmaf(s1, c[3], x[t][nt][3]);
+                        const uint4 u0 = q0[(nt * NG + g) * 32], u1 = SPLIT ? q1[(nt * NG + g) * 32] : u0;
+                        const float2 qc = qb[(nt * NG + g) * 32];
+                        float c[TT][4];
+                        ptx::mma16816_f16(c[0], a0[0], u0.x, u0.y, qc.x, qc.y, qc.x, qc.y);
+                        ptx::mma16816<true>(c[0], a1[0], u0.z, u0.w);
+                        if constexpr (SPLIT)
+                            ptx::mma16816<true>(c[0], a0[1], u1.x, u1.y);
+                        else
+                            ptx::mma16816_f16(c[TT - 1], a0[1], u1.x, u1.y, qc.x, qc.y, qc.x, qc.y);
+                        ptx::mma16816<true>(c[TT - 1], a1[1], u1.z, u1.w);
+#pragma unroll
+                        for (int t = 0; t < TT; ++t)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                const float sc = g & 1 ? H::hi(ks[t][r][g / 2]) : H::lo(ks[t][r][g / 2]);
+                                x[t][nt][2 * r] = fmaf(sc, c[t][2 * r], x[t][nt][2 * r]);
+                                x[t][nt][2 * r + 1] = fmaf(sc, c[t][2 * r + 1], x[t][nt][2 * r + 1]);
+                            }
                     }
                 }
             }
             // ---- the reference of a token: the logarithm of its largest scale
-            float ref[2][2];
+            float ref[TT][2];
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < TT; ++t)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     float top = fmaxf(fabsf(H::lo(vs[t][r][0])), fabsf(H::hi(vs[t][r][0])));
@@ -296,19 +414,18 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
                     ref[t][r] = fmaxf(ptx::lg2(top), -60.f);
                 }
             // ---- positions that are not seen: their scales may be NaN
-            if (base + kChunk > w.plan.len || (base < w.plan.lo && base + kChunk > w.plan.s_end)) {
+            if (seen != 0xffffffffu) {
+                if (seen == 0u) bad = 1;
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < TT; ++t)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int pos = base + t * 16 + r * 8 + tok;
-                        if (pos >= w.plan.len || (pos < w.plan.lo && pos >= w.plan.s_end)) {
+                    for (int r = 0; r < 2; ++r)
+                        if (!((seen >> (t * 16 + own + r * 8 + tok)) & 1u)) {
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) x[t][nt][2 * r] = x[t][nt][2 * r + 1] = -INFINITY;
 #pragma unroll
                             for (int g = 0; g < NG / 2; ++g) vs[t][r][g] = 0u;
                         }
-                    }
             }
             // ---- the running reference moves if a weight could pass 2^8, or is NaN
             float mx[NT][2];
@@ -317,11 +434,11 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float y[4];
+                    mx[nt][j] = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        y[i] = fmaf(x[i >> 1][nt][j + (i & 1) * 2], qs[nt][j], ref[i >> 1][i & 1]);
-                    mx[nt][j] = fmaxf(ptx::fmax3(y[0], y[1], y[2]), y[3]);
+                    for (int t = 0; t < TT; ++t)
+                        mx[nt][j] = ptx::fmax3(mx[nt][j], fmaf(x[t][nt][j], qs[nt][j], ref[t][0]),
+                                               fmaf(x[t][nt][j + 2], qs[nt][j], ref[t][1]));
                     // (fmax leaves NaN out: a NaN score shows in its weight)
                     far = far || !(mx[nt][j] <= m[nt][j] + 8.f) || m[nt][j] == -INFINITY;
                 }
@@ -350,22 +467,39 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < TT; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         x[t][nt][i] = ptx::ex2(fmaf(x[t][nt][i], qs[nt][i & 1], -mu[nt][i & 1]));
                         l[nt][i & 1] += x[t][nt][i];
                     }
             // ---- O^T += V^T P^T, a weight's scale in P
+            const uint32_t minus[4] = {kMinus24, kMinus264, kMinus24, kMinus264};
+            uint32_t ph[NT][NG][2];                    // of one block (SPLIT: both, side by side)
+            auto weigh = [&](int t) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const float s0 = g & 1 ? H::hi(vs[t][0][g / 2]) : H::lo(vs[t][0][g / 2]);
+                    const float s1 = g & 1 ? H::hi(vs[t][1][g / 2]) : H::lo(vs[t][1][g / 2]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        ph[nt][g][0] = ptx::transpose8x8(pack_f16x2(x[t][nt][0] * s0, x[t][nt][1] * s0));
+                        ph[nt][g][1] = ptx::transpose8x8(pack_f16x2(x[t][nt][2] * s1, x[t][nt][3] * s1));
+                        ptx::mma16816<true>(acc[nt][2 * g], minus, ph[nt][g][0], ph[nt][g][1]);
+                        ptx::mma16816<true>(acc[nt][2 * g + 1], minus, ph[nt][g][0], ph[nt][g][1]);
+                    }
+                }
+            };
+            if constexpr (SPLIT) weigh(0);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
+                if constexpr (!SPLIT) weigh(t < TT ? t : 0);
                 uint32_t vw[2][2][NG / 2];             // [block of 8][token of the pair]
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     read_words<NG / 2>(tile + (t * 16 + r * 8 + tv0) * C::ROW + D / 2 + quad * (D / 16), vw[r][0]);
                     read_words<NG / 2>(tile + (t * 16 + r * 8 + tv1) * C::ROW + D / 2 + quad * (D / 16), vw[r][1]);
                 }
-                const uint32_t minus[4] = {kMinus24, kMinus264, kMinus24, kMinus264};
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     uint32_t u[2], y[2];
@@ -376,16 +510,12 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
                     }
                     const uint32_t a0[4] = {code16(y[0]), code256(u[0]), code16(y[1]), code256(u[1])};
                     const uint32_t a1[4] = {code16(u[0]), code256(y[0]), code16(u[1]), code256(y[1])};
-                    const float s0 = g & 1 ? H::hi(vs[t][0][g / 2]) : H::lo(vs[t][0][g / 2]);
-                    const float s1 = g & 1 ? H::hi(vs[t][1][g / 2]) : H::lo(vs[t][1][g / 2]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const uint32_t b0 = ptx::transpose8x8(pack_f16x2(x[t][nt][0] * s0, x[t][nt][1] * s0));
-                        const uint32_t b1 = ptx::transpose8x8(pack_f16x2(x[t][nt][2] * s1, x[t][nt][3] * s1));
+                        const uint32_t keep = !SPLIT ? 0xffffffffu : t == 0 ? keep0 : keep1;
+                        const uint32_t b0 = ph[nt][g][0] & keep, b1 = ph[nt][g][1] & keep;
                         ptx::mma16816<true>(acc[nt][2 * g], a0, b0, b1);
                         ptx::mma16816<true>(acc[nt][2 * g + 1], a1, b0, b1);
-                        ptx::mma16816<true>(acc[nt][2 * g], minus, b0, b1);
-                        ptx::mma16816<true>(acc[nt][2 * g + 1], minus, b0, b1);
                     }
                 }
             }
@@ -393,17 +523,24 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
             __syncwarp();
             issue();
             ++taken;
-            fc += team;
+            --todo;
             s = s + 1 == NS ? 0 : s + 1;
             parity ^= s == 0;
         }
-        f = f_end;
-
         // this segment (the walk goes on to the next one)
-        const int seg_b = w.b, seg_kvh = w.kvh, seg_v0 = w.v0, seg_cnt = w.cnt, seg_n = w.plan.n;
-        const int u0 = w.flat - w.v0;                  // flat index of the unit's first chunk
-        more = w.next();
-        T *const o_unit = static_cast<T *>(p.o) + seg_b * p.o_sb + (long long)seg_kvh * p.G * p.o_sh;
+        const WalkState seg = mine->work;
+        const int u0 = seg.flat - seg.v0;              // flat index of the unit's first chunk
+        {
+            Walk w(p, seg);
+            more = w.next();
+            __syncwarp();
+            if (lane == 0) {
+                mine->work = w;
+                mine->work_f += seg.cnt;
+            }
+            __syncwarp();
+        }
+        T *const o_unit = static_cast<T *>(p.o) + seg.b * p.o_sb + (long long)seg.kvh * p.G * p.o_sh;
 
         // ---- the warps' (reference, sum, O) -> one per head
 #pragma unroll
@@ -425,10 +562,10 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
                                     acc[nt][2 * g + 1][j + 2]);
             }
         if (alone)
-            store_alone<D, C::HP, C::LDM, F16>(p, mg, mml, bad, o_unit);
+            store_alone<D, C::HP, C::LDM, SPLIT ? 2 : 1, F16>(p, mg, mml, bad, o_unit);
         else
-            join_segment<D, CW, C::HP, C::LDM, F16>(p, ms, mg, mml, range, seg_b * p.Hkv + seg_kvh, seg_v0, seg_cnt,
-                                                    seg_n, u0, bad, o_unit);
+            join_segment<D, CW, C::HP, C::LDM, SPLIT ? 2 : 1, F16>(p, ms, mg, mml, range, seg.b * p.Hkv + seg.kvh,
+                                                                   seg.v0, seg.cnt, seg.plan.n, u0, bad, o_unit);
     }
     // after a timeout: let the copies this warp asked for land (bounded) before
     // the CTA's shared memory is released
@@ -436,11 +573,19 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
         for (int i = taken; i < issued; ++i) ptx::mbar_wait(&full[i % NS], (i / NS) & 1, nullptr);
 }
 
-template <int D, int NT, bool F16>
+// As in the 16-bit kernel the partials come first, at their largest size (4 CTAs
+// per SM with 8 heads, or 3 with 16), so that the tickets lie at one place.
+constexpr size_t kSlots = size_t(2) * kMaxSms * 48;    // slots x heads
+constexpr size_t kPartBytes = kSlots * 128 * sizeof(float);
+constexpr size_t kMlBytes = kSlots * 2 * sizeof(float);
+static_assert(kPartBytes % 256 == 0 && kMlBytes % 256 == 0, "aligned workspace parts");
+
+template <int D, int NT, bool SPLIT, bool F16>
 attn_status_t launch_q4(const Ctx &c, const PgParams &p, const PagesQ4 &pages) {
     using C = Q4Cfg<D, NT>;
     static int done_mask = 0;
-    auto kern = decode_paged_q4_kernel<D, NT, F16>;
+    static_assert(2 * C::PER_SM * kMaxSms * C::HP <= kSlots, "the partials must fit the workspace");
+    auto kern = decode_paged_q4_kernel<D, NT, SPLIT, F16>;
     if (!ensure_smem_attr(reinterpret_cast<const void *>(kern), C::SMEM, c.device, &done_mask))
         return ATTN_ERR_RESOURCE;
     cudaLaunchConfig_t cfg = {};
@@ -460,12 +605,12 @@ attn_status_t launch_q4(const Ctx &c, const PgParams &p, const PagesQ4 &pages) {
     return launch_status(kFamDecodePaged);
 }
 
-// As in the 16-bit kernel the partials come first, at their largest size (3 CTAs
-// per SM with 8 heads, or 2 with 16), so that the tickets lie at one place.
-constexpr size_t kSlots = size_t(2) * kMaxSms * 32;    // slots x heads
-constexpr size_t kPartBytes = kSlots * 128 * sizeof(float);
-constexpr size_t kMlBytes = kSlots * 2 * sizeof(float);
-static_assert(kPartBytes % 256 == 0 && kMlBytes % 256 == 0, "aligned workspace parts");
+template <int D>
+attn_status_t launch_d(const Ctx &c, const PgParams &p, const PagesQ4 &pages, bool f16) {
+    if (p.G <= 4) return f16 ? launch_q4<D, 1, true, true>(c, p, pages) : launch_q4<D, 1, true, false>(c, p, pages);
+    if (p.G <= 8) return f16 ? launch_q4<D, 1, false, true>(c, p, pages) : launch_q4<D, 1, false, false>(c, p, pages);
+    return f16 ? launch_q4<D, 2, false, true>(c, p, pages) : launch_q4<D, 2, false, false>(c, p, pages);
+}
 
 }  // namespace
 
@@ -493,12 +638,7 @@ attn_status_t decode_paged_q4(const Ctx &c, attn_dtype_t dt, const PagedDecodeQ4
     p.tickets = reinterpret_cast<unsigned *>(w + kPartBytes + kMlBytes);
     p.err = c.err;
     const PagesQ4 pages{static_cast<const uint8_t *>(a.pages), a.p_st[0], a.p_st[1]};
-    if (a.D == 128) {
-        if (a.G <= 8) return f16 ? launch_q4<128, 1, true>(c, p, pages) : launch_q4<128, 1, false>(c, p, pages);
-        return f16 ? launch_q4<128, 2, true>(c, p, pages) : launch_q4<128, 2, false>(c, p, pages);
-    }
-    if (a.G <= 8) return f16 ? launch_q4<64, 1, true>(c, p, pages) : launch_q4<64, 1, false>(c, p, pages);
-    return f16 ? launch_q4<64, 2, true>(c, p, pages) : launch_q4<64, 2, false>(c, p, pages);
+    return a.D == 128 ? launch_d<128>(c, p, pages, f16) : launch_d<64>(c, p, pages, f16);
 }
 
 }  // namespace attn

@@ -117,8 +117,7 @@ __device__ __forceinline__ int chunk_of(const Plan &r, int v) {
 }
 
 // One CTA's range of the flat chunk list, a segment (part of one unit) at a time.
-struct Walk {
-    const PgParams &p;
+struct WalkState {
     int list;
     Plan plan;
     int b, kvh, v0, cnt;
@@ -126,9 +125,18 @@ struct Walk {
     int flat;                              // flat index of the segment's first chunk
 
     int ahead;                             // seq_len[b + 1], loaded before it is needed
+};
+struct Walk : WalkState {
+    const PgParams &p;
 
-    __device__ Walk(const PgParams &pp, int l, int b0, int len0, int kvh0, int v, int f0, int count)
-        : p(pp), list(l), b(b0), kvh(kvh0), v0(v), left(count), flat(f0) {
+    __device__ Walk(const PgParams &pp, const WalkState &s) : WalkState(s), p(pp) {}
+    __device__ Walk(const PgParams &pp, int l, int b0, int len0, int kvh0, int v, int f0, int count) : p(pp) {
+        list = l;
+        b = b0;
+        kvh = kvh0;
+        v0 = v;
+        left = count;
+        flat = f0;
         plan = make_plan(p, len0);
         ahead = b + 1 < p.B ? p.seq_len[b + 1] : 0;
         if (kvh == p.Hkv) next_sequence();
@@ -515,8 +523,8 @@ struct Feed {
 };
 
 // A whole unit in one warp's registers: through its own merge rows to 8-byte
-// stores.
-template <int D, int HP, int LDM, bool F16>
+// stores.  A head has ROWS partials per warp, HP / ROWS rows apart.
+template <int D, int HP, int LDM, int ROWS, bool F16>
 __device__ __forceinline__ void store_alone(const PgParams &p, const float *mg, const float *mml, int bad,
                                             typename H16<F16>::T *o_unit) {
     using H = H16<F16>;
@@ -524,9 +532,19 @@ __device__ __forceinline__ void store_alone(const PgParams &p, const float *mg, 
     __syncwarp();
 #pragma unroll 1
     for (int e = lane; e < p.G * (D / 4) && !bad; e += 32) {
-        const int h = e / (D / 4), d = (e % (D / 4)) * 4;
-        const float inv = 1.f / mml[(warp * HP + h) * 2 + 1];
-        const float4 x = *reinterpret_cast<const float4 *>(mg + (warp * HP + h) * LDM + d);
+        const int h = e / (D / 4), d = (e % (D / 4)) * 4, row = warp * HP + h;
+        float L = mml[row * 2 + 1];
+        float4 x = *reinterpret_cast<const float4 *>(mg + row * LDM + d);
+        if constexpr (ROWS == 2) {
+            const int row2 = row + HP / 2;
+            const float m1 = mml[row * 2], m2 = mml[row2 * 2], M = fmaxf(m1, m2);
+            const float w1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - M), w2 = m2 == -INFINITY ? 0.f : ptx::ex2(m2 - M);
+            const float l2 = mml[row2 * 2 + 1];
+            L = (m1 == -INFINITY ? L : w1 * L) + (m2 == -INFINITY ? l2 : w2 * l2);
+            const float4 y = *reinterpret_cast<const float4 *>(mg + row2 * LDM + d);
+            x = make_float4(w1 * x.x + w2 * y.x, w1 * x.y + w2 * y.y, w1 * x.z + w2 * y.z, w1 * x.w + w2 * y.w);
+        }
+        const float inv = 1.f / L;
         *reinterpret_cast<uint2 *>(o_unit + h * p.o_sh + d) =
             make_uint2(H::pack(x.x * inv, x.y * inv), H::pack(x.z * inv, x.w * inv));
     }
@@ -536,9 +554,10 @@ __device__ __forceinline__ void store_alone(const PgParams &p, const float *mg, 
 // Joins a segment's warps (their maxima and sums in mml, their sums of values in
 // the rows of mg) and, where the range cuts the unit, the segment with the
 // unit's others: chunks [v0, v0 + cnt) of a unit of n chunks whose first has the
-// flat index u0.  HP: padded heads, LDM: floats per row of mg.  All threads of
+// flat index u0.  HP: rows per warp, LDM: floats per row of mg, ROWS: partials of a
+// head per warp, HP / ROWS rows apart.  All threads of
 // the CTA; `bad`: the segment has a page that is none.
-template <int D, int CW, int HP, int LDM, bool F16>
+template <int D, int CW, int HP, int LDM, int ROWS, bool F16>
 __device__ __forceinline__ void join_segment(const PgParams &p, Schedule *ms, const float *mg, const float *mml,
                                              const Range &range, int unit, int v0, int cnt, int n, int u0,
                                              int bad, typename H16<F16>::T *o_unit) {
@@ -562,17 +581,17 @@ __device__ __forceinline__ void join_segment(const PgParams &p, Schedule *ms, co
         const int h = e / (D / 4), d = (e % (D / 4)) * 4;
         float M = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < CW; ++i) M = fmaxf(M, mml[(i * HP + h) * 2]);
+        for (int i = 0; i < CW * ROWS; ++i) M = fmaxf(M, mml[(i * (HP / ROWS) + h) * 2]);
         float L = 0.f;
         float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < CW; ++i) {
-            const float mi = mml[(i * HP + h) * 2], li = mml[(i * HP + h) * 2 + 1];
+        for (int i = 0; i < CW * ROWS; ++i) {
+            const float mi = mml[(i * (HP / ROWS) + h) * 2], li = mml[(i * (HP / ROWS) + h) * 2 + 1];
             // a warp that saw nothing, or only scores of -inf, adds nothing
             // (its sum is zero, or NaN if one of its scores was)
             const float wt = mi == -INFINITY ? 0.f : ptx::ex2(mi - M);
             L += mi == -INFINITY ? li : wt * li;
-            const float4 x = *reinterpret_cast<const float4 *>(mg + (i * HP + h) * LDM + d);
+            const float4 x = *reinterpret_cast<const float4 *>(mg + (i * (HP / ROWS) + h) * LDM + d);
             O.x += wt * x.x;
             O.y += wt * x.y;
             O.z += wt * x.z;
