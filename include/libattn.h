@@ -323,7 +323,7 @@ ATTN_API attn_status_t attn_causal_gqa_window_fwd(const void *q, const void *k, 
  *   The lengths are read on the device: Nq and Nkv are the arrays' extents, and
  *   a captured call serves any lengths within them.  bf16 and f16 run on the
  *   tensor cores for D in {64, 128}; fp32 (and the 16-bit types with D = 32) on
- *   the exact-FFMA SIMT kernel.  B <= 65535, Nq and Nkv <= 2^30.
+ *   the exact-FFMA SIMT kernel.  B <= 65535, Nq and Nkv <= 2^26.
  * Passage: fak "GPU - the in-kernel forward pass", section 3 (Llama prefill of
  * a grouped-query model), for a batch of prompts without padding.
  */

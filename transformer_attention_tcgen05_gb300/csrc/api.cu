@@ -862,7 +862,8 @@ attn_status_t attn_causal_gqa_varlen_fwd(const void *q, const void *k, const voi
     if (B < 1 || Nq < 1 || Nkv < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !valid_d(D) || !valid_dtype(dtype) ||
         sinks < 0)
         return ATTN_ERR_INVALID_ARG;
-    if (B > 65535 || Hq > 65535 || Nq > (1 << 30) || Nkv > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+    // (beyond 2^26 keys an item could outlast the limit of the waits for the next one)
+    if (B > 65535 || Hq > 65535 || Nq > (1 << 26) || Nkv > (1 << 26)) return ATTN_ERR_UNSUPPORTED;
     if (o == q || o == k || o == v) return ATTN_ERR_INVALID_ARG;
     VarlenArgs a{};
     const int64_t *const in[4] = {q_strides, k_strides, v_strides, o_strides};

@@ -61,79 +61,11 @@
 
 #include "common.cuh"
 #include "kernels.h"
-#include "packed.cuh"
 #include "ptx.cuh"
+#include "window_tiles.cuh"
 
 namespace attn {
 namespace {
-
-constexpr int kBM = 128;      // query rows per tile (MMA M)
-constexpr int kNQ = 2;        // query tiles per CTA
-constexpr int kBN = 128;      // keys per key tile (MMA N of S)
-constexpr int kFew = 32;      // keys of the tile that holds a few sinks only
-
-template <int D>
-struct WnCfg {
-    static constexpr int BN = kBN;                         // keys per key tile
-    static constexpr int PANELS = D / 64;                  // 128-byte swizzle panels
-    static constexpr int PANEL_Q = kBM * 128;              // bytes per Q panel
-    static constexpr int PANEL_KV = BN * 128;              // bytes per K/V panel
-    static constexpr int Q_BYTES = PANELS * PANEL_Q;
-    static constexpr int KV_BYTES = PANELS * PANEL_KV;     // one K (or V) stage
-    static constexpr int BUDGET = 227 * 1024 - 2048;
-    static constexpr int NS_ALL = (BUDGET - kNQ * Q_BYTES) / KV_BYTES;
-    // K and V rings of equal depth (a third K stage at D = 128 measured slower)
-    static constexpr int KS = NS_ALL / 2 > 4 ? 4 : NS_ALL / 2;               // K stages
-    static constexpr int VS = NS_ALL - NS_ALL / 2 > 4 ? 4 : NS_ALL - NS_ALL / 2;  // V stages
-    static_assert(KS >= 2 && VS >= 2, "at least two K and two V stages");
-    static constexpr int OFF_Q = 0;
-    static constexpr int OFF_K = kNQ * Q_BYTES;
-    static constexpr int OFF_V = OFF_K + KS * KV_BYTES;
-    static constexpr int OFF_BAR = OFF_V + VS * KV_BYTES;
-    static constexpr int SMEM = OFF_BAR + 512 + 1024;      // barriers + 1024 B alignment slack
-    // Tensor memory (512 columns): S_t at t BN, O_t at kNQ BN + t D; P (16-bit,
-    // two per column) over the first half of S_t (D = 128) or in columns of
-    // its own after the O's (D = 64).
-    static constexpr bool SEP_P = kNQ * (BN + D + BN / 2) <= 512;
-    static constexpr uint32_t tm_s(int t) { return t * BN; }
-    static constexpr uint32_t tm_o(int t) { return kNQ * BN + t * D; }
-    static constexpr uint32_t tm_p(int t) { return SEP_P ? kNQ * BN + kNQ * D + t * (BN / 2) : t * BN; }
-    static constexpr uint32_t TM_COLS = 512;
-    static_assert(tm_o(kNQ - 1) + D <= TM_COLS && (!SEP_P || tm_p(kNQ) <= TM_COLS),
-                  "tensor-memory layout must fit 512 columns");
-    static constexpr int NSOFT = 4 * kNQ;
-    static constexpr int W_MMA = NSOFT;                   // MMA issuer, TMEM owner
-    static constexpr int W_LOAD = NSOFT + 1;              // Q and K copies
-    static constexpr int W_LOADV = NSOFT + 2;             // V copies
-    static constexpr int W_INIT = NSOFT + 3;              // barrier set-up
-    static constexpr int NT = (NSOFT + 4) * 32;            // 3 warpgroups
-    // register split: launch 168 x 384 = 64512; 2 x 128 x 216 + 128 x 72 = 64512
-    static constexpr int REGS_LAUNCH = 168;
-    static constexpr int REGS_SOFTMAX = 216;
-    static constexpr int REGS_OTHER = 72;
-    static_assert(2 * 128 * REGS_SOFTMAX + 128 * REGS_OTHER <= NT * REGS_LAUNCH,
-                  "setmaxnreg split must fit the launch's register file share");
-    static constexpr int k_off(int s) { return OFF_K + s * KV_BYTES; }
-    static constexpr int v_off(int s) { return OFF_V + s * KV_BYTES; }
-};
-
-// Division by a number that a launch knows: n / d by a multiplication (every CTA
-// starts with three of them, and everything waits for its loaders).
-struct Div {
-    unsigned mul;
-    int sh, d;
-    Div() = default;
-    explicit Div(int n) : d(n) {
-        int l = 0;
-        while ((1ll << l) < d) ++l;
-        mul = unsigned((((1ull << l) - d) << 32) / unsigned(d) + 1);
-        sh = l - 1;
-    }
-    __device__ __forceinline__ int operator()(int n) const {
-        const unsigned t = __umulhi(mul, unsigned(n));
-        return d == 1 ? n : int((t + ((unsigned(n) - t) >> 1)) >> sh);
-    }
-};
 
 struct WnParams {
     int Nq, Nkv;             // query / key tokens per (batch, head)
@@ -145,47 +77,10 @@ struct WnParams {
     int by_head;             // a pair is two heads of one KV head (else two row tiles)
     int blocks;              // row blocks
     Div by_hp, by_h, by_group;   // pairs (or heads) per row block, heads, heads per KV head
-    PackedSeqs seqs;         // packed: the sequences' starts (Nq, Nkv, off, pairs, whole, blocks unused)
-    int sms;                 // packed: SMs
     const void *v;           // with element strides: values cleared from an edge tile
     TensorStrides sv;
     void *o;
     long long o_sb, o_sh, o_sn;
-};
-
-// a[t] for a per-query-tile array and a run-time t, by selects
-template <typename T>
-__device__ __forceinline__ T pick(const T (&a)[kNQ], int t) { return t == 0 ? a[0] : a[1]; }
-
-// One work item: a pair of query tiles, or one tile alone.  Query tile t (rows
-// q0 + t dq, head fh + t dh) works in steps [f[t], n[t]) of the item's key tile
-// list.
-struct Item {
-    int q0, fb, fh, fkh, dq, dh;
-    int n[kNQ], f[kNQ], steps;
-    int w_lo, w_sk;                // first window tile, sink tiles before it
-    bool few;                      // step 0 is the sinks' tile and holds at most kFew keys
-    int nq, nkv, off;              // the sequence's lengths, its first query's position
-    int q_row, k_row;              // packed: its rows in the arrays
-    int e0, e1, e2;                // steps of the tiles on an edge: [e0, e1), [e2, steps), a leading one
-
-    // key tile of step j: the leading tile of the first query tile (if any),
-    // the sink tiles, the window
-    __device__ __forceinline__ int tile(int j) const {
-        const int i = j - f[1];
-        return i < 0 ? w_lo : i < w_sk ? i : w_lo + j - w_sk;
-    }
-    // step j is a tile of sinks in front of every row's window
-    __device__ __forceinline__ bool sink_tile(int j) const { return j >= f[1] && j < f[1] + w_sk; }
-    // some row does not see all keys of step j's tile (sink tiles left out)
-    __device__ __forceinline__ bool edge(int j) const {
-        return j >= e2 || (j >= e0 && j < e1) || j < f[1];
-    }
-    // step j's values are looked over (packed: no tensor map ends behind a
-    // sequence's sinks)
-    template <bool PACKED> __device__ __forceinline__ bool checked(int j) const {
-        return edge(j) || (PACKED && sink_tile(j));
-    }
 };
 
 // Barrier block at OFF_BAR.
@@ -201,33 +96,7 @@ struct Bars {
     uint64_t drain, checked;       // checked: every edge tile has been looked over
     uint32_t tmem_base;
     int abort, wild;               // wild: a value was cleared from one of them
-    Item item;                     // packed: the CTA's item
 };
-
-// Completes an item of query rows q0 of one sequence: its heads are w.fh, of the
-// pair or (half >= 0) one tile of it.
-__device__ __forceinline__ void plan_item(const WnParams &p, Item &w, int half) {
-    const int pos = w.off + w.q0;
-    const bool one = w.q0 < w.nq, two = half < 0 && w.q0 + w.dq < w.nq;
-    const int ns = cdiv(p.sinks, kBN);
-    w.w_lo = imax(0, pos - p.window + 1) / kBN;
-    const int lo1 = imax(0, pos + w.dq - p.window + 1) / kBN;
-    w.w_sk = imin(ns, w.w_lo);
-    w.few = w.w_sk > 0 && p.sinks <= kFew;
-    w.f[0] = 0;
-    w.f[1] = two && lo1 > w.w_lo && w.w_lo >= ns ? 1 : 0;
-    w.few = w.few && w.f[1] == 0;
-    // (a single second row tile past the sequence's end has no step)
-    w.n[0] = one ? w.w_sk + (w.off + imin(w.q0 + kBM, w.nq) - 1) / kBN - w.w_lo + 1 : 0;
-    w.n[1] = two ? w.w_sk + (w.off + imin(w.q0 + w.dq + kBM, w.nq) - 1) / kBN - w.w_lo + 1 : 0;
-    w.steps = imax(w.n[0], w.n[1]);
-    // the window of the last query tile starts behind its first key, or the first
-    // one's diagonal comes before its last
-    const int lead = two ? pos + w.dq : pos;
-    w.e0 = w.w_sk + w.f[1];
-    w.e1 = w.w_sk + cdiv(imax(0, lead + kBM - p.window), kBN) - w.w_lo;
-    w.e2 = w.w_sk + imax(0, (pos + 1) / kBN - w.w_lo);
-}
 
 // This CTA's item: whole pairs, late queries first, then the rest as single
 // tiles.
@@ -243,160 +112,28 @@ __device__ __forceinline__ Item get_item(const WnParams &p) {
     w.fh = bh - w.fb * p.by_h.d + (half > 0 ? w.dh : 0);
     w.fkh = p.by_group(w.fh);
     w.q0 = qb * (p.by_head ? kBM : kNQ * kBM) + (half > 0 ? w.dq : 0);
-    w.nq = p.Nq;
-    w.nkv = p.Nkv;
-    w.off = p.off;
-    w.q_row = w.k_row = 0;
-    plan_item(p, w, half);
+    plan_item(w, p.off, p.Nq, p.window, p.sinks, half);
     return w;
 }
 
-// The same for packed sequences (one warp): the blocks of all sequences by falling
-// level (packed.cuh), the pairs of a last round split by the same rule.  A CTA
-// behind the last item has one without steps.
-__device__ __forceinline__ Item find_item(const WnParams &p) {
-    const BlockFinder finder(p.seqs, p.by_head ? 7 : 8, blockIdx.x == 0, p.err);
-    const int pairs = finder.total * p.by_hp.d, rest = pairs % p.sms;
-    const int whole = 2 * rest <= p.sms ? pairs - rest : pairs;
-    const int s = int(blockIdx.x) - whole;
-    const int pair = s < 0 ? int(blockIdx.x) : whole + (s >> 1), half = s < 0 ? -1 : s & 1;
-    Item w;
-    w.n[0] = w.n[1] = w.f[0] = w.f[1] = w.steps = 0;
-    w.w_lo = w.w_sk = w.e0 = w.e1 = w.e2 = 0;
-    w.few = false;
-    w.q0 = w.nq = w.nkv = w.off = w.q_row = w.k_row = 0;
-    w.fb = w.fh = w.fkh = 0;
-    w.dq = p.by_head ? 0 : kBM;
-    w.dh = p.by_head ? 1 : 0;
-    if (pair >= pairs) return w;
-    const int block = p.by_hp(pair);
-    const PackedBlock b = finder.find(block);
-    w.fh = (pair - block * p.by_hp.d) * (p.by_head ? 2 : 1) + (half > 0 ? w.dh : 0);
-    w.fkh = p.by_group(w.fh);
-    w.q0 = b.q0 + (half > 0 ? w.dq : 0);
-    w.nq = b.nq;
-    w.nkv = b.nkv;
-    w.off = b.nkv - b.nq;
-    w.q_row = b.q_row;
-    w.k_row = b.k_row;
-    plan_item(p, w, half);
-    return w;
-}
-
-// The bits of a 16-bit value that are all ones if it is infinite or NaN.
-template <bool F16> constexpr uint32_t kWild = F16 ? 0x7c00u : 0x7f80u;
-
-template <bool F16>
-__device__ __forceinline__ bool wild_pair(uint32_t w) {
-    constexpr uint32_t lo = kWild<F16>, hi = lo << 16;
-    return (w & lo) == lo || (w & hi) == hi;
-}
-
-// a + 0 x in both halves: NaN where x is infinite or NaN.
-template <bool F16>
-__device__ __forceinline__ uint32_t add_zero_times(uint32_t a, uint32_t x) {
-    uint32_t r;
-    if constexpr (F16)
-        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(a));
-    else
-        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(a));
-    return r;
-}
-
-// Clears the infinite and NaN values of a V stage; returns whether there were
-// any.  One warp; the writes are visible to the tensor cores behind the barrier
-// that follows.
+// spoil_rows for the CTA's item.
 template <int D, bool F16>
-__device__ __forceinline__ bool clear_wild(uint8_t *stage) {
-    constexpr int VECS = kBN * D / 8, U = 8;
-    constexpr uint32_t lo = kWild<F16>, hi = lo << 16;
-    uint4 *at = reinterpret_cast<uint4 *>(stage) + (threadIdx.x & 31);
-    uint32_t z[4] = {0u, 0u, 0u, 0u};
-#pragma unroll 2
-    for (int i = 0; i < VECS; i += U * 32) {
-        uint4 x[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) x[u] = at[i + u * 32];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            z[0] = add_zero_times<F16>(z[0], x[u].x);
-            z[1] = add_zero_times<F16>(z[1], x[u].y);
-            z[2] = add_zero_times<F16>(z[2], x[u].z);
-            z[3] = add_zero_times<F16>(z[3], x[u].w);
-        }
-    }
-    const bool any = ((z[0] | z[1] | z[2] | z[3]) & 0x7fff7fffu) != 0;   // 0 x is +-0
-    if (any) {
-#pragma unroll 1
-        for (int e = 0; e < VECS / 32 * 4; ++e) {
-            uint32_t *y = reinterpret_cast<uint32_t *>(at + (e >> 2) * 32) + (e & 3);
-            uint32_t w = *y;
-            if ((w & lo) == lo) w &= 0xffff0000u;
-            if ((w & hi) == hi) w &= 0x0000ffffu;
-            *y = w;
-        }
-        ptx::fence_proxy_async_smem();
-    }
-    return __any_sync(0xffffffffu, any);
-}
-
-// Adds the infinite and NaN values that were cleared from the item's edge tiles to
-// the warp's staged output rows that see them: whatever its (positive) weight,
-// such a value makes its channel of the row infinite or NaN.  Rare, so the
-// values are read again from memory, a row of V at a time.
-template <int D, bool F16, bool PACKED>
-__device__ __noinline__ void spoil_rows(const WnParams &p, const Item *packed, uint8_t *stage, int first_pos,
-                                        int rows) {
-    const Item w = PACKED ? *packed : get_item(p);   // (handed over it would live in memory)
-    using H = H16<F16>;
-    constexpr int CW = D / 64;                       // 32-bit words (two channels) per lane
-    constexpr int CH = D / 8, U = 8;
+__device__ __noinline__ void spoil_item(const WnParams &p, uint8_t *stage, int first_pos, int rows) {
+    const Item w = get_item(p);                      // (handed over it would live in memory)
     const int lane = threadIdx.x & 31;
-    const uint32_t *v = reinterpret_cast<const uint32_t *>(static_cast<const typename H::T *>(p.v) +
-                                                           w.fb * p.sv.b + w.fkh * p.sv.h +
-                                                           w.k_row * p.sv.n) + lane * CW;
-    for (int j = 0; j < w.steps; ++j) {
-        if (!w.template checked<PACKED>(j)) continue;
-        const int k0 = w.tile(j) * kBN, keys = imin(kBN, w.nkv - k0);
-        for (int i = 0; i < keys; i += U) {
-            uint32_t x[U][CW];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int c = 0; c < CW; ++c) x[u][c] = i + u < keys ? v[(k0 + i + u) * (p.sv.n / 2) + c] : 0u;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                bool here = false;
-#pragma unroll
-                for (int c = 0; c < CW; ++c) here = here || wild_pair<F16>(x[u][c]);
-                if (!__any_sync(0xffffffffu, here)) continue;
-                const int key = k0 + i + u;
-#pragma unroll 1
-                for (int r = 0; r < rows; ++r) {
-                    const int pos = first_pos + r;
-                    if (key > pos || (key <= pos - p.window && key >= p.sinks)) continue;
-                    uint32_t *y = reinterpret_cast<uint32_t *>(
-                                      stage + (r * CH + ((lane * CW / 4) ^ (r & 7))) * 16) + lane * CW % 4;
-#pragma unroll
-                    for (int c = 0; c < CW; ++c) {
-                        const float a = H::lo(x[u][c]), b = H::hi(x[u][c]);
-                        y[c] = H::pack(fabsf(a) < INFINITY ? H::lo(y[c]) : H::lo(y[c]) + a,
-                                       fabsf(b) < INFINITY ? H::hi(y[c]) : H::hi(y[c]) + b);
-                    }
-                }
-            }
-        }
-    }
-    __syncwarp();
+    constexpr int CW = D / 64, CH = D / 8;
+    auto at = [&](int r) {
+        return reinterpret_cast<uint32_t *>(stage + (r * CH + ((lane * CW / 4) ^ (r & 7))) * 16) + lane * CW % 4;
+    };
+    spoil_rows<D, F16>(w, static_cast<const typename H16<F16>::T *>(p.v) + w.fb * p.sv.b + w.fkh * p.sv.h, p.sv.n,
+                       p.Nkv, p.window, p.sinks, false, at, first_pos, rows);
 }
 
-// PACKED: q, k, v and o hold sequences of different lengths one behind the other
-// (p.seqs); a warp finds the CTA's item while the rest is set up.
-template <int D, bool F16, bool PACKED>
+template <int D, bool F16>
 __global__ void __launch_bounds__(WnCfg<D>::NT, 1)
 tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                  const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tvs,
-                 const WnParams p) {
+                 const __grid_constant__ WnParams p) {
     using C = WnCfg<D>;
     using BarsT = Bars<C::KS, C::VS>;
     static_assert(sizeof(BarsT) <= 512, "barrier block must fit its reserved bytes");
@@ -438,16 +175,8 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     if (warp == C::W_LOAD || warp == C::W_LOADV) {
         ptx::prefetch_tmap(warp == C::W_LOAD ? &tk : &tv);
         if (warp == C::W_LOAD) ptx::prefetch_tmap(&tq);
-        if constexpr (PACKED) {
-            if (warp == C::W_LOAD) {
-                ptx::griddep_wait();                   // the starts may be the previous kernel's
-                load_item = find_item(p);
-                if (lane == 0) bars->item = load_item;
-            }
-        } else {
-            load_item = get_item(p);
-            if (warp == C::W_LOADV && load_item.w_sk > 0) ptx::prefetch_tmap(&tvs);
-        }
+        load_item = get_item(p);
+        if (warp == C::W_LOADV && load_item.w_sk > 0) ptx::prefetch_tmap(&tvs);
     }
     ptx::tc_fence_before();
     __syncthreads();
@@ -456,7 +185,6 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     // programmatic dependent launch: the set-up above touches nothing global
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    auto my_item = [&]() -> Item { return PACKED ? bars->item : get_item(p); };
 
     if (warp >= C::NSOFT) {
         ptx::regs_decrease<C::REGS_OTHER>();
@@ -469,7 +197,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             uint64_t *empty = which == 0 ? bars->k_empty : bars->v_empty;
             const int NS = which == 0 ? C::KS : C::VS;   // depth of this ring
             const uint64_t pol_kv = ptx::l2_policy_evict_last(), pol_q = ptx::l2_policy_evict_first();
-            const Item w = PACKED && which == 1 ? bars->item : load_item;
+            const Item w = load_item;
             int q_out = 0, issued = 0;
             auto load_q = [&](int t) {
                 if (t >= (w.n[1] > 0 ? kNQ : 1)) return;
@@ -477,7 +205,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 ptx::mbar_arrive_expect_tx(&bars->q_full[t], C::Q_BYTES);
                 for (int pn = 0; pn < C::PANELS; ++pn)
                     ptx::tma_load_4d(smem + C::OFF_Q + t * C::Q_BYTES + pn * C::PANEL_Q, &tq, pn * 64,
-                                     w.q_row + w.q0 + t * w.dq, w.fh + t * w.dh, w.fb, &bars->q_full[t], pol_q);
+                                     w.q0 + t * w.dq, w.fh + t * w.dh, w.fb, &bars->q_full[t], pol_q);
             };
             if (which == 0 && w.steps > 0) load_q(0);
             for (int j = 0; j < w.steps; ++j) {
@@ -487,8 +215,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 ptx::mbar_arrive_expect_tx(&full[s], C::KV_BYTES);
                 for (int pn = 0; pn < C::PANELS; ++pn)
                     ptx::tma_load_4d(smem + (which == 0 ? C::k_off(s) : C::v_off(s)) + pn * C::PANEL_KV,
-                                     !PACKED && which == 1 && w.sink_tile(j) ? &tvs : tm, pn * 64,
-                                     w.k_row + w.tile(j) * kBN, w.fkh, w.fb, &full[s], pol_kv);
+                                     which == 1 && w.sink_tile(j) ? &tvs : tm, pn * 64, w.tile(j) * kBN, w.fkh, w.fb, &full[s], pol_kv);
                 // the first scores need one query tile and the first keys
                 if (which == 0 && j == 0) load_q(1);
             }
@@ -515,7 +242,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             const uint32_t dk0 = ptx::desc_lo_sw128(ptx::smem_addr(smem + C::k_off(0)), 16);
             const uint32_t dv0 = ptx::desc_lo_sw128(ptx::smem_addr(smem + C::v_off(0)), C::PANEL_KV);
             constexpr int nkv = BNt / 16;                // k-steps of P V
-            const Item w = my_item();
+            const Item w = get_item(p);
             auto issue_qk = [&](int t, int gk) {
                 if (!lead) return;
                 const uint32_t id = w.few && gk == 0 ? id_few : id_qk;
@@ -615,12 +342,12 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             // ============================================= the V of edge tiles is
             // looked over as it arrives, while the tile's scores are computed and
             // exponentiated; other tiles are passed on at once
-            const Item w = my_item();
+            const Item w = get_item(p);
             for (int j = 0; j < w.steps; ++j) {
                 const int s = j % C::VS;
                 if (!__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&bars->v_in[s], (j / C::VS) & 1, p.err, abort)))
                     break;
-                const bool any = w.template checked<PACKED>(j) && clear_wild<D, F16>(smem + C::v_off(s));
+                const bool any = w.edge(j) && clear_wild<D, F16>(smem + C::v_off(s));
                 __syncwarp();
                 if (lane == 0) {
                     if (any) bars->wild = 1;
@@ -639,11 +366,10 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         const uint32_t o_addr = lane_base + C::tm_o(t);
         const uint32_t s_addr = lane_base + C::tm_s(t);
         const uint32_t p_addr = lane_base + C::tm_p(t);
-        const float cl = p.c_log2;
         bool ok = true;
-        const Item w = my_item();
+        const Item w = get_item(p);
         const int f = pick(w.f, t), nt = pick(w.n, t) - f;   // this query tile's key tiles
-        const int pos = w.off + w.q0 + w.dq * t;             // position of its first row
+        const int pos = p.off + w.q0 + w.dq * t;             // position of its first row
 
         // waits for the P V product of key tile jj of this query tile (and so
         // for every earlier one: one thread's MMAs complete in issue order)
@@ -654,42 +380,24 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             return true;
         };
 
-        float m = -INFINITY, l = 0.f;
+        SoftRows<D, F16> rows{s_addr, p_addr, o_addr, p.c_log2};
+        // S_t is in registers: the next QK_t may overwrite it
+        auto s_read = [&]() {
+            if constexpr (C::SEP_P) {
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&bars->s_free[t]);
+            }
+        };
         int j = 0;
         // the key tile from which on every row of the warp has seen a key before: of
         // the first one the last rows may see nothing, and then see the next
         const int k_first = w.tile(f) * kBN;
         const int seen_from = k_first < p.sinks || pos + quarter * 32 + 32 - p.window < k_first + kBN ? 1 : 2;
-        // ---- a first tile of a few sinks, which every row sees: kFew columns
         if (w.few && nt > 0) {
             ok = __all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&bars->s_full[t], 0, p.err, abort));
             if (ok) {
                 ptx::tc_fence_after();
-                float x[kFew];
-                ptx::tmem_ld32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
-                ptx::tmem_wait_ld();
-                if constexpr (C::SEP_P) {
-                    ptx::tc_fence_before();
-                    ptx::mbar_arrive(&bars->s_free[t]);
-                }
-                float mx = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < kFew; ++e) {
-                    if (e >= p.sinks) x[e] = -INFINITY;
-                    mx = fmaxf(mx, x[e]);
-                }
-                m = mx * cl;
-                const float nmu = m == -INFINITY ? 0.f : -m;
-                uint32_t pk[16];
-#pragma unroll
-                for (int e = 0; e < kFew; e += 2) {
-                    const float p0 = ptx::ex2(fmaf(x[e], cl, nmu)), p1 = ptx::ex2(fmaf(x[e + 1], cl, nmu));
-                    l += p0 + p1;
-                    pk[e / 2] = H16<F16>::pack(p0, p1);
-                }
-                ptx::tmem_st16(p_addr, pk);
-                ptx::tmem_wait_st();
-                ptx::tc_fence_before();
+                rows.few_sinks(p.sinks, s_read);
                 ptx::mbar_arrive(&bars->p_ready[t]);
                 j = 1;
             }
@@ -700,147 +408,10 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 break;
             }
             ptx::tc_fence_after();
-
-            float sv[BNt];
-#pragma unroll
-            for (int c = 0; c < BNt / 32; ++c)
-                ptx::tmem_ld32(s_addr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[c * 32]));
-            ptx::tmem_wait_ld();
-            if constexpr (C::SEP_P) {
-                // S_t is in registers: the next QK_t may overwrite it
-                ptx::tc_fence_before();
-                ptx::mbar_arrive(&bars->s_free[t]);
-            }
-
-            // ---- masks: rows at positions pos + row; only tiles on an edge of
-            //      the window are masked per element
-            {
-                const int k0 = w.tile(f + j) * BNt;
-                const bool late = k0 + BNt - 1 > pos;                    // a key behind the first row
-                const bool early = k0 + p.window < pos + kBM;            // one before the last row's window
-                if (late || (early && k0 + BNt > p.sinks)) {
-                    // key e of the tile is seen iff e <= hi and (e >= lo or e < sk);
-                    // all but tiny windows need only one bound per tile: the
-                    // diagonal's, the end of the sinks, or the window's start
-                    const int hi = pos + row - k0, lo = hi - p.window + 1, sk = p.sinks - k0;
-                    if (!early || (!late && k0 + p.window + BNt <= pos + 1)) {
-                        const int last = early ? sk - 1 : hi;
-#pragma unroll
-                        for (int e = 0; e < BNt; ++e)
-                            if (e > last) sv[e] = -INFINITY;
-                    } else if (!late && sk <= 0) {
-#pragma unroll
-                        for (int e = 0; e < BNt; ++e)
-                            if (e < lo) sv[e] = -INFINITY;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < BNt; ++e)
-                            if (e > hi || (e < lo && e >= sk)) sv[e] = -INFINITY;
-                    }
-                }
-            }
-
-            // P = 2^(x - m) in 16-bit into TMEM; returns the tile's row sum (fp32)
-            auto emit_p = [&](float nmu) -> float {
-                float acc[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-#pragma unroll
-                for (int c = 0; c < BNt / 32; ++c) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float x0, x1;
-                        ptx::ffma2(x0, x1, sv[c * 32 + 2 * e], sv[c * 32 + 2 * e + 1], cl, cl, nmu, nmu);
-                        const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
-                        ptx::fadd2(acc[(2 * e) & 7], acc[(2 * e + 1) & 7], acc[(2 * e) & 7],
-                                   acc[(2 * e + 1) & 7], p0, p1);
-                        pk[e] = H16<F16>::pack(p0, p1);
-                    }
-                    ptx::tmem_st16(p_addr + c * 16, pk);
-                }
-                return ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
-            };
-
-            // ---- P in columns of its own: the P V product that last read them
-            //      (key tile j - 1) must be done.  P over S needs no wait: the
-            //      Q K^T that wrote this S was issued after the P V that read the
-            //      P last held here, and MMAs complete in issue order.
-            bool prev_done = false;              // P V of tile j - 1 observed complete
-            if (C::SEP_P && j >= 1) {
-                if (!wait_pv(j - 1)) {
-                    ok = false;
-                    break;
-                }
-                prev_done = true;
-            }
-
-            // ---- fast path: exponentiate against the running maximum m as it
-            //      stands, with no tile maximum.  P only has to stay finite in its
-            //      16-bit type, not below 1: a tile whose row sum exceeds 2^24 (2^15
-            //      for f16, whose largest finite value is 65504) or is not finite
-            //      is redone below against its own maximum.  After the first tiles
-            //      m is close to the row maximum and the redo almost never runs.
-            bool fast = false, keep = false;      // this row's maximum may stay
-            if (j >= seen_from) {
-                const float lt = emit_p(-m);      // infinite or NaN if m is still -inf
-                keep = lt <= (F16 ? 32768.f : 16777216.f);
-                fast = __all_sync(0xffffffffu, keep);   // else redo the tile (P is rewritten below)
-                if (fast) l += lt;
-            }
-
-            if (!fast) {
-                // ---- tile maximum
-                float mx[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < BNt; e += 8) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) mx[i] = fmaxf(mx[i], sv[e + i]);
-                }
-                const float tmax = fmaxf(ptx::fmax3(ptx::fmax3(mx[0], mx[1], mx[2]), ptx::fmax3(mx[3], mx[4], mx[5]),
-                                                    mx[6]),
-                                         mx[7]);
-                const float mt = tmax * cl;      // cl > 0: max commutes with the scaling
-
-                // ---- the previous P V must be done before O is rescaled
-                // (a row that a redo for other rows' sake takes along keeps it)
-                const bool want = j == 0 || (!keep && mt > m + 8.f);   // this row moves its maximum
-                const bool any_want = __any_sync(0xffffffffu, want);
-                if (j > 0 && any_want && !prev_done) {
-                    if (!wait_pv(j - 1)) {
-                        ok = false;
-                        break;
-                    }
-                }
-                // ---- running maximum (moved lazily) and O rescale in TMEM
-                if (j == 0) {
-                    m = mt;
-                } else if (any_want) {
-                    // rows that move m scale their O row; the others multiply by 1
-                    const float f = want ? ptx::ex2(m - mt) : 1.f;   // m == -inf -> 0
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t ov[32];
-                        ptx::tmem_ld32(o_addr + c * 32, ov);
-                        ptx::tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float a0, a1;
-                            ptx::ffma2(a0, a1, __uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), f,
-                                       f, 0.f, 0.f);
-                            ov[e] = __float_as_uint(a0);
-                            ov[e + 1] = __float_as_uint(a1);
-                        }
-                        ptx::tmem_st32(o_addr + c * 32, ov);
-                    }
-                    if (want) {
-                        l *= f;
-                        m = mt;
-                    }
-                }
-                l += emit_p((m == -INFINITY) ? 0.f : -m);
+            if (!rows.tile(w.tile(f + j) * kBN, pos, row, p.window, p.sinks, j == 0, j >= seen_from, s_read,
+                           [&]() { return wait_pv(j - 1); })) {
+                ok = false;
+                break;
             }
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
@@ -850,7 +421,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
 
         // ---- epilogue: O / l -> 16-bit -> global
         if (ok && nt > 0 && wait_pv(nt - 1)) {
-            const float inv = 1.f / l;
+            const float inv = 1.f / rows.l;
             int ln = threadIdx.x & 31;           // opaque: nothing of the epilogue is computed ahead
             asm volatile("" : "+r"(ln));
             const int q_first = w.q0 + t * w.dq + quarter * 32, qh = w.fh + t * w.dh;   // the warp's first row
@@ -878,15 +449,15 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             __syncwarp();
             if (__all_sync(0xffffffffu, ptx::mbar_wait_or_abort(&bars->checked, 0, p.err, abort)) &&
                 *reinterpret_cast<volatile int *>(&bars->wild))
-                spoil_rows<D, F16, PACKED>(p, &bars->item, stage, w.off + q_first, imin(32, w.nq - q_first));
+                spoil_item<D, F16>(p, stage, p.off + q_first, imin(32, p.Nq - q_first));
             typename H16<F16>::T *const o0 = static_cast<typename H16<F16>::T *>(p.o) + w.fb * p.o_sb + qh * p.o_sh;
             const int col = ln % CH;
 #pragma unroll
             for (int r0 = 0; r0 < 32; r0 += 32 / CH) {
                 const int r = r0 + ln / CH;
                 const uint4 x = *reinterpret_cast<const uint4 *>(stage + (r * CH + (col ^ (r & 7))) * 16);
-                if (q_first + r < w.nq)
-                    *reinterpret_cast<uint4 *>(o0 + (w.q_row + q_first + r) * p.o_sn + col * 8) = x;
+                if (q_first + r < p.Nq)
+                    *reinterpret_cast<uint4 *>(o0 + (q_first + r) * p.o_sn + col * 8) = x;
             }
         }
     }
@@ -900,13 +471,13 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     }
 }
 
-template <int D, bool F16, bool PACKED>
+template <int D, bool F16>
 attn_status_t launch_window(const Ctx &c, const CUtensorMap &tq, const CUtensorMap &tk,
-                            const CUtensorMap &tv, const CUtensorMap &tvs, const WnParams &p, int grid) {
+                            const CUtensorMap &tv, const CUtensorMap &tvs, const WnParams &p) {
     using C = WnCfg<D>;
     static int done_mask = 0;
     static int regs = -1;
-    auto kern = tc_window_kernel<D, F16, PACKED>;
+    auto kern = tc_window_kernel<D, F16>;
     if (!ensure_smem_attr(reinterpret_cast<const void *>(kern), C::SMEM, c.device, &done_mask))
         return ATTN_ERR_RESOURCE;
     // the setmaxnreg split is only valid for the per-thread count it was computed for
@@ -920,7 +491,7 @@ attn_status_t launch_window(const Ctx &c, const CUtensorMap &tq, const CUtensorM
     }
     if (regs != C::REGS_LAUNCH) return ATTN_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = dim3(p.whole + 2 * (p.pairs - p.whole));
     cfg.blockDim = dim3(C::NT);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = c.stream;
@@ -976,45 +547,9 @@ attn_status_t tc_causal_window(const Ctx &c, attn_dtype_t dt, const void *q, con
     p.v = v; p.o = o;
     p.sv = st[2];
     p.o_sb = st[3].b; p.o_sh = st[3].h; p.o_sn = st[3].n;
-    const int grid = p.whole + 2 * (p.pairs - p.whole);
     if (D == 128)
-        return f16 ? launch_window<128, true, false>(c, tq, tk, tv, tvs, p, grid)
-                   : launch_window<128, false, false>(c, tq, tk, tv, tvs, p, grid);
-    return f16 ? launch_window<64, true, false>(c, tq, tk, tv, tvs, p, grid)
-               : launch_window<64, false, false>(c, tq, tk, tv, tvs, p, grid);
-}
-
-attn_status_t tc_causal_varlen(const Ctx &c, attn_dtype_t dt, const VarlenArgs &a) {
-    const bool f16 = dt == ATTN_F16;
-    const bool by_head = (a.Hq / a.Hkv) % 2 == 0;
-    const int bs = by_head ? kBM : kNQ * kBM, hp = by_head ? a.Hq / 2 : a.Hq;
-    // the most blocks that sequences of Nq queries together can have
-    const long long blocks = (a.Nq + (long long)imin(a.B, a.Nq) * (bs - 1)) / bs;
-    if (blocks * hp > (1 << 29)) return ATTN_ERR_UNSUPPORTED;
-    CUtensorMap tq, tk, tv;
-    if (!make_tmap4(&tq, a.q, a.D, a.Nq, a.Hq, 1, a.st[0], f16) ||
-        !make_tmap4(&tk, a.k, a.D, a.Nkv, a.Hkv, 1, a.st[1], f16) ||
-        !make_tmap4(&tv, a.v, a.D, a.Nkv, a.Hkv, 1, a.st[2], f16))
-        return ATTN_ERR_UNSUPPORTED;
-    WnParams p{};
-    p.seqs = PackedSeqs{a.cu_q, a.cu_k, a.B, a.Nq, a.Nkv};
-    p.sms = imax(1, c.sm_count);
-    p.window = a.window;
-    p.sinks = a.sinks;
-    p.c_log2 = a.scale * kLog2e;
-    p.err = c.err;
-    p.by_hp = Div(hp);
-    p.by_group = Div(a.Hq / a.Hkv);
-    p.by_head = by_head;
-    p.v = a.v; p.o = a.o;
-    p.sv = a.st[2];
-    p.o_sh = a.st[3].h; p.o_sn = a.st[3].n;
-    const int grid = int(blocks * hp) + p.sms / 2;     // and the halves of a split last round
-    if (a.D == 128)
-        return f16 ? launch_window<128, true, true>(c, tq, tk, tv, tv, p, grid)
-                   : launch_window<128, false, true>(c, tq, tk, tv, tv, p, grid);
-    return f16 ? launch_window<64, true, true>(c, tq, tk, tv, tv, p, grid)
-               : launch_window<64, false, true>(c, tq, tk, tv, tv, p, grid);
+        return f16 ? launch_window<128, true>(c, tq, tk, tv, tvs, p) : launch_window<128, false>(c, tq, tk, tv, tvs, p);
+    return f16 ? launch_window<64, true>(c, tq, tk, tv, tvs, p) : launch_window<64, false>(c, tq, tk, tv, tvs, p);
 }
 
 }  // namespace attn
