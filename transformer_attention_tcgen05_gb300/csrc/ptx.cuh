@@ -56,6 +56,35 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
                  : "memory");
 }
 
+// Takes the next CTA of this grid that has not started off the launch: its index, as
+// 16 bytes at `answer` (16-byte aligned), completes that many on bar.
+__device__ __forceinline__ void take_block(void *answer, uint64_t *bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_addr(answer)),
+                 "r"(smem_addr(bar))
+                 : "memory");
+}
+
+// The blockIdx.x that such an answer holds, or -1: every CTA has started (no further
+// one may be asked for).
+__device__ __forceinline__ int taken_block(const void *answer) {
+    int x = -1;
+    asm volatile(
+        "{\n"
+        ".reg .b64 lo, hi;\n"
+        ".reg .b128 a;\n"
+        ".reg .pred ok;\n"
+        "ld.shared.v2.b64 {lo, hi}, [%1];\n"
+        "mov.b128 a, {lo, hi};\n"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 ok, a;\n"
+        "@ok clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, a;\n"
+        "}\n"
+        : "+r"(x)
+        : "r"(smem_addr(answer))
+        : "memory");
+    return x;
+}
+
 __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
     uint32_t done;
     asm volatile(

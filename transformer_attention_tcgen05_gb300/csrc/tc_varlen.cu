@@ -7,9 +7,10 @@
 //
 //  * Items come from the device.  A block of query rows and the head pair that works on
 //    it are found from the sequences' starts (packed.cuh), longest first.
-//  * One CTA per SM takes an item of every round of the list (the second round in
-//    reverse order, and so on, so that no SM has the longest of each).  A batch of
-//    prompts has many short items: of the 7.4 us that an item of one key tile took as a
+//  * A CTA stays on its SM and takes items of CTAs that have not started off the launch
+//    (clusterlaunchcontrol), in the order of the list, one ahead.  Items differ in length
+//    and number of tiles: dealt out in turn, some SMs worked twice as long as others
+//    (chunks behind long pasts: 39 to 77 us).  A batch of prompts has many short items: of the 7.4 us that an item of one key tile took as a
 //    CTA of its own, 5.7 were start, finding the item, first copies and scores (4.1),
 //    and the last P V and the way out (1.6).  Here the loader finds the next item and
 //    copies its queries and first keys while the current one is computed, and the MMA
@@ -40,6 +41,7 @@ struct VlParams {
     unsigned *err;
     int by_head;             // a pair is two heads of one KV head (else two row tiles)
     Div by_hp, by_group;     // pairs (or heads) per block of rows, heads per KV head
+    Div by_sm;               // SMs
     const void *v;
     void *o;
     long long sv_h, sv_n, o_sh, o_sn;    // element strides (head, token)
@@ -71,27 +73,23 @@ struct VlBars {
     // item's O, s_free (separate P, D = 64) the softmax holds S_t in registers
     uint64_t s_full[kNQ], p_ready[kNQ], o_done[kNQ], o_free[kNQ], s_free[kNQ];
     uint64_t drain, checked[2];    // checked: every value of the item has been looked over
+    uint64_t taken;                // the answer has come
+    alignas(16) uint64_t answer[2];
     uint32_t tmem_base;
     int abort, wild[2];            // wild: a value was cleared from one of them
     VlItem item[2];                // steps -1: there are no more
 };
 
-// The index of this CTA's item of round i.
-__device__ __forceinline__ int item_index(int i) {
-    const int g = gridDim.x, c = blockIdx.x;
-    return i * g + (i & 1 ? g - 1 - c : c);
-}
-
 // An item by its index (one warp): whole pairs, longest first, then the pairs of a last
-// round that takes at most half of the CTAs as single tiles.
+// round that takes at most half of the SMs as single tiles.
 __device__ __forceinline__ VlItem find_item(const VlParams &p, const BlockFinder &finder, int index) {
-    const int g = gridDim.x, pairs = finder.total * p.by_hp.d, rest = pairs % g;
-    const int whole = 2 * rest <= g ? pairs - rest : pairs;
+    const int pairs = finder.total * p.by_hp.d, rest = pairs - p.by_sm(pairs) * p.by_sm.d;
+    const int whole = 2 * rest <= p.by_sm.d ? pairs - rest : pairs;
     const int s = index - whole;
     const int pair = s < 0 ? index : whole + (s >> 1), half = s < 0 ? -1 : s & 1;
     VlItem w{};
     w.steps = -1;
-    if (pair >= pairs) return w;
+    if (index < 0 || pair >= pairs) return w;
     const int block = p.by_hp(pair);
     const PackedBlock b = finder.find(block);
     w.dq = p.by_head ? 0 : kBM;
@@ -166,6 +164,7 @@ tc_varlen_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             ptx::mbar_init(&bars->checked[s], 1);
         }
         ptx::mbar_init(&bars->drain, 1);
+        ptx::mbar_init(&bars->taken, 1);
         bars->abort = 0;
         ptx::fence_barrier_init();
     }
@@ -203,11 +202,30 @@ tc_varlen_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             int g = 0;                                 // key tiles so far
             int q_out[kNQ] = {0, 0};                   // copies of each query tile so far
             bool ok = true;
+            int index = blockIdx.x, asked = 0;         // -1: every item has been taken
+            bool open = false;                         // an answer is on its way
+            auto next = [&]() {
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(&bars->taken, 16);
+                    ptx::take_block(bars->answer, &bars->taken);
+                }
+                open = true;
+                ok = wait_all(&bars->taken, asked & 1);
+                if (!ok) return;
+                ++asked;
+                open = false;
+                index = ptx::taken_block(bars->answer);
+                __syncwarp();
+                ptx::fence_proxy_async_smem();         // read before the next answer is written
+            };
             for (int it = 0; ok; ++it) {
                 const int s = it & 1;
                 if (it >= 2) ok = wait_all(&bars->item_empty[s], ((it >> 1) - 1) & 1);
                 if (!ok) break;
-                const VlItem w = find_item(p, finder, item_index(it));
+                VlItem w = find_item(p, finder, index);
+                // behind the last item: take what is left, so that no CTA starts for it
+                while (ok && index >= 0 && w.steps < 0) next();
+                if (!ok) break;
                 if (lane == 0) {
                     bars->item[s] = w;
                     bars->wild[s] = 0;
@@ -240,10 +258,14 @@ tc_varlen_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                     }
                 }
                 ok = __all_sync(0xffffffffu, ok);
+                // Only now, with the item's last keys on their way: whoever asks before its
+                // item is nearly done has the next one too early, and the SMs end unevenly
+                if (ok) next();
             }
             // after a timeout: let the copies this thread issued land (bounded) before
             // the CTA's shared memory is released
             if (*abort && lane == 0) {
+                if (open) ptx::mbar_wait(&bars->taken, asked & 1, nullptr);
                 for (int t = 0; t < kNQ; ++t)
                     if (q_out[t] > 0) ptx::mbar_wait(&bars->q_full[t], (q_out[t] - 1) & 1, nullptr);
                 for (int i = imax(0, g - C::KS); i < g; ++i)
@@ -615,13 +637,15 @@ attn_status_t tc_causal_varlen(const Ctx &c, attn_dtype_t dt, const VarlenArgs &
     p.by_head = by_head;
     p.by_hp = Div(hp);
     p.by_group = Div(a.Hq / a.Hkv);
+    p.by_sm = Div(c.sm_count);
     p.v = a.v;
     p.o = a.o;
     p.sv_h = a.st[2].h; p.sv_n = a.st[2].n;
     p.o_sh = a.st[3].h; p.o_sn = a.st[3].n;
     p.wide = ((reinterpret_cast<uintptr_t>(a.o) | uintptr_t(p.o_sh * 2) | uintptr_t(p.o_sn * 2)) & 31u) == 0;
-    // a CTA per SM; a call of few items is spread over twice as many, in single tiles
-    const int grid = int(blocks * hp * 2 < c.sm_count ? blocks * hp * 2 : c.sm_count);
+    // an index for every item that there can be (at most half an SM count of pairs is
+    // given out as two single tiles)
+    const int grid = int(blocks * hp + (blocks * hp < c.sm_count / 2 ? blocks * hp : c.sm_count / 2));
     if (a.D == 128)
         return f16 ? launch_varlen<128, true>(c, tq, tk, tv, p, grid) : launch_varlen<128, false>(c, tq, tk, tv, p, grid);
     return f16 ? launch_varlen<64, true>(c, tq, tk, tv, p, grid) : launch_varlen<64, false>(c, tq, tk, tv, p, grid);
