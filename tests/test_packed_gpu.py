@@ -238,6 +238,29 @@ def test_append_starts_that_do_not_rise_are_reported(ta):
     assert int((vp != 0).any(-1).sum()) == 4
 
 
+@pytest.mark.parametrize("q4", [False, True])
+def test_append_sequences_that_overlap_stay_in_the_table(ta, q4):
+    """Starts that fall let others claim the same rows: the call reports it, and what it
+    writes lies on pages of the sequences that rise."""
+    g = torch.Generator().manual_seed(41)
+    c = Cache([0, 0, 30, 0, 0], [32] * 5, 8, 6)
+    q, kn, vn, _ = new_rows(g, [32], 1, 1, 64, "bf16")
+    cu = torch.tensor([0, 32, 0, 2, 1, 32]).int().cuda()
+    f = ta.rope_frequencies(64)
+    kp, vp = (torch.full((c.P, 1, 8, 64), 5.0, dtype=torch.bfloat16).cuda() for _ in "kv")
+    pages = torch.full((c.P, 1, 8, 72), 5, dtype=torch.uint8).cuda()
+    if q4:
+        ta.kv_append_paged_q4(pages, kn, vn, c.dev, c.sl, f, cu_new=cu)
+    else:
+        ta.kv_append_paged_rope(kp, vp, kn, vn, c.dev, c.sl, f, cu_new=cu)
+    assert ta.device_status() == 6
+    x = (pages == 5).all(-1) if q4 else (kp == 5).all(-1) & (vp == 5).all(-1)
+    own = torch.zeros(c.P, dtype=torch.bool)
+    own[[int(i) for b in (0, 2, 4) for i in c.table[b] if i < c.P]] = True
+    assert x.all(-1).all(-1).cpu()[~own].all()
+    assert c.sl.tolist()[1] == 0 and c.sl.tolist()[3] == 0
+
+
 # ------------------------------------------------------------- 4-bit cache
 
 @pytest.mark.parametrize("dt,lens,news,Hkv,D,S", [
@@ -761,6 +784,39 @@ def test_varlen_sequences_that_cannot_be_are_reported(ta):
         o.fill_(7.0)
         ta.causal_gqa_varlen_fwd(q, k, v, empty, o=o)
         assert ta.device_status() == 0 and (o == 7).all()
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 64), ("f32", 64)])
+def test_varlen_sequences_that_overlap(ta, dt, D):
+    """The same rows claimed over and over: more blocks than the rows can have.  What is
+    written is right, and the call reports it."""
+    g = torch.Generator().manual_seed(42)
+    n = 300
+    q, _ = packed(g, dt, [n], 2, D)
+    k, _ = packed(g, dt, [n], 1, D)
+    v, _ = packed(g, dt, [n], 1, D)
+    once = ta.causal_gqa_varlen_fwd(q, k, v, starts([n]))
+    assert ta.device_status() == 0
+    o = torch.full_like(q, 7.0)
+    ta.causal_gqa_varlen_fwd(q, k, v, torch.tensor([0, n] * 150).int().cuda(), o=o)
+    assert ta.device_status() == 6
+    same = (o == once).all(-1)
+    assert (same | (o == 7).all(-1)).all() and same.any()
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 128), ("f16", 64)])
+def test_varlen_rows_on_16_byte_boundaries(ta, dt, D):
+    """Rows of q, k, v and o that start between two sectors."""
+    g = torch.Generator().manual_seed(43)
+    lens, H = [130, 1, 260], 4
+    n = sum(lens)
+    q, k, v = (randn(g, n, h * D + 8).to(DT[dt]).cuda()[:, 8:].unflatten(1, (h, D)) for h in (H, 2, 2))
+    wide = torch.full((n, H * D + 24), 7.0, dtype=DT[dt]).cuda()
+    cu = starts(lens)
+    o = ta.causal_gqa_varlen_fwd(q, k, v, cu, window=140, sinks=3, o=wide[:, 8:-16].unflatten(1, (H, D)))
+    assert o.data_ptr() % 32 == 16 and (wide[:, :8] == 7).all() and (wide[:, -16:] == 7).all()
+    assert torch.equal(o, ta.causal_gqa_varlen_fwd(q, k, v, cu, window=140, sinks=3)) and ta.device_status() == 0
+    check_varlen(dt, q, k, v, cu, cu, o, 140, 3, [0, 127, 128, 129, 130, 131, 258, -1])
 
 
 def test_varlen_long_and_many(ta):

@@ -7,9 +7,14 @@
 // which grows with the keys that it reads.  Blocks are numbered by falling level, and
 // within one by sequence, so that the longest start first.  The block of a number
 // is found by bisection: with F(L) the blocks of level L or more, it lies in the
-// largest L with F(L) > number.  One warp, 32 sequences at a time; the first 64
-// stay in registers (16 sequences: 0.2 us beside the rest of a CTA's set-up).  No list
-// is written, so a call needs no workspace and one launch.
+// largest L with F(L) > number.  One warp, 32 sequences at a time, of which the first
+// 64 stay in registers (16 sequences: 1.0 to 1.4 us to a block's rows, which a kernel
+// hides behind the block before).  No list is written, so a call needs no workspace and
+// one launch.
+//
+// Sequences whose starts do not rise have no rows and are reported.  Such starts may
+// make others overlap, in any number: no sum passes kMost per lane, and no more blocks
+// are given out than disjoint sequences can have.
 #pragma once
 
 #include "common.cuh"
@@ -19,6 +24,7 @@ namespace attn {
 struct PackedSeqs {
     const int32_t *cu_q, *cu_k;
     int B, Nq, Nkv;
+    int most;                              // blocks that disjoint sequences can have, at most kMost
 };
 
 struct PackedBlock {
@@ -27,6 +33,8 @@ struct PackedBlock {
 };
 
 class BlockFinder {
+    static constexpr int kMost = 1 << 25;  // (of 32 lanes together: 2^30)
+
   public:
     // All lanes of a warp; report: invalid sequences set the device error word.
     __device__ __forceinline__ BlockFinder(const PackedSeqs &s, int bs_log, bool report, unsigned *err)
@@ -40,14 +48,14 @@ class BlockFinder {
         for (int b = lane_ + 64; b < s_.B; b += 32) {
             const Seq q = load(b, wrong);
             top = imax(top, q.level + q.blocks);
-            sum += q.blocks;
+            sum = imin(sum + q.blocks, kMost);
         }
         if (report && wrong) raise_device_error(err, kDevCheck);
         top_ = __reduce_max_sync(0xffffffffu, top);
-        total = __reduce_add_sync(0xffffffffu, sum);
+        total = imin(__reduce_add_sync(0xffffffffu, sum), s_.most);
     }
 
-    int total;                             // blocks of all sequences
+    int total;                             // blocks to work on
 
     // The block of a number below `total`.
     __device__ __forceinline__ PackedBlock find(int number) const {
@@ -109,7 +117,7 @@ class BlockFinder {
     __device__ __forceinline__ int from_level(int level) const {
         int sum = from(first_, level) + from(second_, level);
         bool wrong = false;
-        for (int b = lane_ + 64; b < s_.B; b += 32) sum += from(load(b, wrong), level);
+        for (int b = lane_ + 64; b < s_.B; b += 32) sum = imin(sum + from(load(b, wrong), level), kMost);
         return __reduce_add_sync(0xffffffffu, sum);
     }
     const PackedSeqs &s_;

@@ -239,7 +239,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm) append_rows_kernel(const App
         if (b >= 0) {
             const int len = d.pos[tid];
             if (append_fits(p, len, d.count[tid])) {
-                pos = len + t0 + tid - d.first[tid];
+                // (of sequences that overlap, which takes starts that do not rise, a row
+                // may hold one's length and another's start)
+                const long long at = (long long)len + t0 + tid - d.first[tid];
+                if (at >= 0 && at < (long long)p.max_pages * p.S) pos = int(at);
+            }
+            if (pos >= 0) {
                 row = pos % p.S;
                 page = p.table[b * p.table_stride + pos / p.S];
                 if (page < 0 || page >= p.P) page = -1;

@@ -426,7 +426,6 @@ attn_status_t simt_causal_window(const Ctx &c, attn_dtype_t dt, const void *q, c
 attn_status_t simt_causal_varlen(const Ctx &c, attn_dtype_t dt, const VarlenArgs &a) {
     WinParams p{};
     p.q = a.q; p.k = a.k; p.v = a.v; p.o = a.o;
-    p.seqs = PackedSeqs{a.cu_q, a.cu_k, a.B, a.Nq, a.Nkv};
     p.window = a.window;
     p.sinks = a.sinks;
     p.H = a.Hq;
@@ -435,8 +434,9 @@ attn_status_t simt_causal_varlen(const Ctx &c, attn_dtype_t dt, const VarlenArgs
     p.err = c.err;
     p.sq = a.st[0]; p.sk = a.st[1]; p.sv = a.st[2]; p.so = a.st[3];
     // the most blocks that sequences of Nq queries together can have
-    const long long blocks = (a.Nq + (long long)imin(a.B, a.Nq) * (kBM - 1)) / kBM;
-    return dispatch_win<true>(c, dt, a.D, p, int(blocks), a.Hq);
+    const int blocks = int((a.Nq + (long long)imin(a.B, a.Nq) * (kBM - 1)) / kBM);
+    p.seqs = PackedSeqs{a.cu_q, a.cu_k, a.B, a.Nq, a.Nkv, blocks};
+    return dispatch_win<true>(c, dt, a.D, p, blocks, a.Hq);
 }
 
 }  // namespace attn

@@ -629,7 +629,7 @@ attn_status_t tc_causal_varlen(const Ctx &c, attn_dtype_t dt, const VarlenArgs &
         !make_tmap4(&tv, a.v, a.D, a.Nkv, a.Hkv, 1, a.st[2], f16))
         return ATTN_ERR_UNSUPPORTED;
     VlParams p{};
-    p.seqs = PackedSeqs{a.cu_q, a.cu_k, a.B, a.Nq, a.Nkv};
+    p.seqs = PackedSeqs{a.cu_q, a.cu_k, a.B, a.Nq, a.Nkv, int(blocks)};
     p.window = a.window;
     p.sinks = a.sinks;
     p.c_log2 = a.scale * kLog2e;
