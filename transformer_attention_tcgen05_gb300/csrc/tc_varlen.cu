@@ -59,13 +59,26 @@ constexpr int kRegsSoftmax = 224, kRegsOther = 56;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsOther <= WnCfg<128>::NT * WnCfg<128>::REGS_LAUNCH,
               "setmaxnreg split must fit the launch's register file share");
 
+// Query tiles for D = 64 lie in two places in turn, so that an item's are copied as soon
+// as it is found (7 sequences of 2048, 24 heads, window 1024: 103 us with one place, 100);
+// for D = 128 the rings leave no room, and they follow the last scores of the item before.
+template <int D>
+struct VlCfg : WnCfg<D> {
+    using W = WnCfg<D>;
+    static constexpr int QS = D == 64 ? 2 : 1;
+    static constexpr int q_off(int slot) { return slot ? W::OFF_BAR : W::OFF_Q; }
+    static constexpr int OFF_BAR = W::OFF_BAR + (QS - 1) * kNQ * W::Q_BYTES;
+    static constexpr int SMEM = OFF_BAR + W::BARS + 1024;
+    static_assert(SMEM <= 227 * 1024, "must fit a CTA's shared memory");
+};
+
 constexpr int kItemUsers = 2 + 1 + 4 * kNQ;    // V loader, MMA, check; softmax warps
 
 // Barrier block at OFF_BAR.  Phases run on from item to item.
-template <int KS, int VS>
+template <int KS, int VS, int QS>
 struct VlBars {
     uint64_t item_full[2], item_empty[2];
-    uint64_t q_full[kNQ], q_empty[kNQ];
+    uint64_t q_full[QS][kNQ], q_empty[kNQ];        // q_empty: QS 1 (else the item before the last is)
     // v_in: the stage's copies have landed; v_full: the checking warp has passed it on
     uint64_t k_full[KS], k_empty[KS], v_in[VS], v_full[VS], v_empty[VS];
     // per query tile t: s_full its Q K^T has completed, p_ready the softmax has written P,
@@ -129,8 +142,8 @@ template <int D, bool F16>
 __global__ void __launch_bounds__(WnCfg<D>::NT, 1)
 tc_varlen_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                  const __grid_constant__ CUtensorMap tv, const __grid_constant__ VlParams p) {
-    using C = WnCfg<D>;
-    using BarsT = VlBars<C::KS, C::VS>;
+    using C = VlCfg<D>;
+    using BarsT = VlBars<C::KS, C::VS, C::QS>;
     static_assert(sizeof(BarsT) <= C::BARS, "barrier block must fit its reserved bytes");
     extern __shared__ uint8_t smem_raw[];
     // 1024-byte alignment for the 128-byte swizzle atoms
@@ -150,7 +163,7 @@ tc_varlen_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             ptx::mbar_init(&bars->v_empty[s], 1);
         }
         for (int t = 0; t < kNQ; ++t) {
-            ptx::mbar_init(&bars->q_full[t], 1);
+            for (int s = 0; s < C::QS; ++s) ptx::mbar_init(&bars->q_full[s][t], 1);
             ptx::mbar_init(&bars->q_empty[t], 1);
             ptx::mbar_init(&bars->s_full[t], 1);
             ptx::mbar_init(&bars->p_ready[t], 128);
@@ -200,7 +213,8 @@ tc_varlen_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             // warp finds an item, one thread copies
             const BlockFinder finder(p.seqs, p.by_head ? 7 : 8, blockIdx.x == 0, p.err);
             int g = 0;                                 // key tiles so far
-            int q_out[kNQ] = {0, 0};                   // copies of each query tile so far
+            // per place of a query tile (bit): copied to before, parity of the copies so far
+            uint32_t q_used = 0, q_par = 0;
             bool ok = true;
             int index = blockIdx.x, asked = 0;         // -1: every item has been taken
             bool open = false;                         // an answer is on its way
@@ -235,14 +249,17 @@ tc_varlen_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 if (lane == 0) {
                     auto load_q = [&](int t) {
                         if (w.n[t] <= 0) return;
-                        const int n = pick(q_out, t);
-                        if (n > 0) ok = ok && wait(&bars->q_empty[t], (n - 1) & 1);
+                        const int slot = C::QS == 1 ? 0 : s;
+                        const uint32_t bit = 1u << (slot * kNQ + t);
+                        if (C::QS == 1 && (q_used & bit)) ok = ok && wait(&bars->q_empty[t], (q_par & bit) == 0);
                         if (!ok) return;
-                        ++q_out[t];
-                        ptx::mbar_arrive_expect_tx(&bars->q_full[t], C::Q_BYTES);
+                        q_used |= bit;
+                        q_par ^= bit;
+                        uint64_t *const full = &bars->q_full[slot][t];
+                        ptx::mbar_arrive_expect_tx(full, C::Q_BYTES);
                         for (int pn = 0; pn < C::PANELS; ++pn)
-                            ptx::tma_load_4d(smem + C::OFF_Q + t * C::Q_BYTES + pn * C::PANEL_Q, &tq, pn * 64,
-                                             w.q_row + w.q0 + t * w.dq, w.fh + t * w.dh, 0, &bars->q_full[t], pol_q);
+                            ptx::tma_load_4d(smem + C::q_off(slot) + t * C::Q_BYTES + pn * C::PANEL_Q, &tq, pn * 64,
+                                             w.q_row + w.q0 + t * w.dq, w.fh + t * w.dh, 0, full, pol_q);
                     };
                     load_q(0);
                     for (int j = 0; ok && j < w.steps; ++j, ++g) {
@@ -266,8 +283,8 @@ tc_varlen_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             // the CTA's shared memory is released
             if (*abort && lane == 0) {
                 if (open) ptx::mbar_wait(&bars->taken, asked & 1, nullptr);
-                for (int t = 0; t < kNQ; ++t)
-                    if (q_out[t] > 0) ptx::mbar_wait(&bars->q_full[t], (q_out[t] - 1) & 1, nullptr);
+                for (int i = 0; i < C::QS * kNQ; ++i)
+                    if ((q_used >> i) & 1) ptx::mbar_wait(&bars->q_full[0][0] + i, ((q_par >> i) & 1) ^ 1, nullptr);
                 for (int i = imax(0, g - C::KS); i < g; ++i)
                     ptx::mbar_wait(&bars->k_full[i % C::KS], (i / C::KS) & 1, nullptr);
             }
@@ -306,18 +323,19 @@ tc_varlen_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             const uint32_t id_few = ptx::idesc_16_f32(kBM, kFew, false, F16);
             const uint32_t id_pv = ptx::idesc_16_f32(kBM, D, true, F16);
             constexpr uint32_t HI128 = ptx::desc_hi_sw128(1024);
-            const uint32_t dq0 = ptx::desc_lo_sw128(ptx::smem_addr(smem + C::OFF_Q), 16);
+            const uint32_t dq0 = ptx::desc_lo_sw128(ptx::smem_addr(smem + C::q_off(0)), 16);
             const uint32_t dk0 = ptx::desc_lo_sw128(ptx::smem_addr(smem + C::k_off(0)), 16);
             const uint32_t dv0 = ptx::desc_lo_sw128(ptx::smem_addr(smem + C::v_off(0)), C::PANEL_KV);
             // ring slots and their phases' parities; per query tile (bit t) the parities of
             // its scores, weights and items.  (A fresh barrier's phase before the first
             // counts as completed: "free" barriers are waited on with the other parity.)
             int ks = 0, kp = 0, vs = 0, vp = 0;
-            uint32_t score_par = 0, weigh_par = 0, item_par = 0;
+            uint32_t score_par = 0, weigh_par = 0, item_par = 0, q_par = 0;   // (q_par: per place)
+            int slot = 0;                              // place of the item's query tiles
             bool ok = true;
             auto issue_qk = [&](int t, uint32_t id) {
                 if (!lead) return;
-                const uint32_t a0 = dq0 + uint32_t((t * C::Q_BYTES) >> 4);
+                const uint32_t a0 = dq0 + uint32_t((slot * (C::q_off(1) - C::q_off(0)) + t * C::Q_BYTES) >> 4);
                 const uint32_t b0 = dk0 + uint32_t(ks * (C::KV_BYTES >> 4));
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
@@ -367,7 +385,7 @@ tc_varlen_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             auto next_k = [&](bool last, const int (&n)[kNQ]) {
                 if (ok && lead) {
                     ptx::tc_commit(&bars->k_empty[ks]);
-                    if (last)
+                    if (C::QS == 1 && last)
                         for (int t = 0; t < kNQ; ++t)
                             if (n[t] > 0) ptx::tc_commit(&bars->q_empty[t]);
                 }
@@ -385,9 +403,14 @@ tc_varlen_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 const bool few = same(item.few) != 0;
                 if (steps < 0) break;
                 if (steps > 0) {                       // (0: a second row tile past its sequence's end)
+                    if (C::QS == 2) slot = it & 1;
 #pragma unroll
                     for (int t = 0; t < kNQ; ++t)
-                        if (n[t] > 0) ok = ok && wait(&bars->q_full[t], (item_par >> t) & 1);
+                        if (n[t] > 0) {
+                            const int i = slot * kNQ + t;
+                            ok = ok && wait(&bars->q_full[0][0] + i, (q_par >> i) & 1);
+                            q_par ^= 1u << i;
+                        }
                     ok = ok && wait(&bars->k_full[ks], kp);
                     qk(0, few ? id_few : id_qk);
                     if (n[1] > 0 && f1 == 0) qk(1, few ? id_few : id_qk);
@@ -579,7 +602,7 @@ tc_varlen_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
 template <int D, bool F16>
 attn_status_t launch_varlen(const Ctx &c, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                             const VlParams &p, int grid) {
-    using C = WnCfg<D>;
+    using C = VlCfg<D>;
     static int done_mask = 0;
     static int regs = -1;
     auto kern = tc_varlen_kernel<D, F16>;
