@@ -7,19 +7,32 @@
 //
 //  * Items come from the device.  A block of query rows and the head pair that works on
 //    it are found from the sequences' starts (packed.cuh), longest first.
-//  * A CTA stays on its SM and takes items of CTAs that have not started off the launch
-//    (clusterlaunchcontrol), in the order of the list, one ahead.  Items differ in length
-//    and number of tiles: dealt out in turn, some SMs worked twice as long as others
-//    (chunks behind long pasts: 39 to 77 us).  A batch of prompts has many short items: of the 7.4 us that an item of one key tile took as a
-//    CTA of its own, 5.7 were start, finding the item, first copies and scores (4.1),
-//    and the last P V and the way out (1.6).  Here the loader finds the next item and
-//    copies its queries and first keys while the current one is computed, and the MMA
-//    warp computes its first scores while the softmax warps write the current rows out.
+//  * A CTA stays on its SM and takes the items of CTAs that have not started off the
+//    launch (clusterlaunchcontrol), in the order of the list.  Items differ in length and
+//    number of tiles: dealt out in turn, some SMs worked twice as long as others (chunks
+//    behind long pasts: 39 to 77 us).
+//  * A batch of prompts has many short items: of the 7.4 us that an item of one key tile
+//    took as a CTA of its own, 5.7 were start, finding the item, first copies and scores
+//    (4.1), and the last P V and the way out (1.6).  Here the loader finds the next item
+//    and copies its first keys while the current one is computed, and the MMA warp computes
+//    its first scores while the softmax warps write the current rows out: the last rows of
+//    an item and the next one's first scores are 1.5 to 3 us apart.
 //  * A thread writes its output row itself, in whole sectors (32-byte stores), so that
 //    the query tiles are free for the next item as soon as the last scores are computed
 //    and nothing of the way out waits (through shared memory it took 2 us per item).
 //  * The values of a sequence's sinks cannot come through a tensor map that ends behind
 //    them: sink tiles are looked over like the tiles of an edge.
+//
+// 16-bit, 32 heads on 8, D 128: one prompt of 4096 tokens 95 us (1440 TFLOP/s over the
+// visible pairs; 92 in the kernel for one length), 8 of 1024 74 us (79), 64 of 128 43 us
+// (50), 16 prompts of 1 to 6000 tokens 192 us (1345 TFLOP/s, 71% of the measured product).  A
+// step of two tiles takes 1.18 us for D 128 and 0.77 for D 64 (0.99 and 0.49 at the
+// tensor pipe's rate); 1.5 us where all of its rows are on an edge, and 1.1 for a tile
+// alone.  Measured and not kept: masks 32 keys at a time as bits (chunks 68 -> 66 us, the
+// plain step 0.71 -> 0.76), no exponentials for keys that no row of a warp sees (step
+// 0.77 -> 0.87: the exponentials of a tile are no longer one block of instructions; as a
+// second copy of them 0.86 and cold instructions), heads in pairs also where
+// the group is odd (7 x 2048 tokens 101 -> 109 us).
 //
 // All spin-waits are bounded (1 s); on a timeout the CTA raises the device error word,
 // drains what it issued, frees TMEM and exits.

@@ -16,6 +16,12 @@ KERNEL is one of:
           (attn_causal_gqa_window_fwd)
   decode_paged  the decode case over scattered pages of 16 tokens
           (attn_decode_gqa_paged)
+  decode_paged_q4  the decode case over 4-bit pages (attn_decode_gqa_paged_q4)
+  rope    token-major rows of 8192 tokens, 32 heads, D 128 (attn_rope_fwd)
+  append_rope  6 prompts of 500 to 8000 tokens of a packed projection, 32 query
+          / 8 KV heads, D 128, into pages of 16 (attn_kv_append_paged_rope)
+  varlen  packed prompts of 5 to 4096 tokens, 32 query / 8 KV heads, D 128
+          (attn_causal_gqa_varlen_fwd)
 
 The inputs are the benchmark's seeded bf16 draws.  W untimed launches run
 first, then N more; the process exits non-zero if the device reports an
@@ -99,12 +105,52 @@ def build_case(kernel: str, frames: int, dev):
         ws = torch.zeros(ta.decode_paged_workspace_bytes(w.B, w.H, w.Hkv, w.D), dtype=torch.uint8,
                          device=dev)
         return lambda: ta.decode_gqa_paged(q, *pages, table, sl, o=o, workspace=ws)
+    if kernel == "decode_paged_q4":
+        w, S = WORKLOADS["gqa_decode"], 16
+        h = make_inputs(w)
+        q = _dev(h["q"], dev)
+        k, v = (_dev(h[n], dev).transpose(1, 2).flatten(0, 1) for n in "kv")     # [B L, Hkv, D]
+        n = w.B * w.Lmax // S
+        table = torch.randperm(n, generator=torch.Generator().manual_seed(1008)).view(w.B, w.Lmax // S).int().to(dev)
+        pages = torch.zeros(n, w.Hkv, S, ta.kv_q4_row_bytes(w.D), dtype=torch.uint8, device=dev)
+        sl = torch.zeros(w.B, dtype=torch.int32, device=dev)
+        cu = torch.arange(0, (w.B + 1) * w.Lmax, w.Lmax, dtype=torch.int32, device=dev)
+        ta.kv_append_paged_q4(pages, k, v, table, sl, cu_new=cu)
+        o = torch.empty_like(q)
+        ws = torch.zeros(ta.decode_paged_q4_workspace_bytes(w.B, w.H, w.Hkv, w.D), dtype=torch.uint8, device=dev)
+        return lambda: ta.decode_gqa_paged_q4(q, pages, table, sl, o=o, workspace=ws)
+    if kernel == "rope":
+        g = torch.Generator(device="cpu").manual_seed(1009)
+        x = torch.randn(8192, 32, 128, generator=g).bfloat16().to(dev)
+        pos = torch.arange(8192, dtype=torch.int32, device=dev)
+        freq, y = ta.rope_frequencies(128), torch.empty_like(x)
+        return lambda: ta.rope_fwd(x, freq, pos, o=y)
+    if kernel in ("append_rope", "varlen"):
+        g = torch.Generator(device="cpu").manual_seed(1010)
+        lens = [8000, 5200, 700, 4096, 2500, 500] if kernel == "append_rope" else [4096, 5, 1500, 700, 130, 2048, 37]
+        x = torch.randn(sum(lens), 48, 128, generator=g).bfloat16().to(dev)
+        q, k, v = x[:, :32], x[:, 32:40], x[:, 40:]
+        cu = torch.tensor([0] + lens).cumsum(0).int().to(dev)
+        o = torch.empty(sum(lens), 32, 128, dtype=torch.bfloat16, device=dev)
+        if kernel == "varlen":
+            return lambda: ta.causal_gqa_varlen_fwd(q, k, v, cu, o=o)
+        S = 16
+        n = [-(-t // S) for t in lens]
+        table = torch.full((len(lens), max(n)), -1, dtype=torch.int32)
+        perm = torch.randperm(sum(n), generator=g).int()
+        for b, (lo, m) in enumerate(zip([0] + torch.tensor(n).cumsum(0).tolist(), n)):
+            table[b, :m] = perm[lo:lo + m]
+        table = table.to(dev)
+        kp, vp = (torch.zeros(sum(n), 8, S, 128, dtype=torch.bfloat16, device=dev) for _ in "kv")
+        sl, freq = torch.zeros(len(lens), dtype=torch.int32, device=dev), ta.rope_frequencies(128)
+        return lambda: ta.kv_append_paged_rope(kp, vp, k, v, table, sl, freq, cu_new=cu, q=q, q_out=o, advance=False)
     raise SystemExit(f"unknown kernel {kernel!r}")
 
 
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
-    ap.add_argument("kernel", choices=["joint", "na3d", "decode", "causal", "window", "decode_paged"])
+    ap.add_argument("kernel", choices=["joint", "na3d", "decode", "causal", "window", "decode_paged",
+                                       "decode_paged_q4", "rope", "append_rope", "varlen"])
     ap.add_argument("--frames", type=int, default=0, help="na3d: T extent (default 21)")
     ap.add_argument("--warmup", type=int, default=2)
     ap.add_argument("--launches", type=int, default=1)
