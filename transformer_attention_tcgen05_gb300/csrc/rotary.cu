@@ -2,14 +2,21 @@
 // their way into a paged cache, 16-bit / fp32 or held in 4 bits, with the reader
 // that gives a 4-bit cache's rows back.
 //
-// All of it is bound by memory: a thread owns two times eight channels of a row
-// (both halves of eight pairs, two 16-byte vectors of a 16-bit type), walks the heads
-// of its token and has the vectors of four rows in flight.  A row belongs to D / 16
-// lanes and nothing of it passes through shared memory, so it may be rotated in place.
+// Rows that stay 16-bit or fp32 are bound by memory: a thread owns two times eight
+// channels of a row (both halves of eight pairs, two 16-byte vectors of a 16-bit type),
+// walks the heads of its token and has the vectors of four rows in flight.  A row belongs
+// to D / 16 lanes and nothing of it passes through shared memory, so it may be rotated in place.
 // The angles of a tile of tokens are computed once into shared memory while the first
 // rows arrive.  (Eight channels per thread with the partners read a second time, and
 // the angles computed by every thread for itself, executed four times the
-// instructions: 8192 x 32 rows of D 128 took 29.2 us, prompts of 23 000 tokens 193 us.)
+// instructions.)  bf16, 8192 x 32 rows of D 128: 22.5 us, 6.0 TB/s (29.2 that way);
+// append of 20 000 tokens, 32 heads on 8: 78.5 us, 6.3 TB/s (193); 64 tokens 2.9 us.
+//
+// Rows coded in 4 bits are bound by instructions (340 per warp and two rows, a quarter of
+// them angles; 63% of the issue slots): 20 000 tokens 39.5 us for K and V alone, 78 with
+// their queries, whose CTAs they run beside; 64 tokens 3.1 us.  Extrema in packed pairs
+// and with NaN carried along, and the next heads' rows on the way, brought K and V of 5000
+// tokens from 15.8 to 13.5 us.  The reader: 22 500 rows 22.1 us, 5.3 TB/s (ALU 64%, then the copies).
 #include <math.h>
 
 #include "kernels.h"
@@ -153,6 +160,7 @@ struct AppendRows {
     int32_t *seq_len;
     const int32_t *cu;                                 // null: token b is the next one of sequence b
     int B, N, Hq, Hkv, D, S, P, max_pages, advance;
+    int apart;                                         // 4-bit: q, and K and V, in CTAs of their own
     Rotation rot;
     Tile tile;
     unsigned *err;
@@ -192,39 +200,9 @@ __device__ __forceinline__ bool append_fits(const AppendRows &p, int len, int n)
     return len >= 0 && (long long)len + n <= (long long)p.max_pages * p.S;
 }
 
-// Rows of q, and of K and V into a 16-bit or fp32 cache: D / 16 lanes each.  Rows of K
-// and V into a cache held in 4 bits: D / 8 lanes, so that 4 neighbours hold a group of
-// 32 channels; the partners of a rotated half are read a second time.
-template <typename T, bool Q4>
-__global__ void __launch_bounds__(kThreads, kPerSm) append_rows_kernel(const AppendRows p) {
-    constexpr int U = sizeof(T) == 4 ? 2 : 4;
-    __shared__ Dest d;
-    __shared__ __align__(16) float2 tab[kTile * 64];
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
-    const int tid = threadIdx.x, TB = p.tile.tokens(), hl = p.tile.lanes();
-    const int t0 = blockIdx.x * TB, tl = p.tile.token(tid), t = t0 + tl;
-    const bool in = t < p.N;
-    const Channels ch(p.rot, p.tile.vec(tid));
-    const int heads = Q4 ? p.Hq : p.Hq + 2 * p.Hkv;    // of q, then K, then V
-    // row h is at base + h stride of its tensor
-    const T *const sq = static_cast<const T *>(p.q) + t * p.q_st[0] + ch.a;
-    const T *const sk = static_cast<const T *>(p.kn) + t * p.kn_st[0] - p.Hq * p.kn_st[1] + ch.a;
-    const T *const sv = static_cast<const T *>(p.vn) + t * p.vn_st[0] - (p.Hq + p.Hkv) * p.vn_st[1] + ch.a;
-    const int apart = ch.b - ch.a;
-    Row8<T> va[U], vb[U];
-    auto load = [&](int h0) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * hl;
-            if (!in || h >= heads) continue;
-            const bool is_q = Q4 || h < p.Hq, is_k = h < p.Hq + p.Hkv;
-            const T *src = (is_q ? sq : is_k ? sk : sv) + h * (is_q ? p.q_st[1] : is_k ? p.kn_st[1] : p.vn_st[1]);
-            va[u].load(src);
-            vb[u].load(src + apart);
-        }
-    };
-    load(p.tile.lane(tid));                            // on the way while their places are looked up
+// Looks up where the tile's tokens go, and the angles of their positions.
+__device__ __forceinline__ void find_places(const AppendRows &p, Dest &d, float2 *tab, int t0) {
+    const int tid = threadIdx.x, TB = p.tile.tokens();
     if (p.cu) {
         find_sequences(d, p.cu, p.seq_len, p.B, p.N, t0, TB, p.err);
     } else if (tid < TB) {
@@ -260,93 +238,176 @@ __global__ void __launch_bounds__(kThreads, kPerSm) append_rows_kernel(const App
         fill_turns(p.rot, tab, TB, [&](int i) { return d.pos[i]; });
         __syncthreads();
     }
-    const bool known = in && d.pos[tl] >= 0;
-    const long long page = d.page[tl], row = d.row[tl];
-    const bool stored = in && page >= 0;
-    const int step = p.rot.rot / 16;                   // lanes that rotate
-    const float4 *turns = reinterpret_cast<const float4 *>(tab) + tl * (p.rot.rot / 4) + p.tile.vec(tid);
-    T *const dq = static_cast<T *>(p.qo) + t * p.qo_st[0] + ch.a;
-    T *const dk = static_cast<T *>(p.k) + page * p.k_st[0] + row * p.k_st[2] - p.Hq * p.k_st[1] + ch.a;
-    T *const dv = static_cast<T *>(p.v) + page * p.v_st[0] + row * p.v_st[2] - (p.Hq + p.Hkv) * p.v_st[1] + ch.a;
-#pragma unroll 1
-    for (int h0 = p.tile.lane(tid); h0 < heads; h0 += U * hl) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * hl;
-            const bool is_q = Q4 || h < p.Hq, is_k = h < p.Hq + p.Hkv;
-            if (h >= heads || !(is_q ? known : stored)) continue;
-            if (ch.turns && (is_q || is_k)) rotate16<T>(turns, step, p.rot.interleaved, va[u], vb[u]);
-            T *dst = (is_q ? dq : is_k ? dk : dv) + h * (is_q ? p.qo_st[1] : is_k ? p.k_st[1] : p.v_st[1]);
-            va[u].store(dst);
-            vb[u].store(dst + apart);
-        }
-        if (h0 + U * hl < heads) load(h0 + U * hl);
-    }
-    if constexpr (Q4) {
+}
+
+// Rows of K and V into a cache held in 4 bits: D / 8 lanes each, so that 4 neighbours
+// hold a group of 32 channels; the partners of a rotated half are read a second time.
+// The rows of a thread's next two heads are on the way while one's are coded.
+template <typename T>
+struct CodedRows {
+    const AppendRows &p;
+    const T *kn, *vn;
+    int c0, token, first, step, other;                 // channels, token, heads of the thread
+    bool in, rotated;
+    Row8<T> k[2], kp[2], v[2];
+
+    __device__ __forceinline__ CodedRows(const AppendRows &p_, int t0) : p(p_) {
         const Tile fine = p.tile.finer();
-        const int vec = fine.vec(tid), c0 = vec * 8, g = vec >> 2, pl = vec & 3, fl = fine.token(tid);
-        const bool rotated = c0 < p.rot.rot, inter = p.rot.interleaved;
-        const bool upper = !inter && c0 >= p.rot.rot / 2;
-        const int other = inter ? c0 : upper ? c0 - p.rot.rot / 2 : c0 + p.rot.rot / 2;
+        c0 = fine.vec(threadIdx.x) * 8;
+        token = fine.token(threadIdx.x);
+        first = fine.lane(threadIdx.x);
+        step = fine.lanes();
+        in = t0 + token < p.N;
+        rotated = c0 < p.rot.rot;
+        const int half = p.rot.rot / 2;
+        other = !rotated || p.rot.interleaved ? 0 : c0 >= half ? -half : half;
+        kn = static_cast<const T *>(p.kn) + (t0 + token) * p.kn_st[0] + first * p.kn_st[1] + c0;
+        vn = static_cast<const T *>(p.vn) + (t0 + token) * p.vn_st[0] + first * p.vn_st[1] + c0;
+        load(0, first);
+        load(1, first + step);
+    }
+    __device__ __forceinline__ void load(int u, int h) {
+        if (in && h < p.Hkv) {
+            k[u].load(kn);
+            if (other != 0) kp[u].load(kn + other);
+            v[u].load(vn);
+        }
+        kn += step * p.kn_st[1];
+        vn += step * p.vn_st[1];
+    }
+    // All lanes take every step: their neighbours' values pass by shuffles.
+    __device__ __forceinline__ void run(const Dest &d, const float2 *tab) {
+        const int rot = p.rot.rot, g = c0 >> 5, pl = (c0 >> 3) & 3;
+        const bool inter = p.rot.interleaved, upper = other < 0;
         // y = x c + partner s, s of either sign
         float c[8], s[8];
         if (rotated) {
-            const float2 *w = tab + fl * (p.rot.rot / 2);
+            const float2 *w = tab + token * (rot / 2);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float2 x = w[turn_at(p.rot.rot, inter ? (c0 + i) / 2 : (upper ? other : c0) + i)];
+                const float2 x = w[turn_at(rot, inter ? (c0 + i) / 2 : (upper ? c0 + other : c0) + i)];
                 c[i] = x.x;
                 s[i] = (inter ? i & 1 : upper) ? x.y : -x.y;
             }
         }
-        const int tf = t0 + fl;
-        const long long fp = d.page[fl];
-        const bool keep = tf < p.N && fp >= 0;
-        uint8_t *to = static_cast<uint8_t *>(p.k) + (keep ? fp * p.k_st[0] + d.row[fl] * p.k_st[2] : 0);
-        const T *kn = static_cast<const T *>(p.kn) + tf * p.kn_st[0], *vn = static_cast<const T *>(p.vn) + tf * p.vn_st[0];
-        // every lane takes every step: its neighbours' values pass by shuffles
-        constexpr int V = 2;
-        for (int h0 = 0; h0 < p.Hkv; h0 += V * fine.lanes()) {
-            Row8<T> k[V], kp[V], v[V];
+        const long long page = d.page[token];
+        const bool keep = in && page >= 0;
+        uint8_t *to = static_cast<uint8_t *>(p.k) + (keep ? page * p.k_st[0] + d.row[token] * p.k_st[2] : 0) +
+                      first * p.k_st[1];
+        const int at_k = pl * (p.D / 8) + 4 * g, at_v = p.D / 2 + (2 * pl + (g & 1)) * (p.D / 16) + 2 * (g & ~1);
+        const uint32_t order = g & 1 ? 0x3276u : 0x5410u;
+        auto code = [&](int u, int h) {
+            float x[8], inv;
+            k[u].get(x);
+            if (rotated) {
+                float y[8];
+                if (inter) {
 #pragma unroll
-            for (int u = 0; u < V; ++u) {
-                const int h = h0 + fine.lane(tid) + u * fine.lanes();
-                if (!keep || h >= p.Hkv) continue;
-                k[u].load(kn + h * p.kn_st[1] + c0);
-                if (rotated && !inter) kp[u].load(kn + h * p.kn_st[1] + other);
-                v[u].load(vn + h * p.vn_st[1] + c0);
-            }
-#pragma unroll
-            for (int u = 0; u < V; ++u) {
-                const int h = h0 + fine.lane(tid) + u * fine.lanes();
-                float x[8], y[8], inv;
-                k[u].get(x);
-                if (rotated) {
-                    float z[8];
-                    if (!inter) kp[u].get(y);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) z[i] = fmaf(inter ? x[i ^ 1] : y[i], s[i], x[i] * c[i]);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = z[i];
+                    for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
+                } else {
+                    kp[u].get(y);
                 }
-                const T sk = q4_scale<T>(x, inv);
-                const uint32_t wk = q4_codes(x, inv);
-                v[u].get(x);
-                const T sv = q4_scale<T>(x, inv);
-                const uint32_t wv = q4_codes(x, inv);
-                // V: words of two neighbouring groups, one of this lane's own and one of the
-                // lane of the other group that holds the same channels of it
-                const uint32_t o = __shfl_xor_sync(0xffffffffu, wv, 4);
-                if (!keep || h >= p.Hkv) continue;
-                uint8_t *r = to + h * p.k_st[1];
-                *reinterpret_cast<uint32_t *>(r + pl * (p.D / 8) + 4 * g) = wk;
-                *reinterpret_cast<uint32_t *>(r + p.D / 2 + (2 * pl + (g & 1)) * (p.D / 16) + 2 * (g & ~1)) =
-                    g & 1 ? __byte_perm(o, wv, 0x7632) : __byte_perm(wv, o, 0x5410);
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    ptx::ffma2(x[i], x[i + 1], x[i], x[i + 1], c[i], c[i + 1], -0.f, -0.f);
+                    ptx::ffma2(x[i], x[i + 1], y[i], y[i + 1], s[i], s[i + 1], x[i], x[i + 1]);
+                }
+            }
+            const T sk = q4_scale<T>(q4_best(x), inv);
+            const uint32_t wk = q4_codes<H16F<T>::f16>(x, inv);
+            const T sv = q4_scale<T>(q4_best<T>(v[u].u), inv);
+            v[u].get(x);
+            const uint32_t wv = q4_codes<H16F<T>::f16>(x, inv);
+            // V: words of two neighbouring groups, one of this lane's own and one of the
+            // lane of the other group that holds the same channels of it
+            const uint32_t o = __shfl_xor_sync(0xffffffffu, wv, 4);
+            if (keep && h < p.Hkv) {
+                *reinterpret_cast<uint32_t *>(to + at_k) = wk;
+                *reinterpret_cast<uint32_t *>(to + at_v) = __byte_perm(wv, o, order);
                 if (pl == 0) {
-                    *reinterpret_cast<T *>(r + p.D + 2 * g) = sk;
-                    *reinterpret_cast<T *>(r + p.D + p.D / 16 + 2 * g) = sv;
+                    *reinterpret_cast<T *>(to + p.D + 2 * g) = sk;
+                    *reinterpret_cast<T *>(to + p.D + p.D / 16 + 2 * g) = sv;
                 }
             }
+            to += step * p.k_st[1];
+        };
+#pragma unroll 1
+        for (int h = first; h - first < p.Hkv; h += 2 * step) {
+            code(0, h);
+            if (h + step - first >= p.Hkv) break;
+            load(0, h + 2 * step);
+            code(1, h + step);
+            load(1, h + 3 * step);
+        }
+    }
+};
+
+// Rows of q, and of K and V into a 16-bit or fp32 cache: D / 16 lanes each.  Q4: K and V
+// as CodedRows, in CTAs of their own where no CTA may see another's new lengths.
+template <typename T, bool Q4>
+__global__ void __launch_bounds__(kThreads, kPerSm) append_rows_kernel(const AppendRows p) {
+    constexpr int U = sizeof(T) == 4 ? 2 : 4;
+    __shared__ Dest d;
+    __shared__ __align__(16) float2 tab[kTile * 64];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int tid = threadIdx.x, TB = p.tile.tokens();
+    const bool two = Q4 && p.apart;                    // odd CTAs: K and V, even ones: q
+    const int t0 = (two ? blockIdx.x >> 1 : blockIdx.x) * TB;
+    if (Q4 && (p.Hq == 0 || (two && (blockIdx.x & 1)))) {
+        if constexpr (Q4) {
+            CodedRows<T> rows(p, t0);                  // on the way while their places are looked up
+            find_places(p, d, tab, t0);
+            rows.run(d, tab);
+        }
+    } else {
+        const int hl = p.tile.lanes(), tl = p.tile.token(tid), t = t0 + tl;
+        const bool in = t < p.N;
+        const Channels ch(p.rot, p.tile.vec(tid));
+        const int heads = Q4 ? p.Hq : p.Hq + 2 * p.Hkv;    // of q, then K, then V
+        // row h is at base + h stride of its tensor
+        const T *const sq = static_cast<const T *>(p.q) + t * p.q_st[0] + ch.a;
+        const T *const sk = static_cast<const T *>(p.kn) + t * p.kn_st[0] - p.Hq * p.kn_st[1] + ch.a;
+        const T *const sv = static_cast<const T *>(p.vn) + t * p.vn_st[0] - (p.Hq + p.Hkv) * p.vn_st[1] + ch.a;
+        const int apart = ch.b - ch.a;
+        Row8<T> va[U], vb[U];
+        auto load = [&](int h0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int h = h0 + u * hl;
+                if (!in || h >= heads) continue;
+                const bool is_q = Q4 || h < p.Hq, is_k = h < p.Hq + p.Hkv;
+                const T *src = (is_q ? sq : is_k ? sk : sv) + h * (is_q ? p.q_st[1] : is_k ? p.kn_st[1] : p.vn_st[1]);
+                va[u].load(src);
+                vb[u].load(src + apart);
+            }
+        };
+        load(p.tile.lane(tid));                        // on the way while their places are looked up
+        find_places(p, d, tab, t0);
+        const bool known = in && d.pos[tl] >= 0;
+        const long long page = d.page[tl], row = d.row[tl];
+        const bool stored = in && page >= 0;
+        const int step = p.rot.rot / 16;               // lanes that rotate
+        const float4 *turns = reinterpret_cast<const float4 *>(tab) + tl * (p.rot.rot / 4) + p.tile.vec(tid);
+        T *const dq = static_cast<T *>(p.qo) + t * p.qo_st[0] + ch.a;
+        T *const dk = static_cast<T *>(p.k) + page * p.k_st[0] + row * p.k_st[2] - p.Hq * p.k_st[1] + ch.a;
+        T *const dv = static_cast<T *>(p.v) + page * p.v_st[0] + row * p.v_st[2] - (p.Hq + p.Hkv) * p.v_st[1] + ch.a;
+#pragma unroll 1
+        for (int h0 = p.tile.lane(tid); h0 < heads; h0 += U * hl) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int h = h0 + u * hl;
+                const bool is_q = Q4 || h < p.Hq, is_k = h < p.Hq + p.Hkv;
+                if (h >= heads || !(is_q ? known : stored)) continue;
+                if (ch.turns && (is_q || is_k)) rotate16<T>(turns, step, p.rot.interleaved, va[u], vb[u]);
+                T *dst = (is_q ? dq : is_k ? dk : dv) + h * (is_q ? p.qo_st[1] : is_k ? p.k_st[1] : p.v_st[1]);
+                va[u].store(dst);
+                vb[u].store(dst + apart);
+            }
+            if (h0 + U * hl < heads) load(h0 + U * hl);
+        }
+        if constexpr (Q4) {
+            if (!two) CodedRows<T>(p, t0).run(d, tab);
         }
     }
     // one token per sequence: no other CTA reads this length
@@ -504,7 +565,8 @@ attn_status_t append_rows(const Ctx &c, attn_dtype_t dt, const RowsAppend &a) {
     // (a 4-bit row costs more per token than its angles do)
     p.tile = make_tile(a.D, a.N, a.q4 ? imax(a.Hq, 2 * a.Hkv) : a.Hq + 2 * a.Hkv, (a.q4 ? 2ll : 8ll) * c.sm_count);
     p.err = c.err;
-    const dim3 grid(unsigned(cdiv(a.N, p.tile.tokens())));
+    p.apart = a.q4 && a.q && (a.cu || !a.advance);     // (else a CTA advances the lengths it has read)
+    const dim3 grid(unsigned(cdiv(a.N, p.tile.tokens())) * (p.apart ? 2 : 1));
     attn_status_t st;
     if (a.q4)
         st = dt == ATTN_F16 ? launch(c, kFamKvPages, append_rows_kernel<__half, true>, grid, p)

@@ -11,6 +11,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace attn {
 
@@ -147,91 +148,145 @@ __device__ __forceinline__ void rotate16(const float4 *tab, int step, bool inter
 
 __device__ __forceinline__ int q4_row_bytes(int D) { return D + D / 8; }
 
-// The scale of the group whose values 4 neighbouring lanes hold, 8 each; the
-// factor that turns values into codes.
-template <typename T>
-__device__ __forceinline__ T q4_scale(const float (&x)[8], float &inv) {
-    float hi = x[0], lo = x[0], z = 0.f * x[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) {
-        hi = fmaxf(hi, x[i]);
-        lo = fminf(lo, x[i]);
-        z = fmaf(0.f, x[i], z);                        // NaN if a value is infinite or NaN
-    }
+// Pairs of the 16-bit types.
+template <typename T> struct H16F;
+template <> struct H16F<__half> {
+    static constexpr bool f16 = true;
+    using P = __half2;
+    static __device__ __forceinline__ P pair(uint32_t x) { return *reinterpret_cast<P *>(&x); }
+    static __device__ __forceinline__ P same(__half x) { return __half2half2(x); }
+    static __device__ __forceinline__ P same(float x) { return __floats2half2_rn(x, x); }
+};
+template <> struct H16F<__nv_bfloat16> {
+    static constexpr bool f16 = false;
+    using P = __nv_bfloat162;
+    static __device__ __forceinline__ P pair(uint32_t x) { return *reinterpret_cast<P *>(&x); }
+    static __device__ __forceinline__ P same(__nv_bfloat16 x) { return __bfloat162bfloat162(x); }
+    static __device__ __forceinline__ P same(float x) { return __floats2bfloat162_rn(x, x); }
+};
+template <typename P> __device__ __forceinline__ uint32_t pair_bits(P x) { return *reinterpret_cast<uint32_t *>(&x); }
+
+// Largest and least, NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// x* of the group whose values 4 neighbouring lanes hold, 8 each; NaN if one of them is,
+// infinite if one is.
+__device__ __forceinline__ float q4_best(const float (&x)[8]) {
+    float hi = max_nan(max_nan(x[0], x[1], x[2]), max_nan(x[3], x[4], x[5]), max_nan(x[6], x[7]));
+    float lo = min_nan(min_nan(x[0], x[1], x[2]), min_nan(x[3], x[4], x[5]), min_nan(x[6], x[7]));
 #pragma unroll
     for (int off = 1; off < 4; off <<= 1) {
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-        z += __shfl_xor_sync(0xffffffffu, z, off);
+        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
     }
+    return hi >= -lo ? hi : lo;
+}
+
+// The same of values as they lie in memory: pairs, and then the largest and the negative
+// of the least side by side.
+template <typename T>
+__device__ __forceinline__ float q4_best(const uint4 &u) {
+    using H = H16F<T>;
+    const auto a = H::pair(u.x), b = H::pair(u.y), c = H::pair(u.z), d = H::pair(u.w);
+    const uint32_t hi = pair_bits(__hmax2_nan(__hmax2_nan(a, b), __hmax2_nan(c, d)));
+    const uint32_t lo = pair_bits(__hmin2_nan(__hmin2_nan(a, b), __hmin2_nan(c, d))) ^ 0x80008000u;
+    auto m = __hmax2_nan(H::pair(__byte_perm(hi, lo, 0x5410)), H::pair(__byte_perm(hi, lo, 0x7632)));
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1)
+        m = __hmax2_nan(m, H::pair(__shfl_xor_sync(0xffffffffu, pair_bits(m), off)));
+    const uint32_t w = pair_bits(m);
+    const float x = H16<H::f16>::lo(w), y = H16<H::f16>::hi(w);
+    return x >= y ? x : -y;
+}
+
+// The scale of a group with that x*, and the factor that turns values into codes.
+template <typename T>
+__device__ __forceinline__ T q4_scale(float best, float &inv) {
     T s;
-    Elem<T>::store(&s, (hi >= -lo ? hi : lo) * -0.125f + z);
+    Elem<T>::store(&s, best * -0.125f);
     float f = Elem<T>::load(&s);
+    if (!(fabsf(f) < INFINITY)) {
+        f = NAN;
+        Elem<T>::store(&s, f);
+    }
     if (fabsf(f) < 0x1p-126f) {                        // a subnormal bf16 has no reciprocal
-        Elem<T>::store(&s, 0.f);
         f = 0.f;
+        Elem<T>::store(&s, f);
     }
     inv = f == 0.f ? 0.f : 1.f / f;
     return s;
 }
 
-// Pairs of the 16-bit types.
-template <typename T> struct H16F;
-template <> struct H16F<__half> {
-    static constexpr bool f16 = true;
-    static __device__ __forceinline__ uint32_t minus24(uint32_t x) {
-        const __half2 r = __hsub2(*reinterpret_cast<__half2 *>(&x), __floats2half2_rn(24.f, 24.f));
-        return *reinterpret_cast<const uint32_t *>(&r);
-    }
-    static __device__ __forceinline__ uint32_t mul(uint32_t x, __half s) {
-        const __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&x), __half2half2(s));
-        return *reinterpret_cast<const uint32_t *>(&r);
-    }
-};
-template <> struct H16F<__nv_bfloat16> {
-    static constexpr bool f16 = false;
-    static __device__ __forceinline__ uint32_t minus24(uint32_t x) {
-        const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&x), __floats2bfloat162_rn(24.f, 24.f));
-        return *reinterpret_cast<const uint32_t *>(&r);
-    }
-    static __device__ __forceinline__ uint32_t mul(uint32_t x, __nv_bfloat16 s) {
-        const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&x), __bfloat162bfloat162(s));
-        return *reinterpret_cast<const uint32_t *>(&r);
-    }
-};
-
 // The two 16-bit words of 8 channels' codes, the first in the low half.  1.5 2^23 + 8
 // is added so that rint(x inv) + 8 stands in the sum's last bits.
+template <bool F16>
 __device__ __forceinline__ uint32_t q4_codes(const float (&x)[8], float inv) {
     uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float n = fminf(fmaxf(x[i] * inv, -8.f), 7.f);       // NaN: -8
-        w += __float_as_uint(n + 12582920.f) << (4 * i);
+    for (int i = 0; i < 8; i += 2) {
+        float a, b;
+        ptx::ffma2(a, b, x[i], x[i + 1], inv, inv, -0.f, -0.f);
+        a = fminf(a, 7.f);
+        b = fminf(b, 7.f);
+        if (F16) {                                     // (a normal s leaves nothing below -8.5)
+            a = fmaxf(a, -8.f);
+            b = fmaxf(b, -8.f);
+        }
+        ptx::fadd2(a, b, a, b, 12582920.f, 12582920.f);
+        w += (__float_as_uint(a) << (4 * i)) + (__float_as_uint(b) << (4 * i + 4));
     }
     w -= 0x4b400000u * 0x11111111u;
+    w = inv == inv ? w : 0u;                           // a group of NaN
     return ((w >> 2) & 0x3fff3fffu) | ((w << 14) & 0xc000c000u);
+}
+
+// x & mask | bits in one instruction (as two constants it would be two).
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(x), "r"(mask), "r"(bits));
+    return d;
 }
 
 // The values of 8 codes in the 16-bit type: n - 8 is exact in either, so one product
 // rounds once.
 template <typename T>
 __device__ __forceinline__ uint4 q4_values(uint32_t w, T scale) {
+    using H = H16F<T>;
     const uint32_t y = __byte_perm(w, 0, 0x2301);
-    uint32_t c[4];                                     // channels (i, i + 4) as 16 + n
-    if constexpr (H16F<T>::f16) {
-        c[0] = (y & 0x03c003c0u) | 0x4c004c00u;
-        c[1] = ((w << 4) & 0x03c003c0u) | 0x4c004c00u;
-        c[2] = (w & 0x03c003c0u) | 0x4c004c00u;
-        c[3] = ((y << 4) & 0x03c003c0u) | 0x4c004c00u;
+    uint32_t c[4];                                     // channels (i, i + 4) as 16 + n (f16), 32 + n (bf16)
+    if constexpr (H::f16) {
+        c[0] = and_or(y, 0x03c003c0u, 0x4c004c00u);
+        c[1] = and_or(w << 4, 0x03c003c0u, 0x4c004c00u);
+        c[2] = and_or(w, 0x03c003c0u, 0x4c004c00u);
+        c[3] = and_or(y << 4, 0x03c003c0u, 0x4c004c00u);
     } else {
-        c[0] = ((y >> 3) & 0x00780078u) | 0x41804180u;
-        c[1] = ((w << 1) & 0x00780078u) | 0x41804180u;
-        c[2] = ((w >> 3) & 0x00780078u) | 0x41804180u;
-        c[3] = ((y << 1) & 0x00780078u) | 0x41804180u;
+        c[0] = and_or(y >> 4, 0x003c003cu, 0x42004200u);
+        c[1] = and_or(w, 0x003c003cu, 0x42004200u);
+        c[2] = and_or(w >> 4, 0x003c003cu, 0x42004200u);
+        c[3] = and_or(y, 0x003c003cu, 0x42004200u);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = H16F<T>::mul(H16F<T>::minus24(c[i]), scale);
+    for (int i = 0; i < 4; ++i)
+        c[i] = pair_bits(__hmul2(__hsub2(H::pair(c[i]), H::same(H::f16 ? 24.f : 40.f)), H::same(scale)));
     return make_uint4(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410),
                       __byte_perm(c[0], c[1], 0x7632), __byte_perm(c[2], c[3], 0x7632));
 }
