@@ -26,6 +26,8 @@
 // product instead of multiplying by zero.
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "packed.cuh"
@@ -44,10 +46,14 @@ struct WinParams {
     void *o;
     int Nq, Nkv, off, window, sinks, H, group;
     float qscale;            // scale * log2(e)
-    PackedSeqs seqs;         // packed: the sequences' starts (Nq, Nkv, off unused)
-    unsigned *err;
     TensorStrides sq, sk, sv, so;
 };
+
+struct PackedParams : WinParams {    // Nq, Nkv, off unused
+    PackedSeqs seqs;         // the sequences' starts
+    unsigned *err;
+};
+template <bool PACKED> using ParamsOf = std::conditional_t<PACKED, PackedParams, WinParams>;
 
 template <int D>
 struct WinSmem {
@@ -109,7 +115,7 @@ template <int N> __device__ __forceinline__ void read(const float *p, float (&x)
 // PACKED: sequences of different lengths one behind the other; every warp finds the
 // CTA's block of rows (packed.cuh).
 template <typename T, int D, bool PACKED>
-__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) simt_window_kernel(const WinParams p) {
+__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) simt_window_kernel(const ParamsOf<PACKED> p) {
     using S = WinSmem<D>;
     constexpr int CH = D / 32;
     extern __shared__ float sm[];
@@ -380,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) simt_window_kernel
 }
 
 template <typename T, int D, bool PACKED>
-attn_status_t launch_win(const Ctx &c, const WinParams &p, int tiles, int BH) {
+attn_status_t launch_win(const Ctx &c, const ParamsOf<PACKED> &p, int tiles, int BH) {
     static int done_mask = 0;
     auto kern = simt_window_kernel<T, D, PACKED>;
     if (!ensure_smem_attr(reinterpret_cast<const void *>(kern), WinSmem<D>::BYTES, c.device, &done_mask))
@@ -390,14 +396,14 @@ attn_status_t launch_win(const Ctx &c, const WinParams &p, int tiles, int BH) {
 }
 
 template <typename T, bool PACKED>
-attn_status_t dispatch_d(const Ctx &c, int D, const WinParams &p, int tiles, int BH) {
+attn_status_t dispatch_d(const Ctx &c, int D, const ParamsOf<PACKED> &p, int tiles, int BH) {
     if (D == 32) return launch_win<T, 32, PACKED>(c, p, tiles, BH);
     if (D == 64) return launch_win<T, 64, PACKED>(c, p, tiles, BH);
     return launch_win<T, 128, PACKED>(c, p, tiles, BH);
 }
 
 template <bool PACKED>
-attn_status_t dispatch_win(const Ctx &c, attn_dtype_t dt, int D, const WinParams &p, int tiles, int BH) {
+attn_status_t dispatch_win(const Ctx &c, attn_dtype_t dt, int D, const ParamsOf<PACKED> &p, int tiles, int BH) {
     if (dt == ATTN_F32) return dispatch_d<float, PACKED>(c, D, p, tiles, BH);
     if (dt == ATTN_F16) return dispatch_d<__half, PACKED>(c, D, p, tiles, BH);
     return dispatch_d<__nv_bfloat16, PACKED>(c, D, p, tiles, BH);
@@ -424,7 +430,7 @@ attn_status_t simt_causal_window(const Ctx &c, attn_dtype_t dt, const void *q, c
 }
 
 attn_status_t simt_causal_varlen(const Ctx &c, attn_dtype_t dt, const VarlenArgs &a) {
-    WinParams p{};
+    PackedParams p{};
     p.q = a.q; p.k = a.k; p.v = a.v; p.o = a.o;
     p.window = a.window;
     p.sinks = a.sinks;
