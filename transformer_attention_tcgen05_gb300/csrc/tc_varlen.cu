@@ -488,6 +488,7 @@ tc_varlen_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                         ptx::mbar_arrive(&bars->v_full[r]);
                     }
                 }
+                __syncwarp();
                 if (lane == 0) {
                     ptx::mbar_arrive(&bars->checked[s]);
                     ptx::mbar_arrive(&bars->item_empty[s]);
@@ -599,6 +600,7 @@ tc_varlen_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                     ok = false;
                 }
             }
+            __syncwarp();                            // (every lane has read the item)
             if (lane == 0) ptx::mbar_arrive(&bars->item_empty[s]);
         }
     }
