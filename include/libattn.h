@@ -319,7 +319,8 @@ ATTN_API attn_status_t attn_causal_gqa_window_fwd(const void *q, const void *k, 
  *   outside every sequence are left as they were.  A sequence with more queries
  *   than keys, or whose starts do not rise or pass Nq / Nkv, sets
  *   ATTN_ERR_DEVICE_CHECK and its rows of o are left as they were (but for rows
- *   that another sequence, whose own starts rise, claims as well).
+ *   that another sequence, whose own starts rise, claims as well).  Starts that
+ *   fall may leave other sequences' rows as they were, too.
  *   The lengths are read on the device: Nq and Nkv are the arrays' extents, and
  *   a captured call serves any lengths within them.  bf16 and f16 run on the
  *   tensor cores for D in {64, 128}; fp32 (and the 16-bit types with D = 32) on

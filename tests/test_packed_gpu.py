@@ -786,6 +786,26 @@ def test_varlen_sequences_that_cannot_be_are_reported(ta):
         assert ta.device_status() == 0 and (o == 7).all()
 
 
+@pytest.mark.parametrize("dt,Hq,Hkv,D,window", [("bf16", 4, 2, 128, 0), ("f16", 3, 1, 64, 60), ("f32", 2, 1, 64, 0)])
+def test_varlen_more_sequences_than_a_warp_holds(ta, dt, Hq, Hkv, D, window):
+    """Empty ones at either end and in runs, long ones among them, rows before and behind;
+    a bad one at the far end leaves the others as they were."""
+    g = torch.Generator().manual_seed(44)
+    lens = ([0] * 40 + [1, 700, 0, 33, 128, 129, 0, 0, 5] + [17, 0, 64] * 30 + [300, 0, 31] + [0] * 35) * 2
+    past = [(3 * i) % 50 if n else 0 for i, n in enumerate(lens)]
+    q, cu_q = packed(g, dt, lens, Hq, D, 140, 70)
+    k, cu_k = packed(g, dt, [n + m for n, m in zip(lens, past)], Hkv, D, 3, 2)
+    v, _ = packed(g, dt, [n + m for n, m in zip(lens, past)], Hkv, D, 3, 2)
+    o = torch.full_like(q, 7.0)
+    ta.causal_gqa_varlen_fwd(q, k, v, cu_q, cu_k, window=window, o=o)
+    assert ta.device_status() == 0 and (o[:140] == 7).all() and (o[-70:] == 7).all()
+    check_varlen(dt, q, k, v, cu_q, cu_k, o, window, 0, [0, 15, 16, 31, 32, 127, 128, 129, 511, 512, -1])
+    bad, again = cu_q.clone(), torch.full_like(q, 7.0)
+    bad[-1] += 1000                                      # past the rows, and more queries than keys
+    ta.causal_gqa_varlen_fwd(q, k, v, bad, cu_k, window=window, o=again)
+    assert ta.device_status() == 6 and torch.equal(again, o)
+
+
 @pytest.mark.parametrize("dt,D", [("bf16", 64), ("f32", 64)])
 def test_varlen_sequences_that_overlap(ta, dt, D):
     """The same rows claimed over and over: more blocks than the rows can have.  What is

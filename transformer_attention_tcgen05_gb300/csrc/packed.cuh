@@ -3,18 +3,24 @@
 // and the SIMT attention kernels).
 //
 // Sequence b has n queries, the last of its t keys.  Its rows are cut into blocks
-// of BS; block i starts at position t - n + i BS and has the level (t - n) / BS + i,
-// which grows with the keys that it reads.  Blocks are numbered by falling level, and
-// within one by sequence, so that the longest start first.  The block of a number
-// is found by bisection: with F(L) the blocks of level L or more, it lies in the
-// largest L with F(L) > number.  One warp, 32 sequences at a time, of which the first
-// 64 stay in registers (16 sequences: 1.0 to 1.4 us to a block's rows, which a kernel
-// hides behind the block before).  No list is written, so a call needs no workspace and
-// one launch.
+// of BS; block i starts at position t - n + i BS.
 //
-// Sequences whose starts do not rise have no rows and are reported.  Such starts may
-// make others overlap, in any number: no sum passes kMost per lane, and no more blocks
-// are given out than disjoint sequences can have.
+// Up to 64 sequences, which a warp holds in registers: a block has the level (t - n) / BS
+// + i, which grows with the keys that it reads.  Blocks are numbered by falling level,
+// and within one by sequence, so that the longest start first.  The block of a number
+// is found by bisection: with F(L) the blocks of level L or more, it lies in the
+// largest L with F(L) > number (16 sequences: 1.0 to 1.4 us to a block's rows, which a
+// kernel hides behind the block before).
+//
+// More of them: in the order of the sequences, those of b from number cu_q[b] / BS + b on.
+// That leaves each at least as many numbers as it has blocks, and one at most empty, so
+// that a search among the starts themselves finds a number, 32 probes at a time (two to
+// four rounds).  (By levels, where every step of the bisection goes over all sequences,
+// 4096 prompts of 20 tokens, 32 heads, took 8054 us; now 1845.)
+//
+// No list is written, so a call needs no workspace and one launch.  Sequences whose
+// starts do not rise have no rows and are reported; others of such a call may go without
+// theirs, where they overlap or stand behind those.
 #pragma once
 
 #include "common.cuh"
@@ -24,71 +30,96 @@ namespace attn {
 struct PackedSeqs {
     const int32_t *cu_q, *cu_k;
     int B, Nq, Nkv;
-    int most;                              // blocks that disjoint sequences can have, at most kMost
+    int most;                              // numbers that disjoint sequences can need (BlockFinder::most)
 };
 
 struct PackedBlock {
     int q_row, nq, k_row, nkv;             // the sequence's rows
-    int q0;                                // first query of the block, within the sequence
+    int q0;                                // first query of the block, within the sequence (>= nq: none)
 };
 
 class BlockFinder {
-    static constexpr int kMost = 1 << 25;  // (of 32 lanes together: 2^30)
-
   public:
+    static constexpr int kFew = 64;
+
+    // The numbers that sequences of Nq queries together can need.
+    static long long most(int B, int Nq, int bs) {
+        return B > kFew ? (long long)Nq / bs + B : (Nq + (long long)imin(B, Nq) * (bs - 1)) / bs;
+    }
+
     // All lanes of a warp; report: invalid sequences set the device error word.
     __device__ __forceinline__ BlockFinder(const PackedSeqs &s, int bs_log, bool report, unsigned *err)
         : s_(s), log_(bs_log), lane_(threadIdx.x & 31) {
         bool wrong = false;
-        int top = 0, sum = 0;
+        int sum;
         first_ = load(lane_, wrong);
         second_ = load(lane_ + 32, wrong);
-        top = imax(first_.level + first_.blocks, second_.level + second_.blocks);
-        sum = first_.blocks + second_.blocks;
-        for (int b = lane_ + 64; b < s_.B; b += 32) {
-            const Seq q = load(b, wrong);
-            top = imax(top, q.level + q.blocks);
-            sum = imin(sum + q.blocks, kMost);
+        if (s_.B <= kFew) {
+            top_ = __reduce_max_sync(0xffffffffu,
+                                     imax(first_.level + first_.blocks, second_.level + second_.blocks));
+            sum = __reduce_add_sync(0xffffffffu, first_.blocks + second_.blocks);
+        } else {
+            top_ = 0;
+            sum = number_of(s_.B);
+            if (report)
+#pragma unroll 4
+                for (int b = lane_ + kFew; b < s_.B; b += 32) load(b, wrong);
         }
         if (report && wrong) raise_device_error(err, kDevCheck);
-        top_ = __reduce_max_sync(0xffffffffu, top);
-        total = imin(__reduce_add_sync(0xffffffffu, sum), s_.most);
+        total = imax(0, imin(sum, s_.most));           // (starts that do not rise: anything)
     }
 
-    int total;                             // blocks to work on
+    int total;                             // numbers given out
 
-    // The block of a number below `total`.
+    // The block of a number below `total`; q0 >= nq: there is none.
     __device__ __forceinline__ PackedBlock find(int number) const {
-        int lo = 0, hi = top_;             // F(lo) > number >= F(hi)
-        int behind = 0;                    // F(hi)
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1, f = from_level(mid);
-            if (f > number) {
-                lo = mid;
-            } else {
-                hi = mid;
-                behind = f;
+        int b, q0;
+        if (s_.B <= kFew) {
+            int lo = 0, hi = top_;         // F(lo) > number >= F(hi)
+            int behind = 0;                // F(hi)
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                const int f = __reduce_add_sync(0xffffffffu, from(first_, mid) + from(second_, mid));
+                if (f > number) {
+                    lo = mid;
+                } else {
+                    hi = mid;
+                    behind = f;
+                }
             }
-        }
-        int left = number - behind;        // blocks of this level before ours
-        for (int b0 = 0;; b0 += 32) {      // one of the sequences has it
-            const Seq q = get(b0 + lane_);
-            const unsigned here = __ballot_sync(0xffffffffu, lo >= q.level && lo < q.level + q.blocks);
+            int left = number - behind;    // blocks of this level before ours
+            unsigned here = __ballot_sync(0xffffffffu, has(first_, lo));
             const int n = __popc(here);
-            if (left >= n && b0 + 32 < s_.B) {
+            b = 0;
+            if (left >= n) {
                 left -= n;
-                continue;
+                here = __ballot_sync(0xffffffffu, has(second_, lo));
+                b = 32;
             }
-            const int at = __fns(here, 0, left + 1) & 31;
-            const int b = imin(b0 + at, s_.B - 1);
-            PackedBlock r;
-            r.q_row = s_.cu_q[b];
-            r.nq = s_.cu_q[b + 1] - r.q_row;
-            r.k_row = s_.cu_k[b];
-            r.nkv = s_.cu_k[b + 1] - r.k_row;
-            r.q0 = (lo - ((r.nkv - r.nq) >> log_)) << log_;
-            return r;
+            b = imin(b + (__fns(here, 0, left + 1) & 31), s_.B - 1);
+            const int level = __shfl_sync(0xffffffffu, b < 32 ? first_.level : second_.level, b & 31);
+            q0 = (lo - level) << log_;
+        } else {
+            b = 0;
+            int end = s_.B;                // number_of(b) <= number < number_of(end)
+            while (end - b > 1) {
+                const int step = (end - b + 31) >> 5, at = b + lane_ * step;
+                const unsigned ahead = __ballot_sync(0xffffffffu, at < end && (lane_ == 0 || number_of(at) <= number));
+                b += (31 - __clz(ahead)) * step;
+                end = imin(end, b + step);
+            }
+            q0 = (number - number_of(b)) << log_;
         }
+        bool wrong = false;
+        load(b, wrong);
+        PackedBlock r{0, 0, 0, 0, 0};
+        if (wrong || q0 < 0) return r;
+        r.q_row = s_.cu_q[b];
+        r.nq = s_.cu_q[b + 1] - r.q_row;
+        r.k_row = s_.cu_k[b];
+        r.nkv = s_.cu_k[b + 1] - r.k_row;
+        r.q0 = q0;
+        return r;
     }
 
   private:
@@ -107,18 +138,13 @@ class BlockFinder {
         q.blocks = (q1 - q0 + (1 << log_) - 1) >> log_;
         return q;
     }
-    __device__ __forceinline__ Seq get(int b) const {
-        bool wrong = false;
-        return b == lane_ ? first_ : b == lane_ + 32 ? second_ : load(b, wrong);
-    }
+    // The first number of a sequence's blocks (more than kFew sequences).
+    __device__ __forceinline__ int number_of(int b) const { return (s_.cu_q[b] >> log_) + b; }
     static __device__ __forceinline__ int from(const Seq &q, int level) {
         return imin(imax(q.level + q.blocks - level, 0), q.blocks);
     }
-    __device__ __forceinline__ int from_level(int level) const {
-        int sum = from(first_, level) + from(second_, level);
-        bool wrong = false;
-        for (int b = lane_ + 64; b < s_.B; b += 32) sum = imin(sum + from(load(b, wrong), level), kMost);
-        return __reduce_add_sync(0xffffffffu, sum);
+    static __device__ __forceinline__ bool has(const Seq &q, int level) {
+        return level >= q.level && level < q.level + q.blocks;
     }
     const PackedSeqs &s_;
     int log_, lane_, top_;

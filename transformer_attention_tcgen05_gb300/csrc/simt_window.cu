@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) simt_window_kernel
         const BlockFinder finder(p.seqs, 5, blockIdx.x == 0 && h == 0 && tid < 32, p.err);
         if (int(blockIdx.x) >= finder.total) return;
         const PackedBlock at = finder.find(blockIdx.x);
+        if (at.q0 >= at.nq) return;
         q0 = at.q0;
         nq = at.nq;
         off = at.nkv - at.nq;
@@ -439,8 +440,7 @@ attn_status_t simt_causal_varlen(const Ctx &c, attn_dtype_t dt, const VarlenArgs
     p.qscale = a.scale * kLog2e;
     p.err = c.err;
     p.sq = a.st[0]; p.sk = a.st[1]; p.sv = a.st[2]; p.so = a.st[3];
-    // the most blocks that sequences of Nq queries together can have
-    const int blocks = int((a.Nq + (long long)imin(a.B, a.Nq) * (kBM - 1)) / kBM);
+    const int blocks = int(BlockFinder::most(a.B, a.Nq, kBM));
     p.seqs = PackedSeqs{a.cu_q, a.cu_k, a.B, a.Nq, a.Nkv, blocks};
     return dispatch_win<true>(c, dt, a.D, p, blocks, a.Hq);
 }

@@ -107,7 +107,8 @@ struct VlBars {
 };
 
 // An item by its index (one warp): whole pairs, longest first, then the pairs of a last
-// round that takes at most half of the SMs as single tiles.
+// round that takes at most half of the SMs as single tiles.  No steps: there is no such
+// item, or it is a second row tile past its sequence's end.
 __device__ __forceinline__ VlItem find_item(const VlParams &p, const BlockFinder &finder, int index) {
     const int pairs = finder.total * p.by_hp.d, rest = pairs - p.by_sm(pairs) * p.by_sm.d;
     const int whole = 2 * rest <= p.by_sm.d ? pairs - rest : pairs;
@@ -249,9 +250,13 @@ tc_varlen_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 const int s = it & 1;
                 if (it >= 2) ok = wait_all(&bars->item_empty[s], ((it >> 1) - 1) & 1);
                 if (!ok) break;
-                VlItem w = find_item(p, finder, index);
-                // behind the last item: take what is left, so that no CTA starts for it
-                while (ok && index >= 0 && w.steps < 0) next();
+                // (behind the last item, too, every index is taken: no CTA starts for it)
+                VlItem w{};
+                while (ok) {
+                    w = find_item(p, finder, index);
+                    if (w.steps > 0 || index < 0) break;
+                    next();
+                }
                 if (!ok) break;
                 if (lane == 0) {
                     bars->item[s] = w;
@@ -415,20 +420,18 @@ tc_varlen_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 const int steps = same(item.steps), n[kNQ] = {same(item.n[0]), same(item.n[1])}, f1 = same(item.f[1]);
                 const bool few = same(item.few) != 0;
                 if (steps < 0) break;
-                if (steps > 0) {                       // (0: a second row tile past its sequence's end)
-                    if (C::QS == 2) slot = it & 1;
+                if (C::QS == 2) slot = it & 1;
 #pragma unroll
-                    for (int t = 0; t < kNQ; ++t)
-                        if (n[t] > 0) {
-                            const int i = slot * kNQ + t;
-                            ok = ok && wait(&bars->q_full[0][0] + i, (q_par >> i) & 1);
-                            q_par ^= 1u << i;
-                        }
-                    ok = ok && wait(&bars->k_full[ks], kp);
-                    qk(0, few ? id_few : id_qk);
-                    if (n[1] > 0 && f1 == 0) qk(1, few ? id_few : id_qk);
-                    next_k(steps == 1, n);
-                }
+                for (int t = 0; t < kNQ; ++t)
+                    if (n[t] > 0) {
+                        const int i = slot * kNQ + t;
+                        ok = ok && wait(&bars->q_full[0][0] + i, (q_par >> i) & 1);
+                        q_par ^= 1u << i;
+                    }
+                ok = ok && wait(&bars->k_full[ks], kp);
+                qk(0, few ? id_few : id_qk);
+                if (n[1] > 0 && f1 == 0) qk(1, few ? id_few : id_qk);
+                next_k(steps == 1, n);
                 for (int j = 0; ok && j < steps; ++j) {
                     // (tile 0 works in steps [0, n[0]), tile 1 in [f1, n[1]))
                     const bool more = j + 1 < steps, few_now = few && j == 0;
@@ -657,8 +660,7 @@ attn_status_t tc_causal_varlen(const Ctx &c, attn_dtype_t dt, const VarlenArgs &
     // pairs of heads where the group is even, else pairs of row tiles (tc_window.cu)
     const bool by_head = (a.Hq / a.Hkv) % 2 == 0;
     const int bs = by_head ? kBM : kNQ * kBM, hp = by_head ? a.Hq / 2 : a.Hq;
-    // the most blocks that sequences of Nq queries together can have
-    const long long blocks = (a.Nq + (long long)imin(a.B, a.Nq) * (bs - 1)) / bs;
+    const long long blocks = BlockFinder::most(a.B, a.Nq, bs);
     if (blocks * hp > (1 << 29)) return ATTN_ERR_UNSUPPORTED;
     CUtensorMap tq, tk, tv;
     // a layout the tensor-map encoder refuses goes to the SIMT kernel
