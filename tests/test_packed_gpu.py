@@ -492,6 +492,8 @@ Q4_CASES = [
     ("bf16", [1200, 300, 700] * 8, 8, 4, 64, 16, 0, 0),            # ranges that end inside units
     ("bf16", [3000, 1, 0, 40, 257, 256, 7], 8, 8, 64, 16, 0, 0),   # short units beside long ones
     ("bf16", [2000] * 6, 32, 4, 128, 16, 0, 0),
+    ("bf16", [7000, 40, 0, 300, 1], 32, 2, 128, 16, 0, 0),         # 16 heads of 128 channels
+    ("f16", [1500, 129] * 3, 48, 3, 128, 24, 500, 4),
 ]
 
 

@@ -30,7 +30,7 @@
 //  * Up to 4 heads fill half of an MMA's 8 columns.  Then (SPLIT) the columns are heads by
 //    two halves of a chunk's tokens: half the MMAs, one exponential per lane instead of a
 //    column of nothing (8 x 4096 tokens, 32 heads on 8: 17.4 -> 16.2 us).
-//  * 3 CTAs of 4 warps per SM; what a warp keeps of its range beside the chunk at hand
+//  * 3 CTAs of 4 warps per SM (2 for 9 to 16 heads of D 128); what a warp keeps of its range beside the chunk at hand
 //    lies in shared memory, so that the registers suffice (12 documents of 9000 to 60 000
 //    tokens, 64 heads on 8: 2 CTAs 88.9 us, 3 84.9, 4 88.5).
 //
@@ -57,7 +57,9 @@ constexpr int kMaxSms = 192;               // workspace slots
 template <int D, int NT>
 struct Q4Cfg {
     static constexpr int CW = 4;                            // warps
-    static constexpr int PER_SM = 3;                        // CTAs (168 registers per thread)
+    // CTAs: 168 registers per thread, which 16 heads of D 128 do not fit (12 documents, 128
+    // heads on 8: 132 us so, 122 with 2)
+    static constexpr int PER_SM = NT == 2 && D == 128 ? 2 : 3;
     static constexpr int NS = D == 64 ? 4 : 2;              // chunks in flight per warp
     static constexpr int THREADS = CW * 32;
     static constexpr int HP = NT * 8;                       // padded heads per KV head
