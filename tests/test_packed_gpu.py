@@ -841,6 +841,28 @@ def test_varlen_rows_on_16_byte_boundaries(ta, dt, D):
     check_varlen(dt, q, k, v, cu, cu, o, 140, 3, [0, 127, 128, 129, 130, 131, 258, -1])
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_beyond_32_bit_offsets(ta, D):
+    """Tokens 2 M elements apart: rope in place and attention on views of one buffer."""
+    g = torch.Generator().manual_seed(45)
+    lens = [300, 1, 799]
+    n = sum(lens)
+    far = torch.empty(n, 2 ** 21, dtype=torch.bfloat16, device="cuda")
+    assert far.numel() > 2 ** 31
+    q, k, v, o = (far[:, i * 512:i * 512 + h * D].unflatten(1, (h, D)) for i, h in enumerate((2, 1, 1, 2)))
+    for x in (q, k, v):
+        x.copy_(randn(g, *x.shape))
+    o.fill_(7.0)
+    cu, f = starts(lens), ta.rope_frequencies(D)
+    pos = torch.cat([torch.arange(m) for m in lens]).int().cuda()
+    near = [ta.rope_fwd(x.contiguous(), f, pos) for x in (q, k)]
+    for x, y in zip((q, k), near):
+        assert torch.equal(ta.rope_fwd(x, f, pos, o=x), y)
+    want = ta.causal_gqa_varlen_fwd(*near, v.contiguous(), cu)
+    assert torch.equal(ta.causal_gqa_varlen_fwd(q, k, v, cu, o=o), want)
+    assert ta.device_status() == 0 and not (o == 7).all(-1).any()
+
+
 def test_varlen_long_and_many(ta):
     g = torch.Generator().manual_seed(33)
     lens = [9000, 3, 700, 1, 2500]

@@ -28,17 +28,17 @@
 //  * The rows of a (page, head) are contiguous: a chunk of 32 tokens is one to four
 //    plain bulk copies (4.6 KB at D = 128) for K, V and scales together.
 //  * Up to 4 heads fill half of an MMA's 8 columns.  Then (SPLIT) the columns are heads by
-//    two halves of a chunk's tokens: half the MMAs, one exponential per lane instead of a
-//    column of nothing (8 x 4096 tokens, 32 heads on 8: 17.4 -> 16.2 us).
-//  * 3 CTAs of 4 warps per SM (2 for 9 to 16 heads of D 128); what a warp keeps of its range beside the chunk at hand
-//    lies in shared memory, so that the registers suffice (12 documents of 9000 to 60 000
-//    tokens, 64 heads on 8: 2 CTAs 88.9 us, 3 84.9, 4 88.5).
+//    two halves of a chunk's tokens: half the scales, exponentials and weights per lane
+//    (8 x 4096 tokens, 32 heads on 8: 17.4 -> 16.2 us).
+//  * 3 CTAs of 4 warps per SM (2 for 9 to 16 heads of D 128); what a warp keeps of its
+//    range beside the chunk at hand lies in shared memory, so that the registers suffice
+//    (12 documents of 9000 to 60 000 tokens, 64 heads on 8: 2 CTAs 88.9 us, 3 84.9, 4 88.5).
 //
 // Measured (bf16, D 128): 8 x 4096 tokens, 32 heads on 8, 16.2 us (2.35 TB/s; 26 us from
 // 16-bit pages); 12 documents, 64 heads on 8, 84 us (4.45 TB/s; 55 at the copy rate).  Of
 // these, 12.2 and 64 are the copies, the work list, the merges and joins alone; the rest is
-// arithmetic that does not hide behind them: 642 instructions per chunk in SPLIT form (889 with a mask and an
-// OR as two).  Leaving out V's part took the documents from 86 to 68 us, K's to 70, the
+// arithmetic that does not hide behind them: 642 instructions per chunk (889 with a mask and
+// an OR as two).  Leaving out V's part took the documents from 86 to 68 us, K's to 70, the
 // softmax to 76, the MMAs of the constants to 79.5.
 //
 // Sums and statistics are fp32; the output is rounded once.
