@@ -1043,6 +1043,40 @@ def test_other_streams_and_devices_do_not_matter(ta):
     assert ta.device_status() == 0
 
 
+def test_packed_calls_side_by_side_and_replayed(ta):
+    """Two calls that each fill the GPU, on two streams, one of them a replayed graph that
+    meets other lengths: each takes its own items."""
+    g = torch.Generator().manual_seed(46)
+    lens = [2500, 1, 1800, 700]
+    n = sum(lens)
+    sets = []
+    for D, dt in ((128, "bf16"), (64, "f16")):
+        q, k, v = (randn(g, n, h, D).to(DT[dt]).cuda() for h in (16, 4, 4))
+        sets.append((q, k, v))
+    cus = [starts(lens), starts([n]), starts([5] * 70 + [n - 350 - 900] + [30] * 30)]
+    want = [[ta.causal_gqa_varlen_fwd(*x, cu) for cu in cus] for x in sets]
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    held, o = starts(lens), torch.empty_like(sets[0][0])
+    graphs = {}
+    for B, cu in ((4, held), (1, cus[1]), (101, cus[2])):    # the number of sequences is an argument
+        graphs[B] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graphs[B], stream=a):
+            ta.causal_gqa_varlen_fwd(*sets[0], cu, o=o)
+    for i, B in enumerate((4, 1, 101) * 2):
+        with torch.cuda.stream(a):
+            graphs[B].replay()
+        with torch.cuda.stream(b):
+            got = [ta.causal_gqa_varlen_fwd(*sets[1], cu) for cu in cus]
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0][(4, 1, 101).index(B)])
+        assert all(torch.equal(x, y) for x, y in zip(got, want[1]))
+    held.copy_(starts([700, 1800, 1, 2500]))             # the captured call with other lengths
+    graphs[4].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, ta.causal_gqa_varlen_fwd(*sets[0], held)) and ta.device_status() == 0
+
+
 def test_layout_of_the_tests_is_the_headers():
     k, v, bit = layout(128)
     assert k[:9] == [0, 0, 0, 0, 2, 2, 2, 2, 16] and v[:9] == [64, 64, 64, 64, 72, 72, 72, 72, 80]
