@@ -313,21 +313,20 @@ struct CodedRows {
                     ptx::ffma2(x[i], x[i + 1], y[i], y[i + 1], s[i], s[i + 1], x[i], x[i + 1]);
                 }
             }
-            const T sk = q4_scale<T>(q4_best(x), inv);
-            const uint32_t wk = q4_codes<H16F<T>::f16>(x, inv);
-            const T sv = q4_scale<T>(q4_best<T>(v[u].u), inv);
+            // the even lanes of a group work out K's scale, the odd ones V's
+            const float best_k = q4_best(x), best_v = q4_best<T>(v[u].u);
+            const T scale = q4_scale<T>(pl & 1 ? best_v : best_k, inv);
+            const float inv2 = __shfl_xor_sync(0xffffffffu, inv, 1);
+            const uint32_t wk = q4_codes<H16F<T>::f16>(x, pl & 1 ? inv2 : inv);
             v[u].get(x);
-            const uint32_t wv = q4_codes<H16F<T>::f16>(x, inv);
+            const uint32_t wv = q4_codes<H16F<T>::f16>(x, pl & 1 ? inv : inv2);
             // V: words of two neighbouring groups, one of this lane's own and one of the
             // lane of the other group that holds the same channels of it
             const uint32_t o = __shfl_xor_sync(0xffffffffu, wv, 4);
             if (keep && h < p.Hkv) {
                 *reinterpret_cast<uint32_t *>(to + at_k) = wk;
                 *reinterpret_cast<uint32_t *>(to + at_v) = __byte_perm(wv, o, order);
-                if (pl == 0) {
-                    *reinterpret_cast<T *>(to + p.D + 2 * g) = sk;
-                    *reinterpret_cast<T *>(to + p.D + p.D / 16 + 2 * g) = sv;
-                }
+                if (pl < 2) *reinterpret_cast<T *>(to + p.D + pl * (p.D / 16) + 2 * g) = scale;
             }
             to += step * p.k_st[1];
         };
@@ -451,7 +450,7 @@ struct GatherRows {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) gather_rows_kernel(const GatherRows p) {
-    constexpr int U = 4;
+    constexpr int U = 8;
     __shared__ Dest d;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
