@@ -45,12 +45,18 @@ __device__ __forceinline__ int turn_at(int rot, int pair) {
 // threads of the CTA; a barrier must follow.
 template <typename F>
 __device__ __forceinline__ void fill_turns(const Rotation &r, float2 *tab, int tokens, F pos) {
-    const int pairs = r.rot / 2;
-    for (int e = threadIdx.x; e < tokens * pairs; e += blockDim.x) {
-        const int t = e / pairs, pair = e - t * pairs;
+    const int pairs = r.rot / 2, dt = int(blockDim.x) / pairs, dp = int(blockDim.x) - dt * pairs;
+    int t = int(threadIdx.x) / pairs, pair = int(threadIdx.x) - t * pairs;
+    while (t < tokens) {
         float c, s;
         turn_by(pos(t), r.freq[pair], r.mscale, c, s);
         tab[t * pairs + turn_at(r.rot, pair)] = make_float2(c, r.inverse ? -s : s);
+        t += dt;
+        pair += dp;
+        if (pair >= pairs) {
+            pair -= pairs;
+            ++t;
+        }
     }
 }
 
