@@ -12,11 +12,12 @@
 // instructions.)  bf16, 8192 x 32 rows of D 128: 22.5 us, 6.0 TB/s (29.2 that way);
 // append of 20 000 tokens, 32 heads on 8: 78.5 us, 6.3 TB/s (193); 64 tokens 2.9 us.
 //
-// Rows coded in 4 bits are bound by instructions (340 per warp and two rows, a quarter of
-// them angles; 63% of the issue slots): 20 000 tokens 39.5 us for K and V alone, 78 with
+// Rows coded in 4 bits are bound by instructions (320 per warp and two rows, a quarter of
+// them angles; 63% of the issue slots): 20 000 tokens 37.4 us for K and V alone, 76 with
 // their queries, whose CTAs they run beside; 64 tokens 3.1 us.  Extrema in packed pairs
-// and with NaN carried along, and the next heads' rows on the way, brought K and V of 5000
-// tokens from 15.8 to 13.5 us.  The reader: 22 500 rows 22.1 us, 5.3 TB/s (ALU 64%, then the copies).
+// and with NaN carried along, the next heads' rows on the way and the scales of K and V in
+// different lanes brought K and V of 5000 tokens from 15.8 to 12.9 us; a fourth CTA per SM
+// leaves too few registers (18.3).  The reader: 22 500 rows 21.7 us, 5.4 TB/s.
 #include <math.h>
 
 #include "kernels.h"
