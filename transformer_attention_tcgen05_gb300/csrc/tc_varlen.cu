@@ -24,15 +24,14 @@
 //    them: sink tiles are looked over like the tiles of an edge.
 //
 // 16-bit, 32 heads on 8, D 128: one prompt of 4096 tokens 95 us (1440 TFLOP/s over the
-// visible pairs; 92 in the kernel for one length), 8 of 1024 74 us (79), 64 of 128 43 us
-// (50), 16 prompts of 1 to 6000 tokens 192 us (1345 TFLOP/s, 71% of the measured product).  A
+// visible pairs; 92 in the kernel for one length), 8 of 1024 73 us (79), 64 of 128 43 us
+// (50), 16 prompts of 1 to 6000 tokens 190 us (1355 TFLOP/s, 71% of the measured product).  A
 // step of two tiles takes 1.18 us for D 128 and 0.77 for D 64 (0.99 and 0.49 at the
 // tensor pipe's rate); 1.5 us where all of its rows are on an edge, and 1.1 for a tile
-// alone.  Measured and not kept: masks 32 keys at a time as bits (chunks 68 -> 66 us, the
-// plain step 0.71 -> 0.76), no exponentials for keys that no row of a warp sees (step
+// alone.  Measured and not kept: no exponentials for keys that no row of a warp sees (step
 // 0.77 -> 0.87: the exponentials of a tile are no longer one block of instructions; as a
-// second copy of them 0.86 and cold instructions), heads in pairs also where
-// the group is odd (7 x 2048 tokens 101 -> 109 us).
+// second copy of them 0.86 and cold instructions), heads in pairs also where the group is
+// odd (7 x 2048 tokens 101 -> 109 us).
 //
 // All spin-waits are bounded (1 s); on a timeout the CTA raises the device error word,
 // drains what it issued, frees TMEM and exits.
@@ -535,7 +534,7 @@ tc_varlen_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                     const int i = lead + j;
                     return (i < 0 ? lo : i < sk ? i : lo + f + j - sk) * kBN;
                 };
-                SoftRows<D, F16> rows{lane_base + C::tm_s(t), lane_base + C::tm_p(t), o_addr, p.c_log2};
+                SoftRows<D, F16, true> rows{lane_base + C::tm_s(t), lane_base + C::tm_p(t), o_addr, p.c_log2};
                 int j = 0;
                 // the key tile from which on every row of the warp has seen a key before: of
                 // the first one the last rows may see nothing, and then see the next

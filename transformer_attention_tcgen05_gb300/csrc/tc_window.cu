@@ -380,7 +380,7 @@ tc_window_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             return true;
         };
 
-        SoftRows<D, F16> rows{s_addr, p_addr, o_addr, p.c_log2};
+        SoftRows<D, F16, false> rows{s_addr, p_addr, o_addr, p.c_log2};
         // S_t is in registers: the next QK_t may overwrite it
         auto s_read = [&]() {
             if constexpr (C::SEP_P) {

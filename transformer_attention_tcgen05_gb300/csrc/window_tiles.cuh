@@ -236,10 +236,22 @@ __device__ __forceinline__ void spoil_rows(const Item &w, const typename H16<F16
     __syncwarp();
 }
 
+// The n lowest bits (none for n < 0).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    uint32_t x;
+    asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(x) : "r"(imax(n, 0)));
+    return x;
+}
+
 // The rows of a softmax warp's query tile: a row per thread, its running maximum m
 // and sum l (base 2, scores scaled by cl).  s_read is called when the scores are in
 // registers, wait_prev waits for the P V of the tile before (false: gave up).
-template <int D, bool F16>
+// BITS: masks as bits of 32 keys, which chunks of keys that a warp sees go without.  Packed
+// sequences start anywhere in a tile, so that twice as many are masked (chunks of a window of 1024:
+// 66.8 us with one bound per tile, 61.5 with bits; 8 x 1024 tokens 74.6 and 73.1); the
+// kernel for one length loses more on plain steps (D 64 0.706 us, 0.762 with bits; 4096
+// tokens of D 128 91.5 us, 93.6).
+template <int D, bool F16, bool BITS>
 struct SoftRows {
     using C = WnCfg<D>;
     static constexpr int BN = kBN;
@@ -293,10 +305,21 @@ struct SoftRows {
             const bool late = k0 + BN - 1 > pos;                    // a key behind the first row
             const bool early = k0 + window < pos + kBM;            // one before the last row's window
             if (late || (early && k0 + BN > sinks)) {
-                // key e of the tile is seen iff e <= hi and (e >= lo or e < sk);
+                // key e of the tile is seen iff e <= hi and (e >= lo or e < sk)
+                const int hi = pos + row - k0, lo = hi - window + 1, sk = sinks - k0;
+                if constexpr (BITS) {
+                    // 32 keys at a time, untouched where every row of the warp sees them all
+#pragma unroll
+                    for (int c = 0; c < BN; c += 32) {
+                        const uint32_t seen = low_bits(hi + 1 - c) & (~low_bits(lo - c) | low_bits(sk - c));
+                        if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(seen & (1u << e))) sv[c + e] = -INFINITY;
+                    }
+                } else
                 // all but tiny windows need only one bound per tile: the
                 // diagonal's, the end of the sinks, or the window's start
-                const int hi = pos + row - k0, lo = hi - window + 1, sk = sinks - k0;
                 if (!early || (!late && k0 + window + BN <= pos + 1)) {
                     const int last = early ? sk - 1 : hi;
 #pragma unroll
