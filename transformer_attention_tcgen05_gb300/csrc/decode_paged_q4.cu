@@ -588,8 +588,8 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
         for (int i = taken; i < issued; ++i) ptx::mbar_wait(&full[i % NS], (i / NS) & 1, nullptr);
 }
 
-// As in the 16-bit kernel the partials come first, at their largest size (4 CTAs
-// per SM with 8 heads, or 3 with 16), so that the tickets lie at one place.
+// As in the 16-bit kernel the partials come first, at their largest size (3 CTAs per SM
+// with 16 heads), so that the tickets lie at one place.
 constexpr size_t kSlots = size_t(2) * kMaxSms * 48;    // slots x heads
 constexpr size_t kPartBytes = kSlots * 128 * sizeof(float);
 constexpr size_t kMlBytes = kSlots * 2 * sizeof(float);

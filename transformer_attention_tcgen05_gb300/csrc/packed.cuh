@@ -12,7 +12,9 @@
 // largest L with F(L) > number (16 sequences: 1.0 to 1.4 us to a block's rows, which a
 // kernel hides behind the block before).
 //
-// More of them: in the order of the sequences, those of b from number cu_q[b] / BS + b on.
+// More of them: in the order of the sequences, from the last one's last block back, so
+// that the longest blocks of each start first (99 prompts of 50 tokens and then one of
+// 8000: 357 us, 390 from the front); those of b from number cu_q[b] / BS + b on.
 // That leaves each at least as many numbers as it has blocks, and one at most empty, so
 // that a search among the starts themselves finds a number, 32 probes at a time (two to
 // four rounds).  (By levels, where every step of the bisection goes over all sequences,
@@ -100,6 +102,7 @@ class BlockFinder {
             const int level = __shfl_sync(0xffffffffu, b < 32 ? first_.level : second_.level, b & 31);
             q0 = (lo - level) << log_;
         } else {
+            number = total - 1 - number;
             b = 0;
             int end = s_.B;                // number_of(b) <= number < number_of(end)
             while (end - b > 1) {
