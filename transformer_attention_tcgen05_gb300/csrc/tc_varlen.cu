@@ -3,10 +3,11 @@
 //
 // The tile arithmetic is that of the windowed kernel (tc_window.cu, window_tiles.cuh):
 // pairs of 128-row query tiles over a list of 128-key tiles, P in tensor memory, a
-// row per softmax thread, masks by one bound on the tiles of an edge.  What differs:
+// row per softmax thread; masks are made of bits (SoftRows).  What differs:
 //
 //  * Items come from the device.  A block of query rows and the head pair that works on
-//    it are found from the sequences' starts (packed.cuh), longest first.
+//    it are found from the sequences' starts (packed.cuh), the longest first for up to 64
+//    of them.
 //  * A CTA stays on its SM and takes the items of CTAs that have not started off the
 //    launch (clusterlaunchcontrol), in the order of the list.  Items differ in length and
 //    number of tiles: dealt out in turn, some SMs worked twice as long as others (chunks
