@@ -540,7 +540,9 @@ ATTN_API attn_status_t attn_kv_append_paged_rope(
  *   arguments, visibility, errors and workspace rules, with a workspace of
  *   attn_decode_gqa_paged_q4_workspace_bytes(...) bytes.  Codes are multiplied as they are and
  *   scaled in fp32; a weight times its value's scale is rounded to 11 bits for
- *   the P V product.  Outputs are finite for scales of up to 2^100.
+ *   the P V product (below 2^-21 of the largest such product of its head and group
+ *   of 32 channels, to a multiple of 2^-31 of that one).  Outputs are finite for
+ *   scales of up to 2^100.
  * Passage: fak "GPU - the in-kernel forward pass", section 3b (the device KV
  * cache), section 4 (decode attention), and candle PR #11's int8 rows with a scale
  * for the idea of holding rows in fewer bits.

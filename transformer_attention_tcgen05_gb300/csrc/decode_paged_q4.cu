@@ -20,11 +20,15 @@
 //    row is laid out such that a lane's operands are consecutive: one 16-byte read
 //    per token for K, one 8-byte read for V, no ldmatrix, no swizzle.
 //  * V's scale belongs to the token, so it is multiplied into the weight:
-//    w_jg = p_j s_jg is the P operand of channel group g, f16 (a rounding of 2^-12 of
-//    each weight), and a second MMA with a matrix of -24 (16 + 8) and -264 (256 + 8)
-//    takes the constants out again with the very same rounded weights.  The running
-//    reference of the softmax is the maximum of x_j + log2 max_g |s_jg|, which keeps
-//    every w_jg below 1 in any cache (below 2^8: the reference moves only when it must).
+//    w_jg = r_g p_j s_jg is the P operand of channel group g, f16, and a second MMA with a
+//    matrix of -24 (16 + 8) and -264 (256 + 8) takes the constants out again with the very
+//    same rounded weights.  r_g, a power of two per head and group, puts the group's
+//    largest |p_j s_jg| so far into [2^7, 2^14), so that a product loses 2^-11 of itself
+//    down to 2^-21 of that one, and 2^-32 of that one below, however far apart the scales
+//    of a token's groups are.  (One reference for all groups of a token, their largest
+//    scale, left a group 2^-14 of it at the edge of f16's normal range.)  The running
+//    maximum of the scores moves in whole powers of two and takes r_g along, so that the
+//    sums of P V stay as they are; they are divided by r_g at a segment's end.
 //  * The rows of a (page, head) are contiguous: a chunk of 32 tokens is one to four
 //    plain bulk copies (4.6 KB at D = 128) for K, V and scales together.
 //  * Up to 4 heads fill half of an MMA's 8 columns.  Then (SPLIT) the columns are heads by
@@ -112,6 +116,21 @@ __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t b
 __device__ __forceinline__ uint32_t code16(uint32_t w) { return and_or(w, 0x03c003c0u, 0x4c004c00u); }
 __device__ __forceinline__ uint32_t code256(uint32_t w) { return and_or(w, 0x003c003cu, 0x5c005c00u); }
 constexpr uint32_t kMinus24 = 0xce00ce00u, kMinus264 = 0xdc20dc20u;   // f16 pairs
+
+// Powers of two.  2^n for an integer n in [-126, 126].
+__device__ __forceinline__ float pow2(float n) { return __int_as_float((127 + int(n)) << 23); }
+// a b / c, zero where it is too small.
+__device__ __forceinline__ float pow2_ratio(float a, float b, float c) {
+    return __int_as_float(imax(__float_as_int(a) + (__float_as_int(b) - __float_as_int(c)), 0));
+}
+// The larger values of two pairs of bf16 (NaN left out).
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+constexpr float kMostUp = 0x1p100f;        // the largest r_g (and where it starts)
+constexpr float kFull = 0x1p14f;           // from here on r_g moves
 
 // N 32-bit words of shared memory (the widest load that fits)
 template <int N> __device__ __forceinline__ void read_words(const uint8_t *p, uint32_t (&w)[N]) {
@@ -329,16 +348,20 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
     int dead = 0, s = 0, warm = 0;
     uint32_t parity = 0;
     for (bool more = true; more;) {
-        // m: the running reference, and what weights are taken against (0 while it is -inf)
-        float m[NT][2], mu[NT][2], l[NT][2], acc[NT][2 * NG][4];
+        // m: the running maximum, and what weights are taken against (0 while it is -inf);
+        // up: r_g
+        float m[NT][2], mu[NT][2], l[NT][2], up[NT][NG][2], acc[NT][2 * NG][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = -INFINITY;
             mu[nt][0] = mu[nt][1] = l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
+            for (int g = 0; g < NG; ++g) up[nt][g][0] = up[nt][g][1] = kMostUp;
+#pragma unroll
             for (int i = 0; i < 2 * NG; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
         }
         int bad = dead;
+        bool fresh = true;                             // no product yet
 
         // this warp's chunks of the segment: the range's chunk number modulo the team.
         // The first NS rounds of all only ask for chunks; then come the segment's queries.
@@ -411,23 +434,12 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
                                 const float sc = g & 1 ? H::hi(ks[t][r][g / 2]) : H::lo(ks[t][r][g / 2]);
-                                x[t][nt][2 * r] = fmaf(sc, c[t][2 * r], x[t][nt][2 * r]);
-                                x[t][nt][2 * r + 1] = fmaf(sc, c[t][2 * r + 1], x[t][nt][2 * r + 1]);
+                                ptx::ffma2(x[t][nt][2 * r], x[t][nt][2 * r + 1], sc, sc, c[t][2 * r], c[t][2 * r + 1],
+                                           x[t][nt][2 * r], x[t][nt][2 * r + 1]);
                             }
                     }
                 }
             }
-            // ---- the reference of a token: the logarithm of its largest scale
-            float ref[TT][2];
-#pragma unroll
-            for (int t = 0; t < TT; ++t)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    float top = fmaxf(fabsf(H::lo(vs[t][r][0])), fabsf(H::hi(vs[t][r][0])));
-                    if constexpr (NG == 4)
-                        top = ptx::fmax3(fabsf(H::lo(vs[t][r][NG / 2 - 1])), fabsf(H::hi(vs[t][r][NG / 2 - 1])), top);
-                    ref[t][r] = fmaxf(ptx::lg2(top), -60.f);
-                }
             // ---- positions that are not seen: their scales may be NaN
             if (seen != 0xffffffffu) {
                 if (seen == 0u) bad = 1;
@@ -442,79 +454,146 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
                             for (int g = 0; g < NG / 2; ++g) vs[t][r][g] = 0u;
                         }
             }
-            // ---- the running reference moves if a weight could pass 2^8, or is NaN
-            float mx[NT][2];
-            bool far = false;
+            // scales a group's sums of one column
+            auto scale_sums = [&](int nt, int g, int j, float f) {
+                acc[nt][2 * g][j] *= f;
+                acc[nt][2 * g][j + 2] *= f;
+                acc[nt][2 * g + 1][j] *= f;
+                acc[nt][2 * g + 1][j + 2] *= f;
+            };
+            // ---- weights against the running maximum as it stands (a score of -inf weighs
+            //      nothing, NaN stays NaN); returns the largest (NaN left out)
+            float w[TT][NT][4];
+            auto exponentials = [&]() {
+                float top = 0.f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    mx[nt][j] = -INFINITY;
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int t = 0; t < TT; ++t)
-                        mx[nt][j] = ptx::fmax3(mx[nt][j], fmaf(x[t][nt][j], qs[nt][j], ref[t][0]),
-                                               fmaf(x[t][nt][j + 2], qs[nt][j], ref[t][1]));
-                    // (fmax leaves NaN out: a NaN score shows in its weight)
-                    far = far || !(mx[nt][j] <= m[nt][j] + 8.f) || m[nt][j] == -INFINITY;
-                }
-            if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+                        for (int i = 0; i < 4; i += 2) {
+                            float a, b;
+                            ptx::ffma2(a, b, x[t][nt][i], x[t][nt][i + 1], qs[nt][0], qs[nt][1], -mu[nt][0],
+                                       -mu[nt][1]);
+                            w[t][nt][i] = ptx::ex2(a);
+                            w[t][nt][i + 1] = ptx::ex2(b);
+                            top = ptx::fmax3(w[t][nt][i], w[t][nt][i + 1], top);
+                        }
+                return top;
+            };
+            // the running maximum of this chunk's scores too
+            auto move_maximum = [&]() {
+                bool none = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float top = mx[nt][j];
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int t = 0; t < TT; ++t) top = ptx::fmax3(top, x[t][nt][j], x[t][nt][j + 2]);
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1)
                             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                        const float mn = fmaxf(m[nt][j], top);
-                        const float alpha = mn == -INFINITY ? 1.f : ptx::ex2(m[nt][j] - mn);
+                        const float mn = fmaxf(m[nt][j], ceilf(top * qs[nt][j]));
+                        // (both infinite: NaN, and then 0)
+                        const float k = fminf(fmaxf(mn - m[nt][j], 0.f), 126.f), less = pow2(-k), more = pow2(k);
                         m[nt][j] = mn;
                         mu[nt][j] = mn == -INFINITY ? 0.f : mn;
-                        l[nt][j] *= alpha;
+                        none = none || mn == -INFINITY;
+                        l[nt][j] *= less;
+                        // weights fall and r_g rises: the sums stay, but where it may not
 #pragma unroll
-                        for (int i = 0; i < 2 * NG; ++i) {
-                            acc[nt][i][j] *= alpha;
-                            acc[nt][i][j + 2] *= alpha;
+                        for (int g = 0; g < NG; ++g) {
+                            const float r = fminf(up[nt][g][j] * more, kMostUp);
+                            scale_sums(nt, g, j, pow2_ratio(less, r, up[nt][g][j]));
+                            up[nt][g][j] = r;
                         }
                     }
-            }
-            // ---- weights (a score of -inf weighs nothing, NaN stays NaN)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int t = 0; t < TT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[t][nt][i] = ptx::ex2(fmaf(x[t][nt][i], qs[nt][i & 1], -mu[nt][i & 1]));
-                        l[nt][i & 1] += x[t][nt][i];
-                    }
+                fresh = __any_sync(0xffffffffu, none);
+            };
+            float most = exponentials();
             // ---- O^T += V^T P^T, a weight's scale in P
             const uint32_t minus[4] = {kMinus24, kMinus264, kMinus24, kMinus264};
             uint32_t ph[NT][NG][2];                    // of one block (SPLIT: both, side by side)
-            auto weigh = [&](int t) {
+            // a token pair's weights times their scales, of the lane's two columns
+            auto products = [&](int t, int nt, int g, float (&y)[4]) {
+                const float s0 = g & 1 ? H::hi(vs[t][0][g / 2]) : H::lo(vs[t][0][g / 2]);
+                const float s1 = g & 1 ? H::hi(vs[t][1][g / 2]) : H::lo(vs[t][1][g / 2]);
+                ptx::ffma2(y[0], y[1], w[t][nt][0], w[t][nt][1], s0, s0, -0.f, -0.f);
+                ptx::ffma2(y[2], y[3], w[t][nt][2], w[t][nt][3], s1, s1, -0.f, -0.f);
+            };
+            auto fill = [&](int t) {                   // returns the largest magnitude (NaN left out)
+                float top = 0.f;
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const float s0 = g & 1 ? H::hi(vs[t][0][g / 2]) : H::lo(vs[t][0][g / 2]);
-                    const float s1 = g & 1 ? H::hi(vs[t][1][g / 2]) : H::lo(vs[t][1][g / 2]);
+                for (int g = 0; g < NG; ++g)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        ph[nt][g][0] = ptx::transpose8x8(pack_f16x2(x[t][nt][0] * s0, x[t][nt][1] * s0));
-                        ph[nt][g][1] = ptx::transpose8x8(pack_f16x2(x[t][nt][2] * s1, x[t][nt][3] * s1));
+                        float y[4];
+                        products(t, nt, g, y);
+                        ptx::ffma2(y[0], y[1], y[0], y[1], up[nt][g][0], up[nt][g][1], -0.f, -0.f);
+                        ptx::ffma2(y[2], y[3], y[2], y[3], up[nt][g][0], up[nt][g][1], -0.f, -0.f);
+                        top = ptx::fmax3(fabsf(y[0]), fabsf(y[1]), top);
+                        top = ptx::fmax3(fabsf(y[2]), fabsf(y[3]), top);
+                        ph[nt][g][0] = ptx::transpose8x8(pack_f16x2(y[0], y[1]));
+                        ph[nt][g][1] = ptx::transpose8x8(pack_f16x2(y[2], y[3]));
+                    }
+                return top;
+            };
+            auto weigh = [&](int t) {
+                if ((t == 0 && fresh) ||
+                    __any_sync(0xffffffffu, fmaxf(fill(t), t == 0 ? most * (kFull / 256.f) : 0.f) >= kFull)) {
+                    if (t == 0) {
+                        move_maximum();
+                        most = exponentials();
+                    }
+                    // r_g: the largest product of the block's tokens into [2^7, 2^8)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            float y[4];
+                            products(t, nt, g, y);
+                            uint32_t top = pack_bf16x2(fmaxf(fabsf(y[0]), fabsf(y[2])), fmaxf(fabsf(y[1]), fabsf(y[3])));
+#pragma unroll
+                            for (int off = 4; off < 32; off <<= 1)
+                                top = max_bf16x2(top, __shfl_xor_sync(0xffffffffu, top, off));
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const int e = int(j ? top >> 23 : (top >> 7) & 0xffu);
+                                const float r = fminf(__int_as_float(imin(127 + 7 + 127 - e, 227) << 23), up[nt][g][j]);
+                                scale_sums(nt, g, j, pow2_ratio(1.f, r, up[nt][g][j]));
+                                up[nt][g][j] = r;
+                            }
+                        }
+                    fill(t);
+                }
+                if (t == 0) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int u = 0; u < TT; ++u) {
+                            ptx::fadd2(l[nt][0], l[nt][1], l[nt][0], l[nt][1], w[u][nt][0], w[u][nt][1]);
+                            ptx::fadd2(l[nt][0], l[nt][1], l[nt][0], l[nt][1], w[u][nt][2], w[u][nt][3]);
+                        }
+                }
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
                         ptx::mma16816<true>(acc[nt][2 * g], minus, ph[nt][g][0], ph[nt][g][1]);
                         ptx::mma16816<true>(acc[nt][2 * g + 1], minus, ph[nt][g][0], ph[nt][g][1]);
                     }
-                }
             };
             if constexpr (SPLIT) weigh(0);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                if constexpr (!SPLIT) weigh(t < TT ? t : 0);
                 uint32_t vw[2][2][NG / 2];             // [block of 8][token of the pair]
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     read_words<NG / 2>(tile + (t * 16 + r * 8 + tv0) * C::ROW + D / 2 + quad * (D / 16), vw[r][0]);
                     read_words<NG / 2>(tile + (t * 16 + r * 8 + tv1) * C::ROW + D / 2 + quad * (D / 16), vw[r][1]);
                 }
+                if constexpr (!SPLIT) weigh(t < TT ? t : 0);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     uint32_t u[2], y[2];
@@ -571,10 +650,12 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
                 }
                 float *row = mg + (warp * C::HP + h) * C::LDM + quad * 4;
 #pragma unroll
-                for (int g = 0; g < NG; ++g)
+                for (int g = 0; g < NG; ++g) {
+                    const float f = pow2_ratio(1.f, 1.f, up[nt][g][j]);
                     *reinterpret_cast<float4 *>(row + g * 32) =
-                        make_float4(acc[nt][2 * g][j], acc[nt][2 * g][j + 2], acc[nt][2 * g + 1][j],
-                                    acc[nt][2 * g + 1][j + 2]);
+                        make_float4(acc[nt][2 * g][j] * f, acc[nt][2 * g][j + 2] * f, acc[nt][2 * g + 1][j] * f,
+                                    acc[nt][2 * g + 1][j + 2] * f);
+                }
             }
         if (alone)
             store_alone<D, C::HP, C::LDM, SPLIT ? 2 : 1, F16>(p, mg, mml, bad, o_unit);

@@ -442,13 +442,6 @@ __device__ __forceinline__ void mma16816_f16(float (&d)[4], const uint32_t (&a)[
                    "f"(c3));
 }
 
-// log2 x on the special-function unit (subnormal x: -inf).
-__device__ __forceinline__ float lg2(float x) {
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // ---------------------------------------------------------- packed fp32x2
 // Blackwell executes these as one instruction on two fp32 lanes.
 
