@@ -102,6 +102,7 @@ struct Outer {
     explicit Outer(const at::Tensor &t) {
         if (t.is_contiguous()) return;
         const int n = int(t.dim()) - 1;
+        if (n > 4) value_error("a tensor has more axes than any argument");
         if (t.size(n) != 1 && t.stride(n) != 1) value_error("the last (D) dimension must be contiguous");
         for (int i = 0; i < n; ++i) st[i] = t.stride(i);
         p = st;
