@@ -176,17 +176,19 @@ struct Dest {
 };
 
 // Sequence, first row and row count of the tile's tokens [t0, t0 + n), from the
-// starts cu[0..B] of the packed sequences, and the sequence's `base` (null: 0).
+// starts cu[0..B] of the packed sequences, and the sequence's `base` (null: 0).  The first
+// CTA reports sequences that cannot be, and empty ones whose base is not `valid` (others'
+// rows tell).
+template <typename F>
 __device__ __forceinline__ void find_sequences(Dest &d, const int32_t *cu, const int32_t *base, int B, int N, int t0,
-                                               int n, unsigned *err) {
+                                               int n, unsigned *err, F valid) {
     if (threadIdx.x < kTile) d.seq[threadIdx.x] = -1;
     __syncthreads();
     for (int b = threadIdx.x; b < B; b += kThreads) {
         const int lo = cu[b], hi = cu[b + 1], from = base ? base[b] : 0;
-        if (lo < 0 || hi < lo || hi > N) {
-            if (blockIdx.x == 0) raise_device_error(err, kDevCheck);
-            continue;
-        }
+        const bool wrong = lo < 0 || hi < lo || hi > N;
+        if (blockIdx.x == 0 && (wrong || (hi == lo && !valid(from)))) raise_device_error(err, kDevCheck);
+        if (wrong) continue;
         for (int t = imax(lo, t0); t < imin(hi, t0 + n); ++t) {
             d.seq[t - t0] = b;
             d.first[t - t0] = lo;
@@ -205,7 +207,7 @@ __device__ __forceinline__ bool append_fits(const AppendRows &p, int len, int n)
 __device__ __forceinline__ void find_places(const AppendRows &p, Dest &d, float2 *tab, int t0) {
     const int tid = threadIdx.x, TB = p.tile.tokens();
     if (p.cu) {
-        find_sequences(d, p.cu, p.seq_len, p.B, p.N, t0, TB, p.err);
+        find_sequences(d, p.cu, p.seq_len, p.B, p.N, t0, TB, p.err, [&](int len) { return append_fits(p, len, 0); });
     } else if (tid < TB) {
         d.seq[tid] = t0 + tid < p.N ? t0 + tid : -1;
         d.first[tid] = t0 + tid;
@@ -425,7 +427,6 @@ __global__ void __launch_bounds__(kThreads) advance_rows_kernel(const AppendRows
     const int lo = p.cu[b], n = p.cu[b + 1] - lo, len = p.seq_len[b];
     if (lo < 0 || n < 0 || lo + n > p.N) return;
     bool ok = append_fits(p, len, n);
-    if (!ok && n == 0 && lane == 0) raise_device_error(p.err, kDevCheck);
     if (!ok || n == 0) return;
     for (int i = len / p.S + lane; i <= (len + n - 1) / p.S; i += 32) {
         const int page = p.table[b * p.table_stride + i];
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(kThreads) gather_rows_kernel(const GatherRows 
     ptx::griddep_launch_dependents();
     const int tid = threadIdx.x, TB = p.tile.tokens(), hl = p.tile.lanes();
     const int t0 = blockIdx.x * TB, tl = p.tile.token(tid);
-    find_sequences(d, p.cu, p.start, p.B, p.N, t0, TB, p.err);
+    find_sequences(d, p.cu, p.start, p.B, p.N, t0, TB, p.err, [](int) { return true; });
     if (tid < TB) {
         int page = -1, row = 0;
         const int b = d.seq[tid];
