@@ -435,7 +435,8 @@ ATTN_API size_t attn_decode_gqa_paged_workspace_bytes(int B, int Hq, int Hkv, in
  * The other channels are copied.  rotary_dim is a multiple of 16, at most D.
  *   freq: DEVICE uint64 [rotary_dim / 2], theta_i as a fraction of a turn per
  *     position, 2^64 theta_i / (2 pi) (8-byte aligned).  The angle is the product
- *     modulo 2^64, so it is as exact at position 2^31 - 1 as at 0.
+ *     modulo 2^64, within 2^-31 of a turn at every 32-bit position where the table
+ *     holds nearest integers, as attn_rope_frequencies' does.
  *   mscale: the factor m (1 for plain rotary positions; not for the copied
  *     channels).  Must be finite.
  *

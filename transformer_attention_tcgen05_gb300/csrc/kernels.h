@@ -84,6 +84,7 @@ struct RotaryArgs {
 attn_status_t rope_rows(const Ctx &c, attn_dtype_t dt, const void *x, void *y, const int32_t *pos,
                         long long pos_stride, int B, int H, int N, int D, const TensorStrides &sx,
                         const TensorStrides &sy, const RotaryArgs &rot);
+// (rotary_table.cu)
 attn_status_t rope_frequencies(uint64_t *freq, int rot, double theta, attn_rope_scaling_t scaling, double factor,
                                double original_len, double alpha, double beta);
 

@@ -18,8 +18,6 @@
 // and with NaN carried along, the next heads' rows on the way and the scales of K and V in
 // different lanes brought K and V of 5000 tokens from 15.8 to 12.9 us; a fourth CTA per SM
 // leaves too few registers (18.3).  The reader: 22 500 rows 21.7 us, 5.4 TB/s.
-#include <math.h>
-
 #include "kernels.h"
 #include "ptx.cuh"
 #include "rotary.cuh"
@@ -599,30 +597,6 @@ attn_status_t gather_rows(const Ctx &c, attn_dtype_t dt, const RowsGather &a) {
     const dim3 grid(unsigned(cdiv(a.N, p.tile.tokens())));
     return dt == ATTN_F16 ? launch(c, kFamKvPages, gather_rows_kernel<__half>, grid, p)
                           : launch(c, kFamKvPages, gather_rows_kernel<__nv_bfloat16>, grid, p);
-}
-
-// theta_i as 64-bit fractions of a turn.  double has 53 bits: the error at
-// position t is t 2^-55 of a turn.
-attn_status_t rope_frequencies(uint64_t *freq, int rot, double theta, attn_rope_scaling_t scaling, double factor,
-                               double original_len, double alpha, double beta) {
-    constexpr double two_pi = 6.283185307179586476925;
-    for (int i = 0; i < rot / 2; ++i) {
-        const double e = 2.0 * i / rot;
-        double f = pow(theta, -e);
-        if (scaling == ATTN_ROPE_LINEAR) {
-            f /= factor;
-        } else if (scaling == ATTN_ROPE_NTK) {
-            f = pow(theta * pow(factor, double(rot) / (rot - 2)), -e);
-        } else if (scaling == ATTN_ROPE_BY_PARTS) {
-            const double turns = original_len * f / two_pi;
-            const double share = fmin(1.0, fmax(0.0, (turns - alpha) / (beta - alpha)));
-            f = (1.0 - share) * f / factor + share * f;
-        }
-        f = f / two_pi;
-        if (!(f < 0.5)) return ATTN_ERR_INVALID_ARG;   // half a turn per position, or NaN
-        freq[i] = uint64_t(ldexp(f, 64) + 0.5);
-    }
-    return ATTN_OK;
 }
 
 }  // namespace attn
