@@ -460,7 +460,8 @@ ATTN_API size_t attn_decode_gqa_paged_workspace_bytes(int B, int Hq, int Hkv, in
  *   all batches); any value, negative ones too.  inverse != 0: the transposed
  *   rotation (angles negated), which is the gradient of the call with respect
  *   to x.  y may be x itself, with x's strides (in place); it must not overlap x
- *   otherwise.  All dtypes, D in {32, 64, 128}; fp32 arithmetic, rounded once.
+ *   otherwise.  All dtypes, D in {32, 64, 128}, H <= 2^30; fp32 arithmetic, rounded
+ *   once.
  * Passage: iris.c issue #15 "CUDA codepath !" (custom RoPE kernel) and fak
  * "GPU - the in-kernel forward pass", section 3 (the rotary step of a Llama
  * layer); the scalings are published extensions of it.

@@ -617,6 +617,7 @@ attn_status_t attn_rope_fwd(const void *x, void *y, const uint64_t *freq, const 
     if (B > 1 && (pos_stride < 0 || (pos_stride > 0 && pos_stride < N) || pos_stride > (1ll << 40)))
         return ATTN_ERR_INVALID_ARG;
     if ((const void *)positions == y || (const void *)freq == y) return ATTN_ERR_INVALID_ARG;
+    if (H > (1 << 30)) return ATTN_ERR_UNSUPPORTED;    // heads are counted past the last one
     const long long ext[3] = {B, H, N};
     long long sx[3], sy[3];
     if (!row_strides(x_strides, ext, 3, D, dtype, false, sx) || !row_strides(y_strides, ext, 3, D, dtype, true, sy))
