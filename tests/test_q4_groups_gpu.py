@@ -98,3 +98,29 @@ def test_a_token_that_outweighs_all_without_values(ta, ups):
 
     o = run(ta, "bf16", [40, 700], 4, 128, ups, 3, last)
     assert (o[..., 32:].abs().amax(-1) > 0).all()
+
+
+@pytest.mark.parametrize("dt,G", [("bf16", 2), ("f16", 8), ("bf16", 12)])
+def test_tiny_scales_and_queries_of_zero(ta, dt, G):
+    """Scores that vanish weigh every visible token alike, and the others not at all."""
+    g = torch.Generator().manual_seed(5)
+    lens = [45, 700]
+    c = Cache(lens, [0, 0], 16, 6)
+    pages = torch.full((c.P, 1, 16, 144), 255, dtype=torch.uint8)          # (unseen scales are NaN)
+    vs = []
+    for b, n in enumerate(lens):
+        rows = pack(randn(g, 1, n, 128), randn(g, 1, n, 128), dt)
+        page, row = c.rows(b, 0, n)
+        pages[page, :, row] = rows.transpose(0, 1)
+        vs.append(unpack(rows, dt)[1][0])
+    q = randn(g, 2, G, 128).to(DT[dt])
+    q[:, 0] = 0
+    q[:, -1] *= torch.finfo(DT[dt]).tiny
+    for scale in (1e-20, 1e-30, 1e-38):
+        o = ta.decode_gqa_paged_q4(q.cuda(), pages.cuda(), c.dev, c.sl, scale=scale).double().cpu()
+        for b, n in enumerate(lens):
+            # half a step, weights of one in f16 times a scale (2^-11), and fp32 sums
+            lim = 2.0 ** -8 * vs[b].mean(0).abs() + (2.0 ** -11 + n * 2.0 ** -22) * vs[b].abs().mean(0)
+            lim = lim + 272 * 2.0 ** -23 * 32 * vs[b].abs().unflatten(-1, (-1, 32)).amax(-1).mean(0).repeat_interleave(32) / 8
+            assert ((o[b] - vs[b].mean(0)).abs() <= lim).all(), (scale, b, o[b, :, 0])
+    assert ta.device_status() == 0

@@ -326,7 +326,8 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
 #pragma unroll
                 for (int off = 1; off < 4; off <<= 1) sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], off);
             }
-            const float sc = p.c_log2 * __uint_as_float(unsigned(127 - 13 + e) << 23);
+            // (not 0, which a score of -inf would make NaN; scores times so little vanish)
+            const float sc = fmaxf(p.c_log2 * __uint_as_float(unsigned(127 - 13 + e) << 23), 0x1p-126f);
             // of the lane's two columns
 #pragma unroll
             for (int j = 0; j < 2; ++j) qs[nt][j] = __shfl_sync(0xffffffffu, sc, (pair * 2 + j) * 4);
