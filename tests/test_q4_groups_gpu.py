@@ -124,3 +124,19 @@ def test_tiny_scales_and_queries_of_zero(ta, dt, G):
             lim = lim + 272 * 2.0 ** -23 * 32 * vs[b].abs().unflatten(-1, (-1, 32)).amax(-1).mean(0).repeat_interleave(32) / 8
             assert ((o[b] - vs[b].mean(0)).abs() <= lim).all(), (scale, b, o[b, :, 0])
     assert ta.device_status() == 0
+
+
+def test_products_near_the_least_fp32_numbers(ta):
+    """Weights of 2^-45 times scales of 2^-77 are 2^3 and more above 2^-126."""
+    def last(b, q, k, v):
+        q[b, :, :32] = 1
+        k *= 0.1
+        k[0, :, :32] = 1.0
+        k[0, -1, :32] = 12.0
+        v.abs_().clamp_(0.25 * 2.0 ** -75)
+        v[0, -1, 32:] = 0
+        p = torch.softmax(q[b].double() @ k[0].double().T / 128 ** 0.5, -1)[:, :-1]
+        assert (p > 2.0 ** -46).all() and (p < 2.0 ** -44).all()
+
+    o = run(ta, "bf16", [40, 700], 4, 128, [0, -75, -60, -70], 7, last)
+    assert (o[..., 32:].abs().amax(-1) > 0).all()

@@ -129,7 +129,7 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-constexpr float kMostUp = 0x1p100f;        // the largest r_g (and where it starts)
+constexpr float kMostUp = 0x1p126f;        // the largest r_g (and where it starts)
 constexpr float kFull = 0x1p14f;           // from here on r_g moves
 
 // N 32-bit words of shared memory (the widest load that fits)
@@ -561,7 +561,7 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
                                 const int e = int(j ? top >> 23 : (top >> 7) & 0xffu);
-                                const float r = fminf(__int_as_float(imin(127 + 7 + 127 - e, 227) << 23), up[nt][g][j]);
+                                const float r = fminf(__int_as_float(imin(127 + 7 + 127 - e, 253) << 23), up[nt][g][j]);
                                 scale_sums(nt, g, j, pow2_ratio(1.f, r, up[nt][g][j]));
                                 up[nt][g][j] = r;
                             }
