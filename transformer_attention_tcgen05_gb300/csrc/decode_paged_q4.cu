@@ -108,13 +108,8 @@ __device__ __forceinline__ uint32_t seen_bits(const Plan &r, int base) {
 
 // Fields of two 16-bit words as f16 pairs: bits 6-9 as 16 + n, bits 2-5 as 256 + n;
 // one instruction each.
-__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
-    uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(x), "r"(mask), "r"(bits));
-    return d;
-}
-__device__ __forceinline__ uint32_t code16(uint32_t w) { return and_or(w, 0x03c003c0u, 0x4c004c00u); }
-__device__ __forceinline__ uint32_t code256(uint32_t w) { return and_or(w, 0x003c003cu, 0x5c005c00u); }
+__device__ __forceinline__ uint32_t code16(uint32_t w) { return ptx::and_or(w, 0x03c003c0u, 0x4c004c00u); }
+__device__ __forceinline__ uint32_t code256(uint32_t w) { return ptx::and_or(w, 0x003c003cu, 0x5c005c00u); }
 constexpr uint32_t kMinus24 = 0xce00ce00u, kMinus264 = 0xdc20dc20u;   // f16 pairs
 
 // Powers of two.  2^n for an integer n in [-126, 126].

@@ -442,6 +442,13 @@ __device__ __forceinline__ void mma16816_f16(float (&d)[4], const uint32_t (&a)[
                    "f"(c3));
 }
 
+// x & mask | bits in one instruction (as two constants it would be two).
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(x), "r"(mask), "r"(bits));
+    return d;
+}
+
 // ---------------------------------------------------------- packed fp32x2
 // Blackwell executes these as one instruction on two fp32 lanes.
 

@@ -265,13 +265,6 @@ __device__ __forceinline__ uint32_t q4_codes(const float (&x)[8], float inv) {
     return ((w >> 2) & 0x3fff3fffu) | ((w << 14) & 0xc000c000u);
 }
 
-// x & mask | bits in one instruction (as two constants it would be two).
-__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
-    uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(x), "r"(mask), "r"(bits));
-    return d;
-}
-
 // The values of 8 codes in the 16-bit type: n - 8 is exact in either, so one product
 // rounds once.
 template <typename T>
@@ -280,15 +273,15 @@ __device__ __forceinline__ uint4 q4_values(uint32_t w, T scale) {
     const uint32_t y = __byte_perm(w, 0, 0x2301);
     uint32_t c[4];                                     // channels (i, i + 4) as 16 + n (f16), 32 + n (bf16)
     if constexpr (H::f16) {
-        c[0] = and_or(y, 0x03c003c0u, 0x4c004c00u);
-        c[1] = and_or(w << 4, 0x03c003c0u, 0x4c004c00u);
-        c[2] = and_or(w, 0x03c003c0u, 0x4c004c00u);
-        c[3] = and_or(y << 4, 0x03c003c0u, 0x4c004c00u);
+        c[0] = ptx::and_or(y, 0x03c003c0u, 0x4c004c00u);
+        c[1] = ptx::and_or(w << 4, 0x03c003c0u, 0x4c004c00u);
+        c[2] = ptx::and_or(w, 0x03c003c0u, 0x4c004c00u);
+        c[3] = ptx::and_or(y << 4, 0x03c003c0u, 0x4c004c00u);
     } else {
-        c[0] = and_or(y >> 4, 0x003c003cu, 0x42004200u);
-        c[1] = and_or(w, 0x003c003cu, 0x42004200u);
-        c[2] = and_or(w >> 4, 0x003c003cu, 0x42004200u);
-        c[3] = and_or(y, 0x003c003cu, 0x42004200u);
+        c[0] = ptx::and_or(y >> 4, 0x003c003cu, 0x42004200u);
+        c[1] = ptx::and_or(w, 0x003c003cu, 0x42004200u);
+        c[2] = ptx::and_or(w >> 4, 0x003c003cu, 0x42004200u);
+        c[3] = ptx::and_or(y, 0x003c003cu, 0x42004200u);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
