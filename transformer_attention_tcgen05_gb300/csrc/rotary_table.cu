@@ -95,13 +95,15 @@ Wide logarithm(double x, const Constants &c) {
 
 attn_status_t rope_frequencies(uint64_t *freq, int rot, double theta, attn_rope_scaling_t scaling, double factor,
                                double original_len, double alpha, double beta) {
-    const Constants c;
+    static const Constants c;
     Wide base = logarithm(theta, c);
     if (scaling == ATTN_ROPE_NTK)
         base = add(base, div(mul(logarithm(factor, c), wide(rot)), wide(rot - 2)));
-    for (int i = 0; i < rot / 2; ++i) {
-        // turns per position
-        Wide f = div(exponential(div(mul(base, wide(-2.0 * i)), wide(rot)), c), c.two_pi);
+    // turns per position, unscaled, of a pair and of the next one for each
+    Wide turns = div(wide(1.0), c.two_pi);
+    const Wide ratio = exponential(div(mul(base, wide(-2.0)), wide(rot)), c);
+    for (int i = 0; i < rot / 2; ++i, turns = mul(turns, ratio)) {
+        Wide f = turns;
         if (scaling == ATTN_ROPE_LINEAR) {
             f = div(f, wide(factor));
         } else if (scaling == ATTN_ROPE_BY_PARTS) {
