@@ -456,8 +456,8 @@ ATTN_API size_t attn_decode_gqa_paged_workspace_bytes(int B, int Hq, int Hkv, in
  *
  * attn_rope_fwd: y = the rotated rows of x, both [B, H, N, D] with element
  *   strides (batch, head, token) in x_strides / y_strides[3] (NULL: contiguous).
- *   positions: DEVICE int32 [B, N], rows pos_stride entries apart (0: one row for
- *   all batches); any value, negative ones too.  inverse != 0: the transposed
+ *   positions: DEVICE int32 [B, N], rows pos_stride entries apart (at least N, or 0:
+ *   one row for all batches); any value, negative ones too.  inverse != 0: the transposed
  *   rotation (angles negated), which is the gradient of the call with respect
  *   to x.  y may be x itself, with x's strides (in place); it must not overlap x
  *   otherwise.  All dtypes, D in {32, 64, 128}, H <= 2^30; fp32 arithmetic, rounded

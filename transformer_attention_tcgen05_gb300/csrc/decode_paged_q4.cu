@@ -33,17 +33,21 @@
 //    plain bulk copies (4.6 KB at D = 128) for K, V and scales together.
 //  * Up to 4 heads fill half of an MMA's 8 columns.  Then (SPLIT) the columns are heads by
 //    two halves of a chunk's tokens: half the scales, exponentials and weights per lane
-//    (8 x 4096 tokens, 32 heads on 8: 17.4 -> 16.2 us).
+//    (8 x 4096 tokens, 32 heads on 8: 17.4 -> 16.2 us, before r_g).
 //  * 3 CTAs of 4 warps per SM (2 for 9 to 16 heads of D 128); what a warp keeps of its
 //    range beside the chunk at hand lies in shared memory, so that the registers suffice
-//    (12 documents of 9000 to 60 000 tokens, 64 heads on 8: 2 CTAs 88.9 us, 3 84.9, 4 88.5).
+//    (12 documents of 9000 to 60 000 tokens, 64 heads on 8, before r_g: 2 CTAs 88.9 us, 3
+//    84.9, 4 88.5).
 //
-// Measured (bf16, D 128): 8 x 4096 tokens, 32 heads on 8, 16.2 us (2.35 TB/s; 26 us from
-// 16-bit pages); 12 documents, 64 heads on 8, 84 us (4.45 TB/s; 55 at the copy rate).  Of
-// these, 12.2 and 64 are the copies, the work list, the merges and joins alone; the rest is
-// arithmetic that does not hide behind them: 642 instructions per chunk (889 with a mask and
-// an OR as two).  Leaving out V's part took the documents from 86 to 68 us, K's to 70, the
-// softmax to 76, the MMAs of the constants to 79.5.
+// Measured (bf16, D 128): 8 x 4096 tokens, 32 heads on 8, 16.5 us (2.3 TB/s; 26 us from
+// 16-bit pages); 12 documents, 64 heads on 8, 85.4 us (4.36 TB/s; 55 at the copy rate), 128
+// heads on 8, 130 us.  Of the first two, 12.2 and 64 are the copies, the work list, the
+// merges and joins alone; the rest is arithmetic that does not hide behind them: a chunk
+// takes a warp 469 instructions with up to 4 heads, 548 with 5 to 8, 742 with 9 to 16.  For
+// the documents those are 36 us of issue slots: the chains within a chunk, which three
+// warps per scheduler do not cover, count for more.  r_g and its check cost 0.3, 1.3 and 8 us.
+// (Before them, leaving out V's part took the documents from 86 to 68 us, K's to 70, the
+// softmax to 76, the MMAs of the constants to 79.5.)
 //
 // Sums and statistics are fp32; the output is rounded once.
 #include <math.h>
@@ -62,7 +66,7 @@ template <int D, int NT>
 struct Q4Cfg {
     static constexpr int CW = 4;                            // warps
     // CTAs: 168 registers per thread, which 16 heads of D 128 do not fit (12 documents, 128
-    // heads on 8: 132 us so, 122 with 2)
+    // heads on 8, before r_g: 132 us so, 122 with 2)
     static constexpr int PER_SM = NT == 2 && D == 128 ? 2 : 3;
     static constexpr int NS = D == 64 ? 4 : 2;              // chunks in flight per warp
     static constexpr int THREADS = CW * 32;

@@ -73,7 +73,8 @@ static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsOther <= WnCfg<128>::NT * WnCf
               "setmaxnreg split must fit the launch's register file share");
 
 // Query tiles for D = 64 lie in two places in turn, so that an item's are copied as soon
-// as it is found (7 sequences of 2048, 24 heads, window 1024: 103 us with one place, 100);
+// as it is found (7 sequences of 2048, 24 heads, window 1024: 103 us with one place, 100;
+// 97 with the masks as bits);
 // for D = 128 the rings leave no room, and they follow the last scores of the item before.
 template <int D>
 struct VlCfg : WnCfg<D> {
