@@ -140,3 +140,36 @@ def test_products_near_the_least_fp32_numbers(ta):
 
     o = run(ta, "bf16", [40, 700], 4, 128, [0, -75, -60, -70], 7, last)
     assert (o[..., 32:].abs().amax(-1) > 0).all()
+
+
+@pytest.mark.parametrize("dt,D,G", [("bf16", 128, 4), ("f16", 128, 4), ("f16", 64, 8), ("f16", 128, 12)])
+def test_a_token_with_all_the_weight_is_given_back_exactly(ta, dt, D, G):
+    """Values of few bits, so that nothing but the output is rounded where the weight is 1:
+    whatever the scores' size and the scale of a group."""
+    g = torch.Generator().manual_seed(8)
+    n, B = 300, 12
+    c = Cache([n] * B, [0] * B, 16, 9)
+    s = (1 + torch.randint(0, 32, (B, n, D // 32), generator=g) / 32) * 2.0 ** torch.randint(-9, 3, (B, n, D // 32), generator=g)
+    code = torch.randint(0, 16, (B, n, D), generator=g)
+    code[..., ::32] = 0                                        # the value that the scale comes from
+    v = (code - 8) * s.repeat_interleave(32, -1)
+    k = torch.zeros(B, n, D)
+    at = torch.randint(0, n, (B,), generator=g)
+    q = randn(g, B, G, D).abs().to(DT[dt])
+    k[torch.arange(B), at] = torch.rand(B, 1, generator=g) * 10 + 20
+    p = torch.softmax(q.double() @ k.to(DT[dt]).double().transpose(1, 2) / D ** 0.5, -1)
+    p[torch.arange(B), :, at] = 0
+    assert p.max() < 2.0 ** -60
+    pages = torch.zeros(c.P, 1, 16, D + D // 8, dtype=torch.uint8)
+    for b in range(B):
+        rows = pack(k[b][None], v[b][None], dt)
+        page, row = c.rows(b, 0, n)
+        pages[page, :, row] = rows.transpose(0, 1)
+        assert torch.equal(unpack(rows, dt)[1][0], v[b].double())
+    o = ta.decode_gqa_paged_q4(q.cuda(), pages.cuda(), c.dev, c.sl)
+    assert ta.device_status() == 0
+    # a scale of 6 bits times a code of 3 has up to 9: f16 holds them, bf16 (8) rounds some
+    want = v[torch.arange(B), at][:, None].expand(B, G, D)
+    fits = want.to(DT[dt]).float() == want
+    assert fits.all() or dt == "bf16"
+    assert ((o.float().cpu() - want).abs() <= torch.where(fits, 0.0, torch.finfo(DT[dt]).eps / 2 * want.abs())).all()

@@ -26,28 +26,25 @@
 //    largest |p_j s_jg| so far into [2^7, 2^14), so that a product loses 2^-11 of itself
 //    down to 2^-21 of that one, and 2^-32 of that one below, however far apart the scales
 //    of a token's groups are.  (One reference for all groups of a token, their largest
-//    scale, left a group 2^-14 of it at the edge of f16's normal range.)  The running
-//    maximum of the scores moves in whole powers of two and takes r_g along, so that the
-//    sums of P V stay as they are; they are divided by r_g at a segment's end.
+//    scale, left a group 2^-14 of it at the edge of f16's normal range.)  The token
+//    at the running maximum of the scores weighs 1, so that its products, and often most
+//    of the sum, lose nothing.  Where the maximum moves, r_g rises by the whole powers of
+//    two that weights fall by; the sums of P V are divided by r_g at a segment's end.
 //  * The rows of a (page, head) are contiguous: a chunk of 32 tokens is one to four
 //    plain bulk copies (4.6 KB at D = 128) for K, V and scales together.
 //  * Up to 4 heads fill half of an MMA's 8 columns.  Then (SPLIT) the columns are heads by
 //    two halves of a chunk's tokens: half the scales, exponentials and weights per lane
-//    (8 x 4096 tokens, 32 heads on 8: 17.4 -> 16.2 us, before r_g).
+//    (8 x 4096 tokens, 32 heads on 8: 17.4 -> 16.2 us).
 //  * 3 CTAs of 4 warps per SM (2 for 9 to 16 heads of D 128); what a warp keeps of its
 //    range beside the chunk at hand lies in shared memory, so that the registers suffice
-//    (12 documents of 9000 to 60 000 tokens, 64 heads on 8, before r_g: 2 CTAs 88.9 us, 3
-//    84.9, 4 88.5).
+//    (12 documents of 9000 to 60 000 tokens, 64 heads on 8: 2 CTAs 88.9 us, 3 84.9, 4 88.5).
 //
-// Measured (bf16, D 128): 8 x 4096 tokens, 32 heads on 8, 16.5 us (2.3 TB/s; 26 us from
-// 16-bit pages); 12 documents, 64 heads on 8, 85.4 us (4.36 TB/s; 55 at the copy rate), 128
-// heads on 8, 130 us.  Of the first two, 12.2 and 64 are the copies, the work list, the
-// merges and joins alone; the rest is arithmetic that does not hide behind them: a chunk
-// takes a warp 469 instructions with up to 4 heads, 548 with 5 to 8, 742 with 9 to 16.  For
-// the documents those are 36 us of issue slots: the chains within a chunk, which three
-// warps per scheduler do not cover, count for more.  r_g and its check cost 0.3, 1.3 and 8 us.
-// (Before them, leaving out V's part took the documents from 86 to 68 us, K's to 70, the
-// softmax to 76, the MMAs of the constants to 79.5.)
+// Measured (bf16, D 128): 8 x 4096 tokens, 32 heads on 8, 16.2 us (2.35 TB/s; 26 us from
+// 16-bit pages); 12 documents, 64 heads on 8, 84 us (4.45 TB/s; 55 at the copy rate).  Of
+// these, 12.2 and 64 are the copies, the work list, the merges and joins alone; the rest is
+// arithmetic that does not hide behind them: 642 instructions per chunk (889 with a mask and
+// an OR as two).  Leaving out V's part took the documents from 86 to 68 us, K's to 70, the
+// softmax to 76, the MMAs of the constants to 79.5.
 //
 // Sums and statistics are fp32; the output is rounded once.
 #include <math.h>
@@ -66,7 +63,7 @@ template <int D, int NT>
 struct Q4Cfg {
     static constexpr int CW = 4;                            // warps
     // CTAs: 168 registers per thread, which 16 heads of D 128 do not fit (12 documents, 128
-    // heads on 8, before r_g: 132 us so, 122 with 2)
+    // heads on 8: 132 us so, 122 with 2)
     static constexpr int PER_SM = NT == 2 && D == 128 ? 2 : 3;
     static constexpr int NS = D == 64 ? 4 : 2;              // chunks in flight per warp
     static constexpr int THREADS = CW * 32;
@@ -361,7 +358,7 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
             for (int i = 0; i < 2 * NG; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
         }
         int bad = dead;
-        bool fresh = true;                             // no product yet
+        bool fresh = true, empty = true;               // a column, all of them without a score yet
 
         // this warp's chunks of the segment: the range's chunk number modulo the team.
         // The first NS rounds of all only ask for chunks; then come the segment's queries.
@@ -494,19 +491,22 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1)
                             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                        const float mn = fmaxf(m[nt][j], ceilf(top * qs[nt][j]));
+                        const float mn = fmaxf(m[nt][j], top * qs[nt][j]);
                         // (both infinite: NaN, and then 0)
-                        const float k = fminf(fmaxf(mn - m[nt][j], 0.f), 126.f), less = pow2(-k), more = pow2(k);
+                        const float d = fmaxf(mn - m[nt][j], 0.f), less = ptx::ex2(-d);
+                        const float more = pow2(floorf(fminf(d, 126.f)));
                         m[nt][j] = mn;
                         mu[nt][j] = mn == -INFINITY ? 0.f : mn;
                         none = none || mn == -INFINITY;
                         l[nt][j] *= less;
-                        // weights fall and r_g rises: the sums stay, but where it may not
+                        // weights fall and r_g rises, so far as it may
+                        if (!empty) {
 #pragma unroll
-                        for (int g = 0; g < NG; ++g) {
-                            const float r = fminf(up[nt][g][j] * more, kMostUp);
-                            scale_sums(nt, g, j, pow2_ratio(less, r, up[nt][g][j]));
-                            up[nt][g][j] = r;
+                            for (int g = 0; g < NG; ++g) {
+                                const float r = fminf(up[nt][g][j] * more, kMostUp);
+                                scale_sums(nt, g, j, less * pow2_ratio(1.f, r, up[nt][g][j]));
+                                up[nt][g][j] = r;
+                            }
                         }
                     }
                 fresh = __any_sync(0xffffffffu, none);
@@ -566,6 +566,7 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
                             }
                         }
                     fill(t);
+                    empty = false;
                 }
                 if (t == 0) {
 #pragma unroll
