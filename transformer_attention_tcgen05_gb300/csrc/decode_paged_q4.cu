@@ -28,23 +28,30 @@
 //    of a token's groups are.  (One reference for all groups of a token, their largest
 //    scale, left a group 2^-14 of it at the edge of f16's normal range.)  The token
 //    at the running maximum of the scores weighs 1, so that its products, and often most
-//    of the sum, lose nothing.  Where the maximum moves, r_g rises by the whole powers of
-//    two that weights fall by; the sums of P V are divided by r_g at a segment's end.
+//    of the sum, lose nothing (f16 outputs are 1.1 times as far from 64 bits as one rounding
+//    is, 1.4 with the maximum rounded up to a whole power of two).  Where the maximum
+//    moves, r_g rises by the power of two that weights fall by or the next one, so that the
+//    largest product stays in that range; the sums of P V are divided by r_g at a segment's
+//    end.
 //  * The rows of a (page, head) are contiguous: a chunk of 32 tokens is one to four
 //    plain bulk copies (4.6 KB at D = 128) for K, V and scales together.
 //  * Up to 4 heads fill half of an MMA's 8 columns.  Then (SPLIT) the columns are heads by
 //    two halves of a chunk's tokens: half the scales, exponentials and weights per lane
-//    (8 x 4096 tokens, 32 heads on 8: 17.4 -> 16.2 us).
+//    (8 x 4096 tokens, 32 heads on 8: 17.4 -> 16.2 us, before r_g).
 //  * 3 CTAs of 4 warps per SM (2 for 9 to 16 heads of D 128); what a warp keeps of its
 //    range beside the chunk at hand lies in shared memory, so that the registers suffice
-//    (12 documents of 9000 to 60 000 tokens, 64 heads on 8: 2 CTAs 88.9 us, 3 84.9, 4 88.5).
+//    (12 documents of 9000 to 60 000 tokens, 64 heads on 8, before r_g: 2 CTAs 88.9 us, 3
+//    84.9, 4 88.5).
 //
-// Measured (bf16, D 128): 8 x 4096 tokens, 32 heads on 8, 16.2 us (2.35 TB/s; 26 us from
-// 16-bit pages); 12 documents, 64 heads on 8, 84 us (4.45 TB/s; 55 at the copy rate).  Of
-// these, 12.2 and 64 are the copies, the work list, the merges and joins alone; the rest is
-// arithmetic that does not hide behind them: 642 instructions per chunk (889 with a mask and
-// an OR as two).  Leaving out V's part took the documents from 86 to 68 us, K's to 70, the
-// softmax to 76, the MMAs of the constants to 79.5.
+// Measured (bf16, D 128): 8 x 4096 tokens, 32 heads on 8, 16.4 us (2.3 TB/s; 26 us from
+// 16-bit pages); 12 documents, 64 heads on 8, 85 us (4.38 TB/s; 55 at the copy rate), 128
+// heads on 8, 131 us.  Of the first two, 12.2 and 64 are the copies, the work list, the
+// merges and joins alone; the rest is arithmetic that does not hide behind them: a chunk
+// takes a warp 469 instructions with up to 4 heads, 548 with 5 to 8, 744 with 9 to 16.  For
+// the documents those are 36 us of issue slots: the chains within a chunk, which three
+// warps per scheduler do not cover, count for more.  r_g and its check cost 0.3, 1 and 8 us.
+// (Before them, leaving out V's part took the documents from 86 to 68 us, K's to 70, the
+// softmax to 76, the MMAs of the constants to 79.5.)
 //
 // Sums and statistics are fp32; the output is rounded once.
 #include <math.h>
@@ -63,7 +70,7 @@ template <int D, int NT>
 struct Q4Cfg {
     static constexpr int CW = 4;                            // warps
     // CTAs: 168 registers per thread, which 16 heads of D 128 do not fit (12 documents, 128
-    // heads on 8: 132 us so, 122 with 2)
+    // heads on 8, before r_g: 132 us so, 122 with 2)
     static constexpr int PER_SM = NT == 2 && D == 128 ? 2 : 3;
     static constexpr int NS = D == 64 ? 4 : 2;              // chunks in flight per warp
     static constexpr int THREADS = CW * 32;
@@ -494,7 +501,7 @@ decode_paged_q4_kernel(const PgParams p, const PagesQ4 pages) {
                         const float mn = fmaxf(m[nt][j], top * qs[nt][j]);
                         // (both infinite: NaN, and then 0)
                         const float d = fmaxf(mn - m[nt][j], 0.f), less = ptx::ex2(-d);
-                        const float more = pow2(floorf(fminf(d, 126.f)));
+                        const float more = pow2(ceilf(fminf(d, 126.f)));
                         m[nt][j] = mn;
                         mu[nt][j] = mn == -INFINITY ? 0.f : mn;
                         none = none || mn == -INFINITY;
